@@ -66,6 +66,7 @@ typedef enum { DEC_F32 = 0, DEC_BF16 = 1, DEC_Q4G64 = 2 } dec_dtype;
 #define DEC_DEVERR_EXCHANGE_TIMEOUT 0x10u /* persistent engine: a wait for another CTA's words gave up */
 #define DEC_DEVERR_GEMM_TIMEOUT 0x20u     /* chunked prefill: a tensor-core GEMM pipeline wait gave up */
 #define DEC_DEVERR_BARRIER_TIMEOUT 0x40u  /* persistent 4-bit engine: a grid barrier gave up (dec_reset clears it) */
+#define DEC_DEVERR_BAD_PAGE 0x80u         /* a sequence, page or parent index of the paged calls was out of range */
 
 /* dec_config.engine */
 #define DEC_ENGINE_PERSISTENT 0 /* one cooperative launch runs whole forwards (default) */
@@ -405,6 +406,219 @@ dec_status greedy_head_noalloc(int32_t wdtype, const void* d_embed, const float*
  * Errors: DEC_EINVAL (sizes, alignment), DEC_EDEVICE, DEC_ECUDA. */
 dec_status gemm_bf16(const uint16_t* d_A, const uint16_t* d_W, float* d_C, int32_t M, int32_t N, int32_t K,
                      int32_t ldc, int32_t accumulate, void* stream);
+
+/* ---- Branches of one prompt ------------------------------------------------
+ *
+ * The calls below decode several continuations of ONE prefilled prompt
+ * together. The prompt's keys and values stay where dec_prefill_chunk put
+ * them (dec_get_kv: [n_kv][max_seq][head_dim]) and are shared by every
+ * branch; each branch keeps its own later tokens in pages. A step of all
+ * branches: kv_append_paged (per-head Q/K norm and rotation, new keys and
+ * values into the pages), attn_shared_prefix, and after the vocabulary
+ * projection beam_select and beam_reorder_pages. qk_norm_rope is the norm and
+ * rotation alone. The sources decode a single stream; these calls
+ * extend "Megakernels", "What runs in the DSL" (per-head Q/K RMSNorm, RoPE,
+ * grouped-query attention and KV update) and "GPU-wide end-to-end generation"
+ * (lowest-ID selection on the GPU) to several.
+ *
+ * Pools and tables: k_pages and v_pages are [num_pages][n_kv][page_size]
+ * [head_dim] in kvdtype, 16-byte aligned; page_size is a power of two up to
+ * 1024. Row b of page_table ([.][table_stride] int32) lists the pages of
+ * sequence b in order: its token i lies in page table[b][i / page_size], row
+ * i % page_size. A table entry that a call needs and that is outside
+ * [0, num_pages) sets DEC_DEVERR_BAD_PAGE in the context-free error word
+ * (gemv_device_errors) and the rows behind it are left out (not stored, not
+ * attended to); nothing outside the pools is read or written.
+ *
+ * All of them take their arguments in a struct, are asynchronous on `stream`
+ * (the struct may be reused once the call returns; the buffers when the work
+ * is done), allocate nothing and can be captured into a graph. Calls that
+ * share a workspace or write the same buffers must be ordered by the caller
+ * (one stream, or events). Every pointer must belong to the current device.
+ * Common errors: DEC_EINVAL (NULL struct, sizes, dtype, NULL or misaligned
+ * pointers), DEC_EDEVICE, DEC_ECUDA. */
+
+/* Frequencies of the position rotation, angle = position * inv_freq[i] for
+ * pair i of rot_dim / 2, from inv_freq[i] = theta^(-2i / rot_dim):
+ * ROPE_LINEAR divides all of them by `factor` (positions interpolated);
+ * ROPE_BASE stretches the base, theta * factor^(rot_dim / (rot_dim - 2)), so
+ * that the slowest pair is divided by factor and the fastest kept;
+ * ROPE_RAMP keeps the pairs that turn at least beta_fast times in
+ * orig_context positions, divides those that turn at most beta_slow times by
+ * factor, blends linearly in the number of turns between them, and gives
+ * cosine and sine the factor 0.1 ln(factor) + 1 (the published YaRN rule);
+ * the other kinds give 1. */
+enum { ROPE_PLAIN = 0, ROPE_LINEAR = 1, ROPE_BASE = 2, ROPE_RAMP = 3 };
+
+typedef struct {
+  int32_t rot_dim; /* even, 2..128 */
+  int32_t kind;    /* ROPE_* */
+  double theta;    /* > 0, e.g. 1e6 */
+  double factor;   /* >= 1 (unused by ROPE_PLAIN) */
+  double orig_context, beta_slow, beta_fast; /* ROPE_RAMP: > 0, beta_slow < beta_fast, e.g. 32768, 1, 32 */
+} rope_scaling;
+
+/* Fills h_inv_freq (HOST, rot_dim / 2 doubles) and *h_factor (HOST). Runs on
+ * the host only ("Megakernels", "What runs in the DSL": the host precomputes
+ * the rotary constants once). Errors: DEC_EINVAL. */
+dec_status rope_frequencies(const rope_scaling* s, double* h_inv_freq, float* h_factor);
+
+/* rows x (n_q + n_kv) heads of head_dim (a multiple of 8 up to 128); row r of
+ * q starts at q + r * q_stride elements and holds n_q heads side by side, k
+ * likewise with n_kv. Each head is RMS-normalised over head_dim (skipped where
+ * its gain is NULL), y = x / sqrt(mean(x^2) + eps) * g, and its first rot_dim
+ * elements are rotated: pairs (i, i + rot_dim / 2), or (2i, 2i + 1) with
+ * interleaved != 0, by positions[r] * inv_freq[i], cosine and sine times
+ * rope_factor. rot_dim 0: no rotation. The arithmetic is float32 (angles are
+ * reduced exactly, so far positions lose nothing) and each output is rounded
+ * once. positions[r] < 0 marks a padded row: its outputs are left as they
+ * were. q_out may be q itself (same dtype and stride), k_out likewise. */
+typedef struct {
+  int32_t rows, n_q, n_kv, head_dim; /* n_q or n_kv may be 0 */
+  int32_t xdtype, ydtype;            /* q, k; q_out, k_out: DEC_F32 or DEC_BF16 */
+  const void *q, *k;
+  void *q_out, *k_out;
+  int64_t q_stride, k_stride, q_out_stride, k_out_stride;
+  const float *g_q, *g_k; /* [head_dim] or NULL */
+  const int32_t* positions;
+  const double* inv_freq; /* device, [rot_dim / 2] */
+  float eps, rope_factor;
+  int32_t rot_dim, interleaved;
+} qk_rope_args;
+
+/* Per-head Q/K RMSNorm and RoPE of "Megakernels", "What runs in the DSL", as a
+ * call of its own. */
+dec_status qk_norm_rope(const qk_rope_args* a, void* stream);
+
+/* qk_norm_rope whose keys, with the values v beside them, go to pages: row r
+ * is the token at positions[r] of sequence seq[r], stored at index
+ * positions[r] - base_pos of that sequence's pages (base_pos: the tokens of
+ * the shared prefix, which are not in pages). Keys are stored normalised and
+ * rotated, values as they are, both rounded once to kvdtype. seq NULL: row r
+ * belongs to sequence r. A padded row (positions[r] < 0) stores nothing and
+ * leaves its q_out as it was. A seq[r] outside [0, n_seq) or an index outside
+ * the table's width counts as a bad page; the row's q_out is still written.
+ * Two rows at the same index of one sequence leave either one's values. */
+typedef struct {
+  int32_t rows, n_q, n_kv, head_dim; /* n_q may be 0 */
+  int32_t xdtype, ydtype, kvdtype;   /* q, k, v; q_out; pages */
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const float *g_q, *g_k;
+  const int32_t* positions;
+  const double* inv_freq;
+  float eps, rope_factor;
+  int32_t rot_dim, interleaved;
+  void *k_pages, *v_pages;
+  const int32_t* page_table;
+  const int32_t* seq;
+  int32_t n_seq, num_pages, page_size, table_stride, base_pos;
+} kv_append_args;
+
+/* "Megakernels", "What runs in the DSL": norm, RoPE and KV update, here into
+ * pages. */
+dec_status kv_append_paged(const kv_append_args* a, void* stream);
+
+/* Grouped-query attention of one query token for each of `batch` branches over
+ * the shared prefix followed by the branch's own paged tokens:
+ * out[b][h] = softmax(scale * q[b][h] . [Kp; Ks]) [Vp; Vs], query head h on
+ * key/value head h / (n_q / n_kv). The prefix is prefix_len keys and values a
+ * head, head g at prefix_k + g * prefix_stride * head_dim elements (the layout
+ * of dec_get_kv with prefix_stride = max_seq), kvdtype like the pages; rows
+ * past prefix_len are never used, whatever they hold. It is read once for all
+ * branches. seq_len[b] is the number of the branch's own tokens (more than
+ * table_stride * page_size counts as a bad page); seq_len[b] < 0 marks an
+ * unused slot, whose out and lse are left as they were. A branch with nothing
+ * to attend to gets zeros (and lse -inf). lse (nullable, float32
+ * [batch][n_q]) receives the natural log of the softmax's denominator.
+ * n_q / n_kv <= 16. Scores, softmax sums and outputs are accumulated in
+ * float32; with DEC_BF16 q and out the result is rounded once to bfloat16. The
+ * result does not depend on timing (partial results join in a fixed order).
+ * d_workspace: attn_shared_prefix_workspace(a) bytes, 256-byte aligned; its
+ * contents need no initialisation. */
+typedef struct {
+  int32_t batch, n_q, n_kv, head_dim;
+  int32_t qdtype, kvdtype; /* q and out; prefix and pages: DEC_F32 or DEC_BF16 */
+  const void* q;
+  void* out;
+  float* lse;
+  int64_t q_stride, out_stride; /* elements between branches */
+  const void *prefix_k, *prefix_v;
+  int32_t prefix_len;
+  int64_t prefix_stride; /* rows between heads, >= prefix_len */
+  const void *k_pages, *v_pages;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  int32_t num_pages, page_size, table_stride;
+  float scale;
+  void* d_workspace;
+  size_t workspace_bytes;
+} attn_shared_args;
+
+/* Bytes of workspace for a call with these sizes (the pointers are not looked
+ * at); 0 if they are invalid or the device is not supported. */
+size_t attn_shared_prefix_workspace(const attn_shared_args* a);
+
+/* "Megakernels", "What runs in the DSL": grouped-query attention, here of
+ * several branches. Additional error: DEC_ENOMEM (workspace too small). */
+dec_status attn_shared_prefix(const attn_shared_args* a, void* stream);
+
+/* Beam search's selection: the n_out best of the beams x vocab continuations
+ * by scores[b] + log_softmax(logits[b])[v], best first; of equal ones the
+ * lowest b * vocab + v comes first (log-softmax and comparison in double over
+ * float32 exponentials). out_scores float32, out_parents (b) and out_tokens
+ * (v) int32 [n_out]. A logit of -inf or NaN is never chosen (NaN counts as
+ * masked, as in the greedy argmax); a beam whose score is not finite, whose
+ * logits hold +inf, or which has no finite logit offers nothing. Slots that
+ * nothing fills get parent -1, token -1 and score -inf.
+ * beams 1..1024, n_out 1..1024, beams * vocab < 2^31; logits float32,
+ * row b at logits + b * logits_stride. d_workspace as for
+ * attn_shared_prefix. */
+typedef struct {
+  int32_t beams, vocab, n_out;
+  const float* logits;
+  int64_t logits_stride;
+  const float* scores;
+  float* out_scores;
+  int32_t *out_parents, *out_tokens;
+  void* d_workspace;
+  size_t workspace_bytes;
+} beam_select_args;
+
+size_t beam_select_workspace(const beam_select_args* a);
+
+/* "Megakernels", "GPU-wide end-to-end generation": the selection of the next
+ * tokens on the GPU with lowest-ID ties, here over several beams. Additional
+ * error: DEC_ENOMEM. */
+dec_status beam_select(const beam_select_args* a, void* stream);
+
+/* After a selection: beam i continues beam p = parents[i]. Its new table row
+ * lists p's filled pages (shared from now on, they are not written again),
+ * then spare[i], which receives a copy of the old_len[p] % page_size tokens of
+ * p's last, partly filled page (nothing where that is 0), in every layer; the
+ * entries behind are -1, and new_len[i] = old_len[p]. So each beam owns the
+ * page its next token goes to. The spare pages must differ from each other and
+ * from every page of the old tables; old and new tables and lengths must not
+ * overlap. parents[i] < 0, or a parent that is itself unused (old_len < 0),
+ * makes slot i unused: new_len -1 and a row of -1. old_len[p] must leave room
+ * for the next token (< table_stride * page_size); a longer one, a parent
+ * >= beams, or a page or spare page outside the pool sets DEC_DEVERR_BAD_PAGE
+ * and makes the slot unused. Layer l's pools start l * layer_stride elements
+ * after k_pages and v_pages. */
+typedef struct {
+  int32_t beams, layers, n_kv, head_dim, kvdtype;
+  void *k_pages, *v_pages;
+  int64_t layer_stride;
+  int32_t num_pages, page_size, table_stride;
+  const int32_t *parents, *spare; /* [beams] */
+  const int32_t *old_table, *old_len;
+  int32_t *new_table, *new_len;
+} beam_reorder_args;
+
+/* Counterpart of "Megakernels", "GPU-wide end-to-end generation" (the cache
+ * entries a generation leaves) for branches that share entries. */
+dec_status beam_reorder_pages(const beam_reorder_args* a, void* stream);
 
 #ifdef __cplusplus
 }

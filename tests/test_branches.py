@@ -1,0 +1,215 @@
+"""Host side of the calls for several branches: index arithmetic, rotation frequencies, refusals (no GPU)."""
+import ctypes
+import itertools
+import math
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+import oracle.branches as OB
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+@pytest.fixture(scope="module")
+def W():
+    from weight_streaming_gemv_token_gb300 import build as bld
+
+    bld.build()
+    import weight_streaming_gemv_token_gb300 as W
+
+    return W
+
+
+@pytest.fixture(scope="module")
+def paging(tmp_path_factory):
+    """csrc/paging.h compiled as plain C++."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("paging")
+    src = d / "p.cpp"
+    src.write_text('#include "paging.h"\nusing namespace wsg;\nextern "C" {\n'
+                   "int shift_of(int n) { return page_shift(n); }\n"
+                   "int page(int pages, int n_kv, int shift, int width, const int32_t* row, int64_t i) {\n"
+                   "  return page_of(PagePool{pages, n_kv, shift, width}, row, i); }\n"
+                   "int64_t row(int pages, int n_kv, int shift, int page, int g, int64_t i) {\n"
+                   "  return pool_row(PagePool{pages, n_kv, shift, 0}, page, g, i); }\n}\n")
+    lib = d / "p.so"
+    inc = os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(src), "-o", str(lib)], check=True)
+    L = ctypes.CDLL(str(lib))
+    L.page.argtypes = [ctypes.c_int] * 4 + [ctypes.c_void_p, ctypes.c_int64]
+    L.row.argtypes = [ctypes.c_int] * 5 + [ctypes.c_int64]
+    L.row.restype = ctypes.c_int64
+    return L
+
+
+def test_page_sizes(paging):
+    for n in range(-2, 1100):
+        ok = 1 <= n <= 1024 and n & (n - 1) == 0
+        assert paging.shift_of(n) == (int(math.log2(n)) if ok else -1), n
+
+
+def test_every_page_lookup_stays_inside(paging):
+    """Indexes around both ends of a table, entries around both ends of the pool."""
+    for pages, width, shift in itertools.product((0, 1, 3), (0, 1, 2, 5), (0, 1, 4)):
+        row = np.array([2, -1, 0, 3, 2**31 - 1][:width] + [77], dtype=np.int32)  # 77: behind the row, never to be read
+        for i in list(range(-3, (width + 1) << shift)) + [-2**31, 2**31 - 1, 2**31, 2**40, -2**40]:
+            p = paging.page(pages, 2, shift, width, row.ctypes.data, i)
+            want = -1
+            if 0 <= i < width << shift and 0 <= row[i >> shift] < pages:
+                want = row[i >> shift]
+            assert p == want, (pages, width, shift, i)
+
+
+def test_pool_rows_are_64_bit_and_distinct(paging):
+    seen = set()
+    for page, g, i in itertools.product(range(3), range(4), range(8)):
+        r = paging.row(3, 4, 3, page, g, i)
+        assert r == (page * 4 + g) * 8 + i
+        seen.add(r)
+    assert len(seen) == 96
+    # token indexes of later pages use their place inside the page
+    assert paging.row(3, 4, 3, 1, 2, 8 * 7 + 5) == (1 * 4 + 2) * 8 + 5
+    assert paging.row(2**31 - 1, 64, 10, 2**31 - 2, 63, 1023) == ((2**31 - 2) * 64 + 63) * 1024 + 1023
+
+
+def test_frequencies(W):
+    w, f = W.rope_frequencies(128, 1e6)
+    np.testing.assert_allclose(w, 1e6 ** (-np.arange(0, 128, 2) / 128), rtol=1e-14)
+    assert f == 1.0
+    lin, f = W.rope_frequencies(64, 1e4, W.ROPE_LINEAR, factor=8.0)
+    np.testing.assert_allclose(lin, 1e4 ** (-np.arange(0, 64, 2) / 64) / 8, rtol=1e-14)
+    assert f == 1.0
+    base, f = W.rope_frequencies(64, 1e4, W.ROPE_BASE, factor=8.0)
+    plain = 1e4 ** (-np.arange(0, 64, 2) / 64)
+    assert base[0] == 1.0 and f == 1.0
+    np.testing.assert_allclose(base[-1], plain[-1] / 8, rtol=1e-12)  # the slowest pair takes the whole factor
+    ramp, f = W.rope_frequencies(128, 1e6, W.ROPE_RAMP, factor=4.0, orig_context=32768)
+    plain = 1e6 ** (-np.arange(0, 128, 2) / 128)
+    turns = 32768 * plain / (2 * np.pi)
+    fast, slow = turns >= 32, turns <= 1
+    assert fast.any() and slow.any() and not (fast | slow).all()
+    np.testing.assert_allclose(np.array(ramp)[fast], plain[fast], rtol=1e-13)
+    np.testing.assert_allclose(np.array(ramp)[slow], plain[slow] / 4, rtol=1e-13)
+    mid = ~(fast | slow)
+    assert ((np.array(ramp)[mid] < plain[mid]) & (np.array(ramp)[mid] > plain[mid] / 4)).all()
+    assert abs(f - (0.1 * math.log(4.0) + 1.0)) < 1e-6
+
+
+def test_frequency_refusals(W):
+    for kw in ({"rot_dim": 3}, {"rot_dim": 0}, {"rot_dim": 130}, {"theta": 0.0}, {"theta": -1.0}, {"theta": math.nan},
+               {"theta": math.inf}, {"kind": 4}, {"kind": -1}, {"kind": 1, "factor": 0.5}, {"kind": 1, "factor": math.nan},
+               {"kind": 2, "factor": 2.0, "rot_dim": 2}, {"kind": 3, "factor": 2.0, "orig_context": 0.0},
+               {"kind": 3, "factor": 2.0, "orig_context": 10.0, "beta_slow": 4.0, "beta_fast": 4.0},
+               {"kind": 3, "factor": 2.0, "orig_context": 10.0, "beta_slow": 0.0}):
+        with pytest.raises(W.WsgError) as e:
+            W.rope_frequencies(**{"rot_dim": 64, "theta": 1e4, **kw})
+        assert e.value.status == 1, kw
+    assert W.library().rope_frequencies(None, None, None) == 1
+
+
+P = 4096  # an address that is never used: every call below is refused before any kernel
+
+ROPE = dict(rows=4, n_q=4, n_kv=2, head_dim=16, xdtype=0, ydtype=0, q=P, k=P, q_out=P, k_out=P, q_stride=64, k_stride=32,
+            q_out_stride=64, k_out_stride=32, g_q=P, g_k=P, positions=P, inv_freq=P, eps=1e-6, rope_factor=1.0,
+            rot_dim=16, interleaved=0)
+APPEND = dict(rows=4, n_q=4, n_kv=2, head_dim=16, xdtype=0, ydtype=0, kvdtype=1, q=P, k=P, v=P, q_out=P, q_stride=64,
+              k_stride=32, v_stride=32, q_out_stride=64, g_q=P, g_k=P, positions=P, inv_freq=P, eps=1e-6,
+              rope_factor=1.0, rot_dim=16, interleaved=0, k_pages=P, v_pages=P, page_table=P, seq=P, n_seq=4,
+              num_pages=8, page_size=16, table_stride=2, base_pos=0)
+ATTN = dict(batch=4, n_q=4, n_kv=2, head_dim=16, qdtype=0, kvdtype=1, q=P, out=P, lse=P, q_stride=64, out_stride=64,
+            prefix_k=P, prefix_v=P, prefix_len=8, prefix_stride=8, k_pages=P, v_pages=P, page_table=P, seq_len=P,
+            num_pages=8, page_size=16, table_stride=2, scale=0.25, d_workspace=P, workspace_bytes=1 << 30)
+SELECT = dict(beams=4, vocab=100, n_out=8, logits=P, logits_stride=100, scores=P, out_scores=P, out_parents=P,
+              out_tokens=P, d_workspace=P, workspace_bytes=1 << 30)
+REORDER = dict(beams=4, layers=2, n_kv=2, head_dim=16, kvdtype=1, k_pages=P, v_pages=P, layer_stride=1024, num_pages=8,
+               page_size=16, table_stride=2, parents=P, spare=P, old_table=P, old_len=P, new_table=2 * P, new_len=2 * P)
+CALLS = {"qk_norm_rope": ("qk_rope_args", ROPE), "kv_append_paged": ("kv_append_args", APPEND),
+         "attn_shared_prefix": ("attn_shared_args", ATTN), "beam_select": ("beam_select_args", SELECT),
+         "beam_reorder_pages": ("beam_reorder_args", REORDER)}
+HEADS = [{"head_dim": 4}, {"head_dim": 20}, {"head_dim": 136}, {"head_dim": 0}, {"head_dim": -8}]
+ROWS = HEADS + [{"rows": -1}, {"n_q": -1}, {"n_kv": -1}, {"xdtype": 2}, {"ydtype": 5}, {"rot_dim": 3}, {"rot_dim": 18},
+                {"rot_dim": -2}, {"eps": -1.0}, {"eps": math.nan}, {"q": None}, {"k": None}, {"q_out": None},
+                {"positions": None}, {"inv_freq": None}, {"q_stride": -1}, {"k_stride": -1}, {"q_out_stride": 63}]
+PAGES = [{"page_size": 0}, {"page_size": 3}, {"page_size": 2048}, {"page_size": -16}, {"num_pages": -1},
+         {"k_pages": P + 2}, {"v_pages": P + 8}, {"k_pages": None}, {"v_pages": None}]
+BAD = {
+    "qk_norm_rope": ROWS + [{"k_out": None}, {"k_out_stride": 31}],
+    "kv_append_paged": ROWS + PAGES + [{"n_kv": 0}, {"kvdtype": 2}, {"v": None}, {"page_table": None}, {"n_seq": -1},
+                                       {"table_stride": -1}, {"base_pos": -1}, {"v_stride": -1}],
+    "attn_shared_prefix": HEADS + PAGES + [
+        {"batch": -1}, {"batch": 65536}, {"n_q": 3}, {"n_q": 0}, {"n_kv": 0}, {"n_q": 34, "n_kv": 2}, {"qdtype": 2},
+        {"kvdtype": 2}, {"q": None}, {"out": None}, {"seq_len": None}, {"prefix_k": None}, {"prefix_v": None},
+        {"prefix_len": -1}, {"prefix_stride": 7}, {"page_table": None}, {"out_stride": 63}, {"q_stride": -1},
+        {"table_stride": -1}, {"table_stride": 1 << 30}, {"prefix_k": P + 4}, {"d_workspace": None},
+        {"d_workspace": P + 16}],
+    "beam_select": [{"beams": 0}, {"beams": 1025}, {"vocab": 0}, {"n_out": 0}, {"n_out": 1025},
+                    {"beams": 1024, "vocab": 1 << 21, "logits_stride": 1 << 21}, {"logits": None}, {"scores": None},
+                    {"out_scores": None}, {"out_parents": None}, {"out_tokens": None}, {"logits_stride": 99},
+                    {"logits_stride": -100}, {"d_workspace": None}, {"d_workspace": P + 16}],
+    "beam_reorder_pages": HEADS + PAGES + [
+        {"beams": -1}, {"layers": 0}, {"layers": 65536}, {"n_kv": 0}, {"kvdtype": 2}, {"table_stride": 0},
+        {"layer_stride": -1024}, {"layer_stride": 1025}, {"parents": None}, {"spare": None}, {"old_table": None},
+        {"old_len": None}, {"new_table": None}, {"new_len": None}, {"new_table": P}, {"new_len": P}],
+}
+
+
+@pytest.mark.parametrize("call,change", [(c, b) for c, bs in BAD.items() for b in bs], ids=str)
+def test_refusals(W, call, change):
+    args, good = CALLS[call]
+    with pytest.raises(W.WsgError) as e:
+        getattr(W, call)(getattr(W, args)(**{**good, **change}))
+    assert e.value.status == 1, str(e.value)
+    assert call in str(e.value)
+
+
+def test_null_arguments_and_empty_calls(W):
+    lib = W.library()
+    for call in CALLS:
+        assert getattr(lib, call)(None, None) == 1, call
+    assert lib.attn_shared_prefix_workspace(None) == 0 and lib.beam_select_workspace(None) == 0
+    W.qk_norm_rope(W.qk_rope_args(**{**ROPE, "rows": 0}))
+    W.qk_norm_rope(W.qk_rope_args(**{**ROPE, "n_q": 0, "n_kv": 0}))
+    W.kv_append_paged(W.kv_append_args(**{**APPEND, "rows": 0}))
+    W.attn_shared_prefix(W.attn_shared_args(**{**ATTN, "batch": 0}))
+    W.beam_reorder_pages(W.beam_reorder_args(**{**REORDER, "beams": 0}))
+
+
+def test_argument_blocks(W):
+    torch = pytest.importorskip("torch")
+    with pytest.raises(TypeError, match="missing rows"):
+        W.qk_rope_args(**{k: v for k, v in ROPE.items() if k != "rows"})
+    with pytest.raises(TypeError, match="no field"):
+        W.beam_select_args(**SELECT, speed=1)
+    with pytest.raises(W.WsgError, match="not on a CUDA device"):
+        W.qk_rope_args(**{**ROPE, "q": torch.zeros(4)})
+
+
+def test_oracle_rotation_layouts():
+    """Both layouts turn each pair by its angle and leave lengths as they are; position 0 turns nothing."""
+    rng = np.random.default_rng(0)
+    x, w = rng.standard_normal((3, 16)), np.array([1.0, 0.3, 0.01])
+    for inter in (0, 1):
+        y = OB.rotate(x, 7, w, 6, inter)
+        a, b = (slice(0, 6, 2), slice(1, 6, 2)) if inter else (slice(0, 3), slice(3, 6))
+        z = (x[:, a] + 1j * x[:, b]) * np.exp(7j * w)
+        np.testing.assert_allclose(y[:, a] + 1j * y[:, b], z)
+        np.testing.assert_array_equal(y[:, 6:], x[:, 6:])
+        np.testing.assert_array_equal(OB.rotate(x, 0, w, 6, inter), x)
+
+
+def test_oracle_attention_joins_and_selects():
+    rng = np.random.default_rng(1)
+    q, k, v = rng.standard_normal((2, 8)), rng.standard_normal((5, 8)), rng.standard_normal((5, 8))
+    o, lse, _ = OB.attend(q, k, v, 0.5)
+    parts = [OB.attend(q, k[s], v[s], 0.5) for s in (slice(0, 2), slice(2, 5))]
+    wts = np.exp(np.array([p[1] for p in parts]) - lse)
+    np.testing.assert_allclose(sum(w[:, None] * p[0] for w, p in zip(wts, parts)), o)
+    sc, pa, to = OB.beam_select(np.zeros((2, 3)), np.array([0.0, 0.0]), 4)
+    assert pa.tolist() == [0, 0, 0, 1] and to.tolist() == [0, 1, 2, 0]
+    np.testing.assert_allclose(sc, -np.log(3.0))

@@ -23,6 +23,8 @@ DEC_ENGINE_PERSISTENT, DEC_ENGINE_STAGED = 0, 1
 DEC_DEVERR_WAIT_TIMEOUT, DEC_DEVERR_ARGMAX_NAN, DEC_DEVERR_BAD_TOKEN = 0x1, 0x2, 0x4
 DEC_DEVERR_BAD_POSITION, DEC_DEVERR_EXCHANGE_TIMEOUT, DEC_DEVERR_GEMM_TIMEOUT, DEC_DEVERR_BARRIER_TIMEOUT = (
     0x8, 0x10, 0x20, 0x40)
+DEC_DEVERR_BAD_PAGE = 0x80
+ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_RAMP = range(4)
 
 # Every symbol include/wsg.h declares.
 EXPORTED = (
@@ -31,6 +33,8 @@ EXPORTED = (
     "dec_destroy", "dec_last_error",
     "gemv", "gemv_q4", "gemv_q4_rows_per_warp", "gemv_device_errors", "greedy_head_noalloc", "gemm_bf16",
     "pack_bf16_exact", "dec_verify2", "dec_set_wait_limit",
+    "rope_frequencies", "qk_norm_rope", "kv_append_paged", "attn_shared_prefix", "attn_shared_prefix_workspace",
+    "beam_select", "beam_select_workspace", "beam_reorder_pages",
 )
 
 
@@ -56,6 +60,96 @@ class dec_layer_weights(ctypes.Structure):
 
 class dec_weights(ctypes.Structure):
     _fields_ = [("embed", c_void_p), ("g_final", c_void_p), ("layers", ctypes.POINTER(dec_layer_weights))]
+
+
+class _Args(ctypes.Structure):
+    """An argument block of the calls for several branches: fields by keyword, every one but `_optional` required.
+    Pointers may be tensors, which the block keeps alive; it can be used for any number of calls."""
+
+    _optional = ()
+
+    def __init__(self, **kw):
+        super().__init__()
+        self._keep = {}
+        names = {f[0] for f in self._fields_}
+        missing = names - kw.keys() - set(self._optional)
+        if missing:
+            raise TypeError(f"{type(self).__name__}: missing {', '.join(sorted(missing))}")
+        for name, value in kw.items():
+            self.set(name, value)
+
+    def set(self, name, value):
+        """Set one field (a number, a device pointer or a tensor)."""
+        for f, kind in self._fields_:
+            if f == name:
+                break
+        else:
+            raise TypeError(f"{type(self).__name__} has no field {name}")
+        if kind is c_void_p:
+            if getattr(value, "is_cuda", True) is False:
+                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is not on a CUDA device")
+            self._keep[name] = value
+            value = _ptr(value)
+        setattr(self, name, value)
+        return self
+
+    def with_workspace(self, workspace):
+        """Set the workspace to a tensor of bytes (its size too)."""
+        self.set("d_workspace", workspace)
+        self.workspace_bytes = workspace.numel() * workspace.element_size()
+        return self
+
+
+class rope_scaling(ctypes.Structure):
+    _fields_ = [("rot_dim", c_int32), ("kind", c_int32)] + [
+        (n, ctypes.c_double) for n in ("theta", "factor", "orig_context", "beta_slow", "beta_fast")]
+
+
+c_int64 = ctypes.c_int64
+
+
+class qk_rope_args(_Args):
+    _fields_ = ([(n, c_int32) for n in ("rows", "n_q", "n_kv", "head_dim", "xdtype", "ydtype")]
+                + [(n, c_void_p) for n in ("q", "k", "q_out", "k_out")]
+                + [(n, c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
+                + [(n, c_void_p) for n in ("g_q", "g_k", "positions", "inv_freq")]
+                + [("eps", c_float), ("rope_factor", c_float), ("rot_dim", c_int32), ("interleaved", c_int32)])
+
+
+class kv_append_args(_Args):
+    _fields_ = ([(n, c_int32) for n in ("rows", "n_q", "n_kv", "head_dim", "xdtype", "ydtype", "kvdtype")]
+                + [(n, c_void_p) for n in ("q", "k", "v", "q_out")]
+                + [(n, c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
+                + [(n, c_void_p) for n in ("g_q", "g_k", "positions", "inv_freq")]
+                + [("eps", c_float), ("rope_factor", c_float), ("rot_dim", c_int32), ("interleaved", c_int32)]
+                + [(n, c_void_p) for n in ("k_pages", "v_pages", "page_table", "seq")]
+                + [(n, c_int32) for n in ("n_seq", "num_pages", "page_size", "table_stride", "base_pos")])
+
+
+class attn_shared_args(_Args):
+    _optional = ("lse", "d_workspace", "workspace_bytes")
+    _fields_ = ([(n, c_int32) for n in ("batch", "n_q", "n_kv", "head_dim", "qdtype", "kvdtype")]
+                + [(n, c_void_p) for n in ("q", "out", "lse")]
+                + [(n, c_int64) for n in ("q_stride", "out_stride")]
+                + [("prefix_k", c_void_p), ("prefix_v", c_void_p), ("prefix_len", c_int32), ("prefix_stride", c_int64)]
+                + [(n, c_void_p) for n in ("k_pages", "v_pages", "page_table", "seq_len")]
+                + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
+                + [("scale", c_float), ("d_workspace", c_void_p), ("workspace_bytes", c_size_t)])
+
+
+class beam_select_args(_Args):
+    _optional = ("d_workspace", "workspace_bytes")
+    _fields_ = ([(n, c_int32) for n in ("beams", "vocab", "n_out")]
+                + [("logits", c_void_p), ("logits_stride", c_int64)]
+                + [(n, c_void_p) for n in ("scores", "out_scores", "out_parents", "out_tokens", "d_workspace")]
+                + [("workspace_bytes", c_size_t)])
+
+
+class beam_reorder_args(_Args):
+    _fields_ = ([(n, c_int32) for n in ("beams", "layers", "n_kv", "head_dim", "kvdtype")]
+                + [("k_pages", c_void_p), ("v_pages", c_void_p), ("layer_stride", c_int64)]
+                + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
+                + [(n, c_void_p) for n in ("parents", "spare", "old_table", "old_len", "new_table", "new_len")])
 
 
 _lib = None
@@ -95,6 +189,14 @@ def library() -> ctypes.CDLL:
             "gemm_bf16": (c_int32, [c_void_p, c_void_p, c_void_p, c_int32, c_int32, c_int32, c_int32, c_int32, c_void_p]),
             "greedy_head_noalloc": (c_int32, [c_int32, c_void_p, c_void_p, c_void_p, c_float, c_int32, c_int32,
                                               c_void_p, c_void_p, c_void_p]),
+            "rope_frequencies": (c_int32, [P(rope_scaling), P(ctypes.c_double), P(c_float)]),
+            "qk_norm_rope": (c_int32, [P(qk_rope_args), c_void_p]),
+            "kv_append_paged": (c_int32, [P(kv_append_args), c_void_p]),
+            "attn_shared_prefix": (c_int32, [P(attn_shared_args), c_void_p]),
+            "attn_shared_prefix_workspace": (c_size_t, [P(attn_shared_args)]),
+            "beam_select": (c_int32, [P(beam_select_args), c_void_p]),
+            "beam_select_workspace": (c_size_t, [P(beam_select_args)]),
+            "beam_reorder_pages": (c_int32, [P(beam_reorder_args), c_void_p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -255,3 +357,56 @@ def gemm_bf16(A, W, C, M: int, N: int, K: int, ldc: int | None = None, accumulat
     """C[M][N] (=, or += with accumulate) A[M][K] . W[N][K]^T, bfloat16 operands, FP32 accumulation (tensor cores)."""
     _check(library().gemm_bf16(_ptr(A), _ptr(W), _ptr(C), M, N, K, N if ldc is None else ldc, int(bool(accumulate)),
                                _stream(stream)))
+
+
+# ---- several branches of one prompt ----
+
+def rope_frequencies(rot_dim: int, theta: float, kind: int = ROPE_PLAIN, factor: float = 1.0, orig_context: float = 0.0,
+                     beta_slow: float = 1.0, beta_fast: float = 32.0) -> tuple[list[float], float]:
+    """Angular frequency of each of the rot_dim / 2 pairs (host, double) and the factor on cosine and sine."""
+    if not 0 <= rot_dim <= 4096:
+        raise WsgError(DEC_EINVAL, f"rope_frequencies: rot_dim {rot_dim}")
+    s = rope_scaling(rot_dim=rot_dim, kind=kind, theta=theta, factor=factor, orig_context=orig_context,
+                     beta_slow=beta_slow, beta_fast=beta_fast)
+    out, f = (ctypes.c_double * max(1, rot_dim // 2))(), c_float()
+    _check(library().rope_frequencies(ctypes.byref(s), out, ctypes.byref(f)))
+    return list(out), f.value
+
+
+def qk_norm_rope(args: qk_rope_args, stream=None):
+    """Per-head RMS norm of queries and keys with the position rotation in the same pass."""
+    _check(library().qk_norm_rope(args, _stream(stream)))
+
+
+def kv_append_paged(args: kv_append_args, stream=None):
+    """qk_norm_rope whose keys, and the values beside them, go to a paged cache."""
+    _check(library().kv_append_paged(args, _stream(stream)))
+
+
+def attn_shared_prefix_workspace(args: attn_shared_args) -> int:
+    n = library().attn_shared_prefix_workspace(args)
+    if n == 0:
+        raise WsgError(DEC_EINVAL, "attn_shared_prefix_workspace: invalid sizes")
+    return n
+
+
+def attn_shared_prefix(args: attn_shared_args, stream=None):
+    """Attention of one token of each branch over the shared prefix and the branch's own pages."""
+    _check(library().attn_shared_prefix(args, _stream(stream)))
+
+
+def beam_select_workspace(args: beam_select_args) -> int:
+    n = library().beam_select_workspace(args)
+    if n == 0:
+        raise WsgError(DEC_EINVAL, "beam_select_workspace: invalid sizes")
+    return n
+
+
+def beam_select(args: beam_select_args, stream=None):
+    """The n_out best continuations over all beams and the vocabulary."""
+    _check(library().beam_select(args, _stream(stream)))
+
+
+def beam_reorder_pages(args: beam_reorder_args, stream=None):
+    """New page tables after a selection, and copies of the tail pages that beams must own."""
+    _check(library().beam_reorder_pages(args, _stream(stream)))

@@ -1,0 +1,412 @@
+// qk_norm_rope and kv_append_paged: per-head RMS norm of queries and keys with
+// the position rotation in the same pass, and the store of keys and values
+// into pages ("Megakernels", "What runs in the DSL": per-head Q/K RMSNorm,
+// RoPE, KV update).
+//
+// Mathematics: y = x / sqrt(mean(x^2) + eps) * g per head; the pair (a, b) at
+// angle t becomes (a cos t - b sin t, a sin t + b cos t), t = position * w_i.
+// The angle is kept in turns as a 64-bit fixed-point fraction, F_i = frac(w_i /
+// 2 pi) * 2^64: position * F_i modulo 2^64 is the exact fraction of a turn for
+// that F_i, by integer multiplication, so a far position costs no precision
+// (F_i is off by at most 2^-54 turns: under 2^-22 turns at position 2^31) and
+// no double arithmetic per row. The top 32 bits go to sincospif.
+//
+// Layout: a unit of lanes holds one head, 8 consecutive elements a lane (one
+// 16-byte load of bfloat16, two of float32), and walks several heads of one row
+// so that the row's cosines and sines are computed once and stay in registers.
+// The half layout pairs element i with i + rot / 2, which another lane of the
+// unit holds (a shuffle; a staged copy in shared memory where rot / 2 is not a
+// multiple of 8); interleaved pairs lie inside a lane. Reads and writes each
+// element once: bound by memory for many rows, by latency for few.
+#include <cmath>
+
+#include "common.h"
+#include "paging.h"
+#include "ptx.cuh"
+
+namespace wsg {
+namespace {
+
+constexpr int kRowsThreads = 256;
+
+struct QkRowsArgs {
+  const void *q, *k, *v;
+  void *q_out, *k_out, *v_out;  // k_out, v_out: rows, or the pools
+  long long q_stride, k_stride, v_stride, qo_stride, ko_stride;
+  const float *g_q, *g_k;
+  const int32_t* pos;
+  const double* inv_freq;
+  float eps, factor;
+  int rows, n_q, n_kv, d, rot, interleaved;
+  int heads;     // n_q + n_kv (+ n_kv value heads)
+  int per_unit;  // heads a unit walks
+  int units_per_row;
+  int vec_x, vec_y;  // 16-byte accesses possible
+  int paged;
+  PagePool pool;
+  const int32_t* table;
+  const int32_t* seq;
+  int n_seq, base_pos;
+  uint32_t* err;
+};
+
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    if (vec) {
+      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = p[e];
+    }
+  } else {
+    if (vec) {
+      const uint4 a = *reinterpret_cast<const uint4*>(p);
+      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        x[2 * e] = __uint_as_float(w[e] << 16);
+        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32(p[e]);
+    }
+  }
+}
+
+// Two floats as packed bfloat16 (low half: x), rounded to nearest even (NaN stays NaN).
+__device__ __forceinline__ uint32_t pack2(float x, float y) {
+  uint32_t h;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  return h;
+}
+
+template <typename T>
+__device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
+  if constexpr (sizeof(T) == 4) {
+    if (vec) {
+      reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
+      reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = x[e];
+    }
+  } else {
+    uint32_t w[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) w[e] = pack2(x[2 * e], x[2 * e + 1]);
+    if (vec) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) p[e] = static_cast<T>(w[e >> 1] >> (16 * (e & 1)));
+    }
+  }
+}
+
+// Cosine and sine of position * w, w in radians per position.
+__device__ __forceinline__ void turn(double w, uint32_t pos, float factor, float* c, float* s) {
+  const double f = w * 0.15915494309189533577;  // turns per position
+  const unsigned long long F = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
+  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>((F * pos) >> 32));
+  sincospif(static_cast<float>(t) * 0x1p-31f, s, c);  // in half turns
+  *c *= factor;
+  *s *= factor;
+}
+
+// LPH: lanes of a unit (a power of two, 8 LPH >= d).
+template <typename XT, typename YT, typename KT, int LPH>
+__global__ void __launch_bounds__(kRowsThreads) qk_rows_kernel(const QkRowsArgs a) {
+  __shared__ float stage[kRowsThreads * 8];
+  const int tid = threadIdx.x, li = tid % LPH;
+  const long long unit = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
+  const int r = static_cast<int>(unit / a.units_per_row);
+  const int h0 = static_cast<int>(unit % a.units_per_row) * a.per_unit;
+  const int e0 = li * 8;
+  const bool inside = r < a.rows && e0 < a.d;
+  const int pos = r < a.rows ? a.pos[r] : -1;
+  const bool live = inside && pos >= 0;
+  const int half = a.rot >> 1;
+
+  // where this row's keys and values go
+  long long kv_row0 = -1;
+  if (a.paged && live) {
+    const int s = a.seq ? a.seq[r] : r;
+    const long long idx = static_cast<long long>(pos) - a.base_pos;
+    const int page = s >= 0 && s < a.n_seq ? page_of(a.pool, a.table + static_cast<long long>(s) * a.pool.width, idx) : -1;
+    if (page >= 0)
+      kv_row0 = pool_row(a.pool, page, 0, idx);
+    else if (li == 0 && h0 + a.per_unit > a.n_q)
+      atomicOr(a.err, ERR_BAD_PAGE);
+  }
+
+  // element e of this lane: y = x * cs + partner * sn (sn carries the sign)
+  float cs[8], sn[8];
+  bool turned[8];
+  if (a.interleaved) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = e0 + 2 * j;
+      float c = 1.f, s = 0.f;
+      const bool t = live && e < a.rot;
+      if (t) turn(a.inv_freq[e >> 1], static_cast<uint32_t>(pos), a.factor, &c, &s);
+      cs[2 * j] = cs[2 * j + 1] = c;
+      sn[2 * j] = -s;
+      sn[2 * j + 1] = s;
+      turned[2 * j] = turned[2 * j + 1] = t;
+    }
+  } else {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int e = e0 + j;
+      float c = 1.f, s = 0.f;
+      const bool t = live && e < a.rot;
+      if (t) turn(a.inv_freq[e < half ? e : e - half], static_cast<uint32_t>(pos), a.factor, &c, &s);
+      cs[j] = c;
+      sn[j] = e < half ? -s : s;
+      turned[j] = t;
+    }
+  }
+  // lane that holds the partners (half layout in whole lanes)
+  const bool whole = (half & 7) == 0;
+  const int shift = half >> 3;
+  const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? shift : -shift);
+
+  for (int i = 0; i < a.per_unit; ++i) {
+    const int h = h0 + i;
+    const bool on = live && h < a.heads;
+    const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;  // query, key, value
+    const int hh = kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (on) {
+      const XT* src = static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                      (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * r + hh * a.d + e0;
+      load8(src, a.vec_x, x);
+    }
+    const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    if (g && on) {
+      const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e0 + e];
+    }
+    float y[8];
+    if (a.interleaved) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = turned[e] && kind < 2 ? fmaf(x[e ^ 1], sn[e], x[e] * cs[e]) : x[e];
+    } else if (whole) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float p = __shfl_sync(0xffffffffu, x[e], mate);
+        y[e] = turned[e] && kind < 2 ? fmaf(p, sn[e], x[e] * cs[e]) : x[e];
+      }
+    } else {
+      float* st = stage + (tid - li) * 8;
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
+      __syncwarp();
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        y[e] = turned[e] && kind < 2 ? fmaf(st[e0 + e < half ? e0 + e + half : e0 + e - half], sn[e], x[e] * cs[e]) : x[e];
+    }
+    if (!on) continue;
+    if (kind == 0) {
+      store8(static_cast<YT*>(a.q_out) + a.qo_stride * r + hh * a.d + e0, a.vec_y, y);
+    } else if (!a.paged) {
+      store8(static_cast<KT*>(a.k_out) + a.ko_stride * r + hh * a.d + e0, a.vec_y, y);
+    } else if (kv_row0 >= 0) {
+      KT* dst = static_cast<KT*>(kind == 1 ? a.k_out : a.v_out);
+      store8(dst + (kv_row0 + (static_cast<long long>(hh) << a.pool.shift)) * a.d + e0, true, y);
+    }
+  }
+}
+
+template <typename XT, typename YT, typename KT>
+cudaError_t launch_rows(const QkRowsArgs& a, int lph, cudaStream_t st) {
+  const long long units = static_cast<long long>(a.rows) * a.units_per_row;
+  const long long per_block = kRowsThreads / lph;
+  const dim3 grid(static_cast<unsigned>((units + per_block - 1) / per_block));
+  switch (lph) {
+    case 1: return launch_k(qk_rows_kernel<XT, YT, KT, 1>, grid, dim3(kRowsThreads), 0, st, false, a);
+    case 2: return launch_k(qk_rows_kernel<XT, YT, KT, 2>, grid, dim3(kRowsThreads), 0, st, false, a);
+    case 4: return launch_k(qk_rows_kernel<XT, YT, KT, 4>, grid, dim3(kRowsThreads), 0, st, false, a);
+    case 8: return launch_k(qk_rows_kernel<XT, YT, KT, 8>, grid, dim3(kRowsThreads), 0, st, false, a);
+    default: return launch_k(qk_rows_kernel<XT, YT, KT, 16>, grid, dim3(kRowsThreads), 0, st, false, a);
+  }
+}
+
+bool is_float(int t) { return t == DEC_F32 || t == DEC_BF16; }
+
+// Whether rows at p with a stride in elements can be read or written in 16-byte pieces.
+bool pieces16(const void* p, long long stride, int dtype) {
+  return aligned16(p) && stride * (dtype == DEC_F32 ? 4 : 2) % 16 == 0;
+}
+
+// Checks common to both calls, on the fields they share.
+template <typename A>
+dec_status check_rows(const A* a, const char* who) {
+  if (a->rows < 0 || a->n_q < 0 || a->n_kv < 0 || a->n_q > 65535 || a->n_kv > 65535)
+    return fail(nullptr, DEC_EINVAL, "%s: rows %d, n_q %d, n_kv %d", who, a->rows, a->n_q, a->n_kv);
+  if (a->head_dim < 8 || a->head_dim > 128 || a->head_dim % 8)
+    return fail(nullptr, DEC_EINVAL, "%s: head_dim must be a multiple of 8 up to 128, got %d", who, a->head_dim);
+  if (!is_float(a->xdtype) || !is_float(a->ydtype))
+    return fail(nullptr, DEC_EINVAL, "%s: xdtype %d, ydtype %d", who, a->xdtype, a->ydtype);
+  if (a->rot_dim < 0 || a->rot_dim > a->head_dim || a->rot_dim % 2)
+    return fail(nullptr, DEC_EINVAL, "%s: rot_dim must be even and at most head_dim, got %d", who, a->rot_dim);
+  if (!(a->eps >= 0.f)) return fail(nullptr, DEC_EINVAL, "%s: eps must be >= 0", who);
+  if (a->rows == 0) return DEC_OK;
+  if (!a->positions || (a->n_q > 0 && (!a->q || !a->q_out)) || (a->n_kv > 0 && !a->k) ||
+      (a->rot_dim > 0 && !a->inv_freq))
+    return fail(nullptr, DEC_EINVAL, "%s: NULL pointer", who);
+  if (a->q_stride < 0 || a->k_stride < 0) return fail(nullptr, DEC_EINVAL, "%s: negative row stride", who);
+  if (a->rows > 1 && a->n_q > 0 && a->q_out_stride < static_cast<long long>(a->n_q) * a->head_dim)
+    return fail(nullptr, DEC_EINVAL, "%s: q_out rows overlap at stride %lld", who,
+                static_cast<long long>(a->q_out_stride));
+  return DEC_OK;
+}
+
+template <typename A>
+QkRowsArgs shared_fields(const A* a) {
+  QkRowsArgs k{};
+  k.q = a->q;
+  k.k = a->k;
+  k.q_out = a->q_out;
+  k.q_stride = a->q_stride;
+  k.k_stride = a->k_stride;
+  k.qo_stride = a->q_out_stride;
+  k.g_q = a->g_q;
+  k.g_k = a->g_k;
+  k.pos = a->positions;
+  k.inv_freq = a->inv_freq;
+  k.eps = a->eps;
+  k.factor = a->rope_factor;
+  k.rows = a->rows;
+  k.n_q = a->n_q;
+  k.n_kv = a->n_kv;
+  k.d = a->head_dim;
+  k.rot = a->rot_dim;
+  k.interleaved = a->interleaved != 0;
+  k.vec_x = (a->n_q == 0 || pieces16(a->q, a->q_stride, a->xdtype)) && (a->n_kv == 0 || pieces16(a->k, a->k_stride, a->xdtype));
+  k.vec_y = a->n_q == 0 || pieces16(a->q_out, a->q_out_stride, a->ydtype);
+  return k;
+}
+
+dec_status run_rows(QkRowsArgs& k, int xd, int yd, int kd, const DeviceInfo& di, cudaStream_t st) {
+  int lph = 1;
+  while (lph * 8 < k.d) lph *= 2;
+  // Heads a unit walks: more share the row's angles, fewer give more units.
+  k.per_unit = 1;
+  while (k.per_unit < 8 && k.per_unit < k.heads &&
+         static_cast<long long>(k.rows) * ((k.heads + 2 * k.per_unit - 1) / (2 * k.per_unit)) * lph >= 2048ll * di.sms)
+    k.per_unit *= 2;
+  k.units_per_row = (k.heads + k.per_unit - 1) / k.per_unit;
+  cudaError_t e;
+  const bool xf = xd == DEC_F32, yf = yd == DEC_F32, kf = kd == DEC_F32;
+  using H = uint16_t;
+  if (xf)
+    e = yf ? (kf ? launch_rows<float, float, float>(k, lph, st) : launch_rows<float, float, H>(k, lph, st))
+           : (kf ? launch_rows<float, H, float>(k, lph, st) : launch_rows<float, H, H>(k, lph, st));
+  else
+    e = yf ? (kf ? launch_rows<H, float, float>(k, lph, st) : launch_rows<H, float, H>(k, lph, st))
+           : (kf ? launch_rows<H, H, float>(k, lph, st) : launch_rows<H, H, H>(k, lph, st));
+  WSG_CUDA_TRY(nullptr, e);
+  return DEC_OK;
+}
+
+}  // namespace
+}  // namespace wsg
+
+using namespace wsg;
+
+extern "C" dec_status rope_frequencies(const rope_scaling* s, double* h_inv_freq, float* h_factor) {
+  if (!s || !h_inv_freq || !h_factor) return fail(nullptr, DEC_EINVAL, "rope_frequencies: NULL pointer");
+  if (s->rot_dim < 2 || s->rot_dim > 128 || s->rot_dim % 2)
+    return fail(nullptr, DEC_EINVAL, "rope_frequencies: rot_dim must be even, 2..128, got %d", s->rot_dim);
+  if (!(s->theta > 0.0) || !std::isfinite(s->theta)) return fail(nullptr, DEC_EINVAL, "rope_frequencies: theta must be positive");
+  if (s->kind < ROPE_PLAIN || s->kind > ROPE_RAMP) return fail(nullptr, DEC_EINVAL, "rope_frequencies: kind %d", s->kind);
+  if (s->kind != ROPE_PLAIN && !(s->factor >= 1.0 && std::isfinite(s->factor)))
+    return fail(nullptr, DEC_EINVAL, "rope_frequencies: factor must be at least 1");
+  if (s->kind == ROPE_BASE && s->rot_dim < 4)
+    return fail(nullptr, DEC_EINVAL, "rope_frequencies: ROPE_BASE needs rot_dim >= 4");
+  if (s->kind == ROPE_RAMP &&
+      !(s->orig_context > 0.0 && s->beta_slow > 0.0 && s->beta_fast > s->beta_slow && std::isfinite(s->beta_fast)))
+    return fail(nullptr, DEC_EINVAL, "rope_frequencies: ROPE_RAMP needs orig_context > 0 and 0 < beta_slow < beta_fast");
+  const double rot = s->rot_dim;
+  const double base = s->kind == ROPE_BASE ? s->theta * std::pow(s->factor, rot / (rot - 2.0)) : s->theta;
+  for (int i = 0; i < s->rot_dim / 2; ++i) {
+    double w = std::pow(base, -2.0 * i / rot);
+    if (s->kind == ROPE_LINEAR) w /= s->factor;
+    if (s->kind == ROPE_RAMP) {
+      const double turns = s->orig_context * w / 6.283185307179586;
+      double keep = (turns - s->beta_slow) / (s->beta_fast - s->beta_slow);
+      keep = keep < 0.0 ? 0.0 : keep > 1.0 ? 1.0 : keep;
+      w = w * keep + w / s->factor * (1.0 - keep);
+    }
+    h_inv_freq[i] = w;
+  }
+  *h_factor = s->kind == ROPE_RAMP ? static_cast<float>(0.1 * std::log(s->factor) + 1.0) : 1.f;
+  return DEC_OK;
+}
+
+extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
+  if (!a) return fail(nullptr, DEC_EINVAL, "qk_norm_rope: NULL arguments");
+  dec_status s = check_rows(a, "qk_norm_rope");
+  if (s != DEC_OK) return s;
+  if (a->rows == 0 || a->n_q + a->n_kv == 0) return DEC_OK;
+  if (a->n_kv > 0 && !a->k_out) return fail(nullptr, DEC_EINVAL, "qk_norm_rope: NULL k_out");
+  if (a->rows > 1 && a->n_kv > 0 && a->k_out_stride < static_cast<long long>(a->n_kv) * a->head_dim)
+    return fail(nullptr, DEC_EINVAL, "qk_norm_rope: k_out rows overlap at stride %lld",
+                static_cast<long long>(a->k_out_stride));
+  DeviceInfo di;
+  if ((s = device_info(&di, nullptr)) != DEC_OK) return s;
+  QkRowsArgs k = shared_fields(a);
+  k.k_out = a->k_out;
+  k.ko_stride = a->k_out_stride;
+  k.vec_y = k.vec_y && (a->n_kv == 0 || pieces16(a->k_out, a->k_out_stride, a->ydtype));
+  k.heads = a->n_q + a->n_kv;
+  k.err = di.err;
+  return run_rows(k, a->xdtype, a->ydtype, a->ydtype, di, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
+  if (!a) return fail(nullptr, DEC_EINVAL, "kv_append_paged: NULL arguments");
+  dec_status s = check_rows(a, "kv_append_paged");
+  if (s != DEC_OK) return s;
+  if (a->n_kv < 1) return fail(nullptr, DEC_EINVAL, "kv_append_paged: n_kv must be >= 1");
+  if (!is_float(a->kvdtype)) return fail(nullptr, DEC_EINVAL, "kv_append_paged: kvdtype %d", a->kvdtype);
+  const int shift = page_shift(a->page_size);
+  if (shift < 0)
+    return fail(nullptr, DEC_EINVAL, "kv_append_paged: page_size must be a power of two up to %d, got %d", kPageSizeMax,
+                a->page_size);
+  if (a->n_seq < 0 || a->num_pages < 0 || a->table_stride < 0 || a->base_pos < 0 || a->v_stride < 0)
+    return fail(nullptr, DEC_EINVAL, "kv_append_paged: n_seq %d, num_pages %d, table_stride %d, base_pos %d", a->n_seq,
+                a->num_pages, a->table_stride, a->base_pos);
+  if (a->rows == 0) return DEC_OK;
+  if (!a->v || !a->k_pages || !a->v_pages || !a->page_table) return fail(nullptr, DEC_EINVAL, "kv_append_paged: NULL pointer");
+  if (!aligned16(a->k_pages) || !aligned16(a->v_pages))
+    return fail(nullptr, DEC_EINVAL, "kv_append_paged: the pools must be 16-byte aligned");
+  DeviceInfo di;
+  if ((s = device_info(&di, nullptr)) != DEC_OK) return s;
+  QkRowsArgs k = shared_fields(a);
+  k.v = a->v;
+  k.v_stride = a->v_stride;
+  k.vec_x = k.vec_x && pieces16(a->v, a->v_stride, a->xdtype);
+  k.k_out = a->k_pages;
+  k.v_out = a->v_pages;
+  k.heads = a->n_q + 2 * a->n_kv;
+  k.paged = 1;
+  k.pool = PagePool{a->num_pages, a->n_kv, shift, a->table_stride};
+  k.table = a->page_table;
+  k.seq = a->seq;
+  k.n_seq = a->n_seq;
+  k.base_pos = a->base_pos;
+  k.err = di.err;
+  return run_rows(k, a->xdtype, a->ydtype, a->kvdtype, di, static_cast<cudaStream_t>(stream));
+}
