@@ -68,24 +68,24 @@ class _Args(ctypes.Structure):
 
     _optional = ()
 
+    def __init_subclass__(cls):
+        cls._kind = dict(cls._fields_)
+        cls._needed = cls._kind.keys() - set(cls._optional)
+
     def __init__(self, **kw):
         super().__init__()
         self._keep = {}
-        names = {f[0] for f in self._fields_}
-        missing = names - kw.keys() - set(self._optional)
-        if missing:
-            raise TypeError(f"{type(self).__name__}: missing {', '.join(sorted(missing))}")
+        if not self._needed <= kw.keys():
+            raise TypeError(f"{type(self).__name__}: missing {', '.join(sorted(self._needed - kw.keys()))}")
         for name, value in kw.items():
             self.set(name, value)
 
     def set(self, name, value):
         """Set one field (a number, a device pointer or a tensor)."""
-        for f, kind in self._fields_:
-            if f == name:
-                break
-        else:
+        kind = self._kind.get(name)
+        if kind is None:
             raise TypeError(f"{type(self).__name__} has no field {name}")
-        if kind is c_void_p:
+        if kind is c_void_p and value is not None:
             if getattr(value, "is_cuda", True) is False:
                 raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is not on a CUDA device")
             self._keep[name] = value

@@ -1,0 +1,503 @@
+// Partial attention of a few query rows over a range of keys, on warp-level
+// matrix instructions; the partial results join in attn_join_kernel.
+//
+// An item is up to 16 MT query rows of one key/value head and a range of its
+// keys: rows of all branches over a range of the shared prefix, or the rows of
+// one branch over a range of its own pages. A CTA of four warps takes an item.
+// Each warp streams its own blocks of keys (16 bfloat16 or 8 float32 ones) with
+// 16-byte asynchronous copies through its own ring in shared memory, so the
+// main loop has no CTA-wide barrier:
+//   S = Q K^T (rows x block), masked and scaled; running reference maximum and
+//   sum of a softmax; P = 2^(S - reference) stays in registers and becomes the A
+//   operand of O += P V. The reference moves only when a block's maximum passes
+//   it by 2^8, so O is rarely rescaled.
+//   At the end the warps' (O, m, l) join through shared memory and the CTA
+//   writes one partial result.
+//
+// Precision: float32 sums throughout. bfloat16 keys and values enter exactly; a
+// float32 query is split into three bfloat16 parts (24 bits, exact), a
+// probability into two (QP 1: bfloat16 queries, whose result is rounded to 8
+// bits: 2^-16 is lost) or three. Float32 keys and values run on tf32 instructions
+// as value + remainder, three of the four products (2^-21 relative is lost).
+//
+// Rows in shared memory are 16 bytes longer than the head, which makes every
+// matrix load and the float32 value loads free of bank conflicts. Memory bounds
+// it while the matrix instructions per key stay below the copy time.
+#pragma once
+#include <cstdint>
+
+#include "common.h"
+#include "paging.h"
+#include "ptx.cuh"
+
+namespace wsg {
+
+constexpr int kAmWarps = 4, kAmThreads = 32 * kAmWarps;
+constexpr float kAmMargin = 8.f;  // the reference moves past this margin (log2 units)
+
+struct AmArgs {
+  int batch, n_q, n_kv, d, group, rows;  // rows = batch * group
+  const void* q;
+  long long q_stride;
+  const void *pk, *pv;
+  int plen;
+  long long pstride;
+  const void *kp, *vp;
+  PagePool pool;
+  const int32_t *table, *len;
+  float scale_log2;
+  // items: first the prefix's, item = (split * n_kv + head) * row_groups + row group,
+  // then the branches', item = (split * batch + branch) * n_kv + head
+  int prefix_items, row_groups, prefix_chunk, own_chunk;  // chunks: keys a split covers
+  int own_slot0;                                          // slot of the branches' split 0
+  float* part_o;                                          // [slot][batch * n_q][d]
+  float2* part_ml;                                        // [slot][batch * n_q]: (reference, sum)
+  uint32_t* err;
+};
+
+template <int DP, int QP, int MT, bool F32>
+struct AmGeom {
+  static constexpr int KB = F32 ? 8 : 16;                              // keys a block
+  static constexpr int E = F32 ? 4 : 2;                                // bytes an element
+  static constexpr int PITCH = DP * E + 16;                            // bytes a row
+  static constexpr int STAGES = F32 || QP == 3 ? 2 : 3;
+  static constexpr int TILE = KB * PITCH;                              // keys (or values) of a block
+  static constexpr int QBYTES = F32 ? MT * 2 * (DP / 8) * 32 * 16 : QP * 16 * MT * PITCH;
+  static constexpr int RING = STAGES * 2 * TILE;                       // per warp
+  static constexpr int JOIN = kAmWarps * 16 * MT * DP * 4;             // reuses the rings
+  static constexpr int SMEM = QBYTES + (kAmWarps * RING > JOIN ? kAmWarps * RING : JOIN);
+};
+
+__device__ __forceinline__ void am_copy16(uint32_t dst, const void* src, uint32_t bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void am_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void am_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void am_ld4(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void am_ld4t(uint32_t (&r)[4], uint32_t addr) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+__device__ __forceinline__ void am_mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void am_mma8(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+               : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ float am_exp2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// x = hi + lo in tf32 (10 mantissa bits each, hi rounded to nearest).
+__device__ __forceinline__ void am_split_tf32(float x, uint32_t* hi, uint32_t* lo) {
+  const uint32_t h = (__float_as_uint(x) + 0x1000u) & 0xFFFFE000u;
+  *hi = h;
+  *lo = __float_as_uint(x - __uint_as_float(h));
+}
+
+// Two floats as PARTS packed bfloat16 pairs (low half: x) that sum to them.
+template <int PARTS>
+__device__ __forceinline__ void am_split_bf16(float x, float y, uint32_t (&p)[PARTS]) {
+#pragma unroll
+  for (int i = 0; i < PARTS; ++i) {
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(p[i]) : "f"(y), "f"(x));
+    x -= __uint_as_float(p[i] << 16);
+    y -= __uint_as_float(p[i] & 0xFFFF0000u);
+  }
+}
+
+template <typename QT, int DP, int QP, int MT, bool F32>
+__global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a) {
+  using G = AmGeom<DP, QP, MT, F32>;
+  constexpr int KB = G::KB, NT = DP / 8, PP = QP == 1 ? 2 : 3;  // PP: bfloat16 parts of a probability
+  extern __shared__ __align__(128) unsigned char am_raw[];
+  __shared__ float s_m[kAmWarps][16 * MT], s_l[kAmWarps][16 * MT];
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_trigger();  // the join's CTAs may take their places and wait
+
+  // ---- the item ----
+  const bool shared_item = static_cast<int>(blockIdx.x) < a.prefix_items;
+  int g, row0, nrows, slot, k0, k1, branch = 0;
+  if (shared_item) {
+    const int rg = blockIdx.x % a.row_groups, t = blockIdx.x / a.row_groups;
+    g = t % a.n_kv;
+    slot = t / a.n_kv;
+    row0 = rg * 16 * MT;
+    nrows = min(16 * MT, a.rows - row0);
+    k0 = slot * a.prefix_chunk;
+    k1 = min(a.plen, k0 + a.prefix_chunk);
+  } else {
+    const int t = blockIdx.x - a.prefix_items;
+    g = t % a.n_kv;
+    branch = t / a.n_kv % a.batch;
+    const int split = t / a.n_kv / a.batch;
+    slot = a.own_slot0 + split;
+    row0 = branch * a.group;
+    nrows = a.group;
+    int n = a.len[branch];
+    if (n > page_capacity(a.pool)) {
+      n = static_cast<int>(page_capacity(a.pool));
+      if (split == 0 && g == 0 && tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
+    }
+    k0 = split * a.own_chunk;
+    k1 = min(n, k0 + a.own_chunk);
+    if (k0 >= k1) return;  // attn_join_kernel knows which splits hold keys
+  }
+  const int nblk = (k1 - k0 + KB - 1) / KB;
+  const int32_t* trow = a.table + static_cast<long long>(branch) * a.pool.width;
+  const char* kbase = static_cast<const char*>(shared_item ? a.pk : a.kp);
+  const char* vbase = static_cast<const char*>(shared_item ? a.pv : a.vp);
+
+  unsigned char* ring = am_raw + G::QBYTES + warp * G::RING;
+  const uint32_t ring32 = smem_u32(ring);
+  const int chunks = a.d * G::E / 16;  // 16-byte pieces of a key
+
+  // key `lane` of a block: its row in the cache, -1 past the range or without a page
+  auto row_of = [&](int blk) -> long long {
+    const int k = k0 + blk * KB + lane;
+    if (lane >= KB || k >= k1) return -1;
+    if (shared_item) return a.pstride * g + k;
+    const int page = page_of(a.pool, trow, k);
+    if (page < 0) {
+      atomicOr(a.err, ERR_BAD_PAGE);
+      return -1;
+    }
+    return pool_row(a.pool, page, g, k);
+  };
+  auto request = [&](int stage, long long row) {
+    const uint32_t kd = ring32 + stage * 2 * G::TILE, vd = kd + G::TILE;
+    constexpr int CP = DP * G::E / 16;  // pieces of a padded row (a power of two)
+#pragma unroll
+    for (int i = 0; i < KB * CP / 32; ++i) {
+      const int key = (i * 32 + lane) / CP, c = (i * 32 + lane) % CP;
+      const long long r = __shfl_sync(0xffffffffu, row, key);
+      if (c < chunks) {
+        const long long off = r < 0 ? 0 : r * (static_cast<long long>(a.d) * G::E) + c * 16;
+        const uint32_t n = r < 0 ? 0 : 16;  // 0: zeros are written
+        am_copy16(kd + key * G::PITCH + c * 16, kbase + off, n);
+        am_copy16(vd + key * G::PITCH + c * 16, vbase + off, n);
+      }
+    }
+  };
+
+  // ---- first blocks on their way, then the query rows ----
+  uint32_t valid[G::STAGES];  // keys of the stage's block that count (one bit each)
+  int ahead = warp;           // next block to request
+#pragma unroll
+  for (int s = 0; s < G::STAGES - 1; ++s, ahead += kAmWarps) {
+    valid[s] = 0;
+    if (ahead < nblk) {
+      const long long r = row_of(ahead);
+      valid[s] = __ballot_sync(0xffffffffu, r >= 0);
+      request(s, r);
+    }
+    am_commit();
+  }
+  valid[G::STAGES - 1] = 0;
+  if (a.d < DP) {  // columns past the head stay zero
+    const int pad = DP * G::E / 16 - chunks;
+    for (int i = lane; i < G::STAGES * 2 * KB * pad; i += 32)
+      *reinterpret_cast<uint4*>(ring + (i / pad) * G::PITCH + (chunks + i % pad) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  for (int i = tid; i < 16 * MT * (DP / 2); i += kAmThreads) {
+    const int r = i / (DP / 2), e = i % (DP / 2) * 2;
+    float x[2] = {0.f, 0.f};
+    if (r < nrows && e < a.d) {
+      const int row = row0 + r;
+      const QT* src = static_cast<const QT*>(a.q) + a.q_stride * (row / a.group) +
+                      static_cast<long long>(g * a.group + row % a.group) * a.d + e;
+      if constexpr (sizeof(QT) == 4) {
+        x[0] = src[0], x[1] = src[1];
+      } else {
+        x[0] = bf16_to_f32(src[0]), x[1] = bf16_to_f32(src[1]);
+      }
+    }
+    if constexpr (F32) {
+      // in the order of the A fragments: [m tile][part][k step][lane][register]
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int k = (e + j) % 8, ln = (r % 8) * 4 + k % 4, reg = (r % 16) / 8 + 2 * (k / 4);
+        uint32_t hi, lo;
+        am_split_tf32(x[j], &hi, &lo);
+        uint32_t* f = reinterpret_cast<uint32_t*>(am_raw) + (((r / 16) * 2 * NT + (e + j) / 8) * 32 + ln) * 4 + reg;
+        f[0] = hi;
+        f[NT * 32 * 4] = lo;
+      }
+    } else {
+      uint32_t p[QP];
+      am_split_bf16<QP>(x[0], x[1], p);
+#pragma unroll
+      for (int part = 0; part < QP; ++part)
+        *reinterpret_cast<uint32_t*>(am_raw + (part * 16 * MT + r) * G::PITCH + e * 2) = p[part];
+    }
+  }
+  __syncthreads();
+
+  const bool two = MT == 1 || nrows > 16;  // the second row tile holds rows
+
+  // ---- main loop ----
+  float o[MT][NT][4] = {};
+  float mref[MT][2], l[MT][2];
+#pragma unroll
+  for (int t = 0; t < MT; ++t) mref[t][0] = mref[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
+  const uint32_t q32 = smem_u32(am_raw);
+  int stage = 0;
+  for (int blk = warp; blk < nblk; blk += kAmWarps) {
+    am_wait<G::STAGES - 2>();
+    __syncwarp();  // this block has landed, and every lane is done with the block before it
+    {
+      const int s = stage == 0 ? G::STAGES - 1 : stage - 1;
+      uint32_t v = 0;
+      if (ahead < nblk) {
+        const long long r = row_of(ahead);
+        v = __ballot_sync(0xffffffffu, r >= 0);
+        request(s, r);
+      }
+      am_commit();
+      ahead += kAmWarps;
+#pragma unroll
+      for (int i = 0; i < G::STAGES; ++i)
+        if (i == s) valid[i] = v;
+    }
+    uint32_t ok = 0;
+#pragma unroll
+    for (int i = 0; i < G::STAGES; ++i)
+      if (i == stage) ok = valid[i];
+    const uint32_t kt = ring32 + stage * 2 * G::TILE, vt = kt + G::TILE;
+    constexpr int ST = KB / 8;  // score tiles of 8 keys
+    float s[MT][ST][4] = {};
+    if constexpr (!F32) {
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        uint32_t b[4];
+        am_ld4(b, kt + ((lane >> 4) * 8 + (lane & 7)) * G::PITCH + kk * 32 + ((lane >> 3) & 1) * 16);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int part = 0; part < QP; ++part) {
+            if (t == 1 && !two) continue;
+            uint32_t qa[4];
+            am_ld4(qa, q32 + (part * 16 * MT + t * 16 + (lane & 15)) * G::PITCH + kk * 32 + (lane >> 4) * 16);
+            am_mma16(s[t][0], qa, b[0], b[1]);
+            am_mma16(s[t][1], qa, b[2], b[3]);
+          }
+      }
+    } else {
+      float s2[MT][4] = {}, s3[MT][4] = {};  // the remainders' products, chains of their own
+#pragma unroll
+      for (int kk = 0; kk < DP / 16; ++kk) {
+        uint32_t b[4];
+        am_ld4(b, kt + (lane & 7) * G::PITCH + kk * 64 + (lane >> 3) * 16);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t bh0, bl0, bh1, bl1;
+          am_split_tf32(__uint_as_float(b[2 * h]), &bh0, &bl0);
+          am_split_tf32(__uint_as_float(b[2 * h + 1]), &bh1, &bl1);
+#pragma unroll
+          for (int t = 0; t < MT; ++t) {
+            const uint4* f = reinterpret_cast<const uint4*>(am_raw) + ((t * 2 * NT + 2 * kk + h) * 32 + lane);
+            const uint4 fh = f[0], fl = f[NT * 32];
+            const uint32_t qh[4] = {fh.x, fh.y, fh.z, fh.w}, ql[4] = {fl.x, fl.y, fl.z, fl.w};
+            am_mma8(s[t][0], qh, bh0, bh1);
+            am_mma8(s2[t], qh, bl0, bl1);
+            am_mma8(s3[t], ql, bh0, bh1);
+          }
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[t][0][j] += s2[t][j] + s3[t][j];
+    }
+    // scale and mask: register j of tile n is key 8 n + 2 (lane % 4) + j % 2
+#pragma unroll
+    for (int t = 0; t < MT; ++t)
+#pragma unroll
+      for (int n = 0; n < ST; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          s[t][n][j] = (ok >> (n * 8 + 2 * (lane & 3) + (j & 1))) & 1u ? s[t][n][j] * a.scale_log2 : -INFINITY;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+      if (t == 1 && !two) continue;
+      float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+      for (int n = 0; n < ST; ++n)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j >> 1] = fmaxf(mx[j >> 1], s[t][n][j]);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+      }
+      const bool move = mx[0] > mref[t][0] + kAmMargin || mx[1] > mref[t][1] + kAmMargin;
+      if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          const float nr = mx[h] > mref[t][h] + kAmMargin ? mx[h] : mref[t][h];
+          const float f = nr == mref[t][h] ? 1.f : am_exp2(mref[t][h] - nr);  // 0 on the first move
+          mref[t][h] = nr;
+          l[t][h] *= f;
+#pragma unroll
+          for (int n = 0; n < NT; ++n) o[t][n][2 * h] *= f, o[t][n][2 * h + 1] *= f;
+        }
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float m = mref[t][h] == -INFINITY ? 0.f : mref[t][h];  // nothing seen yet: every term is 0
+        float sum = 0.f;
+#pragma unroll
+        for (int n = 0; n < ST; ++n)
+#pragma unroll
+          for (int j = 2 * h; j < 2 * h + 2; ++j) {
+            s[t][n][j] = am_exp2(s[t][n][j] - m);
+            sum += s[t][n][j];
+          }
+        l[t][h] += sum;  // this thread's keys only
+      }
+    }
+    if constexpr (!F32) {
+      uint32_t pa[MT][PP][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          uint32_t p[PP];
+          am_split_bf16<PP>(s[t][r >> 1][(r & 1) * 2], s[t][r >> 1][(r & 1) * 2 + 1], p);
+#pragma unroll
+          for (int part = 0; part < PP; ++part) pa[t][part][r] = p[part];
+        }
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        uint32_t b[4];
+        am_ld4t(b, vt + (((lane >> 3) & 1) * 8 + (lane & 7)) * G::PITCH + n * 16 + (lane >> 4) * 16);
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+#pragma unroll
+          for (int part = 0; part < PP; ++part) {
+            if (t == 1 && !two) continue;
+            am_mma16(o[t][n], pa[t][part], b[0], b[1]);
+            am_mma16(o[t][n + 1], pa[t][part], b[2], b[3]);
+          }
+      }
+    } else {
+      // A column c is key 2 c, column c + 4 key 2 c + 1: the scores' own registers
+      uint32_t ph[MT][4], pl[MT][4];
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        am_split_tf32(s[t][0][0], &ph[t][0], &pl[t][0]);
+        am_split_tf32(s[t][0][2], &ph[t][1], &pl[t][1]);
+        am_split_tf32(s[t][0][1], &ph[t][2], &pl[t][2]);
+        am_split_tf32(s[t][0][3], &ph[t][3], &pl[t][3]);
+      }
+      const unsigned char* vrow = ring + stage * 2 * G::TILE + G::TILE + 2 * (lane & 3) * G::PITCH + (lane >> 2) * 4;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        uint32_t bh0, bl0, bh1, bl1;
+        am_split_tf32(*reinterpret_cast<const float*>(vrow + n * 32), &bh0, &bl0);
+        am_split_tf32(*reinterpret_cast<const float*>(vrow + G::PITCH + n * 32), &bh1, &bl1);
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+          am_mma8(o[t][n], ph[t], bh0, bh1);
+          am_mma8(o[t][n], ph[t], bl0, bl1);
+          am_mma8(o[t][n], pl[t], bh0, bh1);
+        }
+      }
+    }
+    stage = stage == G::STAGES - 1 ? 0 : stage + 1;
+  }
+  am_wait<0>();
+
+  // ---- join the four warps ----
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 1);
+      l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 2);
+      if ((lane & 3) == 0) {
+        s_m[warp][t * 16 + h * 8 + (lane >> 2)] = mref[t][h];
+        s_l[warp][t * 16 + h * 8 + (lane >> 2)] = l[t][h];
+      }
+    }
+  __syncthreads();  // every warp is past its ring
+  float* join = reinterpret_cast<float*>(am_raw + G::QBYTES);
+#pragma unroll
+  for (int t = 0; t < MT; ++t)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = t * 16 + h * 8 + (lane >> 2);
+      float m = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < kAmWarps; ++w) m = fmaxf(m, s_m[w][r]);
+      const float f = m == -INFINITY ? 1.f : am_exp2(mref[t][h] - m);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+        *reinterpret_cast<float2*>(join + (warp * 16 * MT + r) * DP + n * 8 + 2 * (lane & 3)) =
+            make_float2(o[t][n][2 * h] * f, o[t][n][2 * h + 1] * f);
+    }
+  __syncthreads();
+  const long long total_rows = static_cast<long long>(a.batch) * a.n_q;
+  for (int i = tid; i < nrows * (a.d / 4); i += kAmThreads) {
+    const int r = i / (a.d / 4), e = i % (a.d / 4) * 4, row = row0 + r;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kAmWarps; ++w) {
+      const float4 y = *reinterpret_cast<const float4*>(join + (w * 16 * MT + r) * DP + e);
+      x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+    }
+    const long long at = slot * total_rows + static_cast<long long>(row / a.group) * a.n_q + g * a.group + row % a.group;
+    *reinterpret_cast<float4*>(a.part_o + at * a.d + e) = x;
+    if (e == 0) {
+      float m = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < kAmWarps; ++w) m = fmaxf(m, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < kAmWarps; ++w) sum += m == -INFINITY ? s_l[w][r] : s_l[w][r] * am_exp2(s_m[w][r] - m);
+      a.part_ml[at] = make_float2(m, sum);
+    }
+  }
+}
+
+// Launches attn_mma_kernel for a head size and row tiles (1 or 2); sets the
+// kernel's shared-memory limit on its first launch on a device.
+template <typename QT, int DP, int QP, int MT, bool F32>
+cudaError_t am_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) {
+  constexpr size_t smem = AmGeom<DP, QP, MT, F32>::SMEM;
+  static bool lifted[64] = {};
+  if (!lifted[dev]) {
+    const cudaError_t e = allow_smem(attn_mma_kernel<QT, DP, QP, MT, F32>, smem);
+    if (e != cudaSuccess) return e;
+    lifted[dev] = true;
+  }
+  return launch_k(attn_mma_kernel<QT, DP, QP, MT, F32>, dim3(items), dim3(kAmThreads), smem, st, false, a);
+}
+
+template <typename QT, int QP, int MT, bool F32>
+cudaError_t am_launch_head(const AmArgs& a, int items, int dev, cudaStream_t st) {
+  if (a.d <= 16) return am_launch_one<QT, 16, QP, MT, F32>(a, items, dev, st);
+  if (a.d <= 64) return am_launch_one<QT, 64, QP, MT, F32>(a, items, dev, st);
+  return am_launch_one<QT, 128, QP, MT, F32>(a, items, dev, st);
+}
+
+// bfloat16 and float32 caches (attn_shared.cu, attn_shared_f32.cu).
+cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st);
+cudaError_t am_launch_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st);
+
+}  // namespace wsg
