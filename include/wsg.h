@@ -566,8 +566,8 @@ dec_status attn_shared_prefix(const attn_shared_args* a, void* stream);
 
 /* Beam search's selection: the n_out best of the beams x vocab continuations
  * by scores[b] + log_softmax(logits[b])[v], best first; of equal ones the
- * lowest b * vocab + v comes first (log-softmax and comparison in double over
- * float32 exponentials). out_scores float32, out_parents (b) and out_tokens
+ * lowest b * vocab + v comes first (candidates are compared in 48 bits, over a
+ * float32 sum of exponentials). out_scores float32, out_parents (b) and out_tokens
  * (v) int32 [n_out]. A logit of -inf or NaN is never chosen (NaN counts as
  * masked, as in the greedy argmax); a beam whose score is not finite, whose
  * logits hold +inf, or which has no finite logit offers nothing. Slots that

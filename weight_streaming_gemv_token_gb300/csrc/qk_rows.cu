@@ -7,9 +7,9 @@
 // angle t becomes (a cos t - b sin t, a sin t + b cos t), t = position * w_i.
 // The angle is kept in turns as a 64-bit fixed-point fraction, F_i = frac(w_i /
 // 2 pi) * 2^64: position * F_i modulo 2^64 is the exact fraction of a turn for
-// that F_i, by integer multiplication, so a far position costs no precision
-// (F_i is off by at most 2^-54 turns: under 2^-22 turns at position 2^31) and
-// no double arithmetic per row. The top 32 bits go to sincospif.
+// that F_i, by integer multiplication, so a far position costs no precision (F_i
+// keeps every bit of w_i) and nothing runs on the slow double pipe. The top 32
+// bits go to sincospif.
 //
 // Layout: a unit of lanes holds one head, 8 consecutive elements a lane (one
 // 16-byte load of bfloat16, two of float32), and walks several heads of one row
@@ -28,6 +28,7 @@ namespace wsg {
 namespace {
 
 constexpr int kRowsThreads = 256;
+constexpr int kRowsBatch = 4;  // heads whose loads go out together
 
 struct QkRowsArgs {
   const void *q, *k, *v;
@@ -49,32 +50,6 @@ struct QkRowsArgs {
   int n_seq, base_pos;
   uint32_t* err;
 };
-
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, bool vec, float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
-    if (vec) {
-      const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-      x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = p[e];
-    }
-  } else {
-    if (vec) {
-      const uint4 a = *reinterpret_cast<const uint4*>(p);
-      const uint32_t w[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        x[2 * e] = __uint_as_float(w[e] << 16);
-        x[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-      }
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = bf16_to_f32(p[e]);
-    }
-  }
-}
 
 // Two floats as packed bfloat16 (low half: x), rounded to nearest even (NaN stays NaN).
 __device__ __forceinline__ uint32_t pack2(float x, float y) {
@@ -106,14 +81,69 @@ __device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
   }
 }
 
+// frac(w / 2 pi) * 2^64 for w in radians, in integers: |w| = M 2^(E - 63) with a
+// 64-bit M, 1 / 2 pi = C 2^-66, so the product is (M C) 2^(E - 129).
+__device__ __forceinline__ unsigned long long turns64(double w) {
+  const unsigned long long bits = static_cast<unsigned long long>(__double_as_longlong(w));
+  const int E = static_cast<int>((bits >> 52) & 0x7FFu) - 1023;
+  const unsigned long long M = (bits << 11) | 0x8000000000000000ull, C = 0xA2F9836E4E441529ull;  // 2 / pi * 2^64
+  const unsigned long long hi = __umul64hi(M, C), lo = M * C;
+  unsigned long long f;  // floor(M C 2^(E - 65)) mod 2^64
+  if (E <= 1)
+    f = E > -63 ? hi >> (1 - E) : 0;
+  else if (E <= 64)
+    f = (hi << (E - 1)) | (lo >> (65 - E));
+  else
+    f = 0;  // beyond 2^65 radians a position the double itself holds no fraction of a turn
+  return static_cast<long long>(bits) < 0 ? 0ull - f : f;
+}
+
 // Cosine and sine of position * w, w in radians per position.
 __device__ __forceinline__ void turn(double w, uint32_t pos, float factor, float* c, float* s) {
-  const double f = w * 0.15915494309189533577;  // turns per position
-  const unsigned long long F = static_cast<unsigned long long>((f - floor(f)) * 18446744073709551616.0);
-  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>((F * pos) >> 32));
+  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>((turns64(w) * pos) >> 32));
   sincospif(static_cast<float>(t) * 0x1p-31f, s, c);  // in half turns
   *c *= factor;
   *s *= factor;
+}
+
+// 8 elements as they lie in memory.
+template <typename T>
+struct Raw8 {
+  uint4 w[sizeof(T) == 4 ? 2 : 1];
+};
+
+template <typename T>
+__device__ __forceinline__ Raw8<T> fetch8(const T* p, bool vec) {
+  Raw8<T> r;
+  if (vec) {
+    r.w[0] = reinterpret_cast<const uint4*>(p)[0];
+    if constexpr (sizeof(T) == 4) r.w[1] = reinterpret_cast<const uint4*>(p)[1];
+  } else {
+    uint32_t v[4 * sizeof(r.w) / sizeof(uint4)];
+#pragma unroll
+    for (int i = 0; i < static_cast<int>(sizeof(v) / 4); ++i) {
+      if constexpr (sizeof(T) == 4)
+        v[i] = __float_as_uint(p[i]);
+      else
+        v[i] = p[2 * i] | (static_cast<uint32_t>(p[2 * i + 1]) << 16);
+    }
+    r.w[0] = make_uint4(v[0], v[1], v[2], v[3]);
+    if constexpr (sizeof(T) == 4) r.w[1] = make_uint4(v[4], v[5], v[6], v[7]);
+  }
+  return r;
+}
+
+template <typename T>
+__device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
+  const uint32_t a[4] = {r.w[0].x, r.w[0].y, r.w[0].z, r.w[0].w};
+  if constexpr (sizeof(T) == 4) {
+    const uint32_t b[4] = {r.w[1].x, r.w[1].y, r.w[1].z, r.w[1].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = __uint_as_float(a[e]), x[4 + e] = __uint_as_float(b[e]);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[2 * e] = __uint_as_float(a[e] << 16), x[2 * e + 1] = __uint_as_float(a[e] & 0xFFFF0000u);
+  }
 }
 
 // LPH: lanes of a unit (a power of two, 8 LPH >= d).
@@ -142,6 +172,11 @@ __global__ void __launch_bounds__(kRowsThreads) qk_rows_kernel(const QkRowsArgs 
       atomicOr(a.err, ERR_BAD_PAGE);
   }
 
+  // lane that holds the partners (half layout in whole lanes)
+  const bool whole = (half & 7) == 0;
+  const int shift = half >> 3;
+  const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? shift : -shift);
+
   // element e of this lane: y = x * cs + partner * sn (sn carries the sign)
   float cs[8], sn[8];
   bool turned[8];
@@ -157,6 +192,21 @@ __global__ void __launch_bounds__(kRowsThreads) qk_rows_kernel(const QkRowsArgs 
       sn[2 * j + 1] = s;
       turned[2 * j] = turned[2 * j + 1] = t;
     }
+  } else if (whole) {
+    // a lane and its mate turn the same 8 pairs: each computes four of them
+    const bool t = live && e0 < a.rot, upper = e0 >= half;
+    const int p0 = upper ? e0 - half + 4 : e0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float c = 1.f, s = 0.f;
+      if (t) turn(a.inv_freq[p0 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
+      const float c2 = __shfl_sync(0xffffffffu, c, mate), s2 = __shfl_sync(0xffffffffu, s, mate);
+      cs[j] = upper ? c2 : c;
+      cs[4 + j] = upper ? c : c2;
+      sn[j] = upper ? s2 : -s;
+      sn[4 + j] = upper ? s : -s2;
+      turned[j] = turned[4 + j] = t;
+    }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
@@ -169,61 +219,78 @@ __global__ void __launch_bounds__(kRowsThreads) qk_rows_kernel(const QkRowsArgs 
       turned[j] = t;
     }
   }
-  // lane that holds the partners (half layout in whole lanes)
-  const bool whole = (half & 7) == 0;
-  const int shift = half >> 3;
-  const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? shift : -shift);
 
-  for (int i = 0; i < a.per_unit; ++i) {
-    const int h = h0 + i;
-    const bool on = live && h < a.heads;
-    const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;  // query, key, value
-    const int hh = kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv;
-    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (on) {
-      const XT* src = static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                      (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * r + hh * a.d + e0;
-      load8(src, a.vec_x, x);
+  float gain[8];
+  int gain_of = -1;
+  for (int i0 = 0; i0 < a.per_unit; i0 += kRowsBatch) {
+    // the loads of a batch of heads first
+    Raw8<XT> raw[kRowsBatch];
+#pragma unroll
+    for (int i = 0; i < kRowsBatch; ++i) {
+      const int h = h0 + i0 + i;
+      const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;  // query, key, value
+      const int hh = kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv;
+      raw[i].w[0] = make_uint4(0, 0, 0, 0);
+      if constexpr (sizeof(XT) == 4) raw[i].w[1] = make_uint4(0, 0, 0, 0);
+      if (live && i0 + i < a.per_unit && h < a.heads)
+        raw[i] = fetch8(static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                            (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * r + hh * a.d + e0,
+                        a.vec_x);
     }
-    const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
-    float ss = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+    for (int i = 0; i < kRowsBatch; ++i) {
+      if (i0 + i >= a.per_unit) break;
+      const int h = h0 + i0 + i;
+      const bool on = live && h < a.heads;
+      const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;
+      const int hh = kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv;
+      float x[8];
+      widen8(raw[i], x);
+      const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
+      if (on && g && gain_of != kind) {
+        gain_of = kind;
 #pragma unroll
-    for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (g && on) {
-      const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * g[e0 + e];
-    }
-    float y[8];
-    if (a.interleaved) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = turned[e] && kind < 2 ? fmaf(x[e ^ 1], sn[e], x[e] * cs[e]) : x[e];
-    } else if (whole) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float p = __shfl_sync(0xffffffffu, x[e], mate);
-        y[e] = turned[e] && kind < 2 ? fmaf(p, sn[e], x[e] * cs[e]) : x[e];
+        for (int e = 0; e < 8; ++e) gain[e] = g[e0 + e];
       }
-    } else {
-      float* st = stage + (tid - li) * 8;
-      __syncwarp();
+      float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
-      __syncwarp();
+      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        y[e] = turned[e] && kind < 2 ? fmaf(st[e0 + e < half ? e0 + e + half : e0 + e - half], sn[e], x[e] * cs[e]) : x[e];
-    }
-    if (!on) continue;
-    if (kind == 0) {
-      store8(static_cast<YT*>(a.q_out) + a.qo_stride * r + hh * a.d + e0, a.vec_y, y);
-    } else if (!a.paged) {
-      store8(static_cast<KT*>(a.k_out) + a.ko_stride * r + hh * a.d + e0, a.vec_y, y);
-    } else if (kv_row0 >= 0) {
-      KT* dst = static_cast<KT*>(kind == 1 ? a.k_out : a.v_out);
-      store8(dst + (kv_row0 + (static_cast<long long>(hh) << a.pool.shift)) * a.d + e0, true, y);
+      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+      if (g && on) {
+        const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * gain[e];
+      }
+      float y[8];
+      if (a.interleaved) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) y[e] = turned[e] && kind < 2 ? fmaf(x[e ^ 1], sn[e], x[e] * cs[e]) : x[e];
+      } else if (whole) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float p = __shfl_sync(0xffffffffu, x[e], mate);
+          y[e] = turned[e] && kind < 2 ? fmaf(p, sn[e], x[e] * cs[e]) : x[e];
+        }
+      } else {
+        float* st = stage + (tid - li) * 8;
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          y[e] = turned[e] && kind < 2 ? fmaf(st[e0 + e < half ? e0 + e + half : e0 + e - half], sn[e], x[e] * cs[e]) : x[e];
+      }
+      if (!on) continue;
+      if (kind == 0) {
+        store8(static_cast<YT*>(a.q_out) + a.qo_stride * r + hh * a.d + e0, a.vec_y, y);
+      } else if (!a.paged) {
+        store8(static_cast<KT*>(a.k_out) + a.ko_stride * r + hh * a.d + e0, a.vec_y, y);
+      } else if (kv_row0 >= 0) {
+        KT* dst = static_cast<KT*>(kind == 1 ? a.k_out : a.v_out);
+        store8(dst + (kv_row0 + (static_cast<long long>(hh) << a.pool.shift)) * a.d + e0, true, y);
+      }
     }
   }
 }
