@@ -157,7 +157,10 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
     }
     k0 = split * a.own_chunk;
     k1 = min(n, k0 + a.own_chunk);
-    if (k0 >= k1) return;  // attn_join_kernel knows which splits hold keys
+    if (k0 >= k1) {  // attn_join_kernel knows which splits hold keys
+      pdl_wait();
+      return;
+    }
   }
   const int nblk = (k1 - k0 + KB - 1) / KB;
   const int32_t* trow = a.table + static_cast<long long>(branch) * a.pool.width;
@@ -473,12 +476,15 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
       a.part_ml[at] = make_float2(m, sum);
     }
   }
+  // This launch may run beside attn_prefix_tc_kernel: it ends after that one, so
+  // that the join, which waits for this launch, finds both.
+  pdl_wait();
 }
 
 // Launches attn_mma_kernel for a head size and row tiles (1 or 2); sets the
 // kernel's shared-memory limit on its first launch on a device.
 template <typename QT, int DP, int QP, int MT, bool F32>
-cudaError_t am_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) {
+cudaError_t am_launch_one(const AmArgs& a, int items, bool pdl, int dev, cudaStream_t st) {
   constexpr size_t smem = AmGeom<DP, QP, MT, F32>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[dev]) {
@@ -486,18 +492,19 @@ cudaError_t am_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) 
     if (e != cudaSuccess) return e;
     lifted[dev] = true;
   }
-  return launch_k(attn_mma_kernel<QT, DP, QP, MT, F32>, dim3(items), dim3(kAmThreads), smem, st, false, a);
+  return launch_k(attn_mma_kernel<QT, DP, QP, MT, F32>, dim3(items), dim3(kAmThreads), smem, st, pdl, a);
 }
 
 template <typename QT, int QP, int MT, bool F32>
-cudaError_t am_launch_head(const AmArgs& a, int items, int dev, cudaStream_t st) {
-  if (a.d <= 16) return am_launch_one<QT, 16, QP, MT, F32>(a, items, dev, st);
-  if (a.d <= 64) return am_launch_one<QT, 64, QP, MT, F32>(a, items, dev, st);
-  return am_launch_one<QT, 128, QP, MT, F32>(a, items, dev, st);
+cudaError_t am_launch_head(const AmArgs& a, int items, bool pdl, int dev, cudaStream_t st) {
+  if (a.d <= 16) return am_launch_one<QT, 16, QP, MT, F32>(a, items, pdl, dev, st);
+  if (a.d <= 64) return am_launch_one<QT, 64, QP, MT, F32>(a, items, pdl, dev, st);
+  return am_launch_one<QT, 128, QP, MT, F32>(a, items, pdl, dev, st);
 }
 
 // bfloat16 and float32 caches (attn_shared.cu, attn_shared_f32.cu).
-cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st);
+// pdl: as a programmatic dependent of attn_prefix_tc_kernel.
+cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, bool pdl, int dev, cudaStream_t st);
 cudaError_t am_launch_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st);
 
 }  // namespace wsg

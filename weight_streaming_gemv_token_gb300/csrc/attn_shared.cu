@@ -11,23 +11,25 @@
 #include <cmath>
 
 #include "attn_mma.cuh"
+#include "attn_prefix_tc.cuh"
 #include "common.h"
 
 namespace wsg {
 
-cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st) {
+cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, bool pdl, int dev, cudaStream_t st) {
   if (q_f32)
-    return mt == 2 ? am_launch_head<float, 3, 2, false>(a, items, dev, st)
-                   : am_launch_head<float, 3, 1, false>(a, items, dev, st);
-  return mt == 2 ? am_launch_head<uint16_t, 1, 2, false>(a, items, dev, st)
-                 : am_launch_head<uint16_t, 1, 1, false>(a, items, dev, st);
+    return mt == 2 ? am_launch_head<float, 3, 2, false>(a, items, pdl, dev, st)
+                   : am_launch_head<float, 3, 1, false>(a, items, pdl, dev, st);
+  return mt == 2 ? am_launch_head<uint16_t, 1, 2, false>(a, items, pdl, dev, st)
+                 : am_launch_head<uint16_t, 1, 1, false>(a, items, pdl, dev, st);
 }
 
 namespace {
 
 struct AmJoinArgs {
   int batch, n_q, d;
-  int prefix_slots, own_slots, own_chunk;
+  int warps;  // a row
+  int prefix_slots, own_chunk;
   PagePool pool;
   const int32_t* len;
   const float* part_o;
@@ -37,55 +39,101 @@ struct AmJoinArgs {
   float* lse;
 };
 
-// One warp per (branch, query head): the partial results of its slots (those
-// of the prefix, then those of the branch's own keys that hold any), in slot
-// order. Lane i holds elements 4 i .. 4 i + 3 of the head.
+// The partial results of one (branch, query head): its slots (those of the
+// prefix, then those of the branch's own keys that hold any) are dealt to
+// `warps` warps (1 or 4: four rows or one row a CTA), which join in order. Lane i
+// holds elements 4 i .. 4 i + 3 of the head.
 template <typename QT>
 __global__ void __launch_bounds__(128) attn_join_kernel(const AmJoinArgs a) {
+  __shared__ float s_m[4], s_l[4];
+  __shared__ float4 s_x[4][32];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = a.warps == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
+  const int first = a.warps == 4 ? warp : 0;
   pdl_wait();
-  const int w = blockIdx.x * 4 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
   if (w >= a.batch * a.n_q) return;
   const int b = w / a.n_q;
   const int n = a.len[b];
-  if (n < 0) return;
+  if (n < 0) return;  // (the same for the whole CTA where it works on one row)
   const long long held = n < page_capacity(a.pool) ? n : page_capacity(a.pool);
   const int slots = a.prefix_slots + static_cast<int>((held + a.own_chunk - 1) / a.own_chunk);
   const long long total = static_cast<long long>(a.batch) * a.n_q;
-  float m = -INFINITY, l = 0.f;
-  for (int s = lane; s < slots; s += 32) m = fmaxf(m, a.part_ml[s * total + w].x);
-  m = warp_max(m);
-  for (int s = lane; s < slots; s += 32) {
-    const float2 p = a.part_ml[s * total + w];
-    l += m == -INFINITY ? p.y : p.y * am_exp2(p.x - m);
-  }
-  l = warp_sum(l);
-  float x[4] = {};
   const bool in = lane * 4 < a.d;
-#pragma unroll 4
-  for (int s = 0; s < slots; ++s) {
-    const float f = m == -INFINITY ? 1.f : am_exp2(a.part_ml[s * total + w].x - m);
-    if (in) {
-      const float4 y = *reinterpret_cast<const float4*>(a.part_o + (s * total + w) * a.d + lane * 4);
-      x[0] = fmaf(y.x, f, x[0]), x[1] = fmaf(y.y, f, x[1]), x[2] = fmaf(y.z, f, x[2]), x[3] = fmaf(y.w, f, x[3]);
+  float m = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  // eight slots at a time: their loads go out together
+  for (int s0 = first; s0 < slots; s0 += 8 * a.warps) {
+    float2 p[8];
+    float4 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i * a.warps;
+      p[i] = s < slots ? a.part_ml[s * total + w] : make_float2(-INFINITY, 0.f);
+      y[i] = s < slots && in ? *reinterpret_cast<const float4*>(a.part_o + (s * total + w) * a.d + lane * 4)
+                             : make_float4(0.f, 0.f, 0.f, 0.f);
     }
+    float mn = m;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) mn = fmaxf(mn, p[i].x);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    const float f = am_exp2(m - mu);
+    l *= f;
+    x.x *= f, x.y *= f, x.z *= f, x.w *= f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      // a part whose scores are all -inf has the sum 0; a NaN in it stays one
+      const float e = p[i].x == -INFINITY ? 1.f : am_exp2(p[i].x - mu);
+      l = fmaf(p[i].y, e, l);
+      x.x = fmaf(y[i].x, e, x.x), x.y = fmaf(y[i].y, e, x.y), x.z = fmaf(y[i].z, e, x.z), x.w = fmaf(y[i].w, e, x.w);
+    }
+    m = mn;
+  }
+  if (a.warps == 4) {
+    if (lane == 0) s_m[warp] = m, s_l[warp] = l;
+    s_x[warp][lane] = x;
+    __syncthreads();
+    if (warp != 0) return;
+    float mn = m;
+#pragma unroll
+    for (int i = 1; i < 4; ++i) mn = fmaxf(mn, s_m[i]);
+    const float mu = mn == -INFINITY ? 0.f : mn;
+    l = 0.f;
+    x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float e = s_m[i] == -INFINITY ? 1.f : am_exp2(s_m[i] - mu);
+      const float4 y = s_x[i][lane];
+      l = fmaf(s_l[i], e, l);
+      x.x = fmaf(y.x, e, x.x), x.y = fmaf(y.y, e, x.y), x.z = fmaf(y.z, e, x.z), x.w = fmaf(y.w, e, x.w);
+    }
+    m = mn;
   }
   const float inv = l == 0.f ? 0.f : 1.0f / l;  // a NaN sum stays one
   if (in) {
     QT* dst = static_cast<QT*>(a.out) + a.out_stride * b + static_cast<long long>(w % a.n_q) * a.d + lane * 4;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (sizeof(QT) == 4) {
-        dst[e] = x[e] * inv;
+    const float r[4] = {x.x * inv, x.y * inv, x.z * inv, x.w * inv};
+    const bool vec = reinterpret_cast<uintptr_t>(dst) % (4 * sizeof(QT)) == 0;
+    if constexpr (sizeof(QT) == 4) {
+      if (vec) {
+        *reinterpret_cast<float4*>(dst) = make_float4(r[0], r[1], r[2], r[3]);
       } else {
-        uint32_t h;
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(0.f), "f"(x[e] * inv));
-        dst[e] = static_cast<uint16_t>(h);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = r[e];
+      }
+    } else {
+      uint32_t h[2];
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[0]) : "f"(r[1]), "f"(r[0]));
+      asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h[1]) : "f"(r[3]), "f"(r[2]));
+      if (vec) {
+        *reinterpret_cast<uint2*>(dst) = make_uint2(h[0], h[1]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) dst[e] = static_cast<uint16_t>(h[e >> 1] >> (16 * (e & 1)));
       }
     }
   }
   if (a.lse && lane == 0) a.lse[w] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
-
 
 bool attn_sizes_ok(const attn_shared_args* a) {
   auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
@@ -97,11 +145,14 @@ bool attn_sizes_ok(const attn_shared_args* a) {
 }
 
 
+constexpr int kTcRowsMin = 16;  // rows of a key/value head above which the prefix runs on tcgen05
+
 // How a call is cut up.
 struct AsPlan {
+  bool tc;  // the prefix on attn_prefix_tc_kernel (row_groups: blocks of 128 rows)
   int mt, row_groups;
   int prefix_slots, prefix_chunk, own_slots, own_chunk;
-  long long items;
+  long long prefix_items, own_items;  // CTAs
   size_t o, ml, total;  // workspace offsets and size
 };
 
@@ -111,21 +162,28 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
   const int group = a->n_q / a->n_kv, rows = a->batch * group;
   const int unit = kAmWarps * (f32 ? 8 : 16);  // keys the warps of a CTA take at once
   const long long resident = 2ll * sms;        // CTAs the GPU holds
-  p.mt = !f32 && rows > 16 ? 2 : 1;
-  p.row_groups = (rows + 16 * p.mt - 1) / (16 * p.mt);
-  // splits of an axis of `keys` keys into whole units, given that one split is `each` CTAs
-  auto cut = [&](long long keys, long long each, int* slots, int* chunk) {
+  p.tc = !f32 && a->qdtype == DEC_BF16 && a->head_dim == kApD && rows > kTcRowsMin && a->prefix_len > 0 &&
+         a->prefix_stride < 1ll << 31;
+  p.mt = !f32 && !p.tc && rows > 16 ? 2 : 1;
+  const int block = p.tc ? kApRows : 16 * p.mt;
+  p.row_groups = (rows + block - 1) / block;
+  // an axis of `keys` keys into about `want` splits of whole units
+  auto cut = [&](long long keys, long long unit, long long want, int* slots, int* chunk) {
     const long long units = (keys + unit - 1) / unit;
-    const long long want = (resident + each - 1) / each;
-    const long long per = (units + want - 1) / (want < 1 ? 1 : want);
+    if (want < 1) want = 1;
+    const long long per = (units + want - 1) / want;
     *chunk = static_cast<int>((per < 1 ? 1 : per) * unit);
     *slots = static_cast<int>((keys + *chunk - 1) / *chunk);
   };
-  cut(a->prefix_len, static_cast<long long>(a->n_kv) * p.row_groups, &p.prefix_slots, &p.prefix_chunk);
-  cut(static_cast<long long>(a->table_stride) << page_shift(a->page_size),
-      static_cast<long long>(a->batch) * a->n_kv, &p.own_slots, &p.own_chunk);
-  p.items = static_cast<long long>(p.prefix_slots) * a->n_kv * p.row_groups +
-            static_cast<long long>(p.own_slots) * a->batch * a->n_kv;
+  const long long each = static_cast<long long>(a->n_kv) * p.row_groups, own = static_cast<long long>(a->batch) * a->n_kv;
+  if (p.tc)
+    cut(a->prefix_len, kApKeys, sms / each, &p.prefix_slots, &p.prefix_chunk);
+  else
+    cut(a->prefix_len, unit, (resident + each - 1) / each, &p.prefix_slots, &p.prefix_chunk);
+  cut(static_cast<long long>(a->table_stride) << page_shift(a->page_size), unit, (resident + own - 1) / own, &p.own_slots,
+      &p.own_chunk);
+  p.prefix_items = p.prefix_slots * each;
+  p.own_items = p.own_slots * own;
   const long long parts = static_cast<long long>(p.prefix_slots + p.own_slots) * a->batch * a->n_q;
   p.o = 0;
   p.ml = (static_cast<size_t>(parts) * a->head_dim * 4 + 255) / 256 * 256;
@@ -173,7 +231,8 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   if (a->workspace_bytes < p.total)
     return fail(nullptr, DEC_ENOMEM, "attn_shared_prefix: workspace has %zu bytes, %zu needed", a->workspace_bytes,
                 p.total);
-  if (p.items >= 1ll << 31) return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: %lld work items", p.items);
+  if (p.prefix_items + p.own_items >= 1ll << 31)
+    return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: %lld work items", p.prefix_items + p.own_items);
   char* w = static_cast<char*>(a->d_workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AmArgs k{};
@@ -196,7 +255,7 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   k.len = a->seq_len;
   k.scale_log2 = a->scale * 1.44269504088896340736f;
   k.row_groups = p.row_groups;
-  k.prefix_items = p.prefix_slots * a->n_kv * p.row_groups;
+  k.prefix_items = p.tc ? 0 : static_cast<int>(p.prefix_items);
   k.prefix_chunk = p.prefix_chunk;
   k.own_chunk = p.own_chunk;
   k.own_slot0 = p.prefix_slots;
@@ -204,16 +263,46 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   k.part_ml = reinterpret_cast<float2*>(w + p.ml);
   k.err = di.err;
   const bool qf = a->qdtype == DEC_F32;
-  if (p.items > 0)
-    WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32
-                              ? am_launch_f32(k, qf, static_cast<int>(p.items), di.device, s)
-                              : am_launch_bf16(k, qf, p.mt, static_cast<int>(p.items), di.device, s));
+  if (p.tc) {
+    ApArgs t{};
+    t.q = static_cast<const uint16_t*>(a->q);
+    t.q_stride = a->q_stride;
+    t.batch = a->batch;
+    t.n_q = a->n_q;
+    t.n_kv = a->n_kv;
+    t.group = k.group;
+    t.rows = k.rows;
+    t.row_blocks = p.row_groups;
+    t.plen = a->prefix_len;
+    t.chunk = p.prefix_chunk;
+    t.scale_log2 = k.scale_log2;
+    t.part_o = k.part_o;
+    t.part_ml = k.part_ml;
+    t.err = di.err;
+    alignas(64) CUtensorMap maps[2];
+    for (int i = 0; i < 2; ++i) {
+      const dec_status m = encode_map_3d_bf16(&maps[i], i ? a->prefix_v : a->prefix_k, a->n_kv, a->prefix_len, kApD,
+                                              a->prefix_stride * kApD * 2, 64, kApKeys, nullptr);
+      if (m != DEC_OK) return m;
+    }
+    static bool lifted[64] = {};
+    if (!lifted[di.device]) {
+      WSG_CUDA_TRY(nullptr, allow_smem(attn_prefix_tc_kernel, kApSmem));
+      lifted[di.device] = true;
+    }
+    WSG_CUDA_TRY(nullptr, launch_k(attn_prefix_tc_kernel, dim3(static_cast<unsigned>(p.prefix_items)), dim3(kApThreads),
+                                   kApSmem, s, false, maps[0], maps[1], t));
+  }
+  const int items = k.prefix_items + static_cast<int>(p.own_items);
+  if (items > 0)
+    WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? am_launch_f32(k, qf, items, di.device, s)
+                                                : am_launch_bf16(k, qf, p.mt, items, p.tc, di.device, s));
   AmJoinArgs j{};
   j.batch = a->batch;
   j.n_q = a->n_q;
   j.d = a->head_dim;
   j.prefix_slots = p.prefix_slots;
-  j.own_slots = p.own_slots;
+  j.warps = p.prefix_slots + p.own_slots > 8 ? 4 : 1;
   j.own_chunk = p.own_chunk;
   j.pool = k.pool;
   j.len = a->seq_len;
@@ -222,9 +311,10 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   j.out = a->out;
   j.out_stride = a->out_stride;
   j.lse = a->lse;
-  const dim3 grid((a->batch * a->n_q + 3) / 4);
+  const int jrows = a->batch * a->n_q;
+  const dim3 grid(j.warps == 4 ? jrows : (jrows + 3) / 4);
   // a join without partial results may not overtake the stream's previous kernel
-  WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_join_kernel<float>, grid, dim3(128), 0, s, p.items > 0, j)
-                           : launch_k(attn_join_kernel<uint16_t>, grid, dim3(128), 0, s, p.items > 0, j));
+  WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_join_kernel<float>, grid, dim3(128), 0, s, p.tc || items > 0, j)
+                           : launch_k(attn_join_kernel<uint16_t>, grid, dim3(128), 0, s, p.tc || items > 0, j));
   return DEC_OK;
 }

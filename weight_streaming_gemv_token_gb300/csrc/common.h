@@ -81,4 +81,10 @@ inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 
 dec_status encode_map_2d(void* out, const void* base, long long rows, long long cols, int elem, int box_cols,
                          int box_rows, bool swizzle128, std::string* err);
 
+// The same for a bfloat16 tensor [planes][rows][cols] whose planes lie
+// plane_bytes apart (a multiple of 16): boxes of one plane, 128-byte swizzle,
+// box_cols 64. Rows past `rows` read as 0, not as the next plane.
+dec_status encode_map_3d_bf16(void* out, const void* base, long long planes, long long rows, long long cols,
+                              long long plane_bytes, int box_cols, int box_rows, std::string* err);
+
 }  // namespace wsg

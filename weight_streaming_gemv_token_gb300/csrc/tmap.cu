@@ -49,4 +49,21 @@ dec_status encode_map_2d(void* out, const void* base, long long rows, long long 
   return DEC_OK;
 }
 
+dec_status encode_map_3d_bf16(void* out, const void* base, long long planes, long long rows, long long cols,
+                              long long plane_bytes, int box_cols, int box_rows, std::string* err) {
+  auto enc = tensor_map_encoder();
+  if (!enc) return fail(err, DEC_ECUDA, "cuTensorMapEncodeTiled is not available");
+  cuuint64_t dims[3] = {static_cast<cuuint64_t>(cols), static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(planes)};
+  cuuint64_t strides[2] = {static_cast<cuuint64_t>(cols) * 2, static_cast<cuuint64_t>(plane_bytes)};
+  cuuint32_t box[3] = {static_cast<cuuint32_t>(box_cols), static_cast<cuuint32_t>(box_rows), 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  const CUresult r = enc(static_cast<CUtensorMap*>(out), CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base),
+                         dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(err, DEC_EINVAL, "cuTensorMapEncodeTiled failed (%d) for %lld planes of %lld x %lld, %lld bytes apart",
+                static_cast<int>(r), planes, rows, cols, plane_bytes);
+  return DEC_OK;
+}
+
 }  // namespace wsg
