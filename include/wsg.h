@@ -474,7 +474,7 @@ dec_status rope_frequencies(const rope_scaling* s, double* h_inv_freq, float* h_
  * once. positions[r] < 0 marks a padded row: its outputs are left as they
  * were. q_out may be q itself (same dtype and stride), k_out likewise. */
 typedef struct {
-  int32_t rows, n_q, n_kv, head_dim; /* n_q or n_kv may be 0 */
+  int32_t rows, n_q, n_kv, head_dim; /* n_q or n_kv may be 0; each at most 16384 */
   int32_t xdtype, ydtype;            /* q, k; q_out, k_out: DEC_F32 or DEC_BF16 */
   const void *q, *k;
   void *q_out, *k_out;

@@ -15,9 +15,9 @@
 // 16-byte load of bfloat16, two of float32), and walks several heads of one row
 // so that the row's cosines and sines are computed once and stay in registers.
 // The half layout pairs element i with i + rot / 2, which another lane of the
-// unit holds (a shuffle; a staged copy in shared memory where rot / 2 is not a
-// multiple of 8); interleaved pairs lie inside a lane. Reads and writes each
-// element once: bound by memory for many rows, by latency for few.
+// unit holds (a shuffle); interleaved pairs lie inside a lane; partners that
+// straddle lanes go through shared memory. Each element is read and written once:
+// bound by memory for many rows, by latency for few.
 #include <cmath>
 
 #include "common.h"
@@ -41,8 +41,8 @@ struct QkRowsArgs {
   int rows, n_q, n_kv, d, rot, interleaved;
   int heads;     // n_q + n_kv (+ n_kv value heads)
   int per_unit;  // heads a unit walks
-  int units_per_row;
   int vec_x, vec_y;  // 16-byte accesses possible
+  int y_f32, kv_f32;  // type of q_out (and k_out of qk_norm_rope), of the pools
   int paged;
   PagePool pool;
   const int32_t* table;
@@ -58,9 +58,10 @@ __device__ __forceinline__ uint32_t pack2(float x, float y) {
   return h;
 }
 
-template <typename T>
-__device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
-  if constexpr (sizeof(T) == 4) {
+// 8 elements to float32 or bfloat16 memory, rounded once.
+__device__ __forceinline__ void put8(void* base, long long at, int f32, int vec, const float (&x)[8]) {
+  if (f32) {
+    float* p = static_cast<float*>(base) + at;
     if (vec) {
       reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
       reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
@@ -69,6 +70,7 @@ __device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
       for (int e = 0; e < 8; ++e) p[e] = x[e];
     }
   } else {
+    uint16_t* p = static_cast<uint16_t*>(base) + at;
     uint32_t w[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) w[e] = pack2(x[2 * e], x[2 * e + 1]);
@@ -76,7 +78,7 @@ __device__ __forceinline__ void store8(T* p, bool vec, const float (&x)[8]) {
       *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
     } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) p[e] = static_cast<T>(w[e >> 1] >> (16 * (e & 1)));
+      for (int e = 0; e < 8; ++e) p[e] = static_cast<uint16_t>(w[e >> 1] >> (16 * (e & 1)));
     }
   }
 }
@@ -146,167 +148,186 @@ __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
   }
 }
 
-// LPH: lanes of a unit (a power of two, 8 LPH >= d).
-template <typename XT, typename YT, typename KT, int LPH>
-__global__ void __launch_bounds__(kRowsThreads) qk_rows_kernel(const QkRowsArgs a) {
-  __shared__ float stage[kRowsThreads * 8];
-  const int tid = threadIdx.x, li = tid % LPH;
-  const long long unit = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
-  const int r = static_cast<int>(unit / a.units_per_row);
-  const int h0 = static_cast<int>(unit % a.units_per_row) * a.per_unit;
-  const int e0 = li * 8;
-  const bool inside = r < a.rows && e0 < a.d;
+// How a head's pairs lie in its lanes.
+enum PairMode : int {
+  PAIR_LANES = 0,   // half layout, rot / 2 a multiple of 8: whole lanes are partners
+  PAIR_INSIDE = 1,  // interleaved, rot a multiple of 8: inside a lane
+  PAIR_STAGED = 2   // any other: through shared memory, decided for each element
+};
+
+// One unit of LPH lanes (a power of two, 8 LPH >= d) per row; blockIdx.y is the
+// group of per_unit heads that the CTA's units walk, so that the kind of head
+// (query, key, value) is the same for the whole CTA.
+template <typename XT, int LPH, int MODE>
+__global__ void __launch_bounds__(kRowsThreads, sizeof(XT) == 4 ? 3 : 4) qk_rows_kernel(const QkRowsArgs a) {
+  __shared__ float stage[MODE == PAIR_STAGED ? kRowsThreads * 8 : 1];
+  const int tid = threadIdx.x, li = tid % LPH, e0 = li * 8;
+  const int r = static_cast<int>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
+  const int h0 = blockIdx.y * a.per_unit, h1 = min(h0 + a.per_unit, a.heads);
   const int pos = r < a.rows ? a.pos[r] : -1;
-  const bool live = inside && pos >= 0;
+  const bool live = pos >= 0 && e0 < a.d;
   const int half = a.rot >> 1;
 
   // where this row's keys and values go
   long long kv_row0 = -1;
-  if (a.paged && live) {
+  if (a.paged && live && h1 > a.n_q) {
     const int s = a.seq ? a.seq[r] : r;
     const long long idx = static_cast<long long>(pos) - a.base_pos;
     const int page = s >= 0 && s < a.n_seq ? page_of(a.pool, a.table + static_cast<long long>(s) * a.pool.width, idx) : -1;
     if (page >= 0)
       kv_row0 = pool_row(a.pool, page, 0, idx);
-    else if (li == 0 && h0 + a.per_unit > a.n_q)
+    else if (li == 0)
       atomicOr(a.err, ERR_BAD_PAGE);
   }
-
-  // lane that holds the partners (half layout in whole lanes)
-  const bool whole = (half & 7) == 0;
-  const int shift = half >> 3;
-  const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? shift : -shift);
+  auto kind_of = [&](int h) { return h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2; };
+  auto within = [&](int h, int kind) { return kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv; };
+  // the loads of a batch of heads go out together, the first batch's before the angles are computed
+  Raw8<XT> raw[kRowsBatch];
+  auto fetch = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < kRowsBatch; ++i) {
+      const int h = b0 + i, kind = kind_of(h);
+      if (live && h < h1) {
+        const XT* src = static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
+                        (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * r + within(h, kind) * a.d + e0;
+        raw[i] = fetch8(src, a.vec_x);
+      } else {
+        raw[i] = Raw8<XT>{};
+      }
+    }
+  };
+  fetch(h0);
 
   // element e of this lane: y = x * cs + partner * sn (sn carries the sign)
-  float cs[8], sn[8];
-  bool turned[8];
-  if (a.interleaved) {
+  constexpr int NC = MODE == PAIR_INSIDE ? 4 : 8;
+  float cs[NC], sn[NC];
+  bool turned = live && e0 < a.rot;  // PAIR_STAGED: some of the elements
+  const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? half >> 3 : -(half >> 3));  // PAIR_LANES
+  if (MODE == PAIR_INSIDE) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int e = e0 + 2 * j;
-      float c = 1.f, s = 0.f;
-      const bool t = live && e < a.rot;
-      if (t) turn(a.inv_freq[e >> 1], static_cast<uint32_t>(pos), a.factor, &c, &s);
-      cs[2 * j] = cs[2 * j + 1] = c;
-      sn[2 * j] = -s;
-      sn[2 * j + 1] = s;
-      turned[2 * j] = turned[2 * j + 1] = t;
+      cs[j] = 1.f, sn[j] = 0.f;
+      if (turned) turn(a.inv_freq[e0 / 2 + j], static_cast<uint32_t>(pos), a.factor, &cs[j], &sn[j]);
     }
-  } else if (whole) {
+  } else if (MODE == PAIR_LANES) {
     // a lane and its mate turn the same 8 pairs: each computes four of them
-    const bool t = live && e0 < a.rot, upper = e0 >= half;
+    const bool upper = e0 >= half;
     const int p0 = upper ? e0 - half + 4 : e0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       float c = 1.f, s = 0.f;
-      if (t) turn(a.inv_freq[p0 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
+      if (turned) turn(a.inv_freq[p0 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
       const float c2 = __shfl_sync(0xffffffffu, c, mate), s2 = __shfl_sync(0xffffffffu, s, mate);
       cs[j] = upper ? c2 : c;
-      cs[4 + j] = upper ? c : c2;
+      cs[j + 4] = upper ? c : c2;
       sn[j] = upper ? s2 : -s;
-      sn[4 + j] = upper ? s : -s2;
-      turned[j] = turned[4 + j] = t;
+      sn[j + 4] = upper ? s : -s2;
     }
   } else {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int e = e0 + j;
       float c = 1.f, s = 0.f;
-      const bool t = live && e < a.rot;
-      if (t) turn(a.inv_freq[e < half ? e : e - half], static_cast<uint32_t>(pos), a.factor, &c, &s);
+      const bool upper = a.interleaved ? e & 1 : e >= half;
+      if (turned && e < a.rot)
+        turn(a.inv_freq[a.interleaved ? e >> 1 : upper ? e - half : e], static_cast<uint32_t>(pos), a.factor, &c, &s);
       cs[j] = c;
-      sn[j] = e < half ? -s : s;
-      turned[j] = t;
+      sn[j] = upper ? s : -s;
     }
   }
 
   float gain[8];
   int gain_of = -1;
-  for (int i0 = 0; i0 < a.per_unit; i0 += kRowsBatch) {
-    // the loads of a batch of heads first
-    Raw8<XT> raw[kRowsBatch];
+  const float mean = 1.f / static_cast<float>(a.d);
+  for (int b0 = h0; b0 < h1; b0 += kRowsBatch) {
+    if (b0 != h0) fetch(b0);
 #pragma unroll
     for (int i = 0; i < kRowsBatch; ++i) {
-      const int h = h0 + i0 + i;
-      const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;  // query, key, value
-      const int hh = kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv;
-      raw[i].w[0] = make_uint4(0, 0, 0, 0);
-      if constexpr (sizeof(XT) == 4) raw[i].w[1] = make_uint4(0, 0, 0, 0);
-      if (live && i0 + i < a.per_unit && h < a.heads)
-        raw[i] = fetch8(static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                            (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * r + hh * a.d + e0,
-                        a.vec_x);
-    }
-#pragma unroll
-    for (int i = 0; i < kRowsBatch; ++i) {
-      if (i0 + i >= a.per_unit) break;
-      const int h = h0 + i0 + i;
-      const bool on = live && h < a.heads;
-      const int kind = h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2;
-      const int hh = kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv;
+      const int h = b0 + i;
+      if (h >= h1) break;
+      const int kind = kind_of(h), hh = within(h, kind);
       float x[8];
       widen8(raw[i], x);
       const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
-      if (on && g && gain_of != kind) {
-        gain_of = kind;
+      if (g) {
+        if (gain_of != kind) {
+          gain_of = kind;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) gain[e] = g[e0 + e];
-      }
-      float ss = 0.f;
+          for (int e = 0; e < 8; ++e) gain[e] = e0 < a.d ? g[e0 + e] : 0.f;
+        }
+        float ss = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-      for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (g && on) {
-        const float inv = 1.0f / sqrtf(ss / static_cast<float>(a.d) + a.eps);
+        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        // 1 / sqrt by the approximation and one Newton step
+        const float t = fmaf(ss, mean, a.eps);
+        float inv = rsqrtf(t);
+        if (t > 0.f && t < INFINITY) inv = fmaf(0.5f * inv, fmaf(-t * inv, inv, 1.f), inv);
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * gain[e];
       }
-      float y[8];
-      if (a.interleaved) {
+      if (kind < 2) {
+        if (MODE == PAIR_INSIDE) {
+          if (turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) y[e] = turned[e] && kind < 2 ? fmaf(x[e ^ 1], sn[e], x[e] * cs[e]) : x[e];
-      } else if (whole) {
+            for (int j = 0; j < 4; ++j) {
+              const float u = x[2 * j], w = x[2 * j + 1];
+              x[2 * j] = fmaf(-w, sn[j], u * cs[j]);
+              x[2 * j + 1] = fmaf(u, sn[j], w * cs[j]);
+            }
+          }
+        } else if (MODE == PAIR_LANES) {
+          float p[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float p = __shfl_sync(0xffffffffu, x[e], mate);
-          y[e] = turned[e] && kind < 2 ? fmaf(p, sn[e], x[e] * cs[e]) : x[e];
+          for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], mate);
+          if (turned) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = fmaf(p[e], sn[e], x[e] * cs[e]);
+          }
+        } else {
+          float* st = stage + (tid - li) * 8;
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
+          __syncwarp();
+          if (turned) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const int w = e0 + e, m = a.interleaved ? w ^ 1 : w < half ? w + half : w - half;
+              if (w < a.rot) x[e] = fmaf(st[m], sn[e], x[e] * cs[e]);
+            }
+          }
         }
-      } else {
-        float* st = stage + (tid - li) * 8;
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
-        __syncwarp();
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          y[e] = turned[e] && kind < 2 ? fmaf(st[e0 + e < half ? e0 + e + half : e0 + e - half], sn[e], x[e] * cs[e]) : x[e];
       }
-      if (!on) continue;
+      if (!live) continue;
+      const long long off = hh * a.d + e0;
       if (kind == 0) {
-        store8(static_cast<YT*>(a.q_out) + a.qo_stride * r + hh * a.d + e0, a.vec_y, y);
+        put8(a.q_out, a.qo_stride * r + off, a.y_f32, a.vec_y, x);
       } else if (!a.paged) {
-        store8(static_cast<KT*>(a.k_out) + a.ko_stride * r + hh * a.d + e0, a.vec_y, y);
+        put8(a.k_out, a.ko_stride * r + off, a.y_f32, a.vec_y, x);
       } else if (kv_row0 >= 0) {
-        KT* dst = static_cast<KT*>(kind == 1 ? a.k_out : a.v_out);
-        store8(dst + (kv_row0 + (static_cast<long long>(hh) << a.pool.shift)) * a.d + e0, true, y);
+        put8(kind == 1 ? a.k_out : a.v_out, (kv_row0 + (static_cast<long long>(hh) << a.pool.shift)) * a.d + e0, a.kv_f32,
+             1, x);
       }
     }
   }
 }
 
-template <typename XT, typename YT, typename KT>
+template <typename XT, int LPH>
+cudaError_t launch_mode(const QkRowsArgs& a, cudaStream_t st) {
+  constexpr int kUnits = kRowsThreads / LPH;
+  const dim3 grid(static_cast<unsigned>((a.rows + static_cast<long long>(kUnits) - 1) / kUnits),
+                  static_cast<unsigned>((a.heads + a.per_unit - 1) / a.per_unit));
+  if (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0)
+    return a.interleaved ? launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE>, grid, dim3(kRowsThreads), 0, st, false, a)
+                         : launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES>, grid, dim3(kRowsThreads), 0, st, false, a);
+  return launch_k(qk_rows_kernel<XT, LPH, PAIR_STAGED>, grid, dim3(kRowsThreads), 0, st, false, a);
+}
+
+template <typename XT>
 cudaError_t launch_rows(const QkRowsArgs& a, int lph, cudaStream_t st) {
-  const long long units = static_cast<long long>(a.rows) * a.units_per_row;
-  const long long per_block = kRowsThreads / lph;
-  const dim3 grid(static_cast<unsigned>((units + per_block - 1) / per_block));
-  switch (lph) {
-    case 1: return launch_k(qk_rows_kernel<XT, YT, KT, 1>, grid, dim3(kRowsThreads), 0, st, false, a);
-    case 2: return launch_k(qk_rows_kernel<XT, YT, KT, 2>, grid, dim3(kRowsThreads), 0, st, false, a);
-    case 4: return launch_k(qk_rows_kernel<XT, YT, KT, 4>, grid, dim3(kRowsThreads), 0, st, false, a);
-    case 8: return launch_k(qk_rows_kernel<XT, YT, KT, 8>, grid, dim3(kRowsThreads), 0, st, false, a);
-    default: return launch_k(qk_rows_kernel<XT, YT, KT, 16>, grid, dim3(kRowsThreads), 0, st, false, a);
-  }
+  return lph == 2 ? launch_mode<XT, 2>(a, st) : lph == 8 ? launch_mode<XT, 8>(a, st) : launch_mode<XT, 16>(a, st);
 }
 
 bool is_float(int t) { return t == DEC_F32 || t == DEC_BF16; }
@@ -319,7 +340,7 @@ bool pieces16(const void* p, long long stride, int dtype) {
 // Checks common to both calls, on the fields they share.
 template <typename A>
 dec_status check_rows(const A* a, const char* who) {
-  if (a->rows < 0 || a->n_q < 0 || a->n_kv < 0 || a->n_q > 65535 || a->n_kv > 65535)
+  if (a->rows < 0 || a->n_q < 0 || a->n_kv < 0 || a->n_q > 16384 || a->n_kv > 16384)
     return fail(nullptr, DEC_EINVAL, "%s: rows %d, n_q %d, n_kv %d", who, a->rows, a->n_q, a->n_kv);
   if (a->head_dim < 8 || a->head_dim > 128 || a->head_dim % 8)
     return fail(nullptr, DEC_EINVAL, "%s: head_dim must be a multiple of 8 up to 128, got %d", who, a->head_dim);
@@ -360,30 +381,20 @@ QkRowsArgs shared_fields(const A* a) {
   k.d = a->head_dim;
   k.rot = a->rot_dim;
   k.interleaved = a->interleaved != 0;
+  k.y_f32 = a->ydtype == DEC_F32;
   k.vec_x = (a->n_q == 0 || pieces16(a->q, a->q_stride, a->xdtype)) && (a->n_kv == 0 || pieces16(a->k, a->k_stride, a->xdtype));
   k.vec_y = a->n_q == 0 || pieces16(a->q_out, a->q_out_stride, a->ydtype);
   return k;
 }
 
-dec_status run_rows(QkRowsArgs& k, int xd, int yd, int kd, const DeviceInfo& di, cudaStream_t st) {
-  int lph = 1;
-  while (lph * 8 < k.d) lph *= 2;
+dec_status run_rows(QkRowsArgs& k, int xd, const DeviceInfo& di, cudaStream_t st) {
+  const int lph = k.d <= 16 ? 2 : k.d <= 64 ? 8 : 16;  // lanes of a unit
   // Heads a unit walks: more share the row's angles, fewer give more units.
   k.per_unit = 1;
   while (k.per_unit < 8 && k.per_unit < k.heads &&
          static_cast<long long>(k.rows) * ((k.heads + 2 * k.per_unit - 1) / (2 * k.per_unit)) * lph >= 2048ll * di.sms)
     k.per_unit *= 2;
-  k.units_per_row = (k.heads + k.per_unit - 1) / k.per_unit;
-  cudaError_t e;
-  const bool xf = xd == DEC_F32, yf = yd == DEC_F32, kf = kd == DEC_F32;
-  using H = uint16_t;
-  if (xf)
-    e = yf ? (kf ? launch_rows<float, float, float>(k, lph, st) : launch_rows<float, float, H>(k, lph, st))
-           : (kf ? launch_rows<float, H, float>(k, lph, st) : launch_rows<float, H, H>(k, lph, st));
-  else
-    e = yf ? (kf ? launch_rows<H, float, float>(k, lph, st) : launch_rows<H, float, H>(k, lph, st))
-           : (kf ? launch_rows<H, H, float>(k, lph, st) : launch_rows<H, H, H>(k, lph, st));
-  WSG_CUDA_TRY(nullptr, e);
+  WSG_CUDA_TRY(nullptr, xd == DEC_F32 ? launch_rows<float>(k, lph, st) : launch_rows<uint16_t>(k, lph, st));
   return DEC_OK;
 }
 
@@ -439,7 +450,7 @@ extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
   k.vec_y = k.vec_y && (a->n_kv == 0 || pieces16(a->k_out, a->k_out_stride, a->ydtype));
   k.heads = a->n_q + a->n_kv;
   k.err = di.err;
-  return run_rows(k, a->xdtype, a->ydtype, a->ydtype, di, static_cast<cudaStream_t>(stream));
+  return run_rows(k, a->xdtype, di, static_cast<cudaStream_t>(stream));
 }
 
 extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
@@ -475,5 +486,6 @@ extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
   k.n_seq = a->n_seq;
   k.base_pos = a->base_pos;
   k.err = di.err;
-  return run_rows(k, a->xdtype, a->ydtype, a->kvdtype, di, static_cast<cudaStream_t>(stream));
+  k.kv_f32 = a->kvdtype == DEC_F32;
+  return run_rows(k, a->xdtype, di, static_cast<cudaStream_t>(stream));
 }
