@@ -12,8 +12,8 @@
 // bits go to sincospif.
 //
 // Layout: a unit of lanes holds one head, 8 consecutive elements a lane (one
-// 16-byte load of bfloat16, two of float32), and walks several heads of one row
-// so that the row's cosines and sines are computed once and stay in registers.
+// 16-byte load of bfloat16, two of float32), and walks several heads of a row so
+// that the row's cosines and sines are computed once and stay in registers.
 // The half layout pairs element i with i + rot / 2, which another lane of the
 // unit holds (a shuffle); interleaved pairs lie inside a lane; partners that
 // straddle lanes go through shared memory. Each element is read and written once:
@@ -28,8 +28,6 @@ namespace wsg {
 namespace {
 
 constexpr int kRowsThreads = 256;
-constexpr int kRowsBatch = 4;  // heads whose loads go out together
-
 struct QkRowsArgs {
   const void *q, *k, *v;
   void *q_out, *k_out, *v_out;  // k_out, v_out: rows, or the pools
@@ -39,8 +37,8 @@ struct QkRowsArgs {
   const double* inv_freq;
   float eps, factor;
   int rows, n_q, n_kv, d, rot, interleaved;
-  int heads;     // n_q + n_kv (+ n_kv value heads)
-  int per_unit;  // heads a unit walks
+  int per_unit;             // heads a unit walks
+  int q_groups, kv_groups;  // groups of that many query and key (or value) heads
   int vec_x, vec_y;  // 16-byte accesses possible
   int y_f32, kv_f32;  // type of q_out (and k_out of qk_norm_rope), of the pools
   int paged;
@@ -155,170 +153,182 @@ enum PairMode : int {
   PAIR_STAGED = 2   // any other: through shared memory, decided for each element
 };
 
-// One unit of LPH lanes (a power of two, 8 LPH >= d) per row; blockIdx.y is the
-// group of per_unit heads that the CTA's units walk, so that the kind of head
-// (query, key, value) is the same for the whole CTA.
+// A unit of LPH lanes (a power of two, 8 LPH >= d) walks rows; blockIdx.y is a
+// group of up to per_unit heads of one kind (queries, keys, values in turn), so
+// that what depends on the kind is settled once. The next batch of heads is
+// always on its way while one is worked on, across rows too.
 template <typename XT, int LPH, int MODE>
-__global__ void __launch_bounds__(kRowsThreads, sizeof(XT) == 4 ? 3 : 4) qk_rows_kernel(const QkRowsArgs a) {
+__global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsArgs a) {
+  constexpr int kBatch = sizeof(XT) == 4 ? 2 : 4;  // heads a batch
   __shared__ float stage[MODE == PAIR_STAGED ? kRowsThreads * 8 : 1];
   const int tid = threadIdx.x, li = tid % LPH, e0 = li * 8;
-  const int r = static_cast<int>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
-  const int h0 = blockIdx.y * a.per_unit, h1 = min(h0 + a.per_unit, a.heads);
-  const int pos = r < a.rows ? a.pos[r] : -1;
-  const bool live = pos >= 0 && e0 < a.d;
   const int half = a.rot >> 1;
-
-  // where this row's keys and values go
-  long long kv_row0 = -1;
-  if (a.paged && live && h1 > a.n_q) {
-    const int s = a.seq ? a.seq[r] : r;
-    const long long idx = static_cast<long long>(pos) - a.base_pos;
-    const int page = s >= 0 && s < a.n_seq ? page_of(a.pool, a.table + static_cast<long long>(s) * a.pool.width, idx) : -1;
-    if (page >= 0)
-      kv_row0 = pool_row(a.pool, page, 0, idx);
-    else if (li == 0)
-      atomicOr(a.err, ERR_BAD_PAGE);
-  }
-  auto kind_of = [&](int h) { return h < a.n_q ? 0 : h < a.n_q + a.n_kv ? 1 : 2; };
-  auto within = [&](int h, int kind) { return kind == 0 ? h : kind == 1 ? h - a.n_q : h - a.n_q - a.n_kv; };
-  // the loads of a batch of heads go out together, the first batch's before the angles are computed
-  Raw8<XT> raw[kRowsBatch];
-  auto fetch = [&](int b0) {
-#pragma unroll
-    for (int i = 0; i < kRowsBatch; ++i) {
-      const int h = b0 + i, kind = kind_of(h);
-      if (live && h < h1) {
-        const XT* src = static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) +
-                        (kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride) * r + within(h, kind) * a.d + e0;
-        raw[i] = fetch8(src, a.vec_x);
-      } else {
-        raw[i] = Raw8<XT>{};
-      }
-    }
-  };
-  fetch(h0);
-
-  // element e of this lane: y = x * cs + partner * sn (sn carries the sign)
-  constexpr int NC = MODE == PAIR_INSIDE ? 4 : 8;
-  float cs[NC], sn[NC];
-  bool turned = live && e0 < a.rot;  // PAIR_STAGED: some of the elements
+  int group = blockIdx.y, kind = 0;
+  if (group >= a.q_groups) group -= a.q_groups, kind = 1;
+  if (kind == 1 && group >= a.kv_groups) group -= a.kv_groups, kind = 2;
+  const int h0 = group * a.per_unit, n = min(a.per_unit, (kind == 0 ? a.n_q : a.n_kv) - h0);
+  const XT* in = static_cast<const XT*>(kind == 0 ? a.q : kind == 1 ? a.k : a.v) + h0 * a.d + e0;
+  const long long in_stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
+  void* out = kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out;
+  const bool pool = kind > 0 && a.paged;
+  const int out_f32 = pool ? a.kv_f32 : a.y_f32, vec_out = pool ? 1 : a.vec_y;
+  const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
   const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? half >> 3 : -(half >> 3));  // PAIR_LANES
-  if (MODE == PAIR_INSIDE) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      cs[j] = 1.f, sn[j] = 0.f;
-      if (turned) turn(a.inv_freq[e0 / 2 + j], static_cast<uint32_t>(pos), a.factor, &cs[j], &sn[j]);
-    }
-  } else if (MODE == PAIR_LANES) {
-    // a lane and its mate turn the same 8 pairs: each computes four of them
-    const bool upper = e0 >= half;
-    const int p0 = upper ? e0 - half + 4 : e0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      float c = 1.f, s = 0.f;
-      if (turned) turn(a.inv_freq[p0 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
-      const float c2 = __shfl_sync(0xffffffffu, c, mate), s2 = __shfl_sync(0xffffffffu, s, mate);
-      cs[j] = upper ? c2 : c;
-      cs[j + 4] = upper ? c : c2;
-      sn[j] = upper ? s2 : -s;
-      sn[j + 4] = upper ? s : -s2;
-    }
-  } else {
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const int e = e0 + j;
-      float c = 1.f, s = 0.f;
-      const bool upper = a.interleaved ? e & 1 : e >= half;
-      if (turned && e < a.rot)
-        turn(a.inv_freq[a.interleaved ? e >> 1 : upper ? e - half : e], static_cast<uint32_t>(pos), a.factor, &c, &s);
-      cs[j] = c;
-      sn[j] = upper ? s : -s;
-    }
-  }
-
-  float gain[8];
-  int gain_of = -1;
+  // the element that partners element e
+  auto partner = [&](int e) { return e >= a.rot ? e : a.interleaved ? e ^ 1 : e < half ? e + half : e - half; };
   const float mean = 1.f / static_cast<float>(a.d);
-  for (int b0 = h0; b0 < h1; b0 += kRowsBatch) {
-    if (b0 != h0) fetch(b0);
+
+  // (a padded row's elements are read for nothing)
+  Raw8<XT> next[kBatch];
+  auto fetch = [&](long long r, int b0) {
 #pragma unroll
-    for (int i = 0; i < kRowsBatch; ++i) {
-      const int h = b0 + i;
-      if (h >= h1) break;
-      const int kind = kind_of(h), hh = within(h, kind);
-      float x[8];
-      widen8(raw[i], x);
-      const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
-      if (g) {
-        if (gain_of != kind) {
-          gain_of = kind;
-#pragma unroll
-          for (int e = 0; e < 8; ++e) gain[e] = e0 < a.d ? g[e0 + e] : 0.f;
-        }
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
-#pragma unroll
-        for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        // 1 / sqrt by the approximation and one Newton step
-        const float t = fmaf(ss, mean, a.eps);
-        float inv = rsqrtf(t);
-        if (t > 0.f && t < INFINITY) inv = fmaf(0.5f * inv, fmaf(-t * inv, inv, 1.f), inv);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * gain[e];
+    for (int i = 0; i < kBatch; ++i)
+      next[i] = r < a.rows && b0 + i < n && e0 < a.d ? fetch8(in + in_stride * r + (b0 + i) * a.d, a.vec_x) : Raw8<XT>{};
+  };
+  long long r = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
+  const long long rstep = static_cast<long long>(gridDim.x) * (kRowsThreads / LPH);
+  fetch(r, 0);
+  int pos_next = r < a.rows ? a.pos[r] : -1;
+  // the trip count is the CTA's: its first unit's rows
+  for (long long rc = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH); rc < a.rows; rc += rstep, r += rstep) {
+    const int pos = pos_next;
+    const bool live = pos >= 0 && e0 < a.d;
+    pos_next = r + rstep < a.rows ? a.pos[r + rstep] : -1;
+
+    // where this row's heads go: element e0 of head h0, and from head to head
+    long long to = (kind == 0 ? a.qo_stride : a.ko_stride) * r + h0 * a.d + e0, step = a.d;
+    bool stores = live;
+    if (pool && live) {
+      const int s = a.seq ? a.seq[r] : static_cast<int>(r);
+      const long long idx = static_cast<long long>(pos) - a.base_pos;
+      const int page = s >= 0 && s < a.n_seq ? page_of(a.pool, a.table + static_cast<long long>(s) * a.pool.width, idx) : -1;
+      stores = page >= 0;
+      if (stores) {
+        to = pool_row(a.pool, page, h0, idx) * a.d + e0;
+        step = static_cast<long long>(a.d) << a.pool.shift;
+      } else if (li == 0) {
+        atomicOr(a.err, ERR_BAD_PAGE);
       }
-      if (kind < 2) {
-        if (MODE == PAIR_INSIDE) {
-          if (turned) {
+    }
+
+    // element e of this lane: y = (x * cg + partner * sg) / rms with the gains of
+    // both and the sign in cg and sg; lanes that are not turned only scale
+    const bool turned = kind < 2 && live && e0 < a.rot;  // PAIR_STAGED: some of the elements
+    float cg[8], sg[8];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float u = x[2 * j], w = x[2 * j + 1];
-              x[2 * j] = fmaf(-w, sn[j], u * cs[j]);
-              x[2 * j + 1] = fmaf(u, sn[j], w * cs[j]);
-            }
+    for (int e = 0; e < 8; ++e) cg[e] = 1.f, sg[e] = 0.f;
+    if (kind < 2 && a.rot > 0) {
+      if (MODE == PAIR_INSIDE) {
+        if (turned) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            float c, s;
+            turn(a.inv_freq[e0 / 2 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
+            cg[2 * j] = cg[2 * j + 1] = c;
+            sg[2 * j] = -s, sg[2 * j + 1] = s;
           }
-        } else if (MODE == PAIR_LANES) {
+        }
+      } else if (MODE == PAIR_LANES) {
+        // a lane and its mate turn the same 8 pairs: each computes four of them
+        const bool upper = e0 >= half;
+        const int p0 = upper ? e0 - half + 4 : e0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          float c = 1.f, s = 0.f;
+          if (turned) turn(a.inv_freq[p0 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
+          const float c2 = __shfl_sync(0xffffffffu, c, mate), s2 = __shfl_sync(0xffffffffu, s, mate);
+          cg[j] = upper ? c2 : c;
+          cg[j + 4] = upper ? c : c2;
+          sg[j] = upper ? s2 : -s;
+          sg[j + 4] = upper ? s : -s2;
+        }
+      } else if (turned) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int e = e0 + j;
+          const bool upper = a.interleaved ? e & 1 : e >= half;
+          if (e >= a.rot) continue;
+          float c, s;
+          turn(a.inv_freq[a.interleaved ? e >> 1 : upper ? e - half : e], static_cast<uint32_t>(pos), a.factor, &c, &s);
+          cg[j] = c;
+          sg[j] = upper ? s : -s;
+        }
+      }
+    }
+    if (g && e0 < a.d) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        cg[j] *= g[e0 + j];
+        if (turned) sg[j] *= g[partner(e0 + j)];
+      }
+    }
+
+    for (int b0 = 0; b0 < n; b0 += kBatch) {
+      Raw8<XT> raw[kBatch];
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) raw[i] = next[i];
+      if (b0 + kBatch < n)
+        fetch(r, b0 + kBatch);
+      else
+        fetch(r + rstep, 0);
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i) {
+        float x[8];
+        widen8(raw[i], x);
+        if (kind < 2) {
+          float inv = 1.f;
+          if (g) {
+            float ss = 0.f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+#pragma unroll
+            for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+            // 1 / sqrt by the approximation and one Newton step
+            const float t = fmaf(ss, mean, a.eps);
+            inv = rsqrtf(t);
+            if (t > 0.f && t < INFINITY) inv = fmaf(0.5f * inv, fmaf(-t * inv, inv, 1.f), inv);
+          }
           float p[8];
+          if (MODE == PAIR_INSIDE) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], mate);
-          if (turned) {
+            for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+          } else if (MODE == PAIR_LANES) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = fmaf(p[e], sn[e], x[e] * cs[e]);
+            for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], mate);
+          } else {
+            float* st = stage + (tid - li) * 8;
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
+            __syncwarp();
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = e0 + e < a.rot ? st[partner(e0 + e)] : 0.f;
           }
-        } else {
-          float* st = stage + (tid - li) * 8;
-          __syncwarp();
-#pragma unroll
-          for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
-          __syncwarp();
           if (turned) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-              const int w = e0 + e, m = a.interleaved ? w ^ 1 : w < half ? w + half : w - half;
-              if (w < a.rot) x[e] = fmaf(st[m], sn[e], x[e] * cs[e]);
+              const float y = fmaf(p[e], sg[e], x[e] * cg[e]);
+              x[e] = g ? y * inv : y;
             }
+          } else if (g) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * cg[e];
           }
         }
-      }
-      if (!live) continue;
-      const long long off = hh * a.d + e0;
-      if (kind == 0) {
-        put8(a.q_out, a.qo_stride * r + off, a.y_f32, a.vec_y, x);
-      } else if (!a.paged) {
-        put8(a.k_out, a.ko_stride * r + off, a.y_f32, a.vec_y, x);
-      } else if (kv_row0 >= 0) {
-        put8(kind == 1 ? a.k_out : a.v_out, (kv_row0 + (static_cast<long long>(hh) << a.pool.shift)) * a.d + e0, a.kv_f32,
-             1, x);
+        if (stores && b0 + i < n) put8(out, to + (b0 + i) * step, out_f32, vec_out, x);
       }
     }
   }
 }
 
 template <typename XT, int LPH>
-cudaError_t launch_mode(const QkRowsArgs& a, cudaStream_t st) {
+cudaError_t launch_mode(const QkRowsArgs& a, int sms, cudaStream_t st) {
   constexpr int kUnits = kRowsThreads / LPH;
-  const dim3 grid(static_cast<unsigned>((a.rows + static_cast<long long>(kUnits) - 1) / kUnits),
-                  static_cast<unsigned>((a.heads + a.per_unit - 1) / a.per_unit));
+  const long long blocks = (a.rows + static_cast<long long>(kUnits) - 1) / kUnits;
+  const int groups = a.q_groups + (a.paged ? 2 : 1) * a.kv_groups;
+  // three CTAs an SM; each walks the same number of rows
+  const long long most = (3ll * sms + groups - 1) / groups, turns = (blocks + most - 1) / most;
+  const dim3 grid(static_cast<unsigned>((blocks + turns - 1) / turns), static_cast<unsigned>(groups));
   if (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0)
     return a.interleaved ? launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE>, grid, dim3(kRowsThreads), 0, st, false, a)
                          : launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES>, grid, dim3(kRowsThreads), 0, st, false, a);
@@ -326,8 +336,10 @@ cudaError_t launch_mode(const QkRowsArgs& a, cudaStream_t st) {
 }
 
 template <typename XT>
-cudaError_t launch_rows(const QkRowsArgs& a, int lph, cudaStream_t st) {
-  return lph == 2 ? launch_mode<XT, 2>(a, st) : lph == 8 ? launch_mode<XT, 8>(a, st) : launch_mode<XT, 16>(a, st);
+cudaError_t launch_rows(const QkRowsArgs& a, int lph, int sms, cudaStream_t st) {
+  return lph == 2   ? launch_mode<XT, 2>(a, sms, st)
+         : lph == 8 ? launch_mode<XT, 8>(a, sms, st)
+                    : launch_mode<XT, 16>(a, sms, st);
 }
 
 bool is_float(int t) { return t == DEC_F32 || t == DEC_BF16; }
@@ -390,11 +402,14 @@ QkRowsArgs shared_fields(const A* a) {
 dec_status run_rows(QkRowsArgs& k, int xd, const DeviceInfo& di, cudaStream_t st) {
   const int lph = k.d <= 16 ? 2 : k.d <= 64 ? 8 : 16;  // lanes of a unit
   // Heads a unit walks: more share the row's angles, fewer give more units.
+  auto groups = [&](int per) {
+    return static_cast<long long>(k.n_q + per - 1) / per + (k.paged ? 2 : 1) * static_cast<long long>((k.n_kv + per - 1) / per);
+  };
   k.per_unit = 1;
-  while (k.per_unit < 8 && k.per_unit < k.heads &&
-         static_cast<long long>(k.rows) * ((k.heads + 2 * k.per_unit - 1) / (2 * k.per_unit)) * lph >= 2048ll * di.sms)
-    k.per_unit *= 2;
-  WSG_CUDA_TRY(nullptr, xd == DEC_F32 ? launch_rows<float>(k, lph, st) : launch_rows<uint16_t>(k, lph, st));
+  while (k.per_unit < 8 && k.rows * groups(2 * k.per_unit) * lph >= 3ll * kRowsThreads * di.sms) k.per_unit *= 2;
+  k.q_groups = (k.n_q + k.per_unit - 1) / k.per_unit;
+  k.kv_groups = (k.n_kv + k.per_unit - 1) / k.per_unit;
+  WSG_CUDA_TRY(nullptr, xd == DEC_F32 ? launch_rows<float>(k, lph, di.sms, st) : launch_rows<uint16_t>(k, lph, di.sms, st));
   return DEC_OK;
 }
 
@@ -448,7 +463,6 @@ extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
   k.k_out = a->k_out;
   k.ko_stride = a->k_out_stride;
   k.vec_y = k.vec_y && (a->n_kv == 0 || pieces16(a->k_out, a->k_out_stride, a->ydtype));
-  k.heads = a->n_q + a->n_kv;
   k.err = di.err;
   return run_rows(k, a->xdtype, di, static_cast<cudaStream_t>(stream));
 }
@@ -478,7 +492,6 @@ extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
   k.vec_x = k.vec_x && pieces16(a->v, a->v_stride, a->xdtype);
   k.k_out = a->k_pages;
   k.v_out = a->v_pages;
-  k.heads = a->n_q + 2 * a->n_kv;
   k.paged = 1;
   k.pool = PagePool{a->num_pages, a->n_kv, shift, a->table_stride};
   k.table = a->page_table;
