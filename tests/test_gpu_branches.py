@@ -403,6 +403,28 @@ def test_attn_shared_prefix_large_scores(kv):
     check_attn(t, 2, 4, 2, 128, 700, lens, 64, "f32")
 
 
+@pytest.mark.parametrize("types,batch", [(("bf16", "bf16"), 2), (("bf16", "bf16"), 20), (("f32", "f32"), 2)], ids=str)
+@pytest.mark.parametrize("scale", [-0.1, 0.0])
+def test_attn_shared_prefix_negative_scale(types, batch, scale):
+    import torch
+
+    W = lib()
+    lens = [33] * batch
+    a, t = attn_case(W, batch, 4, 2, 128, 200, lens, 16, *types, scale=scale)
+    W.attn_shared_prefix(a)
+    torch.cuda.synchronize()
+    group, k = 2, None
+    Q, got = f64(t["q"]).reshape(batch, 2, group, 128), f64(t["out"]).reshape(batch, 2, group, 128)
+    for b in range(batch):
+        for g in range(2):
+            i = np.arange(33)
+            at = t["table"][b, i // 16], g, i % 16
+            k = np.concatenate([f64(t["pk"])[g], f64(t["kp"])[at]])
+            v = np.concatenate([f64(t["pv"])[g], f64(t["vp"])[at]])
+            o, l, size = OB.attend(Q[b, g], k, v, float(np.float32(scale)))
+            inside(got[b, g], o, attn_tol(Q[b, g], k, l, o, size, abs(scale), types[0])[0], (b, g))
+
+
 def test_attn_shared_prefix_bad_pages():
     """Entries outside the pool are left out and reported; so are tokens past the table's width."""
     import torch

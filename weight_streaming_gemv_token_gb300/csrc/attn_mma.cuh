@@ -5,10 +5,10 @@
 // keys: rows of all branches over a range of the shared prefix, or the rows of
 // one branch over a range of its own pages. A CTA of four warps takes an item.
 // Each warp streams its own blocks of keys (16 bfloat16 or 8 float32 ones) with
-// 16-byte asynchronous copies through its own ring in shared memory, so the
-// main loop has no CTA-wide barrier:
-//   S = Q K^T (rows x block), masked and scaled; running reference maximum and
-//   sum of a softmax; P = 2^(S - reference) stays in registers and becomes the A
+// 16-byte asynchronous copies through two stages of its own in shared memory, so
+// the main loop has no CTA-wide barrier:
+//   S = Q K^T (rows x block), masked; running reference maximum and sum of a
+//   softmax; P = 2^(S - reference) stays in registers and becomes the A
 //   operand of O += P V. The reference moves only when a block's maximum passes
 //   it by 2^8, so O is rarely rescaled.
 //   At the end the warps' (O, m, l) join through shared memory and the CTA
@@ -45,11 +45,15 @@ struct AmArgs {
   const void *kp, *vp;
   PagePool pool;
   const int32_t *table, *len;
+  // |scale| log2(e), and the scale's sign, which the queries take on: a masked
+  // score stays -inf whatever the scale. Scale 0: queries of 0, scale_log2 1.
   float scale_log2;
+  int q_sign;
   // items: first the prefix's, item = (split * n_kv + head) * row_groups + row group,
   // then the branches', item = (split * batch + branch) * n_kv + head
   int prefix_items, row_groups, prefix_chunk, own_chunk;  // chunks: keys a split covers
   int own_slot0;                                          // slot of the branches' split 0
+  int first;                                              // the call's first kernel
   float* part_o;                                          // [slot][batch * n_q][d]
   float2* part_ml;                                        // [slot][batch * n_q]: (reference, sum)
   uint32_t* err;
@@ -60,10 +64,9 @@ struct AmGeom {
   static constexpr int KB = F32 ? 8 : 16;                              // keys a block
   static constexpr int E = F32 ? 4 : 2;                                // bytes an element
   static constexpr int PITCH = DP * E + 16;                            // bytes a row
-  static constexpr int STAGES = F32 || QP == 3 ? 2 : 3;
   static constexpr int TILE = KB * PITCH;                              // keys (or values) of a block
   static constexpr int QBYTES = F32 ? MT * 2 * (DP / 8) * 32 * 16 : QP * 16 * MT * PITCH;
-  static constexpr int RING = STAGES * 2 * TILE;                       // per warp
+  static constexpr int RING = 2 * 2 * TILE;                            // per warp: two stages
   static constexpr int JOIN = kAmWarps * 16 * MT * DP * 4;             // reuses the rings
   static constexpr int SMEM = QBYTES + (kAmWarps * RING > JOIN ? kAmWarps * RING : JOIN);
 };
@@ -123,12 +126,15 @@ __device__ __forceinline__ void am_split_bf16(float x, float y, uint32_t (&p)[PA
 }
 
 template <typename QT, int DP, int QP, int MT, bool F32>
-__global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a) {
+__global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2) attn_mma_kernel(const AmArgs a) {
   using G = AmGeom<DP, QP, MT, F32>;
   constexpr int KB = G::KB, NT = DP / 8, PP = QP == 1 ? 2 : 3;  // PP: bfloat16 parts of a probability
   extern __shared__ __align__(128) unsigned char am_raw[];
   __shared__ float s_m[kAmWarps][16 * MT], s_l[kAmWarps][16 * MT];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  // The call's first kernel waits for the stream's previous one; as the second
+  // it runs beside attn_prefix_tc_kernel, which has waited before it let it start.
+  if (a.first) pdl_wait();
   pdl_trigger();  // the join's CTAs may take their places and wait
 
   // ---- the item ----
@@ -171,51 +177,77 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
   const uint32_t ring32 = smem_u32(ring);
   const int chunks = a.d * G::E / 16;  // 16-byte pieces of a key
 
-  // key `lane` of a block: its row in the cache, -1 past the range or without a page
-  auto row_of = [&](int blk) -> long long {
-    const int k = k0 + blk * KB + lane;
-    if (lane >= KB || k >= k1) return -1;
-    if (shared_item) return a.pstride * g + k;
-    const int page = page_of(a.pool, trow, k);
-    if (page < 0) {
-      atomicOr(a.err, ERR_BAD_PAGE);
-      return -1;
-    }
-    return pool_row(a.pool, page, g, k);
-  };
-  auto request = [&](int stage, long long row) {
-    const uint32_t kd = ring32 + stage * 2 * G::TILE, vd = kd + G::TILE;
-    constexpr int CP = DP * G::E / 16;  // pieces of a padded row (a power of two)
+  // Request block blk into a stage; the mask of its keys that count (those past
+  // the range or without a page arrive as zeros).
+  constexpr int CP = DP * G::E / 16, KPI = 32 / CP > 0 ? 32 / CP : 1;  // 16-byte pieces of a padded row; keys a step
+  constexpr int STEPS = KB * CP / 32;
+  const int lkey = lane / CP, lc = lane % CP;
+  const uint32_t lane_dst = ring32 + lkey * G::PITCH + lc * 16;
+  const int row_bytes = a.d * G::E;
+  const bool whole = shared_item || (1 << a.pool.shift) >= KB;  // a block's keys are contiguous
+  auto request = [&](int stage, int blk) -> uint32_t {
+    const int k = k0 + blk * KB, n = min(KB, k1 - k);
+    const uint32_t dst = lane_dst + stage * 2 * G::TILE;
+    if (whole) {
+      long long row = a.pstride * g + k;
+      bool have = true;
+      if (!shared_item) {
+        const int page = page_of(a.pool, trow, k);
+        have = page >= 0;
+        row = have ? pool_row(a.pool, page, g, k) : 0;
+        if (!have && lane == 0) atomicOr(a.err, ERR_BAD_PAGE);
+      }
+      const long long off = row * row_bytes + lkey * row_bytes + lc * 16;
+      const char *ks = kbase + off, *vs = vbase + off;
+      if (have && n == KB) {
+        if (lc < chunks) {
 #pragma unroll
-    for (int i = 0; i < KB * CP / 32; ++i) {
-      const int key = (i * 32 + lane) / CP, c = (i * 32 + lane) % CP;
-      const long long r = __shfl_sync(0xffffffffu, row, key);
-      if (c < chunks) {
-        const long long off = r < 0 ? 0 : r * (static_cast<long long>(a.d) * G::E) + c * 16;
-        const uint32_t n = r < 0 ? 0 : 16;  // 0: zeros are written
-        am_copy16(kd + key * G::PITCH + c * 16, kbase + off, n);
-        am_copy16(vd + key * G::PITCH + c * 16, vbase + off, n);
+          for (int i = 0; i < STEPS; ++i) {
+            am_copy16(dst + i * KPI * G::PITCH, ks + i * (KPI * row_bytes), 16);
+            am_copy16(dst + i * KPI * G::PITCH + G::TILE, vs + i * (KPI * row_bytes), 16);
+          }
+        }
+        return 0xffffffffu >> (32 - KB);
+      }
+      const int lim = have ? n : 0;
+      if (lc < chunks) {
+#pragma unroll
+        for (int i = 0; i < STEPS; ++i) {
+          const bool in = lkey + i * KPI < lim;  // zeros are written where not
+          am_copy16(dst + i * KPI * G::PITCH, in ? ks + i * (KPI * row_bytes) : kbase, in ? 16 : 0);
+          am_copy16(dst + i * KPI * G::PITCH + G::TILE, in ? vs + i * (KPI * row_bytes) : vbase, in ? 16 : 0);
+        }
+      }
+      return (1u << lim) - 1u;
+    }
+    // pages shorter than a block: lane `key` looks its own up
+    long long row = -1;
+    if (lane < n) {
+      const int page = page_of(a.pool, trow, k + lane);
+      if (page >= 0)
+        row = pool_row(a.pool, page, g, k + lane);
+      else
+        atomicOr(a.err, ERR_BAD_PAGE);
+    }
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const long long r = __shfl_sync(0xffffffffu, row, lkey + i * KPI);
+      if (lc < chunks) {
+        const long long off = r < 0 ? 0 : r * row_bytes + lc * 16;
+        am_copy16(dst + i * KPI * G::PITCH, kbase + off, r < 0 ? 0 : 16);
+        am_copy16(dst + i * KPI * G::PITCH + G::TILE, vbase + off, r < 0 ? 0 : 16);
       }
     }
+    return __ballot_sync(0xffffffffu, row >= 0);
   };
 
-  // ---- first blocks on their way, then the query rows ----
-  uint32_t valid[G::STAGES];  // keys of the stage's block that count (one bit each)
-  int ahead = warp;           // next block to request
-#pragma unroll
-  for (int s = 0; s < G::STAGES - 1; ++s, ahead += kAmWarps) {
-    valid[s] = 0;
-    if (ahead < nblk) {
-      const long long r = row_of(ahead);
-      valid[s] = __ballot_sync(0xffffffffu, r >= 0);
-      request(s, r);
-    }
-    am_commit();
-  }
-  valid[G::STAGES - 1] = 0;
+  // ---- the first block on its way, then the query rows ----
+  uint32_t ok = 0;  // keys of the block in hand that count
+  if (warp < nblk) ok = request(0, warp);
+  am_commit();
   if (a.d < DP) {  // columns past the head stay zero
     const int pad = DP * G::E / 16 - chunks;
-    for (int i = lane; i < G::STAGES * 2 * KB * pad; i += 32)
+    for (int i = lane; i < 2 * 2 * KB * pad; i += 32)
       *reinterpret_cast<uint4*>(ring + (i / pad) * G::PITCH + (chunks + i % pad) * 16) = make_uint4(0, 0, 0, 0);
   }
   for (int i = tid; i < 16 * MT * (DP / 2); i += kAmThreads) {
@@ -231,6 +263,7 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
         x[0] = bf16_to_f32(src[0]), x[1] = bf16_to_f32(src[1]);
       }
     }
+    if (a.q_sign != 1) x[0] *= a.q_sign, x[1] *= a.q_sign;
     if constexpr (F32) {
       // in the order of the A fragments: [m tile][part][k step][lane][register]
 #pragma unroll
@@ -261,27 +294,12 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
   for (int t = 0; t < MT; ++t) mref[t][0] = mref[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
   const uint32_t q32 = smem_u32(am_raw);
   int stage = 0;
-  for (int blk = warp; blk < nblk; blk += kAmWarps) {
-    am_wait<G::STAGES - 2>();
-    __syncwarp();  // this block has landed, and every lane is done with the block before it
-    {
-      const int s = stage == 0 ? G::STAGES - 1 : stage - 1;
-      uint32_t v = 0;
-      if (ahead < nblk) {
-        const long long r = row_of(ahead);
-        v = __ballot_sync(0xffffffffu, r >= 0);
-        request(s, r);
-      }
-      am_commit();
-      ahead += kAmWarps;
-#pragma unroll
-      for (int i = 0; i < G::STAGES; ++i)
-        if (i == s) valid[i] = v;
-    }
-    uint32_t ok = 0;
-#pragma unroll
-    for (int i = 0; i < G::STAGES; ++i)
-      if (i == stage) ok = valid[i];
+  for (int blk = warp; blk < nblk; blk += kAmWarps, stage ^= 1) {
+    __syncwarp();  // every lane is done with the block before this one
+    const uint32_t next_ok = blk + kAmWarps < nblk ? request(stage ^ 1, blk + kAmWarps) : 0;
+    am_commit();
+    am_wait<1>();
+    __syncwarp();  // this block has landed for every lane
     const uint32_t kt = ring32 + stage * 2 * G::TILE, vt = kt + G::TILE;
     constexpr int ST = KB / 8;  // score tiles of 8 keys
     float s[MT][ST][4] = {};
@@ -328,14 +346,16 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
 #pragma unroll
         for (int j = 0; j < 4; ++j) s[t][0][j] += s2[t][j] + s3[t][j];
     }
-    // scale and mask: register j of tile n is key 8 n + 2 (lane % 4) + j % 2
+    // mask: register j of tile n is key 8 n + 2 (lane % 4) + j % 2
+    if (ok != 0xffffffffu >> (32 - KB)) {
 #pragma unroll
-    for (int t = 0; t < MT; ++t)
+      for (int t = 0; t < MT; ++t)
 #pragma unroll
-      for (int n = 0; n < ST; ++n)
+        for (int n = 0; n < ST; ++n)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          s[t][n][j] = (ok >> (n * 8 + 2 * (lane & 3) + (j & 1))) & 1u ? s[t][n][j] * a.scale_log2 : -INFINITY;
+          for (int j = 0; j < 4; ++j)
+            if (!((ok >> (n * 8 + 2 * (lane & 3) + (j & 1))) & 1u)) s[t][n][j] = -INFINITY;
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
       if (t == 1 && !two) continue;
@@ -347,7 +367,7 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2));
+        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
       }
       const bool move = mx[0] > mref[t][0] + kAmMargin || mx[1] > mref[t][1] + kAmMargin;
       if (__any_sync(0xffffffffu, move)) {
@@ -369,7 +389,7 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
         for (int n = 0; n < ST; ++n)
 #pragma unroll
           for (int j = 2 * h; j < 2 * h + 2; ++j) {
-            s[t][n][j] = am_exp2(s[t][n][j] - m);
+            s[t][n][j] = am_exp2(fmaf(s[t][n][j], a.scale_log2, -m));
             sum += s[t][n][j];
           }
         l[t][h] += sum;  // this thread's keys only
@@ -423,7 +443,7 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
         }
       }
     }
-    stage = stage == G::STAGES - 1 ? 0 : stage + 1;
+    ok = next_ok;
   }
   am_wait<0>();
 
@@ -484,7 +504,7 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_mma_kernel(const AmArgs a)
 // Launches attn_mma_kernel for a head size and row tiles (1 or 2); sets the
 // kernel's shared-memory limit on its first launch on a device.
 template <typename QT, int DP, int QP, int MT, bool F32>
-cudaError_t am_launch_one(const AmArgs& a, int items, bool pdl, int dev, cudaStream_t st) {
+cudaError_t am_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) {
   constexpr size_t smem = AmGeom<DP, QP, MT, F32>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[dev]) {
@@ -492,19 +512,18 @@ cudaError_t am_launch_one(const AmArgs& a, int items, bool pdl, int dev, cudaStr
     if (e != cudaSuccess) return e;
     lifted[dev] = true;
   }
-  return launch_k(attn_mma_kernel<QT, DP, QP, MT, F32>, dim3(items), dim3(kAmThreads), smem, st, pdl, a);
+  return launch_k(attn_mma_kernel<QT, DP, QP, MT, F32>, dim3(items), dim3(kAmThreads), smem, st, true, a);
 }
 
 template <typename QT, int QP, int MT, bool F32>
-cudaError_t am_launch_head(const AmArgs& a, int items, bool pdl, int dev, cudaStream_t st) {
-  if (a.d <= 16) return am_launch_one<QT, 16, QP, MT, F32>(a, items, pdl, dev, st);
-  if (a.d <= 64) return am_launch_one<QT, 64, QP, MT, F32>(a, items, pdl, dev, st);
-  return am_launch_one<QT, 128, QP, MT, F32>(a, items, pdl, dev, st);
+cudaError_t am_launch_head(const AmArgs& a, int items, int dev, cudaStream_t st) {
+  if (a.d <= 16) return am_launch_one<QT, 16, QP, MT, F32>(a, items, dev, st);
+  if (a.d <= 64) return am_launch_one<QT, 64, QP, MT, F32>(a, items, dev, st);
+  return am_launch_one<QT, 128, QP, MT, F32>(a, items, dev, st);
 }
 
 // bfloat16 and float32 caches (attn_shared.cu, attn_shared_f32.cu).
-// pdl: as a programmatic dependent of attn_prefix_tc_kernel.
-cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, bool pdl, int dev, cudaStream_t st);
+cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st);
 cudaError_t am_launch_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st);
 
 }  // namespace wsg

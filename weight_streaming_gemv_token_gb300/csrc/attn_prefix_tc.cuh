@@ -6,7 +6,7 @@
 // one per tensor-memory lane. The pipeline is that of the prompt's attention
 // (prefill_attn_tc.cuh), with 128-key tiles:
 //   warp 0      one thread streams keys and values (two 128 x 64 boxes a tile,
-//               128-byte swizzle) into 3-stage rings; the tensor maps end at the
+//               128-byte swizzle) into two-stage rings; the tensor maps end at the
 //               prefix's last row, so rows behind it arrive as zeros;
 //   warp 1      one thread issues S_j = Q K_j^T one tile ahead, then O += P_j V_j
 //               with P_j over the scores in tensor memory;
@@ -30,7 +30,7 @@
 namespace wsg {
 
 constexpr int kApD = 128, kApRows = 128, kApKeys = 128;  // head size, rows a CTA, keys a tile
-constexpr int kApStages = 3, kApThreads = 32 * 10;
+constexpr int kApStages = 2, kApThreads = 32 * 10;
 constexpr uint32_t kApTile = kApKeys * kApD * 2, kApBox = kApTile / 2;
 constexpr uint32_t kApTmO = 256, kApTmQ = 384;
 constexpr size_t kApSmem = 2 * kApStages * kApTile + 1024;
@@ -40,7 +40,8 @@ struct ApArgs {
   long long q_stride;
   int batch, n_q, n_kv, group, rows;
   int row_blocks, plen, chunk;  // chunk: keys a split covers, a multiple of 128
-  float scale_log2;
+  float scale_log2;  // as in AmArgs
+  int q_sign;
   float* part_o;  // as in AmArgs, the splits in slots 0 ..
   float2* part_ml;
   uint32_t* err;
@@ -56,7 +57,7 @@ __device__ __forceinline__ void tma_load_3d_map(void* dst, const CUtensorMap* ma
 
 // Grid: blockIdx.x = (split * n_kv + head) * row_blocks + row block. kmap, vmap:
 // the prefix as [n_kv][plen][128] in 128-row x 64-column boxes.
-__global__ void __launch_bounds__(kApThreads, 1)
+__global__ void __maxnreg__(128)
     attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const ApArgs a) {
   extern __shared__ __align__(1024) unsigned char ap_raw[];
@@ -76,7 +77,6 @@ __global__ void __launch_bounds__(kApThreads, 1)
   const int live = (nrows + 31) / 32;               // lane quarters that hold rows
   volatile int* vfail = &s_fail;
 
-  pdl_trigger();
   if (tid == 0) {
     for (int s = 0; s < kApStages; ++s) {
       mbar_init(&k_full[s], 1);
@@ -93,6 +93,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&pair_bar[i], 64);
     s_fail = 0;
     fence_mbar_init();
+    pdl_wait();  // keys and values may come from the previous kernel
     // the first tiles, ahead of everything else in the CTA
     for (int j = 0; j < kApStages && j < T; ++j) {
       unsigned char *kd = Ks + j * kApTile, *vd = Vs + j * kApTile;
@@ -115,6 +116,8 @@ __global__ void __launch_bounds__(kApThreads, 1)
   const bool have = v < nrows;
   const bool works = warp >= 2 && q < live;
   const long long prow = static_cast<long long>((row0 + v) / a.group) * a.n_q + g * a.group + (row0 + v) % a.group;
+  pdl_wait();
+  pdl_trigger();  // after the wait: the kernel that runs beside this one does not wait itself
   uint32_t qr[32];
 #pragma unroll
   for (int i = 0; i < 32; ++i) qr[i] = 0;
@@ -130,6 +133,10 @@ __global__ void __launch_bounds__(kApThreads, 1)
 #pragma unroll
       for (int i = 0; i < 32; ++i) qr[i] = src[2 * i] | (static_cast<uint32_t>(src[2 * i + 1]) << 16);
     }
+  }
+  if (a.q_sign != 1) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) qr[i] = a.q_sign == 0 ? 0u : qr[i] ^ 0x80008000u;
   }
   tc_fence_before();
   __syncthreads();
@@ -239,7 +246,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
       tc_wait_ld();
       float x[64];
 #pragma unroll
-      for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(k < 32 ? s0[k] : s1[k - 32]) * c;
+      for (int k = 0; k < 64; ++k) x[k] = __uint_as_float(k < 32 ? s0[k] : s1[k - 32]);
       const int left = k1 - (k0 + j * kApKeys + half * 64);  // keys of this half inside the range
       if (left < 64) {
 #pragma unroll
@@ -258,7 +265,7 @@ __global__ void __launch_bounds__(kApThreads, 1)
         ok = false;
         break;
       }
-      const float mx = fmaxf(mh[0], xch[j & 1][half ^ 1][v]);
+      const float mx = fmaxf(mh[0], xch[j & 1][half ^ 1][v]) * c;
       const bool move = mx > m_ref + kAmMargin;
       if (__any_sync(0xffffffffu, move)) {
         const float nref = move ? mx : m_ref;
@@ -284,21 +291,21 @@ __global__ void __launch_bounds__(kApThreads, 1)
         m_ref = nref;
       }
       const float m = m_ref == -INFINITY ? 0.f : m_ref;  // no score seen yet: every term is 0
-      uint32_t ph[32], pl[32];
-      float sh[32];
+      // 32 at a time, over the scores that this warp has read
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int k = 0; k < 32; ++k) {
-        const float p0 = at_exp2(x[2 * k] - m), p1 = at_exp2(x[2 * k + 1] - m);
-        sh[k] = p0 + p1;
-        at_pack_split(p0, p1, &ph[k], &pl[k]);
+      for (int h = 0; h < 2; ++h) {
+        uint32_t ph[16], pl[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const float p0 = at_exp2(fmaf(x[32 * h + 2 * k], c, -m)), p1 = at_exp2(fmaf(x[32 * h + 2 * k + 1], c, -m));
+          sum[k & 3] += p0 + p1;
+          at_pack_split(p0, p1, &ph[k], &pl[k]);
+        }
+        tc_st16(tb + half * 32 + h * 16, ph);
+        tc_st16(tb + 64 + half * 32 + h * 16, pl);
       }
-#pragma unroll
-      for (int w = 16; w >= 1; w >>= 1)
-#pragma unroll
-        for (int k = 0; k < w; ++k) sh[k] += sh[k + w];
-      lsum += sh[0];
-      tc_st32(tb + half * 32, ph);
-      tc_st32(tb + 64 + half * 32, pl);
+      lsum += (sum[0] + sum[1]) + (sum[2] + sum[3]);
       tc_wait_st();
       tc_fence_before();
       __syncwarp();

@@ -16,12 +16,12 @@
 
 namespace wsg {
 
-cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, bool pdl, int dev, cudaStream_t st) {
+cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st) {
   if (q_f32)
-    return mt == 2 ? am_launch_head<float, 3, 2, false>(a, items, pdl, dev, st)
-                   : am_launch_head<float, 3, 1, false>(a, items, pdl, dev, st);
-  return mt == 2 ? am_launch_head<uint16_t, 1, 2, false>(a, items, pdl, dev, st)
-                 : am_launch_head<uint16_t, 1, 1, false>(a, items, pdl, dev, st);
+    return mt == 2 ? am_launch_head<float, 3, 2, false>(a, items, dev, st)
+                   : am_launch_head<float, 3, 1, false>(a, items, dev, st);
+  return mt == 2 ? am_launch_head<uint16_t, 1, 2, false>(a, items, dev, st)
+                 : am_launch_head<uint16_t, 1, 1, false>(a, items, dev, st);
 }
 
 namespace {
@@ -50,6 +50,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AmJoinArgs a) {
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int w = a.warps == 4 ? blockIdx.x : blockIdx.x * 4 + warp;
   const int first = a.warps == 4 ? warp : 0;
+  pdl_trigger();  // a following call's set-up may begin
   pdl_wait();
   if (w >= a.batch * a.n_q) return;
   const int b = w / a.n_q;
@@ -253,7 +254,8 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   k.pool = PagePool{a->num_pages, a->n_kv, page_shift(a->page_size), a->table_stride};
   k.table = a->page_table;
   k.len = a->seq_len;
-  k.scale_log2 = a->scale * 1.44269504088896340736f;
+  k.scale_log2 = a->scale == 0.f ? 1.f : fabsf(a->scale) * 1.44269504088896340736f;
+  k.q_sign = a->scale == 0.f ? 0 : a->scale < 0.f ? -1 : 1;
   k.row_groups = p.row_groups;
   k.prefix_items = p.tc ? 0 : static_cast<int>(p.prefix_items);
   k.prefix_chunk = p.prefix_chunk;
@@ -276,6 +278,7 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
     t.plen = a->prefix_len;
     t.chunk = p.prefix_chunk;
     t.scale_log2 = k.scale_log2;
+    t.q_sign = k.q_sign;
     t.part_o = k.part_o;
     t.part_ml = k.part_ml;
     t.err = di.err;
@@ -291,12 +294,13 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
       lifted[di.device] = true;
     }
     WSG_CUDA_TRY(nullptr, launch_k(attn_prefix_tc_kernel, dim3(static_cast<unsigned>(p.prefix_items)), dim3(kApThreads),
-                                   kApSmem, s, false, maps[0], maps[1], t));
+                                   kApSmem, s, true, maps[0], maps[1], t));
   }
   const int items = k.prefix_items + static_cast<int>(p.own_items);
+  k.first = !p.tc;
   if (items > 0)
     WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? am_launch_f32(k, qf, items, di.device, s)
-                                                : am_launch_bf16(k, qf, p.mt, items, p.tc, di.device, s));
+                                                : am_launch_bf16(k, qf, p.mt, items, di.device, s));
   AmJoinArgs j{};
   j.batch = a->batch;
   j.n_q = a->n_q;
@@ -313,8 +317,7 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   j.lse = a->lse;
   const int jrows = a->batch * a->n_q;
   const dim3 grid(j.warps == 4 ? jrows : (jrows + 3) / 4);
-  // a join without partial results may not overtake the stream's previous kernel
-  WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_join_kernel<float>, grid, dim3(128), 0, s, p.tc || items > 0, j)
-                           : launch_k(attn_join_kernel<uint16_t>, grid, dim3(128), 0, s, p.tc || items > 0, j));
+  WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_join_kernel<float>, grid, dim3(128), 0, s, true, j)
+                           : launch_k(attn_join_kernel<uint16_t>, grid, dim3(128), 0, s, true, j));
   return DEC_OK;
 }
