@@ -1,28 +1,27 @@
-// Partial attention of a few query rows over a range of keys, on warp-level
-// matrix instructions; the partial results join in attn_join_kernel.
+// Partial attention over a float32 cache on warp-level tf32 instructions, and the
+// arguments and helpers that the attention kernels for several branches share.
+// The partial results join in attn_join_kernel.
 //
-// An item is up to 16 MT query rows of one key/value head and a range of its
-// keys: rows of all branches over a range of the shared prefix, or the rows of
-// one branch over a range of its own pages. A CTA of four warps takes an item.
-// Each warp streams its own blocks of keys (16 bfloat16 or 8 float32 ones) with
-// 16-byte asynchronous copies through two stages of its own in shared memory, so
-// the main loop has no CTA-wide barrier:
+// An item is up to 16 query rows of one key/value head and a range of its keys:
+// rows of all branches over a range of the shared prefix, or the rows of one
+// branch over a range of its own pages. A CTA of four warps takes an item. Each
+// warp streams its own blocks of 8 keys with 16-byte asynchronous copies through
+// two stages of its own in shared memory, so the main loop has no CTA-wide
+// barrier:
 //   S = Q K^T (rows x block), masked; running reference maximum and sum of a
-//   softmax; P = 2^(S - reference) stays in registers and becomes the A
-//   operand of O += P V. The reference moves only when a block's maximum passes
-//   it by 2^8, so O is rarely rescaled.
-//   At the end the warps' (O, m, l) join through shared memory and the CTA
-//   writes one partial result.
+//   softmax; P = 2^(S - reference) stays in registers and becomes the A operand of
+//   O += P V. The reference moves only when a block's maximum passes it by 2^8, so
+//   O is rarely rescaled.
+//   At the end the warps' (O, m, l) join through shared memory and the CTA writes
+//   one partial result.
 //
-// Precision: float32 sums throughout. bfloat16 keys and values enter exactly; a
-// float32 query is split into three bfloat16 parts (24 bits, exact), a
-// probability into two (QP 1: bfloat16 queries, whose result is rounded to 8
-// bits: 2^-16 is lost) or three. Float32 keys and values run on tf32 instructions
-// as value + remainder, three of the four products (2^-21 relative is lost).
+// Precision: every operand as tf32 value + remainder, three of the four products
+// (about 2^-21 relative is lost), float32 sums.
 //
-// Rows in shared memory are 16 bytes longer than the head, which makes every
-// matrix load and the float32 value loads free of bank conflicts. Memory bounds
-// it while the matrix instructions per key stay below the copy time.
+// Rows in shared memory are 16 bytes longer than the head, which makes the matrix
+// loads of the keys and the scalar loads of the values free of bank conflicts.
+// The matrix instructions bound it: 192 a block, one in two cycles an SM, against
+// 350 cycles for the block's 8 KB at the SM's share of the memory.
 #pragma once
 #include <cstdint>
 
@@ -49,25 +48,29 @@ struct AmArgs {
   // score stays -inf whatever the scale. Scale 0: queries of 0, scale_log2 1.
   float scale_log2;
   int q_sign;
-  // items: first the prefix's, item = (split * n_kv + head) * row_groups + row group,
-  // then the branches', item = (split * batch + branch) * n_kv + head
-  int prefix_items, row_groups, prefix_chunk, own_chunk;  // chunks: keys a split covers
-  int own_slot0;                                          // slot of the branches' split 0
-  int first;                                              // the call's first kernel
-  float* part_o;                                          // [slot][batch * n_q][d]
-  float2* part_ml;                                        // [slot][batch * n_q]: (reference, sum)
+  int q_even;  // two queries at a time can be read
+  // Prefix items: item = (split * n_kv + head) * row_groups + row group, a split
+  // covering prefix_chunk keys, its slot the split. Behind them the branches' keys:
+  // batch * n_kv segments (branch, head) of own_seg blocks of own_block keys in one
+  // line, cut into pieces of own_per blocks; piece w of a segment whose first piece
+  // is f has the slot own_slot0 + w - f.
+  int prefix_items, row_groups, prefix_chunk;
+  int own_block, own_slot0;
+  long long own_seg, own_per;
+  int first;        // the call's first kernel
+  float* part_o;    // [slot][batch * n_q][d]
+  float2* part_ml;  // [slot][batch * n_q]: (reference, sum)
   uint32_t* err;
 };
 
-template <int DP, int QP, int MT, bool F32>
+template <int DP>
 struct AmGeom {
-  static constexpr int KB = F32 ? 8 : 16;                              // keys a block
-  static constexpr int E = F32 ? 4 : 2;                                // bytes an element
-  static constexpr int PITCH = DP * E + 16;                            // bytes a row
-  static constexpr int TILE = KB * PITCH;                              // keys (or values) of a block
-  static constexpr int QBYTES = F32 ? MT * 2 * (DP / 8) * 32 * 16 : QP * 16 * MT * PITCH;
-  static constexpr int RING = 2 * 2 * TILE;                            // per warp: two stages
-  static constexpr int JOIN = kAmWarps * 16 * MT * DP * 4;             // reuses the rings
+  static constexpr int KB = 8;                       // keys a block
+  static constexpr int PITCH = DP * 4 + 16;          // bytes a row
+  static constexpr int TILE = KB * PITCH;            // keys (or values) of a block
+  static constexpr int QBYTES = 2 * (DP / 8) * 32 * 16;
+  static constexpr int RING = 2 * 2 * TILE;          // per warp: two stages
+  static constexpr int JOIN = kAmWarps * 16 * DP * 4;  // in the place of the rings
   static constexpr int SMEM = QBYTES + (kAmWarps * RING > JOIN ? kAmWarps * RING : JOIN);
 };
 
@@ -125,16 +128,16 @@ __device__ __forceinline__ void am_split_bf16(float x, float y, uint32_t (&p)[PA
   }
 }
 
-template <typename QT, int DP, int QP, int MT, bool F32>
-__global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2) attn_mma_kernel(const AmArgs a) {
-  using G = AmGeom<DP, QP, MT, F32>;
-  constexpr int KB = G::KB, NT = DP / 8, PP = QP == 1 ? 2 : 3;  // PP: bfloat16 parts of a probability
+// Grid: prefix items, then one CTA per branch, head and piece (own_per 1, a block
+// being a whole range of own_block keys).
+template <typename QT, int DP>
+__global__ void __launch_bounds__(kAmThreads, 2) attn_f32_kernel(const AmArgs a) {
+  using G = AmGeom<DP>;
+  constexpr int KB = G::KB, NT = DP / 8;
   extern __shared__ __align__(128) unsigned char am_raw[];
-  __shared__ float s_m[kAmWarps][16 * MT], s_l[kAmWarps][16 * MT];
+  __shared__ float s_m[kAmWarps][16], s_l[kAmWarps][16];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // The call's first kernel waits for the stream's previous one; as the second
-  // it runs beside attn_prefix_tc_kernel, which has waited before it let it start.
-  if (a.first) pdl_wait();
+  pdl_wait();
   pdl_trigger();  // the join's CTAs may take their places and wait
 
   // ---- the item ----
@@ -144,15 +147,15 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
     const int rg = blockIdx.x % a.row_groups, t = blockIdx.x / a.row_groups;
     g = t % a.n_kv;
     slot = t / a.n_kv;
-    row0 = rg * 16 * MT;
-    nrows = min(16 * MT, a.rows - row0);
+    row0 = rg * 16;
+    nrows = min(16, a.rows - row0);
     k0 = slot * a.prefix_chunk;
     k1 = min(a.plen, k0 + a.prefix_chunk);
   } else {
     const int t = blockIdx.x - a.prefix_items;
-    g = t % a.n_kv;
-    branch = t / a.n_kv % a.batch;
-    const int split = t / a.n_kv / a.batch;
+    const int seg = static_cast<int>(t / a.own_seg), split = static_cast<int>(t - seg * a.own_seg);
+    g = seg % a.n_kv;
+    branch = seg / a.n_kv;
     slot = a.own_slot0 + split;
     row0 = branch * a.group;
     nrows = a.group;
@@ -161,12 +164,9 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
       n = static_cast<int>(page_capacity(a.pool));
       if (split == 0 && g == 0 && tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
     }
-    k0 = split * a.own_chunk;
-    k1 = min(n, k0 + a.own_chunk);
-    if (k0 >= k1) {  // attn_join_kernel knows which splits hold keys
-      pdl_wait();
-      return;
-    }
+    k0 = split * a.own_block;
+    k1 = min(n, k0 + a.own_block);
+    if (k0 >= k1) return;  // attn_join_kernel knows which pieces hold keys
   }
   const int nblk = (k1 - k0 + KB - 1) / KB;
   const int32_t* trow = a.table + static_cast<long long>(branch) * a.pool.width;
@@ -175,15 +175,15 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
 
   unsigned char* ring = am_raw + G::QBYTES + warp * G::RING;
   const uint32_t ring32 = smem_u32(ring);
-  const int chunks = a.d * G::E / 16;  // 16-byte pieces of a key
+  const int chunks = a.d / 4;  // 16-byte pieces of a key
 
   // Request block blk into a stage; the mask of its keys that count (those past
   // the range or without a page arrive as zeros).
-  constexpr int CP = DP * G::E / 16, KPI = 32 / CP > 0 ? 32 / CP : 1;  // 16-byte pieces of a padded row; keys a step
+  constexpr int CP = DP / 4, KPI = 32 / CP > 0 ? 32 / CP : 1;  // 16-byte pieces of a padded row; keys a step
   constexpr int STEPS = KB * CP / 32;
   const int lkey = lane / CP, lc = lane % CP;
   const uint32_t lane_dst = ring32 + lkey * G::PITCH + lc * 16;
-  const int row_bytes = a.d * G::E;
+  const int row_bytes = a.d * 4;
   const bool whole = shared_item || (1 << a.pool.shift) >= KB;  // a block's keys are contiguous
   auto request = [&](int stage, int blk) -> uint32_t {
     const int k = k0 + blk * KB, n = min(KB, k1 - k);
@@ -246,53 +246,41 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
   if (warp < nblk) ok = request(0, warp);
   am_commit();
   if (a.d < DP) {  // columns past the head stay zero
-    const int pad = DP * G::E / 16 - chunks;
+    const int pad = DP / 4 - chunks;
     for (int i = lane; i < 2 * 2 * KB * pad; i += 32)
       *reinterpret_cast<uint4*>(ring + (i / pad) * G::PITCH + (chunks + i % pad) * 16) = make_uint4(0, 0, 0, 0);
   }
-  for (int i = tid; i < 16 * MT * (DP / 2); i += kAmThreads) {
-    const int r = i / (DP / 2), e = i % (DP / 2) * 2;
-    float x[2] = {0.f, 0.f};
+  for (int i = tid; i < 16 * (DP / 8); i += kAmThreads) {
+    // 8 elements of a row, in the order of the A fragments: [part][k step][lane][register]
+    const int r = i / (DP / 8), e = i % (DP / 8) * 8;
+    float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (r < nrows && e < a.d) {
       const int row = row0 + r;
       const QT* src = static_cast<const QT*>(a.q) + a.q_stride * (row / a.group) +
                       static_cast<long long>(g * a.group + row % a.group) * a.d + e;
-      if constexpr (sizeof(QT) == 4) {
-        x[0] = src[0], x[1] = src[1];
-      } else {
-        x[0] = bf16_to_f32(src[0]), x[1] = bf16_to_f32(src[1]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        if constexpr (sizeof(QT) == 4)
+          x[j] = src[j] * a.q_sign;
+        else
+          x[j] = bf16_to_f32(src[j]) * a.q_sign;
       }
     }
-    if (a.q_sign != 1) x[0] *= a.q_sign, x[1] *= a.q_sign;
-    if constexpr (F32) {
-      // in the order of the A fragments: [m tile][part][k step][lane][register]
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int k = (e + j) % 8, ln = (r % 8) * 4 + k % 4, reg = (r % 16) / 8 + 2 * (k / 4);
-        uint32_t hi, lo;
-        am_split_tf32(x[j], &hi, &lo);
-        uint32_t* f = reinterpret_cast<uint32_t*>(am_raw) + (((r / 16) * 2 * NT + (e + j) / 8) * 32 + ln) * 4 + reg;
-        f[0] = hi;
-        f[NT * 32 * 4] = lo;
-      }
-    } else {
-      uint32_t p[QP];
-      am_split_bf16<QP>(x[0], x[1], p);
-#pragma unroll
-      for (int part = 0; part < QP; ++part)
-        *reinterpret_cast<uint32_t*>(am_raw + (part * 16 * MT + r) * G::PITCH + e * 2) = p[part];
+    for (int j = 0; j < 8; ++j) {
+      const int ln = (r % 8) * 4 + j % 4, reg = r / 8 + 2 * (j / 4);
+      uint32_t hi, lo;
+      am_split_tf32(x[j], &hi, &lo);
+      uint32_t* f = reinterpret_cast<uint32_t*>(am_raw) + ((e / 8) * 32 + ln) * 4 + reg;
+      f[0] = hi;
+      f[NT * 32 * 4] = lo;
     }
   }
   __syncthreads();
 
-  const bool two = MT == 1 || nrows > 16;  // the second row tile holds rows
-
   // ---- main loop ----
-  float o[MT][NT][4] = {};
-  float mref[MT][2], l[MT][2];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) mref[t][0] = mref[t][1] = -INFINITY, l[t][0] = l[t][1] = 0.f;
-  const uint32_t q32 = smem_u32(am_raw);
+  float o[NT][4] = {};
+  float mref[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
   int stage = 0;
   for (int blk = warp; blk < nblk; blk += kAmWarps, stage ^= 1) {
     __syncwarp();  // every lane is done with the block before this one
@@ -300,148 +288,71 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
     am_commit();
     am_wait<1>();
     __syncwarp();  // this block has landed for every lane
-    const uint32_t kt = ring32 + stage * 2 * G::TILE, vt = kt + G::TILE;
-    constexpr int ST = KB / 8;  // score tiles of 8 keys
-    float s[MT][ST][4] = {};
-    if constexpr (!F32) {
+    const uint32_t kt = ring32 + stage * 2 * G::TILE;
+    float s[4] = {}, s2[4] = {}, s3[4] = {};  // the remainders' products are chains of their own
 #pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        uint32_t b[4];
-        am_ld4(b, kt + ((lane >> 4) * 8 + (lane & 7)) * G::PITCH + kk * 32 + ((lane >> 3) & 1) * 16);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int part = 0; part < QP; ++part) {
-            if (t == 1 && !two) continue;
-            uint32_t qa[4];
-            am_ld4(qa, q32 + (part * 16 * MT + t * 16 + (lane & 15)) * G::PITCH + kk * 32 + (lane >> 4) * 16);
-            am_mma16(s[t][0], qa, b[0], b[1]);
-            am_mma16(s[t][1], qa, b[2], b[3]);
-          }
-      }
-    } else {
-      float s2[MT][4] = {}, s3[MT][4] = {};  // the remainders' products, chains of their own
-#pragma unroll
-      for (int kk = 0; kk < DP / 16; ++kk) {
-        uint32_t b[4];
-        am_ld4(b, kt + (lane & 7) * G::PITCH + kk * 64 + (lane >> 3) * 16);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          uint32_t bh0, bl0, bh1, bl1;
-          am_split_tf32(__uint_as_float(b[2 * h]), &bh0, &bl0);
-          am_split_tf32(__uint_as_float(b[2 * h + 1]), &bh1, &bl1);
-#pragma unroll
-          for (int t = 0; t < MT; ++t) {
-            const uint4* f = reinterpret_cast<const uint4*>(am_raw) + ((t * 2 * NT + 2 * kk + h) * 32 + lane);
-            const uint4 fh = f[0], fl = f[NT * 32];
-            const uint32_t qh[4] = {fh.x, fh.y, fh.z, fh.w}, ql[4] = {fl.x, fl.y, fl.z, fl.w};
-            am_mma8(s[t][0], qh, bh0, bh1);
-            am_mma8(s2[t], qh, bl0, bl1);
-            am_mma8(s3[t], ql, bh0, bh1);
-          }
-        }
-      }
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) s[t][0][j] += s2[t][j] + s3[t][j];
-    }
-    // mask: register j of tile n is key 8 n + 2 (lane % 4) + j % 2
-    if (ok != 0xffffffffu >> (32 - KB)) {
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int n = 0; n < ST; ++n)
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (!((ok >> (n * 8 + 2 * (lane & 3) + (j & 1))) & 1u)) s[t][n][j] = -INFINITY;
-    }
-#pragma unroll
-    for (int t = 0; t < MT; ++t) {
-      if (t == 1 && !two) continue;
-      float mx[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-      for (int n = 0; n < ST; ++n)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) mx[j >> 1] = fmaxf(mx[j >> 1], s[t][n][j]);
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      uint32_t b[4];
+      am_ld4(b, kt + (lane & 7) * G::PITCH + kk * 64 + (lane >> 3) * 16);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
-        mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
-      }
-      const bool move = mx[0] > mref[t][0] + kAmMargin || mx[1] > mref[t][1] + kAmMargin;
-      if (__any_sync(0xffffffffu, move)) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          const float nr = mx[h] > mref[t][h] + kAmMargin ? mx[h] : mref[t][h];
-          const float f = nr == mref[t][h] ? 1.f : am_exp2(mref[t][h] - nr);  // 0 on the first move
-          mref[t][h] = nr;
-          l[t][h] *= f;
-#pragma unroll
-          for (int n = 0; n < NT; ++n) o[t][n][2 * h] *= f, o[t][n][2 * h + 1] *= f;
-        }
-      }
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        const float m = mref[t][h] == -INFINITY ? 0.f : mref[t][h];  // nothing seen yet: every term is 0
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < ST; ++n)
-#pragma unroll
-          for (int j = 2 * h; j < 2 * h + 2; ++j) {
-            s[t][n][j] = am_exp2(fmaf(s[t][n][j], a.scale_log2, -m));
-            sum += s[t][n][j];
-          }
-        l[t][h] += sum;  // this thread's keys only
-      }
-    }
-    if constexpr (!F32) {
-      uint32_t pa[MT][PP][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-          uint32_t p[PP];
-          am_split_bf16<PP>(s[t][r >> 1][(r & 1) * 2], s[t][r >> 1][(r & 1) * 2 + 1], p);
-#pragma unroll
-          for (int part = 0; part < PP; ++part) pa[t][part][r] = p[part];
-        }
-#pragma unroll
-      for (int n = 0; n < NT; n += 2) {
-        uint32_t b[4];
-        am_ld4t(b, vt + (((lane >> 3) & 1) * 8 + (lane & 7)) * G::PITCH + n * 16 + (lane >> 4) * 16);
-#pragma unroll
-        for (int t = 0; t < MT; ++t)
-#pragma unroll
-          for (int part = 0; part < PP; ++part) {
-            if (t == 1 && !two) continue;
-            am_mma16(o[t][n], pa[t][part], b[0], b[1]);
-            am_mma16(o[t][n + 1], pa[t][part], b[2], b[3]);
-          }
-      }
-    } else {
-      // A column c is key 2 c, column c + 4 key 2 c + 1: the scores' own registers
-      uint32_t ph[MT][4], pl[MT][4];
-#pragma unroll
-      for (int t = 0; t < MT; ++t) {
-        am_split_tf32(s[t][0][0], &ph[t][0], &pl[t][0]);
-        am_split_tf32(s[t][0][2], &ph[t][1], &pl[t][1]);
-        am_split_tf32(s[t][0][1], &ph[t][2], &pl[t][2]);
-        am_split_tf32(s[t][0][3], &ph[t][3], &pl[t][3]);
-      }
-      const unsigned char* vrow = ring + stage * 2 * G::TILE + G::TILE + 2 * (lane & 3) * G::PITCH + (lane >> 2) * 4;
-#pragma unroll
-      for (int n = 0; n < NT; ++n) {
         uint32_t bh0, bl0, bh1, bl1;
-        am_split_tf32(*reinterpret_cast<const float*>(vrow + n * 32), &bh0, &bl0);
-        am_split_tf32(*reinterpret_cast<const float*>(vrow + G::PITCH + n * 32), &bh1, &bl1);
-#pragma unroll
-        for (int t = 0; t < MT; ++t) {
-          am_mma8(o[t][n], ph[t], bh0, bh1);
-          am_mma8(o[t][n], ph[t], bl0, bl1);
-          am_mma8(o[t][n], pl[t], bh0, bh1);
-        }
+        am_split_tf32(__uint_as_float(b[2 * h]), &bh0, &bl0);
+        am_split_tf32(__uint_as_float(b[2 * h + 1]), &bh1, &bl1);
+        const uint4* f = reinterpret_cast<const uint4*>(am_raw) + ((2 * kk + h) * 32 + lane);
+        const uint4 fh = f[0], fl = f[NT * 32];
+        const uint32_t qh[4] = {fh.x, fh.y, fh.z, fh.w}, ql[4] = {fl.x, fl.y, fl.z, fl.w};
+        am_mma8(s, qh, bh0, bh1);
+        am_mma8(s2, qh, bl0, bl1);
+        am_mma8(s3, ql, bh0, bh1);
       }
+    }
+    // register j is row lane / 4 + 8 (j / 2), key 2 (lane % 4) + j % 2
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[j] += s2[j] + s3[j];
+      if (!((ok >> (2 * (lane & 3) + (j & 1))) & 1u)) s[j] = -INFINITY;
+    }
+    float mx[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(s[2 * h], s[2 * h + 1]);
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * a.scale_log2;
+    }
+    if (__any_sync(0xffffffffu, mx[0] > mref[0] + kAmMargin || mx[1] > mref[1] + kAmMargin)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float nr = mx[h] > mref[h] + kAmMargin ? mx[h] : mref[h];
+        const float f = nr == mref[h] ? 1.f : am_exp2(mref[h] - nr);  // 0 on the first move
+        mref[h] = nr;
+        l[h] *= f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float m = mref[h] == -INFINITY ? 0.f : mref[h];  // nothing seen yet: every term is 0
+#pragma unroll
+      for (int j = 2 * h; j < 2 * h + 2; ++j) s[j] = am_exp2(fmaf(s[j], a.scale_log2, -m));
+      l[h] += s[2 * h] + s[2 * h + 1];  // this thread's keys only
+    }
+    // A column c is key 2 c, column c + 4 key 2 c + 1: the scores' own registers
+    uint32_t ph[4], pl[4];
+    am_split_tf32(s[0], &ph[0], &pl[0]);
+    am_split_tf32(s[2], &ph[1], &pl[1]);
+    am_split_tf32(s[1], &ph[2], &pl[2]);
+    am_split_tf32(s[3], &ph[3], &pl[3]);
+    const unsigned char* vrow = ring + stage * 2 * G::TILE + G::TILE + 2 * (lane & 3) * G::PITCH + (lane >> 2) * 4;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      uint32_t bh0, bl0, bh1, bl1;
+      am_split_tf32(*reinterpret_cast<const float*>(vrow + n * 32), &bh0, &bl0);
+      am_split_tf32(*reinterpret_cast<const float*>(vrow + G::PITCH + n * 32), &bh1, &bl1);
+      am_mma8(o[n], ph, bh0, bh1);
+      am_mma8(o[n], ph, bl0, bl1);
+      am_mma8(o[n], pl, bh0, bh1);
     }
     ok = next_ok;
   }
@@ -449,40 +360,38 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
 
   // ---- join the four warps ----
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 1);
-      l[t][h] += __shfl_xor_sync(0xffffffffu, l[t][h], 2);
-      if ((lane & 3) == 0) {
-        s_m[warp][t * 16 + h * 8 + (lane >> 2)] = mref[t][h];
-        s_l[warp][t * 16 + h * 8 + (lane >> 2)] = l[t][h];
-      }
+  for (int h = 0; h < 2; ++h) {
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+    l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+    if ((lane & 3) == 0) {
+      s_m[warp][h * 8 + (lane >> 2)] = mref[h];
+      s_l[warp][h * 8 + (lane >> 2)] = l[h];
     }
+  }
   __syncthreads();  // every warp is past its ring
   float* join = reinterpret_cast<float*>(am_raw + G::QBYTES);
 #pragma unroll
-  for (int t = 0; t < MT; ++t)
+  for (int h = 0; h < 2; ++h) {
+    const int r = h * 8 + (lane >> 2);
+    if (r >= nrows) continue;
+    float m = -INFINITY;
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      const int r = t * 16 + h * 8 + (lane >> 2);
-      float m = -INFINITY;
+    for (int w = 0; w < kAmWarps; ++w) m = fmaxf(m, s_m[w][r]);
+    const float f = m == -INFINITY ? 1.f : am_exp2(mref[h] - m);
 #pragma unroll
-      for (int w = 0; w < kAmWarps; ++w) m = fmaxf(m, s_m[w][r]);
-      const float f = m == -INFINITY ? 1.f : am_exp2(mref[t][h] - m);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-        *reinterpret_cast<float2*>(join + (warp * 16 * MT + r) * DP + n * 8 + 2 * (lane & 3)) =
-            make_float2(o[t][n][2 * h] * f, o[t][n][2 * h + 1] * f);
-    }
+    for (int n = 0; n < NT; ++n)
+      *reinterpret_cast<float2*>(join + (warp * 16 + r) * DP + n * 8 + 2 * (lane & 3)) =
+          make_float2(o[n][2 * h] * f, o[n][2 * h + 1] * f);
+  }
   __syncthreads();
   const long long total_rows = static_cast<long long>(a.batch) * a.n_q;
-  for (int i = tid; i < nrows * (a.d / 4); i += kAmThreads) {
-    const int r = i / (a.d / 4), e = i % (a.d / 4) * 4, row = row0 + r;
+  for (int i = tid; i < nrows * (DP / 4); i += kAmThreads) {
+    const int r = i / (DP / 4), e = i % (DP / 4) * 4, row = row0 + r;
+    if (e >= a.d) continue;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kAmWarps; ++w) {
-      const float4 y = *reinterpret_cast<const float4*>(join + (w * 16 * MT + r) * DP + e);
+      const float4 y = *reinterpret_cast<const float4*>(join + (w * 16 + r) * DP + e);
       x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
     }
     const long long at = slot * total_rows + static_cast<long long>(row / a.group) * a.n_q + g * a.group + row % a.group;
@@ -496,34 +405,32 @@ __global__ void __launch_bounds__(kAmThreads, MT == 1 && !F32 && QP == 1 ? 3 : 2
       a.part_ml[at] = make_float2(m, sum);
     }
   }
-  // This launch may run beside attn_prefix_tc_kernel: it ends after that one, so
-  // that the join, which waits for this launch, finds both.
-  pdl_wait();
 }
 
-// Launches attn_mma_kernel for a head size and row tiles (1 or 2); sets the
-// kernel's shared-memory limit on its first launch on a device.
-template <typename QT, int DP, int QP, int MT, bool F32>
+// Launches attn_f32_kernel for a head size; sets its shared-memory limit on its
+// first launch on a device.
+template <typename QT, int DP>
 cudaError_t am_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) {
-  constexpr size_t smem = AmGeom<DP, QP, MT, F32>::SMEM;
+  constexpr size_t smem = AmGeom<DP>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[dev]) {
-    const cudaError_t e = allow_smem(attn_mma_kernel<QT, DP, QP, MT, F32>, smem);
+    const cudaError_t e = allow_smem(attn_f32_kernel<QT, DP>, smem);
     if (e != cudaSuccess) return e;
     lifted[dev] = true;
   }
-  return launch_k(attn_mma_kernel<QT, DP, QP, MT, F32>, dim3(items), dim3(kAmThreads), smem, st, true, a);
+  return launch_k(attn_f32_kernel<QT, DP>, dim3(items), dim3(kAmThreads), smem, st, true, a);
 }
 
-template <typename QT, int QP, int MT, bool F32>
-cudaError_t am_launch_head(const AmArgs& a, int items, int dev, cudaStream_t st) {
-  if (a.d <= 16) return am_launch_one<QT, 16, QP, MT, F32>(a, items, dev, st);
-  if (a.d <= 64) return am_launch_one<QT, 64, QP, MT, F32>(a, items, dev, st);
-  return am_launch_one<QT, 128, QP, MT, F32>(a, items, dev, st);
+template <typename QT>
+cudaError_t am_launch(const AmArgs& a, int items, int dev, cudaStream_t st) {
+  if (a.d <= 16) return am_launch_one<QT, 16>(a, items, dev, st);
+  if (a.d <= 64) return am_launch_one<QT, 64>(a, items, dev, st);
+  return am_launch_one<QT, 128>(a, items, dev, st);
 }
 
-// bfloat16 and float32 caches (attn_shared.cu, attn_shared_f32.cu).
-cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st);
-cudaError_t am_launch_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st);
+// The launches over a cache type for float32 or bfloat16 queries
+// (attn_shared_f32.cu, attn_shared_bf16.cu). na: rows of a prefix item, 8 or 16.
+cudaError_t launch_attn_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st);
+cudaError_t launch_attn_bf16(const AmArgs& a, bool q_f32, int na, int items, int dev, cudaStream_t st);
 
 }  // namespace wsg

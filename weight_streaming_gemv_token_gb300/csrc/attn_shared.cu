@@ -16,20 +16,13 @@
 
 namespace wsg {
 
-cudaError_t am_launch_bf16(const AmArgs& a, bool q_f32, int mt, int items, int dev, cudaStream_t st) {
-  if (q_f32)
-    return mt == 2 ? am_launch_head<float, 3, 2, false>(a, items, dev, st)
-                   : am_launch_head<float, 3, 1, false>(a, items, dev, st);
-  return mt == 2 ? am_launch_head<uint16_t, 1, 2, false>(a, items, dev, st)
-                 : am_launch_head<uint16_t, 1, 1, false>(a, items, dev, st);
-}
-
 namespace {
 
 struct AmJoinArgs {
   int batch, n_q, d;
   int warps;  // a row
-  int prefix_slots, own_chunk;
+  int prefix_slots, own_block, n_kv, group;
+  long long own_seg, own_per;  // as in AmArgs
   PagePool pool;
   const int32_t* len;
   const float* part_o;
@@ -57,7 +50,11 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AmJoinArgs a) {
   const int n = a.len[b];
   if (n < 0) return;  // (the same for the whole CTA where it works on one row)
   const long long held = n < page_capacity(a.pool) ? n : page_capacity(a.pool);
-  const int slots = a.prefix_slots + static_cast<int>((held + a.own_chunk - 1) / a.own_chunk);
+  // the pieces of the line of own blocks that this row's segment lies in
+  const long long blocks = (held + a.own_block - 1) / a.own_block;
+  const long long seg0 = (static_cast<long long>(b) * a.n_kv + w % a.n_q / a.group) * a.own_seg;
+  const int own = blocks > 0 ? static_cast<int>((seg0 + blocks - 1) / a.own_per - seg0 / a.own_per) + 1 : 0;
+  const int slots = a.prefix_slots + own;
   const long long total = static_cast<long long>(a.batch) * a.n_q;
   const bool in = lane * 4 < a.d;
   float m = -INFINITY, l = 0.f;
@@ -151,40 +148,59 @@ constexpr int kTcRowsMin = 16;  // rows of a key/value head above which the pref
 // How a call is cut up.
 struct AsPlan {
   bool tc;  // the prefix on attn_prefix_tc_kernel (row_groups: blocks of 128 rows)
-  int mt, row_groups;
-  int prefix_slots, prefix_chunk, own_slots, own_chunk;
+  int na, row_groups;  // rows of a prefix item otherwise
+  int prefix_slots, prefix_chunk, own_slots, own_block;
+  long long own_seg, own_per;
   long long prefix_items, own_items;  // CTAs
-  size_t o, ml, total;  // workspace offsets and size
+  size_t o, ml, total;                // workspace offsets and size
 };
 
 AsPlan attn_plan(const attn_shared_args* a, int sms) {
   AsPlan p{};
+  auto up = [](long long x, long long y) { return (x + y - 1) / y; };
   const bool f32 = a->kvdtype == DEC_F32;
   const int group = a->n_q / a->n_kv, rows = a->batch * group;
-  const int unit = kAmWarps * (f32 ? 8 : 16);  // keys the warps of a CTA take at once
-  const long long resident = 2ll * sms;        // CTAs the GPU holds
   p.tc = !f32 && a->qdtype == DEC_BF16 && a->head_dim == kApD && rows > kTcRowsMin && a->prefix_len > 0 &&
          a->prefix_stride < 1ll << 31;
-  p.mt = !f32 && !p.tc && rows > 16 ? 2 : 1;
-  const int block = p.tc ? kApRows : 16 * p.mt;
-  p.row_groups = (rows + block - 1) / block;
+  p.na = f32 || (rows > 8 && !p.tc) ? 16 : 8;
+  const int block = p.tc ? kApRows : p.na;
+  p.row_groups = static_cast<int>(up(rows, block));
+  const long long capacity = static_cast<long long>(a->table_stride) << page_shift(a->page_size);
+  const long long segments = static_cast<long long>(a->batch) * a->n_kv;      // of own keys
+  const long long heads = static_cast<long long>(a->n_kv) * p.row_groups;     // prefix items of a split
   // an axis of `keys` keys into about `want` splits of whole units
   auto cut = [&](long long keys, long long unit, long long want, int* slots, int* chunk) {
-    const long long units = (keys + unit - 1) / unit;
-    if (want < 1) want = 1;
-    const long long per = (units + want - 1) / want;
+    const long long per = up(up(keys, unit), want < 1 ? 1 : want);
     *chunk = static_cast<int>((per < 1 ? 1 : per) * unit);
-    *slots = static_cast<int>((keys + *chunk - 1) / *chunk);
+    *slots = static_cast<int>(up(keys, *chunk));
   };
-  const long long each = static_cast<long long>(a->n_kv) * p.row_groups, own = static_cast<long long>(a->batch) * a->n_kv;
-  if (p.tc)
-    cut(a->prefix_len, kApKeys, sms / each, &p.prefix_slots, &p.prefix_chunk);
-  else
-    cut(a->prefix_len, unit, (resident + each - 1) / each, &p.prefix_slots, &p.prefix_chunk);
-  cut(static_cast<long long>(a->table_stride) << page_shift(a->page_size), unit, (resident + own - 1) / own, &p.own_slots,
-      &p.own_chunk);
-  p.prefix_items = p.prefix_slots * each;
-  p.own_items = p.own_slots * own;
+  if (f32) {
+    // two CTAs an SM
+    cut(a->prefix_len, kAmWarps * 8, up(2ll * sms, heads), &p.prefix_slots, &p.prefix_chunk);
+    cut(capacity, kAmWarps * 8, up(2ll * sms, segments), &p.own_slots, &p.own_block);
+    p.own_seg = p.own_slots;
+    p.own_per = 1;
+    p.own_items = p.own_slots * segments;
+  } else {
+    // The CTAs that the GPU holds (three an SM; two with float32 queries) are shared
+    // out by the number of 64-key units; the own ones walk equal pieces.
+    const long long resident = (a->qdtype == DEC_BF16 ? 3ll : 2ll) * sms;
+    const long long units = p.tc ? 0 : up(a->prefix_len, 64) * heads;
+    p.own_block = 16;
+    p.own_seg = up(capacity, 16);
+    const long long line = p.own_seg * segments;  // own blocks
+    long long pre = units ? resident * units / (units + up(line, 4)) : 0;
+    if (p.tc)
+      cut(a->prefix_len, kApKeys, sms / heads, &p.prefix_slots, &p.prefix_chunk);
+    else
+      cut(a->prefix_len, 64, pre / heads, &p.prefix_slots, &p.prefix_chunk);
+    pre = p.tc ? 0 : p.prefix_slots * heads;
+    const long long left = resident - pre > resident / 4 ? resident - pre : resident / 4;
+    p.own_per = line > 0 ? up(line, left * kAmWarps) : 1;
+    p.own_items = up(up(line, p.own_per), kAmWarps);
+    p.own_slots = p.own_seg > 0 ? static_cast<int>((p.own_seg - 1 + p.own_per - 1) / p.own_per + 1) : 0;
+  }
+  p.prefix_items = p.prefix_slots * heads;
   const long long parts = static_cast<long long>(p.prefix_slots + p.own_slots) * a->batch * a->n_q;
   p.o = 0;
   p.ml = (static_cast<size_t>(parts) * a->head_dim * 4 + 255) / 256 * 256;
@@ -259,7 +275,10 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   k.row_groups = p.row_groups;
   k.prefix_items = p.tc ? 0 : static_cast<int>(p.prefix_items);
   k.prefix_chunk = p.prefix_chunk;
-  k.own_chunk = p.own_chunk;
+  k.own_block = p.own_block;
+  k.own_seg = p.own_seg;
+  k.own_per = p.own_per;
+  k.q_even = reinterpret_cast<uintptr_t>(a->q) % 4 == 0 && a->q_stride % 2 == 0;
   k.own_slot0 = p.prefix_slots;
   k.part_o = reinterpret_cast<float*>(w + p.o);
   k.part_ml = reinterpret_cast<float2*>(w + p.ml);
@@ -299,15 +318,19 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   const int items = k.prefix_items + static_cast<int>(p.own_items);
   k.first = !p.tc;
   if (items > 0)
-    WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? am_launch_f32(k, qf, items, di.device, s)
-                                                : am_launch_bf16(k, qf, p.mt, items, di.device, s));
+    WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_attn_f32(k, qf, items, di.device, s)
+                                                : launch_attn_bf16(k, qf, p.na, items, di.device, s));
   AmJoinArgs j{};
   j.batch = a->batch;
   j.n_q = a->n_q;
   j.d = a->head_dim;
   j.prefix_slots = p.prefix_slots;
   j.warps = p.prefix_slots + p.own_slots > 8 ? 4 : 1;
-  j.own_chunk = p.own_chunk;
+  j.own_block = p.own_block;
+  j.own_seg = p.own_seg;
+  j.own_per = p.own_per;
+  j.n_kv = a->n_kv;
+  j.group = k.group;
   j.pool = k.pool;
   j.len = a->seq_len;
   j.part_o = k.part_o;

@@ -1,11 +1,10 @@
-// attn_shared_prefix over float32 caches: the launches of attn_mma_kernel's tf32 form.
+// attn_shared_prefix over float32 caches: the launches of attn_f32_kernel.
 #include "attn_mma.cuh"
 
 namespace wsg {
 
-cudaError_t am_launch_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st) {
-  return q_f32 ? am_launch_head<float, 3, 1, true>(a, items, dev, st)
-               : am_launch_head<uint16_t, 1, 1, true>(a, items, dev, st);
+cudaError_t launch_attn_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st) {
+  return q_f32 ? am_launch<float>(a, items, dev, st) : am_launch<uint16_t>(a, items, dev, st);
 }
 
 }  // namespace wsg
