@@ -414,7 +414,7 @@ cudaError_t am_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) 
   constexpr size_t smem = AmGeom<DP>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[dev]) {
-    const cudaError_t e = allow_smem(attn_f32_kernel<QT, DP>, smem);
+    const cudaError_t e = allow_smem_shared(attn_f32_kernel<QT, DP>, smem);
     if (e != cudaSuccess) return e;
     lifted[dev] = true;
   }

@@ -34,6 +34,8 @@ constexpr int kApStages = 2, kApThreads = 32 * 10;
 constexpr uint32_t kApTile = kApKeys * kApD * 2, kApBox = kApTile / 2;
 constexpr uint32_t kApTmO = 256, kApTmQ = 384;
 constexpr size_t kApSmem = 2 * kApStages * kApTile + 1024;
+constexpr int kApPitch = kApD + 4;  // floats a row of O in shared memory
+static_assert(kApRows * kApPitch * 4 <= 2 * kApStages * kApTile, "O fits in the rings");
 
 struct ApArgs {
   const uint16_t* q;
@@ -57,7 +59,7 @@ __device__ __forceinline__ void tma_load_3d_map(void* dst, const CUtensorMap* ma
 
 // Grid: blockIdx.x = (split * n_kv + head) * row_blocks + row block. kmap, vmap:
 // the prefix as [n_kv][plen][128] in 128-row x 64-column boxes.
-__global__ void __maxnreg__(128)
+__global__ void __maxnreg__(120)
     attn_prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                           const ApArgs a) {
   extern __shared__ __align__(1024) unsigned char ap_raw[];
@@ -318,16 +320,28 @@ __global__ void __maxnreg__(128)
       tc_fence_after();
       const long long at = static_cast<long long>(split) * a.batch * a.n_q + prow;
       if (have && half == 0) a.part_ml[at] = make_float2(m_ref, lsum + xch[T & 1][1][v]);
+      // O through shared memory (the rings are done with), so that a warp writes
+      // whole rows: 16-byte pieces a row apart from every lane kept the CTA 5 us
+      // longer on its SM
+      float* so = reinterpret_cast<float*>(Ks);
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 32) {
         uint32_t o[32];
         tc_ld32(o, to + c0);
         tc_wait_ld();
-        if (have) {
-          uint4* dst = reinterpret_cast<uint4*>(a.part_o + at * kApD + half * 64 + c0);
+        uint4* dst = reinterpret_cast<uint4*>(so + v * kApPitch + half * 64 + c0);
 #pragma unroll
-          for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-        }
+        for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+      }
+      asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");  // the two warps of the lane quarter
+#pragma unroll 4
+      for (int r = q * 32 + half * 16; r < q * 32 + half * 16 + 16; ++r) {
+        if (r >= nrows) break;
+        const int row = row0 + r;
+        const long long to_row = static_cast<long long>(split) * a.batch * a.n_q +
+                                 static_cast<long long>(row / a.group) * a.n_q + g * a.group + row % a.group;
+        *reinterpret_cast<float4*>(a.part_o + to_row * kApD + lane * 4) =
+            *reinterpret_cast<const float4*>(so + r * kApPitch + lane * 4);
       }
     }
     if (!ok && lane == 0) fail();

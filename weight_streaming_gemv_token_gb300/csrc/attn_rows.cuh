@@ -481,7 +481,7 @@ cudaError_t ar_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) 
   constexpr size_t smem = ArGeom<DP, NA>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[dev]) {
-    const cudaError_t e = allow_smem(attn_rows_kernel<QT, DP, QP, NA, NB>, smem);
+    const cudaError_t e = allow_smem_shared(attn_rows_kernel<QT, DP, QP, NA, NB>, smem);
     if (e != cudaSuccess) return e;
     lifted[dev] = true;
   }

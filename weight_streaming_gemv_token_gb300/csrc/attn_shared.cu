@@ -309,7 +309,7 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
     }
     static bool lifted[64] = {};
     if (!lifted[di.device]) {
-      WSG_CUDA_TRY(nullptr, allow_smem(attn_prefix_tc_kernel, kApSmem));
+      WSG_CUDA_TRY(nullptr, allow_smem_shared(attn_prefix_tc_kernel, kApSmem));
       lifted[di.device] = true;
     }
     WSG_CUDA_TRY(nullptr, launch_k(attn_prefix_tc_kernel, dim3(static_cast<unsigned>(p.prefix_items)), dim3(kApThreads),

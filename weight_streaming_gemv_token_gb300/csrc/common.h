@@ -72,6 +72,17 @@ cudaError_t allow_smem(K kern, size_t bytes) {
   return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
 }
 
+// The same for a kernel whose CTAs share their SMs with another kernel's: the SM
+// is asked for all the shared memory it can give, or the first kernel's need sets
+// the split and the other does not fit beside it.
+template <typename K>
+cudaError_t allow_smem_shared(K kern, size_t bytes) {
+  cudaError_t e = allow_smem(kern, bytes);
+  if (e == cudaSuccess)
+    e = cudaFuncSetAttribute(kern, cudaFuncAttributePreferredSharedMemoryCarveout, cudaSharedmemCarveoutMaxShared);
+  return e;
+}
+
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 // Tiled TMA descriptor (CUtensorMap, 128 bytes, opaque here) of a row-major
