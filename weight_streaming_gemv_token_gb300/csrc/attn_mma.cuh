@@ -429,7 +429,8 @@ cudaError_t am_launch(const AmArgs& a, int items, int dev, cudaStream_t st) {
 }
 
 // The launches over a cache type for float32 or bfloat16 queries
-// (attn_shared_f32.cu, attn_shared_bf16.cu). na: rows of a prefix item, 8 or 16.
+// (attn_shared_f32.cu, attn_shared_bf16.cu). na: rows of a prefix item, 8 or 16; 0:
+// no prefix items, beside attn_prefix_tc_kernel.
 cudaError_t launch_attn_f32(const AmArgs& a, bool q_f32, int items, int dev, cudaStream_t st);
 cudaError_t launch_attn_bf16(const AmArgs& a, bool q_f32, int na, int items, int dev, cudaStream_t st);
 

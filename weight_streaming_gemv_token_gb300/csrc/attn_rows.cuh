@@ -13,8 +13,8 @@
 //
 // Each warp streams blocks of 16 keys with 16-byte asynchronous copies through
 // two stages of its own, so the main loop has no CTA-wide barrier:
-//   prefix CTAs  the four warps take the blocks of one range of the prefix in
-//                turn and join through shared memory at its end;
+//   prefix CTAs  the warps take the blocks of one range of the prefix in turn and
+//                join through shared memory at its end;
 //   own CTAs     the blocks of all branches' own keys form one line of
 //                batch * n_kv segments of equal capacity; each warp takes an equal
 //                piece of it, across segments, and writes a partial result per
@@ -34,14 +34,15 @@
 
 namespace wsg {
 
-template <int DP, int NR>
+template <int DP, int NR, int WARPS>
 struct ArGeom {
   static constexpr int KB = 16;               // keys a block
   static constexpr int PITCH = DP * 2 + 16;   // bytes a row
   static constexpr int TILE = KB * PITCH;     // keys (or values) of a block
   static constexpr int RING = 2 * 2 * TILE;   // per warp: two stages
   static constexpr int JOIN = NR * DP * 4;    // per warp, in the place of the ring
-  static constexpr int SMEM = kAmWarps * (RING > JOIN ? RING : JOIN);
+  static constexpr int PER_WARP = RING > JOIN ? RING : JOIN;
+  static constexpr int SMEM = WARPS * PER_WARP;
 };
 
 __device__ __forceinline__ uint32_t ar_transpose(uint32_t x) {
@@ -54,7 +55,7 @@ __device__ __forceinline__ uint32_t ar_transpose(uint32_t x) {
 // pair 2 (lane % 4) of each tile of 8 rows, key (or head element) lane / 4.
 template <typename QT, int DP, int QP, int NR>
 struct ArCore {
-  using G = ArGeom<DP, NR>;
+  static constexpr int PITCH = DP * 2 + 16, TILE = 16 * PITCH;
   static constexpr int T = NR / 8, KK = DP / 16, PP = QP == 1 ? 2 : 3;
   uint32_t q[QP][KK][T][2];
   float o[KK][T][4];
@@ -114,14 +115,14 @@ struct ArCore {
   // One block: keys at shared address kt, values at kt + TILE, `ok` its keys that count.
   __device__ __forceinline__ void consume(uint32_t kt, uint32_t ok, float scale) {
     const int lane = threadIdx.x & 31;
-    const uint32_t vt = kt + G::TILE;
+    const uint32_t vt = kt + TILE;
     float s[T][4];
 #pragma unroll
     for (int t = 0; t < T; ++t) s[t][0] = s[t][1] = s[t][2] = s[t][3] = 0.f;
 #pragma unroll
     for (int k = 0; k < KK; ++k) {
       uint32_t ka[4];
-      am_ld4(ka, kt + (lane & 15) * G::PITCH + k * 32 + (lane >> 4) * 16);
+      am_ld4(ka, kt + (lane & 15) * PITCH + k * 32 + (lane >> 4) * 16);
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -175,7 +176,7 @@ struct ArCore {
 #pragma unroll
     for (int k = 0; k < KK; ++k) {
       uint32_t va[4];
-      am_ld4t(va, vt + ((lane >> 4) * 8 + (lane & 7)) * G::PITCH + k * 32 + ((lane >> 3) & 1) * 16);
+      am_ld4t(va, vt + ((lane >> 4) * 8 + (lane & 7)) * PITCH + k * 32 + ((lane >> 3) & 1) * 16);
 #pragma unroll
       for (int t = 0; t < T; ++t)
 #pragma unroll
@@ -273,14 +274,18 @@ struct ArCopy {
   }
 };
 
-// NA, NB: rows of a prefix item (8 or 16) and of a branch (8, or 16 for groups
-// over 8). CTAs below a.prefix_items are prefix items, the others own CTAs.
+// NA, NB: rows of a prefix item (8 or 16; 0: no prefix items) and of a branch (8,
+// or 16 for groups over 8). CTAs below a.prefix_items are prefix items, the others
+// own CTAs. Eight warps, one CTA an SM, where the prefix is cut here (few splits to
+// join: 4 x 32768 takes 34 us with three CTAs of four warps an SM, 28 with a third
+// of the splits); four warps beside attn_prefix_tc_kernel, whose CTAs leave 152
+// registers a thread and 90 KB of shared memory for one.
 template <typename QT, int DP, int QP, int NA, int NB>
-__global__ void __launch_bounds__(kAmThreads, QP == 1 ? 3 : 2) attn_rows_kernel(const AmArgs a) {
-  using G = ArGeom<DP, NA>;
-  constexpr int PER_WARP = G::SMEM / kAmWarps;
+__global__ void __launch_bounds__(NA ? 256 : 128, NA ? 1 : 3) attn_rows_kernel(const AmArgs a) {
+  constexpr int WARPS = NA ? 8 : 4;
+  using G = ArGeom<DP, NA, WARPS>;
+  constexpr int PER_WARP = G::PER_WARP;
   extern __shared__ __align__(128) unsigned char am_raw[];
-  __shared__ float s_m[kAmWarps][NA], s_l[kAmWarps][NA];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   unsigned char* mine = am_raw + warp * PER_WARP;
   const ArCopy<DP> copy(a.d, mine);
@@ -291,89 +296,92 @@ __global__ void __launch_bounds__(kAmThreads, QP == 1 ? 3 : 2) attn_rows_kernel(
   if (a.first) pdl_wait();
   pdl_trigger();  // the join's CTAs may take their places and wait
 
-  if (static_cast<int>(blockIdx.x) < a.prefix_items) {
-    const int rg = blockIdx.x % a.row_groups, t0 = blockIdx.x / a.row_groups;
-    const int g = t0 % a.n_kv, slot = t0 / a.n_kv;
-    const int row0 = rg * NA, nrows = min(NA, a.rows - row0);
-    const int k0 = slot * a.prefix_chunk, k1 = min(a.plen, k0 + a.prefix_chunk);
-    const int nblk = (k1 - k0 + 15) / 16;
-    auto request = [&](int stage, int blk) {
-      const int k = k0 + blk * 16;
-      return copy.run(stage, a.pk, a.pv, a.pstride * g + k, min(16, k1 - k));
-    };
-    uint32_t ok = 0;
-    if (warp < nblk) ok = request(0, warp);
-    am_commit();
-    auto place = [&](int r) {  // row r of this item among all (branch, query head) rows
-      return static_cast<long long>((row0 + r) / a.group) * a.n_q + g * a.group + (row0 + r) % a.group;
-    };
-    ArCore<QT, DP, QP, NA> core;
-    core.load(a, nrows, [&](int r) {
-      return a.q_stride * ((row0 + r) / a.group) + static_cast<long long>(g * a.group + (row0 + r) % a.group) * a.d;
-    });
-    int stage = 0;
-    for (int blk = warp; blk < nblk; blk += kAmWarps, stage ^= 1) {
-      __syncwarp();  // every lane is done with the block before this one
-      const uint32_t next = blk + kAmWarps < nblk ? request(stage ^ 1, blk + kAmWarps) : 0;
+  if (NA && static_cast<int>(blockIdx.x) < a.prefix_items) {
+    if constexpr (NA > 0) {
+      __shared__ float s_m[WARPS][NA], s_l[WARPS][NA];
+      const int rg = blockIdx.x % a.row_groups, t0 = blockIdx.x / a.row_groups;
+      const int g = t0 % a.n_kv, slot = t0 / a.n_kv;
+      const int row0 = rg * NA, nrows = min(NA, a.rows - row0);
+      const int k0 = slot * a.prefix_chunk, k1 = min(a.plen, k0 + a.prefix_chunk);
+      const int nblk = (k1 - k0 + 15) / 16;
+      auto request = [&](int stage, int blk) {
+        const int k = k0 + blk * 16;
+        return copy.run(stage, a.pk, a.pv, a.pstride * g + k, min(16, k1 - k));
+      };
+      uint32_t ok = 0;
+      if (warp < nblk) ok = request(0, warp);
       am_commit();
-      am_wait<1>();
-      __syncwarp();  // this block has landed for every lane
-      core.consume(ring + stage * 2 * G::TILE, ok, a.scale_log2);
-      ok = next;
-    }
-    am_wait<0>();
-    core.finish();
-    // ---- join the four warps ----
-#pragma unroll
-    for (int t = 0; t < NA / 8; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-        if (lane < 4) {
-          s_m[warp][t * 8 + 2 * lane + j] = core.m[t][j];
-          s_l[warp][t * 8 + 2 * lane + j] = core.l[t][j];
-        }
-    __syncthreads();  // every warp is past its ring
-    float* out = reinterpret_cast<float*>(mine);
-#pragma unroll
-    for (int t = 0; t < NA / 8; ++t)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const int r = t * 8 + 2 * (lane & 3) + j;
-        if (r >= nrows) continue;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kAmWarps; ++w) m = fmaxf(m, s_m[w][r]);
-        const float f = m == -INFINITY ? 1.f : am_exp2(core.m[t][j] - m);
-#pragma unroll
-        for (int k = 0; k < DP / 16; ++k) {
-          out[r * DP + k * 16 + (lane >> 2)] = core.o[k][t][j] * f;
-          out[r * DP + k * 16 + 8 + (lane >> 2)] = core.o[k][t][2 + j] * f;
-        }
+      auto place = [&](int r) {  // row r of this item among all (branch, query head) rows
+        return static_cast<long long>((row0 + r) / a.group) * a.n_q + g * a.group + (row0 + r) % a.group;
+      };
+      ArCore<QT, DP, QP, NA> core;
+      core.load(a, nrows, [&](int r) {
+        return a.q_stride * ((row0 + r) / a.group) + static_cast<long long>(g * a.group + (row0 + r) % a.group) * a.d;
+      });
+      int stage = 0;
+      for (int blk = warp; blk < nblk; blk += WARPS, stage ^= 1) {
+        __syncwarp();  // every lane is done with the block before this one
+        const uint32_t next = blk + WARPS < nblk ? request(stage ^ 1, blk + WARPS) : 0;
+        am_commit();
+        am_wait<1>();
+        __syncwarp();  // this block has landed for every lane
+        core.consume(ring + stage * 2 * G::TILE, ok, a.scale_log2);
+        ok = next;
       }
-    __syncthreads();
-    for (int i = tid; i < nrows * (DP / 4); i += kAmThreads) {
-      const int r = i / (DP / 4), e = i % (DP / 4) * 4;
-      if (e >= a.d) continue;
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < kAmWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(am_raw + w * PER_WARP + (r * DP + e) * 4);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-      }
-      const long long at = slot * total_rows + place(r);
-      *reinterpret_cast<float4*>(a.part_o + at * a.d + e) = x;
-      if (e == 0) {
-        float m = -INFINITY, sum = 0.f;
-#pragma unroll
-        for (int w = 0; w < kAmWarps; ++w) m = fmaxf(m, s_m[w][r]);
-#pragma unroll
-        for (int w = 0; w < kAmWarps; ++w) sum += m == -INFINITY ? s_l[w][r] : s_l[w][r] * am_exp2(s_m[w][r] - m);
-        a.part_ml[at] = make_float2(m, sum);
+      am_wait<0>();
+      core.finish();
+      // ---- join the warps ----
+  #pragma unroll
+      for (int t = 0; t < NA / 8; ++t)
+  #pragma unroll
+        for (int j = 0; j < 2; ++j)
+          if (lane < 4) {
+            s_m[warp][t * 8 + 2 * lane + j] = core.m[t][j];
+            s_l[warp][t * 8 + 2 * lane + j] = core.l[t][j];
+          }
+      __syncthreads();  // every warp is past its ring
+      float* out = reinterpret_cast<float*>(mine);
+  #pragma unroll
+      for (int t = 0; t < NA / 8; ++t)
+  #pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const int r = t * 8 + 2 * (lane & 3) + j;
+          if (r >= nrows) continue;
+          float m = -INFINITY;
+  #pragma unroll
+          for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
+          const float f = m == -INFINITY ? 1.f : am_exp2(core.m[t][j] - m);
+  #pragma unroll
+          for (int k = 0; k < DP / 16; ++k) {
+            out[r * DP + k * 16 + (lane >> 2)] = core.o[k][t][j] * f;
+            out[r * DP + k * 16 + 8 + (lane >> 2)] = core.o[k][t][2 + j] * f;
+          }
+        }
+      __syncthreads();
+      for (int i = tid; i < nrows * (DP / 4); i += 32 * WARPS) {
+        const int r = i / (DP / 4), e = i % (DP / 4) * 4;
+        if (e >= a.d) continue;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  #pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+          const float4 y = *reinterpret_cast<const float4*>(am_raw + w * PER_WARP + (r * DP + e) * 4);
+          x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        }
+        const long long at = slot * total_rows + place(r);
+        *reinterpret_cast<float4*>(a.part_o + at * a.d + e) = x;
+        if (e == 0) {
+          float m = -INFINITY, sum = 0.f;
+  #pragma unroll
+          for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
+  #pragma unroll
+          for (int w = 0; w < WARPS; ++w) sum += m == -INFINITY ? s_l[w][r] : s_l[w][r] * am_exp2(s_m[w][r] - m);
+          a.part_ml[at] = make_float2(m, sum);
+        }
       }
     }
   } else {
     // ---- this warp's piece of the line of own blocks ----
-    const long long w = static_cast<long long>(blockIdx.x - a.prefix_items) * kAmWarps + warp;
+    const long long w = static_cast<long long>(blockIdx.x - a.prefix_items) * WARPS + warp;
     const long long end = min((w + 1) * a.own_per, static_cast<long long>(a.batch) * a.n_kv * a.own_seg);
     // A block of the line: branch, head, first key, keys that count, the table's
     // entry of its page. Positions advance without divisions, and a block's entry
@@ -478,14 +486,15 @@ __global__ void __launch_bounds__(kAmThreads, QP == 1 ? 3 : 2) attn_rows_kernel(
 
 template <typename QT, int DP, int QP, int NA, int NB>
 cudaError_t ar_launch_one(const AmArgs& a, int items, int dev, cudaStream_t st) {
-  constexpr size_t smem = ArGeom<DP, NA>::SMEM;
+  constexpr int WARPS = NA ? 8 : 4;
+  constexpr size_t smem = ArGeom<DP, NA, WARPS>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[dev]) {
     const cudaError_t e = allow_smem_shared(attn_rows_kernel<QT, DP, QP, NA, NB>, smem);
     if (e != cudaSuccess) return e;
     lifted[dev] = true;
   }
-  return launch_k(attn_rows_kernel<QT, DP, QP, NA, NB>, dim3(items), dim3(kAmThreads), smem, st, true, a);
+  return launch_k(attn_rows_kernel<QT, DP, QP, NA, NB>, dim3(items), dim3(32 * WARPS), smem, st, true, a);
 }
 
 template <typename QT, int DP, int QP>
@@ -495,9 +504,14 @@ cudaError_t ar_launch_rows(const AmArgs& a, int na, int items, int dev, cudaStre
                   : ar_launch_one<QT, DP, QP, 8, 8>(a, items, dev, st);
 }
 
-// na: rows of a prefix item, 8 or 16.
+// na: rows of a prefix item, 8 or 16; 0: own keys only, beside attn_prefix_tc_kernel
+// (bfloat16 queries, head size 128).
 template <typename QT, int QP>
 cudaError_t ar_launch(const AmArgs& a, int na, int items, int dev, cudaStream_t st) {
+  if constexpr (QP == 1)
+    if (na == 0)
+      return a.group > 8 ? ar_launch_one<QT, 128, QP, 0, 16>(a, items, dev, st)
+                         : ar_launch_one<QT, 128, QP, 0, 8>(a, items, dev, st);
   if (a.d <= 16) return ar_launch_rows<QT, 16, QP>(a, na, items, dev, st);
   if (a.d <= 64) return ar_launch_rows<QT, 64, QP>(a, na, items, dev, st);
   return ar_launch_rows<QT, 128, QP>(a, na, items, dev, st);

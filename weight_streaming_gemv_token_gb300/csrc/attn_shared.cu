@@ -148,7 +148,7 @@ constexpr int kTcRowsMin = 16;  // rows of a key/value head above which the pref
 // How a call is cut up.
 struct AsPlan {
   bool tc;  // the prefix on attn_prefix_tc_kernel (row_groups: blocks of 128 rows)
-  int na, row_groups;  // rows of a prefix item otherwise
+  int na, row_groups;  // rows of a prefix item otherwise (0 with tc)
   int prefix_slots, prefix_chunk, own_slots, own_block;
   long long own_seg, own_per;
   long long prefix_items, own_items;  // CTAs
@@ -162,7 +162,7 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
   const int group = a->n_q / a->n_kv, rows = a->batch * group;
   p.tc = !f32 && a->qdtype == DEC_BF16 && a->head_dim == kApD && rows > kTcRowsMin && a->prefix_len > 0 &&
          a->prefix_stride < 1ll << 31;
-  p.na = f32 || (rows > 8 && !p.tc) ? 16 : 8;
+  p.na = p.tc ? 0 : f32 || rows > 8 ? 16 : 8;
   const int block = p.tc ? kApRows : p.na;
   p.row_groups = static_cast<int>(up(rows, block));
   const long long capacity = static_cast<long long>(a->table_stride) << page_shift(a->page_size);
@@ -182,22 +182,28 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
     p.own_per = 1;
     p.own_items = p.own_slots * segments;
   } else {
-    // The CTAs that the GPU holds (three an SM; two with float32 queries) are shared
-    // out by the number of 64-key units; the own ones walk equal pieces.
-    const long long resident = (a->qdtype == DEC_BF16 ? 3ll : 2ll) * sms;
-    const long long units = p.tc ? 0 : up(a->prefix_len, 64) * heads;
     p.own_block = 16;
     p.own_seg = up(capacity, 16);
     const long long line = p.own_seg * segments;  // own blocks
-    long long pre = units ? resident * units / (units + up(line, 4)) : 0;
-    if (p.tc)
+    long long warps;                              // that walk it
+    if (p.tc) {
       cut(a->prefix_len, kApKeys, sms / heads, &p.prefix_slots, &p.prefix_chunk);
-    else
-      cut(a->prefix_len, 64, pre / heads, &p.prefix_slots, &p.prefix_chunk);
-    pre = p.tc ? 0 : p.prefix_slots * heads;
-    const long long left = resident - pre > resident / 4 ? resident - pre : resident / 4;
-    p.own_per = line > 0 ? up(line, left * kAmWarps) : 1;
-    p.own_items = up(up(line, p.own_per), kAmWarps);
+      // One CTA of four warps fits beside a prefix CTA, three an SM after those
+      // have ended: a second wave pays when the first would walk over 8 blocks a warp
+      // (16 x 4096 + 256: 17.6 us with one wave, 19.6 with three CTAs an SM; 64 x 32768
+      // + 512: 69 and 60).
+      warps = 4ll * sms;
+      if (line > 8 * warps) warps *= 3;
+    } else {
+      // one CTA of eight warps an SM, shared out by the number of keys
+      const long long units = up(a->prefix_len, 128) * heads;
+      const long long pre = units ? sms * units / (units + up(line, 8)) : 0;
+      cut(a->prefix_len, 128, pre / heads, &p.prefix_slots, &p.prefix_chunk);
+      const long long left = sms - p.prefix_slots * heads;
+      warps = 8 * (left > sms / 4 ? left : sms / 4);
+    }
+    p.own_per = line > 0 ? up(line, warps) : 1;
+    p.own_items = up(up(line, p.own_per), p.tc ? 4 : 8);
     p.own_slots = p.own_seg > 0 ? static_cast<int>((p.own_seg - 1 + p.own_per - 1) / p.own_per + 1) : 0;
   }
   p.prefix_items = p.prefix_slots * heads;
