@@ -4,7 +4,7 @@
 //
 // An item is up to 16 query rows of one key/value head and a range of its keys:
 // rows of all branches over a range of the shared prefix, or the rows of one
-// branch over a range of its own pages. A CTA of four warps takes an item. Each
+// branch over a range of its own pages. A CTA of eight warps takes an item. Each
 // warp streams its own blocks of 8 keys with 16-byte asynchronous copies through
 // two stages of its own in shared memory, so the main loop has no CTA-wide
 // barrier:
@@ -31,7 +31,7 @@
 
 namespace wsg {
 
-constexpr int kAmWarps = 4, kAmThreads = 32 * kAmWarps;
+constexpr int kAmWarps = 8, kAmThreads = 32 * kAmWarps;
 constexpr float kAmMargin = 8.f;  // the reference moves past this margin (log2 units)
 
 struct AmArgs {
@@ -131,7 +131,7 @@ __device__ __forceinline__ void am_split_bf16(float x, float y, uint32_t (&p)[PA
 // Grid: prefix items, then one CTA per branch, head and piece (own_per 1, a block
 // being a whole range of own_block keys).
 template <typename QT, int DP>
-__global__ void __launch_bounds__(kAmThreads, 2) attn_f32_kernel(const AmArgs a) {
+__global__ void __launch_bounds__(kAmThreads, 1) attn_f32_kernel(const AmArgs a) {
   using G = AmGeom<DP>;
   constexpr int KB = G::KB, NT = DP / 8;
   extern __shared__ __align__(128) unsigned char am_raw[];
@@ -358,7 +358,7 @@ __global__ void __launch_bounds__(kAmThreads, 2) attn_f32_kernel(const AmArgs a)
   }
   am_wait<0>();
 
-  // ---- join the four warps ----
+  // ---- join the warps ----
 #pragma unroll
   for (int h = 0; h < 2; ++h) {
     l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);

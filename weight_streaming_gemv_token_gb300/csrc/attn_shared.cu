@@ -175,9 +175,12 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
     *slots = static_cast<int>(up(keys, *chunk));
   };
   if (f32) {
-    // two CTAs an SM
-    cut(a->prefix_len, kAmWarps * 8, up(2ll * sms, heads), &p.prefix_slots, &p.prefix_chunk);
-    cut(capacity, kAmWarps * 8, up(2ll * sms, segments), &p.own_slots, &p.own_block);
+    // one CTA an SM, shared out by the number of keys
+    constexpr int unit = kAmWarps * 8;
+    const long long pre = up(a->prefix_len, unit) * heads, own = up(capacity, unit) * segments;
+    cut(a->prefix_len, unit, pre ? sms * pre / (pre + own) / heads : 0, &p.prefix_slots, &p.prefix_chunk);
+    const long long left = sms - p.prefix_slots * heads;
+    cut(capacity, unit, up(left > sms / 4 ? left : sms / 4, segments), &p.own_slots, &p.own_block);
     p.own_seg = p.own_slots;
     p.own_per = 1;
     p.own_items = p.own_slots * segments;
@@ -198,7 +201,7 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
       // one CTA of eight warps an SM, shared out by the number of keys
       const long long units = up(a->prefix_len, 128) * heads;
       const long long pre = units ? sms * units / (units + up(line, 8)) : 0;
-      cut(a->prefix_len, 128, pre / heads, &p.prefix_slots, &p.prefix_chunk);
+      cut(a->prefix_len, 64, pre / heads, &p.prefix_slots, &p.prefix_chunk);
       const long long left = sms - p.prefix_slots * heads;
       warps = 8 * (left > sms / 4 ? left : sms / 4);
     }
