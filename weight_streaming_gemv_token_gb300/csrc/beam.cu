@@ -7,7 +7,7 @@
 //           index) and sum of exp(x - maximum), the running pair of a softmax;
 //   pass 2  every CTA joins the chunks' pairs into the rows' lse, so that each
 //           chunk's maximum becomes a key. The n_out-th best of these keys (by
-//           bisection) is a lower bound T of the n_out-th best candidate, and only
+//           histograms) is a lower bound T of the n_out-th best candidate, and only
 //           the at most n_out chunks whose maximum reaches T hold selected ones. CTA i
 //           re-reads the i-th of them (from L2) and lists the candidates that
 //           reach T; the last CTA to finish narrows the
@@ -24,20 +24,19 @@ namespace wsg {
 namespace {
 
 constexpr int kChunkThreads = 256, kBeamThreads = 512;
-constexpr int kBeamPer = 8;                               // chunks a thread of pass 2 holds
-constexpr int kBeamChunksMax = kBeamPer * kBeamThreads;  // chunks of one call (all rows)
+constexpr int kBeamChunksMax = 4096;  // chunks of one call (all rows)
 constexpr int kBeamChunkMin = 1024;
 constexpr int kBeamGather = 4096;  // candidates held in shared memory
+constexpr int kBeamRank = 512;     // candidates ranked against each other without narrowing
 constexpr int kBeamsMax = 1024, kBeamOutMax = 1024;
-// dynamic shared memory of pass 2: the chunks' maxima and sums and the rows' offsets, later the candidates
-constexpr size_t kBeamSmem = 12 * kBeamGather;
-static_assert(kBeamSmem >= 8 * kBeamChunksMax + 8 * kBeamsMax, "both fit");
+constexpr size_t kBeamSmem = 12 * kBeamGather;  // dynamic shared memory of pass 2
+static_assert(kBeamChunksMax <= kBeamGather, "the chunks' keys lie where the candidates do");
 
-// Workspace: chunk maxima, their indices, chunk sums; the arrival counter; per
+// Workspace: the chunks' maxima with their sums and indices; the arrival counter; per
 // qualified chunk a count and a list of (key, flat index).
 struct BeamLayout {
   int chunk, per_row, chunks, slots;
-  size_t max, idx, sum, counter, count, key, flat, total;
+  size_t part, counter, count, key, flat, total;
 };
 
 BeamLayout beam_layout(int beams, int vocab, int n_out) {
@@ -55,13 +54,11 @@ BeamLayout beam_layout(int beams, int vocab, int n_out) {
     o = (o + bytes + 255) / 256 * 256;
     return at;
   };
-  L.max = take(sizeof(float) * L.chunks);
-  L.idx = take(sizeof(uint32_t) * L.chunks);
-  L.sum = take(sizeof(float) * L.chunks);
+  L.part = take(sizeof(float4) * L.chunks);
   L.counter = take(4);
   L.count = take(sizeof(uint32_t) * L.slots);
   const size_t list = static_cast<size_t>(L.slots) * (c < vocab ? c : vocab);
-  L.key = take(sizeof(unsigned long long) * list);
+  L.key = take(sizeof(uint2) * list);
   L.flat = take(sizeof(uint32_t) * list);
   L.total = o;
   return L;
@@ -74,9 +71,10 @@ struct BeamArgs {
   const float* scores;
   float* out_scores;
   int32_t *out_parents, *out_tokens;
-  float *max, *sum;
-  uint32_t *idx, *counter, *count, *flat;
-  unsigned long long* key;
+  float4* part;  // of the chunks: maximum, sum, index bits
+  uint32_t *counter, *count, *flat;
+  uint2* key;  // (high word, low word)
+  unsigned long long row_inv;  // k * row_inv >> 32 = k / per_row for k < 4096
   int vec;
 };
 
@@ -96,13 +94,30 @@ __device__ __forceinline__ uint32_t order32(float x) {
 }
 __device__ __forceinline__ float unorder32(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); }
 
-// The key x + off as order bits, off and the sum as two floats (value and
+// The key x + off as two order words, off and the sum as two floats (value and
 // remainder, 48 bits): the slow double pipe takes 7 times as long here.
-__device__ __forceinline__ unsigned long long key_bits(float x, float2 off) {
+__device__ __forceinline__ uint2 key_words(float x, float2 off) {
   const float s = x + off.x, t = s - x;
   const float e = (x - (s - t)) + (off.x - t) + off.y;  // x + off.x - s exactly, then the remainder
   const float hi = s + e, lo = e - (hi - s);
-  return static_cast<unsigned long long>(order32(hi)) << 32 | order32(lo);
+  return make_uint2(order32(hi), order32(lo));
+}
+
+// Two floats that sum to a + b exactly.
+__device__ __forceinline__ float2 two_sum(float a, float b) {
+  const float s = a + b, t = s - a;
+  return make_float2(s, (a - (s - t)) + (b - t));
+}
+
+// score - (m + log s) as two floats. s = 2^e f with f in [0.7, 1.42): log f is
+// below 0.36, so a float32 logarithm of it is good to 3e-8; e log 2 is an exact
+// product by the first 13 bits of log 2 and a small rest.
+__device__ __forceinline__ float2 row_offset(float score, float m, float s) {
+  int e;
+  float f = frexpf(s, &e);
+  if (f < 0.70710678f) f *= 2.f, --e;
+  const float2 a = two_sum(score, -m), b = two_sum(a.x, e * -0.693145751953125f), c = two_sum(b.x, -logf(f));
+  return two_sum(c.x, a.y + b.y + c.y - e * 1.428606820309417e-6f);
 }
 
 // Pass 1: chunk blockIdx.x of row blockIdx.y, 16 logits a thread at a time. The
@@ -164,17 +179,20 @@ __global__ void __launch_bounds__(kChunkThreads) beam_chunks_kernel(const BeamAr
     at = __reduce_min_sync(0xffffffffu, lane < kWarps && wm == m ? s_i[lane] : 0xffffffffu);
     if (lane == 0) {
       const int k = b * a.per_row + c;
-      a.max[k] = m;
-      a.sum[k] = s;
-      a.idx[k] = static_cast<uint32_t>(b) * a.vocab + v0 + at;  // not looked at where m is -inf
+      // (the index is not looked at where m is -inf)
+      a.part[k] = make_float4(m, s, __uint_as_float(static_cast<uint32_t>(b) * a.vocab + v0 + at), 0.f);
     }
   }
 }
 
-// Whether candidate (k, f) is at least (key, index) in the candidates' order.
-__device__ __forceinline__ bool reaches(unsigned long long k, uint32_t f, unsigned long long key, uint32_t index) {
-  return k > key || (k == key && f <= index);
-}
+// A threshold in the candidates' order: a candidate with key words (h, l) and flat
+// index f reaches it if it is not behind it.
+struct BeamBar {
+  uint32_t h, l, f;
+  __device__ __forceinline__ bool reached(uint32_t kh, uint32_t kl, uint32_t kf) const {
+    return (kh > h) | ((kh == h) & ((kl > l) | ((kl == l) & (kf <= f))));
+  }
+};
 
 // Sum over the CTA; every thread gets it. red: one word per warp, twice over
 // (alternate `turn` between calls, so that one barrier a call is enough).
@@ -186,325 +204,329 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*red)[kBeamT
          (32 / (kBeamThreads / 32));
 }
 
-// Smallest and largest of the CTA's values (lo: ~0 and hi: 0 where a thread has
-// none); red64: two words per warp.
-__device__ __forceinline__ void block_range(unsigned long long* lo, unsigned long long* hi, unsigned long long* red64) {
-  constexpr int kWarps = kBeamThreads / 32;
-  unsigned long long l = *lo, h = *hi;
+// Candidates to choose from: n of them in shared memory (a high word of 0 is none;
+// the places up to the next multiple of 4 kBeamThreads hold 0), or (h NULL) the
+// lists of all CTAs in the workspace.
+struct BeamSource {
+  const uint32_t *h, *l, *f;
+  int n;
+};
+
+// fn(high word, place) of each candidate; places in the lists count through them.
+template <typename Fn>
+__device__ __forceinline__ void for_high(const BeamArgs& a, const BeamSource& s, Fn fn) {
+  if (s.h) {
+#pragma unroll 1
+    for (int i0 = threadIdx.x; i0 < s.n; i0 += 4 * kBeamThreads) {
+      uint32_t k[4];
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    const unsigned long long l2 = __shfl_xor_sync(0xffffffffu, l, o), h2 = __shfl_xor_sync(0xffffffffu, h, o);
-    l = l2 < l ? l2 : l;
-    h = h2 > h ? h2 : h;
-  }
-  if ((threadIdx.x & 31) == 0) red64[threadIdx.x >> 5] = l, red64[kWarps + (threadIdx.x >> 5)] = h;
-  __syncthreads();
+      for (int e = 0; e < 4; ++e) k[e] = s.h[i0 + e * kBeamThreads];
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    l = red64[w] < l ? red64[w] : l;
-    h = red64[kWarps + w] > h ? red64[kWarps + w] : h;
+      for (int e = 0; e < 4; ++e) fn(k[e], static_cast<size_t>(i0 + e * kBeamThreads));
+    }
+  } else {
+#pragma unroll 1
+    for (int q = threadIdx.x >> 2; q < a.slots; q += kBeamThreads / 4) {  // four threads a list
+      const uint32_t n = __ldcg(a.count + q);
+#pragma unroll 1
+      for (uint32_t i = threadIdx.x & 3; i < n; i += 4) {
+        const size_t p = static_cast<size_t>(q) * a.list + i;
+        fn(__ldcg(a.key + p).x, p);
+      }
+    }
   }
-  __syncthreads();
-  *lo = l;
-  *hi = h;
 }
 
-// The composite (key, index) that exactly `want` of the CTA's n_all > want
-// entries reach: bisection over the keys, from their range [lo, hi], until that
-// many reach a key; where equal keys straddle it, over their indices.
-// reach(key): how many of this thread's entries have at least this key;
-// equal(key, index): how many have this key and at most this index.
-template <typename Reach, typename Equal>
-__device__ __forceinline__ void bisect(uint32_t want, uint32_t n_all, unsigned long long lo, unsigned long long hi,
-                                       Reach reach, Equal equal, uint32_t (*red)[kBeamThreads / 32], int* turn,
-                                       unsigned long long* key, uint32_t* index) {
-  unsigned long long end = hi + 1;  // n(lo) >= want > n(end)
-  uint32_t n_lo = n_all, n_end = 0;
-  while (n_lo != want && end - lo > 1) {
-    const unsigned long long mid = lo + (end - lo) / 2;
-    const uint32_t n = block_sum(reach(mid), red, (*turn)++);
-    if (n >= want)
-      lo = mid, n_lo = n;
-    else
-      end = mid, n_end = n;
+// Scratch of narrow().
+struct BeamScratch {
+  uint32_t hist[256], red[2][kBeamThreads / 32], found[3];
+};
+
+// The bar that exactly `want` of the source's (more than want) candidates reach.
+// Histograms of the high words over ever narrower ranges, 256 bins each, from
+// [lo, hi], which holds them all; where equal high words straddle the bar,
+// bisection over their low words and indices.
+__device__ __noinline__ BeamBar narrow(const BeamArgs& a, const BeamSource& s, uint32_t want, uint32_t lo, uint32_t hi,
+                                       BeamScratch* x) {
+  const int tid = threadIdx.x;
+  uint32_t above = 0;  // candidates over hi
+#pragma unroll 1
+  while (true) {
+    const int bits = 32 - __clz(hi - lo), shift = bits > 8 ? bits - 8 : 0;
+    __syncthreads();
+    if (tid < 256) x->hist[tid] = 0;
+    __syncthreads();
+    for_high(a, s, [&](uint32_t h, size_t) {
+      if ((h >= lo) & (h <= hi)) atomicAdd(&x->hist[(h - lo) >> shift], 1u);
+    });
+    __syncthreads();
+    if (tid < 32) {
+      // lane l holds bins 8 l .. 8 l + 7; find the bin in which the want-th from above lies
+      uint32_t own = 0;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) own += x->hist[8 * tid + j];
+      uint32_t over = own;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t v = __shfl_down_sync(0xffffffffu, over, o);
+        if (tid + o < 32) over += v;
+      }
+      over += above - own;  // candidates above this lane's bins
+      if (over < want && over + own >= want) {
+        int j = 7;
+        while (over + x->hist[8 * tid + j] < want) over += x->hist[8 * tid + j--];
+        x->found[0] = 8 * tid + j, x->found[1] = over, x->found[2] = x->hist[8 * tid + j];
+      }
+    }
+    __syncthreads();
+    lo += x->found[0] << shift;
+    above = x->found[1];
+    if (above + x->found[2] == want) return BeamBar{lo, 0, 0xffffffffu};
+    if (shift == 0) break;
+    hi = min(hi, lo + ((1u << shift) - 1u));
   }
-  *key = lo;
-  *index = 0xffffffffu;
-  if (n_lo == want) return;
-  uint32_t i0 = 0, i1 = 0xffffffffu;  // the want - n_end lowest indices with key lo
-  while (i0 < i1) {
-    const uint32_t mid = i0 + (i1 - i0) / 2;
-    if (block_sum(equal(lo, mid), red, (*turn)++) >= want - n_end)
-      i1 = mid;
+  // want - above of the candidates with high word lo: the smallest composite
+  // (inverted low word, index) that so many do not pass
+  unsigned long long c0 = 0, c1 = ~0ull;
+  int turn = 0;
+  __syncthreads();
+#pragma unroll 1
+  while (c0 < c1) {
+    const unsigned long long mid = c0 + (c1 - c0) / 2;
+    uint32_t n = 0;
+    for_high(a, s, [&](uint32_t h, size_t p) {
+      if (h == lo) {
+        const uint32_t l = s.h ? s.l[p] : __ldcg(a.key + p).y, f = s.h ? s.f[p] : __ldcg(a.flat + p);
+        n += (static_cast<unsigned long long>(~l) << 32 | f) <= mid;
+      }
+    });
+    if (block_sum(n, x->red, turn++) >= want - above)
+      c1 = mid;
     else
-      i0 = mid + 1;
+      c0 = mid + 1;
   }
-  *index = i1;
+  return BeamBar{lo, ~static_cast<uint32_t>(c1 >> 32), static_cast<uint32_t>(c1)};
 }
 
-// Pass 2. Dynamic shared memory: offsets of the rows, maxima and sums of the
-// chunks.
+// Pass 2. Dynamic shared memory: key words and flat indices of the chunks' maxima
+// (the words' places hold the maxima and sums first), later of the candidates.
+// Short loops rather than unrolled code: what runs once waits for its fetch.
 __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char beam_raw[];
-  float2* off = reinterpret_cast<float2*>(beam_raw);  // of the rows: score - lse
-  float* cmax = reinterpret_cast<float*>(off + a.beams);
-  float* csum = cmax + a.chunks;
-  // the last CTA's candidates, in the place of the chunks' maxima and sums
-  unsigned long long* gkey = reinterpret_cast<unsigned long long*>(beam_raw);
-  uint32_t* gidx = reinterpret_cast<uint32_t*>(gkey + kBeamGather);
-  __shared__ unsigned long long red64[2 * kBeamThreads / 32];
-  __shared__ uint32_t red[2][kBeamThreads / 32], cnt[kBeamPer * kBeamThreads / 32];
-  __shared__ uint32_t s_n, s_mine;
+  uint32_t* sh = reinterpret_cast<uint32_t*>(beam_raw);
+  uint32_t *sl = sh + kBeamGather, *sf = sl + kBeamGather;
+  float *smax = reinterpret_cast<float*>(sh), *ssum = reinterpret_cast<float*>(sl);
+  __shared__ float2 off[kBeamsMax];  // of the rows: score - lse
+  __shared__ BeamScratch scratch;
+  __shared__ uint32_t cnt[kBeamThreads / 32], s_lo, s_hi, s_n, s_mine;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   constexpr int kWarps = kBeamThreads / 32;
+  constexpr float kLog2e = 1.44269504088896340736f;
+  auto pad = [](int n) { return (n + 4 * kBeamThreads - 1) / (4 * kBeamThreads) * (4 * kBeamThreads); };
 
   pdl_wait();
-  uint32_t cidx[kBeamPer];  // this thread's chunks: tid, tid + kBeamThreads, ...
+  const int padded = pad(a.chunks);
+#pragma unroll 1
+  for (int k0 = tid; k0 < padded; k0 += 4 * kBeamThreads) {
+    float4 p[4];
 #pragma unroll
-  for (int j = 0; j < kBeamPer; ++j) {
-    const int k = tid + j * kBeamThreads;
-    cidx[j] = 0;
-    if (k < a.chunks) {
-      cmax[k] = a.max[k];
-      csum[k] = a.sum[k];
-      cidx[j] = a.idx[k];
+    for (int e = 0; e < 4; ++e)
+      p[e] = k0 + e * kBeamThreads < a.chunks ? a.part[k0 + e * kBeamThreads] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      smax[k0 + e * kBeamThreads] = p[e].x;
+      ssum[k0 + e * kBeamThreads] = p[e].y;
+      sf[k0 + e * kBeamThreads] = __float_as_uint(p[e].z);
     }
   }
-  if (tid == 0) s_mine = 0xffffffffu, s_n = 0;
+  if (tid == 0) s_mine = s_lo = 0xffffffffu, s_n = s_hi = 0;
   __syncthreads();
-  // row offsets score - lse; -inf where the row offers nothing
-  for (int b = warp; b < a.beams; b += kWarps) {
-    const float* rm = cmax + b * a.per_row;
-    float m = -INFINITY;
-    for (int c = lane; c < a.per_row; c += 32) m = fmaxf(m, rm[c]);
-    m = warp_max(m);
-    float s = 0.f;
-    if (m > -INFINITY && m < INFINITY)
-      for (int c = lane; c < a.per_row; c += 32) s += csum[b * a.per_row + c] * expf(rm[c] - m);
-    s = warp_sum(s);
-    if (lane == 0) off[b] = make_float2(m, s);
-  }
-  __syncthreads();
-  for (int b = tid; b < a.beams; b += kBeamThreads) {
-    // score - (m + log s), s = 2^e f with f in [0.7, 1.42): log f is below 0.36, so a
-    // float32 logarithm of it is good to 3e-8
-    const float m = off[b].x, s = off[b].y, sc = a.scores[b];
-    float2 o = make_float2(-INFINITY, 0.f);
-    if (m > -INFINITY && m < INFINITY && isfinite(sc)) {
-      int e;
-      float f = frexpf(s, &e);
-      if (f < 0.70710678f) f *= 2.f, --e;
-      const double d = static_cast<double>(sc) - (static_cast<double>(m) + e * 0.69314718055994530942 + logf(f));
-      o.x = static_cast<float>(d);
-      o.y = static_cast<float>(d - static_cast<double>(o.x));
+  // row offsets, as many lanes a row as there are; -inf where the row offers nothing
+  int lanes = 1;
+  while (lanes < 32 && lanes * 2 * a.beams <= kBeamThreads) lanes *= 2;
+#pragma unroll 1
+  for (int b0 = 0; b0 < a.beams; b0 += kBeamThreads / lanes) {
+    const int b = b0 + tid / lanes, c0 = (b < a.beams ? b : 0) * a.per_row;
+    float m = -INFINITY, s = 0.f;
+#pragma unroll 4
+    for (int c = tid % lanes; c < a.per_row; c += lanes) m = fmaxf(m, smax[c0 + c]);
+#pragma unroll 1
+    for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    const bool finite = m > -INFINITY && m < INFINITY;
+#pragma unroll 4
+    for (int c = tid % lanes; c < a.per_row; c += lanes)
+      s = fmaf(ssum[c0 + c], ex2((smax[c0 + c] - (finite ? m : 0.f)) * kLog2e), s);
+#pragma unroll 1
+    for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (b < a.beams && tid % lanes == 0) {
+      const float sc = a.scores[b];
+      off[b] = finite && isfinite(sc) ? row_offset(sc, m, s) : make_float2(-INFINITY, 0.f);
     }
-    off[b] = o;
   }
   __syncthreads();
-  unsigned long long key[kBeamPer];  // of the chunks' maxima, 0: offers nothing
-  unsigned long long lo = ~0ull, hi = 0;
-#pragma unroll
-  for (int j = 0; j < kBeamPer; ++j) {
-    const int k = tid + j * kBeamThreads;
-    key[j] = 0;
-    if (k < a.chunks) {
-      const float2 o = off[k / a.per_row];
-      if (cmax[k] > -INFINITY && o.x > -INFINITY) key[j] = key_bits(cmax[k], o);
-    }
-    if (key[j]) {
-      lo = key[j] < lo ? key[j] : lo;
-      hi = key[j] > hi ? key[j] : hi;
-    }
+  // the chunks' keys, and the range of their high words
+  uint32_t some = 0, lo = 0xffffffffu, hi = 0;
+#pragma unroll 2
+  for (int k = tid; k < padded; k += kBeamThreads) {
+    const float2 o = off[k < a.chunks ? static_cast<uint32_t>((k * a.row_inv) >> 32) : 0];
+    const float m = smax[k];
+    const bool in = (k < a.chunks) & (m > -INFINITY) & (o.x > -INFINITY);
+    const uint2 w = key_words(m, o);
+    sh[k] = in ? w.x : 0;
+    sl[k] = w.y;
+    some += in;
+    lo = in ? min(lo, w.x) : lo;
+    hi = in ? max(hi, w.x) : hi;
   }
-  // threshold: the n_out-th best of the keys
-  uint32_t n_all = 0;
-#pragma unroll
-  for (int j = 0; j < kBeamPer; ++j) n_all += key[j] != 0;
-  int turn = 0;
-  n_all = block_sum(n_all, red, turn++);
-  unsigned long long tk = 1;  // reached by every key
-  uint32_t ti = 0xffffffffu;
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) {
+    atomicMin(&s_lo, lo);
+    atomicMax(&s_hi, hi);
+  }
+  const uint32_t n_all = block_sum(some, scratch.red, 0);
+  // the bar: the n_out-th best of the keys
+  BeamBar bar{1, 0, 0xffffffffu};  // reached by every key
   const uint32_t want = a.n_out;
-  if (n_all > want) {
-    block_range(&lo, &hi, red64);
-    bisect(
-        want, n_all, lo, hi,
-        [&](unsigned long long mid) {
-          uint32_t n = 0;
-#pragma unroll
-          for (int j = 0; j < kBeamPer; ++j) n += key[j] >= mid;
-          return n;
-        },
-        [&](unsigned long long k, uint32_t mid) {
-          uint32_t n = 0;
-#pragma unroll
-          for (int j = 0; j < kBeamPer; ++j) n += key[j] == k && cidx[j] <= mid;
-          return n;
-        },
-        red, &turn, &tk, &ti);
-  }
+  if (n_all > want) bar = narrow(a, BeamSource{sh, sl, sf, a.chunks}, want, s_lo, s_hi, &scratch);
 
-  // the blockIdx.x-th chunk whose maximum reaches the threshold, counted in the
-  // order (j, thread); all CTAs count alike
-  uint32_t bal[kBeamPer];
-#pragma unroll
-  for (int j = 0; j < kBeamPer; ++j) {
-    bal[j] = __ballot_sync(0xffffffffu, key[j] != 0 && reaches(key[j], cidx[j], tk, ti));
-    if (lane == 0) cnt[j * kWarps + warp] = __popc(bal[j]);
-  }
+  // the blockIdx.x-th chunk that reaches the bar, in the order of the chunks: a warp
+  // counts those of its range, and the one that holds it finds it
+  const int range = padded / kWarps, from = warp * range, until = from + range;
+  uint32_t c = 0;
+#pragma unroll 4
+  for (int k = from + lane; k < until; k += 32) c += (sh[k] != 0) & bar.reached(sh[k], sl[k], sf[k]);
+  c = __reduce_add_sync(0xffffffffu, c);
+  if (lane == 0) cnt[warp] = c;
   __syncthreads();
-  {
-    uint32_t before = 0;
-#pragma unroll
-    for (int j = 0; j < kBeamPer; ++j) {
-      const uint32_t c = lane < kWarps ? cnt[j * kWarps + lane] : 0;
-      const uint32_t mine = before + __reduce_add_sync(0xffffffffu, lane < warp ? c : 0);
-      before += __reduce_add_sync(0xffffffffu, c);
-      if (((bal[j] >> lane) & 1u) && mine + __popc(bal[j] & ((1u << lane) - 1u)) == blockIdx.x)
-        s_mine = tid + j * kBeamThreads;
+  const uint32_t before = __reduce_add_sync(0xffffffffu, lane < warp ? cnt[lane & (kWarps - 1)] : 0);
+  if (blockIdx.x >= before && blockIdx.x < before + c) {
+    uint32_t at = before;
+#pragma unroll 1
+    for (int k0 = from; k0 < until; k0 += 32) {
+      const int k = k0 + lane;
+      const bool in = (sh[k] != 0) & bar.reached(sh[k], sl[k], sf[k]);
+      const uint32_t bal = __ballot_sync(0xffffffffu, in);
+      if (in && at + __popc(bal & ((1u << lane) - 1u)) == blockIdx.x) s_mine = k;
+      at += __popc(bal);
     }
   }
   __syncthreads();
   const uint32_t mine = s_mine;
   const size_t base = static_cast<size_t>(blockIdx.x) * a.list;
   if (mine != 0xffffffffu) {
-    const int b = mine / a.per_row, v0 = (mine % a.per_row) * a.chunk, n = min(a.chunk, a.vocab - v0);
+    const int b = static_cast<int>((mine * a.row_inv) >> 32), v0 = (mine - b * a.per_row) * a.chunk,
+              n = min(a.chunk, a.vocab - v0);
     const float* x = a.logits + a.stride * b + v0;
     const float2 o = off[b];
     const uint32_t f0 = static_cast<uint32_t>(b) * a.vocab + v0;
+    const float bar_value = bar.h == 1 ? -INFINITY : unorder32(bar.h);
+    const float low = bar_value - 1e-6f * fabsf(bar_value);  // a few steps of float32 below it
+#pragma unroll 1
     for (int i0 = tid; i0 < n; i0 += kBeamThreads * 8) {
       float y[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = i0 + e * kBeamThreads < n ? masked(x[i0 + e * kBeamThreads]) : -INFINITY;
+      uint32_t near = 0;  // those that are not masked and not clearly below the bar
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const uint32_t f = f0 + i0 + e * kBeamThreads;
-        const unsigned long long k = key_bits(y[e], o);
-        if (y[e] > -INFINITY && reaches(k, f, tk, ti)) {
+      for (int e = 0; e < 8; ++e)
+        near |= static_cast<uint32_t>((y[e] > -INFINITY) & (y[e] + o.x >= low)) << e;
+#pragma unroll 1
+      for (; near; near &= near - 1) {
+        const int i = i0 + (__ffs(near) - 1) * kBeamThreads;
+        const uint2 w = key_words(x[i], o);
+        if (bar.reached(w.x, w.y, f0 + i)) {
           const uint32_t p = atomicAdd(&s_n, 1u);
-          a.key[base + p] = k;
-          a.flat[base + p] = f;
+          a.key[base + p] = w;
+          a.flat[base + p] = f0 + i;
         }
       }
     }
   }
-  __threadfence();  // each thread's listed candidates, before the CTA's arrival
   __syncthreads();
   if (tid == 0) {
     a.count[blockIdx.x] = s_n;
-    __threadfence();
+    __threadfence();  // after the barrier: the whole CTA's list before its arrival
     s_mine = atomicAdd(a.counter, 1u);
   }
   __syncthreads();
   if (s_mine != gridDim.x - 1) return;
   __threadfence();
 
-  // the last CTA: narrow what was listed to the n_out best and rank them. Up to
-  // kBeamGather candidates are held in shared memory; of more (many equal
-  // logits) the lists are bisected where they lie.
+  // the last CTA: rank what was listed. Up to kBeamGather candidates are held in
+  // shared memory; more of them (many equal logits) are narrowed where they lie.
   if (tid == 0) s_n = 0;
   uint32_t listed = 0;
+#pragma unroll 1
   for (int q = tid; q < a.slots; q += kBeamThreads) listed += __ldcg(a.count + q);
-  listed = block_sum(listed, red, turn++);
-  unsigned long long lk = 1;
-  uint32_t li = 0xffffffffu;
-  // four threads a list: fn(key bits, flat index) of each listed candidate
-  auto each = [&](auto fn) {
-    for (int q = tid >> 2; q < a.slots; q += kBeamThreads / 4) {
-      const uint32_t n = __ldcg(a.count + q);
-      for (uint32_t i = tid & 3; i < n; i += 4) {
-        const size_t p = static_cast<size_t>(q) * a.list + i;
-        fn(__ldcg(a.key + p), __ldcg(a.flat + p));
-      }
-    }
-  };
-  if (listed > kBeamGather) {
-    lo = ~0ull, hi = 0;
-    each([&](unsigned long long k, uint32_t) { lo = k < lo ? k : lo, hi = k > hi ? k : hi; });
-    block_range(&lo, &hi, red64);
-    bisect(
-        want, listed, lo, hi,
-        [&](unsigned long long mid) {
-          uint32_t n = 0;
-          each([&](unsigned long long k, uint32_t) { n += k >= mid; });
-          return n;
-        },
-        [&](unsigned long long at, uint32_t mid) {
-          uint32_t n = 0;
-          each([&](unsigned long long k, uint32_t f) { n += k == at && f <= mid; });
-          return n;
-        },
-        red, &turn, &lk, &li);
-  }
-  each([&](unsigned long long k, uint32_t f) {
-    if (reaches(k, f, lk, li)) {
+  __syncthreads();
+  listed = block_sum(listed, scratch.red, 0);
+  bar = BeamBar{1, 0, 0xffffffffu};
+  if (listed > kBeamGather) bar = narrow(a, BeamSource{nullptr, nullptr, nullptr, 0}, want, 1, 0xffffffffu, &scratch);
+  for_high(a, BeamSource{nullptr, nullptr, nullptr, 0}, [&](uint32_t h, size_t p) {
+    const uint32_t l = __ldcg(a.key + p).y, f = __ldcg(a.flat + p);
+    if (bar.reached(h, l, f)) {
       const uint32_t w = atomicAdd(&s_n, 1u);
-      gkey[w] = k;
-      gidx[w] = f;
+      sh[w] = h, sl[w] = l, sf[w] = f;
     }
   });
   __syncthreads();
   uint32_t n = s_n;
-  if (n > want) {
-    unsigned long long k[kBeamGather / kBeamThreads];
-    lo = ~0ull, hi = 0;
-#pragma unroll
-    for (int j = 0; j < kBeamGather / kBeamThreads; ++j) {
-      const uint32_t i = tid + j * kBeamThreads;
-      k[j] = i < n ? gkey[i] : 0;
-      if (k[j]) lo = k[j] < lo ? k[j] : lo, hi = k[j] > hi ? k[j] : hi;
-    }
-    block_range(&lo, &hi, red64);
-    bisect(
-        want, n, lo, hi,
-        [&](unsigned long long mid) {
-          uint32_t c = 0;
-#pragma unroll
-          for (int j = 0; j < kBeamGather / kBeamThreads; ++j) c += k[j] >= mid;
-          return c;
-        },
-        [&](unsigned long long at, uint32_t mid) {
-          uint32_t c = 0;
-#pragma unroll
-          for (int j = 0; j < kBeamGather / kBeamThreads; ++j) c += k[j] == at && gidx[tid + j * kBeamThreads] <= mid;
-          return c;
-        },
-        red, &turn, &lk, &li);
-    // the survivors, in place of the candidates
-    uint32_t f[kBeamGather / kBeamThreads];
-#pragma unroll
-    for (int j = 0; j < kBeamGather / kBeamThreads; ++j) {
-      const uint32_t i = tid + j * kBeamThreads;
-      f[j] = i < n ? gidx[i] : 0;
-    }
+  auto fill = [&]() {  // zeros behind the candidates
+#pragma unroll 1
+    for (int i = n + tid; i < pad(n); i += kBeamThreads) sh[i] = 0;
+    __syncthreads();
+  };
+  fill();
+  if (n > want && n > kBeamRank) {
+    // too many to rank against each other: the n_out best, by way of the first lists' places
+    bar = narrow(a, BeamSource{sh, sl, sf, static_cast<int>(n)}, want, 1, 0xffffffffu, &scratch);
     if (tid == 0) s_n = 0;
     __syncthreads();
-#pragma unroll
-    for (int j = 0; j < kBeamGather / kBeamThreads; ++j)
-      if (k[j] && reaches(k[j], f[j], lk, li)) {
+#pragma unroll 1
+    for (uint32_t i = tid; i < n; i += kBeamThreads)
+      if (bar.reached(sh[i], sl[i], sf[i])) {
         const uint32_t w = atomicAdd(&s_n, 1u);
-        gkey[w] = k[j];
-        gidx[w] = f[j];
+        a.key[w] = make_uint2(sh[i], sl[i]);
+        a.flat[w] = sf[i];
       }
     __syncthreads();
     n = s_n;
+#pragma unroll 1
+    for (uint32_t i = tid; i < n; i += kBeamThreads) sh[i] = a.key[i].x, sl[i] = a.key[i].y, sf[i] = a.flat[i];
+    fill();
   }
-  // ranks by counting, `split` threads a candidate
+  // ranks by counting the better ones, `split` threads a candidate: the high words
+  // four at a time; candidates that share theirs compare the rest
   int split = 1;
   while (split < 32 && n * split * 2 <= kBeamThreads) split *= 2;
+#pragma unroll 1
   for (uint32_t i0 = 0; i0 < n; i0 += kBeamThreads / split) {
-    const uint32_t i = i0 + tid / split;
-    int rank = 0;
-    if (i < n)
-      for (uint32_t j = tid % split; j < n; j += split)
-        rank += gkey[j] > gkey[i] || (gkey[j] == gkey[i] && gidx[j] < gidx[i]);
-    for (int o = split / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
+    const uint32_t i = i0 + tid / split, h = i < n ? sh[i] : 0xffffffffu;
+    uint32_t rank = 0, same = 0;
+#pragma unroll 4
+    for (uint32_t j = tid % split * 4; j < n; j += split * 4) {
+      const uint4 k = *reinterpret_cast<const uint4*>(sh + j);
+      rank += (k.x > h) + (k.y > h) + (k.z > h) + (k.w > h);
+      same += (k.x == h) + (k.y == h) + (k.z == h) + (k.w == h);
+    }
+#pragma unroll 1
+    for (int o = split / 2; o > 0; o >>= 1) {
+      rank += __shfl_xor_sync(0xffffffffu, rank, o);
+      same += __shfl_xor_sync(0xffffffffu, same, o);
+    }
     if (i < n && tid % split == 0) {
-      a.out_scores[rank] = unorder32(static_cast<uint32_t>(gkey[i] >> 32));
-      a.out_parents[rank] = static_cast<int32_t>(gidx[i] / static_cast<uint32_t>(a.vocab));
-      a.out_tokens[rank] = static_cast<int32_t>(gidx[i] % static_cast<uint32_t>(a.vocab));
+      if (same > 1)
+#pragma unroll 1
+        for (uint32_t j = 0; j < n; ++j) rank += sh[j] == h && (sl[j] > sl[i] || (sl[j] == sl[i] && sf[j] < sf[i]));
+      if (rank < want) {
+        a.out_scores[rank] = unorder32(h);
+        a.out_parents[rank] = static_cast<int32_t>(sf[i] / static_cast<uint32_t>(a.vocab));
+        a.out_tokens[rank] = static_cast<int32_t>(sf[i] % static_cast<uint32_t>(a.vocab));
+      }
     }
   }
+#pragma unroll 1
   for (uint32_t i = n + tid; i < want; i += kBeamThreads) {
     a.out_scores[i] = -INFINITY;
     a.out_parents[i] = a.out_tokens[i] = -1;
@@ -614,13 +636,12 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
   k.out_scores = a->out_scores;
   k.out_parents = a->out_parents;
   k.out_tokens = a->out_tokens;
-  k.max = reinterpret_cast<float*>(w + L.max);
-  k.idx = reinterpret_cast<uint32_t*>(w + L.idx);
-  k.sum = reinterpret_cast<float*>(w + L.sum);
+  k.part = reinterpret_cast<float4*>(w + L.part);
   k.counter = reinterpret_cast<uint32_t*>(w + L.counter);
   k.count = reinterpret_cast<uint32_t*>(w + L.count);
-  k.key = reinterpret_cast<unsigned long long*>(w + L.key);
+  k.key = reinterpret_cast<uint2*>(w + L.key);
   k.flat = reinterpret_cast<uint32_t*>(w + L.flat);
+  k.row_inv = (1ull << 32) / L.per_row + 1;
   k.vec = aligned16(a->logits) && a->logits_stride % 4 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // static and dynamic shared memory together pass the 48 KB that need no opt-in
