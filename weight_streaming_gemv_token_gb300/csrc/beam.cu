@@ -24,7 +24,8 @@ namespace wsg {
 namespace {
 
 constexpr int kChunkThreads = 256, kBeamThreads = 512;
-constexpr int kBeamChunksMax = 4096;  // chunks of one call (all rows)
+constexpr int kChunkCtas = 6;  // CTAs of pass 1 an SM, which leaves room for one of pass 2
+constexpr int kBeamChunksMax = 2048;  // chunks of one call (all rows)
 constexpr int kBeamChunkMin = 1024;
 constexpr int kBeamGather = 4096;  // candidates held in shared memory
 constexpr int kBeamRank = 512;     // candidates ranked against each other without narrowing
@@ -74,7 +75,7 @@ struct BeamArgs {
   float4* part;  // of the chunks: maximum, sum, index bits
   uint32_t *counter, *count, *flat;
   uint2* key;  // (high word, low word)
-  unsigned long long row_inv;  // k * row_inv >> 32 = k / per_row for k < 4096
+  unsigned long long row_inv;  // k * row_inv >> 32 = k / per_row for a chunk k
   int vec;
 };
 
@@ -113,74 +114,76 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
 // below 0.36, so a float32 logarithm of it is good to 3e-8; e log 2 is an exact
 // product by the first 13 bits of log 2 and a small rest.
 __device__ __forceinline__ float2 row_offset(float score, float m, float s) {
-  int e;
-  float f = frexpf(s, &e);
-  if (f < 0.70710678f) f *= 2.f, --e;
+  int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;  // (s >= 1)
+  float f = __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u);
+  if (f > 1.41421356f) f *= 0.5f, ++e;
   const float2 a = two_sum(score, -m), b = two_sum(a.x, e * -0.693145751953125f), c = two_sum(b.x, -logf(f));
   return two_sum(c.x, a.y + b.y + c.y - e * 1.428606820309417e-6f);
 }
 
-// Pass 1: chunk blockIdx.x of row blockIdx.y, 16 logits a thread at a time. The
-// exponentials are 2^((x - m) log2 e) with m the warp's maximum so far.
+// Pass 1: chunks blockIdx.x, blockIdx.x + gridDim.x, ..., 16 logits a thread at a
+// time. The exponentials are 2^((x - m) log2 e) with m the warp's maximum so far.
+// Every CTA is resident from the start and leaves room beside it for one of pass
+// 2, which gets ready meanwhile.
 __global__ void __launch_bounds__(kChunkThreads) beam_chunks_kernel(const BeamArgs a) {
   constexpr int kWarps = kChunkThreads / 32;
   constexpr float kLog2e = 1.44269504088896340736f;
-  __shared__ float s_m[kWarps], s_s[kWarps];
-  __shared__ uint32_t s_i[kWarps];
+  __shared__ float s_m[2][kWarps], s_s[2][kWarps];
+  __shared__ uint32_t s_i[2][kWarps];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x, b = blockIdx.y;
-  const int v0 = c * a.chunk, n = min(a.chunk, a.vocab - v0);
-  const float* x = a.logits + a.stride * b + v0;
-  if (tid == 0 && b == 0 && c == 0) *a.counter = 0;
-  float m = -INFINITY, s = 0.f;  // the warp's maximum, this thread's sum relative to it
-  float own = -INFINITY;         // this thread's maximum, first found at `at`
-  uint32_t at = 0xffffffffu;
-  for (int w0 = warp * 128; w0 < n; w0 += kChunkThreads * 16) {
-    float y[16];
+  if (tid == 0 && blockIdx.x == 0) *a.counter = 0;
+  int turn = 0;
+  for (int k = blockIdx.x; k < a.chunks; k += gridDim.x, turn ^= 1) {
+    const int b = static_cast<int>((k * a.row_inv) >> 32), v0 = (k - b * a.per_row) * a.chunk, n = min(a.chunk, a.vocab - v0);
+    const float* x = a.logits + a.stride * b + v0;
+    float m = -INFINITY, s = 0.f;  // the warp's maximum, this thread's sum relative to it
+    float own = -INFINITY;         // this thread's maximum, first found at `at`
+    uint32_t at = 0xffffffffu;
+    for (int w0 = warp * 128; w0 < n; w0 += kChunkThreads * 16) {
+      float y[16];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int i = w0 + lane * 4 + q * kChunkThreads * 4;
-      if (a.vec && i + 4 <= n) {
-        const float4 f = *reinterpret_cast<const float4*>(x + i);
-        y[4 * q] = f.x, y[4 * q + 1] = f.y, y[4 * q + 2] = f.z, y[4 * q + 3] = f.w;
-      } else {
+      for (int q = 0; q < 4; ++q) {
+        const int i = w0 + lane * 4 + q * kChunkThreads * 4;
+        if (a.vec && i + 4 <= n) {
+          const float4 f = *reinterpret_cast<const float4*>(x + i);
+          y[4 * q] = f.x, y[4 * q + 1] = f.y, y[4 * q + 2] = f.z, y[4 * q + 3] = f.w;
+        } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[4 * q + e] = i + e < n ? x[i + e] : -INFINITY;
+          for (int e = 0; e < 4; ++e) y[4 * q + e] = i + e < n ? x[i + e] : -INFINITY;
+        }
+      }
+      float top = -INFINITY;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) y[e] = masked(y[e]), top = fmaxf(top, y[e]);
+      if (top > own) {
+        own = top;
+#pragma unroll
+        for (int e = 15; e >= 0; --e)
+          if (y[e] == top) at = w0 + lane * 4 + (e >> 2) * kChunkThreads * 4 + (e & 3);
+      }
+      const float m2 = fmaxf(m, warp_max(top));
+      if (m2 > -INFINITY) {
+        s *= ex2((m - m2) * kLog2e);  // 0 in the first round
+        m = m2;
+        // (the difference first: m log2 e overflows for the type's lowest values)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s += ex2((y[e] - m) * kLog2e);
       }
     }
-    float top = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < 16; ++e) y[e] = masked(y[e]), top = fmaxf(top, y[e]);
-    if (top > own) {
-      own = top;
-#pragma unroll
-      for (int e = 15; e >= 0; --e)
-        if (y[e] == top) at = w0 + lane * 4 + (e >> 2) * kChunkThreads * 4 + (e & 3);
-    }
-    const float m2 = fmaxf(m, warp_max(top));
-    if (m2 > -INFINITY) {
-      s *= ex2((m - m2) * kLog2e);  // 0 in the first round
-      m = m2;
-      // (the difference first: m log2 e overflows for the type's lowest values)
-#pragma unroll
-      for (int e = 0; e < 16; ++e) s += ex2((y[e] - m) * kLog2e);
-    }
-  }
-  s = warp_sum(s);
-  at = __reduce_min_sync(0xffffffffu, own == m ? at : 0xffffffffu);
-  if (lane == 0) s_m[warp] = m, s_s[warp] = s, s_i[warp] = at;
-  __syncthreads();
-  if (warp == 0) {
-    const float wm = lane < kWarps ? s_m[lane] : -INFINITY;
-    m = warp_max(wm);
-    s = lane < kWarps && wm > -INFINITY ? s_s[lane] * ex2((wm - m) * kLog2e) : 0.f;
     s = warp_sum(s);
-    at = __reduce_min_sync(0xffffffffu, lane < kWarps && wm == m ? s_i[lane] : 0xffffffffu);
-    if (lane == 0) {
-      const int k = b * a.per_row + c;
+    at = __reduce_min_sync(0xffffffffu, own == m ? at : 0xffffffffu);
+    if (lane == 0) s_m[turn][warp] = m, s_s[turn][warp] = s, s_i[turn][warp] = at;
+    __syncthreads();
+    if (warp == 0) {
+      const float wm = lane < kWarps ? s_m[turn][lane] : -INFINITY;
+      m = warp_max(wm);
+      s = lane < kWarps && wm > -INFINITY ? s_s[turn][lane] * ex2((wm - m) * kLog2e) : 0.f;
+      s = warp_sum(s);
+      at = __reduce_min_sync(0xffffffffu, lane < kWarps && wm == m ? s_i[turn][lane] : 0xffffffffu);
       // (the index is not looked at where m is -inf)
-      a.part[k] = make_float4(m, s, __uint_as_float(static_cast<uint32_t>(b) * a.vocab + v0 + at), 0.f);
+      if (lane == 0) a.part[k] = make_float4(m, s, __uint_as_float(static_cast<uint32_t>(b) * a.vocab + v0 + at), 0.f);
     }
   }
 }
@@ -339,6 +342,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
       sf[k0 + e * kBeamThreads] = __float_as_uint(p[e].z);
     }
   }
+#pragma unroll 1
+  for (int b = tid; b < a.beams; b += kBeamThreads) off[b].x = a.scores[b];
   if (tid == 0) s_mine = s_lo = 0xffffffffu, s_n = s_hi = 0;
   __syncthreads();
   // row offsets, as many lanes a row as there are; -inf where the row offers nothing
@@ -359,7 +364,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
 #pragma unroll 1
     for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (b < a.beams && tid % lanes == 0) {
-      const float sc = a.scores[b];
+      const float sc = off[b].x;
       off[b] = finite && isfinite(sc) ? row_offset(sc, m, s) : make_float2(-INFINITY, 0.f);
     }
   }
@@ -650,7 +655,8 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
     WSG_CUDA_TRY(nullptr, cudaFuncSetAttribute(beam_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBeamSmem));
     lifted[di.device] = true;
   }
-  WSG_CUDA_TRY(nullptr, launch_k(beam_chunks_kernel, dim3(L.per_row, a->beams), dim3(kChunkThreads), 0, s, false, k));
+  const int grid = L.chunks < kChunkCtas * di.sms ? L.chunks : kChunkCtas * di.sms;
+  WSG_CUDA_TRY(nullptr, launch_k(beam_chunks_kernel, dim3(grid), dim3(kChunkThreads), 0, s, true, k));
   WSG_CUDA_TRY(nullptr, launch_k(beam_pick_kernel, dim3(L.slots), dim3(kBeamThreads), kBeamSmem, s, true, k));
   return DEC_OK;
 }
