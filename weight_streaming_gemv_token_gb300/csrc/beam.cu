@@ -564,6 +564,8 @@ struct ReorderArgs {
 __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const ReorderArgs a) {
   const int i = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
   const bool first = layer == 0 && blockIdx.z == 0;
+  pdl_wait();  // the parents and the pages come from the stream's previous kernels
+  pdl_trigger();
   const int p = a.parents[i];
   int len = -1, src = -1, dst = -1;
   bool bad = p >= a.beams;
@@ -699,6 +701,6 @@ extern "C" dec_status beam_reorder_pages(const beam_reorder_args* a, void* strea
   k.new_len = a->new_len;
   k.err = di.err;
   WSG_CUDA_TRY(nullptr, launch_k(beam_reorder_kernel, dim3(a->beams, a->layers, 2), dim3(kReorderThreads), 0,
-                                 static_cast<cudaStream_t>(stream), false, k));
+                                 static_cast<cudaStream_t>(stream), true, k));
   return DEC_OK;
 }

@@ -187,6 +187,8 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
   };
   long long r = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
   const long long rstep = static_cast<long long>(gridDim.x) * (kRowsThreads / LPH);
+  pdl_wait();  // inputs come from the stream's previous kernel
+  pdl_trigger();
   fetch(r, 0);
   int pos_next = r < a.rows ? a.pos[r] : -1;
   // the trip count is the CTA's: its first unit's rows
@@ -330,9 +332,9 @@ cudaError_t launch_mode(const QkRowsArgs& a, int sms, cudaStream_t st) {
   const long long most = (3ll * sms + groups - 1) / groups, turns = (blocks + most - 1) / most;
   const dim3 grid(static_cast<unsigned>((blocks + turns - 1) / turns), static_cast<unsigned>(groups));
   if (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0)
-    return a.interleaved ? launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE>, grid, dim3(kRowsThreads), 0, st, false, a)
-                         : launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES>, grid, dim3(kRowsThreads), 0, st, false, a);
-  return launch_k(qk_rows_kernel<XT, LPH, PAIR_STAGED>, grid, dim3(kRowsThreads), 0, st, false, a);
+    return a.interleaved ? launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE>, grid, dim3(kRowsThreads), 0, st, true, a)
+                         : launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES>, grid, dim3(kRowsThreads), 0, st, true, a);
+  return launch_k(qk_rows_kernel<XT, LPH, PAIR_STAGED>, grid, dim3(kRowsThreads), 0, st, true, a);
 }
 
 template <typename XT>
