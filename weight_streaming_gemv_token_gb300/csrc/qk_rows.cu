@@ -98,9 +98,9 @@ __device__ __forceinline__ unsigned long long turns64(double w) {
   return static_cast<long long>(bits) < 0 ? 0ull - f : f;
 }
 
-// Cosine and sine of position * w, w in radians per position.
-__device__ __forceinline__ void turn(double w, uint32_t pos, float factor, float* c, float* s) {
-  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>((turns64(w) * pos) >> 32));
+// Cosine and sine at a position, f the turns per position as turns64 gives them.
+__device__ __forceinline__ void turn(unsigned long long f, uint32_t pos, float factor, float* c, float* s) {
+  const int32_t t = static_cast<int32_t>(static_cast<uint32_t>((f * pos) >> 32));
   sincospif(static_cast<float>(t) * 0x1p-31f, s, c);  // in half turns
   *c *= factor;
   *s *= factor;
@@ -146,6 +146,27 @@ __device__ __forceinline__ void widen8(const Raw8<T>& r, float (&x)[8]) {
   }
 }
 
+// Pairs of floats for the two-wide float32 instructions.
+using Pair = unsigned long long;
+__device__ __forceinline__ Pair pair(float x, float y) {
+  Pair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ void unpair(Pair p, float* x, float* y) {
+  asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p));
+}
+__device__ __forceinline__ Pair mul2(Pair a, Pair b) {
+  Pair d;
+  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ Pair fma2(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+
 // How a head's pairs lie in its lanes.
 enum PairMode : int {
   PAIR_LANES = 0,   // half layout, rot / 2 a multiple of 8: whole lanes are partners
@@ -157,7 +178,7 @@ enum PairMode : int {
 // group of up to per_unit heads of one kind (queries, keys, values in turn), so
 // that what depends on the kind is settled once. The next batch of heads is
 // always on its way while one is worked on, across rows too.
-template <typename XT, int LPH, int MODE>
+template <typename XT, int LPH, int MODE, bool VEC>
 __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsArgs a) {
   constexpr int kBatch = sizeof(XT) == 4 ? 2 : 4;  // heads a batch
   __shared__ float stage[MODE == PAIR_STAGED ? kRowsThreads * 8 : 1];
@@ -171,9 +192,12 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
   const long long in_stride = kind == 0 ? a.q_stride : kind == 1 ? a.k_stride : a.v_stride;
   void* out = kind == 0 ? a.q_out : kind == 1 ? a.k_out : a.v_out;
   const bool pool = kind > 0 && a.paged;
-  const int out_f32 = pool ? a.kv_f32 : a.y_f32, vec_out = pool ? 1 : a.vec_y;
+  const int out_f32 = pool ? a.kv_f32 : a.y_f32, vec_out = VEC || pool;
   const float* g = kind == 0 ? a.g_q : kind == 1 ? a.g_k : nullptr;
   const int mate = (tid & 31) + (e0 >= a.rot ? 0 : e0 < half ? half >> 3 : -(half >> 3));  // PAIR_LANES
+  // register e & 1 of pair e / 2 holds element el(e) of the lane: partners lie in the
+  // same places of neighbouring pairs where they are inside the lane
+  auto el = [](int e) { return MODE == PAIR_INSIDE ? (e & 4) + ((e >> 1) & 1) + 2 * (e & 1) : e; };
   // the element that partners element e
   auto partner = [&](int e) { return e >= a.rot ? e : a.interleaved ? e ^ 1 : e < half ? e + half : e - half; };
   const float mean = 1.f / static_cast<float>(a.d);
@@ -183,13 +207,30 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
   auto fetch = [&](long long r, int b0) {
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
-      next[i] = r < a.rows && b0 + i < n && e0 < a.d ? fetch8(in + in_stride * r + (b0 + i) * a.d, a.vec_x) : Raw8<XT>{};
+      next[i] = r < a.rows && b0 + i < n && e0 < a.d ? fetch8(in + in_stride * r + (b0 + i) * a.d, VEC) : Raw8<XT>{};
   };
   long long r = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH) + tid / LPH;
   const long long rstep = static_cast<long long>(gridDim.x) * (kRowsThreads / LPH);
   pdl_wait();  // inputs come from the stream's previous kernel
   pdl_trigger();
   fetch(r, 0);
+  // the gains, and the turns per position of the pairs this lane computes
+  __shared__ __align__(16) float s_gain[128];
+  if (g) {
+    for (int i = tid; i < a.d; i += kRowsThreads) s_gain[i] = g[i];
+  }
+  constexpr int NF = MODE == PAIR_STAGED ? 8 : 4;
+  unsigned long long turns[NF];
+#pragma unroll
+  for (int j = 0; j < NF; ++j) {
+    const int e = e0 + j;
+    int i;
+    if (MODE == PAIR_INSIDE) i = e0 / 2 + j;
+    else if (MODE == PAIR_LANES) i = e0 >= half ? e - half + 4 : e;  // a lane and its mate: four pairs each
+    else i = a.interleaved ? e >> 1 : e >= half ? e - half : e;
+    turns[j] = kind < 2 && (MODE == PAIR_STAGED ? e : e0) < a.rot ? turns64(a.inv_freq[i]) : 0;
+  }
+  __syncthreads();
   int pos_next = r < a.rows ? a.pos[r] : -1;
   // the trip count is the CTA's: its first unit's rows
   for (long long rc = static_cast<long long>(blockIdx.x) * (kRowsThreads / LPH); rc < a.rows; rc += rstep, r += rstep) {
@@ -225,7 +266,7 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             float c, s;
-            turn(a.inv_freq[e0 / 2 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
+            turn(turns[j], static_cast<uint32_t>(pos), a.factor, &c, &s);
             cg[2 * j] = cg[2 * j + 1] = c;
             sg[2 * j] = -s, sg[2 * j + 1] = s;
           }
@@ -233,11 +274,10 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
       } else if (MODE == PAIR_LANES) {
         // a lane and its mate turn the same 8 pairs: each computes four of them
         const bool upper = e0 >= half;
-        const int p0 = upper ? e0 - half + 4 : e0;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           float c = 1.f, s = 0.f;
-          if (turned) turn(a.inv_freq[p0 + j], static_cast<uint32_t>(pos), a.factor, &c, &s);
+          if (turned) turn(turns[j], static_cast<uint32_t>(pos), a.factor, &c, &s);
           const float c2 = __shfl_sync(0xffffffffu, c, mate), s2 = __shfl_sync(0xffffffffu, s, mate);
           cg[j] = upper ? c2 : c;
           cg[j + 4] = upper ? c : c2;
@@ -251,18 +291,33 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
           const bool upper = a.interleaved ? e & 1 : e >= half;
           if (e >= a.rot) continue;
           float c, s;
-          turn(a.inv_freq[a.interleaved ? e >> 1 : upper ? e - half : e], static_cast<uint32_t>(pos), a.factor, &c, &s);
+          turn(turns[j], static_cast<uint32_t>(pos), a.factor, &c, &s);
           cg[j] = c;
           sg[j] = upper ? s : -s;
         }
       }
     }
     if (g && e0 < a.d) {
+      float ga[8], gm[8];  // of the lane's elements, of their partners
+      const int m0 = MODE == PAIR_LANES && turned ? (e0 < half ? e0 + half : e0 - half) : e0;
+#pragma unroll
+      for (int q = 0; q < 2; ++q) {
+        const float4 u = *reinterpret_cast<const float4*>(s_gain + e0 + 4 * q);
+        const float4 w = *reinterpret_cast<const float4*>(s_gain + m0 + 4 * q);
+        ga[4 * q] = u.x, ga[4 * q + 1] = u.y, ga[4 * q + 2] = u.z, ga[4 * q + 3] = u.w;
+        gm[4 * q] = w.x, gm[4 * q + 1] = w.y, gm[4 * q + 2] = w.z, gm[4 * q + 3] = w.w;
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        cg[j] *= g[e0 + j];
-        if (turned) sg[j] *= g[partner(e0 + j)];
+        cg[j] *= ga[j];
+        sg[j] *= MODE == PAIR_INSIDE ? ga[j ^ 1] : MODE == PAIR_LANES ? gm[j] : s_gain[turned ? partner(e0 + j) : e0];
       }
+    }
+    Pair cg2[4], sg2[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      cg2[j] = pair(cg[el(2 * j)], cg[el(2 * j + 1)]);
+      sg2[j] = pair(sg[el(2 * j)], sg[el(2 * j + 1)]);
     }
 
     for (int b0 = 0; b0 < n; b0 += kBatch) {
@@ -278,11 +333,15 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
         float x[8];
         widen8(raw[i], x);
         if (kind < 2) {
+          Pair v[4], p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = pair(x[el(2 * e)], x[el(2 * e + 1)]);
           float inv = 1.f;
           if (g) {
-            float ss = 0.f;
-#pragma unroll
-            for (int e = 0; e < 8; ++e) ss = fmaf(x[e], x[e], ss);
+            const Pair s2 = fma2(v[3], v[3], fma2(v[2], v[2], fma2(v[1], v[1], mul2(v[0], v[0]))));
+            float s0, s1;
+            unpair(s2, &s0, &s1);
+            float ss = s0 + s1;
 #pragma unroll
             for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
             // 1 / sqrt by the approximation and one Newton step
@@ -290,32 +349,39 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
             inv = rsqrtf(t);
             if (t > 0.f && t < INFINITY) inv = fmaf(0.5f * inv, fmaf(-t * inv, inv, 1.f), inv);
           }
-          float p[8];
           if (MODE == PAIR_INSIDE) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = x[e ^ 1];
+            for (int e = 0; e < 4; ++e) p[e] = v[e ^ 1];
           } else if (MODE == PAIR_LANES) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = __shfl_sync(0xffffffffu, x[e], mate);
+            for (int e = 0; e < 4; ++e)
+              p[e] = pair(__shfl_sync(0xffffffffu, x[2 * e], mate), __shfl_sync(0xffffffffu, x[2 * e + 1], mate));
           } else {
             float* st = stage + (tid - li) * 8;
             __syncwarp();
 #pragma unroll
             for (int e = 0; e < 8; ++e) st[e0 + e] = x[e];
             __syncwarp();
+            float q[8];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) p[e] = e0 + e < a.rot ? st[partner(e0 + e)] : 0.f;
+            for (int e = 0; e < 8; ++e) q[e] = e0 + e < a.rot ? st[partner(e0 + e)] : 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) p[e] = pair(q[2 * e], q[2 * e + 1]);
           }
           if (turned) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float y = fmaf(p[e], sg[e], x[e] * cg[e]);
-              x[e] = g ? y * inv : y;
-            }
+            for (int e = 0; e < 4; ++e) v[e] = fma2(p[e], sg2[e], mul2(v[e], cg2[e]));
           } else if (g) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * cg[e];
+            for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], cg2[e]);
           }
+          if (g) {
+            const Pair i2 = pair(inv, inv);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = mul2(v[e], i2);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) unpair(v[e], &x[el(2 * e)], &x[el(2 * e + 1)]);
         }
         if (stores && b0 + i < n) put8(out, to + (b0 + i) * step, out_f32, vec_out, x);
       }
@@ -331,10 +397,17 @@ cudaError_t launch_mode(const QkRowsArgs& a, int sms, cudaStream_t st) {
   // three CTAs an SM; each walks the same number of rows
   const long long most = (3ll * sms + groups - 1) / groups, turns = (blocks + most - 1) / most;
   const dim3 grid(static_cast<unsigned>((blocks + turns - 1) / turns), static_cast<unsigned>(groups));
-  if (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0)
-    return a.interleaved ? launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE>, grid, dim3(kRowsThreads), 0, st, true, a)
-                         : launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES>, grid, dim3(kRowsThreads), 0, st, true, a);
-  return launch_k(qk_rows_kernel<XT, LPH, PAIR_STAGED>, grid, dim3(kRowsThreads), 0, st, true, a);
+  const dim3 block(kRowsThreads);
+  const bool vec = a.vec_x && a.vec_y;
+  if (a.interleaved ? a.rot % 8 == 0 : a.rot % 16 == 0) {
+    if (a.interleaved)
+      return vec ? launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE, true>, grid, block, 0, st, true, a)
+                 : launch_k(qk_rows_kernel<XT, LPH, PAIR_INSIDE, false>, grid, block, 0, st, true, a);
+    return vec ? launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES, true>, grid, block, 0, st, true, a)
+               : launch_k(qk_rows_kernel<XT, LPH, PAIR_LANES, false>, grid, block, 0, st, true, a);
+  }
+  return vec ? launch_k(qk_rows_kernel<XT, LPH, PAIR_STAGED, true>, grid, block, 0, st, true, a)
+             : launch_k(qk_rows_kernel<XT, LPH, PAIR_STAGED, false>, grid, block, 0, st, true, a);
 }
 
 template <typename XT>
