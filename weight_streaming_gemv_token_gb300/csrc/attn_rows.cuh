@@ -274,6 +274,25 @@ struct ArCopy {
   }
 };
 
+// Eight more partial results of a row (reference and sum p, elements y) into (m, l,
+// x); p = (-inf, 0) and y = 0 is none. A part whose scores are all -inf has the
+// sum 0; a NaN in it stays one.
+__device__ __forceinline__ void ar_merge8(const float2 (&p)[8], const float4 (&y)[8], float* m, float* l, float4* x) {
+  float mn = *m;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mn = fmaxf(mn, p[i].x);
+  const float mu = mn == -INFINITY ? 0.f : mn, f = am_exp2(*m - mu);
+  *l *= f;
+  x->x *= f, x->y *= f, x->z *= f, x->w *= f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float e = p[i].x == -INFINITY ? 1.f : am_exp2(p[i].x - mu);
+    *l = fmaf(p[i].y, e, *l);
+    x->x = fmaf(y[i].x, e, x->x), x->y = fmaf(y[i].y, e, x->y), x->z = fmaf(y[i].z, e, x->z), x->w = fmaf(y[i].w, e, x->w);
+  }
+  *m = mn;
+}
+
 // NA, NB: rows of a prefix item (8 or 16; 0: no prefix items) and of a branch (8,
 // or 16 for groups over 8). CTAs below a.prefix_items are prefix items, the others
 // own CTAs. Eight warps, one CTA an SM, where the prefix is cut here (few splits to

@@ -11,6 +11,7 @@
 #include <cmath>
 
 #include "attn_mma.cuh"
+#include "attn_own.cuh"
 #include "attn_prefix_tc.cuh"
 #include "common.h"
 
@@ -70,21 +71,7 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AmJoinArgs a) {
       y[i] = s < slots && in ? *reinterpret_cast<const float4*>(a.part_o + (s * total + w) * a.d + lane * 4)
                              : make_float4(0.f, 0.f, 0.f, 0.f);
     }
-    float mn = m;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) mn = fmaxf(mn, p[i].x);
-    const float mu = mn == -INFINITY ? 0.f : mn;
-    const float f = am_exp2(m - mu);
-    l *= f;
-    x.x *= f, x.y *= f, x.z *= f, x.w *= f;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      // a part whose scores are all -inf has the sum 0; a NaN in it stays one
-      const float e = p[i].x == -INFINITY ? 1.f : am_exp2(p[i].x - mu);
-      l = fmaf(p[i].y, e, l);
-      x.x = fmaf(y[i].x, e, x.x), x.y = fmaf(y[i].y, e, x.y), x.z = fmaf(y[i].z, e, x.z), x.w = fmaf(y[i].w, e, x.w);
-    }
-    m = mn;
+    ar_merge8(p, y, &m, &l, &x);
   }
   if (a.warps == 4) {
     if (lane == 0) s_m[warp] = m, s_l[warp] = l;
@@ -133,6 +120,18 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AmJoinArgs a) {
   if (a.lse && lane == 0) a.lse[w] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
+template <int NB>
+cudaError_t launch_own(const AmArgs& a, const AoArgs& o, unsigned items, int dev, cudaStream_t st) {
+  constexpr size_t smem = ArGeom<128, NB, 4>::SMEM;
+  static bool lifted[64] = {};
+  if (!lifted[dev]) {
+    const cudaError_t e = allow_smem_shared(attn_own_kernel<NB>, smem);
+    if (e != cudaSuccess) return e;
+    lifted[dev] = true;
+  }
+  return launch_k(attn_own_kernel<NB>, dim3(items), dim3(128), smem, st, true, a, o);
+}
+
 bool attn_sizes_ok(const attn_shared_args* a) {
   auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
   return a->batch >= 0 && a->batch <= 65535 && a->n_kv >= 1 && a->n_q >= a->n_kv && a->n_q <= 65535 &&
@@ -143,11 +142,13 @@ bool attn_sizes_ok(const attn_shared_args* a) {
 }
 
 
+constexpr int kOwnSegMax = 64;  // blocks of 16 own keys up to which attn_own_kernel takes them
 constexpr int kTcRowsMin = 16;  // rows of a key/value head above which the prefix runs on tcgen05
 
 // How a call is cut up.
 struct AsPlan {
   bool tc;  // the prefix on attn_prefix_tc_kernel (row_groups: blocks of 128 rows)
+  bool own_joins;  // ... and the own keys on attn_own_kernel, which joins
   int na, row_groups;  // rows of a prefix item otherwise (0 with tc)
   int prefix_slots, prefix_chunk, own_slots, own_block;
   long long own_seg, own_per;
@@ -197,6 +198,8 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
       // + 512: 69 and 60).
       warps = 4ll * sms;
       if (line > 8 * warps) warps *= 3;
+      // one CTA walks a branch's keys of a head where they are few
+      p.own_joins = p.own_seg <= kOwnSegMax;
     } else {
       // one CTA of eight warps an SM, shared out by the number of keys
       const long long units = up(a->prefix_len, 128) * heads;
@@ -208,6 +211,7 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
     p.own_per = line > 0 ? up(line, warps) : 1;
     p.own_items = up(up(line, p.own_per), p.tc ? 4 : 8);
     p.own_slots = p.own_seg > 0 ? static_cast<int>((p.own_seg - 1 + p.own_per - 1) / p.own_per + 1) : 0;
+    if (p.own_joins) p.own_items = segments, p.own_slots = 0;
   }
   p.prefix_items = p.prefix_slots * heads;
   const long long parts = static_cast<long long>(p.prefix_slots + p.own_slots) * a->batch * a->n_q;
@@ -323,6 +327,16 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
     }
     WSG_CUDA_TRY(nullptr, launch_k(attn_prefix_tc_kernel, dim3(static_cast<unsigned>(p.prefix_items)), dim3(kApThreads),
                                    kApSmem, s, true, maps[0], maps[1], t));
+  }
+  if (p.own_joins) {
+    AoArgs o{};
+    o.prefix_slots = p.prefix_slots;
+    o.out = a->out;
+    o.out_stride = a->out_stride;
+    o.lse = a->lse;
+    WSG_CUDA_TRY(nullptr, k.group > 8 ? launch_own<16>(k, o, static_cast<unsigned>(p.own_items), di.device, s)
+                                      : launch_own<8>(k, o, static_cast<unsigned>(p.own_items), di.device, s));
+    return DEC_OK;
   }
   const int items = k.prefix_items + static_cast<int>(p.own_items);
   k.first = !p.tc;
