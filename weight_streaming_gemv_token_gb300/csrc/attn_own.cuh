@@ -28,6 +28,7 @@ __global__ void __maxnreg__(152) attn_own_kernel(const AmArgs a, const AoArgs j)
   __shared__ float4 s_x[WARPS][32];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x / a.n_kv, g = blockIdx.x % a.n_kv;
+  if (a.first) pdl_wait();  // no prefix: nothing has waited for the stream's previous kernel
   pdl_trigger();
   const int n = a.len[b];
   if (n < 0) {

@@ -523,8 +523,8 @@ cudaError_t ar_launch_rows(const AmArgs& a, int na, int items, int dev, cudaStre
                   : ar_launch_one<QT, DP, QP, 8, 8>(a, items, dev, st);
 }
 
-// na: rows of a prefix item, 8 or 16; 0: own keys only, beside attn_prefix_tc_kernel
-// (bfloat16 queries, head size 128).
+// na: rows of a prefix item, 8 or 16; 0: own keys only (bfloat16 queries, head size
+// 128, whose prefix attn_prefix_tc_kernel takes).
 template <typename QT, int QP>
 cudaError_t ar_launch(const AmArgs& a, int na, int items, int dev, cudaStream_t st) {
   if constexpr (QP == 1)

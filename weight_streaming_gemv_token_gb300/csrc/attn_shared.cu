@@ -142,9 +142,6 @@ bool attn_sizes_ok(const attn_shared_args* a) {
 }
 
 
-constexpr int kOwnSegMax = 64;  // blocks of 16 own keys up to which attn_own_kernel takes them
-constexpr int kTcRowsMin = 16;  // rows of a key/value head above which the prefix runs on tcgen05
-
 // How a call is cut up.
 struct AsPlan {
   bool tc;  // the prefix on attn_prefix_tc_kernel (row_groups: blocks of 128 rows)
@@ -159,11 +156,15 @@ struct AsPlan {
 AsPlan attn_plan(const attn_shared_args* a, int sms) {
   AsPlan p{};
   auto up = [](long long x, long long y) { return (x + y - 1) / y; };
+  auto least = [](long long x, long long y) { return x < y ? x : y; };
+  auto root = [](long long x) { return static_cast<long long>(std::sqrt(static_cast<double>(x))); };
   const bool f32 = a->kvdtype == DEC_F32;
   const int group = a->n_q / a->n_kv, rows = a->batch * group;
-  p.tc = !f32 && a->qdtype == DEC_BF16 && a->head_dim == kApD && rows > kTcRowsMin && a->prefix_len > 0 &&
-         a->prefix_stride < 1ll << 31;
-  p.na = p.tc ? 0 : f32 || rows > 8 ? 16 : 8;
+  // Queries and cache in bfloat16, head size 128: the prefix on tcgen05 for any number
+  // of rows (12 rows x 4096 keys: 9.1 us, with attn_rows_kernel 11.7; 8 rows: the same).
+  const bool fast = !f32 && a->qdtype == DEC_BF16 && a->head_dim == kApD && a->prefix_stride < 1ll << 31;
+  p.tc = fast && a->prefix_len > 0;
+  p.na = fast ? 0 : f32 || rows > 8 ? 16 : 8;
   const int block = p.tc ? kApRows : p.na;
   p.row_groups = static_cast<int>(up(rows, block));
   const long long capacity = static_cast<long long>(a->table_stride) << page_shift(a->page_size);
@@ -179,7 +180,8 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
     // one CTA an SM, shared out by the number of keys
     constexpr int unit = kAmWarps * 8;
     const long long pre = up(a->prefix_len, unit) * heads, own = up(capacity, unit) * segments;
-    cut(a->prefix_len, unit, pre ? sms * pre / (pre + own) / heads : 0, &p.prefix_slots, &p.prefix_chunk);
+    cut(a->prefix_len, unit, pre ? least(sms * pre / (pre + own) / heads, root(10 * up(a->prefix_len, unit))) : 0,
+        &p.prefix_slots, &p.prefix_chunk);
     const long long left = sms - p.prefix_slots * heads;
     cut(capacity, unit, up(left > sms / 4 ? left : sms / 4, segments), &p.own_slots, &p.own_block);
     p.own_seg = p.own_slots;
@@ -190,26 +192,30 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
     p.own_seg = up(capacity, 16);
     const long long line = p.own_seg * segments;  // own blocks
     long long warps;                              // that walk it
-    if (p.tc) {
-      cut(a->prefix_len, kApKeys, sms / heads, &p.prefix_slots, &p.prefix_chunk);
-      // One CTA of four warps fits beside a prefix CTA, three an SM after those
-      // have ended: a second wave pays when the first would walk over 8 blocks a warp
-      // (16 x 4096 + 256: 17.6 us with one wave, 19.6 with three CTAs an SM; 64 x 32768
-      // + 512: 69 and 60).
+    if (fast) {
+      // A tile takes about 1 us where CTAs are few, a split 0.1 us to join: no more
+      // splits than the square root of ten times the tiles.
+      cut(a->prefix_len, kApKeys, least(sms / heads, root(10 * up(a->prefix_len, kApKeys))), &p.prefix_slots,
+          &p.prefix_chunk);
+      // One CTA walks a branch's keys of a head and joins, unless there are few
+      // branches and many keys: 17 branches of one head x 512 own keys take 10.1 us
+      // with that and 11.2 with equal pieces for all warps and a join kernel, x 1024
+      // 15.1 and 11.2; 160 (branch, head) pairs x 1024 23 and 27.
+      p.own_joins = p.own_seg <= 32 || segments >= sms;
+      // Otherwise: one CTA of four warps fits beside a prefix CTA, three an SM after
+      // those have ended; a second wave pays when the first would walk over 8 blocks a warp.
       warps = 4ll * sms;
       if (line > 8 * warps) warps *= 3;
-      // one CTA walks a branch's keys of a head where they are few
-      p.own_joins = p.own_seg <= kOwnSegMax;
     } else {
       // one CTA of eight warps an SM, shared out by the number of keys
       const long long units = up(a->prefix_len, 128) * heads;
       const long long pre = units ? sms * units / (units + up(line, 8)) : 0;
-      cut(a->prefix_len, 64, pre / heads, &p.prefix_slots, &p.prefix_chunk);
+      cut(a->prefix_len, 64, least(pre / heads, root(10 * up(a->prefix_len, 64))), &p.prefix_slots, &p.prefix_chunk);
       const long long left = sms - p.prefix_slots * heads;
       warps = 8 * (left > sms / 4 ? left : sms / 4);
     }
     p.own_per = line > 0 ? up(line, warps) : 1;
-    p.own_items = up(up(line, p.own_per), p.tc ? 4 : 8);
+    p.own_items = up(up(line, p.own_per), fast ? 4 : 8);
     p.own_slots = p.own_seg > 0 ? static_cast<int>((p.own_seg - 1 + p.own_per - 1) / p.own_per + 1) : 0;
     if (p.own_joins) p.own_items = segments, p.own_slots = 0;
   }
@@ -329,6 +335,7 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
                                    kApSmem, s, true, maps[0], maps[1], t));
   }
   if (p.own_joins) {
+    k.first = !p.tc;
     AoArgs o{};
     o.prefix_slots = p.prefix_slots;
     o.out = a->out;
