@@ -351,6 +351,13 @@ ATTN_CASES = [
     (64, 16, 8, 128, 1025, [(i * 7) % 90 for i in range(64)], 32),  # 128 rows
     (70, 8, 2, 128, 385, [3] * 70, 16),                            # 280 rows
     (3, 4, 2, 128, 5000, [700, 20, 1], 64),                        # long for few rows
+    (3, 8, 2, 128, 0, [5, 0, 70], 16),                             # no prefix
+    (2, 4, 2, 128, 0, [1500, 3], 32),                              # ... and long own keys
+    (5, 16, 1, 128, 300, [40, 0, -1, 1, 100], 16),                 # group of 16
+    (2, 16, 1, 128, 100, [900, 10], 8),                            # ... long, pages shorter than a block
+    (4, 12, 4, 128, 2000, [33, 7, 64, 0], 4),                      # group of 3
+    (2, 8, 2, 64, 3000, [1200, 1], 16),                            # both axes cut, a shorter head
+    (40, 32, 8, 128, 1500, [64 - i for i in range(40)], 64),       # 160 rows: two blocks of rows
 ]
 TYPES = [("bf16", "bf16"), ("f32", "bf16"), ("f32", "f32"), ("bf16", "f32")]
 

@@ -24,7 +24,7 @@ namespace wsg {
 namespace {
 
 constexpr int kChunkThreads = 256, kBeamThreads = 512;
-constexpr int kChunkCtas = 6;  // CTAs of pass 1 an SM, which leaves room for one of pass 2
+constexpr int kChunkCtas = 4;  // CTAs of pass 1 an SM: registers and threads for one of pass 2 remain
 constexpr int kBeamChunksMax = 2048;  // chunks of one call (all rows)
 constexpr int kBeamChunkMin = 1024;
 constexpr int kBeamGather = 4096;  // candidates held in shared memory
@@ -77,6 +77,7 @@ struct BeamArgs {
   uint2* key;  // (high word, low word)
   unsigned long long row_inv;  // k * row_inv >> 32 = k / per_row for a chunk k
   int vec;
+  int row_lanes;  // log2 of the lanes that join a row in pass 2
 };
 
 // Masked logits (NaN as well) count as -inf.
@@ -110,14 +111,17 @@ __device__ __forceinline__ float2 two_sum(float a, float b) {
   return make_float2(s, (a - (s - t)) + (b - t));
 }
 
-// score - (m + log s) as two floats. s = 2^e f with f in [0.7, 1.42): log f is
-// below 0.36, so a float32 logarithm of it is good to 3e-8; e log 2 is an exact
-// product by the first 13 bits of log 2 and a small rest.
+// score - (m + log s) as two floats. s = 2^e f with f in [0.7, 1.42]; log f = 2
+// artanh u, u = (f - 1) / (f + 1), |u| < 0.172, by its series to u^9 (the next term
+// is below 7e-10; the whole is good to 3e-8); e log 2 is an exact product by the
+// first 13 bits of log 2 and a small rest.
 __device__ __forceinline__ float2 row_offset(float score, float m, float s) {
   int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;  // (s >= 1)
   float f = __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u);
   if (f > 1.41421356f) f *= 0.5f, ++e;
-  const float2 a = two_sum(score, -m), b = two_sum(a.x, e * -0.693145751953125f), c = two_sum(b.x, -logf(f));
+  const float u = __fdividef(f - 1.f, f + 1.f), u2 = u * u;
+  const float log_f = 2.f * fmaf(u * u2, fmaf(u2, fmaf(u2, fmaf(u2, 1.f / 9.f, 1.f / 7.f), 1.f / 5.f), 1.f / 3.f), u);
+  const float2 a = two_sum(score, -m), b = two_sum(a.x, e * -0.693145751953125f), c = two_sum(b.x, -log_f);
   return two_sum(c.x, a.y + b.y + c.y - e * 1.428606820309417e-6f);
 }
 
@@ -125,7 +129,7 @@ __device__ __forceinline__ float2 row_offset(float score, float m, float s) {
 // time. The exponentials are 2^((x - m) log2 e) with m the warp's maximum so far.
 // Every CTA is resident from the start and leaves room beside it for one of pass
 // 2, which gets ready meanwhile.
-__global__ void __launch_bounds__(kChunkThreads) beam_chunks_kernel(const BeamArgs a) {
+__global__ void __launch_bounds__(kChunkThreads, 6) beam_chunks_kernel(const BeamArgs a) {
   constexpr int kWarps = kChunkThreads / 32;
   constexpr float kLog2e = 1.44269504088896340736f;
   __shared__ float s_m[2][kWarps], s_s[2][kWarps];
@@ -347,23 +351,22 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
   if (tid == 0) s_mine = s_lo = 0xffffffffu, s_n = s_hi = 0;
   __syncthreads();
   // row offsets, as many lanes a row as there are; -inf where the row offers nothing
-  int lanes = 1;
-  while (lanes < 32 && lanes * 2 * a.beams <= kBeamThreads) lanes *= 2;
+  const int lanes = 1 << a.row_lanes;
 #pragma unroll 1
-  for (int b0 = 0; b0 < a.beams; b0 += kBeamThreads / lanes) {
-    const int b = b0 + tid / lanes, c0 = (b < a.beams ? b : 0) * a.per_row;
+  for (int b0 = 0; b0 < a.beams; b0 += kBeamThreads >> a.row_lanes) {
+    const int b = b0 + (tid >> a.row_lanes), c0 = (b < a.beams ? b : 0) * a.per_row;
     float m = -INFINITY, s = 0.f;
 #pragma unroll 4
-    for (int c = tid % lanes; c < a.per_row; c += lanes) m = fmaxf(m, smax[c0 + c]);
+    for (int c = tid & (lanes - 1); c < a.per_row; c += lanes) m = fmaxf(m, smax[c0 + c]);
 #pragma unroll 1
     for (int o = lanes / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
     const bool finite = m > -INFINITY && m < INFINITY;
 #pragma unroll 4
-    for (int c = tid % lanes; c < a.per_row; c += lanes)
+    for (int c = tid & (lanes - 1); c < a.per_row; c += lanes)
       s = fmaf(ssum[c0 + c], ex2((smax[c0 + c] - (finite ? m : 0.f)) * kLog2e), s);
 #pragma unroll 1
     for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (b < a.beams && tid % lanes == 0) {
+    if (b < a.beams && (tid & (lanes - 1)) == 0) {
       const float sc = off[b].x;
       off[b] = finite && isfinite(sc) ? row_offset(sc, m, s) : make_float2(-INFINITY, 0.f);
     }
@@ -503,14 +506,15 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
   }
   // ranks by counting the better ones, `split` threads a candidate: the high words
   // four at a time; candidates that share theirs compare the rest
-  int split = 1;
-  while (split < 32 && n * split * 2 <= kBeamThreads) split *= 2;
+  int lg = 0;
+  while (lg < 5 && (n << (lg + 1)) <= kBeamThreads) ++lg;
+  const int split = 1 << lg;
 #pragma unroll 1
-  for (uint32_t i0 = 0; i0 < n; i0 += kBeamThreads / split) {
-    const uint32_t i = i0 + tid / split, h = i < n ? sh[i] : 0xffffffffu;
+  for (uint32_t i0 = 0; i0 < n; i0 += kBeamThreads >> lg) {
+    const uint32_t i = i0 + (tid >> lg), h = i < n ? sh[i] : 0xffffffffu;
     uint32_t rank = 0, same = 0;
 #pragma unroll 4
-    for (uint32_t j = tid % split * 4; j < n; j += split * 4) {
+    for (uint32_t j = (tid & (split - 1)) * 4; j < n; j += split * 4) {
       const uint4 k = *reinterpret_cast<const uint4*>(sh + j);
       rank += (k.x > h) + (k.y > h) + (k.z > h) + (k.w > h);
       same += (k.x == h) + (k.y == h) + (k.z == h) + (k.w == h);
@@ -520,7 +524,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
       rank += __shfl_xor_sync(0xffffffffu, rank, o);
       same += __shfl_xor_sync(0xffffffffu, same, o);
     }
-    if (i < n && tid % split == 0) {
+    if (i < n && (tid & (split - 1)) == 0) {
       if (same > 1)
 #pragma unroll 1
         for (uint32_t j = 0; j < n; ++j) rank += sh[j] == h && (sl[j] > sl[i] || (sl[j] == sl[i] && sf[j] < sf[i]));
@@ -649,6 +653,7 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
   k.key = reinterpret_cast<uint2*>(w + L.key);
   k.flat = reinterpret_cast<uint32_t*>(w + L.flat);
   k.row_inv = (1ull << 32) / L.per_row + 1;
+  while (k.row_lanes < 5 && (a->beams << (k.row_lanes + 1)) <= kBeamThreads) ++k.row_lanes;
   k.vec = aligned16(a->logits) && a->logits_stride % 4 == 0;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // static and dynamic shared memory together pass the 48 KB that need no opt-in
