@@ -64,7 +64,7 @@ typedef enum { DEC_F32 = 0, DEC_BF16 = 1, DEC_Q4G64 = 2 } dec_dtype;
 #define DEC_DEVERR_BAD_TOKEN 0x4u    /* a token ID outside [0, vocab) was read as 0 */
 #define DEC_DEVERR_BAD_POSITION 0x8u /* a position reached the KV capacity; the step did nothing */
 #define DEC_DEVERR_EXCHANGE_TIMEOUT 0x10u /* persistent engine: a wait for another CTA's words gave up */
-#define DEC_DEVERR_GEMM_TIMEOUT 0x20u     /* chunked prefill: a tensor-core GEMM pipeline wait gave up */
+#define DEC_DEVERR_GEMM_TIMEOUT 0x20u     /* chunked prefill, attn_shared_prefix: a tensor-core pipeline wait gave up */
 #define DEC_DEVERR_BARRIER_TIMEOUT 0x40u  /* persistent 4-bit engine: a grid barrier gave up (dec_reset clears it) */
 #define DEC_DEVERR_BAD_PAGE 0x80u         /* a sequence, page or parent index of the paged calls was out of range */
 
@@ -432,9 +432,13 @@ dec_status gemm_bf16(const uint16_t* d_A, const uint16_t* d_W, float* d_C, int32
  *
  * All of them take their arguments in a struct, are asynchronous on `stream`
  * (the struct may be reused once the call returns; the buffers when the work
- * is done), allocate nothing and can be captured into a graph. Calls that
- * share a workspace or write the same buffers must be ordered by the caller
- * (one stream, or events). Every pointer must belong to the current device.
+ * is done), allocate nothing and can be captured into a graph; the first call
+ * of each kind on a device sets its kernels up and must come before any stream
+ * capture. Calls that share a workspace or write the same buffers must be
+ * ordered by the caller (one stream, or events); a workspace needs no
+ * initialisation and holds nothing between calls. Every pointer must belong to
+ * the current device. Each call is a programmatic dependent of the stream's
+ * previous kernel and reads nothing before that kernel has finished.
  * Common errors: DEC_EINVAL (NULL struct, sizes, dtype, NULL or misaligned
  * pointers), DEC_EDEVICE, DEC_ECUDA. */
 
@@ -532,11 +536,13 @@ dec_status kv_append_paged(const kv_append_args* a, void* stream);
  * unused slot, whose out and lse are left as they were. A branch with nothing
  * to attend to gets zeros (and lse -inf). lse (nullable, float32
  * [batch][n_q]) receives the natural log of the softmax's denominator.
- * n_q / n_kv <= 16. Scores, softmax sums and outputs are accumulated in
+ * n_q / n_kv <= 16, batch * n_q < 2^24. A key or value that is not finite and
+ * attended to makes its rows not finite (a NaN or an infinity). Scores, softmax sums and outputs are accumulated in
  * float32; with DEC_BF16 q and out the result is rounded once to bfloat16. The
  * result does not depend on timing (partial results join in a fixed order).
- * d_workspace: attn_shared_prefix_workspace(a) bytes, 256-byte aligned; its
- * contents need no initialisation. */
+ * A bounded wait that gave up (a broken launch) sets DEC_DEVERR_GEMM_TIMEOUT in
+ * the context-free error word. d_workspace: attn_shared_prefix_workspace(a)
+ * bytes for these sizes, 256-byte aligned. */
 typedef struct {
   int32_t batch, n_q, n_kv, head_dim;
   int32_t qdtype, kvdtype; /* q and out; prefix and pages: DEC_F32 or DEC_BF16 */

@@ -143,7 +143,7 @@ BAD = {
     "kv_append_paged": ROWS + PAGES + [{"n_kv": 0}, {"kvdtype": 2}, {"v": None}, {"page_table": None}, {"n_seq": -1},
                                        {"table_stride": -1}, {"base_pos": -1}, {"v_stride": -1}],
     "attn_shared_prefix": HEADS + PAGES + [
-        {"batch": -1}, {"batch": 65536}, {"n_q": 3}, {"n_q": 0}, {"n_kv": 0}, {"n_q": 34, "n_kv": 2}, {"qdtype": 2},
+        {"batch": -1}, {"batch": 65536}, {"batch": 4096, "n_q": 4096, "n_kv": 4096, "out_stride": 1 << 20}, {"n_q": 3}, {"n_q": 0}, {"n_kv": 0}, {"n_q": 34, "n_kv": 2}, {"qdtype": 2},
         {"kvdtype": 2}, {"q": None}, {"out": None}, {"seq_len": None}, {"prefix_k": None}, {"prefix_v": None},
         {"prefix_len": -1}, {"prefix_stride": 7}, {"page_table": None}, {"out_stride": 63}, {"q_stride": -1},
         {"table_stride": -1}, {"table_stride": 1 << 30}, {"prefix_k": P + 4}, {"d_workspace": None},

@@ -135,6 +135,7 @@ cudaError_t launch_own(const AmArgs& a, const AoArgs& o, unsigned items, int dev
 bool attn_sizes_ok(const attn_shared_args* a) {
   auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
   return a->batch >= 0 && a->batch <= 65535 && a->n_kv >= 1 && a->n_q >= a->n_kv && a->n_q <= 65535 &&
+         static_cast<long long>(a->batch) * a->n_q < 1ll << 24 &&
          a->n_q % a->n_kv == 0 && a->n_q / a->n_kv <= 16 && a->head_dim >= 8 && a->head_dim <= 128 &&
          a->head_dim % 8 == 0 && type(a->qdtype) && type(a->kvdtype) && a->prefix_len >= 0 &&
          page_shift(a->page_size) >= 0 && a->num_pages >= 0 && a->table_stride >= 0 &&
@@ -177,13 +178,23 @@ AsPlan attn_plan(const attn_shared_args* a, int sms) {
     *slots = static_cast<int>(up(keys, *chunk));
   };
   if (f32) {
-    // one CTA an SM, shared out by the number of keys
+    // One CTA an SM. The branches' CTAs follow the prefix's and fill its gaps, so
+    // the number of splits is the one with the least estimated end: the longer of a
+    // prefix CTA and an SM's share of all, half a CTA more where the last wave is
+    // ragged, and 0.06 of a unit of keys for each split to join (8 x 3001: 12 splits
+    // 17.2 us, 11 in one wave with the branches' 18.5; 64 x 8192: 2 splits 136, 1 216).
     constexpr int unit = kAmWarps * 8;
-    const long long pre = up(a->prefix_len, unit) * heads, own = up(capacity, unit) * segments;
-    cut(a->prefix_len, unit, pre ? least(sms * pre / (pre + own) / heads, root(10 * up(a->prefix_len, unit))) : 0,
-        &p.prefix_slots, &p.prefix_chunk);
-    const long long left = sms - p.prefix_slots * heads;
-    cut(capacity, unit, up(left > sms / 4 ? left : sms / 4, segments), &p.own_slots, &p.own_block);
+    const long long units = up(a->prefix_len, unit), own = up(capacity, unit);
+    cut(capacity, unit, own ? sms / ((units ? 2 : 1) * segments) : 0, &p.own_slots, &p.own_block);
+    const double each = static_cast<double>(p.own_block) / unit, all = each * p.own_slots * segments;
+    long long best = 1;
+    double least_end = 0;
+    for (long long n = 1; n <= units && n <= 128; ++n) {
+      const double chunk = static_cast<double>(up(units, n)), share = (chunk * n * heads + all) / sms;
+      const double end = (n * heads > sms ? share + 0.5 * chunk : chunk > share + 0.5 * each ? chunk : share + 0.5 * each) + 0.06 * n;
+      if (n == 1 || end < least_end) best = n, least_end = end;
+    }
+    cut(a->prefix_len, unit, best, &p.prefix_slots, &p.prefix_chunk);
     p.own_seg = p.own_slots;
     p.own_per = 1;
     p.own_items = p.own_slots * segments;
