@@ -78,6 +78,72 @@ def test_pool_rows_are_64_bit_and_distinct(paging):
     assert paging.row(2**31 - 1, 64, 10, 2**31 - 2, 63, 1023) == ((2**31 - 2) * 64 + 63) * 1024 + 1023
 
 
+@pytest.fixture(scope="module")
+def plan(tmp_path_factory):
+    """csrc/attn_plan.h compiled as plain C++: the plan of an attention call on 152 SMs."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("plan")
+    src = d / "p.cpp"
+    src.write_text('#include "attn_plan.h"\nextern "C" int plan(const attn_shared_args* a, long long* o) {\n'
+                   "  if (!wsg::attn_sizes_ok(a)) return 0;\n"
+                   "  const wsg::AsPlan p = wsg::attn_plan(a, 152);\n"
+                   "  const long long v[] = {p.tc, p.own_joins, p.na, p.row_groups, p.prefix_slots, p.prefix_chunk,\n"
+                   "    p.own_slots, p.own_block, p.own_seg, p.own_per, p.prefix_items, p.own_items,\n"
+                   "    (long long)p.o, (long long)p.ml, (long long)p.total};\n"
+                   "  for (int i = 0; i < 15; ++i) o[i] = v[i];\n  return 1;\n}\n")
+    lib = d / "p.so"
+    inc = os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc")
+    cmd = [cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(src), "-o", str(lib)]
+    checked = ["-fsanitize=undefined", "-fno-sanitize-recover=undefined"]  # where the toolchain has its library
+    if subprocess.run(cmd + checked, capture_output=True).returncode != 0:
+        subprocess.run(cmd, check=True)
+    return ctypes.CDLL(str(lib)).plan
+
+
+NAMES = ("tc own_joins na row_groups prefix_slots prefix_chunk own_slots own_block own_seg own_per prefix_items own_items "
+         "o ml total").split()
+
+
+def test_attention_plans_cover_every_key_once(W, plan):
+    """Prefix splits and own pieces cover their axes; every slot that is written or joined lies inside the workspace."""
+    rng = np.random.default_rng(0)
+    for n in range(3000):
+        n_kv = int(rng.choice([1, 2, 3, 8, 16]))
+        group = int(rng.choice([1, 2, 3, 8, 9, 16]))
+        batch = int(np.exp(rng.uniform(0, np.log(300))))
+        page = int(2 ** rng.integers(0, 8))
+        width = int(rng.choice([0, 1, 2, 7, int(np.exp(rng.uniform(0, np.log(5000))))]))
+        plen = int(rng.choice([0, 1, 127, 128, 129, int(np.exp(rng.uniform(0, np.log(300000))))]))
+        d = int(rng.choice([8, 16, 64, 96, 128]))
+        a = W.attn_shared_args(**{**ATTN, "batch": batch, "n_q": n_kv * group, "n_kv": n_kv, "head_dim": d,
+                                  "qdtype": int(rng.integers(0, 2)), "kvdtype": int(rng.integers(0, 2)), "prefix_len": plen,
+                                  "prefix_stride": plen, "page_size": page, "table_stride": width})
+        out = (ctypes.c_longlong * 15)()
+        assert plan(ctypes.byref(a), out) == 1
+        p = dict(zip(NAMES, out))
+        rows, capacity, segs = batch * group, page * width, batch * n_kv
+        block = 128 if p["tc"] else p["na"] or 128
+        assert p["row_groups"] * block >= rows > (p["row_groups"] - 1) * block
+        assert p["prefix_slots"] * p["prefix_chunk"] >= plen and (p["prefix_slots"] - 1) * p["prefix_chunk"] < max(1, plen)
+        assert p["prefix_items"] == p["prefix_slots"] * n_kv * p["row_groups"]
+        assert p["tc"] == (plen > 0 and d == 128 and a.qdtype == 1 and a.kvdtype == 1)
+        assert p["tc"] <= (p["prefix_chunk"] % 128 == 0)
+        slots = p["prefix_slots"] + p["own_slots"]
+        assert p["ml"] >= slots * batch * n_kv * group * d * 4 and p["total"] >= p["ml"] + 8 * slots * batch * n_kv * group
+        if p["own_joins"]:
+            assert p["own_items"] == segs and p["own_slots"] == 0 and a.kvdtype == 1
+            continue
+        assert p["own_seg"] * p["own_block"] >= capacity
+        warps = 1 if a.kvdtype == 0 else 4 if d == 128 and a.qdtype == 1 else 8
+        assert p["own_items"] * warps * p["own_per"] >= p["own_seg"] * segs
+        if capacity:  # the slots that the pieces of a segment take, whatever it holds
+            seg = np.unique(np.clip([0, 1, segs // 2, segs - 1], 0, segs - 1))
+            first, last = seg * p["own_seg"] // p["own_per"], ((seg + 1) * p["own_seg"] - 1) // p["own_per"]
+            assert (last - first < p["own_slots"]).all()
+
+
 def test_frequencies(W):
     w, f = W.rope_frequencies(128, 1e6)
     np.testing.assert_allclose(w, 1e6 ** (-np.arange(0, 128, 2) / 128), rtol=1e-14)

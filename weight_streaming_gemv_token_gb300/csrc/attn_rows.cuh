@@ -28,7 +28,9 @@
 // Rows in shared memory are 16 bytes longer than the head: no matrix load has
 // bank conflicts. Bound by memory for long ranges (the instructions of a block
 // take 24 x 8 cycles of one SM quarter for 8 rows, its 8 KB 350 of the SM's
-// copies), by the latencies of a block's steps for short ones.
+// copies), by the latencies of a block's steps for short ones. Measured: 4 rows a
+// head, head size 64, 20,000 shared keys 11.9 us; 128 rows of float32 queries x
+// 8,192 102 us (the prefix is read from L2 for every 16 rows).
 #pragma once
 #include "attn_mma.cuh"
 

