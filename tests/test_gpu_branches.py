@@ -598,6 +598,22 @@ def test_beam_select_masks():
     assert got[1].tolist() == [-1] * 3
 
 
+@pytest.mark.parametrize("beams", [2, 4, 40])
+@pytest.mark.parametrize("shift", [0.0, 1000.0, -30000.0])
+def test_beam_select_sure_beams(beams, shift):
+    """Beams that are sure of their next token, in equal pairs, so that the best keys are near 0 and the bar is exactly one
+    of them while logits and log-sums are large: what reaches the bar by less than the log-sum's last place is listed."""
+    W = lib()
+    rng = np.random.default_rng(beams)
+    for n_out in (1, 3, beams - 1):
+        logits = (rng.standard_normal((beams, 3000)) * 0.5).astype(np.float32)
+        logits[np.arange(beams), rng.integers(0, 3000, beams)] = rng.uniform(9, 30, beams)
+        logits = (logits + shift).astype(np.float32)
+        logits[1::2] = logits[::2]
+        scores = -np.floor(np.arange(beams) / 2).astype(np.float32)
+        check_select(run_select(W, logits, scores, n_out), logits, scores, n_out)
+
+
 # ---- reorder -------------------------------------------------------------------------------------------------------
 
 REORDER_CASES = [

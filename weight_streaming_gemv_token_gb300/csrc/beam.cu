@@ -431,7 +431,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
     const float2 o = off[b];
     const uint32_t f0 = static_cast<uint32_t>(b) * a.vocab + v0;
     const float bar_value = bar.h == 1 ? -INFINITY : unorder32(bar.h);
-    const float low = bar_value - 1e-6f * fabsf(bar_value);  // a few steps of float32 below it
+    // y + o.x differs from the key by the offset's remainder and a rounding of each
+    const float low = bar_value - (1e-6f * fabsf(bar_value) + 1.001f * fabsf(o.y));
 #pragma unroll 1
     for (int i0 = tid; i0 < n; i0 += kBeamThreads * 8) {
       float y[8];
