@@ -575,9 +575,11 @@ dec_status attn_shared_prefix(const attn_shared_args* a, void* stream);
  * lowest b * vocab + v comes first (candidates are compared in 48 bits, over a
  * float32 sum of exponentials). out_scores float32, out_parents (b) and out_tokens
  * (v) int32 [n_out]. A logit of -inf or NaN is never chosen (NaN counts as
- * masked, as in the greedy argmax); a beam whose score is not finite, whose
- * logits hold +inf, or which has no finite logit offers nothing. Slots that
- * nothing fills get parent -1, token -1 and score -inf.
+ * masked, as in the greedy argmax); a beam whose score, or score less
+ * log-sum, is not finite, whose logits hold +inf, or which has no finite logit
+ * offers nothing. A sum below the lowest finite float32 counts as that value,
+ * behind those that reach it. Slots that nothing fills get parent -1, token -1
+ * and score -inf.
  * beams 1..1024, n_out 1..1024, beams * vocab < 2^31; logits float32,
  * row b at logits + b * logits_stride. d_workspace as for
  * attn_shared_prefix. */

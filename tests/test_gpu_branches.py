@@ -614,6 +614,30 @@ def test_beam_select_sure_beams(beams, shift):
         check_select(run_select(W, logits, scores, n_out), logits, scores, n_out)
 
 
+def test_beam_select_lowest_scores():
+    """Beams at the type's lowest score, whose lowest logits overflow the sum: such a candidate counts as the lowest finite
+    score and comes behind every other."""
+    W = lib()
+    rng = np.random.default_rng(3)
+    low = np.finfo(np.float32).min
+    x = rng.standard_normal((3, 2500)).astype(np.float32)
+    x[:, 40:] = low
+    got = run_select(W, x, [low, -1.0, low], 50)
+    s, p, t = OB.beam_select(x[1:2], np.array([-1.0], dtype=np.float32), 40)
+    assert got[1][:40].tolist() == [1] * 40 and got[2][:40].tolist() == t.tolist()
+    inside(got[0][:40].astype(np.float64), s, 96 * U + U * np.abs(s), "scores")
+    assert (got[0][40:] == low).all()
+    got = run_select(W, x, [low, -1.0, low], 1000)
+    assert np.isfinite(got[0]).all() and (got[1] >= 0).all() and len(set(zip(got[1].tolist(), got[2].tolist()))) == 1000
+    x = np.full((1, 2000), low, dtype=np.float32)
+    x[0, 700] = 0.0
+    got = run_select(W, x, [low], 3)
+    assert got[2].tolist() == [700, 0, 1] and (got[0] == low).all()
+    # score and log-sum together beyond float32, on either side: nothing to offer
+    got = run_select(W, np.array([[1e38, 3e38], [low, low], [0.0, 1.0]], dtype=np.float32), [low, -low, -5.0], 6)
+    assert got[1].tolist() == [2, 2, -1, -1, -1, -1] and got[2].tolist() == [1, 0, -1, -1, -1, -1]
+
+
 # ---- reorder -------------------------------------------------------------------------------------------------------
 
 REORDER_CASES = [

@@ -16,6 +16,7 @@
 // order: T is exact, ties included, and the result does not depend on timing.
 // Measured: 4 beams x 151,936 15 us, 64 beams 26 us, of which pass 1 takes 4 and
 // 10 (3.9 TB/s) and pass 2 a chain of barriers and L2 round trips.
+#include <cfloat>
 #include <cmath>
 
 #include "common.h"
@@ -103,7 +104,8 @@ __device__ __forceinline__ float unorder32(uint32_t k) { return __uint_as_float(
 __device__ __forceinline__ uint2 key_words(float x, float2 off) {
   const float s = x + off.x, t = s - x;
   const float e = (x - (s - t)) + (off.x - t) + off.y;  // x + off.x - s exactly, then the remainder
-  const float hi = s + e, lo = e - (hi - s);
+  // below the lowest finite value: that value, behind those that reach it (fmaxf drops a NaN)
+  const float hi = fmaxf(s + e, -FLT_MAX), lo = fmaxf(e - (hi - s), -INFINITY);
   return make_uint2(order32(hi), order32(lo));
 }
 
@@ -370,7 +372,8 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
     for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (b < a.beams && (tid & (lanes - 1)) == 0) {
       const float sc = off[b].x;
-      off[b] = finite && isfinite(sc) ? row_offset(sc, m, s) : make_float2(-INFINITY, 0.f);
+      const float2 o = finite && isfinite(sc) ? row_offset(sc, m, s) : make_float2(-INFINITY, 0.f);
+      off[b] = isfinite(o.x) ? o : make_float2(-INFINITY, 0.f);
     }
   }
   __syncthreads();
