@@ -25,7 +25,7 @@
 // and leave no room for a CTA of the branches' own keys beside this one.
 //
 // Every wait is bounded; on a timeout the CTA records ERR_TC_TIMEOUT, stops,
-// waits for its issued MMAs and frees its tensor memory.
+// waits for its issued MMAs and copies and frees its tensor memory.
 #pragma once
 #include "attn_mma.cuh"
 #include "tc_attn_util.cuh"
@@ -161,6 +161,7 @@ __global__ void __maxnreg__(120)
 
   if (warp == 0) {
     if (lane == 0) {
+      int nk = min(kApStages, T), nv = nk;  // tiles requested
       for (int j = kApStages; j < T && !*vfail; ++j) {
         const int s = j % kApStages, y = k0 + j * kApKeys;
         if (!mbar_wait(&k_empty[s], ((j / kApStages) - 1) & 1)) {
@@ -171,6 +172,7 @@ __global__ void __maxnreg__(120)
         mbar_arrive_expect_tx(&k_full[s], kApTile);
         tma_load_3d_map(kd, &kmap, 0, y, g, &k_full[s]);
         tma_load_3d_map(kd + kApBox, &kmap, 64, y, g, &k_full[s]);
+        nk = j + 1;
         if (!mbar_wait(&v_empty[s], ((j / kApStages) - 1) & 1)) {
           fail();
           break;
@@ -178,6 +180,12 @@ __global__ void __maxnreg__(120)
         mbar_arrive_expect_tx(&v_full[s], kApTile);
         tma_load_3d_map(vd, &vmap, 0, y, g, &v_full[s]);
         tma_load_3d_map(vd + kApBox, &vmap, 64, y, g, &v_full[s]);
+        nv = j + 1;
+      }
+      // the last copies into each stage have landed before the CTA may end, after a failure too
+      for (int s = 0; s < kApStages; ++s) {
+        if (s < nk && !mbar_wait(&k_full[s], ((nk - 1 - s) / kApStages) & 1)) fail();
+        if (s < nv && !mbar_wait(&v_full[s], ((nv - 1 - s) / kApStages) & 1)) fail();
       }
     }
   } else if (warp == 1) {
