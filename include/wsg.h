@@ -502,7 +502,7 @@ dec_status qk_norm_rope(const qk_rope_args* a, void* stream);
  * belongs to sequence r. A padded row (positions[r] < 0) stores nothing and
  * leaves its q_out as it was. A seq[r] outside [0, n_seq) or an index outside
  * the table's width counts as a bad page; the row's q_out is still written.
- * Two rows at the same index of one sequence leave either one's values. */
+ * Two rows at the same index of one sequence leave a mixture of both there. */
 typedef struct {
   int32_t rows, n_q, n_kv, head_dim; /* n_q may be 0 */
   int32_t xdtype, ydtype, kvdtype;   /* q, k, v; q_out; pages */
@@ -536,10 +536,12 @@ dec_status kv_append_paged(const kv_append_args* a, void* stream);
  * unused slot, whose out and lse are left as they were. A branch with nothing
  * to attend to gets zeros (and lse -inf). lse (nullable, float32
  * [batch][n_q]) receives the natural log of the softmax's denominator.
- * n_q / n_kv <= 16, batch * n_q < 2^24. A key or value that is not finite and
- * attended to makes its rows not finite (a NaN or an infinity). Scores, softmax sums and outputs are accumulated in
- * float32; with DEC_BF16 q and out the result is rounded once to bfloat16. The
- * result does not depend on timing (partial results join in a fixed order).
+ * n_q / n_kv <= 16, batch * n_q < 2^24, prefix_len + table_stride * page_size
+ * <= 2^30. A key or value that is not finite and attended to makes its rows
+ * not finite, except that a score of -inf may have weight 0. Scores, softmax
+ * sums and outputs are accumulated in float32; with DEC_BF16 q and out the
+ * result is rounded once to bfloat16. The result does not depend on timing
+ * (partial results join in a fixed order).
  * A bounded wait that gave up (a broken launch) sets DEC_DEVERR_GEMM_TIMEOUT in
  * the context-free error word. d_workspace: attn_shared_prefix_workspace(a)
  * bytes for these sizes, 256-byte aligned. */

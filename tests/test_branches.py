@@ -212,7 +212,8 @@ BAD = {
         {"batch": -1}, {"batch": 65536}, {"batch": 4096, "n_q": 4096, "n_kv": 4096, "out_stride": 1 << 20}, {"n_q": 3}, {"n_q": 0}, {"n_kv": 0}, {"n_q": 34, "n_kv": 2}, {"qdtype": 2},
         {"kvdtype": 2}, {"q": None}, {"out": None}, {"seq_len": None}, {"prefix_k": None}, {"prefix_v": None},
         {"prefix_len": -1}, {"prefix_stride": 7}, {"page_table": None}, {"out_stride": 63}, {"q_stride": -1},
-        {"table_stride": -1}, {"table_stride": 1 << 30}, {"prefix_k": P + 4}, {"d_workspace": None},
+        {"table_stride": -1}, {"table_stride": 1 << 30},
+        {"prefix_len": (1 << 30) - 31, "prefix_stride": 1 << 30}, {"prefix_k": P + 4}, {"d_workspace": None},
         {"d_workspace": P + 16}],
     "beam_select": [{"beams": 0}, {"beams": 1025}, {"vocab": 0}, {"n_out": 0}, {"n_out": 1025},
                     {"beams": 1024, "vocab": 1 << 21, "logits_stride": 1 << 21}, {"logits": None}, {"scores": None},
@@ -221,7 +222,8 @@ BAD = {
     "beam_reorder_pages": HEADS + PAGES + [
         {"beams": -1}, {"layers": 0}, {"layers": 65536}, {"n_kv": 0}, {"kvdtype": 2}, {"table_stride": 0},
         {"layer_stride": -1024}, {"layer_stride": 1025}, {"parents": None}, {"spare": None}, {"old_table": None},
-        {"old_len": None}, {"new_table": None}, {"new_len": None}, {"new_table": P}, {"new_len": P}],
+        {"old_len": None}, {"new_table": None}, {"new_len": None}, {"new_table": P}, {"new_len": P},
+        {"new_table": P + 28}, {"new_table": P - 28}, {"new_len": P + 12}, {"n_kv": 16385}],
 }
 
 

@@ -19,7 +19,7 @@ inline bool attn_sizes_ok(const attn_shared_args* a) {
          a->n_q % a->n_kv == 0 && a->n_q / a->n_kv <= 16 && a->head_dim >= 8 && a->head_dim <= 128 &&
          a->head_dim % 8 == 0 && type(a->qdtype) && type(a->kvdtype) && a->prefix_len >= 0 &&
          page_shift(a->page_size) >= 0 && a->num_pages >= 0 && a->table_stride >= 0 &&
-         (static_cast<long long>(a->table_stride) << page_shift(a->page_size)) + a->prefix_len < (1ll << 31);
+         (static_cast<long long>(a->table_stride) << page_shift(a->page_size)) + a->prefix_len <= (1ll << 30);
 }
 
 // How a call is cut up.

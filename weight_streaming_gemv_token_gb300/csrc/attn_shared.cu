@@ -173,8 +173,9 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   if (a->workspace_bytes < p.total)
     return fail(nullptr, DEC_ENOMEM, "attn_shared_prefix: workspace has %zu bytes, %zu needed", a->workspace_bytes,
                 p.total);
-  if (p.prefix_items + p.own_items >= 1ll << 31)
-    return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: %lld work items", p.prefix_items + p.own_items);
+  if (p.prefix_items + p.own_items >= 1ll << 31 || p.own_per >= 1ll << 31)
+    return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: %lld work items of %lld blocks",
+                p.prefix_items + p.own_items, p.own_per);
   char* w = static_cast<char*>(a->d_workspace);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   AmArgs k{};

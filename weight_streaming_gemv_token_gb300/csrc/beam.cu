@@ -678,7 +678,7 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
 extern "C" dec_status beam_reorder_pages(const beam_reorder_args* a, void* stream) {
   if (!a) return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: NULL arguments");
   const int shift = page_shift(a->page_size);
-  if (a->beams < 0 || a->layers < 1 || a->layers > 65535 || a->n_kv < 1 || a->head_dim < 8 || a->head_dim > 128 ||
+  if (a->beams < 0 || a->layers < 1 || a->layers > 65535 || a->n_kv < 1 || a->n_kv > 16384 || a->head_dim < 8 || a->head_dim > 128 ||
       a->head_dim % 8 || (a->kvdtype != DEC_F32 && a->kvdtype != DEC_BF16) || shift < 0 || a->num_pages < 0 ||
       a->table_stride < 1 || a->layer_stride < 0)
     return fail(nullptr, DEC_EINVAL,
@@ -691,8 +691,13 @@ extern "C" dec_status beam_reorder_pages(const beam_reorder_args* a, void* strea
   const int elem = a->kvdtype == DEC_F32 ? 4 : 2;
   if (!aligned16(a->k_pages) || !aligned16(a->v_pages) || a->layer_stride * elem % 16)
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the pools must be 16-byte aligned in every layer");
-  if (a->new_table == a->old_table || a->new_len == a->old_len)
-    return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the new table and lengths must be other buffers than the old");
+  auto overlap = [](const int32_t* x, const int32_t* y, size_t n) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x), q = reinterpret_cast<uintptr_t>(y);
+    return (p < q ? q - p : p - q) < 4 * n;
+  };
+  const size_t beams = a->beams;
+  if (overlap(a->new_table, a->old_table, beams * a->table_stride) || overlap(a->new_len, a->old_len, beams))
+    return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the new table and lengths must not overlap the old");
   DeviceInfo di;
   const dec_status st = device_info(&di, nullptr);
   if (st != DEC_OK) return st;
