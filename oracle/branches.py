@@ -53,8 +53,7 @@ def beam_select(logits, scores, n_out):
         m = np.max(x[b])
         if not np.isfinite(m) or not np.isfinite(scores[b]):
             continue
-        lse = m + np.log(np.sum(np.exp(x[b] - m)))
-        key = float(scores[b]) + (x[b] - lse)
+        key = float(scores[b]) + ((x[b] - m) - np.log(np.sum(np.exp(x[b] - m))))  # (m first: it may be the lowest float)
         v = np.flatnonzero(x[b] > -np.inf)
         v = v[np.argsort(-key[v], kind="stable")][:n_out]
         cand += [(-key[t], b, int(t)) for t in v]

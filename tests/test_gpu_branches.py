@@ -633,6 +633,10 @@ def test_beam_select_lowest_scores():
     x[0, 700] = 0.0
     got = run_select(W, x, [low], 3)
     assert got[2].tolist() == [700, 0, 1] and (got[0] == low).all()
+    # rows of nothing but the lowest value are even distributions, whatever its size
+    x = np.full((3, 5), low, dtype=np.float32)
+    x[2, 3] = 0.0
+    check_select(run_select(W, x, [-2.0, -1.5, -4.0], 11), x, [-2.0, -1.5, -4.0], 11)
     # score and log-sum together beyond float32, on either side: nothing to offer
     got = run_select(W, np.array([[1e38, 3e38], [low, low], [0.0, 1.0]], dtype=np.float32), [low, -low, -5.0], 6)
     assert got[1].tolist() == [2, 2, -1, -1, -1, -1] and got[2].tolist() == [1, 0, -1, -1, -1, -1]
