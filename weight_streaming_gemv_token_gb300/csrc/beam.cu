@@ -14,7 +14,7 @@
 //           listed ones to n_out in the same way and ranks them.
 // Candidates are ordered by (key descending, flat index ascending), a total
 // order: T is exact, ties included, and the result does not depend on timing.
-// Measured: 4 beams x 151,936 15 us, 64 beams 26 us, of which pass 1 takes 4 and
+// Measured: 4 beams x 151,936 12 us, 64 beams 23 us, of which pass 1 takes 4 and
 // 10 (3.9 TB/s) and pass 2 a chain of barriers and L2 round trips.
 #include <cfloat>
 #include <cmath>
@@ -667,6 +667,10 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
   static bool lifted[64] = {};
   if (!lifted[di.device]) {
     WSG_CUDA_TRY(nullptr, cudaFuncSetAttribute(beam_pick_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBeamSmem));
+    // A CTA of pass 2 takes its place beside those of pass 1 only where the SM's
+    // shared memory is split for both (without: 15 and 26 us for 4 and 64 beams, with 12 and 23)
+    WSG_CUDA_TRY(nullptr, allow_smem_shared(beam_chunks_kernel, 0));
+    WSG_CUDA_TRY(nullptr, allow_smem_shared(beam_pick_kernel, 0));
     lifted[di.device] = true;
   }
   const int grid = L.chunks < kChunkCtas * di.sms ? L.chunks : kChunkCtas * di.sms;
