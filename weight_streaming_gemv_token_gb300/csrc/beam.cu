@@ -11,11 +11,14 @@
 //           the at most n_out chunks whose maximum reaches T hold selected ones. CTA i
 //           re-reads the i-th of them (from L2) and lists the candidates that
 //           reach T; the last CTA to finish narrows the
-//           listed ones to n_out in the same way and ranks them.
+//           listed ones to n_out in the same way, where they are many, and ranks them.
 // Candidates are ordered by (key descending, flat index ascending), a total
 // order: T is exact, ties included, and the result does not depend on timing.
 // Measured: 4 beams x 151,936 12 us, 64 beams 23 us, of which pass 1 takes 4 and
 // 10 (3.9 TB/s) and pass 2 a chain of barriers and L2 round trips.
+// Many candidates at the bar (equal or sorted logits, fewer chunks than outputs) are
+// narrowed by that one CTA: 4 beams of 151,936 equal logits, 64 outputs 490 us; sorted
+// ones 110.
 #include <cfloat>
 #include <cmath>
 
@@ -28,8 +31,8 @@ namespace {
 
 constexpr int kChunkThreads = 256, kBeamThreads = 512;
 constexpr int kChunkCtas = 4;  // CTAs of pass 1 an SM: registers and threads for one of pass 2 remain
-constexpr int kBeamChunksMax = 2048;  // chunks of one call (all rows)
-constexpr int kBeamChunkMin = 1024;
+constexpr int kBeamChunksMax = 4096;  // chunks of one call (all rows)
+constexpr int kBeamChunkMin = 128, kBeamChunkUsual = 1024;
 constexpr int kBeamGather = 4096;  // candidates held in shared memory
 constexpr int kBeamRank = 512;     // candidates ranked against each other without narrowing
 constexpr int kBeamsMax = 1024, kBeamOutMax = 1024;
@@ -45,9 +48,15 @@ struct BeamLayout {
 
 BeamLayout beam_layout(int beams, int vocab, int n_out) {
   BeamLayout L{};
-  // the smallest power of two within the bound on the number of chunks
-  long long c = kBeamChunkMin;
-  while (static_cast<long long>(beams) * ((vocab + c - 1) / c) > kBeamChunksMax) c *= 2;
+  // The smallest power of two within the bound on the number of chunks, 2,048 for few
+  // outputs (every CTA of pass 2 looks at each). Smaller chunks where they are fewer
+  // than four times the outputs: the n_out-th best chunk would bound little (4 beams
+  // x 151,936, 1,024 outputs: 1,330 us with chunks of 1,024, 91 with 256; 8 outputs: 12).
+  const int most = n_out > 256 ? kBeamChunksMax : kBeamChunksMax / 2;
+  auto chunks = [&](long long size) { return beams * ((vocab + size - 1) / size); };
+  long long c = kBeamChunkUsual;
+  while (chunks(c) > most) c *= 2;
+  while (c > kBeamChunkMin && chunks(c) < 4ll * n_out && chunks(c / 2) <= most) c /= 2;
   L.chunk = static_cast<int>(c);
   L.per_row = static_cast<int>((vocab + c - 1) / c);
   L.chunks = L.per_row * beams;
@@ -216,7 +225,7 @@ __device__ __forceinline__ uint32_t block_sum(uint32_t v, uint32_t (*red)[kBeamT
 }
 
 // Candidates to choose from: n of them in shared memory (a high word of 0 is none;
-// the places up to the next multiple of 4 kBeamThreads hold 0), or (h NULL) the
+// the places up to the next multiple of 4 kBeamThreads hold 0), or (LISTS below) the
 // lists of all CTAs in the workspace.
 struct BeamSource {
   const uint32_t *h, *l, *f;
@@ -224,9 +233,9 @@ struct BeamSource {
 };
 
 // fn(high word, place) of each candidate; places in the lists count through them.
-template <typename Fn>
+template <bool LISTS, typename Fn>
 __device__ __forceinline__ void for_high(const BeamArgs& a, const BeamSource& s, Fn fn) {
-  if (s.h) {
+  if constexpr (!LISTS) {
 #pragma unroll 1
     for (int i0 = threadIdx.x; i0 < s.n; i0 += 4 * kBeamThreads) {
       uint32_t k[4];
@@ -236,13 +245,19 @@ __device__ __forceinline__ void for_high(const BeamArgs& a, const BeamSource& s,
       for (int e = 0; e < 4; ++e) fn(k[e], static_cast<size_t>(i0 + e * kBeamThreads));
     }
   } else {
+    int per = 1;  // threads a list
+    while (per < 32 && a.slots * per * 2 <= kBeamThreads) per *= 2;
 #pragma unroll 1
-    for (int q = threadIdx.x >> 2; q < a.slots; q += kBeamThreads / 4) {  // four threads a list
+    for (int q = threadIdx.x / per; q < a.slots; q += kBeamThreads / per) {
       const uint32_t n = __ldcg(a.count + q);
+      const size_t p0 = static_cast<size_t>(q) * a.list;
 #pragma unroll 1
-      for (uint32_t i = threadIdx.x & 3; i < n; i += 4) {
-        const size_t p = static_cast<size_t>(q) * a.list + i;
-        fn(__ldcg(a.key + p).x, p);
+      for (uint32_t i0 = threadIdx.x & (per - 1); i0 < n; i0 += 8 * per) {
+        uint32_t k[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) k[e] = i0 + e * per < n ? __ldcg(a.key + p0 + i0 + e * per).x : 0;  // 0: none
+#pragma unroll
+        for (int e = 0; e < 8; ++e) fn(k[e], p0 + i0 + e * per);
       }
     }
   }
@@ -253,22 +268,43 @@ struct BeamScratch {
   uint32_t hist[256], red[2][kBeamThreads / 32], found[3];
 };
 
+// One more in a bin of the histogram. Lanes that share the first one's bin (equal
+// logits) add together.
+__device__ __forceinline__ void count_in(uint32_t* hist, uint32_t bin) {
+  const uint32_t here = __activemask(), lead = __ffs(here) - 1;
+  const bool same = __shfl_sync(here, bin, lead) == bin;
+  const uint32_t all = __ballot_sync(here, same);
+  if (!same || (threadIdx.x & 31) == lead) atomicAdd(hist + bin, same ? __popc(all) : 1u);
+}
+
 // The bar that exactly `want` of the source's (more than want) candidates reach.
-// Histograms of the high words over ever narrower ranges, 256 bins each, from
-// [lo, hi], which holds them all; where equal high words straddle the bar,
-// bisection over their low words and indices.
+// Histograms of 256 bins over ever narrower ranges: of the high words from [lo, hi],
+// which holds them all; where equal ones straddle the bar, of their low words,
+// then of their inverted indices.
+template <bool LISTS>
 __device__ __noinline__ BeamBar narrow(const BeamArgs& a, const BeamSource& s, uint32_t want, uint32_t lo, uint32_t hi,
                                        BeamScratch* x) {
   const int tid = threadIdx.x;
   uint32_t above = 0;  // candidates over hi
+  uint32_t high = 0, low = 0;
+  int level = 0;
 #pragma unroll 1
-  while (true) {
+  for (int pass = 0; pass < 12; ++pass) {  // at most four of 8 bits for each word
     const int bits = 32 - __clz(hi - lo), shift = bits > 8 ? bits - 8 : 0;
     __syncthreads();
     if (tid < 256) x->hist[tid] = 0;
     __syncthreads();
-    for_high(a, s, [&](uint32_t h, size_t) {
-      if ((h >= lo) & (h <= hi)) atomicAdd(&x->hist[(h - lo) >> shift], 1u);
+    for_high<LISTS>(a, s, [&](uint32_t h, size_t p) {
+      uint32_t w = h;
+      if (h == 0 || (level > 0 && h != high)) return;
+      if (level > 0) {
+        w = LISTS ? __ldcg(a.key + p).y : s.l[p];
+        if (level > 1) {
+          if (w != low) return;
+          w = ~(LISTS ? __ldcg(a.flat + p) : s.f[p]);
+        }
+      }
+      if ((w >= lo) & (w <= hi)) count_in(x->hist, (w - lo) >> shift);
     });
     __syncthreads();
     if (tid < 32) {
@@ -292,37 +328,24 @@ __device__ __noinline__ BeamBar narrow(const BeamArgs& a, const BeamSource& s, u
     __syncthreads();
     lo += x->found[0] << shift;
     above = x->found[1];
-    if (above + x->found[2] == want) return BeamBar{lo, 0, 0xffffffffu};
-    if (shift == 0) break;
-    hi = min(hi, lo + ((1u << shift) - 1u));
+    if (above + x->found[2] == want) break;
+    if (shift > 0) {
+      hi = lo + min(hi - lo, (1u << shift) - 1u);
+    } else {  // (indices differ: this ends at level 2 at the latest)
+      if (level++ == 0) high = lo; else low = lo;
+      lo = 0;
+      hi = 0xffffffffu;
+      if (level == 2) lo = ~static_cast<uint32_t>(static_cast<uint32_t>(a.beams) * a.vocab - 1u);
+    }
   }
-  // want - above of the candidates with high word lo: the smallest composite
-  // (inverted low word, index) that so many do not pass
-  unsigned long long c0 = 0, c1 = ~0ull;
-  int turn = 0;
-  __syncthreads();
-#pragma unroll 1
-  while (c0 < c1) {
-    const unsigned long long mid = c0 + (c1 - c0) / 2;
-    uint32_t n = 0;
-    for_high(a, s, [&](uint32_t h, size_t p) {
-      if (h == lo) {
-        const uint32_t l = s.h ? s.l[p] : __ldcg(a.key + p).y, f = s.h ? s.f[p] : __ldcg(a.flat + p);
-        n += (static_cast<unsigned long long>(~l) << 32 | f) <= mid;
-      }
-    });
-    if (block_sum(n, x->red, turn++) >= want - above)
-      c1 = mid;
-    else
-      c0 = mid + 1;
-  }
-  return BeamBar{lo, ~static_cast<uint32_t>(c1 >> 32), static_cast<uint32_t>(c1)};
+  return level == 0 ? BeamBar{lo, 0, 0xffffffffu} : level == 1 ? BeamBar{high, lo, 0xffffffffu} : BeamBar{high, low, ~lo};
 }
 
 // Pass 2. Dynamic shared memory: key words and flat indices of the chunks' maxima
 // (the words' places hold the maxima and sums first), later of the candidates.
-// Short loops rather than unrolled code: what runs once waits for its fetch.
-__global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs a) {
+// Short loops rather than unrolled code: what runs once waits for its fetch. The
+// registers of a third of an SM: it waits beside kChunkCtas CTAs of pass 1.
+__global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamArgs a) {
   extern __shared__ __align__(16) unsigned char beam_raw[];
   uint32_t* sh = reinterpret_cast<uint32_t*>(beam_raw);
   uint32_t *sl = sh + kBeamGather, *sf = sl + kBeamGather;
@@ -401,7 +424,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
   // the bar: the n_out-th best of the keys
   BeamBar bar{1, 0, 0xffffffffu};  // reached by every key
   const uint32_t want = a.n_out;
-  if (n_all > want) bar = narrow(a, BeamSource{sh, sl, sf, a.chunks}, want, s_lo, s_hi, &scratch);
+  if (n_all > want) bar = narrow<false>(a, BeamSource{sh, sl, sf, a.chunks}, want, s_lo, s_hi, &scratch);
 
   // the blockIdx.x-th chunk that reaches the bar, in the order of the chunks: a warp
   // counts those of its range, and the one that holds it finds it
@@ -425,7 +448,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
     }
   }
   __syncthreads();
-  const uint32_t mine = s_mine;
+  const uint32_t mine = s_mine, key_lo = bar.h;
   const size_t base = static_cast<size_t>(blockIdx.x) * a.list;
   if (mine != 0xffffffffu) {
     const int b = static_cast<int>((mine * a.row_inv) >> 32), v0 = (mine - b * a.per_row) * a.chunk,
@@ -437,17 +460,26 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
     // y + o.x differs from the key by the offset's remainder and a rounding of each
     const float low = bar_value - (1e-6f * fabsf(bar_value) + 1.001f * fabsf(o.y));
 #pragma unroll 1
-    for (int i0 = tid; i0 < n; i0 += kBeamThreads * 8) {
-      float y[8];
+    for (int i0 = tid * 4; i0 < n; i0 += kBeamThreads * 16) {
+      float y[16];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = i0 + e * kBeamThreads < n ? masked(x[i0 + e * kBeamThreads]) : -INFINITY;
-      uint32_t near = 0;  // those that are not masked and not clearly below the bar
+      for (int q = 0; q < 4; ++q) {
+        const int i = i0 + q * kBeamThreads * 4;
+        if (a.vec && i + 4 <= n) {
+          const float4 f = *reinterpret_cast<const float4*>(x + i);
+          y[4 * q] = f.x, y[4 * q + 1] = f.y, y[4 * q + 2] = f.z, y[4 * q + 3] = f.w;
+        } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
+          for (int e = 0; e < 4; ++e) y[4 * q + e] = i + e < n ? x[i + e] : -INFINITY;
+        }
+      }
+      uint32_t near = 0;  // those that are not masked (a NaN is not) and not clearly below the bar
+#pragma unroll
+      for (int e = 0; e < 16; ++e)
         near |= static_cast<uint32_t>((y[e] > -INFINITY) & (y[e] + o.x >= low)) << e;
 #pragma unroll 1
       for (; near; near &= near - 1) {
-        const int i = i0 + (__ffs(near) - 1) * kBeamThreads;
+        const int e = __ffs(near) - 1, i = i0 + (e >> 2) * kBeamThreads * 4 + (e & 3);
         const uint2 w = key_words(x[i], o);
         if (bar.reached(w.x, w.y, f0 + i)) {
           const uint32_t p = atomicAdd(&s_n, 1u);
@@ -469,23 +501,50 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
 
   // the last CTA: rank what was listed. Up to kBeamGather candidates are held in
   // shared memory; more of them (many equal logits) are narrowed where they lie.
-  if (tid == 0) s_n = 0;
-  uint32_t listed = 0;
+  uint32_t* first = reinterpret_cast<uint32_t*>(off);  // place of each list's first candidate; later ranks
+  uint32_t* taken = first + kBeamOutMax;               // candidates of each rank
+  const int q0 = 2 * tid;
+  const uint32_t c0 = q0 < a.slots ? __ldcg(a.count + q0) : 0, c1 = q0 + 1 < a.slots ? __ldcg(a.count + q0 + 1) : 0;
+  uint32_t sum = c0 + c1;
 #pragma unroll 1
-  for (int q = tid; q < a.slots; q += kBeamThreads) listed += __ldcg(a.count + q);
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, sum, o);
+    if (lane >= o) sum += v;
+  }
+  if (lane == 31) cnt[warp] = sum;
+  if (tid == 0) s_n = 0;
+  taken[tid] = taken[tid + kBeamThreads] = 0;
   __syncthreads();
-  listed = block_sum(listed, scratch.red, 0);
-  bar = BeamBar{1, 0, 0xffffffffu};
-  if (listed > kBeamGather) bar = narrow(a, BeamSource{nullptr, nullptr, nullptr, 0}, want, 1, 0xffffffffu, &scratch);
-  for_high(a, BeamSource{nullptr, nullptr, nullptr, 0}, [&](uint32_t h, size_t p) {
-    const uint32_t l = __ldcg(a.key + p).y, f = __ldcg(a.flat + p);
-    if (bar.reached(h, l, f)) {
-      const uint32_t w = atomicAdd(&s_n, 1u);
-      sh[w] = h, sl[w] = l, sf[w] = f;
+  const uint32_t part = cnt[lane & (kWarps - 1)];
+  const uint32_t listed = __reduce_add_sync(0xffffffffu, lane < kWarps ? part : 0);
+  sum += __reduce_add_sync(0xffffffffu, lane < warp ? part : 0);
+  first[q0] = sum - c0 - c1, first[q0 + 1] = sum - c1;
+  __syncthreads();
+  uint32_t n = listed;
+  if (listed <= kBeamGather) {
+#pragma unroll 1
+    for (uint32_t i = tid; i < listed; i += kBeamThreads) {
+      int q = 0;  // the list that holds the i-th: the last that begins at or before it
+#pragma unroll 1
+      for (int step = kBeamOutMax / 2; step > 0; step >>= 1)
+        if (q + step < a.slots && first[q + step] <= i) q += step;
+      const size_t p = static_cast<size_t>(q) * a.list + (i - first[q]);
+      const uint2 w = __ldcg(a.key + p);
+      sf[i] = __ldcg(a.flat + p);
+      sh[i] = w.x, sl[i] = w.y;
     }
-  });
-  __syncthreads();
-  uint32_t n = s_n;
+  } else {
+    bar = narrow<true>(a, BeamSource{}, want, key_lo, 0xffffffffu, &scratch);
+    for_high<true>(a, BeamSource{}, [&](uint32_t h, size_t p) {
+      const uint32_t l = __ldcg(a.key + p).y, f = __ldcg(a.flat + p);
+      if (bar.reached(h, l, f)) {
+        const uint32_t w = atomicAdd(&s_n, 1u);
+        if (w < kBeamGather) sh[w] = h, sl[w] = l, sf[w] = f;
+      }
+    });
+    __syncthreads();
+    n = min(s_n, want);
+  }
   auto fill = [&]() {  // zeros behind the candidates
 #pragma unroll 1
     for (int i = n + tid; i < pad(n); i += kBeamThreads) sh[i] = 0;
@@ -494,7 +553,7 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
   fill();
   if (n > want && n > kBeamRank) {
     // too many to rank against each other: the n_out best, by way of the first lists' places
-    bar = narrow(a, BeamSource{sh, sl, sf, static_cast<int>(n)}, want, 1, 0xffffffffu, &scratch);
+    bar = narrow<false>(a, BeamSource{sh, sl, sf, static_cast<int>(n)}, want, key_lo, 0xffffffffu, &scratch);
     if (tid == 0) s_n = 0;
     __syncthreads();
 #pragma unroll 1
@@ -505,40 +564,45 @@ __global__ void __launch_bounds__(kBeamThreads) beam_pick_kernel(const BeamArgs 
         a.flat[w] = sf[i];
       }
     __syncthreads();
-    n = s_n;
+    n = min(s_n, want);
 #pragma unroll 1
     for (uint32_t i = tid; i < n; i += kBeamThreads) sh[i] = a.key[i].x, sl[i] = a.key[i].y, sf[i] = a.flat[i];
     fill();
   }
-  // ranks by counting the better ones, `split` threads a candidate: the high words
-  // four at a time; candidates that share theirs compare the rest
+  // ranks by counting the better ones by their high words, four at a time, `split`
+  // threads a candidate; candidates that came to one rank share theirs and compare
+  // the rest (n <= kBeamOutMax here)
   int lg = 0;
   while (lg < 5 && (n << (lg + 1)) <= kBeamThreads) ++lg;
   const int split = 1 << lg;
 #pragma unroll 1
   for (uint32_t i0 = 0; i0 < n; i0 += kBeamThreads >> lg) {
     const uint32_t i = i0 + (tid >> lg), h = i < n ? sh[i] : 0xffffffffu;
-    uint32_t rank = 0, same = 0;
+    uint32_t rank = 0;
 #pragma unroll 4
     for (uint32_t j = (tid & (split - 1)) * 4; j < n; j += split * 4) {
       const uint4 k = *reinterpret_cast<const uint4*>(sh + j);
       rank += (k.x > h) + (k.y > h) + (k.z > h) + (k.w > h);
-      same += (k.x == h) + (k.y == h) + (k.z == h) + (k.w == h);
     }
 #pragma unroll 1
-    for (int o = split / 2; o > 0; o >>= 1) {
-      rank += __shfl_xor_sync(0xffffffffu, rank, o);
-      same += __shfl_xor_sync(0xffffffffu, same, o);
-    }
+    for (int o = split / 2; o > 0; o >>= 1) rank += __shfl_xor_sync(0xffffffffu, rank, o);
     if (i < n && (tid & (split - 1)) == 0) {
-      if (same > 1)
+      atomicAdd(&taken[rank], 1u);
+      first[i] = rank;
+    }
+  }
+  __syncthreads();
 #pragma unroll 1
-        for (uint32_t j = 0; j < n; ++j) rank += sh[j] == h && (sl[j] > sl[i] || (sl[j] == sl[i] && sf[j] < sf[i]));
-      if (rank < want) {
-        a.out_scores[rank] = unorder32(h);
-        a.out_parents[rank] = static_cast<int32_t>(sf[i] / static_cast<uint32_t>(a.vocab));
-        a.out_tokens[rank] = static_cast<int32_t>(sf[i] % static_cast<uint32_t>(a.vocab));
-      }
+  for (uint32_t i = tid; i < n; i += kBeamThreads) {
+    uint32_t rank = first[i];
+    if (taken[rank] > 1)
+#pragma unroll 4
+      for (uint32_t j = 0; j < n; ++j)
+        rank += sh[j] == sh[i] && (sl[j] > sl[i] || (sl[j] == sl[i] && sf[j] < sf[i]));
+    if (rank < want) {
+      a.out_scores[rank] = unorder32(sh[i]);
+      a.out_parents[rank] = static_cast<int32_t>(sf[i] / static_cast<uint32_t>(a.vocab));
+      a.out_tokens[rank] = static_cast<int32_t>(sf[i] % static_cast<uint32_t>(a.vocab));
     }
   }
 #pragma unroll 1
