@@ -281,3 +281,57 @@ def test_oracle_attention_joins_and_selects():
     sc, pa, to = OB.beam_select(np.zeros((2, 3)), np.array([0.0, 0.0]), 4)
     assert pa.tolist() == [0, 0, 0, 1] and to.tolist() == [0, 1, 2, 0]
     np.testing.assert_allclose(sc, -np.log(3.0))
+
+
+@pytest.fixture(scope="module")
+def walk(tmp_path_factory):
+    """csrc/beam_plan.h compiled as plain C++: every place that a CTA's threads load of a selection's lists, with the
+    places that the workspace has. Returns how many are loaded; -1: one outside the workspace, -2: one past its list's
+    count, -3: not each once, -4: another place handed on than loaded."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("walk")
+    src = d / "w.cpp"
+    src.write_text('#include "beam_plan.h"\n#include <vector>\nusing namespace wsg;\n'
+                   'extern "C" long long layout(int beams, int vocab, int n_out, long long* o) {\n'
+                   "  const BeamLayout L = beam_layout(beams, vocab, n_out);\n"
+                   "  o[0] = L.chunk, o[1] = L.per_row, o[2] = L.chunks, o[3] = L.slots, o[4] = L.list;\n"
+                   "  return (long long)L.total; }\n"
+                   'extern "C" long long walk(int beams, int vocab, int n_out, const uint32_t* count) {\n'
+                   "  const BeamLayout L = beam_layout(beams, vocab, n_out);\n"
+                   "  const size_t places = (L.total - L.flat) / 4, listed = (size_t)L.slots * L.list;\n"
+                   "  if (listed > places || L.key + 8 * listed > L.flat) return -1;\n"
+                   "  std::vector<char> seen(listed);\n  long long n = 0, bad = 0;\n"
+                   "  for (int t = 0; t < kBeamThreads; ++t)\n"
+                   "    beam_walk(L.slots, L.list, t, [&](int q) { return count[q]; },\n"
+                   "              [&](size_t p) -> uint32_t {\n"
+                   "                if (p >= listed) { bad = -1; return 0; }\n"
+                   "                if (p % L.list >= count[p / L.list]) bad = -2;\n"
+                   "                if (seen[p]++) bad = -3;\n                ++n;\n                return p * 7 + 1; },\n"
+                   "              [&](uint32_t k, size_t p) { if (k != (uint32_t)(p * 7 + 1)) bad = -4; });\n"
+                   "  return bad ? bad : n;\n}\n")
+    lib = d / "w.so"
+    inc = os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(src), "-o", str(lib)], check=True)
+    L = ctypes.CDLL(str(lib))
+    L.layout.restype = L.walk.restype = ctypes.c_longlong
+    return L
+
+
+def test_selection_reads_no_place_behind_its_lists(walk):
+    """Lists that are full and lists that are not, of lengths that no number of threads divides."""
+    rng = np.random.default_rng(0)
+    cases = [(64, 100, 64), (64, 75, 64), (1, 1, 1), (1000, 40, 1000), (4, 151936, 8), (1, 151936, 1024), (1024, 129, 1024),
+             (3, 9000, 1000), (513, 33, 700)]
+    cases += [(int(np.exp(rng.uniform(0, np.log(1024)))), int(np.exp(rng.uniform(0, np.log(9000)))),
+               int(np.exp(rng.uniform(0, np.log(1024))))) for _ in range(60)]
+    for beams, vocab, n_out in cases:
+        o = (ctypes.c_longlong * 5)()
+        walk.layout(beams, vocab, n_out, o)
+        chunk, per_row, chunks, slots, width = o
+        assert per_row * chunk >= vocab and chunks == beams * per_row <= 4096 and slots == min(n_out, chunks)
+        assert width == min(chunk, vocab)
+        for count in (np.full(slots, width), rng.integers(0, width + 1, slots), np.zeros(slots)):
+            count = np.ascontiguousarray(count, dtype=np.uint32)
+            assert walk.walk(beams, vocab, n_out, count.ctypes.data_as(ctypes.c_void_p)) == count.sum(), (beams, vocab, n_out)

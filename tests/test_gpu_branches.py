@@ -549,6 +549,22 @@ def test_beam_select(c):
     check_select(run_select(W, logits, scores, n_out), logits, scores, n_out)
 
 
+@pytest.mark.parametrize("c", [(64, 100, 64), (64, 75, 64), (64, 100, 200), (47, 129, 33), (3, 9017, 1000)], ids=str)
+@pytest.mark.parametrize("kind", ["normal", "levels", "equal"])
+def test_beam_select_lists_of_odd_lengths(c, kind):
+    """Over 4,096 listed candidates in lists whose lengths no number of threads divides, masked logits among them."""
+    W = lib()
+    beams, vocab, n_out = c
+    rng = np.random.default_rng(vocab)
+    x = {"normal": lambda: rng.standard_normal((beams, vocab)), "levels": lambda: rng.integers(0, 2, (beams, vocab)),
+         "equal": lambda: np.zeros((beams, vocab))}[kind]().astype(np.float32)
+    if kind != "equal":
+        x[rng.random((beams, vocab)) < 0.05] = -np.inf
+    if kind == "levels":
+        x[:] = x[0]  # (equal rows: their float32 sums tie as the definition's do)
+    check_select(run_select(W, x, [-1.0] * beams, n_out), x, [-1.0] * beams, n_out)
+
+
 def test_beam_select_strided_rows():
     W = lib()
     rng = np.random.default_rng(1)

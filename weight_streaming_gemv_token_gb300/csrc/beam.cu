@@ -22,6 +22,7 @@
 #include <cfloat>
 #include <cmath>
 
+#include "beam_plan.h"
 #include "common.h"
 #include "paging.h"
 #include "ptx.cuh"
@@ -29,53 +30,12 @@
 namespace wsg {
 namespace {
 
-constexpr int kChunkThreads = 256, kBeamThreads = 512;
+constexpr int kChunkThreads = 256;
 constexpr int kChunkCtas = 4;  // CTAs of pass 1 an SM: registers and threads for one of pass 2 remain
-constexpr int kBeamChunksMax = 4096;  // chunks of one call (all rows)
-constexpr int kBeamChunkMin = 128, kBeamChunkUsual = 1024;
-constexpr int kBeamGather = 4096;  // candidates held in shared memory
 constexpr int kBeamRank = 512;     // candidates ranked against each other without narrowing
 constexpr int kBeamsMax = 1024, kBeamOutMax = 1024;
 constexpr size_t kBeamSmem = 12 * kBeamGather;  // dynamic shared memory of pass 2
 static_assert(kBeamChunksMax <= kBeamGather, "the chunks' keys lie where the candidates do");
-
-// Workspace: the chunks' maxima with their sums and indices; the arrival counter; per
-// qualified chunk a count and a list of (key, flat index).
-struct BeamLayout {
-  int chunk, per_row, chunks, slots;
-  size_t part, counter, count, key, flat, total;
-};
-
-BeamLayout beam_layout(int beams, int vocab, int n_out) {
-  BeamLayout L{};
-  // The smallest power of two within the bound on the number of chunks, 2,048 for few
-  // outputs (every CTA of pass 2 looks at each). Smaller chunks where they are fewer
-  // than four times the outputs: the n_out-th best chunk would bound little (4 beams
-  // x 151,936, 1,024 outputs: 1,330 us with chunks of 1,024, 91 with 256; 8 outputs: 12).
-  const int most = n_out > 256 ? kBeamChunksMax : kBeamChunksMax / 2;
-  auto chunks = [&](long long size) { return beams * ((vocab + size - 1) / size); };
-  long long c = kBeamChunkUsual;
-  while (chunks(c) > most) c *= 2;
-  while (c > kBeamChunkMin && chunks(c) < 4ll * n_out && chunks(c / 2) <= most) c /= 2;
-  L.chunk = static_cast<int>(c);
-  L.per_row = static_cast<int>((vocab + c - 1) / c);
-  L.chunks = L.per_row * beams;
-  L.slots = n_out < L.chunks ? n_out : L.chunks;
-  size_t o = 0;
-  auto take = [&](size_t bytes) {
-    const size_t at = o;
-    o = (o + bytes + 255) / 256 * 256;
-    return at;
-  };
-  L.part = take(sizeof(float4) * L.chunks);
-  L.counter = take(4);
-  L.count = take(sizeof(uint32_t) * L.slots);
-  const size_t list = static_cast<size_t>(L.slots) * (c < vocab ? c : vocab);
-  L.key = take(sizeof(uint2) * list);
-  L.flat = take(sizeof(uint32_t) * list);
-  L.total = o;
-  return L;
-}
 
 struct BeamArgs {
   int beams, vocab, n_out, chunk, per_row, chunks, slots, list;
@@ -245,21 +205,9 @@ __device__ __forceinline__ void for_high(const BeamArgs& a, const BeamSource& s,
       for (int e = 0; e < 4; ++e) fn(k[e], static_cast<size_t>(i0 + e * kBeamThreads));
     }
   } else {
-    int per = 1;  // threads a list
-    while (per < 32 && a.slots * per * 2 <= kBeamThreads) per *= 2;
-#pragma unroll 1
-    for (int q = threadIdx.x / per; q < a.slots; q += kBeamThreads / per) {
-      const uint32_t n = __ldcg(a.count + q);
-      const size_t p0 = static_cast<size_t>(q) * a.list;
-#pragma unroll 1
-      for (uint32_t i0 = threadIdx.x & (per - 1); i0 < n; i0 += 8 * per) {
-        uint32_t k[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) k[e] = i0 + e * per < n ? __ldcg(a.key + p0 + i0 + e * per).x : 0;  // 0: none
-#pragma unroll
-        for (int e = 0; e < 8; ++e) fn(k[e], p0 + i0 + e * per);
-      }
-    }
+    beam_walk(
+        a.slots, a.list, threadIdx.x, [&](int q) { return __ldcg(a.count + q); },
+        [&](size_t p) { return __ldcg(a.key + p).x; }, fn);
   }
 }
 
@@ -536,6 +484,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
   } else {
     bar = narrow<true>(a, BeamSource{}, want, key_lo, 0xffffffffu, &scratch);
     for_high<true>(a, BeamSource{}, [&](uint32_t h, size_t p) {
+      if (h < bar.h) return;
       const uint32_t l = __ldcg(a.key + p).y, f = __ldcg(a.flat + p);
       if (bar.reached(h, l, f)) {
         const uint32_t w = atomicAdd(&s_n, 1u);
@@ -711,7 +660,7 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
   k.per_row = L.per_row;
   k.chunks = L.chunks;
   k.slots = L.slots;
-  k.list = L.chunk < a->vocab ? L.chunk : a->vocab;
+  k.list = L.list;
   k.logits = a->logits;
   k.stride = a->logits_stride;
   k.scores = a->scores;
