@@ -144,6 +144,26 @@ def test_attention_plans_cover_every_key_once(W, plan):
             assert (last - first < p["own_slots"]).all()
 
 
+def test_attention_plan_of_an_empty_call(W, tmp_path):
+    """No branch is a call with nothing to do, whose workspace can be asked for like any other's. (A process of its own:
+    a division by zero would end it.)"""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no C++ compiler")
+    src = tmp_path / "e.cpp"
+    src.write_text('#include "attn_plan.h"\nint main() {\n  for (int i = 0; i < 32; ++i) {\n    attn_shared_args a{};\n'
+                   "    a.n_q = 16, a.n_kv = 8, a.head_dim = i & 1 ? 128 : 64, a.qdtype = i >> 1 & 1, a.kvdtype = i >> 2 & 1;\n"
+                   "    a.prefix_len = a.prefix_stride = i & 8 ? 512 : 0, a.page_size = 16, a.table_stride = i & 16 ? 4 : 0;\n"
+                   "    if (!wsg::attn_sizes_ok(&a)) return 1;\n    const wsg::AsPlan p = wsg::attn_plan(&a, 152);\n"
+                   "    if (p.total == 0 || p.prefix_items || p.own_items) return 2;\n  }\n  return 0;\n}\n")
+    inc = os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc")
+    # (an integer division by zero has no trap on every machine: the compiler's own check finds it there)
+    cmd = [cxx, "-std=c++17", "-O1", "-I", inc, str(src), "-o", str(tmp_path / "e")]
+    checked = ["-fsanitize=integer-divide-by-zero", "-fsanitize-undefined-trap-on-error"]
+    subprocess.run(cmd + checked, check=True)
+    assert subprocess.run([str(tmp_path / "e")]).returncode == 0
+
+
 def test_frequencies(W):
     w, f = W.rope_frequencies(128, 1e6)
     np.testing.assert_allclose(w, 1e6 ** (-np.arange(0, 128, 2) / 128), rtol=1e-14)

@@ -381,6 +381,21 @@ def test_attn_shared_prefix(c, types):
     assert torch.equal(first, t["out"])
 
 
+@pytest.mark.parametrize("types", TYPES, ids=str)
+def test_attn_shared_prefix_without_branches(types):
+    """A step in which every branch has ended: a workspace can be asked for, the call does nothing."""
+    import torch
+
+    W = lib()
+    for d, plen, width in ((128, 512, 4), (128, 0, 4), (64, 512, 0), (64, 0, 4)):
+        a, t = attn_case(W, 1, 4, 2, d, plen, [min(1, width)], 16, *types, width=width)
+        a.batch = 0
+        a.with_workspace(torch.empty(W.attn_shared_prefix_workspace(a), dtype=torch.uint8, device="cuda"))
+        W.attn_shared_prefix(a)
+        torch.cuda.synchronize()
+        assert (t["out"] == 7.0).all() and W.gemv_device_errors() == 0
+
+
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")], ids=str)
 def test_attn_shared_prefix_strides_and_no_lse(types):
     import torch

@@ -35,6 +35,8 @@ struct AsPlan {
 
 inline AsPlan attn_plan(const attn_shared_args* a, int sms) {
   AsPlan p{};
+  p.total = 256;
+  if (a->batch == 0) return p;  // an empty call: nothing to share out
   auto up = [](long long x, long long y) { return (x + y - 1) / y; };
   auto least = [](long long x, long long y) { return x < y ? x : y; };
   auto root = [](long long x) { return static_cast<long long>(std::sqrt(static_cast<double>(x))); };
