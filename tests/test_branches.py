@@ -3,6 +3,7 @@ import ctypes
 import itertools
 import math
 import os
+import re
 import shutil
 import subprocess
 
@@ -355,3 +356,11 @@ def test_selection_reads_no_place_behind_its_lists(walk):
         for count in (np.full(slots, width), rng.integers(0, width + 1, slots), np.zeros(slots)):
             count = np.ascontiguousarray(count, dtype=np.uint32)
             assert walk.walk(beams, vocab, n_out, count.ctypes.data_as(ctypes.c_void_p)) == count.sum(), (beams, vocab, n_out)
+
+
+def test_prefix_kernel_has_no_wait_without_a_limit():
+    """Warps of the tensor-core prefix kernel that wait for some others, not for the whole CTA, do so on mbarriers, whose
+    waits give up: a named barrier would keep a warp for good whose partner has given up before it."""
+    with open(os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc", "attn_prefix_tc.cuh")) as f:
+        code = "\n".join(line.split("//")[0] for line in f)
+    assert not re.search(r"\bbar(rier)?\.(cta\.)?(sync|red|arrive)|__barrier_sync|__syncthreads_", code)

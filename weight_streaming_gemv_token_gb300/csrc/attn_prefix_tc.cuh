@@ -343,10 +343,12 @@ __global__ void __maxnreg__(120)
 #pragma unroll
         for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
-      asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");  // the two warps of the lane quarter
+      // The two warps of the lane quarter. Bounded like every wait, and reached only by a
+      // warp that has given up nowhere: one whose partner has waits out the limit here.
+      ok = pair_done(T + 1);
 #pragma unroll 4
       for (int r = q * 32 + half * 16; r < q * 32 + half * 16 + 16; ++r) {
-        if (r >= nrows) break;
+        if (!ok || r >= nrows) break;
         const int row = row0 + r;
         const long long to_row = static_cast<long long>(split) * a.batch * a.n_q +
                                  static_cast<long long>(row / a.group) * a.n_q + g * a.group + row % a.group;
