@@ -751,6 +751,40 @@ def test_beam_reorder_pages_bad_indexes():
                 assert torch.equal(kp[:, p], k0[:, p])
 
 
+def test_beam_reorder_pages_bad_filled_pages():
+    """A filled page outside the pool, the first, one in the middle or the last of many, makes the slot unused in every
+    layer, whether its tail page is good or empty."""
+    import torch
+
+    W = lib()
+    page, width, beams, layers = 4, 300, 6, 3
+    pages = beams * width + beams
+    table = np.arange(beams * width, dtype=np.int32).reshape(beams, width)
+    lens = [4 * 299, 4 * 299 + 3, 4 * 290 + 1, 8, 5, 3]
+    table[0, 298], table[1, 0], table[2, 150], table[3, 1] = -1, pages, 2**31 - 1, -2**31
+    table[4, 2] = -1  # behind the tail: not needed
+    spare = beams * width + np.arange(beams)
+    pools = [rand((layers, pages, 1, page, 8), "f32", seed) for seed in (1, 2)]
+    before = [p.clone() for p in pools]
+    nt, nl = ints(np.full((beams, width), 55)), ints(np.full(beams, 55))
+    W.gemv_device_errors()
+    W.beam_reorder_pages(W.beam_reorder_args(
+        beams=beams, layers=layers, n_kv=1, head_dim=8, kvdtype=W.DEC_F32, k_pages=pools[0], v_pages=pools[1],
+        layer_stride=pools[0].stride(0), num_pages=pages, page_size=page, table_stride=width,
+        parents=ints(np.arange(beams)), spare=ints(spare), old_table=ints(table), old_len=ints(lens), new_table=nt,
+        new_len=nl))
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0x80
+    assert nl.tolist() == [-1] * 4 + lens[4:]
+    want = np.full((beams, width), -1)
+    want[4, 0], want[4, 1], want[5, 0] = table[4, 0], spare[4], spare[5]
+    np.testing.assert_array_equal(nt.cpu().numpy(), want)
+    for p, b in zip(pools, before):
+        b[:, spare[4], :, :1] = b[:, table[4, 1], :, :1]
+        b[:, spare[5], :, :3] = b[:, table[5, 0], :, :3]
+        assert torch.equal(p, b)
+
+
 # ---- together --------------------------------------------------------------------------------------------------------
 
 def test_operators_on_another_stream_and_in_a_graph():

@@ -603,7 +603,10 @@ __global__ void __launch_bounds__(kReorderThreads) beam_reorder_kernel(const Reo
       src = page_of(a.pool, row, len);
       bad = src < 0;
     }
+    const int filled = bad ? 0 : full;
+    for (int j = tid; j < filled; j += kReorderThreads) bad |= page_of(a.pool, row, static_cast<int64_t>(j) << a.pool.shift) < 0;
   }
+  bad = __syncthreads_or(bad);  // every CTA of the slot comes to the same answer
   if (bad) len = -1;
   if (first) {
     if (bad && tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
