@@ -279,6 +279,96 @@ def test_argument_blocks(W):
         W.qk_rope_args(**{**ROPE, "q": torch.zeros(4)})
 
 
+class OnDevice:
+    """A CPU tensor that says it is on the GPU (its address is never used: every call with it is refused)."""
+
+    is_cuda = True
+
+    def __init__(self, t):
+        self.t = t
+
+    def __getattr__(self, name):
+        return getattr(self.t, name)
+
+    def __getitem__(self, i):
+        return OnDevice(self.t[i])
+
+
+def test_argument_blocks_refuse_tensors_of_another_type(W):
+    """What a call would read as something else, torch's default types first: int64 indexes, float32 frequencies (half as
+    long as what is read of them), float16 for bfloat16."""
+    torch = pytest.importorskip("torch")
+
+    def t(shape, dtype):
+        return OnDevice(torch.zeros(shape, dtype=getattr(torch, dtype)))
+
+    fixed = {"int32": "positions seq page_table seq_len parents spare old_table old_len new_table new_len out_parents "
+                      "out_tokens".split(),
+             "float32": "g_q g_k lse logits scores out_scores".split(), "float64": ["inv_freq"]}
+    coded = {"q": "xdtype", "k": "xdtype", "v": "xdtype", "q_out": "ydtype", "k_out": "ydtype", "out": "qdtype",
+             "prefix_k": "kvdtype", "prefix_v": "kvdtype", "k_pages": "kvdtype", "v_pages": "kvdtype"}
+    types = ("int32", "int64", "float32", "float64", "float16", "bfloat16")
+    seen = set()
+    for call, (args, good) in CALLS.items():
+        block = getattr(W, args)
+        for name in good:
+            for want, names in fixed.items():
+                if name not in names:
+                    continue
+                seen.add(name)
+                block(**{**good, name: t(4, want)})
+                for other in set(types) - {want}:
+                    with pytest.raises(W.WsgError, match=f"{args}.{name}: the tensor is {other}") as e:
+                        block(**{**good, name: t(4, other)})
+                    assert e.value.status == 1
+            code = coded.get(name)
+            if code and call == "attn_shared_prefix" and name == "q":
+                code = "qdtype"
+            if code is None:
+                continue
+            seen.add(name)
+            for value, ok in ((0, {"float32"}), (1, {"bfloat16"})):
+                for dtype in types:
+                    kw = {**good, code: value, name: t(4, dtype)}
+                    if dtype in ok:
+                        block(**kw)
+                        continue
+                    with pytest.raises(W.WsgError, match=f"{args}.{name}: the tensor is {dtype}") as e:
+                        block(**kw)
+                    assert e.value.status == 1
+                # the same by a later change, in either order: at the call
+                a = block(**{**good, code: 1 - value})
+                a.set(name, t(4, "bfloat16" if value else "float32")).set(code, value).verify()
+                setattr(a, code, 1 - value)
+                with pytest.raises(W.WsgError, match=f"{args}.{name}: the tensor is"):
+                    getattr(W, call)(a)
+    assert seen == set(coded) | {n for names in fixed.values() for n in names}
+
+
+def test_argument_blocks_refuse_tensors_with_gaps(W):
+    """Elements that are not side by side; rows and layers may lie apart."""
+    torch = pytest.importorskip("torch")
+    i32 = dict(dtype=torch.int32)
+    wide, pool = torch.zeros((4, 8), **i32), torch.zeros((3, 2, 8, 2, 16, 16), dtype=torch.bfloat16)
+    W.kv_append_args(**{**APPEND, "page_table": OnDevice(wide[:, :2]), "k_pages": OnDevice(pool[0, 1])})
+    W.beam_reorder_args(**{**REORDER, "k_pages": OnDevice(pool[:, 1]), "old_table": OnDevice(wide[:, 4:])})
+    W.qk_rope_args(**{**ROPE, "q": OnDevice(torch.zeros(4, 200)[:, 7:71])})
+    none = torch.zeros(2, 16, 0, dtype=torch.bfloat16).transpose(1, 2)  # nothing in it, whatever its strides
+    W.attn_shared_args(**{**ATTN, "prefix_len": 0, "prefix_k": OnDevice(none), "k_pages": OnDevice(none)})
+    for call, args, change in ((W.kv_append_args, APPEND, {"page_table": wide.t()}),
+                               (W.kv_append_args, APPEND, {"positions": wide[:, 1]}),
+                               (W.kv_append_args, APPEND, {"v_pages": pool[:, 0, 0]}),
+                               (W.beam_reorder_args, REORDER, {"k_pages": pool[:, :, :, 0]}),
+                               (W.beam_reorder_args, REORDER, {"spare": wide[:, 0]}),
+                               (W.qk_rope_args, ROPE, {"q": torch.zeros(64, 4).t()}),
+                               (W.attn_shared_args, ATTN, {"seq_len": wide[:, 3]}),
+                               (W.beam_select_args, SELECT, {"logits": torch.zeros(100, 4).t()})):
+        call(**{**args, **{k: OnDevice(v.contiguous()) for k, v in change.items()}})
+        with pytest.raises(W.WsgError, match="not contiguous") as e:
+            call(**{**args, **{k: OnDevice(v) for k, v in change.items()}})
+        assert e.value.status == 1
+
+
 def test_oracle_rotation_layouts():
     """Both layouts turn each pair by its angle and leave lengths as they are; position 0 turns nothing."""
     rng = np.random.default_rng(0)

@@ -62,11 +62,22 @@ class dec_weights(ctypes.Structure):
     _fields_ = [("embed", c_void_p), ("g_final", c_void_p), ("layers", ctypes.POINTER(dec_layer_weights))]
 
 
+# Types of the tensors that an argument block takes: by DEC_* code (bfloat16 as such or as its bits) and by field.
+_ELEMENTS = {DEC_F32: ("float32",), DEC_BF16: ("bfloat16", "uint16", "int16")}
+_FIXED = {name: dtype for dtype, names in {
+    "int32": "positions seq page_table seq_len parents spare old_table old_len new_table new_len out_parents out_tokens",
+    "float32": "g_q g_k lse logits scores out_scores",
+    "float64": "inv_freq",
+}.items() for name in names.split()}
+
+
 class _Args(ctypes.Structure):
     """An argument block of the calls for several branches: fields by keyword, every one but `_optional` required.
-    Pointers may be tensors, which the block keeps alive; it can be used for any number of calls."""
+    Pointers may be tensors, which the block keeps alive; it can be used for any number of calls. A tensor must have the
+    type that its field is read in and adjacent elements within its rows (pools: within each layer's pages)."""
 
     _optional = ()
+    _typed = {}  # pointer field -> the field with the DEC_* code of its elements
 
     def __init_subclass__(cls):
         cls._kind = dict(cls._fields_)
@@ -79,19 +90,56 @@ class _Args(ctypes.Structure):
             raise TypeError(f"{type(self).__name__}: missing {', '.join(sorted(self._needed - kw.keys()))}")
         for name, value in kw.items():
             self.set(name, value)
+        self.verify()
 
     def set(self, name, value):
         """Set one field (a number, a device pointer or a tensor)."""
         kind = self._kind.get(name)
         if kind is None:
             raise TypeError(f"{type(self).__name__} has no field {name}")
-        if kind is c_void_p and value is not None:
-            if getattr(value, "is_cuda", True) is False:
-                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is not on a CUDA device")
+        if kind is c_void_p:
+            if value is not None:
+                if getattr(value, "is_cuda", True) is False:
+                    raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is not on a CUDA device")
+                self._fits(name, value)
             self._keep[name] = value
             value = _ptr(value)
         setattr(self, name, value)
         return self
+
+    def __setattr__(self, name, value):
+        super().__setattr__(name, value)
+        if name in self._kind:
+            super().__setattr__("_verified", False)
+
+    def verify(self):
+        """Refuse tensors whose type is not the one that their DEC_* field gives (by the calls after a change: fields may
+        change in any order)."""
+        for name, code in self._typed.items():
+            dtype, want = self._dtype(self._keep.get(name)), _ELEMENTS.get(getattr(self, code))
+            if dtype and want and dtype not in want:
+                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {dtype}, {code} says {want[0]}")
+        self._verified = True
+
+    @staticmethod
+    def _dtype(value):
+        return str(value.dtype).removeprefix("torch.") if hasattr(value, "dtype") else None
+
+    def _fits(self, name, value):
+        """Refuse a tensor that the call would read as something else, whatever the block's other fields."""
+        dtype = self._dtype(value)
+        if dtype is None:
+            return
+        if name in _FIXED and dtype != _FIXED[name]:
+            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {dtype}, not {_FIXED[name]}")
+        if value.numel() == 0:  # (strides of an empty tensor say nothing)
+            return
+        if name in ("k_pages", "v_pages"):
+            layer = value[0] if value.dim() == 5 else value
+            if not layer.is_contiguous():
+                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the pool is not contiguous")
+        elif value.dim() > 0 and value.shape[-1] > 1 and value.stride(-1) != 1:
+            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor's rows are not contiguous")
 
     def with_workspace(self, workspace):
         """Set the workspace to a tensor of bytes (its size too)."""
@@ -109,6 +157,7 @@ c_int64 = ctypes.c_int64
 
 
 class qk_rope_args(_Args):
+    _typed = {"q": "xdtype", "k": "xdtype", "q_out": "ydtype", "k_out": "ydtype"}
     _fields_ = ([(n, c_int32) for n in ("rows", "n_q", "n_kv", "head_dim", "xdtype", "ydtype")]
                 + [(n, c_void_p) for n in ("q", "k", "q_out", "k_out")]
                 + [(n, c_int64) for n in ("q_stride", "k_stride", "q_out_stride", "k_out_stride")]
@@ -117,6 +166,7 @@ class qk_rope_args(_Args):
 
 
 class kv_append_args(_Args):
+    _typed = {"q": "xdtype", "k": "xdtype", "v": "xdtype", "q_out": "ydtype", "k_pages": "kvdtype", "v_pages": "kvdtype"}
     _fields_ = ([(n, c_int32) for n in ("rows", "n_q", "n_kv", "head_dim", "xdtype", "ydtype", "kvdtype")]
                 + [(n, c_void_p) for n in ("q", "k", "v", "q_out")]
                 + [(n, c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
@@ -127,6 +177,8 @@ class kv_append_args(_Args):
 
 
 class attn_shared_args(_Args):
+    _typed = {"q": "qdtype", "out": "qdtype", "prefix_k": "kvdtype", "prefix_v": "kvdtype", "k_pages": "kvdtype",
+              "v_pages": "kvdtype"}
     _optional = ("lse", "d_workspace", "workspace_bytes")
     _fields_ = ([(n, c_int32) for n in ("batch", "n_q", "n_kv", "head_dim", "qdtype", "kvdtype")]
                 + [(n, c_void_p) for n in ("q", "out", "lse")]
@@ -146,6 +198,7 @@ class beam_select_args(_Args):
 
 
 class beam_reorder_args(_Args):
+    _typed = {"k_pages": "kvdtype", "v_pages": "kvdtype"}
     _fields_ = ([(n, c_int32) for n in ("beams", "layers", "n_kv", "head_dim", "kvdtype")]
                 + [("k_pages", c_void_p), ("v_pages", c_void_p), ("layer_stride", c_int64)]
                 + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
@@ -373,14 +426,20 @@ def rope_frequencies(rot_dim: int, theta: float, kind: int = ROPE_PLAIN, factor:
     return list(out), f.value
 
 
+def _verified(args: _Args) -> _Args:
+    if not args._verified:
+        args.verify()
+    return args
+
+
 def qk_norm_rope(args: qk_rope_args, stream=None):
     """Per-head RMS norm of queries and keys with the position rotation in the same pass."""
-    _check(library().qk_norm_rope(args, _stream(stream)))
+    _check(library().qk_norm_rope(_verified(args), _stream(stream)))
 
 
 def kv_append_paged(args: kv_append_args, stream=None):
     """qk_norm_rope whose keys, and the values beside them, go to a paged cache."""
-    _check(library().kv_append_paged(args, _stream(stream)))
+    _check(library().kv_append_paged(_verified(args), _stream(stream)))
 
 
 def attn_shared_prefix_workspace(args: attn_shared_args) -> int:
@@ -392,7 +451,7 @@ def attn_shared_prefix_workspace(args: attn_shared_args) -> int:
 
 def attn_shared_prefix(args: attn_shared_args, stream=None):
     """Attention of one token of each branch over the shared prefix and the branch's own pages."""
-    _check(library().attn_shared_prefix(args, _stream(stream)))
+    _check(library().attn_shared_prefix(_verified(args), _stream(stream)))
 
 
 def beam_select_workspace(args: beam_select_args) -> int:
@@ -404,9 +463,9 @@ def beam_select_workspace(args: beam_select_args) -> int:
 
 def beam_select(args: beam_select_args, stream=None):
     """The n_out best continuations over all beams and the vocabulary."""
-    _check(library().beam_select(args, _stream(stream)))
+    _check(library().beam_select(_verified(args), _stream(stream)))
 
 
 def beam_reorder_pages(args: beam_reorder_args, stream=None):
     """New page tables after a selection, and copies of the tail pages that beams must own."""
-    _check(library().beam_reorder_pages(args, _stream(stream)))
+    _check(library().beam_reorder_pages(_verified(args), _stream(stream)))
