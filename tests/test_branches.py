@@ -257,6 +257,30 @@ def test_refusals(W, call, change):
     assert call in str(e.value)
 
 
+OFF = {  # bytes of an element behind each pointer, with the codes that decide it
+    "qk_norm_rope": {"g_q": 4, "g_k": 4, "positions": 4, "inv_freq": 8, "q": "xdtype", "k": "xdtype", "q_out": "ydtype",
+                     "k_out": "ydtype"},
+    "kv_append_paged": {"g_q": 4, "g_k": 4, "positions": 4, "inv_freq": 8, "q": "xdtype", "k": "xdtype", "v": "xdtype",
+                        "q_out": "ydtype", "page_table": 4, "seq": 4},
+    "attn_shared_prefix": {"q": "qdtype", "out": "qdtype", "lse": 4, "page_table": 4, "seq_len": 4},
+    "beam_select": {"logits": 4, "scores": 4, "out_scores": 4, "out_parents": 4, "out_tokens": 4},
+    "beam_reorder_pages": {"parents": 4, "spare": 4, "old_table": 4, "old_len": 4, "new_table": 4, "new_len": 4},
+}
+
+
+@pytest.mark.parametrize("call,name", [(c, n) for c, names in OFF.items() for n in names], ids=str)
+def test_refusals_of_addresses_off_their_elements(W, call, name):
+    """An address that no element of the field's type can have: the kernel's access would fault."""
+    args, good = CALLS[call]
+    size = OFF[call][name]
+    for code, width in ((0, 4), (1, 2)) if isinstance(size, str) else ((None, size),):
+        kw = {**good, **({size: code} if code is not None else {})}
+        for off in [o for o in (1, 2, 4) if o < width]:
+            with pytest.raises(W.WsgError) as e:
+                getattr(W, call)(getattr(W, args)(**{**kw, name: 8 * P + off}))
+            assert e.value.status == 1 and call in str(e.value) and "aligned to its elements" in str(e.value)
+
+
 def test_null_arguments_and_empty_calls(W):
     lib = W.library()
     for call in CALLS:

@@ -164,6 +164,9 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
                 static_cast<long long>(a->prefix_stride));
   if (!aligned16(a->prefix_k) || !aligned16(a->prefix_v) || !aligned16(a->k_pages) || !aligned16(a->v_pages))
     return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: prefix and pools must be 16-byte aligned");
+  if (!aligned_to(elem_bytes(a->qdtype), a->q, a->out) || !aligned_to(4, a->lse, a->seq_len) ||
+      (a->table_stride > 0 && !aligned_to(4, a->page_table)))
+    return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: a pointer is not aligned to its elements");
   if (!a->d_workspace || reinterpret_cast<uintptr_t>(a->d_workspace) % 256)
     return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: workspace must be non-NULL and 256-byte aligned");
   DeviceInfo di;

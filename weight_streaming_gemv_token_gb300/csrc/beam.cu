@@ -646,6 +646,8 @@ extern "C" dec_status beam_select(const beam_select_args* a, void* stream) {
   if (a->logits_stride < 0 || (a->beams > 1 && a->logits_stride < a->vocab))
     return fail(nullptr, DEC_EINVAL, "beam_select: rows of %d logits overlap at stride %lld", a->vocab,
                 static_cast<long long>(a->logits_stride));
+  if (!aligned_to(4, a->logits, a->scores, a->out_scores, a->out_parents, a->out_tokens))
+    return fail(nullptr, DEC_EINVAL, "beam_select: a pointer is not aligned to its elements");
   if (!a->d_workspace || reinterpret_cast<uintptr_t>(a->d_workspace) % 256)
     return fail(nullptr, DEC_EINVAL, "beam_select: workspace must be non-NULL and 256-byte aligned");
   DeviceInfo di;
@@ -711,6 +713,8 @@ extern "C" dec_status beam_reorder_pages(const beam_reorder_args* a, void* strea
   const int elem = a->kvdtype == DEC_F32 ? 4 : 2;
   if (!aligned16(a->k_pages) || !aligned16(a->v_pages) || a->layer_stride * elem % 16)
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the pools must be 16-byte aligned in every layer");
+  if (!aligned_to(4, a->parents, a->spare, a->old_table, a->old_len, a->new_table, a->new_len))
+    return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: a pointer is not aligned to its elements");
   auto overlap = [](const int32_t* x, const int32_t* y, size_t n) {
     const uintptr_t p = reinterpret_cast<uintptr_t>(x), q = reinterpret_cast<uintptr_t>(y);
     return (p < q ? q - p : p - q) < 4 * n;

@@ -85,6 +85,15 @@ cudaError_t allow_smem_shared(K kern, size_t bytes) {
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
+// Whether each of the pointers (NULL too) is a multiple of `bytes`, a power of two.
+template <typename... P>
+bool aligned_to(size_t bytes, const P*... p) {
+  return ((... | reinterpret_cast<uintptr_t>(p)) & (bytes - 1)) == 0;
+}
+
+// Bytes of an element of a DEC_F32 or DEC_BF16 array.
+inline size_t elem_bytes(int dtype) { return dtype == DEC_F32 ? 4 : 2; }
+
 // Tiled TMA descriptor (CUtensorMap, 128 bytes, opaque here) of a row-major
 // [rows][cols] matrix of `elem`-byte elements (2: bfloat16, 4: float32) with
 // boxes of box_rows x box_cols; swizzle128 selects the 128-byte swizzle

@@ -442,6 +442,11 @@ dec_status check_rows(const A* a, const char* who) {
   if (!a->positions || (a->n_q > 0 && (!a->q || !a->q_out)) || (a->n_kv > 0 && !a->k) ||
       (a->rot_dim > 0 && !a->inv_freq))
     return fail(nullptr, DEC_EINVAL, "%s: NULL pointer", who);
+  if ((a->n_q > 0 && !(aligned_to(elem_bytes(a->xdtype), a->q) && aligned_to(elem_bytes(a->ydtype), a->q_out) &&
+                       aligned_to(4, a->g_q))) ||
+      (a->n_kv > 0 && !(aligned_to(elem_bytes(a->xdtype), a->k) && aligned_to(4, a->g_k))) ||
+      !aligned_to(4, a->positions) || (a->rot_dim > 0 && !aligned_to(8, a->inv_freq)))
+    return fail(nullptr, DEC_EINVAL, "%s: a pointer is not aligned to its elements", who);
   if (a->q_stride < 0 || a->k_stride < 0) return fail(nullptr, DEC_EINVAL, "%s: negative row stride", who);
   if (a->rows > 1 && a->n_q > 0 && a->q_out_stride < static_cast<long long>(a->n_q) * a->head_dim)
     return fail(nullptr, DEC_EINVAL, "%s: q_out rows overlap at stride %lld", who,
@@ -531,6 +536,8 @@ extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
   if (s != DEC_OK) return s;
   if (a->rows == 0 || a->n_q + a->n_kv == 0) return DEC_OK;
   if (a->n_kv > 0 && !a->k_out) return fail(nullptr, DEC_EINVAL, "qk_norm_rope: NULL k_out");
+  if (a->n_kv > 0 && !aligned_to(elem_bytes(a->ydtype), a->k_out))
+    return fail(nullptr, DEC_EINVAL, "qk_norm_rope: k_out is not aligned to its elements");
   if (a->rows > 1 && a->n_kv > 0 && a->k_out_stride < static_cast<long long>(a->n_kv) * a->head_dim)
     return fail(nullptr, DEC_EINVAL, "qk_norm_rope: k_out rows overlap at stride %lld",
                 static_cast<long long>(a->k_out_stride));
@@ -561,6 +568,8 @@ extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
   if (!a->v || !a->k_pages || !a->v_pages || !a->page_table) return fail(nullptr, DEC_EINVAL, "kv_append_paged: NULL pointer");
   if (!aligned16(a->k_pages) || !aligned16(a->v_pages))
     return fail(nullptr, DEC_EINVAL, "kv_append_paged: the pools must be 16-byte aligned");
+  if (!aligned_to(elem_bytes(a->xdtype), a->v) || !aligned_to(4, a->page_table, a->seq))
+    return fail(nullptr, DEC_EINVAL, "kv_append_paged: a pointer is not aligned to its elements");
   DeviceInfo di;
   if ((s = device_info(&di, nullptr)) != DEC_OK) return s;
   QkRowsArgs k = shared_fields(a);
