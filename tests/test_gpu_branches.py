@@ -464,6 +464,27 @@ def test_attn_shared_prefix_bad_pages():
     check_attn(t, 4, 4, 2, 128, 30, lens, page, "bf16", skip={(0, 1), (1, 0), (2, 2)})
 
 
+@pytest.mark.parametrize("types", TYPES, ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("plen,width,lens,bad", [
+    (30, 0, [1, 0, -1], True), (0, 0, [3, 0, -1], True), (30, 0, [0, -1, 0], False), (30, 2, [33, 32, -1], True),
+    (30, 2, [32, 5, -1], False), (30, 70, [70 * 16 + 1, 9, -1], True), (300, 70, [70 * 16, 9, 2**31 - 1], True)])
+def test_attn_shared_prefix_reports_tokens_without_a_page(types, d, plen, width, lens, bad):
+    """Tokens past the table's width are reported by every form of the call, with a table of no pages too; they are left
+    out and the others attended to."""
+    import torch
+
+    W = lib()
+    held = [min(n, 16 * width) for n in lens]
+    a, t = attn_case(W, 3, 4, 2, d, plen, held, 16, *types, width=width)
+    a.set("seq_len", ints(lens))
+    W.gemv_device_errors()
+    W.attn_shared_prefix(a)
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == (0x80 if bad else 0)
+    check_attn(t, 3, 4, 2, d, plen, held, 16, types[0])
+
+
 def test_attn_shared_prefix_reads_a_decoders_cache():
     """The prefix may be a decoder's own cache: one branch without tokens of its own, whose query repeats over the
     prefix, agrees with the definition on that cache."""

@@ -162,11 +162,8 @@ __global__ void __launch_bounds__(kAmThreads, 1) attn_f32_kernel(const AmArgs a)
     slot = a.own_slot0 + split;
     row0 = branch * a.group;
     nrows = a.group;
-    int n = a.len[branch];
-    if (n > page_capacity(a.pool)) {
-      n = static_cast<int>(page_capacity(a.pool));
-      if (split == 0 && g == 0 && tid == 0) atomicOr(a.err, ERR_BAD_PAGE);
-    }
+    // (attn_join_kernel reports a longer branch)
+    const int n = static_cast<int>(min(static_cast<int64_t>(a.len[branch]), page_capacity(a.pool)));
     k0 = split * a.own_block;
     k1 = min(n, k0 + a.own_block);
     if (k0 >= k1) return;  // attn_join_kernel knows which pieces hold keys

@@ -430,11 +430,8 @@ __global__ void __launch_bounds__(NA ? 256 : 128, NA ? 1 : 3) attn_rows_kernel(c
           if (++g == a.n_kv) g = 0, ++b, held = -1;
         }
         if (held < 0) {
-          held = max(0, a.len[b]);
-          if (held > page_capacity(a.pool)) {
-            held = static_cast<int>(page_capacity(a.pool));
-            if (lane == 0) atomicOr(a.err, ERR_BAD_PAGE);
-          }
+          // (attn_join_kernel reports a longer branch)
+          held = static_cast<int>(min(static_cast<int64_t>(max(0, a.len[b])), page_capacity(a.pool)));
         }
         const int k = static_cast<int>(at) * 16;
         if (k < held) {

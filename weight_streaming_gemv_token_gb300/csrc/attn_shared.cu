@@ -32,6 +32,7 @@ struct AmJoinArgs {
   void* out;
   long long out_stride;
   float* lse;
+  uint32_t* err;
 };
 
 // The partial results of one (branch, query head): its slots (those of the prefix,
@@ -52,6 +53,8 @@ __global__ void __launch_bounds__(128) attn_join_kernel(const AmJoinArgs a) {
   const int n = a.len[b];
   if (n < 0) return;  // (the same for the whole CTA where it works on one row)
   const long long held = n < page_capacity(a.pool) ? n : page_capacity(a.pool);
+  // (here and not by those that walk own keys: with a table of no pages there are none)
+  if (n > held && w % a.n_q == 0 && (threadIdx.x & (a.warps == 4 ? 127 : 31)) == 0) atomicOr(a.err, ERR_BAD_PAGE);
   // the pieces of the line of own blocks that this row's segment lies in
   const long long blocks = (held + a.own_block - 1) / a.own_block;
   const long long seg0 = (static_cast<long long>(b) * a.n_kv + w % a.n_q / a.group) * a.own_seg;
@@ -278,6 +281,7 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   j.out = a->out;
   j.out_stride = a->out_stride;
   j.lse = a->lse;
+  j.err = di.err;
   const int jrows = a->batch * a->n_q;
   const dim3 grid(j.warps == 4 ? jrows : (jrows + 3) / 4);
   WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_join_kernel<float>, grid, dim3(128), 0, s, true, j)
