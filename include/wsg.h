@@ -615,7 +615,7 @@ dec_status beam_select(const beam_select_args* a, void* stream);
  * for the next token (< table_stride * page_size); a longer one, a parent
  * >= beams, or a page or spare page outside the pool sets DEC_DEVERR_BAD_PAGE
  * and makes the slot unused. Layer l's pools start l * layer_stride elements
- * after k_pages and v_pages. */
+ * after k_pages and v_pages; layers must not overlap. */
 typedef struct {
   int32_t beams, layers, n_kv, head_dim, kvdtype;
   void *k_pages, *v_pages;

@@ -281,6 +281,18 @@ def test_refusals_of_addresses_off_their_elements(W, call, name):
             assert e.value.status == 1 and call in str(e.value) and "aligned to its elements" in str(e.value)
 
 
+APART = {**REORDER, "layer_stride": 8 * 2 * 16 * 16}  # layers side by side
+
+
+@pytest.mark.parametrize("change", [{"layer_stride": 0}, {"layer_stride": 8 * 2 * 16 * 16 - 8}, {"num_pages": 9},
+                                    {"kvdtype": 0, "layer_stride": 8 * 2 * 16 * 16 - 4}], ids=str)
+def test_refusals_of_layers_that_overlap(W, change):
+    """One layer's copies would be another's sources."""
+    with pytest.raises(W.WsgError, match="beam_reorder_pages: layers of") as e:
+        W.beam_reorder_pages(W.beam_reorder_args(**{**APART, **change}))
+    assert e.value.status == 1
+
+
 def test_null_arguments_and_empty_calls(W):
     lib = W.library()
     for call in CALLS:

@@ -722,6 +722,10 @@ extern "C" dec_status beam_reorder_pages(const beam_reorder_args* a, void* strea
   const size_t beams = a->beams;
   if (overlap(a->new_table, a->old_table, beams * a->table_stride) || overlap(a->new_len, a->old_len, beams))
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the new table and lengths must not overlap the old");
+  const long long layer = static_cast<long long>(a->num_pages) * a->n_kv * a->page_size * a->head_dim;
+  if (a->layers > 1 && a->layer_stride < layer)
+    return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: layers of %lld elements overlap at stride %lld", layer,
+                static_cast<long long>(a->layer_stride));
   DeviceInfo di;
   const dec_status st = device_info(&di, nullptr);
   if (st != DEC_OK) return st;
