@@ -609,9 +609,9 @@ dec_status beam_select(const beam_select_args* a, void* stream);
  * p's last, partly filled page (nothing where that is 0), in every layer; the
  * entries behind are -1, and new_len[i] = old_len[p]. So each beam owns the
  * page its next token goes to. The spare pages must differ from each other and
- * from every page of the old tables; old and new tables and lengths must not
- * overlap. parents[i] < 0, or a parent that is itself unused (old_len < 0),
- * makes slot i unused: new_len -1 and a row of -1. old_len[p] must leave room
+ * from every page of the old tables; the new table and lengths must not
+ * overlap each other nor any input. parents[i] < 0, or a parent that is itself
+ * unused (old_len < 0), makes slot i unused: new_len -1 and a row of -1. old_len[p] must leave room
  * for the next token (< table_stride * page_size); a longer one, a parent
  * >= beams, or a page or spare page outside the pool sets DEC_DEVERR_BAD_PAGE
  * and makes the slot unused. Layer l's pools start l * layer_stride elements

@@ -293,6 +293,21 @@ def test_refusals_of_layers_that_overlap(W, change):
     assert e.value.status == 1
 
 
+@pytest.mark.parametrize("change", [{"new_len": "parents"}, {"new_len": "spare"}, {"new_len": "old_table"},
+                                    {"new_len": "new_table"}, {"new_table": "parents"}, {"new_table": "spare"},
+                                    {"new_table": "old_len"}], ids=str)
+def test_refusals_of_outputs_over_inputs(W, change):
+    """A slot's parent or spare page would be written over while its other layers have yet to read it."""
+    at = {n: 8 * P * (i + 1) for i, n in enumerate(("parents", "spare", "old_table", "old_len", "new_table", "new_len"))}
+    entries = {"old_table": 8, "new_table": 8}
+    (out, over), = change.items()
+    mine, theirs = 4 * entries.get(out, 4), 4 * entries.get(over, 4)
+    for off in (0, theirs - 4, 4 - mine):  # the same place, the last word of the other, its first
+        with pytest.raises(W.WsgError, match="overlap") as e:
+            W.beam_reorder_pages(W.beam_reorder_args(**{**APART, **at, out: at[over] + off}))
+        assert e.value.status == 1
+
+
 def test_null_arguments_and_empty_calls(W):
     lib = W.library()
     for call in CALLS:

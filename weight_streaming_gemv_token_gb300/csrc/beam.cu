@@ -715,17 +715,28 @@ extern "C" dec_status beam_reorder_pages(const beam_reorder_args* a, void* strea
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the pools must be 16-byte aligned in every layer");
   if (!aligned_to(4, a->parents, a->spare, a->old_table, a->old_len, a->new_table, a->new_len))
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: a pointer is not aligned to its elements");
-  auto overlap = [](const int32_t* x, const int32_t* y, size_t n) {
-    const uintptr_t p = reinterpret_cast<uintptr_t>(x), q = reinterpret_cast<uintptr_t>(y);
-    return (p < q ? q - p : p - q) < 4 * n;
+  const size_t beams = a->beams, entries = beams * a->table_stride;
+  struct Array {
+    const int32_t* at;
+    size_t n;
   };
-  const size_t beams = a->beams;
-  if (overlap(a->new_table, a->old_table, beams * a->table_stride) || overlap(a->new_len, a->old_len, beams))
+  auto overlap = [](Array x, Array y) {
+    const uintptr_t p = reinterpret_cast<uintptr_t>(x.at), q = reinterpret_cast<uintptr_t>(y.at);
+    return p < q ? q - p < 4 * x.n : p - q < 4 * y.n;
+  };
+  const Array table{a->new_table, entries}, length{a->new_len, beams};
+  if (overlap(table, {a->old_table, entries}) || overlap(length, {a->old_len, beams}))
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the new table and lengths must not overlap the old");
   const long long layer = static_cast<long long>(a->num_pages) * a->n_kv * a->page_size * a->head_dim;
   if (a->layers > 1 && a->layer_stride < layer)
     return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: layers of %lld elements overlap at stride %lld", layer,
                 static_cast<long long>(a->layer_stride));
+  // (a slot's other CTAs may still have to read what its first one writes over)
+  for (const Array x : {Array{a->parents, beams}, Array{a->spare, beams}})
+    if (overlap(table, x) || overlap(length, x))
+      return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: the new table and lengths must not overlap parents or spare pages");
+  if (overlap(table, {a->old_len, beams}) || overlap(length, {a->old_table, entries}) || overlap(table, length))
+    return fail(nullptr, DEC_EINVAL, "beam_reorder_pages: tables and lengths must not overlap");
   DeviceInfo di;
   const dec_status st = device_info(&di, nullptr);
   if (st != DEC_OK) return st;
