@@ -476,7 +476,8 @@ dec_status rope_frequencies(const rope_scaling* s, double* h_inv_freq, float* h_
  * rope_factor. rot_dim 0: no rotation. The arithmetic is float32 (angles are
  * reduced exactly, so far positions lose nothing) and each output is rounded
  * once. positions[r] < 0 marks a padded row: its outputs are left as they
- * were. q_out may be q itself (same dtype and stride), k_out likewise. */
+ * were. q_out may be q itself (same dtype and stride), k_out likewise; outputs
+ * must not overlap inputs in any other way. */
 typedef struct {
   int32_t rows, n_q, n_kv, head_dim; /* n_q or n_kv may be 0; each at most 16384 */
   int32_t xdtype, ydtype;            /* q, k; q_out, k_out: DEC_F32 or DEC_BF16 */
@@ -611,11 +612,12 @@ dec_status beam_select(const beam_select_args* a, void* stream);
  * page its next token goes to. The spare pages must differ from each other and
  * from every page of the old tables; the new table and lengths must not
  * overlap each other nor any input. parents[i] < 0, or a parent that is itself
- * unused (old_len < 0), makes slot i unused: new_len -1 and a row of -1. old_len[p] must leave room
- * for the next token (< table_stride * page_size); a longer one, a parent
- * >= beams, or a page or spare page outside the pool sets DEC_DEVERR_BAD_PAGE
- * and makes the slot unused. Layer l's pools start l * layer_stride elements
- * after k_pages and v_pages; layers must not overlap. */
+ * unused (old_len < 0), makes slot i unused: new_len -1 and a row of -1.
+ * old_len[p] must leave room for the next token (< table_stride * page_size); a
+ * longer one, a parent >= beams, or a page of its tokens or a spare page outside
+ * the pool sets DEC_DEVERR_BAD_PAGE and makes the slot unused. Layer l's pools
+ * start l * layer_stride elements after k_pages and v_pages; layers must not
+ * overlap. */
 typedef struct {
   int32_t beams, layers, n_kv, head_dim, kvdtype;
   void *k_pages, *v_pages;

@@ -308,6 +308,18 @@ def test_refusals_of_outputs_over_inputs(W, change):
         assert e.value.status == 1
 
 
+@pytest.mark.parametrize("call,out", [("qk_norm_rope", "q"), ("qk_norm_rope", "k"), ("kv_append_paged", "q")], ids=str)
+def test_refusals_of_rows_that_move_in_place(W, call, out):
+    """Outputs over their own inputs with another stride or type would be written over rows that are still to be read."""
+    args, good = CALLS[call]
+    base = {**good, **{n: 8 * P * (i + 1) for i, n in enumerate(("q", "k", "v", "q_out", "k_out")) if n in good}}
+    for change in ({f"{out}_out_stride": base[f"{out}_stride"] + 8}, {f"{out}_stride": 0}, {"ydtype": 1}, {"xdtype": 1},
+                   {"rows": 1, "ydtype": 1}):
+        with pytest.raises(W.WsgError, match=f"{call}: {out}_out over {out} needs") as e:
+            getattr(W, call)(getattr(W, args)(**{**base, f"{out}_out": base[out], **change}))
+        assert e.value.status == 1
+
+
 def test_null_arguments_and_empty_calls(W):
     lib = W.library()
     for call in CALLS:

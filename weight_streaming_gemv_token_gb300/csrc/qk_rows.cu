@@ -426,6 +426,12 @@ bool pieces16(const void* p, long long stride, int dtype) {
   return aligned16(p) && stride * (dtype == DEC_F32 ? 4 : 2) % 16 == 0;
 }
 
+// Whether rows may go from `in` to `out`: over themselves only where every row stays in
+// its place, or a unit writes over rows that others have yet to read.
+bool in_place_ok(const void* in, const void* out, int rows, int xd, int yd, int64_t in_stride, int64_t out_stride) {
+  return in != out || (xd == yd && (rows == 1 || in_stride == out_stride));
+}
+
 // Checks common to both calls, on the fields they share.
 template <typename A>
 dec_status check_rows(const A* a, const char* who) {
@@ -541,6 +547,10 @@ extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
   if (a->rows > 1 && a->n_kv > 0 && a->k_out_stride < static_cast<long long>(a->n_kv) * a->head_dim)
     return fail(nullptr, DEC_EINVAL, "qk_norm_rope: k_out rows overlap at stride %lld",
                 static_cast<long long>(a->k_out_stride));
+  if (a->n_q > 0 && !in_place_ok(a->q, a->q_out, a->rows, a->xdtype, a->ydtype, a->q_stride, a->q_out_stride))
+    return fail(nullptr, DEC_EINVAL, "qk_norm_rope: q_out over q needs q's type and stride");
+  if (a->n_kv > 0 && !in_place_ok(a->k, a->k_out, a->rows, a->xdtype, a->ydtype, a->k_stride, a->k_out_stride))
+    return fail(nullptr, DEC_EINVAL, "qk_norm_rope: k_out over k needs k's type and stride");
   DeviceInfo di;
   if ((s = device_info(&di, nullptr)) != DEC_OK) return s;
   QkRowsArgs k = shared_fields(a);
@@ -570,6 +580,8 @@ extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
     return fail(nullptr, DEC_EINVAL, "kv_append_paged: the pools must be 16-byte aligned");
   if (!aligned_to(elem_bytes(a->xdtype), a->v) || !aligned_to(4, a->page_table, a->seq))
     return fail(nullptr, DEC_EINVAL, "kv_append_paged: a pointer is not aligned to its elements");
+  if (a->n_q > 0 && !in_place_ok(a->q, a->q_out, a->rows, a->xdtype, a->ydtype, a->q_stride, a->q_out_stride))
+    return fail(nullptr, DEC_EINVAL, "kv_append_paged: q_out over q needs q's type and stride");
   DeviceInfo di;
   if ((s = device_info(&di, nullptr)) != DEC_OK) return s;
   QkRowsArgs k = shared_fields(a);
