@@ -432,6 +432,24 @@ def test_argument_blocks_refuse_tensors_with_gaps(W):
         assert e.value.status == 1
 
 
+def test_argument_blocks_refuse_numbers_that_do_not_fit(W):
+    """A size beyond its field would be taken by its low bits: 2^32 + 4 rows as 4."""
+    for call, (args, good) in CALLS.items():
+        block = getattr(W, args)
+        for name, kind in block._kind.items():
+            if kind not in (ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t):
+                continue
+            bits = 8 * ctypes.sizeof(kind)
+            for value in (2**bits + 4, 2 ** (bits - 1 if kind is not ctypes.c_size_t else bits), -2**bits + 4):
+                with pytest.raises(W.WsgError, match=f"{args}.{name}: .* outside") as e:
+                    block(**{**good, name: value})
+                assert e.value.status == 1
+                a = block(**good)
+                with pytest.raises(W.WsgError, match=f"{args}.{name}: .* outside"):
+                    setattr(a, name, value)
+                assert getattr(a, name) == good[name]
+
+
 def test_oracle_rotation_layouts():
     """Both layouts turn each pair by its angle and leave lengths as they are; position 0 turns nothing."""
     rng = np.random.default_rng(0)

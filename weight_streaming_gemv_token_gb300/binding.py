@@ -71,6 +71,9 @@ _FIXED = {name: dtype for dtype, names in {
 }.items() for name in names.split()}
 
 
+_RANGES = {c_int32: (-2**31, 2**31), ctypes.c_int64: (-2**63, 2**63), c_size_t: (0, 2 ** (8 * ctypes.sizeof(c_size_t)))}
+
+
 class _Args(ctypes.Structure):
     """An argument block of the calls for several branches: fields by keyword, every one but `_optional` required.
     Pointers may be tensors, which the block keeps alive; it can be used for any number of calls. A tensor must have the
@@ -108,8 +111,13 @@ class _Args(ctypes.Structure):
         return self
 
     def __setattr__(self, name, value):
+        kind = self._kind.get(name)
+        if kind in _RANGES and isinstance(value, int):  # ctypes would keep the low bits
+            lo, hi = _RANGES[kind]
+            if not lo <= value < hi:
+                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: {value} is outside [{lo}, {hi})")
         super().__setattr__(name, value)
-        if name in self._kind:
+        if kind is not None:
             super().__setattr__("_verified", False)
 
     def verify(self):
