@@ -944,3 +944,88 @@ def test_beam_search_over_a_shared_prompt():
         history = [history[p] for p in parents]
         assert nl.tolist() == [step + 1] * beams
         table, length, scores, tokens = nt, nl, sc.clone(), to.clone()
+
+
+@pytest.mark.parametrize("shape,kv,y", [("TINY", "f32", "f32"), ("TINY", "bf16", "f32"), ("Q4_SMALL", "bf16", "bf16")], ids=str)
+def test_branches_continue_a_decoders_prompt(shape, kv, y):
+    """Branches of a prompt that the decoder prefilled: appended keys carry on the rotation and norm of the prompt's,
+    attention reads the decoder's own cache. Keys, values and logits of every branch are those of the decoder and of the
+    oracle on the branch's whole token sequence, within the tolerances that the decoder itself is held to. (What lies
+    between the operators, products with the weights and the SwiGLU, is computed on the host.)"""
+    import torch
+
+    import oracle as O
+    import workloads as Wl
+    from gpu_util import FP32_TOL, LOW_TOL, close
+    from oracle import primitives as P
+    from weight_streaming_gemv_token_gb300.decoder import Decoder
+
+    W = lib()
+    s = getattr(Wl, shape)
+    tol = FP32_TOL if kv == y == "f32" else LOW_TOL
+    weights = Wl.decoder_weights(s, seed=1, wdtype="f32" if kv == "f32" else "bf16")
+    prompt = [int(x) for x in Wl.prompt_uniform(21, s.vocab, seed=0)]
+    d, n, page, width, steps = s.head_dim, len(prompt), 4, 3, 6
+    rng = np.random.default_rng(3)
+    rows = rng.integers(0, s.vocab, (3, steps))  # the branches' tokens; the last two differ from their second on
+    rows[2, 0] = rows[1, 0]
+    B = len(rows)
+    dec = Decoder(s, weights, kv_dtype=kv, max_seq=n + steps + 4)
+    dec.prefill(prompt, is_last=True)
+    ora = O.OracleDecoder(s, weights, kv_dtype=kv, max_seq=n + steps + 4)
+    freq, factor = W.rope_frequencies(d, s.rope_theta)
+    wd = torch.tensor(freq, dtype=torch.float64, device="cuda")
+    pools = [[torch.full((B * width, s.n_kv, page, d), float("nan"), device="cuda").to(tdt(kv)) for _ in range(2)]
+             for _ in range(s.layers)]
+    table = rng.permutation(B * width).reshape(B, width)
+    table_d, wide = ints(table), (s.n_q + 2 * s.n_kv) * d
+    gains = [[torch.tensor(P.widen(w[g]).astype(np.float32), device="cuda") for g in ("g_q", "g_k")] for w in weights["layers"]]
+    got = np.zeros((B, steps, s.vocab))
+    W.gemv_device_errors()
+    for i in range(steps):
+        h = ora.E[rows[:, i]].copy()
+        for l, w in enumerate(ora.layers):
+            x = P.rmsnorm(h, w["g_in"], s.eps)
+            qkv = torch.tensor(np.concatenate([x @ w[m].T for m in ("w_q", "w_k", "w_v")], 1).astype(np.float32), device="cuda")
+            q_out = torch.empty((B, s.n_q * d), dtype=tdt(y), device="cuda")
+            W.kv_append_paged(W.kv_append_args(
+                rows=B, n_q=s.n_q, n_kv=s.n_kv, head_dim=d, xdtype=W.DEC_F32, ydtype=code(W, y), kvdtype=code(W, kv),
+                q=qkv, k=qkv[:, s.n_q * d:], v=qkv[:, (s.n_q + s.n_kv) * d:], q_out=q_out, q_stride=wide, k_stride=wide,
+                v_stride=wide, q_out_stride=s.n_q * d, g_q=gains[l][0], g_k=gains[l][1], positions=ints([n + i] * B),
+                inv_freq=wd, eps=s.eps, rope_factor=factor, rot_dim=d, interleaved=0, k_pages=pools[l][0],
+                v_pages=pools[l][1], page_table=table_d, seq=None, n_seq=B, num_pages=B * width, page_size=page,
+                table_stride=width, base_pos=n))
+            K, V, held = dec.kv(l)
+            assert held == n
+            out = torch.empty_like(q_out)
+            a = W.attn_shared_args(
+                batch=B, n_q=s.n_q, n_kv=s.n_kv, head_dim=d, qdtype=code(W, y), kvdtype=code(W, kv), q=q_out, out=out,
+                q_stride=s.n_q * d, out_stride=s.n_q * d, prefix_k=K, prefix_v=V, prefix_len=n, prefix_stride=K.shape[1],
+                k_pages=pools[l][0], v_pages=pools[l][1], page_table=table_d, seq_len=ints([i + 1] * B),
+                num_pages=B * width, page_size=page, table_stride=width, scale=d ** -0.5)
+            a.with_workspace(torch.empty(W.attn_shared_prefix_workspace(a), dtype=torch.uint8, device="cuda"))
+            W.attn_shared_prefix(a)
+            h = h + f64(out) @ w["w_o"].T
+            x = P.rmsnorm(h, w["g_post"], s.eps)
+            h = h + P.swiglu(x @ w["w_gate"].T, x @ w["w_up"].T) @ w["w_down"].T
+        got[:, i] = P.rmsnorm(h, ora.g_final, s.eps) @ ora.E.T
+    assert W.gemv_device_errors() == 0
+    dec.close()
+    i = np.arange(steps)
+    for b in range(B):
+        ref = O.OracleDecoder(s, weights, kv_dtype=kv, max_seq=n + steps + 4)
+        ref.prefill(prompt)
+        one = Decoder(s, weights, kv_dtype=kv, max_seq=n + steps + 4)
+        one.prefill(prompt, is_last=True)
+        logits = torch.empty(s.vocab, dtype=torch.float32, device="cuda")
+        for j, t in enumerate(rows[b]):
+            want = ref.step(int(t))
+            one.step(int(t), logits=logits)
+            close(got[b, j], want, tol, f"logits of branch {b}, step {j}")
+            close(got[b, j], f64(logits), 2 * tol, f"the decoder's logits, branch {b}, step {j}")
+        for l in range(s.layers):
+            for pool, theirs, mine in zip(pools[l], ref.kv(l), one.kv(l)[:2]):
+                rows_of = f64(pool)[table[b, i // page], :, i % page].transpose(1, 0, 2)
+                close(rows_of, theirs[:, n:], tol, f"cache of branch {b}, layer {l}")
+                close(rows_of, f64(mine)[:, n: n + steps], 2 * tol, f"the decoder's cache, branch {b}, layer {l}")
+        one.close()
