@@ -1029,3 +1029,92 @@ def test_branches_continue_a_decoders_prompt(shape, kv, y):
                 close(rows_of, theirs[:, n:], tol, f"cache of branch {b}, layer {l}")
                 close(rows_of, f64(mine)[:, n: n + steps], 2 * tol, f"the decoder's cache, branch {b}, layer {l}")
         one.close()
+
+
+def test_operators_on_two_streams_at_once():
+    """Calls with workspaces of their own that run beside each other give the bits that they give alone."""
+    import torch
+
+    W = lib()
+    cases = []
+    for k, (types, batch, n_q, n_kv, d, plen) in enumerate(((("bf16", "bf16"), 16, 16, 8, 128, 3000),
+                                                            (("bf16", "bf16"), 40, 8, 2, 128, 1500),
+                                                            (("f32", "f32"), 6, 8, 4, 64, 700))):
+        a, t = attn_case(W, batch, n_q, n_kv, d, plen, [(7 * i + k) % 90 for i in range(batch)], 16, *types, seed=10 * k)
+        logits, scores = rand((4 + k, 20000), "f32", 50 + k, 2.0), rand((4 + k,), "f32", 60 + k)
+        outs = [torch.zeros(20, dtype=dt, device="cuda") for dt in (torch.float32, torch.int32, torch.int32)]
+        b = W.beam_select_args(beams=4 + k, vocab=20000, n_out=20, logits=logits, logits_stride=20000, scores=scores,
+                               out_scores=outs[0], out_parents=outs[1], out_tokens=outs[2])
+        b.with_workspace(torch.empty(W.beam_select_workspace(b), dtype=torch.uint8, device="cuda"))
+        cases.append((a, b, [t["out"], t["lse"], *outs]))
+    want = []
+    for a, b, outs in cases:
+        W.attn_shared_prefix(a)
+        W.beam_select(b)
+        torch.cuda.synchronize()
+        want.append([x.clone() for x in outs])
+        for x in outs:
+            x.fill_(3)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    for _ in range(30):
+        for (a, b, _outs), st in zip(cases, streams):
+            W.attn_shared_prefix(a, st)
+            W.beam_select(b, st)
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    for (_, _, outs), w in zip(cases, want):
+        for x, y in zip(outs, w):
+            assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("types,d", [(("bf16", "bf16"), 128), (("bf16", "bf16"), 64), (("f32", "f32"), 128)], ids=str)
+def test_a_captured_step_follows_its_lengths_and_tables(types, d):
+    """A graph of append and attention is captured once; positions, lengths and tables change between its replays, as a
+    decoding loop changes them, slots ending and starting again. Each replay gives an eager call's bits and the
+    definition's values."""
+    import torch
+
+    W = lib()
+    B, n_q, n_kv, plen, page, width = 5, 8, 4, 200, 8, 12
+    full = [width * page] * B
+    a, t = attn_case(W, B, n_q, n_kv, d, plen, full, page, *types, poison=False, width=width)
+    s, ra, _, extra = rope_case(W, B, n_q, n_kv, d, d, 0, "f32", types[0], seed=30)
+    v = rand((B, n_kv * d), "f32", 40)
+    lens, pos, table = ints([-1] * B), ints([-1] * B), ints(t["table"])
+    ra.update(q_out=t["q"], positions=pos)
+    kv_args = W.kv_append_args(v=v, v_stride=n_kv * d, kvdtype=code(W, types[1]), k_pages=t["kp"], v_pages=t["vp"],
+                               page_table=table, seq=None, n_seq=B, num_pages=t["kp"].shape[0], page_size=page,
+                               table_stride=width, base_pos=plen, **ra)
+    a.set("seq_len", lens).set("page_table", table)
+
+    def step(stream=None):
+        W.kv_append_paged(kv_args, stream)
+        W.attn_shared_prefix(a, stream)
+
+    side = torch.cuda.Stream()
+    step(side)
+    side.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        step(side)
+    rng = np.random.default_rng(8)
+    for k in range(6):
+        held = rng.integers(1, width * page + 1, B)
+        held[k % B] = -1
+        if k == 3:
+            held[:] = -1  # every slot unused
+        now = rng.permutation(t["table"].reshape(-1)).reshape(B, width).astype(np.int32)
+        lens.copy_(ints(held)), pos.copy_(ints(np.where(held < 0, -1, plen + held - 1))), table.copy_(ints(now))
+        t["table"] = now
+        for x in (t["out"], t["lse"]):
+            x.fill_(7)
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert W.gemv_device_errors() == 0
+        check_attn(t, B, n_q, n_kv, d, plen, held.tolist(), page, types[0])
+        got = [x.clone() for x in (t["out"], t["lse"])]
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], t["out"]) and torch.equal(got[1], t["lse"])
