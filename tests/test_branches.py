@@ -494,15 +494,15 @@ def walk(tmp_path_factory):
                    "  const BeamLayout L = beam_layout(beams, vocab, n_out);\n"
                    "  const size_t places = (L.total - L.flat) / 4, listed = (size_t)L.slots * L.list;\n"
                    "  if (listed > places || L.key + 8 * listed > L.flat) return -1;\n"
-                   "  std::vector<char> seen(listed);\n  long long n = 0, bad = 0;\n"
+                   "  std::vector<char> seen(listed);\n  long long n = 0, handed = 0, bad = 0;\n"
                    "  for (int t = 0; t < kBeamThreads; ++t)\n"
                    "    beam_walk(L.slots, L.list, t, [&](int q) { return count[q]; },\n"
                    "              [&](size_t p) -> uint32_t {\n"
                    "                if (p >= listed) { bad = -1; return 0; }\n"
                    "                if (p % L.list >= count[p / L.list]) bad = -2;\n"
                    "                if (seen[p]++) bad = -3;\n                ++n;\n                return p * 7 + 1; },\n"
-                   "              [&](uint32_t k, size_t p) { if (k != (uint32_t)(p * 7 + 1)) bad = -4; });\n"
-                   "  return bad ? bad : n;\n}\n")
+                   "              [&](uint32_t k, size_t p) { if (k && k != (uint32_t)(p * 7 + 1)) bad = -4; handed += k != 0; });\n"
+                   "  return bad ? bad : handed == n ? n : -4;\n}\n")
     lib = d / "w.so"
     inc = os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc")
     subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(src), "-o", str(lib)], check=True)

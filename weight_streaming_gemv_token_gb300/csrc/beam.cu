@@ -192,7 +192,8 @@ struct BeamSource {
   int n;
 };
 
-// fn(high word, place) of each candidate; places in the lists count through them.
+// fn(high word, place) of each candidate, and of places without one, whose word is 0;
+// places in the lists count through them.
 template <bool LISTS, typename Fn>
 __device__ __forceinline__ void for_high(const BeamArgs& a, const BeamSource& s, Fn fn) {
   if constexpr (!LISTS) {
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
   } else {
     bar = narrow<true>(a, BeamSource{}, want, key_lo, 0xffffffffu, &scratch);
     for_high<true>(a, BeamSource{}, [&](uint32_t h, size_t p) {
-      if (h < bar.h) return;
+      if (h < bar.h) return;  // (0, behind a list's end, is below every bar)
       const uint32_t l = __ldcg(a.key + p).y, f = __ldcg(a.flat + p);
       if (bar.reached(h, l, f)) {
         const uint32_t w = atomicAdd(&s_n, 1u);

@@ -58,9 +58,11 @@ inline BeamLayout beam_layout(int beams, int vocab, int n_out) {
 }
 
 // The places that thread `tid` of kBeamThreads visits in lists of `list` places each,
-// of which the first count(slot) hold a candidate: load(place) of up to eight together,
-// then fn(what it gave, place) of each. No other place is formed: the end of the last
-// list is the end of the workspace.
+// of which the first count(slot) hold a candidate: w = load(place) of up to eight
+// together, then fn(w, place). Behind a list's count nothing is loaded and fn gets a
+// word of 0, with which it must return before it touches the place: the end of the last
+// list is the end of the workspace. (With a test of the word before fn, 4 beams of equal
+// logits, 64 outputs, take 550 us; like this 500.)
 template <typename Count, typename Load, typename Fn>
 WSG_DEV void beam_walk(int slots, int list, int tid, Count count, Load load, Fn fn) {
   int per = 1;  // threads a list
@@ -74,10 +76,10 @@ WSG_DEV void beam_walk(int slots, int list, int tid, Count count, Load load, Fn 
       uint32_t k[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (i0 + e * per < n) k[e] = load(p0 + i0 + e * per);
+        k[e] = i0 + e * per < n ? load(p0 + i0 + e * per) : 0;
 #pragma unroll
       for (int e = 0; e < 8; ++e)
-        if (i0 + e * per < n) fn(k[e], p0 + i0 + e * per);
+        fn(k[e], p0 + i0 + e * per);
     }
   }
 }
