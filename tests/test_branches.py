@@ -531,7 +531,19 @@ def test_selection_reads_no_place_behind_its_lists(walk):
 
 def test_prefix_kernel_has_no_wait_without_a_limit():
     """Warps of the tensor-core prefix kernel that wait for some others, not for the whole CTA, do so on mbarriers, whose
-    waits give up: a named barrier would keep a warp for good whose partner has given up before it."""
+    waits give up, or at a barrier that each of them comes to whatever it has given up: one behind a condition of its own
+    would keep a warp for good whose partner has given up before it."""
     with open(os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc", "attn_prefix_tc.cuh")) as f:
         code = "\n".join(line.split("//")[0] for line in f)
-    assert not re.search(r"\bbar(rier)?\.(cta\.)?(sync|red|arrive)|__barrier_sync|__syncthreads_", code)
+    assert not re.search(r"barrier\.(cta\.)?(sync|red|arrive)|bar\.(red|arrive)|__barrier_sync|__syncthreads_", code)
+    blocks, found = [], 0  # the openings of the blocks around each place
+    for m in re.finditer(r"[{}]|\bbar\.sync", code):
+        if m[0] == "{":
+            blocks.append(code[max(code.rfind(c, 0, m.start()) for c in ";{}") + 1: m.start()].strip())
+        elif m[0] == "}":
+            blocks.pop()
+        else:
+            found += 1
+            inner = [b for b in blocks if "namespace" not in b and "__global__" not in b]
+            assert inner == ["else if (works)"], inner  # (the same for all warps that the barrier counts)
+    assert found == 1 and not blocks

@@ -326,6 +326,7 @@ __global__ void __maxnreg__(120)
     if (ok && !__all_sync(0xffffffffu, mbar_wait(&o_done[(T - 1) & 1], ((T - 1) >> 1) & 1))) ok = false;
     xch[T & 1][half][v] = lsum;
     if (!pair_done(T)) ok = false;  // (after a failure the pair may be out of step: bounded either way)
+    float* so = reinterpret_cast<float*>(Ks);
     if (ok) {
       tc_fence_after();
       const long long at = static_cast<long long>(split) * a.batch * a.n_q + prow;
@@ -333,7 +334,6 @@ __global__ void __maxnreg__(120)
       // O through shared memory (the rings are done with), so that a warp writes
       // whole rows: 16-byte pieces a row apart from every lane kept the CTA 5 us
       // longer on its SM
-      float* so = reinterpret_cast<float*>(Ks);
 #pragma unroll 1
       for (int c0 = 0; c0 < 64; c0 += 32) {
         uint32_t o[32];
@@ -343,12 +343,15 @@ __global__ void __maxnreg__(120)
 #pragma unroll
         for (int k = 0; k < 8; ++k) dst[k] = make_uint4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
       }
-      // The two warps of the lane quarter. Bounded like every wait, and reached only by a
-      // warp that has given up nowhere: one whose partner has waits out the limit here.
-      ok = pair_done(T + 1);
+    }
+    // The two warps of the lane quarter, each of which comes here whatever it gave up:
+    // this barrier ends when their bounded waits have. (As a phase of pair_bar: 4 x 512
+    // and 16 x 4096 take 0.2 us longer.)
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
+    if (ok) {
 #pragma unroll 4
       for (int r = q * 32 + half * 16; r < q * 32 + half * 16 + 16; ++r) {
-        if (!ok || r >= nrows) break;
+        if (r >= nrows) break;
         const int row = row0 + r;
         const long long to_row = static_cast<long long>(split) * a.batch * a.n_q +
                                  static_cast<long long>(row / a.group) * a.n_q + g * a.group + row % a.group;
