@@ -20,10 +20,13 @@
 //
 // Rows in shared memory are 16 bytes longer than the head, which makes the matrix
 // loads of the keys and the scalar loads of the values free of bank conflicts.
-// The matrix instructions bound it: 192 a block, one in two cycles an SM, against
-// 350 cycles for the block's 8 KB at the SM's share of the memory. Measured: 16
-// rows a head x 3,001 keys and 100 own ones a branch 16.4 us a call with its join,
-// x 32,768 57 us (4.7 TB/s).
+// A block's 96 matrix instructions (48 for the scores, 48 for the outputs at head
+// size 128) take 192 cycles of the SM, its 8 KB 350 at the SM's share of the
+// memory: bound by memory for long ranges of few rows, by latency for short ones,
+// where a warp has four blocks in all (tensor pipe 23%, issue 23%, DRAM 23%), by the
+// repeated conversions and reads from L2 for many rows (each 16 walk all keys).
+// Measured: 16 rows a head x 3,001 keys and 100 own ones a branch 16.8 us a call with
+// its join, x 32,768 60 us (4.5 TB/s); 128 rows a head x 8,192 129 us.
 #pragma once
 #include <cstdint>
 

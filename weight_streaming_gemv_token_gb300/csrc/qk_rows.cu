@@ -7,9 +7,9 @@
 // angle t becomes (a cos t - b sin t, a sin t + b cos t), t = position * w_i.
 // The angle is kept in turns as a 64-bit fixed-point fraction, F_i = frac(w_i /
 // 2 pi) * 2^64: position * F_i modulo 2^64 is the exact fraction of a turn for
-// that F_i, by integer multiplication, so a far position costs no precision (F_i
-// keeps every bit of w_i) and nothing runs on the slow double pipe. The top 32
-// bits go to sincospif.
+// that F_i, by integer multiplication, and nothing runs on the slow double pipe. F_i
+// is w_i / 2 pi to 2^-64 of a turn (fewer bits than w_i has where that is small), which
+// the farthest position makes 2^-33. The top 32 bits go to sincospif.
 //
 // Layout: a unit of lanes holds one head, 8 consecutive elements a lane (one
 // 16-byte load of bfloat16, two of float32), and walks several heads of a row so
