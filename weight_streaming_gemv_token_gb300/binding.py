@@ -9,6 +9,7 @@ library is missing the import of a function raises.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 from . import build as _build
@@ -71,6 +72,14 @@ _FIXED = {name: dtype for dtype, names in {
 }.items() for name in names.split()}
 
 
+_set_field = ctypes.Structure.__setattr__
+
+
+@functools.cache
+def _dtype_name(dtype) -> str:
+    return str(dtype).removeprefix("torch.")
+
+
 _RANGES = {c_int32: (-2**31, 2**31), ctypes.c_int64: (-2**63, 2**63), c_size_t: (0, 2 ** (8 * ctypes.sizeof(c_size_t)))}
 
 
@@ -101,7 +110,7 @@ class _Args(ctypes.Structure):
         if kind is None:
             raise TypeError(f"{type(self).__name__} has no field {name}")
         if kind is c_void_p:
-            if value is not None:
+            if value is not None and not isinstance(value, int):
                 if getattr(value, "is_cuda", True) is False:
                     raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is not on a CUDA device")
                 self._fits(name, value)
@@ -111,42 +120,36 @@ class _Args(ctypes.Structure):
         return self
 
     def __setattr__(self, name, value):
-        kind = self._kind.get(name)
-        if kind in _RANGES and isinstance(value, int):  # ctypes would keep the low bits
-            lo, hi = _RANGES[kind]
-            if not lo <= value < hi:
-                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: {value} is outside [{lo}, {hi})")
-        super().__setattr__(name, value)
-        if kind is not None:
-            super().__setattr__("_verified", False)
+        bounds = _RANGES.get(self._kind.get(name))
+        if bounds and isinstance(value, int) and not bounds[0] <= value < bounds[1]:  # ctypes would keep the low bits
+            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: {value} is outside [{bounds[0]}, {bounds[1]})")
+        _set_field(self, name, value)
+        _set_field(self, "_verified", False)
 
     def verify(self):
         """Refuse tensors whose type is not the one that their DEC_* field gives (by the calls after a change: fields may
         change in any order)."""
         for name, code in self._typed.items():
-            dtype, want = self._dtype(self._keep.get(name)), _ELEMENTS.get(getattr(self, code))
-            if dtype and want and dtype not in want:
-                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {dtype}, {code} says {want[0]}")
-        self._verified = True
-
-    @staticmethod
-    def _dtype(value):
-        return str(value.dtype).removeprefix("torch.") if hasattr(value, "dtype") else None
+            dtype = getattr(self._keep.get(name), "dtype", None)
+            want = _ELEMENTS.get(getattr(self, code))
+            if dtype is not None and want and _dtype_name(dtype) not in want:
+                raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {_dtype_name(dtype)}, {code} says "
+                                           f"{want[0]}")
+        _set_field(self, "_verified", True)
 
     def _fits(self, name, value):
         """Refuse a tensor that the call would read as something else, whatever the block's other fields."""
-        dtype = self._dtype(value)
+        dtype = getattr(value, "dtype", None)
         if dtype is None:
             return
-        if name in _FIXED and dtype != _FIXED[name]:
-            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {dtype}, not {_FIXED[name]}")
-        if value.numel() == 0:  # (strides of an empty tensor say nothing)
+        if name in _FIXED and _dtype_name(dtype) != _FIXED[name]:
+            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {_dtype_name(dtype)}, not {_FIXED[name]}")
+        if value.is_contiguous() or value.numel() == 0:  # (strides of an empty tensor say nothing)
             return
         if name in ("k_pages", "v_pages"):
-            layer = value[0] if value.dim() == 5 else value
-            if not layer.is_contiguous():
+            if not (value.dim() == 5 and value[0].is_contiguous()):
                 raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the pool is not contiguous")
-        elif value.dim() > 0 and value.shape[-1] > 1 and value.stride(-1) != 1:
+        elif value.shape[-1] > 1 and value.stride(-1) != 1:
             raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor's rows are not contiguous")
 
     def with_workspace(self, workspace):
