@@ -694,6 +694,23 @@ def test_beam_select_lowest_scores():
     assert got[1].tolist() == [2, 2, -1, -1, -1, -1] and got[2].tolist() == [1, 0, -1, -1, -1, -1]
 
 
+@pytest.mark.parametrize("score", [0.0, -3.0, -1e6, -1e9])
+def test_beam_select_masked_rows_of_beams_far_behind(score):
+    """Rows of nothing but the type's lowest value are even distributions over what is not masked: their log-sums decide,
+    and equal ones tie, whatever the beams' common score and the logits' level take up of the sum. (All rows' sums of
+    exponentials are exact or apart: keys differ by 0.2 or tie.)"""
+    W = lib()
+    low, top = np.finfo(np.float32).min, np.finfo(np.float32).max
+    x = np.full((8, 5), low, dtype=np.float32)
+    x[1, 2:] = -np.inf
+    x[2, 1:] = -np.inf
+    x[3] = [0.0, 1.0, 2.0, -3.0, low]
+    x[4, :2] = -np.inf
+    x[5], x[6], x[7] = -7.0, top, 12345.67
+    for n_out in (1, 4, 9, 17, 40):
+        check_select(run_select(W, x, [score] * 8, n_out), x, [score] * 8, n_out)
+
+
 # ---- reorder -------------------------------------------------------------------------------------------------------
 
 REORDER_CASES = [

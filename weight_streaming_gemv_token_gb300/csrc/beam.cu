@@ -70,34 +70,38 @@ __device__ __forceinline__ uint32_t order32(float x) {
 }
 __device__ __forceinline__ float unorder32(uint32_t k) { return __uint_as_float(k >> 31 ? k & 0x7fffffffu : ~k); }
 
-// The key x + off as two order words, off and the sum as two floats (value and
-// remainder, 48 bits): the slow double pipe takes 7 times as long here.
-__device__ __forceinline__ uint2 key_words(float x, float2 off) {
-  const float s = x + off.x, t = s - x;
-  const float e = (x - (s - t)) + (off.x - t) + off.y;  // x + off.x - s exactly, then the remainder
-  // below the lowest finite value: that value, behind those that reach it (fmaxf drops a NaN)
-  const float hi = fmaxf(s + e, -FLT_MAX), lo = fmaxf(e - (hi - s), -INFINITY);
-  return make_uint2(order32(hi), order32(lo));
-}
-
 // Two floats that sum to a + b exactly.
 __device__ __forceinline__ float2 two_sum(float a, float b) {
   const float s = a + b, t = s - a;
   return make_float2(s, (a - (s - t)) + (b - t));
 }
 
-// score - (m + log s) as two floats. s = 2^e f with f in [0.7, 1.42]; log f = 2
-// artanh u, u = (f - 1) / (f + 1), |u| < 0.172, by its series to u^9 (the next term
-// is below 7e-10; the whole is good to 3e-8); e log 2 is an exact product by the
+// The key x + off + rest as two order words, the sum as two floats (value and remainder,
+// 48 bits): the slow double pipe takes 7 times as long here.
+__device__ __forceinline__ uint2 key_words(float x, float2 off, float rest) {
+  const float2 s = two_sum(x, off.x), e = two_sum(s.y, off.y);
+  // below the lowest finite value: that value, behind those that reach it (fmaxf drops a NaN)
+  const float hi = fmaxf(s.x + e.x, -FLT_MAX), lo = fmaxf(e.x - (hi - s.x) + (e.y + rest), -INFINITY);
+  return make_uint2(order32(hi), order32(lo));
+}
+
+// (score - log s) - m as three floats, the last one `rest`; the bracket is rounded to two
+// first, so that rows of one score and sum have the same key at their maxima whatever m is
+// (float32's lowest value takes the first float for itself). s = 2^e f with f in [0.7,
+// 1.42]; log f = 2 artanh u, u = (f - 1) / (f + 1), |u| < 0.172, by its series to u^9 (the
+// next term is below 7e-10; the whole is good to 3e-8); e log 2 is an exact product by the
 // first 13 bits of log 2 and a small rest.
-__device__ __forceinline__ float2 row_offset(float score, float m, float s) {
+__device__ __forceinline__ float2 row_offset(float score, float m, float s, float* rest) {
   int e = static_cast<int>(__float_as_uint(s) >> 23) - 127;  // (s >= 1)
   float f = __uint_as_float((__float_as_uint(s) & 0x7fffffu) | 0x3f800000u);
   if (f > 1.41421356f) f *= 0.5f, ++e;
   const float u = __fdividef(f - 1.f, f + 1.f), u2 = u * u;
   const float log_f = 2.f * fmaf(u * u2, fmaf(u2, fmaf(u2, fmaf(u2, 1.f / 9.f, 1.f / 7.f), 1.f / 5.f), 1.f / 3.f), u);
-  const float2 a = two_sum(score, -m), b = two_sum(a.x, e * -0.693145751953125f), c = two_sum(b.x, -log_f);
-  return two_sum(c.x, a.y + b.y + c.y - e * 1.428606820309417e-6f);
+  const float2 l = two_sum(e * -0.693145751953125f, -log_f), n = two_sum(score, l.x);
+  const float2 k = two_sum(n.x, n.y + (l.y - e * 1.428606820309417e-6f));
+  const float2 d = two_sum(k.x, -m), r = two_sum(d.y, k.y);
+  *rest = r.y;
+  return make_float2(d.x, r.x);
 }
 
 // Pass 1: chunks blockIdx.x, blockIdx.x + gridDim.x, ..., 16 logits a thread at a
@@ -302,6 +306,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
   uint32_t *sl = sh + kBeamGather, *sf = sl + kBeamGather;
   float *smax = reinterpret_cast<float*>(sh), *ssum = reinterpret_cast<float*>(sl);
   __shared__ float2 off[kBeamsMax];  // of the rows: score - lse
+  __shared__ float rest[kBeamsMax];
   __shared__ BeamScratch scratch;
   __shared__ uint32_t cnt[kBeamThreads / 32], s_lo, s_hi, s_n, s_mine;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -346,8 +351,10 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
     for (int o = lanes / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
     if (b < a.beams && (tid & (lanes - 1)) == 0) {
       const float sc = off[b].x;
-      const float2 o = finite && isfinite(sc) ? row_offset(sc, m, s) : make_float2(-INFINITY, 0.f);
+      float over = 0.f;
+      const float2 o = finite && isfinite(sc) ? row_offset(sc, m, s, &over) : make_float2(-INFINITY, 0.f);
       off[b] = isfinite(o.x) ? o : make_float2(-INFINITY, 0.f);
+      rest[b] = over;
     }
   }
   __syncthreads();
@@ -355,10 +362,11 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
   uint32_t some = 0, lo = 0xffffffffu, hi = 0;
 #pragma unroll 2
   for (int k = tid; k < padded; k += kBeamThreads) {
-    const float2 o = off[k < a.chunks ? static_cast<uint32_t>((k * a.row_inv) >> 32) : 0];
+    const int b = k < a.chunks ? static_cast<int>((k * a.row_inv) >> 32) : 0;
+    const float2 o = off[b];
     const float m = smax[k];
     const bool in = (k < a.chunks) & (m > -INFINITY) & (o.x > -INFINITY);
-    const uint2 w = key_words(m, o);
+    const uint2 w = key_words(m, o, rest[b]);
     sh[k] = in ? w.x : 0;
     sl[k] = w.y;
     some += in;
@@ -406,6 +414,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
               n = min(a.chunk, a.vocab - v0);
     const float* x = a.logits + a.stride * b + v0;
     const float2 o = off[b];
+    const float over = rest[b];
     const uint32_t f0 = static_cast<uint32_t>(b) * a.vocab + v0;
     const float bar_value = bar.h == 1 ? -INFINITY : unorder32(bar.h);
     // y + o.x differs from the key by the offset's remainder and a rounding of each
@@ -431,7 +440,7 @@ __global__ void __launch_bounds__(kBeamThreads, 3) beam_pick_kernel(const BeamAr
 #pragma unroll 1
       for (; near; near &= near - 1) {
         const int e = __ffs(near) - 1, i = i0 + (e >> 2) * kBeamThreads * 4 + (e & 3);
-        const uint2 w = key_words(x[i], o);
+        const uint2 w = key_words(x[i], o, over);
         if (bar.reached(w.x, w.y, f0 + i)) {
           const uint32_t p = atomicAdd(&s_n, 1u);
           a.key[base + p] = w;
