@@ -554,6 +554,8 @@ dec_status kv_append_paged(const kv_append_args* a, void* stream);
  * wider than the branches are long is slower where they are few (16 branches of
  * 256 tokens after 4,096 shared ones 11 us with a table for up to 512, 27 for
  * 4,096).
+ * out may be q itself (with its stride); outputs and workspace must not overlap
+ * anything else.
  * A bounded wait that gave up (a broken launch) sets DEC_DEVERR_GEMM_TIMEOUT in
  * the context-free error word. d_workspace: attn_shared_prefix_workspace(a)
  * bytes for these sizes, 256-byte aligned. */

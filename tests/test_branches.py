@@ -320,6 +320,14 @@ def test_refusals_of_rows_that_move_in_place(W, call, out):
         assert e.value.status == 1
 
 
+def test_refusals_of_attention_over_queries_that_move(W):
+    """A branch's output is written while others have yet to read their queries."""
+    for change in ({"out_stride": 72}, {"q_stride": 0}, {"q_stride": 128}):
+        with pytest.raises(W.WsgError, match="attn_shared_prefix: out over q needs") as e:
+            W.attn_shared_prefix(W.attn_shared_args(**{**ATTN, "q": 8 * P, "out": 8 * P, **change}))
+        assert e.value.status == 1
+
+
 def test_null_arguments_and_empty_calls(W):
     lib = W.library()
     for call in CALLS:

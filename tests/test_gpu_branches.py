@@ -447,6 +447,27 @@ def test_attn_shared_prefix_negative_scale(types, batch, scale):
             inside(got[b, g], o, attn_tol(Q[b, g], k, l, o, size, abs(scale), types[0])[0], (b, g))
 
 
+@pytest.mark.parametrize("types,d", [(("bf16", "bf16"), 128), (("bf16", "bf16"), 64), (("f32", "f32"), 128)], ids=str)
+@pytest.mark.parametrize("width", [8, 80])
+def test_attn_shared_prefix_in_place(types, d, width):
+    """The output over the queries, unused slots left as they are: the bits of a call with buffers of its own."""
+    import torch
+
+    W = lib()
+    batch, n_q, n_kv = 33, 8, 4
+    lens = [(5 * i) % 97 - 1 for i in range(batch)]
+    a, t = attn_case(W, batch, n_q, n_kv, d, 700, lens, 16, *types, width=width)
+    W.attn_shared_prefix(a)
+    torch.cuda.synchronize()
+    want = torch.where((ints(lens) < 0)[:, None], t["q"], t["out"])
+    for _ in range(5):
+        q = t["q"].clone()
+        a.set("q", q).set("out", q)
+        W.attn_shared_prefix(a)
+        torch.cuda.synchronize()
+        assert torch.equal(q, want)
+
+
 def test_attn_shared_prefix_bad_pages():
     """Entries outside the pool are left out and reported; so are tokens past the table's width."""
     import torch

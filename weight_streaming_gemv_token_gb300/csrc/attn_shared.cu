@@ -170,6 +170,9 @@ extern "C" dec_status attn_shared_prefix(const attn_shared_args* a, void* stream
   if (!aligned_to(elem_bytes(a->qdtype), a->q, a->out) || !aligned_to(4, a->lse, a->seq_len) ||
       (a->table_stride > 0 && !aligned_to(4, a->page_table)))
     return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: a pointer is not aligned to its elements");
+  // (a branch's output is written while others have yet to read their queries)
+  if (a->out == a->q && a->batch > 1 && a->out_stride != a->q_stride)
+    return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: out over q needs q's stride");
   if (!a->d_workspace || reinterpret_cast<uintptr_t>(a->d_workspace) % 256)
     return fail(nullptr, DEC_EINVAL, "attn_shared_prefix: workspace must be non-NULL and 256-byte aligned");
   DeviceInfo di;
