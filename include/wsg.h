@@ -595,7 +595,8 @@ dec_status attn_shared_prefix(const attn_shared_args* a, void* stream);
  * log-sum, is not finite, whose logits hold +inf, or which has no finite logit
  * offers nothing. A sum below the lowest finite float32 counts as that value,
  * behind those that reach it. Slots that nothing fills get parent -1, token -1
- * and score -inf.
+ * and score -inf. out_scores may be scores itself; outputs must not overlap
+ * anything else.
  * beams 1..1024, n_out 1..1024, beams * vocab < 2^31; logits float32,
  * row b at logits + b * logits_stride. d_workspace as for
  * attn_shared_prefix; it holds a list of 12 bytes a logit for each of up to n_out

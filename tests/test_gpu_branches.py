@@ -622,6 +622,27 @@ def test_beam_select_lists_of_odd_lengths(c, kind):
     check_select(run_select(W, x, [-1.0] * beams, n_out), x, [-1.0] * beams, n_out)
 
 
+@pytest.mark.parametrize("beams,n_out", [(8, 8), (3, 200), (200, 3)])
+def test_beam_select_scores_in_place(beams, n_out):
+    """New scores over the old ones, as a search keeps them."""
+    import torch
+
+    W = lib()
+    logits, scores = rand((beams, 30000), "f32", 1, 2.0), rand((max(beams, n_out),), "f32", 2)
+    want = run_select(W, logits.cpu().numpy(), scores[:beams].cpu().numpy(), n_out)
+    parents, tokens = ints(np.zeros(n_out)), ints(np.zeros(n_out))
+    for _ in range(5):
+        sc = scores.clone()
+        a = W.beam_select_args(beams=beams, vocab=30000, n_out=n_out, logits=logits, logits_stride=30000, scores=sc,
+                               out_scores=sc, out_parents=parents, out_tokens=tokens)
+        a.with_workspace(torch.empty(W.beam_select_workspace(a), dtype=torch.uint8, device="cuda"))
+        W.beam_select(a)
+        torch.cuda.synchronize()
+        for got, w in zip((sc[:n_out], parents, tokens), want):
+            np.testing.assert_array_equal(got.cpu().numpy(), w)
+        assert torch.equal(sc[n_out:], scores[n_out:])
+
+
 def test_beam_select_strided_rows():
     W = lib()
     rng = np.random.default_rng(1)
