@@ -414,6 +414,8 @@ def test_argument_blocks_refuse_tensors_of_another_type(W):
                 with pytest.raises(W.WsgError, match=f"{args}.{name}: the tensor is"):
                     getattr(W, call)(a)
     assert seen == set(coded) | {n for names in fixed.values() for n in names}
+    for dtype in ("uint8", "uint16", "int16"):  # bytes, or bfloat16 by its bits
+        W.attn_shared_args(**{**ATTN, "kvdtype": 1, **{n: t(4, dtype) for n in ("prefix_k", "prefix_v", "k_pages", "v_pages")}})
 
 
 def test_argument_blocks_refuse_tensors_with_gaps(W):

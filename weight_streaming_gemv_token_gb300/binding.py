@@ -63,8 +63,9 @@ class dec_weights(ctypes.Structure):
     _fields_ = [("embed", c_void_p), ("g_final", c_void_p), ("layers", ctypes.POINTER(dec_layer_weights))]
 
 
-# Types of the tensors that an argument block takes: by DEC_* code (bfloat16 as such or as its bits) and by field.
-_ELEMENTS = {DEC_F32: ("float32",), DEC_BF16: ("bfloat16", "uint16", "int16")}
+# Types of the tensors that an argument block takes: by DEC_* code (bfloat16 as such or as its bits; uint8: a buffer of
+# bytes) and by field.
+_ELEMENTS = {DEC_F32: ("float32", "uint8"), DEC_BF16: ("bfloat16", "uint16", "int16", "uint8")}
 _FIXED = {name: dtype for dtype, names in {
     "int32": "positions seq page_table seq_len parents spare old_table old_len new_table new_len out_parents out_tokens",
     "float32": "g_q g_k lse logits scores out_scores",
