@@ -67,6 +67,7 @@ typedef enum { DEC_F32 = 0, DEC_BF16 = 1, DEC_Q4G64 = 2 } dec_dtype;
 #define DEC_DEVERR_GEMM_TIMEOUT 0x20u     /* chunked prefill, attn_shared_prefix: a tensor-core pipeline wait gave up */
 #define DEC_DEVERR_BARRIER_TIMEOUT 0x40u  /* persistent 4-bit engine: a grid barrier gave up (dec_reset clears it) */
 #define DEC_DEVERR_BAD_PAGE 0x80u         /* a sequence, page or parent index of the paged calls was out of range */
+#define DEC_DEVERR_BAD_TREE 0x100u        /* a drafted row's parent is not an earlier row of its request, or a tree has more rows than its mask */
 
 /* dec_config.engine */
 #define DEC_ENGINE_PERSISTENT 0 /* one cooperative launch runs whole forwards (default) */
@@ -647,6 +648,222 @@ typedef struct {
 /* Counterpart of "Megakernels", "GPU-wide end-to-end generation" (the cache
  * entries a generation leaves) for branches that share entries. */
 dec_status beam_reorder_pages(const beam_reorder_args* a, void* stream);
+
+/* ---- Drafted trees of several requests ---------------------------------------
+ *
+ * The calls below run a step that checks drafted tokens of several requests over
+ * the paged cache above; pools, tables, streams, workspaces and errors are as
+ * for the branches. Request s holds tokens in pages and brings rows row_start[s]
+ * .. row_start[s + 1] - 1: row 0 is its last known token, which is not in the
+ * cache yet, the others are drafted ones, each below an earlier row of the
+ * request (parents: its number within the request; row 0 has none, -1). Without
+ * parents a request's rows are a chain, each row's parent the row before: a draft
+ * in one line, the single tokens of an ordinary step, or a prompt's rows. Row i
+ * goes to index held + i of the request's pages, siblings to different indexes,
+ * and its position is held + its depth. mask gives the rows that a row attends
+ * to, bit j % 32 of word j / 32 for row j of the request; the ancestors and the row
+ * itself as step_slots makes it. A step: step_slots; in every layer kv_append_slots
+ * and attn_tree_paged; after the vocabulary projection logits_adjust, which also
+ * picks the greedy token after each row; tree_accept_paged, whose new lengths are
+ * the next step's. They extend "Megakernels", "What runs in the DSL" and
+ * "GPU-wide end-to-end generation" (greedy tokens on the GPU, lowest ID on ties)
+ * to several drafted tokens at a time, as dec_verify2 does for one. */
+
+/* Tables and slots of a step. held[s]: tokens that request s holds in pages, -1
+ * once it has ended; fresh[s]: rows that it brings (below 0 counts as 0; an ended
+ * request brings none). row_start [requests + 1]: the sum of the rows before, at
+ * most `rows`. A request needs ceil((held + fresh) / page_size) pages and owns the
+ * first owned[s] entries of its table row (the pages of its tokens, others left from
+ * rejected drafts). What it lacks comes from the free pages, a ring of num_pages
+ * entries: free_state[1] of them from entry free_state[0] on, in the requests'
+ * order. A request is served if it lacks nothing or the free pages cover what it
+ * and all requests before it lack; one that needs more pages than table_stride, has
+ * rows past `rows`, or with a mask more than 32 * mask_words rows, is not and
+ * asks for no page. Ended requests' pages go behind the ring's last entry, in order,
+ * and can be given out from the next step on.
+ * new_table: owned entries, then the new pages, then -1 (ended requests: -1); it
+ * may be page_table itself, then the entries behind a request's pages are left as
+ * they were. new_owned, new_free_state: what the next step starts from. ctx_len[s]:
+ * held[s], or -1 for an ended request or one that is not served.
+ * For every row r < rows: seq[r] its request, positions[r] = base_pos + held +
+ * depth (base_pos: tokens of a shared prefix, which are not in pages), slots[r] =
+ * page * page_size + row in the page, mask; -1, -1, -1 and a mask of 0 for rows of
+ * requests that are not served and behind the last row. A row whose parent is not
+ * an earlier row of its request (row 0's is not looked at), and rows below it,
+ * have -1 and 0 too and set DEC_DEVERR_BAD_TREE; so does a request with more rows
+ * than its mask has bits. Tables too narrow, rows past `rows`, an owned count
+ * outside the table, pages out of range, a ring state outside the ring and more
+ * returned pages than the ring has room for set DEC_DEVERR_BAD_PAGE; running out of
+ * pages sets nothing. seq, positions, slots, mask and parents may be NULL (mask
+ * without parents is a chain's). Up to 4096 requests, masks up to 8 words.
+ * Outputs must not overlap inputs or each other otherwise. */
+typedef struct {
+  int32_t requests, rows;
+  int32_t num_pages, page_size, table_stride, base_pos, mask_words;
+  const int32_t *held, *fresh, *owned; /* [requests] */
+  const int32_t* parents;              /* [rows] or NULL */
+  const int32_t* page_table;           /* [requests][table_stride] */
+  int32_t* free_ring;                  /* [num_pages], in and out */
+  const int32_t* free_state;           /* [2] first entry, entries */
+  int32_t *new_table, *new_owned, *new_free_state;
+  int32_t *row_start, *ctx_len;
+  int32_t *seq, *positions;
+  int64_t* slots;
+  uint32_t* mask; /* [rows][mask_words] */
+} step_slots_args;
+
+dec_status step_slots(const step_slots_args* a, void* stream);
+
+/* kv_append_paged by a map of slots: row r's key and value go to slots[r] =
+ * page * page_size + row in the page. A padded row (positions[r] < 0) stores
+ * nothing and leaves its q_out as it was; a slot of -1 stores nothing; one outside
+ * the pool counts as a bad page, and its q_out is written. Two rows of one slot
+ * leave a mixture of both there. */
+typedef struct {
+  int32_t rows, n_q, n_kv, head_dim; /* n_q may be 0 */
+  int32_t xdtype, ydtype, kvdtype;   /* q, k, v; q_out; pages */
+  const void *q, *k, *v;
+  void* q_out;
+  int64_t q_stride, k_stride, v_stride, q_out_stride;
+  const float *g_q, *g_k;
+  const int32_t* positions;
+  const double* inv_freq;
+  float eps, rope_factor;
+  int32_t rot_dim, interleaved;
+  void *k_pages, *v_pages;
+  const int64_t* slots;
+  int32_t num_pages, page_size;
+} kv_slots_args;
+
+dec_status kv_append_slots(const kv_slots_args* a, void* stream);
+
+/* Grouped-query attention of all rows of a step: row i of request s over the shared
+ * prefix (prefix_len keys and values a head, as in attn_shared_prefix; 0: none), the
+ * request's seq_len[s] tokens in pages, and those of its rows that mask says (their
+ * keys and values at index seq_len[s] + j of its pages); mask NULL: rows 0 .. i;
+ * rows past the mask's bits are not attended to. out and lse as in
+ * attn_shared_prefix; a row with nothing to attend to gets zeros (and lse -inf).
+ * seq_len[s] < 0 marks an unused request, whose rows are left as they were, as are
+ * rows of no request. What a row does not attend to does not reach it, whatever is
+ * there (not finite as well), and rows of pages behind a request's last are never
+ * used. row_start must not fall and lie in 0 .. rows (it is taken as if it did).
+ * An index beyond table_stride * page_size counts as a bad page; its keys are left
+ * out. Sizes, precision, order of results and the other rules are those of
+ * attn_shared_prefix, with rows * n_q < 2^24 and batch <= 4096. The work is cut up on
+ * the device by the requests' lengths, equal shares of key tiles for all SMs. */
+typedef struct {
+  int32_t batch, rows, n_q, n_kv, head_dim;
+  int32_t qdtype, kvdtype;
+  const void* q;
+  void* out;
+  float* lse; /* [rows][n_q] or NULL */
+  int64_t q_stride, out_stride;
+  const int32_t* row_start; /* [batch + 1] */
+  const uint32_t* mask;     /* [rows][mask_words] or NULL */
+  int32_t mask_words;
+  const void *prefix_k, *prefix_v;
+  int32_t prefix_len;
+  int64_t prefix_stride;
+  const void *k_pages, *v_pages;
+  const int32_t* page_table;
+  const int32_t* seq_len;
+  int32_t num_pages, page_size, table_stride;
+  float scale;
+  void* d_workspace;
+  size_t workspace_bytes;
+} attn_tree_args;
+
+size_t attn_tree_paged_workspace(const attn_tree_args* a);
+
+/* Additional error: DEC_ENOMEM (workspace too small). */
+dec_status attn_tree_paged(const attn_tree_args* a, void* stream);
+
+/* Logits by the rules of their requests. Row r belongs to request seq[r] (NULL: r;
+ * outside [0, requests): the row is left as it was). Its text is the request's
+ * tokens[0 .. tokens_len + tokens_base), of which the first prompt_len (NULL: 0) are
+ * its prompt, and, with draft_tokens, the drafted tokens of those rows of the
+ * request that mask says (NULL: up to r itself). With n(v) the times that token v
+ * comes after the prompt, a logit x of v becomes
+ *   x / repetition (x > 0) or x * repetition, if v is in the text at all;
+ *   x - frequency * n(v);  x - presence, if n(v) > 0;
+ *   x + bias, if v is in the request's list of bias_len entries (of equal ones the
+ *   last counts);
+ *   -inf, if bit v % 32 of word v / 32 of the row's mask of allowed tokens is 0:
+ *   row allowed_row[r] of `allowed` (< 0: none; NULL: row r; outside [0,
+ *   allowed_rows): none, and DEC_DEVERR_BAD_TOKEN is set).
+ * Each step is rounded to float32, out once to ydtype. repetition, frequency and
+ * presence are float32 [requests] or NULL; repetition > 0. Tokens outside [0,
+ * vocab) count nowhere, rows of a request past the mask's bits neither. next
+ * (nullable, int32 [rows]): the token of the greatest resulting float32 logit, the
+ * lowest of equal ones; NaN counts as masked; -1 if no logit is above -inf. out is
+ * nullable where next is given, and may be logits itself (same dtype, stride).
+ * vocab up to 2^20; up to 2^19 tokens a text, as many drafted ones and 1023 biases a
+ * list (longer ones are cut). Outputs must not overlap anything else. */
+typedef struct {
+  int32_t rows, vocab, requests;
+  int32_t xdtype, ydtype; /* logits; out: DEC_F32 or DEC_BF16 */
+  const void* logits;
+  int64_t logits_stride;
+  void* out;
+  int64_t out_stride;
+  int32_t* next;
+  const int32_t* seq;
+  const int32_t* tokens; /* [requests][tokens_stride] or NULL: no text */
+  int64_t tokens_stride;
+  const int32_t *tokens_len, *prompt_len;
+  int32_t tokens_base;
+  const int32_t* draft_tokens; /* [rows] or NULL */
+  const int32_t* row_start;    /* [requests + 1], with draft_tokens */
+  const uint32_t* mask;        /* [rows][mask_words] or NULL */
+  int32_t mask_words;
+  const float *repetition, *frequency, *presence;
+  const int32_t* bias_tokens; /* [requests][bias_stride] or NULL */
+  const float* bias;
+  const int32_t* bias_len;
+  int32_t bias_stride;
+  const uint32_t* allowed; /* [allowed_rows][allowed_stride words] or NULL */
+  int64_t allowed_stride;
+  int32_t allowed_rows;
+  const int32_t* allowed_row;
+} logits_adjust_args;
+
+dec_status logits_adjust(const logits_adjust_args* a, void* stream);
+
+/* The part of each tree that the greedy tokens confirm. Row 0 of a request is
+ * accepted; after an accepted row r comes the first of its children whose drafted
+ * token is next[r], until there is none (or path_stride rows are accepted).
+ * count[s]: accepted rows; path[s][d]: their numbers within the request, out_tokens
+ * [s][d] = next of them (the last one is the next step's row 0), -1 behind;
+ * new_len[s] = seq_len[s] + count[s]. The keys and values of the accepted rows move
+ * from index seq_len + path[d] of the request's pages to seq_len + d in every layer
+ * (layer l's pools start l * layer_stride elements after k_pages and v_pages);
+ * nothing else in the pools is written. tokens
+ * (nullable): draft_tokens of the accepted rows are written to tokens[s][seq_len +
+ * tokens_base + d]. A request with seq_len < 0 is left alone (count 0, new_len -1,
+ * path and out_tokens -1), one without rows too (new_len = seq_len). A page of an
+ * accepted row outside the pool or the table sets DEC_DEVERR_BAD_PAGE and that row is
+ * not moved; a place outside tokens_stride is not written and sets
+ * DEC_DEVERR_BAD_POSITION. layers may be 0 (nothing moves; no pools). path_stride up
+ * to 256. Outputs must not overlap inputs (tokens apart) or each other. */
+typedef struct {
+  int32_t batch, rows, path_stride;
+  int32_t layers, n_kv, head_dim, kvdtype;
+  const int32_t* row_start; /* [batch + 1] */
+  const int32_t* parents;   /* [rows], or NULL: chains */
+  const int32_t *draft_tokens, *next; /* [rows] */
+  const int32_t* seq_len;   /* [batch] */
+  void *k_pages, *v_pages;
+  int64_t layer_stride;
+  int32_t num_pages, page_size, table_stride;
+  const int32_t* page_table;
+  int32_t* tokens; /* [batch][tokens_stride] or NULL */
+  int64_t tokens_stride;
+  int32_t tokens_base;
+  int32_t *count, *new_len;   /* [batch] */
+  int32_t *path, *out_tokens; /* [batch][path_stride] */
+} tree_accept_args;
+
+dec_status tree_accept_paged(const tree_accept_args* a, void* stream);
 
 #ifdef __cplusplus
 }

@@ -24,7 +24,7 @@ DEC_ENGINE_PERSISTENT, DEC_ENGINE_STAGED = 0, 1
 DEC_DEVERR_WAIT_TIMEOUT, DEC_DEVERR_ARGMAX_NAN, DEC_DEVERR_BAD_TOKEN = 0x1, 0x2, 0x4
 DEC_DEVERR_BAD_POSITION, DEC_DEVERR_EXCHANGE_TIMEOUT, DEC_DEVERR_GEMM_TIMEOUT, DEC_DEVERR_BARRIER_TIMEOUT = (
     0x8, 0x10, 0x20, 0x40)
-DEC_DEVERR_BAD_PAGE = 0x80
+DEC_DEVERR_BAD_PAGE, DEC_DEVERR_BAD_TREE = 0x80, 0x100
 ROPE_PLAIN, ROPE_LINEAR, ROPE_BASE, ROPE_RAMP = range(4)
 
 # Every symbol include/wsg.h declares.
@@ -36,6 +36,7 @@ EXPORTED = (
     "pack_bf16_exact", "dec_verify2", "dec_set_wait_limit",
     "rope_frequencies", "qk_norm_rope", "kv_append_paged", "attn_shared_prefix", "attn_shared_prefix_workspace",
     "beam_select", "beam_select_workspace", "beam_reorder_pages",
+    "step_slots", "kv_append_slots", "attn_tree_paged", "attn_tree_paged_workspace", "logits_adjust", "tree_accept_paged",
 )
 
 
@@ -67,9 +68,13 @@ class dec_weights(ctypes.Structure):
 # bytes) and by field.
 _ELEMENTS = {DEC_F32: ("float32", "uint8"), DEC_BF16: ("bfloat16", "uint16", "int16", "uint8")}
 _FIXED = {name: dtype for dtype, names in {
-    "int32": "positions seq page_table seq_len parents spare old_table old_len new_table new_len out_parents out_tokens",
-    "float32": "g_q g_k lse logits scores out_scores",
-    "float64": "inv_freq",
+    ("int32",): "positions seq page_table seq_len parents spare old_table old_len new_table new_len out_parents out_tokens "
+                "held fresh owned free_ring free_state new_owned new_free_state row_start ctx_len next tokens tokens_len "
+                "prompt_len draft_tokens bias_tokens bias_len allowed_row count path",
+    ("int64",): "slots",
+    ("int32", "uint32"): "mask allowed",
+    ("float32",): "g_q g_k lse scores out_scores repetition frequency presence bias",
+    ("float64",): "inv_freq",
 }.items() for name in names.split()}
 
 
@@ -91,6 +96,7 @@ class _Args(ctypes.Structure):
 
     _optional = ()
     _typed = {}  # pointer field -> the field with the DEC_* code of its elements
+    _fixed = {}  # pointer field -> its elements' types, where this block differs from _FIXED
 
     def __init_subclass__(cls):
         cls._kind = dict(cls._fields_)
@@ -143,13 +149,16 @@ class _Args(ctypes.Structure):
         dtype = getattr(value, "dtype", None)
         if dtype is None:
             return
-        if name in _FIXED and _dtype_name(dtype) != _FIXED[name]:
-            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {_dtype_name(dtype)}, not {_FIXED[name]}")
+        want = self._fixed.get(name) or _FIXED.get(name)
+        if want and _dtype_name(dtype) not in want:
+            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is {_dtype_name(dtype)}, not {want[0]}")
         if value.is_contiguous() or value.numel() == 0:  # (strides of an empty tensor say nothing)
             return
         if name in ("k_pages", "v_pages"):
             if not (value.dim() == 5 and value[0].is_contiguous()):
                 raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the pool is not contiguous")
+        elif name == "mask":  # its rows lie mask_words apart
+            raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor is not contiguous")
         elif value.shape[-1] > 1 and value.stride(-1) != 1:
             raise WsgError(DEC_EINVAL, f"{type(self).__name__}.{name}: the tensor's rows are not contiguous")
 
@@ -202,6 +211,7 @@ class attn_shared_args(_Args):
 
 
 class beam_select_args(_Args):
+    _fixed = {"logits": ("float32",)}
     _optional = ("d_workspace", "workspace_bytes")
     _fields_ = ([(n, c_int32) for n in ("beams", "vocab", "n_out")]
                 + [("logits", c_void_p), ("logits_stride", c_int64)]
@@ -215,6 +225,67 @@ class beam_reorder_args(_Args):
                 + [("k_pages", c_void_p), ("v_pages", c_void_p), ("layer_stride", c_int64)]
                 + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
                 + [(n, c_void_p) for n in ("parents", "spare", "old_table", "old_len", "new_table", "new_len")])
+
+
+class step_slots_args(_Args):
+    _optional = ("parents", "seq", "positions", "slots", "mask", "mask_words", "base_pos")
+    _fields_ = ([(n, c_int32) for n in ("requests", "rows", "num_pages", "page_size", "table_stride", "base_pos", "mask_words")]
+                + [(n, c_void_p) for n in ("held", "fresh", "owned", "parents", "page_table", "free_ring", "free_state",
+                                           "new_table", "new_owned", "new_free_state", "row_start", "ctx_len", "seq",
+                                           "positions", "slots", "mask")])
+
+
+class kv_slots_args(_Args):
+    _typed = kv_append_args._typed
+    _fields_ = ([(n, c_int32) for n in ("rows", "n_q", "n_kv", "head_dim", "xdtype", "ydtype", "kvdtype")]
+                + [(n, c_void_p) for n in ("q", "k", "v", "q_out")]
+                + [(n, c_int64) for n in ("q_stride", "k_stride", "v_stride", "q_out_stride")]
+                + [(n, c_void_p) for n in ("g_q", "g_k", "positions", "inv_freq")]
+                + [("eps", c_float), ("rope_factor", c_float), ("rot_dim", c_int32), ("interleaved", c_int32)]
+                + [(n, c_void_p) for n in ("k_pages", "v_pages", "slots")]
+                + [(n, c_int32) for n in ("num_pages", "page_size")])
+
+
+class attn_tree_args(_Args):
+    _typed = attn_shared_args._typed
+    _optional = ("lse", "mask", "mask_words", "prefix_k", "prefix_v", "prefix_len", "prefix_stride", "d_workspace",
+                 "workspace_bytes")
+    _fields_ = ([(n, c_int32) for n in ("batch", "rows", "n_q", "n_kv", "head_dim", "qdtype", "kvdtype")]
+                + [(n, c_void_p) for n in ("q", "out", "lse")]
+                + [(n, c_int64) for n in ("q_stride", "out_stride")]
+                + [("row_start", c_void_p), ("mask", c_void_p), ("mask_words", c_int32)]
+                + [("prefix_k", c_void_p), ("prefix_v", c_void_p), ("prefix_len", c_int32), ("prefix_stride", c_int64)]
+                + [(n, c_void_p) for n in ("k_pages", "v_pages", "page_table", "seq_len")]
+                + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
+                + [("scale", c_float), ("d_workspace", c_void_p), ("workspace_bytes", c_size_t)])
+
+
+class logits_adjust_args(_Args):
+    _typed = {"logits": "xdtype", "out": "ydtype"}
+    _optional = ("out", "out_stride", "next", "seq", "tokens", "tokens_stride", "tokens_len", "prompt_len", "tokens_base",
+                 "draft_tokens", "row_start", "mask", "mask_words", "repetition", "frequency", "presence", "bias_tokens",
+                 "bias", "bias_len", "bias_stride", "allowed", "allowed_stride", "allowed_rows", "allowed_row")
+    _fields_ = ([(n, c_int32) for n in ("rows", "vocab", "requests", "xdtype", "ydtype")]
+                + [("logits", c_void_p), ("logits_stride", c_int64), ("out", c_void_p), ("out_stride", c_int64)]
+                + [(n, c_void_p) for n in ("next", "seq", "tokens")]
+                + [("tokens_stride", c_int64), ("tokens_len", c_void_p), ("prompt_len", c_void_p), ("tokens_base", c_int32)]
+                + [(n, c_void_p) for n in ("draft_tokens", "row_start", "mask")]
+                + [("mask_words", c_int32)]
+                + [(n, c_void_p) for n in ("repetition", "frequency", "presence", "bias_tokens", "bias", "bias_len")]
+                + [("bias_stride", c_int32), ("allowed", c_void_p), ("allowed_stride", c_int64), ("allowed_rows", c_int32),
+                   ("allowed_row", c_void_p)])
+
+
+class tree_accept_args(_Args):
+    _typed = {"k_pages": "kvdtype", "v_pages": "kvdtype"}
+    _optional = ("parents", "k_pages", "v_pages", "layer_stride", "num_pages", "page_size", "table_stride", "page_table",
+                 "n_kv", "head_dim", "kvdtype", "tokens", "tokens_stride", "tokens_base")
+    _fields_ = ([(n, c_int32) for n in ("batch", "rows", "path_stride", "layers", "n_kv", "head_dim", "kvdtype")]
+                + [(n, c_void_p) for n in ("row_start", "parents", "draft_tokens", "next", "seq_len", "k_pages", "v_pages")]
+                + [("layer_stride", c_int64)]
+                + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
+                + [("page_table", c_void_p), ("tokens", c_void_p), ("tokens_stride", c_int64), ("tokens_base", c_int32)]
+                + [(n, c_void_p) for n in ("count", "new_len", "path", "out_tokens")])
 
 
 _lib = None
@@ -262,6 +333,12 @@ def library() -> ctypes.CDLL:
             "beam_select": (c_int32, [P(beam_select_args), c_void_p]),
             "beam_select_workspace": (c_size_t, [P(beam_select_args)]),
             "beam_reorder_pages": (c_int32, [P(beam_reorder_args), c_void_p]),
+            "step_slots": (c_int32, [P(step_slots_args), c_void_p]),
+            "kv_append_slots": (c_int32, [P(kv_slots_args), c_void_p]),
+            "attn_tree_paged": (c_int32, [P(attn_tree_args), c_void_p]),
+            "attn_tree_paged_workspace": (c_size_t, [P(attn_tree_args)]),
+            "logits_adjust": (c_int32, [P(logits_adjust_args), c_void_p]),
+            "tree_accept_paged": (c_int32, [P(tree_accept_args), c_void_p]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(lib, name)
@@ -481,3 +558,37 @@ def beam_select(args: beam_select_args, stream=None):
 def beam_reorder_pages(args: beam_reorder_args, stream=None):
     """New page tables after a selection, and copies of the tail pages that beams must own."""
     _check(library().beam_reorder_pages(_verified(args), _stream(stream)))
+
+
+# ---- drafted trees of several requests ----
+
+def step_slots(args: step_slots_args, stream=None):
+    """Page tables, row starts, positions, slots and ancestor masks of a step from the requests' lengths."""
+    _check(library().step_slots(_verified(args), _stream(stream)))
+
+
+def kv_append_slots(args: kv_slots_args, stream=None):
+    """kv_append_paged by a map of slots."""
+    _check(library().kv_append_slots(_verified(args), _stream(stream)))
+
+
+def attn_tree_paged_workspace(args: attn_tree_args) -> int:
+    n = library().attn_tree_paged_workspace(args)
+    if n == 0:
+        raise WsgError(DEC_EINVAL, "attn_tree_paged_workspace: invalid sizes")
+    return n
+
+
+def attn_tree_paged(args: attn_tree_args, stream=None):
+    """Attention of every row of a step over the shared prefix, its request's pages and the rows that its mask says."""
+    _check(library().attn_tree_paged(_verified(args), _stream(stream)))
+
+
+def logits_adjust(args: logits_adjust_args, stream=None):
+    """Penalties for repeated tokens, biases and masks of allowed tokens on logits; the greedy token of the result."""
+    _check(library().logits_adjust(_verified(args), _stream(stream)))
+
+
+def tree_accept_paged(args: tree_accept_args, stream=None):
+    """The path of each tree that the greedy tokens confirm; its keys and values move to their places in the cache."""
+    _check(library().tree_accept_paged(_verified(args), _stream(stream)))

@@ -1,0 +1,176 @@
+// attn_tree_paged: grouped-query attention of drafted trees of several requests over a
+// shared prefix, the requests' pages and the rows of their own tree ("Megakernels",
+// "What runs in the DSL": grouped-query attention).
+//
+// The line of key tiles (attn_tree_plan.h) goes by the lengths on the device, so
+// every SM has an equal share of it whatever the requests' lengths and however wide
+// their tables are. A segment that lies in one CTA's share is finished there; the
+// pieces of the others, and of rows that have a prefix too, join exactly in
+// attn_tree_join_kernel:
+//   out = sum_i o_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), m = max_i m_i.
+#include "attn_tree.cuh"
+
+#include <cmath>
+
+#include "common.h"
+#include "spans.h"
+
+namespace wsg {
+namespace {
+
+// One warp a (row, query head): lane i holds elements 4 i .. 4 i + 3 of the head.
+template <typename QT>
+__global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int ctas) {
+  const AmArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = blockIdx.x * 4 + warp;
+  pdl_trigger();  // a following call's set-up may begin
+  pdl_wait();
+  if (w >= a.rows * a.n_q) return;
+  const int row = w / a.n_q, head = w - row * a.n_q, g = head / a.group, h = head - g * a.group;
+  AtRow rec = p.rec[row];
+  if (rec.tiles == 0) return;  // of no request, or an unused one
+  const long long W = *p.total;
+  const int C = static_cast<int>(min(static_cast<long long>(ctas), W));
+  int at = rec.at + h;
+  if (at >= p.cut.mt) {  // the row tile behind the record's
+    at -= p.cut.mt;
+    rec.line += rec.tiles;
+    rec.tiles = rec.next;
+    ++rec.seg;
+  }
+  const long long line = rec.line + static_cast<long long>(g) * rec.head;
+  const int c0 = at_owner(W, C, line), c1 = at_owner(W, C, line + rec.tiles - 1);
+  const long long own = rec.seg + static_cast<long long>(g) * rec.row_tiles + c0;  // number of the first piece
+  const int own_n = c1 - c0 + 1;
+  if (p.prefix_tiles == 0 && own_n == 1) return;  // finished by its CTA
+  long long pre = 0;
+  int pre_n = 0, pre_at = 0;
+  if (p.prefix_tiles > 0) {
+    const long long m = static_cast<long long>(row) * a.group + h, rt = m / p.cut.mt;
+    pre_at = static_cast<int>(m - rt * p.cut.mt);
+    const long long seg = static_cast<long long>(g) * p.prefix_row_tiles + rt, from = seg * p.prefix_tiles;
+    const int d0 = at_owner(W, C, from);
+    pre_n = at_owner(W, C, from + p.prefix_tiles - 1) - d0 + 1;
+    pre = seg + d0;
+  }
+  const bool in = lane * 4 < a.d;
+  const int parts = own_n + pre_n;
+  float m = -INFINITY, l = 0.f;
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  // eight pieces at a time: their loads go out together
+  for (int s0 = 0; s0 < parts; s0 += 8) {
+    float2 q[8];
+    float4 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int s = s0 + i;
+      const long long r = s < pre_n ? (pre + s) * p.cut.mt + pre_at : (own + s - pre_n) * p.cut.mt + at;
+      q[i] = s < parts ? a.part_ml[r] : make_float2(-INFINITY, 0.f);
+      y[i] = s < parts && in ? *reinterpret_cast<const float4*>(a.part_o + r * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    ar_merge8(q, y, &m, &l, &x);
+  }
+  if (in) at_put<QT>(p, row, head, lane * 4, x, m, l);
+}
+
+}  // namespace
+}  // namespace wsg
+
+using namespace wsg;
+
+extern "C" size_t attn_tree_paged_workspace(const attn_tree_args* a) {
+  if (!a || !attn_tree_sizes_ok(a)) return 0;
+  DeviceInfo di;
+  if (device_info(&di, nullptr) != DEC_OK) return 0;
+  return attn_tree_plan(a, di.sms).total;
+}
+
+extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
+  if (!a) return fail(nullptr, DEC_EINVAL, "attn_tree_paged: NULL arguments");
+  if (!attn_tree_sizes_ok(a))
+    return fail(nullptr, DEC_EINVAL,
+                "attn_tree_paged: batch %d, rows %d, n_q %d, n_kv %d, head_dim %d, qdtype %d, kvdtype %d, mask_words %d, "
+                "prefix_len %d, page_size %d, num_pages %d, table_stride %d",
+                a->batch, a->rows, a->n_q, a->n_kv, a->head_dim, a->qdtype, a->kvdtype, a->mask_words, a->prefix_len,
+                a->page_size, a->num_pages, a->table_stride);
+  if (a->batch == 0 || a->rows == 0) return DEC_OK;
+  const long long width = static_cast<long long>(a->n_q) * a->head_dim;
+  if (!a->q || !a->out || !a->row_start || !a->seq_len || (a->prefix_len > 0 && (!a->prefix_k || !a->prefix_v)) ||
+      (a->table_stride > 0 && (!a->page_table || !a->k_pages || !a->v_pages)))
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: NULL pointer");
+  if (a->q_stride < 0 || (a->rows > 1 && a->out_stride < width) || (a->prefix_len > 0 && a->prefix_stride < a->prefix_len))
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: q_stride %lld, out_stride %lld, prefix_stride %lld",
+                static_cast<long long>(a->q_stride), static_cast<long long>(a->out_stride),
+                static_cast<long long>(a->prefix_stride));
+  const bool pages = a->table_stride > 0;
+  if ((a->prefix_len > 0 && (!aligned16(a->prefix_k) || !aligned16(a->prefix_v))) ||
+      (pages && (!aligned16(a->k_pages) || !aligned16(a->v_pages))))
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: prefix and pools must be 16-byte aligned");
+  if (!aligned_to(elem_bytes(a->qdtype), a->q, a->out) || !aligned_to(4, a->lse, a->row_start, a->mask, a->seq_len) ||
+      (pages && !aligned_to(4, a->page_table)))
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: a pointer is not aligned to its elements");
+  if (!a->d_workspace || reinterpret_cast<uintptr_t>(a->d_workspace) % 256)
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: workspace must be non-NULL and 256-byte aligned");
+  // (a row's output is written while others, and other heads' CTAs, have yet to read their queries: only in place)
+  if (a->out == a->q && a->rows > 1 && a->out_stride != a->q_stride)
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: out over q needs q's stride");
+  const size_t qe = elem_bytes(a->qdtype), rows = a->rows, batch = a->batch;
+  const Span q = span_rows(a->out == a->q ? nullptr : a->q, a->rows, a->q_stride, width, qe);
+  if (outputs_meet({span_rows(a->out, a->rows, a->out_stride, width, qe), {a->lse, 4 * rows * a->n_q},
+                    {a->d_workspace, a->workspace_bytes}},
+                   {q, {a->row_start, 4 * (batch + 1)}, {a->mask, 4 * rows * a->mask_words}, {a->seq_len, 4 * batch},
+                    {pages ? a->page_table : nullptr, 4 * batch * a->table_stride}}))
+    return fail(nullptr, DEC_EINVAL, "attn_tree_paged: an output overlaps another argument");
+  DeviceInfo di;
+  const dec_status st = device_info(&di, nullptr);
+  if (st != DEC_OK) return st;
+  if (di.sms < kAtBatch / 64) return fail(nullptr, DEC_EDEVICE, "attn_tree_paged: %d SMs", di.sms);
+  const AtPlan p = attn_tree_plan(a, di.sms);
+  if (a->workspace_bytes < p.total)
+    return fail(nullptr, DEC_ENOMEM, "attn_tree_paged: workspace has %zu bytes, %zu needed", a->workspace_bytes, p.total);
+  char* w = static_cast<char*>(a->d_workspace);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  AtArgs t{};
+  AmArgs& k = t.a;
+  k.batch = a->batch;
+  k.n_q = a->n_q;
+  k.n_kv = a->n_kv;
+  k.d = a->head_dim;
+  k.group = a->n_q / a->n_kv;
+  k.rows = a->rows;
+  k.q = a->q;
+  k.q_stride = a->q_stride;
+  k.pk = a->prefix_k;
+  k.pv = a->prefix_v;
+  k.plen = a->prefix_len;
+  k.pstride = a->prefix_stride;
+  k.kp = a->k_pages;
+  k.vp = a->v_pages;
+  k.pool = PagePool{a->num_pages, a->n_kv, page_shift(a->page_size), a->table_stride};
+  k.table = a->page_table;
+  k.len = a->seq_len;
+  k.scale_log2 = a->scale == 0.f ? 1.f : fabsf(a->scale) * 1.44269504088896340736f;
+  k.q_sign = a->scale == 0.f ? 0 : a->scale < 0.f ? -1 : 1;
+  k.q_even = reinterpret_cast<uintptr_t>(a->q) % 4 == 0 && a->q_stride % 2 == 0;
+  k.part_o = reinterpret_cast<float*>(w + p.o);
+  k.part_ml = reinterpret_cast<float2*>(w + p.ml);
+  k.err = di.err;
+  t.cut = p.cut;
+  t.row_start = a->row_start;
+  t.mask = a->mask;
+  t.words = a->mask_words;
+  t.prefix_row_tiles = p.prefix_row_tiles;
+  t.prefix_tiles = p.prefix_tiles;
+  t.out = a->out;
+  t.out_stride = a->out_stride;
+  t.lse = a->lse;
+  t.rec = reinterpret_cast<AtRow*>(w + p.rec);
+  t.total = reinterpret_cast<long long*>(w + p.line);
+  const bool qf = a->qdtype == DEC_F32;
+  WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_tree_f32(t, qf, di, s) : launch_tree_bf16(t, qf, di, s));
+  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a->rows) * a->n_q + 3) / 4);
+  WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_tree_join_kernel<float>, dim3(grid), dim3(128), 0, s, true, t, di.sms)
+                           : launch_k(attn_tree_join_kernel<uint16_t>, dim3(grid), dim3(128), 0, s, true, t, di.sms));
+  return DEC_OK;
+}

@@ -1,0 +1,116 @@
+// How a call of attn_tree_paged is cut up, and its limits on sizes: arithmetic in
+// plain C++ for host and device, so that it can be tested without a GPU.
+//
+// The work is a line of key tiles: first those of the shared prefix, head by head and,
+// within a head, row tile by row tile (of all rows of the step); then request by
+// request, head by head, row tile by row tile those of the request's own keys. The
+// tiles of one (request, head, row tile) are a segment. CTA c of C takes the tiles
+// [c W / C, (c + 1) W / C) of the W in all, across segments; its part of a segment is
+// a piece. Numbering segments j = 0, 1, .. along the line, the piece of CTA c in
+// segment j has the number c + j: along the line every new piece has a new c or a new
+// j, so no two share a number.
+#pragma once
+#include <cstdint>
+
+#include "../../include/wsg.h"
+#include "paging.h"
+
+namespace wsg {
+
+constexpr int kAtBatch = 4096, kAtKeys = 128;  // requests; keys a tile
+
+// What the cutting goes by.
+struct AtCut {
+  int group, n_kv, mt;     // mt: rows (token, query head of the group) of a row tile
+  int chain;               // no mask: a row sees the rows up to itself
+  long long capacity;      // tokens that a table row can hold
+};
+
+WSG_HD int at_up(long long x, long long y) { return static_cast<int>((x + y - 1) / y); }
+WSG_HD int at_row_tiles(const AtCut& c, int rows) { return at_up(static_cast<long long>(rows) * c.group, c.mt); }
+
+// Keys that row tile t of a request of n tokens and `rows` rows looks at, and its key
+// tiles (one at least: a row without keys has a result too).
+WSG_HD int at_keys(const AtCut& c, int n, int rows, int t) {
+  int seen = rows;
+  if (c.chain) {
+    const long long last = (static_cast<long long>(t + 1) * c.mt - 1) / c.group + 1;
+    if (last < seen) seen = static_cast<int>(last);
+  }
+  const long long keys = static_cast<long long>(n) + seen;
+  return static_cast<int>(keys < c.capacity ? keys : c.capacity);
+}
+WSG_HD int at_tiles(const AtCut& c, int n, int rows, int t) {
+  const int k = at_up(at_keys(c, n, rows, t), kAtKeys);
+  return k < 1 ? 1 : k;
+}
+// Key tiles of one head of a request.
+WSG_HD int at_head_tiles(const AtCut& c, int n, int rows) {
+  const int T = at_row_tiles(c, rows);
+  if (!c.chain) return T * at_tiles(c, n, rows, 0);
+  int sum = 0;
+  for (int t = 0; t < T; ++t) sum += at_tiles(c, n, rows, t);
+  return sum;
+}
+
+// First tile of CTA c of C on a line of W tiles, and the CTA that has tile p.
+WSG_HD long long at_first(long long W, int C, int c) { return c * W / C; }
+WSG_HD int at_owner(long long W, int C, long long p) { return static_cast<int>(((p + 1) * C - 1) / W); }
+
+inline bool attn_tree_sizes_ok(const attn_tree_args* a) {
+  auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
+  return a->batch >= 0 && a->batch <= kAtBatch && a->rows >= 0 && a->n_kv >= 1 && a->n_q >= a->n_kv && a->n_q <= 65535 &&
+         static_cast<long long>(a->rows) * a->n_q < 1ll << 24 && a->n_q % a->n_kv == 0 && a->n_q / a->n_kv <= 16 &&
+         a->head_dim >= 8 && a->head_dim <= 128 && a->head_dim % 8 == 0 && type(a->qdtype) && type(a->kvdtype) &&
+         a->prefix_len >= 0 && page_shift(a->page_size) >= 0 && a->num_pages >= 0 && a->table_stride >= 0 &&
+         a->mask_words >= 0 && a->mask_words <= 1 << 20 &&
+         (static_cast<long long>(a->table_stride) << page_shift(a->page_size)) + a->prefix_len <= (1ll << 30);
+}
+
+// Which kernel runs, and the workspace.
+struct AtPlan {
+  bool tc;            // attn_tree_tc_kernel
+  AtCut cut;
+  int prefix_row_tiles, prefix_tiles;  // of a head; of a segment
+  long long pieces;   // numbers that pieces can have
+  size_t o, ml, rec, line, total;  // workspace: outputs, (reference, sum), a record a row, the line's length
+};
+
+// Where a row's pieces are: its own segment starts at tile `line` for head 0 and takes
+// `tiles` of it (0: a row without a result), `head` tiles on for the next head; its
+// number is seg for head 0, row_tiles on for the next.
+struct AtRow {
+  long long line;
+  int32_t head, tiles, seg, row_tiles;
+  int32_t at, next;  // row (token * group) within the row tile; tiles of the row tile behind it
+};
+
+inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
+  AtPlan p{};
+  p.total = 256;
+  if (a->batch == 0 || a->rows == 0) return p;
+  const int group = a->n_q / a->n_kv;
+  p.cut.group = group;
+  p.cut.n_kv = a->n_kv;
+  p.cut.chain = a->mask == nullptr;
+  p.cut.capacity = static_cast<long long>(a->table_stride) << page_shift(a->page_size);
+  p.tc = false;
+  p.cut.mt = p.tc ? 128 : 16;
+  if (a->prefix_len > 0) {
+    p.prefix_row_tiles = at_row_tiles(p.cut, a->rows);
+    p.prefix_tiles = at_up(a->prefix_len, kAtKeys);
+  }
+  // the requests' row tiles: rows * group / mt whole ones at most, one more each
+  const long long own = static_cast<long long>(a->rows) * group / p.cut.mt + (a->batch < a->rows ? a->batch : a->rows);
+  p.pieces = sms + (own + p.prefix_row_tiles) * a->n_kv;
+  auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+  const size_t rows = static_cast<size_t>(p.pieces) * p.cut.mt;
+  p.o = 0;
+  p.ml = up(rows * a->head_dim * 4);
+  p.rec = p.ml + up(rows * 8);
+  p.line = p.rec + up(static_cast<size_t>(a->rows) * sizeof(AtRow));
+  p.total = p.line + 256;
+  return p;
+}
+
+}  // namespace wsg

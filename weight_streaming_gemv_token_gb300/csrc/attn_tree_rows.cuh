@@ -1,0 +1,556 @@
+// Attention of a step's rows on warp-level matrix instructions, for every type, head
+// size and page size: row tiles of 16 rows (attn_tree_plan.h), a CTA a share of the
+// line of key tiles, its eight warps the blocks of a piece's keys in turn, each
+// through rings of its own (attn_rows.cuh: bfloat16 caches, keys as the M side; float32
+// caches as in attn_mma.cuh: tf32 value and remainder, three products).
+//
+// Blocks that hold drafted rows' keys mask scores row by row. A value that is not
+// finite would reach rows that do not see it through its product with a weight of 0,
+// so in these blocks it enters the products as 0 and is added afterwards to the rows
+// that see it, which it makes not finite.
+#pragma once
+#include "attn_tree.cuh"
+
+namespace wsg {
+
+__device__ __forceinline__ bool at_odd16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }  // a bfloat16 that is not finite
+__device__ __forceinline__ uint32_t at_finite2(uint32_t p) {  // such halves become 0
+  if (at_odd16(p)) p &= 0xFFFF0000u;
+  if (at_odd16(p >> 16)) p &= 0xFFFFu;
+  return p;
+}
+__device__ __forceinline__ bool at_odd(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
+
+// ---- bfloat16 caches -------------------------------------------------------------
+
+template <typename QT, int DP, int QP>
+struct AtCore16 : ArCore<QT, DP, QP, 16> {
+  using Base = ArCore<QT, DP, QP, 16>;
+  static constexpr int KB = 16, TILE = Base::TILE, PITCH = Base::PITCH, KK = Base::KK, PP = Base::PP;
+  static constexpr int RING = 4 * TILE;
+
+  // row, keys' words: seen[t][j] of row 8 t + 2 (lane % 4) + j
+  __device__ __forceinline__ static int row_of(int i) { return 8 * (i >> 1) + 2 * (threadIdx.x & 3) + (i & 1); }
+
+  __device__ __forceinline__ void consume_drafts(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale,
+                                                 const uint32_t (&seen)[4]) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t vt = kt + TILE;
+    float s[2][4] = {};
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      uint32_t ka[4];
+      am_ld4(ka, kt + (lane & 15) * PITCH + k * 32 + (lane >> 4) * 16);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < QP; ++i) am_mma16(s[t], ka, this->q[i][k][t][0], this->q[i][k][t][1]);
+    }
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (!(((ok & seen[2 * t + (i & 1)]) >> ((lane >> 2) + 8 * (i >> 1))) & 1u)) s[t][i] = -INFINITY;
+    uint32_t p[2][PP][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      float mx[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        mx[j] = fmaxf(s[t][j], s[t][2 + j]);
+        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
+        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
+        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16)) * scale;
+      }
+      if (__any_sync(0xffffffffu, mx[0] > this->m[t][0] + kAmMargin || mx[1] > this->m[t][1] + kAmMargin)) {
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float nr = mx[j] > this->m[t][j] + kAmMargin ? mx[j] : this->m[t][j];
+          const float f = nr == this->m[t][j] ? 1.f : am_exp2(this->m[t][j] - nr);
+          this->m[t][j] = nr;
+          this->l[t][j] *= f;
+#pragma unroll
+          for (int k = 0; k < KK; ++k) this->o[k][t][j] *= f, this->o[k][t][2 + j] *= f;
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const float mu = this->m[t][j] == -INFINITY ? 0.f : this->m[t][j];
+        s[t][j] = am_exp2(fmaf(s[t][j], scale, -mu));
+        s[t][2 + j] = am_exp2(fmaf(s[t][2 + j], scale, -mu));
+        this->l[t][j] += s[t][j] + s[t][2 + j];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t w[PP];
+        am_split_bf16<PP>(s[t][2 * h], s[t][2 * h + 1], w);
+#pragma unroll
+        for (int i = 0; i < PP; ++i) p[t][i][h] = ar_transpose(w[i]);
+      }
+    }
+    bool odd = false;
+#pragma unroll
+    for (int k = 0; k < KK; ++k) {
+      uint32_t va[4];
+      am_ld4t(va, vt + ((lane >> 4) * 8 + (lane & 7)) * PITCH + k * 32 + ((lane >> 3) & 1) * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t c = at_finite2(va[i]);
+        odd |= c != va[i];
+        va[i] = c;
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < PP; ++i) am_mma16(this->o[k][t], va, p[t][i][0], p[t][i][1]);
+    }
+    if (__any_sync(0xffffffffu, odd)) {
+      for (int key = 0; key < 16; ++key)
+#pragma unroll
+        for (int k = 0; k < KK; ++k)
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const uint16_t v = *reinterpret_cast<const uint16_t*>(vp + key * PITCH + (k * 16 + h * 8 + (lane >> 2)) * 2);
+            if (!at_odd16(v)) continue;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+              for (int j = 0; j < 2; ++j)
+                if ((ok & seen[2 * t + j]) >> key & 1u) this->o[k][t][2 * h + j] += bf16_to_f32(v);
+          }
+    }
+  }
+
+  __device__ __forceinline__ void block(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale, bool drafts,
+                                        const uint32_t (&seen)[4]) {
+    if (drafts)
+      consume_drafts(kt, vp, ok, scale, seen);
+    else
+      this->consume(kt, ok, scale);
+  }
+
+  // each row's reference and sum, one lane a row
+  template <typename F>
+  __device__ __forceinline__ void sums(F put) {
+    const int lane = threadIdx.x & 31;
+    this->finish();
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        if (lane < 4) put(t * 8 + 2 * lane + j, this->m[t][j], this->l[t][j]);
+  }
+  // outputs of row r times f(r, reference) to put(r, element, value)
+  template <typename F, typename P>
+  __device__ __forceinline__ void outputs(int nrows, F f, P put) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int r = t * 8 + 2 * (lane & 3) + j;
+        if (r >= nrows) continue;
+        const float x = f(r, this->m[t][j]);
+#pragma unroll
+        for (int k = 0; k < KK; ++k) {
+          put(r, k * 16 + (lane >> 2), this->o[k][t][j] * x);
+          put(r, k * 16 + 8 + (lane >> 2), this->o[k][t][2 + j] * x);
+        }
+      }
+  }
+};
+
+template <int DP>
+struct AtCopy16 : ArCopy<DP> {
+  using ArCopy<DP>::ArCopy;
+  __device__ __forceinline__ uint32_t prefix(const AmArgs& a, int stage, int g, int k, int n) const {
+    return this->run(stage, a.pk, a.pv, a.pstride * g + k, n);
+  }
+};
+
+// ---- float32 caches --------------------------------------------------------------
+
+// The state of 16 rows against a stream of blocks of 8 keys; lane: rows lane / 4 and
+// that + 8, keys 2 (lane % 4) and the next of a block's scores.
+template <typename QT, int DP, int QP>
+struct AtCore32 {
+  static constexpr int KB = 8, PITCH = DP * 4 + 16, TILE = KB * PITCH, NT = DP / 8;
+  static constexpr int RING = 4 * TILE;
+  float o[NT][4];
+  float m[2], l[2];
+  const uint4* frag;  // queries in shared memory: [part][k step][lane], split once a piece
+
+  __device__ __forceinline__ static int row_of(int i) { return ((threadIdx.x & 31) >> 2) + 8 * (i & 1); }
+
+  __device__ __forceinline__ void clear() {
+    m[0] = m[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) o[n][0] = o[n][1] = o[n][2] = o[n][3] = 0.f;
+  }
+
+  template <bool DRAFTS>
+  __device__ __forceinline__ void consume(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale,
+                                          const uint32_t (&seen)[4]) {
+    const int lane = threadIdx.x & 31;
+    float s[4] = {}, s2[4] = {}, s3[4] = {};  // the remainders' products are chains of their own
+#pragma unroll
+    for (int kk = 0; kk < DP / 16; ++kk) {
+      uint32_t b[4];
+      am_ld4(b, kt + (lane & 7) * PITCH + kk * 64 + (lane >> 3) * 16);
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        uint32_t bh0, bl0, bh1, bl1;
+        am_split_tf32(__uint_as_float(b[2 * h]), &bh0, &bl0);
+        am_split_tf32(__uint_as_float(b[2 * h + 1]), &bh1, &bl1);
+        const uint4 fh = frag[(2 * kk + h) * 32 + lane], fl = frag[NT * 32 + (2 * kk + h) * 32 + lane];
+        const uint32_t qh[4] = {fh.x, fh.y, fh.z, fh.w}, ql[4] = {fl.x, fl.y, fl.z, fl.w};
+        am_mma8(s, qh, bh0, bh1);
+        am_mma8(s2, qh, bl0, bl1);
+        am_mma8(s3, ql, bh0, bh1);
+      }
+    }
+    // register j is row lane / 4 + 8 (j / 2), key 2 (lane % 4) + j % 2
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      s[j] += s2[j] + s3[j];
+      const uint32_t may = DRAFTS ? ok & seen[j >> 1] : ok;
+      if (!(may >> (2 * (lane & 3) + (j & 1)) & 1u)) s[j] = -INFINITY;
+    }
+    float mx[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      mx[h] = fmaxf(s[2 * h], s[2 * h + 1]);
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 1));
+      mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], 2)) * scale;
+    }
+    if (__any_sync(0xffffffffu, mx[0] > m[0] + kAmMargin || mx[1] > m[1] + kAmMargin)) {
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const float nr = mx[h] > m[h] + kAmMargin ? mx[h] : m[h];
+        const float f = nr == m[h] ? 1.f : am_exp2(m[h] - nr);  // 0 on the first move
+        m[h] = nr;
+        l[h] *= f;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) o[n][2 * h] *= f, o[n][2 * h + 1] *= f;
+      }
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const float mu = m[h] == -INFINITY ? 0.f : m[h];  // nothing seen yet: every term is 0
+#pragma unroll
+      for (int j = 2 * h; j < 2 * h + 2; ++j) s[j] = am_exp2(fmaf(s[j], scale, -mu));
+      l[h] += s[2 * h] + s[2 * h + 1];  // this lane's keys only
+    }
+    // A column c is key 2 c, column c + 4 key 2 c + 1: the scores' own registers
+    uint32_t ph[4], pl[4];
+    am_split_tf32(s[0], &ph[0], &pl[0]);
+    am_split_tf32(s[2], &ph[1], &pl[1]);
+    am_split_tf32(s[1], &ph[2], &pl[2]);
+    am_split_tf32(s[3], &ph[3], &pl[3]);
+    const unsigned char* vrow = vp + 2 * (lane & 3) * PITCH + (lane >> 2) * 4;
+    bool odd = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float v0 = *reinterpret_cast<const float*>(vrow + n * 32), v1 = *reinterpret_cast<const float*>(vrow + PITCH + n * 32);
+      if (DRAFTS) {
+        if (at_odd(v0)) v0 = 0.f, odd = true;
+        if (at_odd(v1)) v1 = 0.f, odd = true;
+      }
+      uint32_t bh0, bl0, bh1, bl1;
+      am_split_tf32(v0, &bh0, &bl0);
+      am_split_tf32(v1, &bh1, &bl1);
+      am_mma8(o[n], ph, bh0, bh1);
+      am_mma8(o[n], ph, bl0, bl1);
+      am_mma8(o[n], pl, bh0, bh1);
+    }
+    if (DRAFTS && __any_sync(0xffffffffu, odd)) {
+      for (int key = 0; key < 8; ++key)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float v = *reinterpret_cast<const float*>(vp + key * PITCH + (n * 8 + 2 * (lane & 3) + e) * 4);
+            if (!at_odd(v)) continue;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+              if ((ok & seen[h]) >> key & 1u) o[n][2 * h + e] += v;
+          }
+    }
+  }
+
+  __device__ __forceinline__ void block(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale, bool drafts,
+                                        const uint32_t (&seen)[4]) {
+    if (drafts)
+      consume<true>(kt, vp, ok, scale, seen);
+    else
+      consume<false>(kt, vp, ok, scale, seen);
+  }
+
+  template <typename F>
+  __device__ __forceinline__ void sums(F put) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 1);
+      l[h] += __shfl_xor_sync(0xffffffffu, l[h], 2);
+      if ((lane & 3) == 0) put(h * 8 + (lane >> 2), m[h], l[h]);
+    }
+  }
+  template <typename F, typename P>
+  __device__ __forceinline__ void outputs(int nrows, F f, P put) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const int r = h * 8 + (lane >> 2);
+      if (r >= nrows) continue;
+      const float x = f(r, m[h]);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        put(r, n * 8 + 2 * (lane & 3), o[n][2 * h] * x);
+        put(r, n * 8 + 2 * (lane & 3) + 1, o[n][2 * h + 1] * x);
+      }
+    }
+  }
+};
+
+// A block's 8 keys and values into a stage by one warp; the mask of the keys that
+// count (the others arrive as zeros).
+template <int DP>
+struct AtCopy32 {
+  static constexpr int KB = 8, PITCH = DP * 4 + 16, TILE = KB * PITCH;
+  static constexpr int CP = DP / 4, KPI = 32 / CP > 0 ? 32 / CP : 1, STEPS = KB * CP / 32;
+  int row_bytes, chunks;
+  uint32_t ring;
+  int lkey, lc;
+
+  __device__ __forceinline__ AtCopy32(int d, unsigned char* at) {
+    const int lane = threadIdx.x & 31;
+    row_bytes = d * 4;
+    chunks = d / 4;
+    ring = smem_u32(at);
+    lkey = lane / CP, lc = lane % CP;
+  }
+  __device__ __forceinline__ void pad(int d, unsigned char* at) const {  // columns past the head stay zero
+    const int n = CP - chunks;
+    if (n > 0)
+      for (int i = threadIdx.x & 31; i < 4 * KB * n; i += 32)
+        *reinterpret_cast<uint4*>(at + i / n * PITCH + (chunks + i % n) * 16) = make_uint4(0, 0, 0, 0);
+  }
+  __device__ __forceinline__ uint32_t run(int stage, const void* kb, const void* vb, long long row, int n) const {
+    const uint32_t dst = ring + stage * 2 * TILE + lkey * PITCH + lc * 16;
+    const long long off = row * row_bytes + lkey * row_bytes + lc * 16;
+    const char *ks = static_cast<const char*>(kb) + off, *vs = static_cast<const char*>(vb) + off;
+    if (lc < chunks) {
+#pragma unroll
+      for (int i = 0; i < STEPS; ++i) {
+        const bool in = lkey + i * KPI < n;
+        am_copy16(dst + i * KPI * PITCH, in ? ks + i * (KPI * row_bytes) : kb, in ? 16 : 0);
+        am_copy16(dst + i * KPI * PITCH + TILE, in ? vs + i * (KPI * row_bytes) : vb, in ? 16 : 0);
+      }
+    }
+    return (1u << n) - 1u;
+  }
+  __device__ __forceinline__ uint32_t prefix(const AmArgs& a, int stage, int g, int k, int n) const {
+    return run(stage, a.pk, a.pv, a.pstride * g + k, n);
+  }
+  __device__ __forceinline__ uint32_t pages(const AmArgs& a, int stage, const int32_t* trow, int32_t entry, int g, int k,
+                                            int n) const {
+    const int lane = threadIdx.x & 31;
+    if (a.pool.shift >= 3) {  // the block lies in one page
+      const int page = entry >= 0 && entry < a.pool.num_pages ? entry : -1;
+      if (page < 0 && lane == 0) atomicOr(a.err, ERR_BAD_PAGE);
+      return run(stage, a.kp, a.vp, page < 0 ? 0 : pool_row(a.pool, page, g, k), page < 0 ? 0 : n);
+    }
+    long long row = -1;  // lane `key` looks its own page up
+    if (lane < n) {
+      const int page = page_of(a.pool, trow, k + lane);
+      if (page >= 0)
+        row = pool_row(a.pool, page, g, k + lane);
+      else
+        atomicOr(a.err, ERR_BAD_PAGE);
+    }
+    const uint32_t dst = ring + stage * 2 * TILE + lkey * PITCH + lc * 16;
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      const long long r = __shfl_sync(0xffffffffu, row, lkey + i * KPI);
+      if (lc < chunks) {
+        const long long off = r < 0 ? 0 : r * row_bytes + lc * 16;
+        am_copy16(dst + i * KPI * PITCH, static_cast<const char*>(a.kp) + off, r < 0 ? 0 : 16);
+        am_copy16(dst + i * KPI * PITCH + TILE, static_cast<const char*>(a.vp) + off, r < 0 ? 0 : 16);
+      }
+    }
+    return __ballot_sync(0xffffffffu, row >= 0);
+  }
+};
+
+// ---- the kernel --------------------------------------------------------------------
+
+template <typename QT, int DP, bool F32>
+struct AtGeom {
+  static constexpr int WARPS = 8;
+  static constexpr int RING = F32 ? 4 * 8 * (DP * 4 + 16) : 4 * 16 * (DP * 2 + 16);
+  static constexpr int JOIN = 16 * DP * 4;
+  static constexpr int PER_WARP = RING > JOIN ? RING : JOIN;
+  static constexpr int QBYTES = F32 ? 2 * (DP / 8) * 32 * 16 : 0;
+  static constexpr int SMEM = QBYTES + WARPS * PER_WARP;
+};
+
+template <typename QT, int DP, int QP, bool F32>
+__global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) {
+  using G = AtGeom<QT, DP, F32>;
+  using Core = std::conditional_t<F32, AtCore32<QT, DP, QP>, AtCore16<QT, DP, QP>>;
+  using Copy = std::conditional_t<F32, AtCopy32<DP>, AtCopy16<DP>>;
+  constexpr int WARPS = G::WARPS, KB = Core::KB, NTHREADS = 32 * WARPS;
+  extern __shared__ __align__(128) unsigned char am_raw[];
+  __shared__ AtShared sh;
+  __shared__ float s_m[WARPS][16], s_l[WARPS][16];
+  const AmArgs& a = p.a;
+  const int tid = threadIdx.x, warp = tid >> 5;
+  unsigned char* mine = am_raw + G::QBYTES + warp * G::PER_WARP;
+  const uint32_t ring = smem_u32(mine);
+  const Copy copy(a.d, mine);
+  pdl_wait();
+  pdl_trigger();
+  AtWalk walk;
+  walk.start<NTHREADS>(p, sh);
+  AtPiece pc;
+  for (bool again = false; walk.next(p, sh, &pc); again = true) {
+    if (again) __syncthreads();  // the piece before this one has left shared memory
+    if constexpr (F32) {
+      copy.pad(a.d, mine);
+    } else if (again && a.d < DP) {
+      Copy(a.d, mine);  // (zeroes the columns past the head)
+    }
+    const int row0 = pc.m0, nrows = pc.nrows;
+    auto src_of = [&](int r) {
+      const int m = row0 + r, token = m / a.group;
+      return a.q_stride * (pc.begin + token) + static_cast<long long>(pc.g * a.group + m - token * a.group) * a.d;
+    };
+    const int32_t* trow = pc.prefix ? nullptr : a.table + static_cast<long long>(pc.s) * a.pool.width;
+    const int nblk = max(0, (pc.k1 - pc.k0 + KB - 1) / KB);
+    auto entry = [&](int blk) {
+      return !pc.prefix && blk < nblk && (KB >> a.pool.shift) <= 1 ? trow[(pc.k0 + blk * KB) >> a.pool.shift] : 0;
+    };
+    auto request = [&](int stage, int blk, int32_t e) {
+      const int k = pc.k0 + blk * KB, n = min(KB, pc.k1 - k);
+      return pc.prefix ? copy.prefix(a, stage, pc.g, k, n) : copy.pages(a, stage, trow, e, pc.g, k, n);
+    };
+    int32_t e0 = entry(warp), e1 = entry(warp + WARPS);
+    __syncwarp();
+    uint32_t ok = 0;
+    if (warp < nblk) ok = request(0, warp, e0);
+    am_commit();
+    Core core;
+    if constexpr (F32) {
+      core.clear();
+      core.frag = reinterpret_cast<const uint4*>(am_raw);
+      for (int i = tid; i < 16 * (DP / 8); i += NTHREADS) {
+        // 8 elements of a row, in the order of the A fragments: [part][k step][lane][register]
+        const int r = i / (DP / 8), e = i % (DP / 8) * 8;
+        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+        if (r < nrows && e < a.d) {
+          const QT* src = static_cast<const QT*>(a.q) + src_of(r) + e;
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if constexpr (sizeof(QT) == 4)
+              x[j] = src[j] * a.q_sign;
+            else
+              x[j] = bf16_to_f32(src[j]) * a.q_sign;
+          }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int ln = (r % 8) * 4 + j % 4, reg = r / 8 + 2 * (j / 4);
+          uint32_t hi, lo;
+          am_split_tf32(x[j], &hi, &lo);
+          uint32_t* f = reinterpret_cast<uint32_t*>(am_raw) + ((e / 8) * 32 + ln) * 4 + reg;
+          f[0] = hi;
+          f[(DP / 8) * 32 * 4] = lo;
+        }
+      }
+      __syncthreads();
+    } else {
+      core.load(a, nrows, src_of);
+    }
+    int token[4];  // of the rows whose scores this lane masks
+#pragma unroll
+    for (int i = 0; i < 4; ++i) token[i] = min(row0 + Core::row_of(i), row0 + nrows - 1) / a.group;
+    int stage = 0;
+    for (int blk = warp; blk < nblk; blk += WARPS, stage ^= 1) {
+      __syncwarp();  // every lane is done with the block before this one
+      const uint32_t next = blk + WARPS < nblk ? request(stage ^ 1, blk + WARPS, e1) : 0;
+      am_commit();
+      e1 = entry(blk + 2 * WARPS);
+      const int k = pc.k0 + blk * KB;
+      const bool drafts = !pc.prefix && k + KB > pc.n;
+      uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+      if (drafts)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) seen[i] = at_seen(p, pc.begin, token[i], k - pc.n);
+      am_wait<1>();
+      __syncwarp();  // this block has landed for every lane
+      const uint32_t kt = ring + stage * 2 * Core::TILE;
+      core.block(kt, mine + stage * 2 * Core::TILE + Core::TILE, ok, a.scale_log2, drafts, seen);
+      ok = next;
+    }
+    am_wait<0>();
+    core.sums([&](int r, float m, float l) { s_m[warp][r] = m, s_l[warp][r] = l; });
+    __syncthreads();  // every warp is past its ring
+    float* out = reinterpret_cast<float*>(mine);
+    core.outputs(
+        nrows,
+        [&](int r, float mine_m) {
+          float m = -INFINITY;
+#pragma unroll
+          for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
+          return m == -INFINITY ? 1.f : am_exp2(mine_m - m);
+        },
+        [&](int r, int e, float x) { out[r * DP + e] = x; });
+    __syncthreads();
+    for (int i = tid; i < nrows * (DP / 4); i += NTHREADS) {
+      const int r = i / (DP / 4), e = i % (DP / 4) * 4;
+      if (e >= a.d) continue;
+      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(am_raw + G::QBYTES + w * G::PER_WARP + (r * DP + e) * 4);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+      }
+      float m = -INFINITY, sum = 0.f;
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
+#pragma unroll
+      for (int w = 0; w < WARPS; ++w) sum += m == -INFINITY ? s_l[w][r] : s_l[w][r] * am_exp2(s_m[w][r] - m);
+      if (pc.whole) {
+        const int token_ = (row0 + r) / a.group, head = pc.g * a.group + (row0 + r) % a.group;
+        at_put<QT>(p, pc.begin + token_, head, e, x, m, sum);
+      } else {
+        const long long at = pc.id * p.cut.mt + r;
+        *reinterpret_cast<float4*>(a.part_o + at * a.d + e) = x;
+        if (e == 0) a.part_ml[at] = make_float2(m, sum);
+      }
+    }
+  }
+}
+
+template <typename QT, int DP, int QP, bool F32>
+cudaError_t at_launch_one(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  constexpr size_t smem = AtGeom<QT, DP, F32>::SMEM;
+  static bool lifted[64] = {};
+  if (!lifted[di.device]) {
+    const cudaError_t e = allow_smem(attn_tree_rows_kernel<QT, DP, QP, F32>, smem);
+    if (e != cudaSuccess) return e;
+    lifted[di.device] = true;
+  }
+  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32>, dim3(di.sms), dim3(256), smem, st, true, a);
+}
+
+template <typename QT, int QP, bool F32>
+cudaError_t at_launch(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  if (a.a.d <= 16) return at_launch_one<QT, 16, QP, F32>(a, di, st);
+  if (a.a.d <= 64) return at_launch_one<QT, 64, QP, F32>(a, di, st);
+  return at_launch_one<QT, 128, QP, F32>(a, di, st);
+}
+
+}  // namespace wsg

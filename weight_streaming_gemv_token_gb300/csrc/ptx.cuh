@@ -21,6 +21,7 @@ enum : uint32_t {
   ERR_BAD_TOKEN = 1u << 2,      // an input token ID was outside [0, vocab)
   ERR_BAD_POSITION = 1u << 3,   // a position reached the KV capacity
   ERR_BAD_PAGE = 1u << 7,       // a sequence, page or parent index of the paged calls was out of range
+  ERR_BAD_TREE = 1u << 8,       // a drafted row hangs below no earlier row, or a tree has more rows than its mask
 };
 
 __device__ __forceinline__ uint32_t smem_u32(const void* p) {

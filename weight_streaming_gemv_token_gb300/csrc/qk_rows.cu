@@ -1,6 +1,6 @@
-// qk_norm_rope and kv_append_paged: per-head RMS norm of queries and keys with
+// qk_norm_rope, kv_append_paged and kv_append_slots: per-head RMS norm of queries and keys with
 // the position rotation in the same pass, and the store of keys and values
-// into pages ("Megakernels", "What runs in the DSL": per-head Q/K RMSNorm,
+// into pages, by tables or by a map of slots ("Megakernels", "What runs in the DSL": per-head Q/K RMSNorm,
 // RoPE, KV update).
 //
 // Mathematics: y = x / sqrt(mean(x^2) + eps) * g per head; the pair (a, b) at
@@ -47,6 +47,7 @@ struct QkRowsArgs {
   PagePool pool;
   const int32_t* table;
   const int32_t* seq;
+  const int64_t* slots;  // or NULL: by table and seq
   int n_seq, base_pos;
   uint32_t* err;
 };
@@ -244,14 +245,23 @@ __global__ void __launch_bounds__(kRowsThreads, 3) qk_rows_kernel(const QkRowsAr
     long long to = (kind == 0 ? a.qo_stride : a.ko_stride) * r + h0 * a.d + e0, step = a.d;
     bool stores = live;
     if (pool && live) {
-      const int s = a.seq ? a.seq[r] : static_cast<int>(r);
-      const long long idx = static_cast<long long>(pos) - a.base_pos;
-      const int page = s >= 0 && s < a.n_seq ? page_of(a.pool, a.table + static_cast<long long>(s) * a.pool.width, idx) : -1;
+      long long idx;
+      int page;
+      bool none = false;  // a slot of -1
+      if (a.slots) {
+        idx = a.slots[r];
+        none = idx == -1;
+        page = idx >= 0 && idx >> a.pool.shift < a.pool.num_pages ? static_cast<int>(idx >> a.pool.shift) : -1;
+      } else {
+        const int s = a.seq ? a.seq[r] : static_cast<int>(r);
+        idx = static_cast<long long>(pos) - a.base_pos;
+        page = s >= 0 && s < a.n_seq ? page_of(a.pool, a.table + static_cast<long long>(s) * a.pool.width, idx) : -1;
+      }
       stores = page >= 0;
       if (stores) {
         to = pool_row(a.pool, page, h0, idx) * a.d + e0;
         step = static_cast<long long>(a.d) << a.pool.shift;
-      } else if (li == 0) {
+      } else if (li == 0 && !none) {
         atomicOr(a.err, ERR_BAD_PAGE);
       }
     }
@@ -561,42 +571,72 @@ extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
   return run_rows(k, a->xdtype, di, static_cast<cudaStream_t>(stream));
 }
 
+namespace {
+
+// The checks and fields of both appends but those of the way to the pages.
+template <typename A>
+dec_status append_fields(const A* a, const char* who, QkRowsArgs* k, DeviceInfo* di) {
+  dec_status s = check_rows(a, who);
+  if (s != DEC_OK) return s;
+  if (a->n_kv < 1) return fail(nullptr, DEC_EINVAL, "%s: n_kv must be >= 1", who);
+  if (!is_float(a->kvdtype)) return fail(nullptr, DEC_EINVAL, "%s: kvdtype %d", who, a->kvdtype);
+  if (page_shift(a->page_size) < 0)
+    return fail(nullptr, DEC_EINVAL, "%s: page_size must be a power of two up to %d, got %d", who, kPageSizeMax, a->page_size);
+  if (a->num_pages < 0 || a->v_stride < 0)
+    return fail(nullptr, DEC_EINVAL, "%s: num_pages %d, v_stride %lld", who, a->num_pages, static_cast<long long>(a->v_stride));
+  if (a->rows == 0) return DEC_OK;
+  if (!a->v || !a->k_pages || !a->v_pages) return fail(nullptr, DEC_EINVAL, "%s: NULL pointer", who);
+  if (!aligned16(a->k_pages) || !aligned16(a->v_pages))
+    return fail(nullptr, DEC_EINVAL, "%s: the pools must be 16-byte aligned", who);
+  if (!aligned_to(elem_bytes(a->xdtype), a->v))
+    return fail(nullptr, DEC_EINVAL, "%s: a pointer is not aligned to its elements", who);
+  if (a->n_q > 0 && !in_place_ok(a->q, a->q_out, a->rows, a->xdtype, a->ydtype, a->q_stride, a->q_out_stride))
+    return fail(nullptr, DEC_EINVAL, "%s: q_out over q needs q's type and stride", who);
+  if ((s = device_info(di, nullptr)) != DEC_OK) return s;
+  *k = shared_fields(a);
+  k->v = a->v;
+  k->v_stride = a->v_stride;
+  k->vec_x = k->vec_x && pieces16(a->v, a->v_stride, a->xdtype);
+  k->k_out = a->k_pages;
+  k->v_out = a->v_pages;
+  k->paged = 1;
+  k->err = di->err;
+  k->kv_f32 = a->kvdtype == DEC_F32;
+  return DEC_OK;
+}
+
+}  // namespace
+
 extern "C" dec_status kv_append_paged(const kv_append_args* a, void* stream) {
   if (!a) return fail(nullptr, DEC_EINVAL, "kv_append_paged: NULL arguments");
-  dec_status s = check_rows(a, "kv_append_paged");
-  if (s != DEC_OK) return s;
-  if (a->n_kv < 1) return fail(nullptr, DEC_EINVAL, "kv_append_paged: n_kv must be >= 1");
-  if (!is_float(a->kvdtype)) return fail(nullptr, DEC_EINVAL, "kv_append_paged: kvdtype %d", a->kvdtype);
-  const int shift = page_shift(a->page_size);
-  if (shift < 0)
-    return fail(nullptr, DEC_EINVAL, "kv_append_paged: page_size must be a power of two up to %d, got %d", kPageSizeMax,
-                a->page_size);
-  if (a->n_seq < 0 || a->num_pages < 0 || a->table_stride < 0 || a->base_pos < 0 || a->v_stride < 0)
-    return fail(nullptr, DEC_EINVAL, "kv_append_paged: n_seq %d, num_pages %d, table_stride %d, base_pos %d", a->n_seq,
-                a->num_pages, a->table_stride, a->base_pos);
-  if (a->rows == 0) return DEC_OK;
-  if (!a->v || !a->k_pages || !a->v_pages || !a->page_table) return fail(nullptr, DEC_EINVAL, "kv_append_paged: NULL pointer");
-  if (!aligned16(a->k_pages) || !aligned16(a->v_pages))
-    return fail(nullptr, DEC_EINVAL, "kv_append_paged: the pools must be 16-byte aligned");
-  if (!aligned_to(elem_bytes(a->xdtype), a->v) || !aligned_to(4, a->page_table, a->seq))
+  if (a->n_seq < 0 || a->table_stride < 0 || a->base_pos < 0)
+    return fail(nullptr, DEC_EINVAL, "kv_append_paged: n_seq %d, table_stride %d, base_pos %d", a->n_seq, a->table_stride,
+                a->base_pos);
+  if (a->rows > 0 && !a->page_table) return fail(nullptr, DEC_EINVAL, "kv_append_paged: NULL pointer");
+  if (a->rows > 0 && !aligned_to(4, a->page_table, a->seq))
     return fail(nullptr, DEC_EINVAL, "kv_append_paged: a pointer is not aligned to its elements");
-  if (a->n_q > 0 && !in_place_ok(a->q, a->q_out, a->rows, a->xdtype, a->ydtype, a->q_stride, a->q_out_stride))
-    return fail(nullptr, DEC_EINVAL, "kv_append_paged: q_out over q needs q's type and stride");
+  QkRowsArgs k{};
   DeviceInfo di;
-  if ((s = device_info(&di, nullptr)) != DEC_OK) return s;
-  QkRowsArgs k = shared_fields(a);
-  k.v = a->v;
-  k.v_stride = a->v_stride;
-  k.vec_x = k.vec_x && pieces16(a->v, a->v_stride, a->xdtype);
-  k.k_out = a->k_pages;
-  k.v_out = a->v_pages;
-  k.paged = 1;
-  k.pool = PagePool{a->num_pages, a->n_kv, shift, a->table_stride};
+  const dec_status s = append_fields(a, "kv_append_paged", &k, &di);
+  if (s != DEC_OK || a->rows == 0) return s;
+  k.pool = PagePool{a->num_pages, a->n_kv, page_shift(a->page_size), a->table_stride};
   k.table = a->page_table;
   k.seq = a->seq;
   k.n_seq = a->n_seq;
   k.base_pos = a->base_pos;
-  k.err = di.err;
-  k.kv_f32 = a->kvdtype == DEC_F32;
+  return run_rows(k, a->xdtype, di, static_cast<cudaStream_t>(stream));
+}
+
+extern "C" dec_status kv_append_slots(const kv_slots_args* a, void* stream) {
+  if (!a) return fail(nullptr, DEC_EINVAL, "kv_append_slots: NULL arguments");
+  if (a->rows > 0 && !a->slots) return fail(nullptr, DEC_EINVAL, "kv_append_slots: NULL pointer");
+  if (a->rows > 0 && !aligned_to(8, a->slots))
+    return fail(nullptr, DEC_EINVAL, "kv_append_slots: a pointer is not aligned to its elements");
+  QkRowsArgs k{};
+  DeviceInfo di;
+  const dec_status s = append_fields(a, "kv_append_slots", &k, &di);
+  if (s != DEC_OK || a->rows == 0) return s;
+  k.pool = PagePool{a->num_pages, a->n_kv, page_shift(a->page_size), 0};
+  k.slots = a->slots;
   return run_rows(k, a->xdtype, di, static_cast<cudaStream_t>(stream));
 }
