@@ -34,15 +34,16 @@ def host(tmp_path_factory):
     src.write_text('#include "attn_tree_plan.h"\n#include "spans.h"\nusing namespace wsg;\nextern "C" {\n'
                    "int plan(const attn_tree_args* a, long long* o) {\n"
                    "  if (!attn_tree_sizes_ok(a)) return 0;\n  const AtPlan p = attn_tree_plan(a, 152);\n"
-                   "  const long long v[] = {p.cut.mt, p.prefix_row_tiles, p.prefix_tiles, p.pieces, (long long)p.o,\n"
+                   "  const long long v[] = {1 << p.cut.mshift, p.prefix_row_tiles, p.prefix_tiles, p.pieces, (long long)p.o,\n"
                    "    (long long)p.ml, (long long)p.rec, (long long)p.line, (long long)p.total, (long long)sizeof(AtRow)};\n"
                    "  for (int i = 0; i < 10; ++i) o[i] = v[i];\n  return 1;\n}\n"
-                   "int keys(int group, int mt, int chain, long long cap, int n, int rows, int t) {\n"
-                   "  return at_keys(AtCut{group, 1, mt, chain, cap}, n, rows, t); }\n"
-                   "int tiles(int group, int mt, int chain, long long cap, int n, int rows, int t) {\n"
-                   "  return at_tiles(AtCut{group, 1, mt, chain, cap}, n, rows, t); }\n"
-                   "int head(int group, int mt, int chain, long long cap, int n, int rows) {\n"
-                   "  return at_head_tiles(AtCut{group, 1, mt, chain, cap}, n, rows); }\n"
+                   "AtCut cut(int group, int mt, int chain, int cap) { return AtCut{group, 1, mt == 128 ? 7 : 4, chain, cap}; }\n"
+                   "int keys(int group, int mt, int chain, int cap, int n, int rows, int t) {\n"
+                   "  return at_keys(cut(group, mt, chain, cap), n, rows, t); }\n"
+                   "int tiles(int group, int mt, int chain, int cap, int n, int rows, int t) {\n"
+                   "  return at_tiles(cut(group, mt, chain, cap), n, rows, t); }\n"
+                   "long long head(int group, int mt, int chain, int cap, int n, int rows) {\n"
+                   "  return at_head_tiles(cut(group, mt, chain, cap), n, rows); }\n"
                    "long long first(long long W, int C, int c) { return at_first(W, C, c); }\n"
                    "int owner(long long W, int C, long long p) { return at_owner(W, C, p); }\n"
                    "int meet(size_t p, size_t a, size_t q, size_t b) {\n"
@@ -55,8 +56,8 @@ def host(tmp_path_factory):
         subprocess.run(cmd, check=True)
     L, q, i, z = ctypes.CDLL(str(lib)), ctypes.c_longlong, ctypes.c_int, ctypes.c_size_t
     L.plan.argtypes = [ctypes.c_void_p, ctypes.c_void_p]
-    L.keys.argtypes = L.tiles.argtypes = [i, i, i, q, i, i, i]
-    L.head.argtypes = [i, i, i, q, i, i]
+    L.keys.argtypes = L.tiles.argtypes = [i] * 7
+    L.head.argtypes, L.head.restype = [i] * 6, q
     L.first.argtypes, L.first.restype = [q, i, i], q
     L.owner.argtypes = [q, i, q]
     L.meet.argtypes = [z] * 4
@@ -68,7 +69,7 @@ NAMES = "mt prefix_row_tiles prefix_tiles pieces o ml rec line total rec_bytes".
 
 def test_keys_of_row_tiles(host):
     """A row tile looks at the request's tokens and its own rows: all of them, or in a chain up to its last token."""
-    big = 1 << 40
+    big = 1 << 30
     for group, mt, n, rows in ((1, 16, 0, 1), (2, 16, 100, 20), (3, 16, 5, 11), (16, 16, 7, 3), (2, 128, 1000, 200),
                                (5, 128, 129, 77)):
         T = -(-rows * group // mt)

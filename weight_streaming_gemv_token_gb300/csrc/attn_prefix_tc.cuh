@@ -51,14 +51,6 @@ struct ApArgs {
   uint32_t* err;
 };
 
-__device__ __forceinline__ void tma_load_3d_map(void* dst, const CUtensorMap* map, int x, int y, int z, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-          smem_u32(dst)),
-      "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // Grid: blockIdx.x = (split * n_kv + head) * row_blocks + row block. kmap, vmap:
 // the prefix as [n_kv][plen][128] in 128-row x 64-column boxes.
 __global__ void __maxnreg__(120)

@@ -33,13 +33,13 @@ __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int
   const long long W = *p.total;
   const int C = static_cast<int>(min(static_cast<long long>(ctas), W));
   int at = rec.at + h;
-  if (at >= p.cut.mt) {  // the row tile behind the record's
-    at -= p.cut.mt;
+  if (at >> p.cut.mshift) {  // the row tile behind the record's
+    at -= 1 << p.cut.mshift;
     rec.line += rec.tiles;
     rec.tiles = rec.next;
     ++rec.seg;
   }
-  const long long line = rec.line + static_cast<long long>(g) * rec.head;
+  const long long line = rec.line + g * rec.head;
   const int c0 = at_owner(W, C, line), c1 = at_owner(W, C, line + rec.tiles - 1);
   const long long own = rec.seg + static_cast<long long>(g) * rec.row_tiles + c0;  // number of the first piece
   const int own_n = c1 - c0 + 1;
@@ -47,8 +47,8 @@ __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int
   long long pre = 0;
   int pre_n = 0, pre_at = 0;
   if (p.prefix_tiles > 0) {
-    const long long m = static_cast<long long>(row) * a.group + h, rt = m / p.cut.mt;
-    pre_at = static_cast<int>(m - rt * p.cut.mt);
+    const int m = row * a.group + h, rt = m >> p.cut.mshift;
+    pre_at = m - (rt << p.cut.mshift);
     const long long seg = static_cast<long long>(g) * p.prefix_row_tiles + rt, from = seg * p.prefix_tiles;
     const int d0 = at_owner(W, C, from);
     pre_n = at_owner(W, C, from + p.prefix_tiles - 1) - d0 + 1;
@@ -65,7 +65,7 @@ __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const int s = s0 + i;
-      const long long r = s < pre_n ? (pre + s) * p.cut.mt + pre_at : (own + s - pre_n) * p.cut.mt + at;
+      const long long r = s < pre_n ? ((pre + s) << p.cut.mshift) + pre_at : ((own + s - pre_n) << p.cut.mshift) + at;
       q[i] = s < parts ? a.part_ml[r] : make_float2(-INFINITY, 0.f);
       y[i] = s < parts && in ? *reinterpret_cast<const float4*>(a.part_o + r * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
     }
@@ -164,11 +164,17 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
   t.prefix_tiles = p.prefix_tiles;
   t.out = a->out;
   t.out_stride = a->out_stride;
+  t.out16 = aligned16(a->out) && (a->rows == 1 || a->out_stride * static_cast<int64_t>(qe) % 16 == 0);
   t.lse = a->lse;
   t.rec = reinterpret_cast<AtRow*>(w + p.rec);
   t.total = reinterpret_cast<long long*>(w + p.line);
   const bool qf = a->qdtype == DEC_F32;
-  WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_tree_f32(t, qf, di, s) : launch_tree_bf16(t, qf, di, s));
+  if (p.tc) {
+    const dec_status e = launch_tree_tc(t, di, s);
+    if (e != DEC_OK) return e;
+  } else {
+    WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_tree_f32(t, qf, di, s) : launch_tree_bf16(t, qf, di, s));
+  }
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(a->rows) * a->n_q + 3) / 4);
   WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_tree_join_kernel<float>, dim3(grid), dim3(128), 0, s, true, t, di.sms)
                            : launch_k(attn_tree_join_kernel<uint16_t>, dim3(grid), dim3(128), 0, s, true, t, di.sms));

@@ -15,6 +15,7 @@ struct AtArgs {
   int prefix_row_tiles, prefix_tiles;
   void* out;
   long long out_stride;
+  int out16;  // rows of out can be written in 16-byte pieces
   float* lse;
   AtRow* rec;
   long long* total;  // [1]: key tiles of the line
@@ -22,187 +23,24 @@ struct AtArgs {
 
 // A piece: keys k0 .. k1 - 1 of a segment against its rows.
 struct AtPiece {
-  bool prefix, whole;  // whole: the whole segment
+  bool prefix, whole;  // whole: the whole segment, whose rows have no prefix
   int s, g;
   int begin, rows, n;  // the request's first row, its rows, its tokens in pages
   int m0, nrows;       // the row tile: first row (token * group + head) and rows
   int k0, k1;
+  int tiles;           // key tiles, one at least; 0: no piece, the share has ended
   long long id;
 };
 
-struct AtShared {
-  long long warp[32][2];
-  int most[32];
-  long long line0, seg0;        // the first request of this CTA's share: tiles and segments before it
-  int s, begin;
-  int count;                    // requests whose records this CTA writes
-  struct {
-    long long line;
-    int s, begin, rows, n, seg;
-  } mine[64];
-};
-
-// The way of a CTA along the line; the same in all of its threads.
+// The way of a CTA along the line.
 struct AtWalk {
   long long pos, end, prefix;  // tiles; those of the prefix
   long long seg;               // number of the segment at hand
-  int cta;
-  // the request at hand
+  // the request at hand (s < 0: none yet)
   int s, begin, rows, n, g, t, tile, row_tiles;
+  int first_s, first_begin;    // where the requests begin for this CTA
 
   __device__ __forceinline__ static int clamp_row(const AtArgs& a, int r) { return min(max(0, r), a.a.rows); }
-
-  // Block-wide (NT threads): sums the lengths, finds this CTA's place, and writes the
-  // records of the requests s with s % gridDim.x == blockIdx.x.
-  template <int NT>
-  __device__ __forceinline__ void start(const AtArgs& a, AtShared& sh) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, batch = a.a.batch;
-    const int per = (batch + NT - 1) / NT, lo = min(batch, tid * per), hi = min(batch, lo + per);
-    cta = blockIdx.x;
-    // the highest row start up to this thread's first request (starts that fall are lifted)
-    int top = 0;
-    for (int i = lo; i < hi; ++i) top = max(top, clamp_row(a, a.row_start[i]));
-    int inc = top;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(0xffffffffu, inc, o);
-      if (lane >= o) inc = max(inc, y);
-    }
-    if (lane == 31) sh.most[warp] = inc;
-    if (tid == 0) sh.count = 0;
-    __syncthreads();
-    int before = __shfl_up_sync(0xffffffffu, inc, 1);
-    if (lane == 0) before = 0;
-    for (int w = 0; w < warp; ++w) before = max(before, sh.most[w]);
-    // tiles and segments of this thread's requests
-    auto size = [&](int i, int* from, int* n_rows, int* len, long long* tiles, long long* segs) {
-      *from = max(*from, clamp_row(a, a.row_start[i]));
-      *n_rows = max(0, clamp_row(a, a.row_start[i + 1]) - *from);
-      *len = a.a.len[i];
-      *tiles = *segs = 0;
-      if (*len < 0) *n_rows = 0;
-      if (*n_rows > 0) {
-        *tiles = static_cast<long long>(a.cut.n_kv) * at_head_tiles(a.cut, *len, *n_rows);
-        *segs = static_cast<long long>(a.cut.n_kv) * at_row_tiles(a.cut, *n_rows);
-      }
-    };
-    long long sum[2] = {0, 0};
-    int from = before, n_rows, len;
-    for (int i = lo; i < hi; ++i) {
-      long long tl, sg;
-      size(i, &from, &n_rows, &len, &tl, &sg);
-      sum[0] += tl, sum[1] += sg;
-    }
-    long long x[2] = {sum[0], sum[1]};
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const long long y = __shfl_up_sync(0xffffffffu, x[i], o);
-        if (lane >= o) x[i] += y;
-      }
-    }
-    if (lane == 31) sh.warp[warp][0] = x[0], sh.warp[warp][1] = x[1];
-    __syncthreads();
-    long long line = x[0] - sum[0], segs = x[1] - sum[1], own = 0;
-    for (int w = 0; w < NT / 32; ++w) {
-      if (w < warp) line += sh.warp[w][0], segs += sh.warp[w][1];
-      own += sh.warp[w][0];
-    }
-    prefix = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles * a.prefix_tiles;
-    const long long W = prefix + own;
-    const int C = static_cast<int>(min(static_cast<long long>(gridDim.x), W));
-    pos = cta < C ? at_first(W, C, cta) : 0;
-    end = cta < C ? at_first(W, C, cta + 1) : 0;
-    const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles;
-    const long long want = max(pos, prefix) - prefix;  // this CTA's first own tile
-    from = before;
-    for (int i = lo; i < hi; ++i) {
-      long long tl, sg;
-      size(i, &from, &n_rows, &len, &tl, &sg);
-      if (tl > 0 && line <= want && want < line + tl) sh.s = i, sh.begin = from, sh.line0 = line, sh.seg0 = segs;
-      if (i % static_cast<int>(gridDim.x) == cta) {  // at most 4096 / CTAs of them
-        const int k = atomicAdd(&sh.count, 1);
-        if (k < 64) {
-          sh.mine[k].line = prefix + line;
-          sh.mine[k].s = i;
-          sh.mine[k].begin = from;
-          sh.mine[k].rows = n_rows;
-          sh.mine[k].n = len;
-          sh.mine[k].seg = static_cast<int>(prefix_segs + segs);
-        }
-      }
-      line += tl, segs += sg;
-    }
-    if (tid == 0 && cta == 0) *a.total = W;
-    __syncthreads();
-    // ---- records, a thread a row ----
-    for (int k = 0; k < min(64, sh.count); ++k) {
-      const int R = sh.mine[k].rows, n_ = sh.mine[k].n, b = sh.mine[k].begin;
-      const int head = R > 0 ? at_head_tiles(a.cut, n_, R) : 0, rt = at_row_tiles(a.cut, R);
-      if (tid == 0 && R > 0 && static_cast<long long>(n_) + R > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
-      for (int i = tid; i < R; i += NT) {
-        // a token's query heads may lie in two row tiles: the record is the first one's,
-        // the other's follows from it (attn_tree_join_kernel)
-        const int t = static_cast<int>(static_cast<long long>(i) * a.cut.group / a.cut.mt);
-        long long l = sh.mine[k].line;
-        if (a.cut.chain)
-          for (int u = 0; u < t; ++u) l += at_tiles(a.cut, n_, R, u);
-        else
-          l += static_cast<long long>(t) * at_tiles(a.cut, n_, R, 0);
-        AtRow r;
-        r.line = l;
-        r.head = head;
-        r.tiles = at_tiles(a.cut, n_, R, t);
-        r.seg = sh.mine[k].seg + t;
-        r.row_tiles = rt;
-        r.at = static_cast<int>(static_cast<long long>(i) * a.cut.group - static_cast<long long>(t) * a.cut.mt);
-        r.next = t + 1 < rt ? at_tiles(a.cut, n_, R, t + 1) : 0;
-        a.rec[b + i] = r;
-      }
-    }
-    // rows of no request, and of unused ones
-    {
-      for (int k = 0; k < min(64, sh.count); ++k) {
-        const int i = sh.mine[k].s;
-        if (sh.mine[k].rows > 0) continue;
-        const int b = sh.mine[k].begin, e = max(b, clamp_row(a, a.row_start[i + 1]));
-        for (int r = b + tid; r < e; r += NT) a.rec[r].tiles = 0;
-      }
-      if (cta == 0) {
-        const int first = clamp_row(a, a.row_start[0]);
-        for (int r = tid; r < first; r += NT) a.rec[r].tiles = 0;
-        int last = 0;
-        for (int w = 0; w < NT / 32; ++w) last = max(last, sh.most[w]);
-        last = max(last, clamp_row(a, a.row_start[batch]));
-        for (int r = last + tid; r < a.a.rows; r += NT) a.rec[r].tiles = 0;
-      }
-    }
-    // ---- this CTA's place ----
-    s = -1;
-    tile = 0;
-    if (pos >= end) return;
-    if (pos < prefix) {
-      seg = pos / a.prefix_tiles;
-      tile = static_cast<int>(pos - seg * a.prefix_tiles);
-    } else {
-      enter(a, sh.s, sh.begin);
-      long long rest = pos - prefix - sh.line0;
-      const int head = at_head_tiles(a.cut, n, rows);
-      g = static_cast<int>(rest / head);
-      rest -= static_cast<long long>(g) * head;
-      t = 0;
-      if (a.cut.chain) {
-        for (int k; rest >= (k = at_tiles(a.cut, n, rows, t)); ++t) rest -= k;
-      } else {
-        const int k = at_tiles(a.cut, n, rows, 0);
-        t = static_cast<int>(rest / k);
-        rest -= static_cast<long long>(t) * k;
-      }
-      tile = static_cast<int>(rest);
-      seg = prefix_segs + sh.seg0 + static_cast<long long>(g) * row_tiles + t;
-    }
-  }
 
   // request i, whose rows start at `from` or behind
   __device__ __forceinline__ void enter(const AtArgs& a, int i, int from) {
@@ -214,62 +52,205 @@ struct AtWalk {
     g = t = 0;
   }
 
-  // The next piece; false at the end of the share.
-  __device__ __forceinline__ bool next(const AtArgs& a, const AtShared& sh, AtPiece* p) {
-    if (pos >= end) return false;
+  // The next piece.
+  __device__ __forceinline__ AtPiece next(const AtArgs& a) {
+    AtPiece p;
+    p.tiles = 0;
+    if (pos >= end) return p;
+    int kt;
     if (pos < prefix) {
-      const int head = static_cast<int>(seg / a.prefix_row_tiles), rt = static_cast<int>(seg - static_cast<long long>(head) * a.prefix_row_tiles);
-      const int take = static_cast<int>(min(static_cast<long long>(a.prefix_tiles - tile), end - pos));
-      p->prefix = true;
-      p->whole = false;  // a row has own keys too
-      p->s = -1;
-      p->g = head;
-      p->begin = 0;
-      p->rows = a.a.rows;
-      p->n = 0;
-      p->m0 = rt * a.cut.mt;
-      p->nrows = static_cast<int>(min(static_cast<long long>(a.cut.mt), static_cast<long long>(a.a.rows) * a.cut.group - p->m0));
-      p->k0 = tile * kAtKeys;
-      p->k1 = min(a.a.plen, (tile + take) * kAtKeys);
-      p->id = seg + cta;
-      pos += take;
-      tile = 0;
-      ++seg;
-      return true;
-    }
-    if (s < 0) {  // the first request with rows
-      enter(a, sh.s, sh.begin);
-    } else if (t >= row_tiles) {
-      t = 0;
-      if (++g >= a.cut.n_kv) {
-        do {
-          if (s + 1 >= a.a.batch) return false;  // (there is one: tiles are left)
-          const int reach = max(begin, clamp_row(a, a.row_start[s + 1]));
-          enter(a, s + 1, reach);
-        } while (rows == 0);
+      const int at = static_cast<int>(seg), head = at / a.prefix_row_tiles, rt = at - head * a.prefix_row_tiles;
+      kt = a.prefix_tiles;
+      p.prefix = true;
+      p.whole = false;  // a row has own keys too
+      p.s = -1;
+      p.g = head;
+      p.begin = 0;
+      p.rows = a.a.rows;
+      p.n = 0;
+      p.m0 = rt << a.cut.mshift;
+      p.k1 = a.a.plen;
+    } else {
+      if (s < 0) {
+        enter(a, first_s, first_begin);  // the first request with rows
+      } else if (t >= row_tiles) {
+        t = 0;
+        if (++g >= a.cut.n_kv) {
+          do {
+            if (s + 1 >= a.a.batch) return p;  // (there is one: tiles are left)
+            const int reach = max(begin, clamp_row(a, a.row_start[s + 1]));
+            enter(a, s + 1, reach);
+          } while (rows == 0);
+        }
       }
+      kt = at_tiles(a.cut, n, rows, t);
+      p.prefix = false;
+      p.whole = tile == 0 && prefix == 0 && kt <= end - pos;
+      p.s = s;
+      p.g = g;
+      p.begin = begin;
+      p.rows = rows;
+      p.n = n;
+      p.m0 = t << a.cut.mshift;
+      p.k1 = at_keys(a.cut, n, rows, t);
+      ++t;
     }
-    const int kt = at_tiles(a.cut, n, rows, t);
     const int take = static_cast<int>(min(static_cast<long long>(kt - tile), end - pos));
-    p->prefix = false;
-    p->whole = tile == 0 && take == kt && prefix == 0;
-    p->s = s;
-    p->g = g;
-    p->begin = begin;
-    p->rows = rows;
-    p->n = n;
-    p->m0 = t * a.cut.mt;
-    p->nrows = static_cast<int>(min(static_cast<long long>(a.cut.mt), static_cast<long long>(rows) * a.cut.group - p->m0));
-    p->k0 = tile * kAtKeys;
-    p->k1 = min(at_keys(a.cut, n, rows, t), (tile + take) * kAtKeys);
-    p->id = seg + cta;
+    p.nrows = min(1 << a.cut.mshift, p.rows * a.cut.group - p.m0);
+    p.k0 = tile << kAtKeyShift;
+    p.k1 = min(p.k1, (tile + take) << kAtKeyShift);
+    p.tiles = take;
+    p.id = seg + blockIdx.x;
     pos += take;
     tile = 0;
     ++seg;
-    ++t;
-    return true;
+    return p;
   }
 };
+
+// A CTA's place on the line, and the requests whose rows' records it writes (s modulo
+// the CTAs; 4096 requests at most, 64 CTAs at least).
+struct AtShared {
+  AtWalk walk;
+  int count, top;  // top: behind the requests' last row
+  struct Mine {
+    long long line;
+    int s, begin, rows, n, seg;
+  } mine[64];
+};
+
+// One warp: sums the requests' lengths, a run of them a lane, and finds this CTA's place.
+__device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
+  const int lane = threadIdx.x & 31, batch = a.a.batch, ctas = gridDim.x, cta = blockIdx.x;
+  const int per = (batch + 31) / 32, lo = min(batch, lane * per), hi = min(batch, lo + per);
+  // the highest row start up to this lane's first request (starts that fall are lifted)
+  int top = 0;
+#pragma unroll 4
+  for (int i = lo; i < hi; ++i) top = max(top, AtWalk::clamp_row(a, a.row_start[i]));
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, top, o);
+    if (lane >= o) top = max(top, y);
+  }
+  const int last = max(__shfl_sync(0xffffffffu, top, 31), AtWalk::clamp_row(a, a.row_start[batch]));
+  int before = __shfl_up_sync(0xffffffffu, top, 1);
+  if (lane == 0) before = 0, sh.count = 0, sh.top = last;
+  __syncwarp();
+  // Tiles and segments of this lane's requests, then with the sums of the lanes before
+  // this CTA's place among them.
+  const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * a.prefix_tiles;
+  long long line = 0, segs = 0, want = -1;
+  AtWalk w;
+  w.s = -1;
+  w.tile = w.g = w.t = w.rows = w.row_tiles = w.n = w.begin = 0;
+  w.seg = 0;
+  w.prefix = prefix;
+  w.first_s = w.first_begin = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int from = before;
+#pragma unroll 2
+    for (int i = lo; i < hi; ++i) {
+      from = max(from, AtWalk::clamp_row(a, a.row_start[i]));
+      const int len = a.a.len[i], n_rows = len < 0 ? 0 : max(0, AtWalk::clamp_row(a, a.row_start[i + 1]) - from);
+      const long long tl = n_rows ? a.cut.n_kv * at_head_tiles(a.cut, len, n_rows) : 0;
+      if (pass) {
+        if (line <= want && want < line + tl) {  // (one lane)
+          sh.walk.first_s = i;
+          sh.walk.first_begin = from;
+          sh.walk.pos = line;
+          sh.walk.seg = segs;
+        }
+        if (i % ctas == cta) {
+          const int k = atomicAdd(&sh.count, 1);
+          if (k < 64) sh.mine[k] = {prefix + line, i, from, n_rows, len, static_cast<int>(prefix_segs + segs)};
+        }
+      }
+      line += tl;
+      segs += static_cast<long long>(a.cut.n_kv) * at_row_tiles(a.cut, n_rows);
+    }
+    if (pass == 0) {
+      long long x = line, y = segs;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
+        if (lane >= o) x += u, y += v;
+      }
+      const long long W = prefix + __shfl_sync(0xffffffffu, x, 31);
+      line = x - line;
+      segs = y - segs;
+      const int C = static_cast<int>(min(static_cast<long long>(ctas), W));
+      w.pos = cta < C ? at_first(W, C, cta) : 0;
+      w.end = cta < C ? at_first(W, C, cta + 1) : 0;
+      want = w.pos < w.end ? max(w.pos, prefix) - prefix : -1;  // this CTA's first own tile
+      if (cta == 0 && lane == 0) *a.total = W;
+    }
+  }
+  __syncwarp();
+  if (w.pos < w.end) {
+    const long long line0 = sh.walk.pos, seg0 = sh.walk.seg;
+    w.first_s = sh.walk.first_s;
+    w.first_begin = sh.walk.first_begin;
+    if (w.pos < prefix) {
+      w.seg = at_div(w.pos, a.prefix_tiles);
+      w.tile = static_cast<int>(w.pos - w.seg * a.prefix_tiles);
+    } else {
+      w.enter(a, w.first_s, w.first_begin);
+      long long rest = w.pos - prefix - line0;
+      const long long head = at_head_tiles(a.cut, w.n, w.rows);
+      w.g = static_cast<int>(at_div(rest, head));
+      rest -= w.g * head;
+      if (a.cut.chain) {
+        for (int k; rest >= (k = at_tiles(a.cut, w.n, w.rows, w.t)); ++w.t) rest -= k;
+      } else {
+        const int k = at_tiles(a.cut, w.n, w.rows, 0);
+        w.t = static_cast<int>(at_div(rest, k));
+        rest -= static_cast<long long>(w.t) * k;
+      }
+      w.tile = static_cast<int>(rest);
+      w.seg = prefix_segs + seg0 + static_cast<long long>(w.g) * w.row_tiles + w.t;
+    }
+  }
+  __syncwarp();
+  if (lane == 0) sh.walk = w;
+  __syncwarp();
+}
+
+// One warp, at any time behind at_start: the records that attn_tree_join_kernel goes by.
+__device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh) {
+  const int lane = threadIdx.x & 31, count = min(64, sh.count);
+  for (int k = 0; k < count; ++k) {
+    const AtShared::Mine x = sh.mine[k];
+    if (x.rows == 0) {  // rows of an unused request
+      const int e = max(x.begin, AtWalk::clamp_row(a, a.row_start[x.s + 1]));
+      for (int r = x.begin + lane; r < e; r += 32) a.rec[r].tiles = 0;
+      continue;
+    }
+    const long long head = at_head_tiles(a.cut, x.n, x.rows);
+    const int rt = at_row_tiles(a.cut, x.rows);
+    if (lane == 0 && static_cast<long long>(x.n) + x.rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
+    for (int i = lane; i < x.rows; i += 32) {
+      // a token's query heads may lie in two row tiles: the record is the first one's,
+      // the other's follows from it
+      const int t = (i * a.cut.group) >> a.cut.mshift;
+      AtRow r;
+      r.line = x.line + at_tiles_before(a.cut, x.n, x.rows, t);
+      r.head = head;
+      r.tiles = at_tiles(a.cut, x.n, x.rows, t);
+      r.seg = x.seg + t;
+      r.row_tiles = rt;
+      r.at = i * a.cut.group - (t << a.cut.mshift);
+      r.next = t + 1 < rt ? at_tiles(a.cut, x.n, x.rows, t + 1) : 0;
+      r.pad = 0;
+      a.rec[x.begin + i] = r;
+    }
+  }
+  if (blockIdx.x == 0) {  // rows of no request
+    const int first = AtWalk::clamp_row(a, a.row_start[0]);
+    for (int r = lane; r < first; r += 32) a.rec[r].tiles = 0;
+    for (int r = sh.top + lane; r < a.a.rows; r += 32) a.rec[r].tiles = 0;
+  }
+}
 
 // Which of the 32 keys from number j0 of the drafted rows on (below 0: tokens in pages)
 // row i of the request sees.
@@ -318,5 +299,6 @@ __device__ __forceinline__ void at_put(const AtArgs& p, int row, int head, int e
 
 cudaError_t launch_tree_bf16(const AtArgs& a, bool q_f32, const DeviceInfo& di, cudaStream_t st);
 cudaError_t launch_tree_f32(const AtArgs& a, bool q_f32, const DeviceInfo& di, cudaStream_t st);
+dec_status launch_tree_tc(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace wsg

@@ -17,45 +17,51 @@
 
 namespace wsg {
 
-constexpr int kAtBatch = 4096, kAtKeys = 128;  // requests; keys a tile
+constexpr int kAtBatch = 4096, kAtKeyShift = 7, kAtKeys = 1 << kAtKeyShift;  // requests; keys a tile
 
-// What the cutting goes by.
+// What the cutting goes by. rows * group < 2^24, capacity <= 2^30: 32-bit arithmetic.
 struct AtCut {
-  int group, n_kv, mt;     // mt: rows (token, query head of the group) of a row tile
+  int group, n_kv;
+  int mshift;              // log2 of the rows (token, query head of the group) of a row tile
   int chain;               // no mask: a row sees the rows up to itself
-  long long capacity;      // tokens that a table row can hold
+  int capacity;            // tokens that a table row can hold
 };
 
-WSG_HD int at_up(long long x, long long y) { return static_cast<int>((x + y - 1) / y); }
-WSG_HD int at_row_tiles(const AtCut& c, int rows) { return at_up(static_cast<long long>(rows) * c.group, c.mt); }
+WSG_HD int at_row_tiles(const AtCut& c, int rows) { return (rows * c.group + (1 << c.mshift) - 1) >> c.mshift; }
 
 // Keys that row tile t of a request of n tokens and `rows` rows looks at, and its key
 // tiles (one at least: a row without keys has a result too).
 WSG_HD int at_keys(const AtCut& c, int n, int rows, int t) {
-  int seen = rows;
+  unsigned seen = static_cast<unsigned>(rows);
   if (c.chain) {
-    const long long last = (static_cast<long long>(t + 1) * c.mt - 1) / c.group + 1;
-    if (last < seen) seen = static_cast<int>(last);
+    const unsigned last = ((static_cast<unsigned>(t + 1) << c.mshift) - 1u) / static_cast<unsigned>(c.group) + 1u;
+    if (last < seen) seen = last;
   }
-  const long long keys = static_cast<long long>(n) + seen;
-  return static_cast<int>(keys < c.capacity ? keys : c.capacity);
+  const unsigned keys = static_cast<unsigned>(n) + seen, cap = static_cast<unsigned>(c.capacity);
+  return static_cast<int>(keys < cap ? keys : cap);
 }
 WSG_HD int at_tiles(const AtCut& c, int n, int rows, int t) {
-  const int k = at_up(at_keys(c, n, rows, t), kAtKeys);
+  const int k = (at_keys(c, n, rows, t) + kAtKeys - 1) >> kAtKeyShift;
   return k < 1 ? 1 : k;
 }
-// Key tiles of one head of a request.
-WSG_HD int at_head_tiles(const AtCut& c, int n, int rows) {
-  const int T = at_row_tiles(c, rows);
-  if (!c.chain) return T * at_tiles(c, n, rows, 0);
-  int sum = 0;
-  for (int t = 0; t < T; ++t) sum += at_tiles(c, n, rows, t);
+// Key tiles of one head of a request's row tiles before t.
+WSG_HD long long at_tiles_before(const AtCut& c, int n, int rows, int t) {
+  if (!c.chain) return static_cast<long long>(t) * at_tiles(c, n, rows, 0);
+  long long sum = 0;
+  for (int u = 0; u < t; ++u) sum += at_tiles(c, n, rows, u);
   return sum;
+}
+WSG_HD long long at_head_tiles(const AtCut& c, int n, int rows) { return at_tiles_before(c, n, rows, at_row_tiles(c, rows)); }
+
+// x / y of non-negative numbers; the 64-bit division, some 100 instructions, only where needed.
+WSG_HD long long at_div(long long x, long long y) {
+  if (((x | y) >> 32) == 0) return static_cast<unsigned>(x) / static_cast<unsigned>(y);
+  return x / y;
 }
 
 // First tile of CTA c of C on a line of W tiles, and the CTA that has tile p.
-WSG_HD long long at_first(long long W, int C, int c) { return c * W / C; }
-WSG_HD int at_owner(long long W, int C, long long p) { return static_cast<int>(((p + 1) * C - 1) / W); }
+WSG_HD long long at_first(long long W, int C, int c) { return at_div(c * W, C); }
+WSG_HD int at_owner(long long W, int C, long long p) { return static_cast<int>(at_div((p + 1) * C - 1, W)); }
 
 inline bool attn_tree_sizes_ok(const attn_tree_args* a) {
   auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
@@ -80,9 +86,9 @@ struct AtPlan {
 // `tiles` of it (0: a row without a result), `head` tiles on for the next head; its
 // number is seg for head 0, row_tiles on for the next.
 struct AtRow {
-  long long line;
-  int32_t head, tiles, seg, row_tiles;
-  int32_t at, next;  // row (token * group) within the row tile; tiles of the row tile behind it
+  long long line, head;
+  int32_t tiles, seg, row_tiles;
+  int32_t at, next, pad;  // row (token * group) within the row tile; tiles of the row tile behind it
 };
 
 inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
@@ -93,18 +99,22 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   p.cut.group = group;
   p.cut.n_kv = a->n_kv;
   p.cut.chain = a->mask == nullptr;
-  p.cut.capacity = static_cast<long long>(a->table_stride) << page_shift(a->page_size);
-  p.tc = false;
-  p.cut.mt = p.tc ? 128 : 16;
+  p.cut.capacity = a->table_stride << page_shift(a->page_size);
+  // bfloat16 throughout, a head of 64 or 128, pages of whole swizzled groups of rows
+  p.tc = a->qdtype == DEC_BF16 && a->kvdtype == DEC_BF16 && (a->head_dim == 128 || a->head_dim == 64) && a->page_size >= 8 &&
+         a->table_stride > 0 && a->num_pages > 0 && static_cast<long long>(a->num_pages) * a->n_kv < 1ll << 31 &&
+         (a->prefix_len == 0 || a->prefix_stride < 1ll << 31);
+  p.cut.mshift = p.tc ? 7 : 4;
+  const int mt = 1 << p.cut.mshift;
   if (a->prefix_len > 0) {
     p.prefix_row_tiles = at_row_tiles(p.cut, a->rows);
-    p.prefix_tiles = at_up(a->prefix_len, kAtKeys);
+    p.prefix_tiles = (a->prefix_len + kAtKeys - 1) / kAtKeys;
   }
   // the requests' row tiles: rows * group / mt whole ones at most, one more each
-  const long long own = static_cast<long long>(a->rows) * group / p.cut.mt + (a->batch < a->rows ? a->batch : a->rows);
+  const long long own = static_cast<long long>(a->rows) * group / mt + (a->batch < a->rows ? a->batch : a->rows);
   p.pieces = sms + (own + p.prefix_row_tiles) * a->n_kv;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-  const size_t rows = static_cast<size_t>(p.pieces) * p.cut.mt;
+  const size_t rows = static_cast<size_t>(p.pieces) * mt;
   p.o = 0;
   p.ml = up(rows * a->head_dim * 4);
   p.rec = p.ml + up(rows * 8);

@@ -412,10 +412,12 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
   const Copy copy(a.d, mine);
   pdl_wait();
   pdl_trigger();
-  AtWalk walk;
-  walk.start<NTHREADS>(p, sh);
-  AtPiece pc;
-  for (bool again = false; walk.next(p, sh, &pc); again = true) {
+  if (warp == 0) at_start(p, sh);
+  __syncthreads();
+  AtWalk walk = sh.walk;
+  for (bool again = false;; again = true) {
+    const AtPiece pc = walk.next(p);
+    if (pc.tiles == 0) break;
     if (again) __syncthreads();  // the piece before this one has left shared memory
     if constexpr (F32) {
       copy.pad(a.d, mine);
@@ -526,12 +528,13 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
         const int token_ = (row0 + r) / a.group, head = pc.g * a.group + (row0 + r) % a.group;
         at_put<QT>(p, pc.begin + token_, head, e, x, m, sum);
       } else {
-        const long long at = pc.id * p.cut.mt + r;
+        const long long at = (pc.id << p.cut.mshift) + r;
         *reinterpret_cast<float4*>(a.part_o + at * a.d + e) = x;
         if (e == 0) a.part_ml[at] = make_float2(m, sum);
       }
     }
   }
+  if (warp == 0) at_records(p, sh);
 }
 
 template <typename QT, int DP, int QP, bool F32>
