@@ -36,7 +36,8 @@
 namespace wsg {
 
 constexpr int kTtSoft = 16;  // warps of the softmax
-constexpr int kTtThreads = 32 * (2 + kTtSoft), kTtRows = 128;
+constexpr int kTtLoaders = 3;  // warps that issue copies: warp 0 and those behind the softmax's
+constexpr int kTtThreads = 32 * (1 + kTtSoft + kTtLoaders), kTtRows = 128;
 constexpr int kTtPieces = 8;  // pieces announced: the rings hold the tiles of fewer
 constexpr uint32_t kTtTmO = 256, kTtTmQ = 384;
 constexpr int kTtStage = 32 * 12;  // floats of a warp's way to memory: 32 rows of 32 bytes and 16 more
@@ -182,30 +183,43 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   };
   const int shift = a.pool.shift, page_shift_ = min(shift, kAtKeyShift), tile_pages = kAtKeys >> page_shift_;
 
-  if (warp == 0) {
+  if (warp == 0 || warp > 1 + kTtSoft) {
     // ---- the share, keys and values ----
-    at_start(p, sh);
-    AtWalk walk = sh.walk;
-    int j = 0, piece = 0;  // tiles, pieces so far
+    const int who = warp == 0 ? 0 : warp - 1 - kTtSoft;  // which of the loaders
+    AtWalk walk;
+    if (who == 0) {
+      at_start(p, sh);
+      walk = sh.walk;
+    }
+    int j = 0;  // tiles so far
     bool ok = true;
     AtPiece pc{};
-    // this lane's page of the tile at key tk, -1 where there is none to read
-    auto entry = [&](int tk) -> int32_t {
-      const int at = tk + (lane << page_shift_);
-      return pc.prefix || lane >= tile_pages || at >= pc.k1
+    // this loader's boxes are numbers who, who + loaders, .. of (page, 64 columns); this lane's one
+    const int unit = lane * kTtLoaders + who, unit_page = unit / G::BOXES, unit_box = unit % G::BOXES;
+    // the table's entry for a page of the tile at key tk, -1 where there is none to read
+    auto entry = [&](int tk, int page) -> int32_t {
+      const int at = tk + (page << page_shift_);
+      return pc.prefix || page >= tile_pages || at >= pc.k1
                  ? -1
                  : a.table[static_cast<long long>(pc.s) * a.pool.width + (at >> shift)];
     };
-    while (true) {
-      pc = walk.next(p);
-      if (lane == 0) {
-        s_piece[piece % kTtPieces] = pc;
-        mbar_arrive(&told[piece % kTtPieces]);
+    for (int piece = 0; ok; ++piece) {
+      if (who == 0) {
+        pc = walk.next(p);
+        if (lane == 0) {
+          s_piece[piece % kTtPieces] = pc;
+          mbar_arrive(&told[piece % kTtPieces]);
+        }
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait(&told[piece % kTtPieces], (piece / kTtPieces) & 1))) {
+          ok = false;
+          break;
+        }
+        pc = s_piece[piece % kTtPieces];
       }
-      ++piece;
       if (pc.tiles == 0) break;
-      // the queries on their way, ahead of the keys that fill the memory's queues
-      {
+      if (who == 0) {
+        // the queries on their way, ahead of the keys that fill the memory's queues
         const int per = p.cut.group * D * 2, t0 = pc.m0 / a.group, t1 = (pc.m0 + pc.nrows - 1) / a.group;
         const char* q0 = static_cast<const char*>(a.q) + (a.q_stride * pc.begin + static_cast<long long>(pc.g) * a.group * D) * 2;
         const int lines = (per + 127) / 128;
@@ -214,33 +228,40 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           asm volatile("prefetch.global.L2 [%0];" ::"l"(q0 + a.q_stride * 2 * (t0 + t) + (i - t * lines) * 128));
         }
       }
-      int32_t e = entry(pc.k0);
+      int32_t e = entry(pc.k0, unit_page), all = who == 0 ? entry(pc.k0, lane) : -1;
       for (int i = 0; i < pc.tiles; ++i, ++j) {
         const int tk = pc.k0 + i * kAtKeys, st = j % STAGES;
-        const bool wanted = !pc.prefix && lane < tile_pages && tk + (lane << page_shift_) < pc.k1;
-        const bool there = wanted && e >= 0 && e < a.pool.num_pages;
-        const unsigned have = __ballot_sync(0xffffffffu, there), holes = __ballot_sync(0xffffffffu, wanted && !there);
+        const bool there = e >= 0 && e < a.pool.num_pages;
         const int plane = e * a.n_kv + pc.g, y = shift > kAtKeyShift ? tk & ((1 << shift) - 1) : 0;
-        e = i + 1 < pc.tiles ? entry(tk + kAtKeys) : -1;
         const uint32_t part = 128u << page_shift_;  // bytes of a page's columns
-        const uint32_t bytes = pc.prefix ? G::TILE : __popc(have) * part * G::BOXES;
+        uint32_t bytes = 0, holes = 0;
+        if (who == 0) {
+          const bool wanted = !pc.prefix && lane < tile_pages && tk + (lane << page_shift_) < pc.k1;
+          const bool got = wanted && all >= 0 && all < a.pool.num_pages;
+          bytes = pc.prefix ? G::TILE : __popc(__ballot_sync(0xffffffffu, got)) * part * G::BOXES;
+          holes = __ballot_sync(0xffffffffu, wanted && !got);
+        }
+        if (i + 1 < pc.tiles) {
+          e = entry(tk + kAtKeys, unit_page);
+          if (who == 0) all = entry(tk + kAtKeys, lane);
+        }
         auto load = [&](unsigned char* dst, const CUtensorMap* pre, const CUtensorMap* pages, uint64_t* bar) {
-          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-          __syncwarp();
-#pragma unroll
-          for (int b = 0; b < G::BOXES; ++b) {
-            if (pc.prefix) {
-              if (lane == 0) tma_load_3d_map(dst + b * G::BOX, pre, b * 64, tk, pc.g, bar);
-            } else if (there) {
-              tma_load_3d_map(dst + b * G::BOX + lane * part, pages, b * 64, y, plane, bar);
-            }
+          if (who == 0) {
+            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+            __syncwarp();
+          }
+          // (copies may complete before the bytes are announced: the phase ends with both)
+          if (pc.prefix) {
+            if (unit < G::BOXES) tma_load_3d_map(dst + unit * G::BOX, pre, unit * 64, tk, pc.g, bar);
+          } else if (there) {
+            tma_load_3d_map(dst + unit_box * G::BOX + unit_page * part, pages, unit_box * 64, y, plane, bar);
           }
         };
         if (j >= STAGES && !__all_sync(0xffffffffu, mbar_wait(&k_empty[st], ((j / STAGES) - 1) & 1))) {
           ok = false;
           break;
         }
-        if (lane == 0) {
+        if (who == 0 && lane == 0) {
           s_holes[j % kTtPieces] = holes;
           if (holes) atomicOr(a.err, ERR_BAD_PAGE);
         }
@@ -248,7 +269,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         if (j >= STAGES && !__all_sync(0xffffffffu, mbar_wait(&v_empty[st], ((j / STAGES) - 1) & 1))) {
           ok = false;
           // the keys of this tile are on their way
-          if (lane == 0 && !mbar_wait(&k_full[st], (j / STAGES) & 1)) fail();
+          if (who == 0 && lane == 0 && !mbar_wait(&k_full[st], (j / STAGES) & 1)) fail();
           break;
         }
         load(Vs + st * G::TILE, &pv, &vp, &v_full[st]);
@@ -258,15 +279,16 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           break;
         }
       }
-      if (!ok) break;
     }
     if (!ok && lane == 0) fail();
-    at_records(p, sh);
-    // the last copies into each stage have landed before the CTA may end, after a failure too
-    if (lane == 0) {
-      for (int s = 0; s < STAGES; ++s)
-        if (s < j && (!mbar_wait(&k_full[s], ((j - 1 - s) / STAGES) & 1) || !mbar_wait(&v_full[s], ((j - 1 - s) / STAGES) & 1)))
-          fail();
+    if (who == 0) {
+      at_records(p, sh);
+      // the last copies into each stage have landed before the CTA may end, after a failure too
+      if (lane == 0) {
+        for (int s = 0; s < STAGES; ++s)
+          if (s < j && (!mbar_wait(&k_full[s], ((j - 1 - s) / STAGES) & 1) || !mbar_wait(&v_full[s], ((j - 1 - s) / STAGES) & 1)))
+            fail();
+      }
     }
   } else if (warp == 1) {
     if (lane == 0) {
