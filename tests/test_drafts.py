@@ -35,7 +35,8 @@ def host(tmp_path_factory):
                    "int plan(const attn_tree_args* a, long long* o) {\n"
                    "  if (!attn_tree_sizes_ok(a)) return 0;\n  const AtPlan p = attn_tree_plan(a, 152);\n"
                    "  const long long v[] = {1 << p.cut.mshift, p.prefix_row_tiles, p.prefix_tiles, p.pieces, (long long)p.o,\n"
-                   "    (long long)p.ml, (long long)p.rec, (long long)p.line, (long long)p.total, (long long)sizeof(AtRow)};\n"
+                   "    (long long)p.ml, (long long)p.rec, (long long)p.line, (long long)p.total,\n"
+                   "    (long long)(a->prefix_len ? a->rows * sizeof(AtRow) : 152 * sizeof(AtSeam))};\n"
                    "  for (int i = 0; i < 10; ++i) o[i] = v[i];\n  return 1;\n}\n"
                    "AtCut cut(int group, int mt, int chain, int cap) { return AtCut{group, 1, mt == 128 ? 7 : 4, chain, cap}; }\n"
                    "int keys(int group, int mt, int chain, int cap, int n, int rows, int t) {\n"
@@ -44,8 +45,8 @@ def host(tmp_path_factory):
                    "  return at_tiles(cut(group, mt, chain, cap), n, rows, t); }\n"
                    "long long head(int group, int mt, int chain, int cap, int n, int rows) {\n"
                    "  return at_head_tiles(cut(group, mt, chain, cap), n, rows); }\n"
-                   "long long first(long long W, int C, int c) { return at_first(W, C, c); }\n"
-                   "int owner(long long W, int C, long long p) { return at_owner(W, C, p); }\n"
+                   "long long first(long long W, int C, int c) { return at_first(at_shares(W, C), c); }\n"
+                   "int owner(long long W, int C, long long p) { return at_owner(at_shares(W, C), p); }\n"
                    "int meet(size_t p, size_t a, size_t q, size_t b) {\n"
                    "  return spans_meet(Span{(void*)p, a}, Span{(void*)q, b}); }\n}\n")
     lib = d / "p.so"
@@ -135,7 +136,7 @@ def test_pieces_have_numbers_of_their_own_inside_the_workspace(W, host):
                 lo, j = end, j + 1
         slots = p["pieces"] * mt
         assert p["o"] == 0 and slots * d * 4 <= p["ml"] and p["ml"] + slots * 8 <= p["rec"]
-        assert p["rec"] + total * p["rec_bytes"] <= p["line"] and p["line"] + 8 <= p["total"]
+        assert p["rec"] + p["rec_bytes"] <= p["line"] and p["line"] + 8 <= p["total"]
         assert p["ml"] % 256 == p["rec"] % 256 == p["line"] % 256 == 0
 
 

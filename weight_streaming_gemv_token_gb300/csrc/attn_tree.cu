@@ -18,7 +18,39 @@
 namespace wsg {
 namespace {
 
-// One warp a (row, query head): lane i holds elements 4 i .. 4 i + 3 of the head.
+// Without a prefix: CTA (y, x) joins a quarter of the rows (32; of 16 rows the first
+// takes all) of the segment that starts in share x and is cut. Eight warps, four rows
+// each, lane i elements 4 i .. 4 i + 3 of a head.
+template <typename QT>
+__global__ void __launch_bounds__(256) attn_tree_seam_kernel(const AtArgs p) {
+  const AmArgs& a = p.a;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();  // a following call's set-up may begin
+  pdl_wait();
+  const AtSeam s = p.seam[blockIdx.x];
+  if (s.pieces == 0) return;
+  const bool in = lane * 4 < a.d;
+  for (int r = blockIdx.y * 32 + warp; r < min(s.nrows, static_cast<int>(blockIdx.y) * 32 + 32); r += 8) {
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int s0 = 0; s0 < s.pieces; s0 += 8) {  // eight pieces at a time: their loads go out together
+      float2 q[8];
+      float4 y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const bool have = s0 + i < s.pieces;
+        const long long at = ((s.id + s0 + i) << p.cut.mshift) + r;
+        q[i] = have ? a.part_ml[at] : make_float2(-INFINITY, 0.f);
+        y[i] = have && in ? *reinterpret_cast<const float4*>(a.part_o + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      ar_merge8(q, y, &m, &l, &x);
+    }
+    const int row = s.m0 + r, token = row / a.group;
+    if (in) at_put<QT>(p, s.begin + token, s.g * a.group + row - token * a.group, lane * 4, x, m, l);
+  }
+}
+
+// With a prefix: one warp a (row, query head).
 template <typename QT>
 __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int ctas) {
   const AmArgs& a = p.a;
@@ -29,9 +61,9 @@ __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int
   if (w >= a.rows * a.n_q) return;
   const int row = w / a.n_q, head = w - row * a.n_q, g = head / a.group, h = head - g * a.group;
   AtRow rec = p.rec[row];
-  if (rec.tiles == 0) return;  // of no request, or an unused one
   const long long W = *p.total;
-  const int C = static_cast<int>(min(static_cast<long long>(ctas), W));
+  if (rec.tiles == 0) return;  // of no request, or an unused one
+  const AtShares C = at_shares(W, static_cast<int>(min(static_cast<long long>(ctas), W)));
   int at = rec.at + h;
   if (at >> p.cut.mshift) {  // the row tile behind the record's
     at -= 1 << p.cut.mshift;
@@ -40,20 +72,13 @@ __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int
     ++rec.seg;
   }
   const long long line = rec.line + g * rec.head;
-  const int c0 = at_owner(W, C, line), c1 = at_owner(W, C, line + rec.tiles - 1);
+  const int c0 = at_owner(C, line), c1 = at_owner(C, line + rec.tiles - 1);
   const long long own = rec.seg + static_cast<long long>(g) * rec.row_tiles + c0;  // number of the first piece
   const int own_n = c1 - c0 + 1;
-  if (p.prefix_tiles == 0 && own_n == 1) return;  // finished by its CTA
-  long long pre = 0;
-  int pre_n = 0, pre_at = 0;
-  if (p.prefix_tiles > 0) {
-    const int m = row * a.group + h, rt = m >> p.cut.mshift;
-    pre_at = m - (rt << p.cut.mshift);
-    const long long seg = static_cast<long long>(g) * p.prefix_row_tiles + rt, from = seg * p.prefix_tiles;
-    const int d0 = at_owner(W, C, from);
-    pre_n = at_owner(W, C, from + p.prefix_tiles - 1) - d0 + 1;
-    pre = seg + d0;
-  }
+  const int pm = row * a.group + h, rt = pm >> p.cut.mshift, pre_at = pm - (rt << p.cut.mshift);
+  const long long seg = static_cast<long long>(g) * p.prefix_row_tiles + rt, from = seg * p.prefix_tiles;
+  const int d0 = at_owner(C, from), pre_n = at_owner(C, from + p.prefix_tiles - 1) - d0 + 1;
+  const long long pre = seg + d0;  // the prefix's pieces, as above
   const bool in = lane * 4 < a.d;
   const int parts = own_n + pre_n;
   float m = -INFINITY, l = 0.f;
@@ -167,6 +192,7 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
   t.out16 = aligned16(a->out) && (a->rows == 1 || a->out_stride * static_cast<int64_t>(qe) % 16 == 0);
   t.lse = a->lse;
   t.rec = reinterpret_cast<AtRow*>(w + p.rec);
+  t.seam = reinterpret_cast<AtSeam*>(w + p.rec);
   t.total = reinterpret_cast<long long*>(w + p.line);
   const bool qf = a->qdtype == DEC_F32;
   if (p.tc) {
@@ -174,6 +200,12 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
     if (e != DEC_OK) return e;
   } else {
     WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_tree_f32(t, qf, di, s) : launch_tree_bf16(t, qf, di, s));
+  }
+  if (a->prefix_len == 0) {
+    const dim3 seams(di.sms, p.tc ? 4 : 1);
+    WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_tree_seam_kernel<float>, seams, dim3(256), 0, s, true, t)
+                             : launch_k(attn_tree_seam_kernel<uint16_t>, seams, dim3(256), 0, s, true, t));
+    return DEC_OK;
   }
   const unsigned grid = static_cast<unsigned>((static_cast<long long>(a->rows) * a->n_q + 3) / 4);
   WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_tree_join_kernel<float>, dim3(grid), dim3(128), 0, s, true, t, di.sms)

@@ -17,7 +17,8 @@ struct AtArgs {
   long long out_stride;
   int out16;  // rows of out can be written in 16-byte pieces
   float* lse;
-  AtRow* rec;
+  AtRow* rec;        // with a prefix: of every row
+  AtSeam* seam;      // without: of every CTA
   long long* total;  // [1]: key tiles of the line
 };
 
@@ -39,6 +40,8 @@ struct AtWalk {
   // the request at hand (s < 0: none yet)
   int s, begin, rows, n, g, t, tile, row_tiles;
   int first_s, first_begin;    // where the requests begin for this CTA
+  AtShares shares;
+  AtSeam seam;                 // the segment that starts in this share and is cut behind it
 
   __device__ __forceinline__ static int clamp_row(const AtArgs& a, int r) { return min(max(0, r), a.a.rows); }
 
@@ -101,6 +104,14 @@ struct AtWalk {
     p.k1 = min(p.k1, (tile + take) << kAtKeyShift);
     p.tiles = take;
     p.id = seg + blockIdx.x;
+    if (tile == 0 && take < kt) {  // (the share's last piece)
+      seam.id = p.id;
+      seam.pieces = at_owner(shares, pos + kt - 1) - static_cast<int>(blockIdx.x) + 1;
+      seam.begin = p.begin;
+      seam.m0 = p.m0;
+      seam.nrows = p.nrows;
+      seam.g = p.g;
+    }
     pos += take;
     tile = 0;
     ++seg;
@@ -120,83 +131,107 @@ struct AtShared {
 };
 
 // One warp: sums the requests' lengths, a run of them a lane, and finds this CTA's place.
+// What it costs is the chain of its loads and shuffles before the first keys can be asked
+// for, so the first request of each lane (up to 32 requests: all) is kept in registers, and
+// key tiles and segments go through the sums as one number.
 __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
   const int lane = threadIdx.x & 31, batch = a.a.batch, ctas = gridDim.x, cta = blockIdx.x;
-  const int per = (batch + 31) / 32, lo = min(batch, lane * per), hi = min(batch, lo + per);
-  // the highest row start up to this lane's first request (starts that fall are lifted)
-  int top = 0;
+  const int per = (batch + 31) >> 5, lo = min(batch, lane * per), hi = min(batch, lo + per);
+  const int rs0 = AtWalk::clamp_row(a, a.row_start[lo]), rs1 = AtWalk::clamp_row(a, a.row_start[min(batch, lo + 1)]);
+  const int len0 = lo < hi ? a.a.len[lo] : -1;
+  const int rs_end = lane == 31 ? AtWalk::clamp_row(a, a.row_start[batch]) : 0;
+  if (lane == 0) sh.count = 0;
+  // the highest row start before this lane's first request (starts that fall are lifted)
+  int top = lo < hi ? rs0 : 0;
 #pragma unroll 4
-  for (int i = lo; i < hi; ++i) top = max(top, AtWalk::clamp_row(a, a.row_start[i]));
+  for (int i = lo + 1; i < hi; ++i) top = max(top, AtWalk::clamp_row(a, a.row_start[i]));
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int y = __shfl_up_sync(0xffffffffu, top, o);
     if (lane >= o) top = max(top, y);
   }
-  const int last = max(__shfl_sync(0xffffffffu, top, 31), AtWalk::clamp_row(a, a.row_start[batch]));
+  if (lane == 31) sh.top = max(top, rs_end);
   int before = __shfl_up_sync(0xffffffffu, top, 1);
-  if (lane == 0) before = 0, sh.count = 0, sh.top = last;
-  __syncwarp();
-  // Tiles and segments of this lane's requests, then with the sums of the lanes before
-  // this CTA's place among them.
+  if (lane == 0) before = 0;
+  // A request from its row start and the next one's, `from` the highest start before: its first
+  // row; rows; key tiles << 26 | segments (at most n_kv times the rows and 2^24 / 16 of those).
+  auto size = [&](int start, int end, int len, int* from, int* n_rows) -> long long {
+    *from = max(*from, start);
+    *n_rows = len < 0 ? 0 : max(0, end - *from);
+    if (*n_rows == 0) return 0;
+    return (a.cut.n_kv * at_head_tiles(a.cut, len, *n_rows)) << 26 | static_cast<long long>(a.cut.n_kv * at_row_tiles(a.cut, *n_rows));
+  };
+  int from0 = before, rows0;
+  const long long size0 = lo < hi ? size(rs0, rs1, len0, &from0, &rows0) : (rows0 = 0, 0);
+  long long sum = size0;
+  int from = from0;
+#pragma unroll 2
+  for (int i = lo + 1; i < hi; ++i) {
+    int r;
+    sum += size(AtWalk::clamp_row(a, a.row_start[i]), AtWalk::clamp_row(a, a.row_start[i + 1]), a.a.len[i], &from, &r);
+  }
+  long long x = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const long long y = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += y;
+  }
   const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * a.prefix_tiles;
-  long long line = 0, segs = 0, want = -1;
+  const long long W = prefix + (__shfl_sync(0xffffffffu, x, 31) >> 26);
+  x -= sum;  // of the requests before this lane's
   AtWalk w;
+  w.pos = w.end = 0;
+  w.shares = AtShares{1, 0};
+  w.seam = AtSeam{};
+  if (cta < W) {
+    w.shares = at_shares(W, static_cast<int>(min(static_cast<long long>(ctas), W)));
+    w.pos = at_first(w.shares, cta);
+    w.end = at_first(w.shares, cta + 1);
+  }
+  if (cta == 0 && lane == 0) *a.total = W;
   w.s = -1;
   w.tile = w.g = w.t = w.rows = w.row_tiles = w.n = w.begin = 0;
   w.seg = 0;
   w.prefix = prefix;
-  w.first_s = w.first_begin = 0;
-#pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    int from = before;
-#pragma unroll 2
-    for (int i = lo; i < hi; ++i) {
-      from = max(from, AtWalk::clamp_row(a, a.row_start[i]));
-      const int len = a.a.len[i], n_rows = len < 0 ? 0 : max(0, AtWalk::clamp_row(a, a.row_start[i + 1]) - from);
-      const long long tl = n_rows ? a.cut.n_kv * at_head_tiles(a.cut, len, n_rows) : 0;
-      if (pass) {
-        if (line <= want && want < line + tl) {  // (one lane)
-          sh.walk.first_s = i;
-          sh.walk.first_begin = from;
-          sh.walk.pos = line;
-          sh.walk.seg = segs;
-        }
-        if (i % ctas == cta) {
-          const int k = atomicAdd(&sh.count, 1);
-          if (k < 64) sh.mine[k] = {prefix + line, i, from, n_rows, len, static_cast<int>(prefix_segs + segs)};
-        }
-      }
-      line += tl;
-      segs += static_cast<long long>(a.cut.n_kv) * at_row_tiles(a.cut, n_rows);
+  // this CTA's first own tile, and the request that has it
+  const long long want = w.pos < w.end ? max(w.pos, prefix) - prefix : -1;
+  int mine_s = -1, mine_from = 0, mine_rows = 0, mine_len = 0;
+  long long mine_at = 0;
+  auto look = [&](int i, int f, int r, int len, long long sz) {
+    const long long line = x >> 26;
+    if (line <= want && want < line + (sz >> 26)) mine_s = i, mine_from = f, mine_rows = r, mine_len = len, mine_at = x;
+    if (i % ctas == cta) {
+      const int k = atomicAdd(&sh.count, 1);
+      if (k < 64) sh.mine[k] = {prefix + line, i, f, r, len, static_cast<int>(prefix_segs + (x & ((1 << 26) - 1)))};
     }
-    if (pass == 0) {
-      long long x = line, y = segs;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long u = __shfl_up_sync(0xffffffffu, x, o), v = __shfl_up_sync(0xffffffffu, y, o);
-        if (lane >= o) x += u, y += v;
-      }
-      const long long W = prefix + __shfl_sync(0xffffffffu, x, 31);
-      line = x - line;
-      segs = y - segs;
-      const int C = static_cast<int>(min(static_cast<long long>(ctas), W));
-      w.pos = cta < C ? at_first(W, C, cta) : 0;
-      w.end = cta < C ? at_first(W, C, cta + 1) : 0;
-      want = w.pos < w.end ? max(w.pos, prefix) - prefix : -1;  // this CTA's first own tile
-      if (cta == 0 && lane == 0) *a.total = W;
-    }
-  }
+    x += sz;
+  };
   __syncwarp();
+  if (lo < hi) look(lo, from0, rows0, len0, size0);
+  from = from0;
+#pragma unroll 1
+  for (int i = lo + 1; i < hi; ++i) {
+    const int len = a.a.len[i];
+    int r;
+    const long long sz = size(AtWalk::clamp_row(a, a.row_start[i]), AtWalk::clamp_row(a, a.row_start[i + 1]), len, &from, &r);
+    look(i, from, r, len, sz);
+  }
+  const unsigned who = __ballot_sync(0xffffffffu, mine_s >= 0);
+  const int src = who ? __ffs(who) - 1 : 0;
+  w.first_s = __shfl_sync(0xffffffffu, mine_s, src);
+  w.first_begin = __shfl_sync(0xffffffffu, mine_from, src);
   if (w.pos < w.end) {
-    const long long line0 = sh.walk.pos, seg0 = sh.walk.seg;
-    w.first_s = sh.walk.first_s;
-    w.first_begin = sh.walk.first_begin;
     if (w.pos < prefix) {
       w.seg = at_div(w.pos, a.prefix_tiles);
       w.tile = static_cast<int>(w.pos - w.seg * a.prefix_tiles);
     } else {
-      w.enter(a, w.first_s, w.first_begin);
-      long long rest = w.pos - prefix - line0;
+      w.s = w.first_s;
+      w.begin = w.first_begin;
+      w.rows = __shfl_sync(0xffffffffu, mine_rows, src);
+      w.n = __shfl_sync(0xffffffffu, mine_len, src);
+      w.row_tiles = at_row_tiles(a.cut, w.rows);
+      const long long at = __shfl_sync(0xffffffffu, mine_at, src);
+      long long rest = w.pos - prefix - (at >> 26);
       const long long head = at_head_tiles(a.cut, w.n, w.rows);
       w.g = static_cast<int>(at_div(rest, head));
       rest -= w.g * head;
@@ -208,17 +243,22 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
         rest -= static_cast<long long>(w.t) * k;
       }
       w.tile = static_cast<int>(rest);
-      w.seg = prefix_segs + seg0 + static_cast<long long>(w.g) * w.row_tiles + w.t;
+      w.seg = prefix_segs + (at & ((1 << 26) - 1)) + static_cast<long long>(w.g) * w.row_tiles + w.t;
     }
   }
-  __syncwarp();
   if (lane == 0) sh.walk = w;
   __syncwarp();
 }
 
-// One warp, at any time behind at_start: the records that attn_tree_join_kernel goes by.
-__device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh) {
+// One warp, behind its share's last piece: the records that the join goes by.
+__device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh, const AtWalk& w) {
   const int lane = threadIdx.x & 31, count = min(64, sh.count);
+  if (a.prefix_tiles == 0) {
+    if (lane == 0) a.seam[blockIdx.x] = w.seam;
+    for (int k = lane; k < count; k += 32)
+      if (sh.mine[k].rows > 0 && static_cast<long long>(sh.mine[k].n) + sh.mine[k].rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
+    return;
+  }
   for (int k = 0; k < count; ++k) {
     const AtShared::Mine x = sh.mine[k];
     if (x.rows == 0) {  // rows of an unused request

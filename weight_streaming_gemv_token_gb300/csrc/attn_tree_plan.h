@@ -4,9 +4,8 @@
 // The work is a line of key tiles: first those of the shared prefix, head by head and,
 // within a head, row tile by row tile (of all rows of the step); then request by
 // request, head by head, row tile by row tile those of the request's own keys. The
-// tiles of one (request, head, row tile) are a segment. CTA c of C takes the tiles
-// [c W / C, (c + 1) W / C) of the W in all, across segments; its part of a segment is
-// a piece. Numbering segments j = 0, 1, .. along the line, the piece of CTA c in
+// tiles of one (request, head, row tile) are a segment. Each CTA takes an equal
+// share of the W tiles in all, across segments; its part of a segment is a piece. Numbering segments j = 0, 1, .. along the line, the piece of CTA c in
 // segment j has the number c + j: along the line every new piece has a new c or a new
 // j, so no two share a number.
 #pragma once
@@ -59,9 +58,20 @@ WSG_HD long long at_div(long long x, long long y) {
   return x / y;
 }
 
-// First tile of CTA c of C on a line of W tiles, and the CTA that has tile p.
-WSG_HD long long at_first(long long W, int C, int c) { return at_div(c * W, C); }
-WSG_HD int at_owner(long long W, int C, long long p) { return static_cast<int>(at_div((p + 1) * C - 1, W)); }
+// The shares of C CTAs of a line of W tiles: W mod C of W / C + 1 tiles, then the others.
+struct AtShares {
+  long long each, more;  // W / C, W mod C
+};
+WSG_HD AtShares at_shares(long long W, int C) {
+  const long long q = at_div(W, C);
+  return AtShares{q, W - q * C};
+}
+// First tile of CTA c, and the CTA that has tile p.
+WSG_HD long long at_first(const AtShares& s, int c) { return s.each * c + (c < s.more ? c : s.more); }
+WSG_HD int at_owner(const AtShares& s, long long p) {
+  const long long big = s.more * (s.each + 1);
+  return static_cast<int>(p < big ? at_div(p, s.each + 1) : s.more + at_div(p - big, s.each));
+}
 
 inline bool attn_tree_sizes_ok(const attn_tree_args* a) {
   auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
@@ -79,7 +89,7 @@ struct AtPlan {
   AtCut cut;
   int prefix_row_tiles, prefix_tiles;  // of a head; of a segment
   long long pieces;   // numbers that pieces can have
-  size_t o, ml, rec, line, total;  // workspace: outputs, (reference, sum), a record a row, the line's length
+  size_t o, ml, rec, line, total;  // workspace: outputs, (reference, sum), records (of rows or seams), the line's length
 };
 
 // Where a row's pieces are: its own segment starts at tile `line` for head 0 and takes
@@ -89,6 +99,14 @@ struct AtRow {
   long long line, head;
   int32_t tiles, seg, row_tiles;
   int32_t at, next, pad;  // row (token * group) within the row tile; tiles of the row tile behind it
+};
+
+// Without a prefix a row has one segment, and only segments that are cut need joining: at
+// most one starts in a CTA's share and ends behind it. Its pieces have the numbers id ..
+// id + pieces - 1 (0 pieces: none).
+struct AtSeam {
+  long long id;
+  int32_t pieces, begin, m0, nrows, g, pad;
 };
 
 inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
@@ -118,7 +136,7 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   p.o = 0;
   p.ml = up(rows * a->head_dim * 4);
   p.rec = p.ml + up(rows * 8);
-  p.line = p.rec + up(static_cast<size_t>(a->rows) * sizeof(AtRow));
+  p.line = p.rec + up(a->prefix_len > 0 ? static_cast<size_t>(a->rows) * sizeof(AtRow) : static_cast<size_t>(sms) * sizeof(AtSeam));
   p.total = p.line + 256;
   return p;
 }

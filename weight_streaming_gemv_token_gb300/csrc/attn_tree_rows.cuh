@@ -534,7 +534,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
       }
     }
   }
-  if (warp == 0) at_records(p, sh);
+  if (warp == 0) at_records(p, sh, walk);
 }
 
 template <typename QT, int DP, int QP, bool F32>

@@ -142,7 +142,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   unsigned char* Vs = Ks + STAGES * G::TILE;
   float* So = reinterpret_cast<float*>(Vs + STAGES * G::TILE);
   __shared__ AtShared sh;
-  __shared__ AtPiece s_piece[kTtPieces];
+  __shared__ AtPiece s_piece[kTtPieces], s_dry;
   __shared__ uint32_t s_holes[kTtPieces];  // by tile: pages that are missing
   __shared__ __align__(8) uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, o_free, drain, row_bar[4], told[kTtPieces];
@@ -163,7 +163,11 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&row_bar[i], 4);
     for (int i = 0; i < kTtPieces; ++i) mbar_init(&told[i], 1);
     s_fail = 0;
-    s_odd = 0;
+    s_odd = -1;
+    s_dry = AtPiece{};
+    s_dry.prefix = true;
+    s_dry.nrows = kTtRows;
+    s_dry.k1 = kAtKeys;
     fence_mbar_init();
   }
   if (warp == 1) {
@@ -175,8 +179,6 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_base;
-  pdl_wait();
-  pdl_trigger();
   auto fail = [&]() {
     *vfail = 1;
     atomicOr(a.err, ERR_TC_TIMEOUT);
@@ -187,6 +189,8 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     // ---- the share, keys and values ----
     const int who = warp == 0 ? 0 : warp - 1 - kTtSoft;  // which of the loaders
     AtWalk walk;
+    pdl_wait();
+    pdl_trigger();
     if (who == 0) {
       at_start(p, sh);
       walk = sh.walk;
@@ -218,7 +222,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         pc = s_piece[piece % kTtPieces];
       }
       if (pc.tiles == 0) break;
-      if (who == 0) {
+      if (who == 1) {
         // the queries on their way, ahead of the keys that fill the memory's queues
         const int per = p.cut.group * D * 2, t0 = pc.m0 / a.group, t1 = (pc.m0 + pc.nrows - 1) / a.group;
         const char* q0 = static_cast<const char*>(a.q) + (a.q_stride * pc.begin + static_cast<long long>(pc.g) * a.group * D) * 2;
@@ -282,7 +286,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     }
     if (!ok && lane == 0) fail();
     if (who == 0) {
-      at_records(p, sh);
+      at_records(p, sh, walk);
       // the last copies into each stage have landed before the CTA may end, after a failure too
       if (lane == 0) {
         for (int s = 0; s < STAGES; ++s)
@@ -361,9 +365,14 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     float* so = So + (warp - 2) * kTtStage;
     int j = 0, ex = 0;  // tiles, exchanges among a row's threads so far
     bool ok = true;
+    // Piece -1 is made up: a tile of whatever tensor memory holds, whose result goes
+    // nowhere. It has the code of tiles and results fetched while the stream's previous kernel ends
+    // (behind the first keys' copies, which fill the memory's queues, that takes 5 us).
+    bool dry = true;
     auto row_done = [&]() {
       tc_fence_before();
       __syncwarp();
+      if (dry) return true;
       if (lane == 0) mbar_arrive(&row_bar[q]);
       const bool r = __all_sync(0xffffffffu, mbar_wait(&row_bar[q], ex & 1));
       tc_fence_after();
@@ -411,23 +420,23 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
     };
-    int T = piece_at(0);
-    if (T > 0) queries(s_piece[0]);
-    for (int piece = 0; T > 0; ++piece) {
-      const AtPiece& cur = s_piece[piece % kTtPieces];
-      const bool works = q * 32 < cur.nrows, have = v < cur.nrows;
+    int T = 1;
+#pragma unroll 1
+    for (int piece = -1; T > 0; ++piece) {
+      const AtPiece& cur = dry ? s_dry : s_piece[piece % kTtPieces];
+      const bool works = q * 32 < cur.nrows, have = v < cur.nrows && !dry;
       const int m_row = cur.m0 + min(v, cur.nrows - 1), token = m_row / a.group;
       const int k0 = cur.k0, k1 = cur.k1;
       const int plain = cur.prefix ? k1 : min(cur.n, k1);  // keys before this one are seen by every row
       float m_ref = -INFINITY, lsum = 0.f;
       for (int t = 0; t < T; ++t, ++j) {
         const int tk = k0 + t * kAtKeys;
-        if (!__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1))) {
+        if (!dry && !__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1))) {
           ok = false;
           break;
         }
         tc_fence_after();
-        const uint32_t holes = s_holes[j % kTtPieces];
+        const uint32_t holes = dry ? 0u : s_holes[j % kTtPieces];
         const bool special = holes || (tk + kAtKeys > plain && !cur.prefix);
         if (works) {
           const uint32_t tb = tl + static_cast<uint32_t>((j & 1) * 128);
@@ -513,13 +522,18 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&p_full[j & 1]);
+        if (lane == 0 && !dry) mbar_arrive(&p_full[j & 1]);
       }
       if (!ok) break;
+      if (dry) {
+        pdl_wait();
+        pdl_trigger();
+        j = 0;
+      }
       T = piece_at(piece + 1);
       if (T > 0) queries(s_piece[(piece + 1) % kTtPieces]);
       // ---- the piece's result ----
-      if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1))) {
+      if (!dry && !__all_sync(0xffffffffu, mbar_wait(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1))) {
         ok = false;
         break;
       }
@@ -551,7 +565,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             const int r = h * 16 + (lane >> 1);
-            if (q * 32 + r < cur.nrows) put(q * 32 + r, *reinterpret_cast<const uint4*>(so + r * 12 + (lane & 1) * 4));
+            if (q * 32 + r < cur.nrows && !dry) put(q * 32 + r, *reinterpret_cast<const uint4*>(so + r * 12 + (lane & 1) * 4));
           }
         };
 #pragma unroll 1
@@ -562,7 +576,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           if (c0 + 16 >= PART) {  // O is read: the next piece may write it
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&o_free);
+            if (lane == 0 && !dry) mbar_arrive(&o_free);
           }
           if (cur.whole) {
             uint32_t w[8];
@@ -598,6 +612,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
       if (__any_sync(0xffffffffu, *vfail)) ok = false;
       if (!ok) break;
+      dry = false;
     }
     if (!ok && lane == 0) fail();
   }
