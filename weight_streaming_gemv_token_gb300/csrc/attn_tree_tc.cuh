@@ -83,6 +83,49 @@ __device__ __noinline__ bool tt_mend(unsigned char* tile, int tk, int n, int k1,
   return odd;
 }
 
+// Pairs of floats for the two-wide float32 instructions.
+using TtPair = unsigned long long;
+__device__ __forceinline__ TtPair tt_pair(float x, float y) {
+  TtPair p;
+  asm("mov.b64 %0, {%1, %2};" : "=l"(p) : "f"(x), "f"(y));
+  return p;
+}
+__device__ __forceinline__ void tt_unpair(TtPair p, float* x, float* y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(*x), "=f"(*y) : "l"(p)); }
+__device__ __forceinline__ TtPair tt_fma(TtPair a, TtPair b, TtPair c) {
+  TtPair d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ TtPair tt_add(TtPair a, TtPair b) {
+  TtPair d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+__device__ __forceinline__ TtPair tt_sub(TtPair a, TtPair b) {
+  TtPair d;
+  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+// A pair as bfloat16 value and remainder pairs (at_pack_split).
+__device__ __forceinline__ void tt_split(TtPair p, uint32_t* hi, uint32_t* lo) {
+  float x, y;
+  tt_unpair(p, &x, &y);
+  uint32_t h;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(h) : "f"(y), "f"(x));
+  float rx, ry;
+  tt_unpair(tt_sub(p, tt_pair(__uint_as_float(h << 16), __uint_as_float(h & 0xFFFF0000u))), &rx, &ry);
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(*lo) : "f"(ry), "f"(rx));
+  *hi = h;
+}
+__device__ __forceinline__ float tt_max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ float tt_max3(uint32_t a, uint32_t b, uint32_t c) {
+  return tt_max3(__uint_as_float(a), __uint_as_float(b), __uint_as_float(c));
+}
+
 // N registers from or to this warp's lanes of tensor memory.
 template <int N>
 __device__ __forceinline__ void tt_ld(uint32_t (&v)[N], uint32_t at) {
@@ -454,13 +497,13 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             for (int k = 0; k < 32; ++k)
               if (!(see >> k & 1u)) s[k] = 0xff800000u;  // -inf
           }
-          float mh[16];
+          float mh[11];  // three at a time: 32 -> 11 -> 4 -> 2 -> 1
 #pragma unroll
-          for (int k = 0; k < 16; ++k) mh[k] = fmaxf(__uint_as_float(s[k]), __uint_as_float(s[k + 16]));
+          for (int k = 0; k < 10; ++k) mh[k] = tt_max3(s[3 * k], s[3 * k + 1], s[3 * k + 2]);
+          mh[10] = fmaxf(__uint_as_float(s[30]), __uint_as_float(s[31]));
 #pragma unroll
-          for (int w = 8; w >= 1; w >>= 1)
-#pragma unroll
-            for (int k = 0; k < w; ++k) mh[k] = fmaxf(mh[k], mh[k + w]);
+          for (int k = 0; k < 3; ++k) mh[k] = tt_max3(mh[3 * k], mh[3 * k + 1], mh[3 * k + 2]);
+          mh[0] = fmaxf(tt_max3(mh[0], mh[1], mh[2]), fmaxf(mh[9], mh[10]));
           float(&x)[4][kTtRows] = xch[ex & 1];
           x[sl][v] = mh[0];
           if (!row_done()) {
@@ -493,22 +536,26 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             m_ref = nref;
           }
           const float m = m_ref == -INFINITY ? 0.f : m_ref;  // no score seen yet: every term is 0
-          float sum[2] = {0.f, 0.f};
+          const TtPair c2 = tt_pair(c, c), m2 = tt_pair(-m, -m);
+          TtPair sum = tt_pair(0.f, 0.f);
           // over the scores, which all four threads of the row have read
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
             uint32_t ph[8], pl[8];
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-              const float p0 = at_exp2(fmaf(__uint_as_float(s[16 * h + 2 * k]), c, -m));
-              const float p1 = at_exp2(fmaf(__uint_as_float(s[16 * h + 2 * k + 1]), c, -m));
-              sum[k & 1] += p0 + p1;
-              at_pack_split(p0, p1, &ph[k], &pl[k]);
+              float x0, x1;
+              tt_unpair(tt_fma(tt_pair(__uint_as_float(s[16 * h + 2 * k]), __uint_as_float(s[16 * h + 2 * k + 1])), c2, m2), &x0, &x1);
+              const TtPair e = tt_pair(at_exp2(x0), at_exp2(x1));
+              sum = tt_add(sum, e);
+              tt_split(e, &ph[k], &pl[k]);
             }
             tc_st8(tb + sl * 16 + 8 * h, ph);
             tc_st8(tb + 64 + sl * 16 + 8 * h, pl);
           }
-          lsum += sum[0] + sum[1];
+          float s0, s1;
+          tt_unpair(sum, &s0, &s1);
+          lsum += s0 + s1;
           tc_wait_st();
         }
         if (special) {
