@@ -43,8 +43,9 @@ def host(tmp_path_factory):
                    "  return at_keys(cut(group, mt, chain, cap), n, rows, t); }\n"
                    "int tiles(int group, int mt, int chain, int cap, int n, int rows, int t) {\n"
                    "  return at_tiles(cut(group, mt, chain, cap), n, rows, t); }\n"
+                   "int extra() { return kAtExtra; }\n"
                    "long long head(int group, int mt, int chain, int cap, int n, int rows) {\n"
-                   "  return at_head_tiles(cut(group, mt, chain, cap), n, rows); }\n"
+                   "  return at_head_units(cut(group, mt, chain, cap), n, rows); }\n"
                    "long long first(long long W, int C, int c) { return at_first(at_shares(W, C), c); }\n"
                    "int owner(long long W, int C, long long p) { return at_owner(at_shares(W, C), p); }\n"
                    "int meet(size_t p, size_t a, size_t q, size_t b) {\n"
@@ -82,7 +83,7 @@ def test_keys_of_row_tiles(host):
             assert host.keys(group, mt, 0, n + 1, n, rows, t) == n + 1  # the table ends there
             assert host.tiles(group, mt, 0, 0, n, rows, t) == 1  # no table: still a tile, for the rows' zeros
         for chain in (0, 1):
-            assert host.head(group, mt, chain, big, n, rows) == sum(host.tiles(group, mt, chain, big, n, rows, t) for t in range(T))
+            assert host.head(group, mt, chain, big, n, rows) == sum(host.tiles(group, mt, chain, big, n, rows, t) + host.extra() for t in range(T))
     assert host.keys(2, 16, 0, 1 << 30, 2**31 - 1, 2**20, 0) == 1 << 30
 
 
@@ -117,23 +118,33 @@ def test_pieces_have_numbers_of_their_own_inside_the_workspace(W, host):
         assert host.plan(ctypes.byref(a), out) == 1
         p = dict(zip(NAMES, out))
         cap, mt = 16 * width, p["mt"]
+        E = host.extra()
         segs = [p["prefix_tiles"]] * (n_kv * p["prefix_row_tiles"])
         for R, n in zip(rows.tolist(), lens.tolist()):
             if n >= 0 and R > 0:
                 segs += [host.tiles(group, mt, chain, cap, n, R, i) for i in range(-(-R * group // mt))] * n_kv
-        line = sum(segs)
-        if line == 0:
+        if not segs:
             continue
+        starts, seen = np.concatenate([[0], np.cumsum(np.array(segs) + E)]), {}
+        line = int(starts[-1])
         C = min(152, line)
-        starts, seen = np.concatenate([[0], np.cumsum(segs)]), set()
         for c in range(C):
             lo, hi = host.first(line, C, c), host.first(line, C, c + 1)
             j = int(np.searchsorted(starts, lo, side="right")) - 1
             while lo < hi:
                 end = min(hi, int(starts[j + 1]))
-                assert c + j not in seen and c + j < p["pieces"], trial
-                seen.add(c + j)
+                t0, t1 = (max(0, x - int(starts[j]) - E) for x in (lo, end))
+                if t1 > t0:
+                    assert c + j not in seen and c + j < p["pieces"], trial
+                    seen[c + j] = (j, t0, t1)
                 lo, j = end, j + 1
+        for j, kt in enumerate(segs):  # the pieces that a join looks at are those there are, and cover the segment
+            c0, c1 = host.owner(line, C, int(starts[j]) + E), host.owner(line, C, int(starts[j]) + E + kt - 1)
+            parts = [seen[c + j] for c in range(c0, c1 + 1)]
+            assert [x[0] for x in parts] == [j] * len(parts)
+            assert [x[1] for x in parts] == [0] + [x[2] for x in parts[:-1]] and parts[-1][2] == kt
+        assert len(seen) == sum(host.owner(line, C, int(starts[j]) + E + kt - 1) - host.owner(line, C, int(starts[j]) + E) + 1
+                                for j, kt in enumerate(segs))
         slots = p["pieces"] * mt
         assert p["o"] == 0 and slots * d * 4 <= p["ml"] and p["ml"] + slots * 8 <= p["rec"]
         assert p["rec"] + p["rec_bytes"] <= p["line"] and p["line"] + 8 <= p["total"]

@@ -18,11 +18,30 @@
 namespace wsg {
 namespace {
 
-// Without a prefix: CTA (y, x) joins a quarter of the rows (32; of 16 rows the first
-// takes all) of the segment that starts in share x and is cut. Eight warps, four rows
-// each, lane i elements 4 i .. 4 i + 3 of a head.
+// N more partial results of a row (reference and sum q, elements y) into (m, l, x), as
+// ar_merge8 does eight.
+template <int N>
+__device__ __forceinline__ void at_merge(const float2 (&q)[N], const float4 (&y)[N], float* m, float* l, float4* x) {
+  float mn = *m;
+#pragma unroll
+  for (int i = 0; i < N; ++i) mn = fmaxf(mn, q[i].x);
+  const float mu = mn == -INFINITY ? 0.f : mn, f = am_exp2(*m - mu);
+  *l *= f;
+  x->x *= f, x->y *= f, x->z *= f, x->w *= f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    const float e = q[i].x == -INFINITY ? 1.f : am_exp2(q[i].x - mu);
+    *l = fmaf(q[i].y, e, *l);
+    x->x = fmaf(y[i].x, e, x->x), x->y = fmaf(y[i].y, e, x->y), x->z = fmaf(y[i].z, e, x->z), x->w = fmaf(y[i].w, e, x->w);
+  }
+  *m = mn;
+}
+
+// Without a prefix: CTAs (x, .) join the rows of the cut segment with record x, a row a
+// warp, lane i elements 4 i .. 4 i + 3 of a head. (All CTAs fit the GPU at once: eight
+// rows of every CTA's record a CTA took 8 us for 152 records, most of them empty.)
 template <typename QT>
-__global__ void __launch_bounds__(256) attn_tree_seam_kernel(const AtArgs p) {
+__global__ void __launch_bounds__(256, 4) attn_tree_seam_kernel(const AtArgs p) {
   const AmArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_trigger();  // a following call's set-up may begin
@@ -30,20 +49,20 @@ __global__ void __launch_bounds__(256) attn_tree_seam_kernel(const AtArgs p) {
   const AtSeam s = p.seam[blockIdx.x];
   if (s.pieces == 0) return;
   const bool in = lane * 4 < a.d;
-  for (int r = blockIdx.y * 32 + warp; r < min(s.nrows, static_cast<int>(blockIdx.y) * 32 + 32); r += 8) {
+  for (int r = blockIdx.y * 8 + warp; r < s.nrows; r += 8 * gridDim.y) {
     float m = -INFINITY, l = 0.f;
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int s0 = 0; s0 < s.pieces; s0 += 8) {  // eight pieces at a time: their loads go out together
-      float2 q[8];
-      float4 y[8];
+    for (int s0 = 0; s0 < s.pieces; s0 += 4) {  // four pieces at a time: their loads go out together
+      float2 q[4];
+      float4 y[4];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int i = 0; i < 4; ++i) {
         const bool have = s0 + i < s.pieces;
         const long long at = ((s.id + s0 + i) << p.cut.mshift) + r;
         q[i] = have ? a.part_ml[at] : make_float2(-INFINITY, 0.f);
         y[i] = have && in ? *reinterpret_cast<const float4*>(a.part_o + at * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
       }
-      ar_merge8(q, y, &m, &l, &x);
+      at_merge(q, y, &m, &l, &x);
     }
     const int row = s.m0 + r, token = row / a.group;
     if (in) at_put<QT>(p, s.begin + token, s.g * a.group + row - token * a.group, lane * 4, x, m, l);
@@ -55,48 +74,75 @@ template <typename QT>
 __global__ void __launch_bounds__(128) attn_tree_join_kernel(const AtArgs p, int ctas) {
   const AmArgs& a = p.a;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int w = blockIdx.x * 4 + warp;
   pdl_trigger();  // a following call's set-up may begin
   pdl_wait();
-  if (w >= a.rows * a.n_q) return;
-  const int row = w / a.n_q, head = w - row * a.n_q, g = head / a.group, h = head - g * a.group;
-  AtRow rec = p.rec[row];
-  const long long W = *p.total;
-  if (rec.tiles == 0) return;  // of no request, or an unused one
-  const AtShares C = at_shares(W, static_cast<int>(min(static_cast<long long>(ctas), W)));
-  int at = rec.at + h;
-  if (at >> p.cut.mshift) {  // the row tile behind the record's
-    at -= 1 << p.cut.mshift;
-    rec.line += rec.tiles;
-    rec.tiles = rec.next;
-    ++rec.seg;
-  }
-  const long long line = rec.line + g * rec.head;
-  const int c0 = at_owner(C, line), c1 = at_owner(C, line + rec.tiles - 1);
-  const long long own = rec.seg + static_cast<long long>(g) * rec.row_tiles + c0;  // number of the first piece
-  const int own_n = c1 - c0 + 1;
-  const int pm = row * a.group + h, rt = pm >> p.cut.mshift, pre_at = pm - (rt << p.cut.mshift);
-  const long long seg = static_cast<long long>(g) * p.prefix_row_tiles + rt, from = seg * p.prefix_tiles;
-  const int d0 = at_owner(C, from), pre_n = at_owner(C, from + p.prefix_tiles - 1) - d0 + 1;
-  const long long pre = seg + d0;  // the prefix's pieces, as above
-  const bool in = lane * 4 < a.d;
-  const int parts = own_n + pre_n;
-  float m = -INFINITY, l = 0.f;
-  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-  // eight pieces at a time: their loads go out together
-  for (int s0 = 0; s0 < parts; s0 += 8) {
-    float2 q[8];
-    float4 y[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int s = s0 + i;
-      const long long r = s < pre_n ? ((pre + s) << p.cut.mshift) + pre_at : ((own + s - pre_n) << p.cut.mshift) + at;
-      q[i] = s < parts ? a.part_ml[r] : make_float2(-INFINITY, 0.f);
-      y[i] = s < parts && in ? *reinterpret_cast<const float4*>(a.part_o + r * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int w = blockIdx.x * 4 + warp; w < a.rows * a.n_q; w += gridDim.x * 4) {
+    const int row = w / a.n_q, head = w - row * a.n_q, g = head / a.group, h = head - g * a.group;
+    AtRow rec = p.rec[row];
+    const long long W = *p.total;
+    if (rec.tiles == 0) continue;  // of no request, or an unused one
+    const AtShares C = at_shares(W, static_cast<int>(min(static_cast<long long>(ctas), W)));
+    int at = rec.at + h;
+    if (at >> p.cut.mshift) {  // the row tile behind the record's
+      at -= 1 << p.cut.mshift;
+      rec.line += rec.tiles + kAtExtra;
+      rec.tiles = rec.next;
+      ++rec.seg;
     }
-    ar_merge8(q, y, &m, &l, &x);
+    const long long line = rec.line + g * rec.head;
+    const int c0 = at_owner(C, line), c1 = at_owner(C, line + rec.tiles - 1);
+    const long long own = rec.seg + static_cast<long long>(g) * rec.row_tiles + c0;  // number of the first piece
+    const int own_n = c1 - c0 + 1;
+    const int pm = row * a.group + h, rt = pm >> p.cut.mshift, pre_at = pm - (rt << p.cut.mshift);
+    const long long seg = static_cast<long long>(g) * p.prefix_row_tiles + rt, from = seg * (p.prefix_tiles + kAtExtra) + kAtExtra;
+    const int d0 = at_owner(C, from), pre_n = at_owner(C, from + p.prefix_tiles - 1) - d0 + 1;
+    const long long pre = seg + d0;  // the prefix's pieces, as above
+    const bool in = lane * 4 < a.d;
+    const int parts = own_n + pre_n;
+    float m = -INFINITY, l = 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    // eight pieces at a time: their loads go out together
+    for (int s0 = 0; s0 < parts; s0 += 8) {
+      float2 q[8];
+      float4 y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int s = s0 + i;
+        const long long r = s < pre_n ? ((pre + s) << p.cut.mshift) + pre_at : ((own + s - pre_n) << p.cut.mshift) + at;
+        q[i] = s < parts ? a.part_ml[r] : make_float2(-INFINITY, 0.f);
+        y[i] = s < parts && in ? *reinterpret_cast<const float4*>(a.part_o + r * a.d + lane * 4) : make_float4(0.f, 0.f, 0.f, 0.f);
+      }
+      at_merge(q, y, &m, &l, &x);
+    }
+    if (in) at_put<QT>(p, row, head, lane * 4, x, m, l);
   }
-  if (in) at_put<QT>(p, row, head, lane * 4, x, m, l);
+}
+
+// The join's kernels ask for the largest shared-memory split, which the kernels beside
+// them in the stream need: an SM that changes its split first runs empty.
+template <typename K>
+cudaError_t at_prepare(K kern, bool* done) {
+  if (*done) return cudaSuccess;
+  const cudaError_t e = allow_smem_shared(kern, 0);
+  *done = e == cudaSuccess;
+  return e;
+}
+
+template <typename QT>
+cudaError_t launch_join(const AtArgs& t, const AtPlan& p, const DeviceInfo& di, cudaStream_t s) {
+  static bool done[2][64] = {};
+  if (t.prefix_tiles == 0) {
+    const cudaError_t e = at_prepare(attn_tree_seam_kernel<QT>, &done[0][di.device]);
+    if (e != cudaSuccess) return e;
+    // as many CTAs of eight rows as the GPU holds at once
+    const int most = 4 * di.sms / p.seams, need = (1 << p.cut.mshift) / 8;
+    return launch_k(attn_tree_seam_kernel<QT>, dim3(p.seams, need < most ? need : most), dim3(256), 0, s, true, t);
+  }
+  const cudaError_t e = at_prepare(attn_tree_join_kernel<QT>, &done[1][di.device]);
+  if (e != cudaSuccess) return e;
+  const long long warps = (static_cast<long long>(t.a.rows) * t.a.n_q + 3) / 4;
+  return launch_k(attn_tree_join_kernel<QT>, dim3(static_cast<unsigned>(warps < 6 * di.sms ? warps : 6 * di.sms)), dim3(128), 0,
+                  s, true, t, di.sms);
 }
 
 }  // namespace
@@ -193,6 +239,8 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
   t.lse = a->lse;
   t.rec = reinterpret_cast<AtRow*>(w + p.rec);
   t.seam = reinterpret_cast<AtSeam*>(w + p.rec);
+  t.seams = p.seams;
+  t.seam_segs = p.pieces - di.sms <= di.sms;
   t.total = reinterpret_cast<long long*>(w + p.line);
   const bool qf = a->qdtype == DEC_F32;
   if (p.tc) {
@@ -201,14 +249,6 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
   } else {
     WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_tree_f32(t, qf, di, s) : launch_tree_bf16(t, qf, di, s));
   }
-  if (a->prefix_len == 0) {
-    const dim3 seams(di.sms, p.tc ? 4 : 1);
-    WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_tree_seam_kernel<float>, seams, dim3(256), 0, s, true, t)
-                             : launch_k(attn_tree_seam_kernel<uint16_t>, seams, dim3(256), 0, s, true, t));
-    return DEC_OK;
-  }
-  const unsigned grid = static_cast<unsigned>((static_cast<long long>(a->rows) * a->n_q + 3) / 4);
-  WSG_CUDA_TRY(nullptr, qf ? launch_k(attn_tree_join_kernel<float>, dim3(grid), dim3(128), 0, s, true, t, di.sms)
-                           : launch_k(attn_tree_join_kernel<uint16_t>, dim3(grid), dim3(128), 0, s, true, t, di.sms));
+  WSG_CUDA_TRY(nullptr, qf ? launch_join<float>(t, p, di, s) : launch_join<uint16_t>(t, p, di, s));
   return DEC_OK;
 }

@@ -18,8 +18,9 @@ struct AtArgs {
   int out16;  // rows of out can be written in 16-byte pieces
   float* lse;
   AtRow* rec;        // with a prefix: of every row
-  AtSeam* seam;      // without: of every CTA
-  long long* total;  // [1]: key tiles of the line
+  AtSeam* seam;      // without: [seams], by segment (seam_segs) or by CTA
+  int seams, seam_segs;
+  long long* total;  // [1]: units of the line
 };
 
 // A piece: keys k0 .. k1 - 1 of a segment against its rows.
@@ -35,13 +36,15 @@ struct AtPiece {
 
 // The way of a CTA along the line.
 struct AtWalk {
-  long long pos, end, prefix;  // tiles; those of the prefix
+  long long pos, end, prefix;  // units; those of the prefix
   long long seg;               // number of the segment at hand
   // the request at hand (s < 0: none yet)
-  int s, begin, rows, n, g, t, tile, row_tiles;
+  int s, begin, rows, n, g, t, unit, row_tiles;  // unit: the place in the segment
   int first_s, first_begin;    // where the requests begin for this CTA
   AtShares shares;
   AtSeam seam;                 // the segment that starts in this share and is cut behind it
+  int seam_seg;
+  int seg0, seg1;              // segments that start in this share, of all requests' for the last CTA
 
   __device__ __forceinline__ static int clamp_row(const AtArgs& a, int r) { return min(max(0, r), a.a.rows); }
 
@@ -88,7 +91,7 @@ struct AtWalk {
       }
       kt = at_tiles(a.cut, n, rows, t);
       p.prefix = false;
-      p.whole = tile == 0 && prefix == 0 && kt <= end - pos;
+      p.whole = prefix == 0;
       p.s = s;
       p.g = g;
       p.begin = begin;
@@ -98,23 +101,27 @@ struct AtWalk {
       p.k1 = at_keys(a.cut, n, rows, t);
       ++t;
     }
-    const int take = static_cast<int>(min(static_cast<long long>(kt - tile), end - pos));
+    const int left = kt + kAtExtra - unit, take = static_cast<int>(min(static_cast<long long>(left), end - pos));
+    const int t0 = max(0, unit - kAtExtra), t1 = max(0, unit + take - kAtExtra);
+    p.whole = p.whole && t0 == 0 && t1 == kt;
     p.nrows = min(1 << a.cut.mshift, p.rows * a.cut.group - p.m0);
-    p.k0 = tile << kAtKeyShift;
-    p.k1 = min(p.k1, (tile + take) << kAtKeyShift);
-    p.tiles = take;
+    p.k0 = t0 << kAtKeyShift;
+    p.k1 = min(p.k1, t1 << kAtKeyShift);
+    p.tiles = t1 - t0;  // (0: the share ends in front of the segment's tiles)
     p.id = seg + blockIdx.x;
-    if (tile == 0 && take < kt) {  // (the share's last piece)
+    if (t0 == 0 && t1 > 0 && t1 < kt) {  // (the share's last piece)
+      seam_seg = static_cast<int>(seg);
       seam.id = p.id;
-      seam.pieces = at_owner(shares, pos + kt - 1) - static_cast<int>(blockIdx.x) + 1;
+      seam.pieces = at_owner(shares, pos + left - 1) - static_cast<int>(blockIdx.x) + 1;
       seam.begin = p.begin;
       seam.m0 = p.m0;
       seam.nrows = p.nrows;
       seam.g = p.g;
     }
     pos += take;
-    tile = 0;
+    unit = 0;
     ++seg;
+    if (t0 == 0 && t1 > 0) seg1 = static_cast<int>(seg);
     return p;
   }
 };
@@ -124,6 +131,7 @@ struct AtWalk {
 struct AtShared {
   AtWalk walk;
   int count, top;  // top: behind the requests' last row
+  int segs;        // segments in all
   struct Mine {
     long long line;
     int s, begin, rows, n, seg;
@@ -154,12 +162,12 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
   int before = __shfl_up_sync(0xffffffffu, top, 1);
   if (lane == 0) before = 0;
   // A request from its row start and the next one's, `from` the highest start before: its first
-  // row; rows; key tiles << 26 | segments (at most n_kv times the rows and 2^24 / 16 of those).
+  // row; rows; units << 26 | segments (at most n_kv times the rows and 2^24 / 16 of those).
   auto size = [&](int start, int end, int len, int* from, int* n_rows) -> long long {
     *from = max(*from, start);
     *n_rows = len < 0 ? 0 : max(0, end - *from);
     if (*n_rows == 0) return 0;
-    return (a.cut.n_kv * at_head_tiles(a.cut, len, *n_rows)) << 26 | static_cast<long long>(a.cut.n_kv * at_row_tiles(a.cut, *n_rows));
+    return (a.cut.n_kv * at_head_units(a.cut, len, *n_rows)) << 26 | static_cast<long long>(a.cut.n_kv * at_row_tiles(a.cut, *n_rows));
   };
   int from0 = before, rows0;
   const long long size0 = lo < hi ? size(rs0, rs1, len0, &from0, &rows0) : (rows0 = 0, 0);
@@ -176,13 +184,14 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * a.prefix_tiles;
-  const long long W = prefix + (__shfl_sync(0xffffffffu, x, 31) >> 26);
+  const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * (a.prefix_tiles + kAtExtra);
+  const long long all = __shfl_sync(0xffffffffu, x, 31), W = prefix + (all >> 26), segments = prefix_segs + (all & ((1 << 26) - 1));
   x -= sum;  // of the requests before this lane's
   AtWalk w;
   w.pos = w.end = 0;
   w.shares = AtShares{1, 0};
   w.seam = AtSeam{};
+  w.seam_seg = -1;
   if (cta < W) {
     w.shares = at_shares(W, static_cast<int>(min(static_cast<long long>(ctas), W)));
     w.pos = at_first(w.shares, cta);
@@ -190,10 +199,10 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
   }
   if (cta == 0 && lane == 0) *a.total = W;
   w.s = -1;
-  w.tile = w.g = w.t = w.rows = w.row_tiles = w.n = w.begin = 0;
+  w.unit = w.g = w.t = w.rows = w.row_tiles = w.n = w.begin = 0;
   w.seg = 0;
   w.prefix = prefix;
-  // this CTA's first own tile, and the request that has it
+  // this CTA's first unit of requests, and the request that has it
   const long long want = w.pos < w.end ? max(w.pos, prefix) - prefix : -1;
   int mine_s = -1, mine_from = 0, mine_rows = 0, mine_len = 0;
   long long mine_at = 0;
@@ -222,8 +231,8 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
   w.first_begin = __shfl_sync(0xffffffffu, mine_from, src);
   if (w.pos < w.end) {
     if (w.pos < prefix) {
-      w.seg = at_div(w.pos, a.prefix_tiles);
-      w.tile = static_cast<int>(w.pos - w.seg * a.prefix_tiles);
+      w.seg = at_div(w.pos, a.prefix_tiles + kAtExtra);
+      w.unit = static_cast<int>(w.pos - w.seg * (a.prefix_tiles + kAtExtra));
     } else {
       w.s = w.first_s;
       w.begin = w.first_begin;
@@ -232,21 +241,24 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
       w.row_tiles = at_row_tiles(a.cut, w.rows);
       const long long at = __shfl_sync(0xffffffffu, mine_at, src);
       long long rest = w.pos - prefix - (at >> 26);
-      const long long head = at_head_tiles(a.cut, w.n, w.rows);
+      const long long head = at_head_units(a.cut, w.n, w.rows);
       w.g = static_cast<int>(at_div(rest, head));
       rest -= w.g * head;
       if (a.cut.chain) {
-        for (int k; rest >= (k = at_tiles(a.cut, w.n, w.rows, w.t)); ++w.t) rest -= k;
+        for (int k; rest >= (k = at_tiles(a.cut, w.n, w.rows, w.t) + kAtExtra); ++w.t) rest -= k;
       } else {
-        const int k = at_tiles(a.cut, w.n, w.rows, 0);
+        const int k = at_tiles(a.cut, w.n, w.rows, 0) + kAtExtra;
         w.t = static_cast<int>(at_div(rest, k));
         rest -= static_cast<long long>(w.t) * k;
       }
-      w.tile = static_cast<int>(rest);
+      w.unit = static_cast<int>(rest);
       w.seg = prefix_segs + (at & ((1 << 26) - 1)) + static_cast<long long>(w.g) * w.row_tiles + w.t;
     }
   }
-  if (lane == 0) sh.walk = w;
+  // (the segment at hand starts here unless its first tile lies before)
+  w.seg0 = static_cast<int>(w.seg) + (w.unit > kAtExtra ? 1 : 0);
+  w.seg1 = w.seg0;
+  if (lane == 0) sh.walk = w, sh.segs = static_cast<int>(segments);
   __syncwarp();
 }
 
@@ -254,7 +266,14 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
 __device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh, const AtWalk& w) {
   const int lane = threadIdx.x & 31, count = min(64, sh.count);
   if (a.prefix_tiles == 0) {
-    if (lane == 0) a.seam[blockIdx.x] = w.seam;
+    if (!a.seam_segs) {
+      if (lane == 0) a.seam[blockIdx.x] = w.seam;
+    } else {
+      // segments that start in this share, and in CTA 0 those that there are not
+      for (int k = w.seg0 + lane; k < w.seg1; k += 32) a.seam[k] = k == w.seam_seg ? w.seam : AtSeam{};
+      if (blockIdx.x == 0)
+        for (int k = sh.segs + lane; k < a.seams; k += 32) a.seam[k] = AtSeam{};
+    }
     for (int k = lane; k < count; k += 32)
       if (sh.mine[k].rows > 0 && static_cast<long long>(sh.mine[k].n) + sh.mine[k].rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
     return;
@@ -266,7 +285,7 @@ __device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh, 
       for (int r = x.begin + lane; r < e; r += 32) a.rec[r].tiles = 0;
       continue;
     }
-    const long long head = at_head_tiles(a.cut, x.n, x.rows);
+    const long long head = at_head_units(a.cut, x.n, x.rows);
     const int rt = at_row_tiles(a.cut, x.rows);
     if (lane == 0 && static_cast<long long>(x.n) + x.rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
     for (int i = lane; i < x.rows; i += 32) {
@@ -274,7 +293,7 @@ __device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh, 
       // the other's follows from it
       const int t = (i * a.cut.group) >> a.cut.mshift;
       AtRow r;
-      r.line = x.line + at_tiles_before(a.cut, x.n, x.rows, t);
+      r.line = x.line + at_units_before(a.cut, x.n, x.rows, t) + kAtExtra;
       r.head = head;
       r.tiles = at_tiles(a.cut, x.n, x.rows, t);
       r.seg = x.seg + t;

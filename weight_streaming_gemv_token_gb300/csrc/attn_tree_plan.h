@@ -4,8 +4,11 @@
 // The work is a line of key tiles: first those of the shared prefix, head by head and,
 // within a head, row tile by row tile (of all rows of the step); then request by
 // request, head by head, row tile by row tile those of the request's own keys. The
-// tiles of one (request, head, row tile) are a segment. Each CTA takes an equal
-// share of the W tiles in all, across segments; its part of a segment is a piece. Numbering segments j = 0, 1, .. along the line, the piece of CTA c in
+// tiles of one (request, head, row tile) are a segment, in front of which kAtExtra units
+// without a tile stand for what a segment costs beside its tiles (queries, first and last
+// steps; without them the CTA with a step's shortest requests ends last: 64 rows behind
+// 131,072 shared tokens 148 us, with them EXTRA_FIGURE). Each CTA takes an equal
+// share of the W units in all, across segments; its part of a segment is a piece. Numbering segments j = 0, 1, .. along the line, the piece of CTA c in
 // segment j has the number c + j: along the line every new piece has a new c or a new
 // j, so no two share a number.
 #pragma once
@@ -17,6 +20,7 @@
 namespace wsg {
 
 constexpr int kAtBatch = 4096, kAtKeyShift = 7, kAtKeys = 1 << kAtKeyShift;  // requests; keys a tile
+constexpr int kAtExtra = 2;
 
 // What the cutting goes by. rows * group < 2^24, capacity <= 2^30: 32-bit arithmetic.
 struct AtCut {
@@ -43,14 +47,14 @@ WSG_HD int at_tiles(const AtCut& c, int n, int rows, int t) {
   const int k = (at_keys(c, n, rows, t) + kAtKeys - 1) >> kAtKeyShift;
   return k < 1 ? 1 : k;
 }
-// Key tiles of one head of a request's row tiles before t.
-WSG_HD long long at_tiles_before(const AtCut& c, int n, int rows, int t) {
-  if (!c.chain) return static_cast<long long>(t) * at_tiles(c, n, rows, 0);
+// Units of one head of a request's row tiles before t.
+WSG_HD long long at_units_before(const AtCut& c, int n, int rows, int t) {
+  if (!c.chain) return static_cast<long long>(t) * (at_tiles(c, n, rows, 0) + kAtExtra);
   long long sum = 0;
-  for (int u = 0; u < t; ++u) sum += at_tiles(c, n, rows, u);
+  for (int u = 0; u < t; ++u) sum += at_tiles(c, n, rows, u) + kAtExtra;
   return sum;
 }
-WSG_HD long long at_head_tiles(const AtCut& c, int n, int rows) { return at_tiles_before(c, n, rows, at_row_tiles(c, rows)); }
+WSG_HD long long at_head_units(const AtCut& c, int n, int rows) { return at_units_before(c, n, rows, at_row_tiles(c, rows)); }
 
 // x / y of non-negative numbers; the 64-bit division, some 100 instructions, only where needed.
 WSG_HD long long at_div(long long x, long long y) {
@@ -58,7 +62,7 @@ WSG_HD long long at_div(long long x, long long y) {
   return x / y;
 }
 
-// The shares of C CTAs of a line of W tiles: W mod C of W / C + 1 tiles, then the others.
+// The shares of C CTAs of a line of W units: W mod C of W / C + 1 units, then the others.
 struct AtShares {
   long long each, more;  // W / C, W mod C
 };
@@ -66,7 +70,7 @@ WSG_HD AtShares at_shares(long long W, int C) {
   const long long q = at_div(W, C);
   return AtShares{q, W - q * C};
 }
-// First tile of CTA c, and the CTA that has tile p.
+// First unit of CTA c, and the CTA that has unit p.
 WSG_HD long long at_first(const AtShares& s, int c) { return s.each * c + (c < s.more ? c : s.more); }
 WSG_HD int at_owner(const AtShares& s, long long p) {
   const long long big = s.more * (s.each + 1);
@@ -89,11 +93,12 @@ struct AtPlan {
   AtCut cut;
   int prefix_row_tiles, prefix_tiles;  // of a head; of a segment
   long long pieces;   // numbers that pieces can have
+  int seams;          // records of seams: the most segments there can be, or the CTAs
   size_t o, ml, rec, line, total;  // workspace: outputs, (reference, sum), records (of rows or seams), the line's length
 };
 
-// Where a row's pieces are: its own segment starts at tile `line` for head 0 and takes
-// `tiles` of it (0: a row without a result), `head` tiles on for the next head; its
+// Where a row's pieces are: its own segment's first tile is unit `line` for head 0, of
+// `tiles` (0: a row without a result), `head` units on for the next head; its
 // number is seg for head 0, row_tiles on for the next.
 struct AtRow {
   long long line, head;
@@ -103,7 +108,8 @@ struct AtRow {
 
 // Without a prefix a row has one segment, and only segments that are cut need joining: at
 // most one starts in a CTA's share and ends behind it. Its pieces have the numbers id ..
-// id + pieces - 1 (0 pieces: none).
+// id + pieces - 1 (0 pieces: none). Records lie by segment where there are no more of
+// those than CTAs, else by CTA.
 struct AtSeam {
   long long id;
   int32_t pieces, begin, m0, nrows, g, pad;
@@ -130,7 +136,9 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   }
   // the requests' row tiles: rows * group / mt whole ones at most, one more each
   const long long own = static_cast<long long>(a->rows) * group / mt + (a->batch < a->rows ? a->batch : a->rows);
-  p.pieces = sms + (own + p.prefix_row_tiles) * a->n_kv;
+  const long long segments = (own + p.prefix_row_tiles) * a->n_kv;
+  p.pieces = sms + segments;
+  p.seams = segments < sms ? static_cast<int>(segments) : sms;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = static_cast<size_t>(p.pieces) * mt;
   p.o = 0;

@@ -542,7 +542,7 @@ cudaError_t at_launch_one(const AtArgs& a, const DeviceInfo& di, cudaStream_t st
   constexpr size_t smem = AtGeom<QT, DP, F32>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[di.device]) {
-    const cudaError_t e = allow_smem(attn_tree_rows_kernel<QT, DP, QP, F32>, smem);
+    const cudaError_t e = allow_smem_shared(attn_tree_rows_kernel<QT, DP, QP, F32>, smem);
     if (e != cudaSuccess) return e;
     lifted[di.device] = true;
   }

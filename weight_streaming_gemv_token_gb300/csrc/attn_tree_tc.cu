@@ -8,7 +8,7 @@ template <int D>
 dec_status launch(const AtArgs& t, const CUtensorMap* maps, const DeviceInfo& di, cudaStream_t st) {
   static bool lifted[64] = {};
   if (!lifted[di.device]) {
-    WSG_CUDA_TRY(nullptr, allow_smem(attn_tree_tc_kernel<D>, TtGeom<D>::SMEM));
+    WSG_CUDA_TRY(nullptr, allow_smem_shared(attn_tree_tc_kernel<D>, TtGeom<D>::SMEM));
     lifted[di.device] = true;
   }
   WSG_CUDA_TRY(nullptr, launch_k(attn_tree_tc_kernel<D>, dim3(di.sms), dim3(kTtThreads), TtGeom<D>::SMEM, st, true, maps[0],
