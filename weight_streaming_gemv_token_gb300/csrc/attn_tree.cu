@@ -196,7 +196,6 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
   DeviceInfo di;
   const dec_status st = device_info(&di, nullptr);
   if (st != DEC_OK) return st;
-  if (di.sms < kAtBatch / 64) return fail(nullptr, DEC_EDEVICE, "attn_tree_paged: %d SMs", di.sms);
   const AtPlan p = attn_tree_plan(a, di.sms);
   if (a->workspace_bytes < p.total)
     return fail(nullptr, DEC_ENOMEM, "attn_tree_paged: workspace has %zu bytes, %zu needed", a->workspace_bytes, p.total);

@@ -126,57 +126,63 @@ struct AtWalk {
   }
 };
 
-// A CTA's place on the line, and the requests whose rows' records it writes (s modulo
-// the CTAs; 4096 requests at most, 64 CTAs at least).
-struct AtShared {
-  AtWalk walk;
-  int count, top;  // top: behind the requests' last row
-  int segs;        // segments in all
-  struct Mine {
-    long long line;
-    int s, begin, rows, n, seg;
-  } mine[64];
+// The requests' sums as one warp forms them, a run of requests a lane: units << 26 |
+// segments of all requests (at most n_kv times the rows and 2^24 / 16 of those), of those
+// before this lane's, and this lane's first request. Row starts that fall are lifted to
+// the highest before.
+struct AtSums {
+  int lo, hi;          // this lane's requests
+  int from, rows, len; // the first one's first row, rows, tokens
+  long long size, before, all;
+  int end;             // behind the requests' last row
 };
 
-// One warp: sums the requests' lengths, a run of them a lane, and finds this CTA's place.
-// What it costs is the chain of its loads and shuffles before the first keys can be asked
-// for, so the first request of each lane (up to 32 requests: all) is kept in registers, and
-// key tiles and segments go through the sums as one number.
-__device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
-  const int lane = threadIdx.x & 31, batch = a.a.batch, ctas = gridDim.x, cta = blockIdx.x;
-  const int per = (batch + 31) >> 5, lo = min(batch, lane * per), hi = min(batch, lo + per);
-  const int rs0 = AtWalk::clamp_row(a, a.row_start[lo]), rs1 = AtWalk::clamp_row(a, a.row_start[min(batch, lo + 1)]);
-  const int len0 = lo < hi ? a.a.len[lo] : -1;
-  const int rs_end = lane == 31 ? AtWalk::clamp_row(a, a.row_start[batch]) : 0;
-  if (lane == 0) sh.count = 0;
-  // the highest row start before this lane's first request (starts that fall are lifted)
-  int top = lo < hi ? rs0 : 0;
-#pragma unroll 4
-  for (int i = lo + 1; i < hi; ++i) top = max(top, AtWalk::clamp_row(a, a.row_start[i]));
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, top, o);
-    if (lane >= o) top = max(top, y);
-  }
-  if (lane == 31) sh.top = max(top, rs_end);
-  int before = __shfl_up_sync(0xffffffffu, top, 1);
-  if (lane == 0) before = 0;
-  // A request from its row start and the next one's, `from` the highest start before: its first
-  // row; rows; units << 26 | segments (at most n_kv times the rows and 2^24 / 16 of those).
-  auto size = [&](int start, int end, int len, int* from, int* n_rows) -> long long {
-    *from = max(*from, start);
-    *n_rows = len < 0 ? 0 : max(0, end - *from);
-    if (*n_rows == 0) return 0;
-    return (a.cut.n_kv * at_head_units(a.cut, len, *n_rows)) << 26 | static_cast<long long>(a.cut.n_kv * at_row_tiles(a.cut, *n_rows));
-  };
-  int from0 = before, rows0;
-  const long long size0 = lo < hi ? size(rs0, rs1, len0, &from0, &rows0) : (rows0 = 0, 0);
-  long long sum = size0;
-  int from = from0;
+// A request from its row start and the next one's, *from the highest start before: *from its
+// first row; *rows; units << 26 | segments.
+__device__ __forceinline__ long long at_size(const AtArgs& a, int start, int end, int len, int* from, int* rows) {
+  *from = max(*from, start);
+  *rows = len < 0 ? 0 : max(0, end - *from);
+  if (*rows == 0) return 0;
+  return (a.cut.n_kv * at_head_units(a.cut, len, *rows)) << 26 | static_cast<long long>(a.cut.n_kv * at_row_tiles(a.cut, *rows));
+}
+
+__device__ __forceinline__ AtSums at_sums(const AtArgs& a) {
+  const int lane = threadIdx.x & 31, batch = a.a.batch, per = (batch + 31) >> 5;
+  AtSums s;
+  s.lo = min(batch, lane * per);
+  s.hi = min(batch, s.lo + per);
+  auto start = [&](int i) { return AtWalk::clamp_row(a, a.row_start[i]); };
+  const int rs0 = start(s.lo), rs1 = start(min(batch, s.lo + 1));
+  s.len = s.lo < s.hi ? a.a.len[s.lo] : -1;
+  s.end = start(batch);
+  bool rising = rs0 <= rs1;
+  int top = s.lo < s.hi ? rs0 : 0;
 #pragma unroll 2
-  for (int i = lo + 1; i < hi; ++i) {
+  for (int i = s.lo + 1; i < s.hi; ++i) {
+    const int x = start(i);
+    rising = rising && x <= start(i + 1);
+    top = max(top, x);
+  }
+  int before = rs0;  // the highest start before this lane's requests, or theirs
+  if (!__all_sync(0xffffffffu, rising)) {
+#pragma unroll 1
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, top, o);
+      if (lane >= o) top = max(top, y);
+    }
+    s.end = max(s.end, __shfl_sync(0xffffffffu, top, 31));
+    before = __shfl_up_sync(0xffffffffu, top, 1);
+    if (lane == 0) before = 0;
+  }
+  s.from = before;
+  s.rows = 0;
+  s.size = s.lo < s.hi ? at_size(a, rs0, rs1, s.len, &s.from, &s.rows) : 0;
+  long long sum = s.size;
+  int from = s.from;
+#pragma unroll 1
+  for (int i = s.lo + 1; i < s.hi; ++i) {
     int r;
-    sum += size(AtWalk::clamp_row(a, a.row_start[i]), AtWalk::clamp_row(a, a.row_start[i + 1]), a.a.len[i], &from, &r);
+    sum += at_size(a, start(i), start(i + 1), a.a.len[i], &from, &r);
   }
   long long x = sum;
 #pragma unroll
@@ -184,9 +190,35 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
     const long long y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
+  s.all = __shfl_sync(0xffffffffu, x, 31);
+  s.before = x - sum;
+  return s;
+}
+
+// Calls f(request, first row, rows, tokens, size, sizes before) for this lane's requests.
+template <typename F>
+__device__ __forceinline__ void at_each(const AtArgs& a, const AtSums& s, F f) {
+  if (s.lo >= s.hi) return;
+  f(s.lo, s.from, s.rows, s.len, s.size, s.before);
+  long long x = s.before + s.size;
+  int from = s.from;
+#pragma unroll 1
+  for (int i = s.lo + 1; i < s.hi; ++i) {
+    const int len = a.a.len[i];
+    int r;
+    const long long size = at_size(a, AtWalk::clamp_row(a, a.row_start[i]), AtWalk::clamp_row(a, a.row_start[i + 1]), len, &from, &r);
+    f(i, from, r, len, size, x);
+    x += size;
+  }
+}
+
+// One warp: this CTA's place on the line. What it costs is a chain of loads, shuffles and
+// divisions before the first keys can be asked for: 2,700 cycles for up to 32 requests.
+__device__ __forceinline__ AtWalk at_start(const AtArgs& a) {
+  const int ctas = gridDim.x, cta = blockIdx.x;
+  const AtSums s = at_sums(a);
   const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * (a.prefix_tiles + kAtExtra);
-  const long long all = __shfl_sync(0xffffffffu, x, 31), W = prefix + (all >> 26), segments = prefix_segs + (all & ((1 << 26) - 1));
-  x -= sum;  // of the requests before this lane's
+  const long long W = prefix + (s.all >> 26);
   AtWalk w;
   w.pos = w.end = 0;
   w.shares = AtShares{1, 0};
@@ -197,7 +229,6 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
     w.pos = at_first(w.shares, cta);
     w.end = at_first(w.shares, cta + 1);
   }
-  if (cta == 0 && lane == 0) *a.total = W;
   w.s = -1;
   w.unit = w.g = w.t = w.rows = w.row_tiles = w.n = w.begin = 0;
   w.seg = 0;
@@ -206,25 +237,9 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
   const long long want = w.pos < w.end ? max(w.pos, prefix) - prefix : -1;
   int mine_s = -1, mine_from = 0, mine_rows = 0, mine_len = 0;
   long long mine_at = 0;
-  auto look = [&](int i, int f, int r, int len, long long sz) {
-    const long long line = x >> 26;
-    if (line <= want && want < line + (sz >> 26)) mine_s = i, mine_from = f, mine_rows = r, mine_len = len, mine_at = x;
-    if (i % ctas == cta) {
-      const int k = atomicAdd(&sh.count, 1);
-      if (k < 64) sh.mine[k] = {prefix + line, i, f, r, len, static_cast<int>(prefix_segs + (x & ((1 << 26) - 1)))};
-    }
-    x += sz;
-  };
-  __syncwarp();
-  if (lo < hi) look(lo, from0, rows0, len0, size0);
-  from = from0;
-#pragma unroll 1
-  for (int i = lo + 1; i < hi; ++i) {
-    const int len = a.a.len[i];
-    int r;
-    const long long sz = size(AtWalk::clamp_row(a, a.row_start[i]), AtWalk::clamp_row(a, a.row_start[i + 1]), len, &from, &r);
-    look(i, from, r, len, sz);
-  }
+  at_each(a, s, [&](int i, int f, int r, int len, long long size, long long x) {
+    if (x >> 26 <= want && want < (x >> 26) + (size >> 26)) mine_s = i, mine_from = f, mine_rows = r, mine_len = len, mine_at = x;
+  });
   const unsigned who = __ballot_sync(0xffffffffu, mine_s >= 0);
   const int src = who ? __ffs(who) - 1 : 0;
   w.first_s = __shfl_sync(0xffffffffu, mine_s, src);
@@ -241,15 +256,16 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
       w.row_tiles = at_row_tiles(a.cut, w.rows);
       const long long at = __shfl_sync(0xffffffffu, mine_at, src);
       long long rest = w.pos - prefix - (at >> 26);
-      const long long head = at_head_units(a.cut, w.n, w.rows);
-      w.g = static_cast<int>(at_div(rest, head));
-      rest -= w.g * head;
       if (a.cut.chain) {
+        const long long head = at_head_units(a.cut, w.n, w.rows);
+        w.g = static_cast<int>(at_div(rest, head));
+        rest -= w.g * head;
         for (int k; rest >= (k = at_tiles(a.cut, w.n, w.rows, w.t) + kAtExtra); ++w.t) rest -= k;
       } else {
-        const int k = at_tiles(a.cut, w.n, w.rows, 0) + kAtExtra;
-        w.t = static_cast<int>(at_div(rest, k));
-        rest -= static_cast<long long>(w.t) * k;
+        const int k = at_tiles(a.cut, w.n, w.rows, 0) + kAtExtra, n = static_cast<int>(at_div(rest, k));
+        rest -= static_cast<long long>(n) * k;
+        w.g = n / w.row_tiles;
+        w.t = n - w.g * w.row_tiles;
       }
       w.unit = static_cast<int>(rest);
       w.seg = prefix_segs + (at & ((1 << 26) - 1)) + static_cast<long long>(w.g) * w.row_tiles + w.t;
@@ -258,56 +274,61 @@ __device__ __forceinline__ void at_start(const AtArgs& a, AtShared& sh) {
   // (the segment at hand starts here unless its first tile lies before)
   w.seg0 = static_cast<int>(w.seg) + (w.unit > kAtExtra ? 1 : 0);
   w.seg1 = w.seg0;
-  if (lane == 0) sh.walk = w, sh.segs = static_cast<int>(segments);
-  __syncwarp();
+  return w;
 }
 
-// One warp, behind its share's last piece: the records that the join goes by.
-__device__ __forceinline__ void at_records(const AtArgs& a, const AtShared& sh, const AtWalk& w) {
-  const int lane = threadIdx.x & 31, count = min(64, sh.count);
-  if (a.prefix_tiles == 0) {
+// One warp, behind its share's last piece: the records that the join goes by, and tokens
+// beyond the tables. Of requests s with s % gridDim.x == blockIdx.x.
+__device__ __forceinline__ void at_records(const AtArgs& a, const AtWalk& w) {
+  const int lane = threadIdx.x & 31;
+  const AtSums s = at_sums(a);
+  const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles;
+  const bool by_row = a.prefix_tiles > 0;
+  if (blockIdx.x == 0 && lane == 0) *a.total = w.prefix + (s.all >> 26);
+  if (!by_row) {
     if (!a.seam_segs) {
       if (lane == 0) a.seam[blockIdx.x] = w.seam;
     } else {
       // segments that start in this share, and in CTA 0 those that there are not
       for (int k = w.seg0 + lane; k < w.seg1; k += 32) a.seam[k] = k == w.seam_seg ? w.seam : AtSeam{};
       if (blockIdx.x == 0)
-        for (int k = sh.segs + lane; k < a.seams; k += 32) a.seam[k] = AtSeam{};
+        for (int k = static_cast<int>(s.all & ((1 << 26) - 1)) + lane; k < a.seams; k += 32) a.seam[k] = AtSeam{};
     }
-    for (int k = lane; k < count; k += 32)
-      if (sh.mine[k].rows > 0 && static_cast<long long>(sh.mine[k].n) + sh.mine[k].rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
-    return;
   }
-  for (int k = 0; k < count; ++k) {
-    const AtShared::Mine x = sh.mine[k];
-    if (x.rows == 0) {  // rows of an unused request
-      const int e = max(x.begin, AtWalk::clamp_row(a, a.row_start[x.s + 1]));
-      for (int r = x.begin + lane; r < e; r += 32) a.rec[r].tiles = 0;
-      continue;
+  at_each(a, s, [&](int i, int from, int rows, int len, long long size, long long x) {
+    if (i % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) return;
+    if (rows > 0 && static_cast<long long>(len) + rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
+    if (!by_row) return;
+    if (rows == 0) {  // rows of an unused request
+      const int e = max(from, AtWalk::clamp_row(a, a.row_start[i + 1]));
+      for (int r = from; r < e; ++r) a.rec[r].tiles = 0;
+      return;
     }
-    const long long head = at_head_units(a.cut, x.n, x.rows);
-    const int rt = at_row_tiles(a.cut, x.rows);
-    if (lane == 0 && static_cast<long long>(x.n) + x.rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
-    for (int i = lane; i < x.rows; i += 32) {
+    const long long head = at_head_units(a.cut, len, rows);
+    const int rt = at_row_tiles(a.cut, rows);
+    long long line = w.prefix + (x >> 26) + kAtExtra;
+    int t = 0, tiles = at_tiles(a.cut, len, rows, 0);
+    for (int k = 0; k < rows; ++k) {
       // a token's query heads may lie in two row tiles: the record is the first one's,
       // the other's follows from it
-      const int t = (i * a.cut.group) >> a.cut.mshift;
+      const int at = (k * a.cut.group) >> a.cut.mshift;
+      for (; t < at; ++t) line += tiles + kAtExtra, tiles = at_tiles(a.cut, len, rows, t + 1);
       AtRow r;
-      r.line = x.line + at_units_before(a.cut, x.n, x.rows, t) + kAtExtra;
+      r.line = line;
       r.head = head;
-      r.tiles = at_tiles(a.cut, x.n, x.rows, t);
-      r.seg = x.seg + t;
+      r.tiles = tiles;
+      r.seg = static_cast<int>(prefix_segs + (x & ((1 << 26) - 1))) + t;
       r.row_tiles = rt;
-      r.at = i * a.cut.group - (t << a.cut.mshift);
-      r.next = t + 1 < rt ? at_tiles(a.cut, x.n, x.rows, t + 1) : 0;
+      r.at = k * a.cut.group - (t << a.cut.mshift);
+      r.next = t + 1 < rt ? at_tiles(a.cut, len, rows, t + 1) : 0;
       r.pad = 0;
-      a.rec[x.begin + i] = r;
+      a.rec[from + k] = r;
     }
-  }
-  if (blockIdx.x == 0) {  // rows of no request
+  });
+  if (by_row && blockIdx.x == 0) {  // rows of no request
     const int first = AtWalk::clamp_row(a, a.row_start[0]);
     for (int r = lane; r < first; r += 32) a.rec[r].tiles = 0;
-    for (int r = sh.top + lane; r < a.a.rows; r += 32) a.rec[r].tiles = 0;
+    for (int r = s.end + lane; r < a.a.rows; r += 32) a.rec[r].tiles = 0;
   }
 }
 

@@ -403,7 +403,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
   using Copy = std::conditional_t<F32, AtCopy32<DP>, AtCopy16<DP>>;
   constexpr int WARPS = G::WARPS, KB = Core::KB, NTHREADS = 32 * WARPS;
   extern __shared__ __align__(128) unsigned char am_raw[];
-  __shared__ AtShared sh;
+  __shared__ AtWalk s_walk;
   __shared__ float s_m[WARPS][16], s_l[WARPS][16];
   const AmArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5;
@@ -412,9 +412,12 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
   const Copy copy(a.d, mine);
   pdl_wait();
   pdl_trigger();
-  if (warp == 0) at_start(p, sh);
+  if (warp == 0) {
+    const AtWalk w = at_start(p);
+    if ((tid & 31) == 0) s_walk = w;
+  }
   __syncthreads();
-  AtWalk walk = sh.walk;
+  AtWalk walk = s_walk;
   for (bool again = false;; again = true) {
     const AtPiece pc = walk.next(p);
     if (pc.tiles == 0) break;
@@ -534,7 +537,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
       }
     }
   }
-  if (warp == 0) at_records(p, sh, walk);
+  if (warp == 0) at_records(p, walk);
 }
 
 template <typename QT, int DP, int QP, bool F32>

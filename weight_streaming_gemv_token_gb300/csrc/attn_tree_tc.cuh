@@ -184,7 +184,6 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   unsigned char* Ks = reinterpret_cast<unsigned char*>((reinterpret_cast<uintptr_t>(tt_raw) + 1023) & ~uintptr_t(1023));
   unsigned char* Vs = Ks + STAGES * G::TILE;
   float* So = reinterpret_cast<float*>(Vs + STAGES * G::TILE);
-  __shared__ AtShared sh;
   __shared__ AtPiece s_piece[kTtPieces], s_dry;
   __shared__ uint32_t s_holes[kTtPieces];  // by tile: pages that are missing
   __shared__ __align__(8) uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
@@ -231,13 +230,10 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   if (warp == 0 || warp > 1 + kTtSoft) {
     // ---- the share, keys and values ----
     const int who = warp == 0 ? 0 : warp - 1 - kTtSoft;  // which of the loaders
-    AtWalk walk;
     pdl_wait();
     pdl_trigger();
-    if (who == 0) {
-      at_start(p, sh);
-      walk = sh.walk;
-    }
+    AtWalk walk;
+    if (who == 0) walk = at_start(p);
     int j = 0;  // tiles so far
     bool ok = true;
     AtPiece pc{};
@@ -329,7 +325,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     }
     if (!ok && lane == 0) fail();
     if (who == 0) {
-      at_records(p, sh, walk);
+      at_records(p, walk);
       // the last copies into each stage have landed before the CTA may end, after a failure too
       if (lane == 0) {
         for (int s = 0; s < STAGES; ++s)
