@@ -797,8 +797,8 @@ dec_status attn_tree_paged(const attn_tree_args* a, void* stream);
  * (nullable, int32 [rows]): the token of the greatest resulting float32 logit, the
  * lowest of equal ones; NaN counts as masked; -1 if no logit is above -inf. out is
  * nullable where next is given, and may be logits itself (same dtype, stride).
- * vocab up to 2^20; up to 2^19 tokens a text, as many drafted ones and 1023 biases a
- * list (longer ones are cut). Outputs must not overlap anything else. */
+ * vocab up to 2^20, rows up to 2^19 - 8; up to 2^19 tokens a text, as many drafted
+ * ones and 1023 biases a list (longer ones are cut). Outputs must not overlap anything else. */
 typedef struct {
   int32_t rows, vocab, requests;
   int32_t xdtype, ydtype; /* logits; out: DEC_F32 or DEC_BF16 */
