@@ -246,7 +246,9 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
     const dec_status e = launch_tree_tc(t, di, s);
     if (e != DEC_OK) return e;
   } else {
-    WSG_CUDA_TRY(nullptr, a->kvdtype == DEC_F32 ? launch_tree_f32(t, qf, di, s) : launch_tree_bf16(t, qf, di, s));
+    const bool kf = a->kvdtype == DEC_F32;
+    WSG_CUDA_TRY(nullptr, kf ? (qf ? launch_tree_f32_f32(t, di, s) : launch_tree_bf16_f32(t, di, s))
+                             : (qf ? launch_tree_f32_bf16(t, di, s) : launch_tree_bf16_bf16(t, di, s)));
   }
   WSG_CUDA_TRY(nullptr, qf ? launch_join<float>(t, p, di, s) : launch_join<uint16_t>(t, p, di, s));
   return DEC_OK;

@@ -377,8 +377,11 @@ __device__ __forceinline__ void at_put(const AtArgs& p, int row, int head, int e
     p.lse[static_cast<long long>(row) * p.a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
-cudaError_t launch_tree_bf16(const AtArgs& a, bool q_f32, const DeviceInfo& di, cudaStream_t st);
-cudaError_t launch_tree_f32(const AtArgs& a, bool q_f32, const DeviceInfo& di, cudaStream_t st);
+// by the types of queries and cache
+cudaError_t launch_tree_bf16_bf16(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_f32_bf16(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_bf16_f32(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_f32_f32(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 dec_status launch_tree_tc(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace wsg

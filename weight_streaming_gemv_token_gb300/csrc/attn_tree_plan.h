@@ -7,10 +7,10 @@
 // tiles of one (request, head, row tile) are a segment, in front of which kAtExtra units
 // without a tile stand for what a segment costs beside its tiles (queries, first and last
 // steps; without them the CTA with a step's shortest requests ends last: 64 rows behind
-// 131,072 shared tokens 148 us, with them EXTRA_FIGURE). Each CTA takes an equal
-// share of the W units in all, across segments; its part of a segment is a piece. Numbering segments j = 0, 1, .. along the line, the piece of CTA c in
-// segment j has the number c + j: along the line every new piece has a new c or a new
-// j, so no two share a number.
+// 131,072 shared tokens 148 us, with them 127). Each CTA takes an equal share
+// of the W units in all, across segments; its part of a segment is a piece. Numbering
+// segments j = 0, 1, .. along the line, the piece of CTA c in segment j has the number
+// c + j: along the line every new piece has a new c or a new j, so no two share a number.
 #pragma once
 #include <cstdint>
 
@@ -128,7 +128,17 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   p.tc = a->qdtype == DEC_BF16 && a->kvdtype == DEC_BF16 && (a->head_dim == 128 || a->head_dim == 64) && a->page_size >= 8 &&
          a->table_stride > 0 && a->num_pages > 0 && static_cast<long long>(a->num_pages) * a->n_kv < 1ll << 31 &&
          (a->prefix_len == 0 || a->prefix_stride < 1ll << 31);
-  p.cut.mshift = p.tc ? 7 : 4;
+  // otherwise as many rows a row tile as a request brings on average, 16 to 64. In tiles of
+  // 16, of 32 or 64, float32 queries: 8 x 32 rows x 4,096 tokens of bfloat16 79 and 74 us,
+  // 32 x 128 rows 932 and 622; of float32, where the products bound either, 117 and 120,
+  // 1,610 and 1,530.
+  const long long most = static_cast<long long>(a->rows) * group / (a->batch < a->rows ? a->batch : a->rows);
+  if (p.tc)
+    p.cut.mshift = 7;
+  else if (a->kvdtype == DEC_F32)
+    p.cut.mshift = most <= 32 ? 4 : 6;
+  else
+    p.cut.mshift = most <= 16 ? 4 : most <= 32 ? 5 : 6;
   const int mt = 1 << p.cut.mshift;
   if (a->prefix_len > 0) {
     p.prefix_row_tiles = at_row_tiles(p.cut, a->rows);

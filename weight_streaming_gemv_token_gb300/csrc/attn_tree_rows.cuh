@@ -1,8 +1,10 @@
 // Attention of a step's rows on warp-level matrix instructions, for every type, head
-// size and page size: row tiles of 16 rows (attn_tree_plan.h), a CTA a share of the
-// line of key tiles, its eight warps the blocks of a piece's keys in turn, each
-// through rings of its own (attn_rows.cuh: bfloat16 caches, keys as the M side; float32
-// caches as in attn_mma.cuh: tf32 value and remainder, three products).
+// size and page size: row tiles of 16, 32 or 64 rows (attn_tree_plan.h), a CTA a share of
+// the line of key tiles. Its eight warps are RG groups of 16 rows times 8 / RG rings: the
+// warps of a ring stream blocks of keys through it together, each copying a part, and each
+// holds its 16 rows against every block (attn_rows.cuh: bfloat16 caches, blocks of 16 keys
+// as the M side; float32 caches as in attn_mma.cuh: blocks of 8 keys, tf32 value and
+// remainder, three products). So the keys are read once for up to 64 rows.
 //
 // Blocks that hold drafted rows' keys mask scores row by row. A value that is not
 // finite would reach rows that do not see it through its product with a weight of 0,
@@ -32,53 +34,74 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
   // row, keys' words: seen[t][j] of row 8 t + 2 (lane % 4) + j
   __device__ __forceinline__ static int row_of(int i) { return 8 * (i >> 1) + 2 * (threadIdx.x & 3) + (i & 1); }
 
-  __device__ __forceinline__ void consume_drafts(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale,
-                                                 const uint32_t (&seen)[4]) {
+  // DRAFTS: scores masked by row, and values that are not finite added afterwards. Products
+  // into one accumulator stand apart: back to back each would wait for the one before it
+  // (two warps a scheduler do not hide that).
+  template <bool DRAFTS>
+  __device__ __forceinline__ void consume_block(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale,
+                                                const uint32_t (&seen)[4]) {
     const int lane = threadIdx.x & 31;
     const uint32_t vt = kt + TILE;
-    float s[2][4] = {};
+    constexpr int CH = QP == 1 ? 2 : QP;  // chains of sums a row group: k steps by parity, or the queries' parts
+    float sc[CH][2][4] = {};
 #pragma unroll
     for (int k = 0; k < KK; ++k) {
       uint32_t ka[4];
       am_ld4(ka, kt + (lane & 15) * PITCH + k * 32 + (lane >> 4) * 16);
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < QP; ++i)
 #pragma unroll
-        for (int i = 0; i < QP; ++i) am_mma16(s[t], ka, this->q[i][k][t][0], this->q[i][k][t][1]);
+        for (int t = 0; t < 2; ++t) am_mma16(sc[QP == 1 ? k & 1 : i][t], ka, this->q[i][k][t][0], this->q[i][k][t][1]);
     }
+    float s[2][4];
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (!(((ok & seen[2 * t + (i & 1)]) >> ((lane >> 2) + 8 * (i >> 1))) & 1u)) s[t][i] = -INFINITY;
-    uint32_t p[2][PP][2];
+      for (int i = 0; i < 4; ++i) {
+        s[t][i] = sc[CH - 1][t][i];
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      float mx[2];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        mx[j] = fmaxf(s[t][j], s[t][2 + j]);
-        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 4));
-        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 8));
-        mx[j] = fmaxf(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], 16)) * scale;
+        for (int c = CH - 2; c >= 0; --c) s[t][i] += sc[c][t][i];
+        const uint32_t may = DRAFTS ? ok & seen[2 * t + (i & 1)] : ok;
+        if (!((may >> ((lane >> 2) + 8 * (i >> 1))) & 1u)) s[t][i] = -INFINITY;
       }
-      if (__any_sync(0xffffffffu, mx[0] > this->m[t][0] + kAmMargin || mx[1] > this->m[t][1] + kAmMargin)) {
+    float mx[2][2];
+    bool move = false;
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mx[t][j] = fmaxf(s[t][j], s[t][2 + j]);
+#pragma unroll
+    for (int d = 4; d < 32; d *= 2)
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) mx[t][j] = fmaxf(mx[t][j], __shfl_xor_sync(0xffffffffu, mx[t][j], d));
+#pragma unroll
+    for (int t = 0; t < 2; ++t)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) mx[t][j] *= scale, move |= mx[t][j] > this->m[t][j] + kAmMargin;
+    if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float nr = mx[j] > this->m[t][j] + kAmMargin ? mx[j] : this->m[t][j];
-          const float f = nr == this->m[t][j] ? 1.f : am_exp2(this->m[t][j] - nr);
+          const float nr = mx[t][j] > this->m[t][j] + kAmMargin ? mx[t][j] : this->m[t][j];
+          const float f = nr == this->m[t][j] ? 1.f : am_exp2(this->m[t][j] - nr);  // 0 on the first move
           this->m[t][j] = nr;
           this->l[t][j] *= f;
 #pragma unroll
           for (int k = 0; k < KK; ++k) this->o[k][t][j] *= f, this->o[k][t][2 + j] *= f;
         }
-      }
+    }
+    uint32_t p[2][PP][2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const float mu = this->m[t][j] == -INFINITY ? 0.f : this->m[t][j];
+        const float mu = this->m[t][j] == -INFINITY ? 0.f : this->m[t][j];  // nothing seen yet: every term is 0
         s[t][j] = am_exp2(fmaf(s[t][j], scale, -mu));
         s[t][2 + j] = am_exp2(fmaf(s[t][2 + j], scale, -mu));
-        this->l[t][j] += s[t][j] + s[t][2 + j];
+        this->l[t][j] += s[t][j] + s[t][2 + j];  // this lane's keys only
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -89,22 +112,30 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
       }
     }
     bool odd = false;
+    constexpr int KS = KK < 2 ? 1 : 2;  // k steps at a time
 #pragma unroll
-    for (int k = 0; k < KK; ++k) {
-      uint32_t va[4];
-      am_ld4t(va, vt + ((lane >> 4) * 8 + (lane & 7)) * PITCH + k * 32 + ((lane >> 3) & 1) * 16);
+    for (int k = 0; k < KK; k += KS) {
+      uint32_t va[KS][4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const uint32_t c = at_finite2(va[i]);
-        odd |= c != va[i];
-        va[i] = c;
+      for (int u = 0; u < KS; ++u) {
+        am_ld4t(va[u], vt + ((lane >> 4) * 8 + (lane & 7)) * PITCH + (k + u) * 32 + ((lane >> 3) & 1) * 16);
+        if (DRAFTS) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t c = at_finite2(va[u][i]);
+            odd |= c != va[u][i];
+            va[u][i] = c;
+          }
+        }
       }
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int i = 0; i < PP; ++i)
 #pragma unroll
-        for (int i = 0; i < PP; ++i) am_mma16(this->o[k][t], va, p[t][i][0], p[t][i][1]);
+        for (int u = 0; u < KS; ++u)
+#pragma unroll
+          for (int t = 0; t < 2; ++t) am_mma16(this->o[k + u][t], va[u], p[t][i][0], p[t][i][1]);
     }
-    if (__any_sync(0xffffffffu, odd)) {
+    if (DRAFTS && __any_sync(0xffffffffu, odd)) {
       for (int key = 0; key < 16; ++key)
 #pragma unroll
         for (int k = 0; k < KK; ++k)
@@ -124,9 +155,9 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
   __device__ __forceinline__ void block(uint32_t kt, const unsigned char* vp, uint32_t ok, float scale, bool drafts,
                                         const uint32_t (&seen)[4]) {
     if (drafts)
-      consume_drafts(kt, vp, ok, scale, seen);
+      consume_block<true>(kt, vp, ok, scale, seen);
     else
-      this->consume(kt, ok, scale);
+      consume_block<false>(kt, vp, ok, scale, seen);
   }
 
   // each row's reference and sum, one lane a row
@@ -157,14 +188,6 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
           put(r, k * 16 + 8 + (lane >> 2), this->o[k][t][2 + j] * x);
         }
       }
-  }
-};
-
-template <int DP>
-struct AtCopy16 : ArCopy<DP> {
-  using ArCopy<DP>::ArCopy;
-  __device__ __forceinline__ uint32_t prefix(const AmArgs& a, int stage, int g, int k, int n) const {
-    return this->run(stage, a.pk, a.pv, a.pstride * g + k, n);
   }
 };
 
@@ -207,7 +230,7 @@ struct AtCore32 {
         const uint32_t qh[4] = {fh.x, fh.y, fh.z, fh.w}, ql[4] = {fl.x, fl.y, fl.z, fl.w};
         am_mma8(s, qh, bh0, bh1);
         am_mma8(s2, qh, bl0, bl1);
-        am_mma8(s3, ql, bh0, bh1);
+        if (sizeof(QT) == 4) am_mma8(s3, ql, bh0, bh1);  // bfloat16 queries have no remainder
       }
     }
     // register j is row lane / 4 + 8 (j / 2), key 2 (lane % 4) + j % 2
@@ -314,36 +337,34 @@ struct AtCore32 {
   }
 };
 
-// A block's 8 keys and values into a stage by one warp; the mask of the keys that
-// count (the others arrive as zeros).
-template <int DP>
-struct AtCopy32 {
-  static constexpr int KB = 8, PITCH = DP * 4 + 16, TILE = KB * PITCH;
-  static constexpr int CP = DP / 4, KPI = 32 / CP > 0 ? 32 / CP : 1, STEPS = KB * CP / 32;
-  int row_bytes, chunks;
+// A block's keys and values into a ring slot by the RG warps that share the ring, `part`
+// being one of them: each copies every RG-th step. The mask of the keys that count; the
+// others arrive as zeros.
+template <int KEYS, int ELEM, int DP, int RG>
+struct AtCopy {
+  static constexpr int PITCH = DP * ELEM + 16, TILE = KEYS * PITCH;
+  static constexpr int CP = DP * ELEM / 16, KPI = 32 / CP, STEPS = KEYS / KPI;  // pieces a padded row; keys a step; steps
+  static_assert(KPI >= 1 && STEPS >= 1, "a step is a warp's copies");
+  int row_bytes, chunks, part, lkey, lc;
   uint32_t ring;
-  int lkey, lc;
 
-  __device__ __forceinline__ AtCopy32(int d, unsigned char* at) {
+  __device__ __forceinline__ AtCopy(int d, uint32_t ring_, int part_) {
     const int lane = threadIdx.x & 31;
-    row_bytes = d * 4;
-    chunks = d / 4;
-    ring = smem_u32(at);
+    row_bytes = d * ELEM;
+    chunks = row_bytes / 16;
+    part = part_;
+    ring = ring_;
     lkey = lane / CP, lc = lane % CP;
   }
-  __device__ __forceinline__ void pad(int d, unsigned char* at) const {  // columns past the head stay zero
-    const int n = CP - chunks;
-    if (n > 0)
-      for (int i = threadIdx.x & 31; i < 4 * KB * n; i += 32)
-        *reinterpret_cast<uint4*>(at + i / n * PITCH + (chunks + i % n) * 16) = make_uint4(0, 0, 0, 0);
-  }
-  __device__ __forceinline__ uint32_t run(int stage, const void* kb, const void* vb, long long row, int n) const {
-    const uint32_t dst = ring + stage * 2 * TILE + lkey * PITCH + lc * 16;
+  __device__ __forceinline__ uint32_t run(int slot, const void* kb, const void* vb, long long row, int n) const {
+    const uint32_t dst = ring + slot * 2 * TILE + lkey * PITCH + lc * 16;
     const long long off = row * row_bytes + lkey * row_bytes + lc * 16;
     const char *ks = static_cast<const char*>(kb) + off, *vs = static_cast<const char*>(vb) + off;
     if (lc < chunks) {
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
+      for (int j = 0; j < (STEPS + RG - 1) / RG; ++j) {
+        const int i = j * RG + part;
+        if (STEPS % RG && i >= STEPS) break;
         const bool in = lkey + i * KPI < n;
         am_copy16(dst + i * KPI * PITCH, in ? ks + i * (KPI * row_bytes) : kb, in ? 16 : 0);
         am_copy16(dst + i * KPI * PITCH + TILE, in ? vs + i * (KPI * row_bytes) : vb, in ? 16 : 0);
@@ -351,16 +372,14 @@ struct AtCopy32 {
     }
     return (1u << n) - 1u;
   }
-  __device__ __forceinline__ uint32_t prefix(const AmArgs& a, int stage, int g, int k, int n) const {
-    return run(stage, a.pk, a.pv, a.pstride * g + k, n);
-  }
-  __device__ __forceinline__ uint32_t pages(const AmArgs& a, int stage, const int32_t* trow, int32_t entry, int g, int k,
+  // keys k .. k + n - 1 of a request's pages; `entry` is the table's for key k
+  __device__ __forceinline__ uint32_t pages(const AmArgs& a, int slot, const int32_t* trow, int32_t entry, int g, int k,
                                             int n) const {
     const int lane = threadIdx.x & 31;
-    if (a.pool.shift >= 3) {  // the block lies in one page
+    if (1 << a.pool.shift >= KEYS) {  // the block lies in one page
       const int page = entry >= 0 && entry < a.pool.num_pages ? entry : -1;
       if (page < 0 && lane == 0) atomicOr(a.err, ERR_BAD_PAGE);
-      return run(stage, a.kp, a.vp, page < 0 ? 0 : pool_row(a.pool, page, g, k), page < 0 ? 0 : n);
+      return run(slot, a.kp, a.vp, page < 0 ? 0 : pool_row(a.pool, page, g, k), page < 0 ? 0 : n);
     }
     long long row = -1;  // lane `key` looks its own page up
     if (lane < n) {
@@ -370,9 +389,11 @@ struct AtCopy32 {
       else
         atomicOr(a.err, ERR_BAD_PAGE);
     }
-    const uint32_t dst = ring + stage * 2 * TILE + lkey * PITCH + lc * 16;
+    const uint32_t dst = ring + slot * 2 * TILE + lkey * PITCH + lc * 16;
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
+    for (int j = 0; j < (STEPS + RG - 1) / RG; ++j) {
+      const int i = j * RG + part;
+      if (STEPS % RG && i >= STEPS) break;
       const long long r = __shfl_sync(0xffffffffu, row, lkey + i * KPI);
       if (lc < chunks) {
         const long long off = r < 0 ? 0 : r * row_bytes + lc * 16;
@@ -386,48 +407,57 @@ struct AtCopy32 {
 
 // ---- the kernel --------------------------------------------------------------------
 
-template <typename QT, int DP, bool F32>
+// RG groups of 16 rows, KG = 8 / RG rings of blocks; SLOTS blocks of a ring.
+template <typename QT, int DP, bool F32, int RG>
 struct AtGeom {
-  static constexpr int WARPS = 8;
-  static constexpr int RING = F32 ? 4 * 8 * (DP * 4 + 16) : 4 * 16 * (DP * 2 + 16);
-  static constexpr int JOIN = 16 * DP * 4;
-  static constexpr int PER_WARP = RING > JOIN ? RING : JOIN;
-  static constexpr int QBYTES = F32 ? 2 * (DP / 8) * 32 * 16 : 0;
-  static constexpr int SMEM = QBYTES + WARPS * PER_WARP;
+  static constexpr int WARPS = 8, KG = WARPS / RG;
+  static constexpr int BLOCK = F32 ? 2 * 8 * (DP * 4 + 16) : 2 * 16 * (DP * 2 + 16);
+  static constexpr int SLOTS = RG == 1 ? 3 : RG == 2 ? 5 : 8;
+  static constexpr int RING = SLOTS * BLOCK;
+  static constexpr int JOIN = WARPS * 16 * DP * 4;
+  static constexpr int QBYTES = F32 ? RG * 2 * (DP / 8) * 32 * 16 : 0;
+  static constexpr int SMEM = QBYTES + (KG * RING > JOIN ? KG * RING : JOIN);
 };
 
-template <typename QT, int DP, int QP, bool F32>
+template <typename QT, int DP, int QP, bool F32, int RG>
 __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) {
-  using G = AtGeom<QT, DP, F32>;
+  using G = AtGeom<QT, DP, F32, RG>;
   using Core = std::conditional_t<F32, AtCore32<QT, DP, QP>, AtCore16<QT, DP, QP>>;
-  using Copy = std::conditional_t<F32, AtCopy32<DP>, AtCopy16<DP>>;
-  constexpr int WARPS = G::WARPS, KB = Core::KB, NTHREADS = 32 * WARPS;
+  constexpr int WARPS = G::WARPS, KG = G::KG, KB = Core::KB, NTHREADS = 32 * WARPS, SLOTS = G::SLOTS;
   extern __shared__ __align__(128) unsigned char am_raw[];
   __shared__ AtWalk s_walk;
+  __shared__ AtPiece s_piece;
   __shared__ float s_m[WARPS][16], s_l[WARPS][16];
   const AmArgs& a = p.a;
-  const int tid = threadIdx.x, warp = tid >> 5;
-  unsigned char* mine = am_raw + G::QBYTES + warp * G::PER_WARP;
-  const uint32_t ring = smem_u32(mine);
-  const Copy copy(a.d, mine);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int rg = warp % RG, kg = warp / RG;  // this warp's rows and ring
+  unsigned char* ring = am_raw + G::QBYTES + kg * G::RING;
+  const uint32_t ring32 = smem_u32(ring);
+  const AtCopy<KB, F32 ? 4 : 2, DP, RG> copy(a.d, ring32, rg);
+  // the warps that share a ring
+  auto meet = [&]() {
+    if constexpr (RG == 1)
+      __syncwarp();
+    else
+      asm volatile("bar.sync %0, %1;" ::"r"(1 + kg), "n"(32 * RG) : "memory");
+  };
   pdl_wait();
   pdl_trigger();
   if (warp == 0) {
-    const AtWalk w = at_start(p);
-    if ((tid & 31) == 0) s_walk = w;
+    AtWalk w = at_start(p);
+    const AtPiece x = w.next(p);
+    if (lane == 0) s_walk = w, s_piece = x;
   }
   __syncthreads();
-  AtWalk walk = s_walk;
-  for (bool again = false;; again = true) {
-    const AtPiece pc = walk.next(p);
-    if (pc.tiles == 0) break;
-    if (again) __syncthreads();  // the piece before this one has left shared memory
-    if constexpr (F32) {
-      copy.pad(a.d, mine);
-    } else if (again && a.d < DP) {
-      Copy(a.d, mine);  // (zeroes the columns past the head)
+  while (s_piece.tiles > 0) {
+    const AtPiece pc = s_piece;
+    if (a.d < DP) {  // columns past the head stay zero
+      constexpr int CP = DP * (F32 ? 4 : 2) / 16;
+      const int chunks = a.d * (F32 ? 4 : 2) / 16, pad = CP - chunks;
+      for (int i = lane + 32 * rg; i < SLOTS * 2 * KB * pad; i += 32 * RG)
+        *reinterpret_cast<uint4*>(ring + i / pad * Core::PITCH + (chunks + i % pad) * 16) = make_uint4(0, 0, 0, 0);
     }
-    const int row0 = pc.m0, nrows = pc.nrows;
+    const int row0 = pc.m0 + 16 * rg, nrows = min(16, pc.nrows - 16 * rg);  // this warp's (none: below 1)
     auto src_of = [&](int r) {
       const int m = row0 + r, token = m / a.group;
       return a.q_stride * (pc.begin + token) + static_cast<long long>(pc.g * a.group + m - token * a.group) * a.d;
@@ -437,25 +467,35 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
     auto entry = [&](int blk) {
       return !pc.prefix && blk < nblk && (KB >> a.pool.shift) <= 1 ? trow[(pc.k0 + blk * KB) >> a.pool.shift] : 0;
     };
-    auto request = [&](int stage, int blk, int32_t e) {
-      const int k = pc.k0 + blk * KB, n = min(KB, pc.k1 - k);
-      return pc.prefix ? copy.prefix(a, stage, pc.g, k, n) : copy.pages(a, stage, trow, e, pc.g, k, n);
+    // block number kg + KG i of the piece to slot i
+    int32_t e_next = entry(kg);
+    auto request = [&](int i) -> uint32_t {
+      const int blk = kg + KG * i, slot = i % SLOTS;
+      uint32_t ok = 0;
+      if (blk < nblk) {
+        const int k = pc.k0 + blk * KB, n = min(KB, pc.k1 - k);
+        ok = pc.prefix ? copy.run(slot, a.pk, a.pv, a.pstride * pc.g + k, n) : copy.pages(a, slot, trow, e_next, pc.g, k, n);
+        e_next = entry(blk + KG);
+      }
+      am_commit();
+      return ok;
     };
-    int32_t e0 = entry(warp), e1 = entry(warp + WARPS);
-    __syncwarp();
-    uint32_t ok = 0;
-    if (warp < nblk) ok = request(0, warp, e0);
-    am_commit();
+    uint32_t ok[SLOTS];  // of the blocks on their way: keys that count (the oldest first)
+    ok[SLOTS - 1] = 0;
+#pragma unroll
+    for (int i = 0; i < SLOTS - 1; ++i) ok[i] = request(i);
     Core core;
     if constexpr (F32) {
       core.clear();
-      core.frag = reinterpret_cast<const uint4*>(am_raw);
-      for (int i = tid; i < 16 * (DP / 8); i += NTHREADS) {
-        // 8 elements of a row, in the order of the A fragments: [part][k step][lane][register]
-        const int r = i / (DP / 8), e = i % (DP / 8) * 8;
+      core.frag = reinterpret_cast<const uint4*>(am_raw) + rg * 2 * (DP / 8) * 32;
+      for (int i = tid; i < 16 * RG * (DP / 8); i += NTHREADS) {
+        // 8 elements of a row, in the order of the A fragments: [row group][part][k step][lane][register]
+        const int rr = i / (DP / 8), e = i % (DP / 8) * 8, r = rr & 15;
         float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (r < nrows && e < a.d) {
-          const QT* src = static_cast<const QT*>(a.q) + src_of(r) + e;
+        if (rr < pc.nrows && e < a.d) {
+          const int m = pc.m0 + rr, token = m / a.group;
+          const QT* src = static_cast<const QT*>(a.q) + a.q_stride * (pc.begin + token) +
+                          static_cast<long long>(pc.g * a.group + m - token * a.group) * a.d + e;
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             if constexpr (sizeof(QT) == 4)
@@ -469,7 +509,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
           const int ln = (r % 8) * 4 + j % 4, reg = r / 8 + 2 * (j / 4);
           uint32_t hi, lo;
           am_split_tf32(x[j], &hi, &lo);
-          uint32_t* f = reinterpret_cast<uint32_t*>(am_raw) + ((e / 8) * 32 + ln) * 4 + reg;
+          uint32_t* f = reinterpret_cast<uint32_t*>(am_raw) + (rr >> 4) * 2 * (DP / 8) * 32 * 4 + ((e / 8) * 32 + ln) * 4 + reg;
           f[0] = hi;
           f[(DP / 8) * 32 * 4] = lo;
         }
@@ -480,83 +520,102 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
     }
     int token[4];  // of the rows whose scores this lane masks
 #pragma unroll
-    for (int i = 0; i < 4; ++i) token[i] = min(row0 + Core::row_of(i), row0 + nrows - 1) / a.group;
-    int stage = 0;
-    for (int blk = warp; blk < nblk; blk += WARPS, stage ^= 1) {
-      __syncwarp();  // every lane is done with the block before this one
-      const uint32_t next = blk + WARPS < nblk ? request(stage ^ 1, blk + WARPS, e1) : 0;
-      am_commit();
-      e1 = entry(blk + 2 * WARPS);
-      const int k = pc.k0 + blk * KB;
-      const bool drafts = !pc.prefix && k + KB > pc.n;
-      uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-      if (drafts)
+    for (int i = 0; i < 4; ++i) token[i] = min(row0 + Core::row_of(i), pc.m0 + pc.nrows - 1) / a.group;
+    const int mine = (nblk - kg + KG - 1) / KG;  // blocks of this ring
+#pragma unroll 1
+    for (int i = 0; i < mine; ++i) {
+      am_wait<SLOTS - 2>();
+      meet();  // block i has landed for every warp of the ring, and all are done with the block before it
+      ok[SLOTS - 1] = request(i + SLOTS - 1);
+      if (nrows > 0) {
+        const int k = pc.k0 + (kg + KG * i) * KB;
+        const bool drafts = !pc.prefix && k + KB > pc.n;
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        if (drafts)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) seen[i] = at_seen(p, pc.begin, token[i], k - pc.n);
-      am_wait<1>();
-      __syncwarp();  // this block has landed for every lane
-      const uint32_t kt = ring + stage * 2 * Core::TILE;
-      core.block(kt, mine + stage * 2 * Core::TILE + Core::TILE, ok, a.scale_log2, drafts, seen);
-      ok = next;
+          for (int j = 0; j < 4; ++j) seen[j] = at_seen(p, pc.begin, token[j], k - pc.n);
+        const int at = i % SLOTS * 2 * Core::TILE;
+        core.block(ring32 + at, ring + at + Core::TILE, ok[0], a.scale_log2, drafts, seen);
+      }
+#pragma unroll
+      for (int j = 0; j < SLOTS - 1; ++j) ok[j] = ok[j + 1];
     }
     am_wait<0>();
     core.sums([&](int r, float m, float l) { s_m[warp][r] = m, s_l[warp][r] = l; });
     __syncthreads();  // every warp is past its ring
-    float* out = reinterpret_cast<float*>(mine);
+    float* out = reinterpret_cast<float*>(am_raw + G::QBYTES) + warp * 16 * DP;
     core.outputs(
         nrows,
         [&](int r, float mine_m) {
           float m = -INFINITY;
 #pragma unroll
-          for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
+          for (int w = 0; w < KG; ++w) m = fmaxf(m, s_m[w * RG + rg][r]);
           return m == -INFINITY ? 1.f : am_exp2(mine_m - m);
         },
         [&](int r, int e, float x) { out[r * DP + e] = x; });
+    // the next piece, while the results are joined
+    if (warp == 0) {
+      AtWalk w = s_walk;
+      const AtPiece x = w.next(p);
+      __syncwarp();
+      if (lane == 0) s_walk = w, s_piece = x;
+    }
     __syncthreads();
-    for (int i = tid; i < nrows * (DP / 4); i += NTHREADS) {
-      const int r = i / (DP / 4), e = i % (DP / 4) * 4;
+    for (int i = tid; i < pc.nrows * (DP / 4); i += NTHREADS) {
+      const int row = i / (DP / 4), e = i % (DP / 4) * 4, g16 = row >> 4, r = row & 15;
       if (e >= a.d) continue;
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int w = 0; w < WARPS; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(am_raw + G::QBYTES + w * G::PER_WARP + (r * DP + e) * 4);
-        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
-      }
       float m = -INFINITY, sum = 0.f;
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) m = fmaxf(m, s_m[w][r]);
+      for (int w = 0; w < KG; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(am_raw + G::QBYTES + (((w * RG + g16) * 16 + r) * DP + e) * 4);
+        x.x += y.x, x.y += y.y, x.z += y.z, x.w += y.w;
+        m = fmaxf(m, s_m[w * RG + g16][r]);
+      }
 #pragma unroll
-      for (int w = 0; w < WARPS; ++w) sum += m == -INFINITY ? s_l[w][r] : s_l[w][r] * am_exp2(s_m[w][r] - m);
+      for (int w = 0; w < KG; ++w) {
+        const float l = s_l[w * RG + g16][r];
+        sum += m == -INFINITY ? l : l * am_exp2(s_m[w * RG + g16][r] - m);
+      }
       if (pc.whole) {
-        const int token_ = (row0 + r) / a.group, head = pc.g * a.group + (row0 + r) % a.group;
-        at_put<QT>(p, pc.begin + token_, head, e, x, m, sum);
+        const int mrow = pc.m0 + row, tok = mrow / a.group;
+        at_put<QT>(p, pc.begin + tok, pc.g * a.group + mrow - tok * a.group, e, x, m, sum);
       } else {
-        const long long at = (pc.id << p.cut.mshift) + r;
+        const long long at = (pc.id << p.cut.mshift) + row;
         *reinterpret_cast<float4*>(a.part_o + at * a.d + e) = x;
         if (e == 0) a.part_ml[at] = make_float2(m, sum);
       }
     }
+    __syncthreads();  // the results have left shared memory
   }
-  if (warp == 0) at_records(p, walk);
+  if (warp == 0) at_records(p, s_walk);
 }
 
-template <typename QT, int DP, int QP, bool F32>
+template <typename QT, int DP, int QP, bool F32, int RG>
 cudaError_t at_launch_one(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  constexpr size_t smem = AtGeom<QT, DP, F32>::SMEM;
+  constexpr size_t smem = AtGeom<QT, DP, F32, RG>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[di.device]) {
-    const cudaError_t e = allow_smem_shared(attn_tree_rows_kernel<QT, DP, QP, F32>, smem);
+    const cudaError_t e = allow_smem_shared(attn_tree_rows_kernel<QT, DP, QP, F32, RG>, smem);
     if (e != cudaSuccess) return e;
     lifted[di.device] = true;
   }
-  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32>, dim3(di.sms), dim3(256), smem, st, true, a);
+  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32, RG>, dim3(di.sms), dim3(256), smem, st, true, a);
+}
+
+template <typename QT, int DP, int QP, bool F32>
+cudaError_t at_launch_rows(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  if (a.cut.mshift == 4) return at_launch_one<QT, DP, QP, F32, 1>(a, di, st);
+  if constexpr (!F32)
+    if (a.cut.mshift == 5) return at_launch_one<QT, DP, QP, F32, 2>(a, di, st);
+  return at_launch_one<QT, DP, QP, F32, 4>(a, di, st);
 }
 
 template <typename QT, int QP, bool F32>
 cudaError_t at_launch(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  if (a.a.d <= 16) return at_launch_one<QT, 16, QP, F32>(a, di, st);
-  if (a.a.d <= 64) return at_launch_one<QT, 64, QP, F32>(a, di, st);
-  return at_launch_one<QT, 128, QP, F32>(a, di, st);
+  if (a.a.d <= 16) return at_launch_rows<QT, 16, QP, F32>(a, di, st);
+  if (a.a.d <= 64) return at_launch_rows<QT, 64, QP, F32>(a, di, st);
+  return at_launch_rows<QT, 128, QP, F32>(a, di, st);
 }
 
 }  // namespace wsg
