@@ -798,7 +798,8 @@ dec_status attn_tree_paged(const attn_tree_args* a, void* stream);
  * lowest of equal ones; NaN counts as masked; -1 if no logit is above -inf. out is
  * nullable where next is given, and may be logits itself (same dtype, stride).
  * vocab up to 2^20, rows up to 2^19 - 8; up to 2^19 tokens a text, as many drafted
- * ones and 1023 biases a list (longer ones are cut). Outputs must not overlap anything else. */
+ * ones and 1023 biases a list (longer ones are cut). Outputs must not overlap
+ * anything else. */
 typedef struct {
   int32_t rows, vocab, requests;
   int32_t xdtype, ydtype; /* logits; out: DEC_F32 or DEC_BF16 */
@@ -839,8 +840,10 @@ dec_status logits_adjust(const logits_adjust_args* a, void* stream);
  * (layer l's pools start l * layer_stride elements after k_pages and v_pages);
  * nothing else in the pools is written. tokens
  * (nullable): draft_tokens of the accepted rows are written to tokens[s][seq_len +
- * tokens_base + d]. A request with seq_len < 0 is left alone (count 0, new_len -1,
- * path and out_tokens -1), one without rows too (new_len = seq_len). A page of an
+ * tokens_base + d]. A request with seq_len < 0 is left alone (count 0, path and
+ * out_tokens -1, new_len = held[s], or -1 without held: with step_slots' ctx_len as
+ * seq_len and its held, a request that was not served keeps its tokens and waits), one
+ * without rows too (new_len = seq_len). A page of an
  * accepted row outside the pool or the table sets DEC_DEVERR_BAD_PAGE and that row is
  * not moved; a place outside tokens_stride is not written and sets
  * DEC_DEVERR_BAD_POSITION. layers may be 0 (nothing moves; no pools). path_stride up
@@ -852,6 +855,7 @@ typedef struct {
   const int32_t* parents;   /* [rows], or NULL: chains */
   const int32_t *draft_tokens, *next; /* [rows] */
   const int32_t* seq_len;   /* [batch] */
+  const int32_t* held;      /* [batch] or NULL */
   void *k_pages, *v_pages;
   int64_t layer_stride;
   int32_t num_pages, page_size, table_stride;

@@ -219,7 +219,7 @@ ADJUST = dict(rows=4, vocab=100, requests=3, xdtype=0, ydtype=0, logits_stride=1
 ACCEPT = dict(batch=3, rows=9, path_stride=4, layers=2, n_kv=2, head_dim=16, kvdtype=1, layer_stride=8 * 2 * 16 * 16,
               num_pages=8, page_size=16, table_stride=2, tokens_stride=40, tokens_base=0,
               **places("row_start", "parents", "draft_tokens", "next", "seq_len", "k_pages", "v_pages", "page_table",
-                       "tokens", "count", "new_len", "path", "out_tokens"))
+                       "tokens", "count", "new_len", "path", "out_tokens", "held"))
 CALLS = {"step_slots": ("step_slots_args", SLOTS), "kv_append_slots": ("kv_slots_args", APPEND),
          "attn_tree_paged": ("attn_tree_args", ATTN), "logits_adjust": ("logits_adjust_args", ADJUST),
          "tree_accept_paged": ("tree_accept_args", ACCEPT)}
@@ -282,7 +282,7 @@ OFF = {  # bytes of an element behind each pointer, with the codes that decide i
         "next", "seq", "tokens", "tokens_len", "prompt_len", "draft_tokens", "row_start", "mask", "repetition", "frequency",
         "presence", "bias_tokens", "bias", "bias_len", "allowed", "allowed_row")}},
     "tree_accept_paged": {n: 4 for n in places("row_start", "parents", "draft_tokens", "next", "seq_len", "page_table", "tokens",
-                                               "count", "new_len", "path", "out_tokens")},
+                                               "count", "new_len", "path", "out_tokens", "held")},
 }
 
 
@@ -307,7 +307,7 @@ OVER = {  # outputs, and the arguments that they must not lie over
                                         "repetition", "frequency", "presence", "bias_tokens", "bias", "bias_len", "allowed",
                                         "allowed_row")),
     "tree_accept_paged": (("count", "new_len", "path", "out_tokens", "tokens"),
-                          ("row_start", "parents", "draft_tokens", "next", "seq_len", "page_table")),
+                          ("row_start", "parents", "draft_tokens", "next", "seq_len", "held", "page_table")),
 }
 IN_PLACE = {("step_slots", "new_table", "page_table"), ("attn_tree_paged", "out", "q"), ("logits_adjust", "out", "logits")}
 
@@ -377,3 +377,20 @@ def test_argument_blocks_refuse_other_tensors(W):
             getattr(W, call)(getattr(W, args)(**{**good, name: OnDevice()}))
         with pytest.raises(W.WsgError, match="not on a CUDA device"):
             getattr(W, args)(**{**good, name: t})
+
+
+def test_argument_blocks_refuse_masks_that_are_not_contiguous(W):
+    import torch
+
+    t = torch.zeros((4, 6), dtype=torch.int32)[:, ::2]
+
+    class OnDevice:
+        is_cuda, dtype, shape = True, t.dtype, t.shape
+
+        def __getattr__(self, n):
+            return getattr(t, n)
+
+    for call in ("step_slots", "attn_tree_paged", "logits_adjust"):
+        args, good = CALLS[call]
+        with pytest.raises(W.WsgError, match=f"{args}.mask"):
+            getattr(W, call)(getattr(W, args)(**{**good, "mask": OnDevice()}))

@@ -409,6 +409,8 @@ TREE_CASES = [
     ([6, 250, 3], 16, 2, 128, 40, [10, 300, 2000], 32, "tree"),
     ([4], 2, 2, 128, 3000, [2500], 64, "tree"),                 # long for few rows
     ([70], 32, 2, 64, 0, [900], 16, "random"),
+    ([300, 20], 4, 2, 64, 0, [5, 640], 8, "tree"),              # masks of ten words
+    ([40, 9], 4, 1, 40, 20, [100, 700], 16, "tree"),            # a request's rows in row tiles of 64, one of them nearly empty
 ]
 
 
@@ -660,8 +662,8 @@ def test_attn_tree_paged_of_single_rows_is_the_branches_attention():
 # ---- logits ------------------------------------------------------------------------------------------------------------------
 
 def adjust_case(W, rows, vocab, x, y, seed=0, history=50, drafts=True, bias=4, masks=2, penalties=True, extra=0, offset=0,
-                mask=True, in_place=False, prompt=True, base=0):
-    """rows: of each request. Returns arguments and what the definition takes."""
+                mask=True, in_place=False, prompt=True, base=0, far=False):
+    """rows: of each request; far: text and drafts over the whole vocabulary. Returns arguments and what the definition takes."""
     import torch
 
     rng = np.random.default_rng(seed)
@@ -676,10 +678,10 @@ def adjust_case(W, rows, vocab, x, y, seed=0, history=50, drafts=True, bias=4, m
     if in_place:
         ys = xs
     p = dict(logits=f64(xs[1]), rows=rows, seq=np.repeat(np.arange(n), rows), start=np.concatenate([[0], np.cumsum(rows)]))
-    p["tokens"] = rng.integers(-1, max(2, min(vocab + 2, 40)), (n, history + 3))  # out of range ones too
-    p["len"] = rng.integers(0, history + 1, n)
+    p["tokens"] = rng.integers(-1, vocab + 2 if far else max(2, min(vocab + 2, 40)), (n, history + 3))  # out of range ones too
+    p["len"] = np.full(n, history) if far else rng.integers(0, history + 1, n)
     p["prompt"] = (p["len"] * rng.random(n)).astype(int) if prompt else np.zeros(n, int)
-    p["draft"] = rng.integers(0, min(vocab, 30), total)
+    p["draft"] = rng.integers(0, vocab if far else min(vocab, 30), total)
     p["trees"] = [random_tree(rng, r) if mask else None for r in rows]
     p["rep"], p["freq"], p["pres"] = (rng.random(n).astype(np.float32) + np.float32(lo) for lo in (0.7, -0.2, -0.3))
     p["bias_tokens"] = rng.integers(-1, min(vocab, 50) + 1, (n, max(1, bias)))
@@ -750,6 +752,9 @@ ADJUST_CASES = [
     ([3], 151936, {"mask": False, "base": 7}),               # chains
     ([2], 300000, {}),                                       # two passes over the vocabulary
     ([1] * 90, 20000, {"in_place": True, "history": 5}),
+    ([400, 2, 290], 700, {"mask": False, "far": True}),      # more drafted tokens before a row than are listed
+    ([270, 9], 1500, {"far": True}),                         # masks of nine words
+    ([1], 40000, {"history": 24000, "far": True}),           # more tokens with a rule than are listed
 ]
 
 
@@ -984,6 +989,164 @@ def test_tree_accept_paged_without_pools_and_bad_places():
     for got, old in zip(t["pools"], t["before"]):
         np.testing.assert_array_equal(f64(got), old)
     assert t["path"][0].tolist() == [0, 2, 3, 4, -1, -1, -1, -1] and text[0, 6:].tolist() == [0, 2]
+
+
+# ---- streams and graphs --------------------------------------------------------------------------------------------------------
+
+def test_attentions_of_two_streams_at_once():
+    """Calls on three streams, each with its own workspace, give the bits that they give alone."""
+    import torch
+
+    W = lib()
+    cases = [([16] * 6, 16, 8, 128, 0, [900, 1, 127, 128, 2000, 40], 16, "tree", "bf16", "bf16"),
+             ([5, 9, 30], 10, 2, 80, 129, [400, 31, 77], 32, "random", "f32", "bf16"),
+             ([64, 33], 16, 8, 128, 300, [300, 1000], 64, "tree", "bf16", "bf16"),
+             ([13, 1], 16, 8, 128, 0, [301, 2000], 8, "tree", "f32", "f32")]
+    made, want = [], []
+    for i, (rows, n_q, n_kv, d, plen, lens, page, mask, q, kv) in enumerate(cases):
+        a, t = tree_case(W, rows, n_q, n_kv, d, plen, lens, page, q, kv, mask=mask, seed=i)
+        W.attn_tree_paged(a)
+        torch.cuda.synchronize()
+        check_tree(t, rows, n_q, n_kv, d, plen, lens, page, q)
+        want.append([t["out"].clone(), t["lse"].clone()])
+        t["out"].fill_(3), t["lse"].fill_(3)
+        made.append((a, t))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in made]
+    for _ in range(30):
+        for (a, _), st in zip(made, streams):
+            W.attn_tree_paged(a, st)
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    for (_, t), w in zip(made, want):
+        assert torch.equal(t["out"], w[0]) and torch.equal(t["lse"], w[1])
+
+
+class Step:
+    """A step of trees over one layer, its state kept on the device from step to step."""
+
+    def __init__(self, W, B, R, n_q, n_kv, d, page, width, vocab, q, kv, plen, seed=0):
+        import torch
+
+        total, num = B * R, 2 * B + 2  # (enough for all at the start, not later)
+        i32 = dict(dtype=torch.int32, device="cuda")
+        z = lambda *shape: torch.zeros(shape, **i32)
+        self.fresh, self.parents, self.draft = z(B), z(total), z(total)
+        self.qkv = torch.zeros((total, (n_q + 2 * n_kv) * d), device="cuda")
+        self.logits = torch.zeros((total, vocab), device="cuda")
+        self.held, self.owned, self.state = z(B), z(B), ints([0, num])
+        self.table, self.ring = torch.full((B, width), -1, **i32), ints(np.random.default_rng(seed).permutation(num))
+        self.text = z(B, width * page + R)
+        new_owned, new_state, row_start, ctx, seq, pos, mask = z(B), z(2), z(B + 1), z(B), z(total), z(total), z(total, 1)
+        slots = torch.zeros(total, dtype=torch.int64, device="cuda")
+        self.back = [(self.owned, new_owned), (self.state, new_state)]
+        self.pools = torch.zeros((2, 1, num, n_kv, page, d), device="cuda").to(tdt(kv))
+        pk, pv = (rand((n_kv, max(plen, 1), d), kv, seed + k) for k in (1, 2))
+        q_out = torch.zeros((total, n_q * d), dtype=tdt(q), device="cuda")
+        self.out, self.adjusted, self.next = torch.zeros_like(q_out), torch.zeros_like(self.logits), z(total)
+        self.count, self.path, self.acc = z(B), z(B, R), z(B, R)
+        new_len = z(B)
+        self.back.append((self.held, new_len))
+        freq, factor = W.rope_frequencies(d, 1e4)
+        wide = (n_q + 2 * n_kv) * d
+        self.calls = [
+            (W.step_slots, W.step_slots_args(
+                requests=B, rows=total, num_pages=num, page_size=page, table_stride=width, base_pos=plen, mask_words=1,
+                held=self.held, fresh=self.fresh, owned=self.owned, parents=self.parents, page_table=self.table,
+                free_ring=self.ring, free_state=self.state, new_table=self.table, new_owned=new_owned, new_free_state=new_state,
+                row_start=row_start, ctx_len=ctx, seq=seq, positions=pos, slots=slots, mask=mask)),
+            (W.kv_append_slots, W.kv_slots_args(
+                rows=total, n_q=n_q, n_kv=n_kv, head_dim=d, xdtype=W.DEC_F32, ydtype=code(W, q), kvdtype=code(W, kv), q=self.qkv,
+                k=self.qkv[:, n_q * d:], v=self.qkv[:, (n_q + n_kv) * d:], q_out=q_out, q_stride=wide, k_stride=wide,
+                v_stride=wide, q_out_stride=n_q * d, g_q=None, g_k=None, positions=pos, inv_freq=torch.tensor(freq, dtype=torch.float64, device="cuda"),
+                eps=1e-6, rope_factor=factor, rot_dim=d, interleaved=0, k_pages=self.pools[0], v_pages=self.pools[1],
+                slots=slots, num_pages=num, page_size=page))]
+        a = W.attn_tree_args(
+            batch=B, rows=total, n_q=n_q, n_kv=n_kv, head_dim=d, qdtype=code(W, q), kvdtype=code(W, kv), q=q_out, out=self.out,
+            q_stride=n_q * d, out_stride=n_q * d, row_start=row_start, mask=mask, mask_words=1, prefix_k=pk, prefix_v=pv,
+            prefix_len=plen, prefix_stride=max(plen, 1), k_pages=self.pools[0], v_pages=self.pools[1], page_table=self.table,
+            seq_len=ctx, num_pages=num, page_size=page, table_stride=width, scale=d ** -0.5)
+        a.with_workspace(torch.empty(W.attn_tree_paged_workspace(a), dtype=torch.uint8, device="cuda"))
+        self.calls += [
+            (W.attn_tree_paged, a),
+            (W.logits_adjust, W.logits_adjust_args(
+                rows=total, vocab=vocab, requests=B, xdtype=0, ydtype=0, logits=self.logits, logits_stride=vocab,
+                out=self.adjusted, out_stride=vocab, next=self.next, seq=seq, tokens=self.text, tokens_stride=self.text.shape[1],
+                tokens_len=self.held, draft_tokens=self.draft, row_start=row_start, mask=mask, mask_words=1,
+                repetition=torch.full((B,), 1.25, device="cuda"), frequency=torch.full((B,), 0.5, device="cuda"))),
+            (W.tree_accept_paged, W.tree_accept_args(
+                batch=B, rows=total, path_stride=R, layers=1, n_kv=n_kv, head_dim=d, kvdtype=code(W, kv), row_start=row_start,
+                parents=self.parents, draft_tokens=self.draft, next=self.next, seq_len=ctx, held=self.held, k_pages=self.pools[0],
+                v_pages=self.pools[1], layer_stride=self.pools[0].numel(), num_pages=num, page_size=page, table_stride=width,
+                page_table=self.table, tokens=self.text, tokens_stride=self.text.shape[1], count=self.count, new_len=new_len,
+                path=self.path, out_tokens=self.acc))]
+        self.ctx = ctx
+        self.seen = [ctx, self.out, self.adjusted, self.next, self.count, self.path, self.acc, self.held, self.owned, self.state,
+                     self.table, self.ring, self.text, self.pools, q_out, pos, slots, mask]
+
+    def run(self, stream=None):
+        for call, a in self.calls:
+            call(a, stream)
+        for to, new in self.back:
+            to.copy_(new)
+
+
+@pytest.mark.parametrize("q,kv,d,plen", [("bf16", "bf16", 128, 0), ("bf16", "bf16", 64, 70), ("f32", "f32", 128, 0),
+                                         ("f32", "bf16", 80, 33)], ids=str)
+def test_a_captured_step_of_trees_follows_its_inputs(q, kv, d, plen):
+    """A graph of a step's calls is captured once and replayed on its own state, requests growing, ending and starting again;
+    an equal state is driven by eager calls on another stream. Both hold the same bits after every step."""
+    import torch
+
+    W = lib()
+    B, R, width, page, vocab = 5, 9, 12, 8, 900
+    eager, graph = (Step(W, B, R, 8, 4, d, page, width, vocab, q, kv, plen) for _ in range(2))
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        graph.run(side)
+    W.gemv_device_errors()
+    rng = np.random.default_rng(3)
+    moved = waited = 0
+    for step in range(20):
+        held = eager.held.cpu().numpy()
+        held[held > width * page - 2 * R] = -1
+        if step % 4 == 3:
+            held[step % B] = -1
+        start = eager.held.cpu().numpy() < 0
+        held[start] = 0  # an ended request's place is taken again
+        before = held.copy()
+        fresh = rng.integers(0, R + 1, B)
+        fresh[step % B] = R
+        total = np.clip(fresh, 0, None)
+        total[held < 0] = 0
+        parents, drafts = np.zeros(B * R, int), rng.integers(0, 3, B * R)
+        at = 0
+        for r in total:
+            parents[at: at + r] = random_tree(rng, int(r))
+            at += r
+        logits = rng.standard_normal((B * R, vocab)).astype(np.float32)
+        logits[:, :3] += 4  # (drafted tokens come often)
+        qkv = rng.standard_normal((B * R, graph.qkv.shape[1])).astype(np.float32)
+        for s in (eager, graph):
+            for x, y in ((s.fresh, fresh), (s.parents, parents), (s.draft, drafts), (s.held, held)):
+                x.copy_(ints(y))
+            s.logits.copy_(torch.tensor(logits)), s.qkv.copy_(torch.tensor(qkv))
+        torch.cuda.synchronize()
+        g.replay()
+        with torch.cuda.stream(side if step % 2 else torch.cuda.default_stream()):
+            eager.run(side if step % 2 else None)
+        torch.cuda.synchronize()
+        assert W.gemv_device_errors() == 0
+        for i, (x, y) in enumerate(zip(eager.seen, graph.seen)):
+            assert torch.equal(x, y), (step, i)
+        moved += int((eager.count - 1).clamp(min=0).sum())
+        wait = (before >= 0) & (eager.ctx.cpu().numpy() < 0)  # not served: they keep what they have
+        waited += int(wait.sum())
+        np.testing.assert_array_equal(eager.held.cpu().numpy()[wait], before[wait])
+        assert (eager.held.cpu().numpy()[before < 0] == -1).all()
+    assert moved > 0 and waited > 0  # rows were accepted behind the first ones; some requests had to wait
 
 
 # ---- together ------------------------------------------------------------------------------------------------------------------

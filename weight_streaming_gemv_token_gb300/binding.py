@@ -278,10 +278,10 @@ class logits_adjust_args(_Args):
 
 class tree_accept_args(_Args):
     _typed = {"k_pages": "kvdtype", "v_pages": "kvdtype"}
-    _optional = ("parents", "k_pages", "v_pages", "layer_stride", "num_pages", "page_size", "table_stride", "page_table",
+    _optional = ("parents", "held", "k_pages", "v_pages", "layer_stride", "num_pages", "page_size", "table_stride", "page_table",
                  "n_kv", "head_dim", "kvdtype", "tokens", "tokens_stride", "tokens_base")
     _fields_ = ([(n, c_int32) for n in ("batch", "rows", "path_stride", "layers", "n_kv", "head_dim", "kvdtype")]
-                + [(n, c_void_p) for n in ("row_start", "parents", "draft_tokens", "next", "seq_len", "k_pages", "v_pages")]
+                + [(n, c_void_p) for n in ("row_start", "parents", "draft_tokens", "next", "seq_len", "held", "k_pages", "v_pages")]
                 + [("layer_stride", c_int64)]
                 + [(n, c_int32) for n in ("num_pages", "page_size", "table_stride")]
                 + [("page_table", c_void_p), ("tokens", c_void_p), ("tokens_stride", c_int64), ("tokens_base", c_int32)]

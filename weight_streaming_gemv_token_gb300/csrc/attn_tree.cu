@@ -4,9 +4,9 @@
 //
 // The line of key tiles (attn_tree_plan.h) goes by the lengths on the device, so
 // every SM has an equal share of it whatever the requests' lengths and however wide
-// their tables are. A segment that lies in one CTA's share is finished there; the
-// pieces of the others, and of rows that have a prefix too, join exactly in
-// attn_tree_join_kernel:
+// their tables are. A segment that lies in one CTA's share is finished there. The pieces
+// of the others join exactly in attn_tree_seam_kernel, those of rows that have a prefix
+// too (two segments each, whole or cut) in attn_tree_join_kernel:
 //   out = sum_i o_i 2^(m_i - m) / sum_i l_i 2^(m_i - m), m = max_i m_i.
 #include "attn_tree.cuh"
 

@@ -44,7 +44,7 @@ struct AtWalk {
   AtShares shares;
   AtSeam seam;                 // the segment that starts in this share and is cut behind it
   int seam_seg;
-  int seg0, seg1;              // segments that start in this share, of all requests' for the last CTA
+  int seg0, seg1;              // segments whose first tile lies in this share: seg0 .. seg1 - 1
 
   __device__ __forceinline__ static int clamp_row(const AtArgs& a, int r) { return min(max(0, r), a.a.rows); }
 
@@ -127,9 +127,9 @@ struct AtWalk {
 };
 
 // The requests' sums as one warp forms them, a run of requests a lane: units << 26 |
-// segments of all requests (at most n_kv times the rows and 2^24 / 16 of those), of those
-// before this lane's, and this lane's first request. Row starts that fall are lifted to
-// the highest before.
+// segments of all requests (at most n_kv times the rows and 2^24 / 16 of those; 2^37 units
+// are hours of work), of those before this lane's, and this lane's first request. Row
+// starts that fall are lifted to the highest before.
 struct AtSums {
   int lo, hi;          // this lane's requests
   int from, rows, len; // the first one's first row, rows, tokens
@@ -213,7 +213,7 @@ __device__ __forceinline__ void at_each(const AtArgs& a, const AtSums& s, F f) {
 }
 
 // One warp: this CTA's place on the line. What it costs is a chain of loads, shuffles and
-// divisions before the first keys can be asked for: 2,700 cycles for up to 32 requests.
+// divisions before the first keys can be asked for, about 2 us of a call.
 __device__ __forceinline__ AtWalk at_start(const AtArgs& a) {
   const int ctas = gridDim.x, cta = blockIdx.x;
   const AtSums s = at_sums(a);

@@ -25,7 +25,7 @@ constexpr int kTaThreads = 256, kTaPath = 256, kTaStage = 1024, kTaBatch = 8;
 
 struct TaArgs {
   int batch, rows, path_stride, layers, n_kv, row16;  // row16: 16-byte pieces of a key
-  const int32_t *row_start, *parents, *draft, *next, *len;
+  const int32_t *row_start, *parents, *draft, *next, *len, *held;
   uint4 *k, *v;
   long long layer16;
   PagePool pool;
@@ -50,7 +50,7 @@ __global__ void __launch_bounds__(kTaThreads) tree_accept_kernel(const TaArgs a)
   const int begin = min(max(0, a.row_start[b]), a.rows), n = min(a.row_start[b + 1], a.rows) - begin;
   if (len < 0 || n <= 0) {
     if (first) {
-      if (tid == 0) a.count[b] = 0, a.new_len[b] = len < 0 ? -1 : len;
+      if (tid == 0) a.count[b] = 0, a.new_len[b] = len >= 0 ? len : a.held ? a.held[b] : -1;
       for (int d = tid; d < a.path_stride; d += kTaThreads)
         a.path[static_cast<long long>(b) * a.path_stride + d] = a.out[static_cast<long long>(b) * a.path_stride + d] = -1;
     }
@@ -183,7 +183,7 @@ extern "C" dec_status tree_accept_paged(const tree_accept_args* a, void* stream)
   const int elem = a->layers > 0 && a->kvdtype == DEC_BF16 ? 2 : 4;
   if (a->layers > 0 && (!aligned16(a->k_pages) || !aligned16(a->v_pages) || a->layer_stride * elem % 16))
     return fail(nullptr, DEC_EINVAL, "tree_accept_paged: the pools must be 16-byte aligned in every layer");
-  if (!aligned_to(4, a->row_start, a->parents, a->draft_tokens, a->next, a->seq_len, a->page_table, a->tokens, a->count,
+  if (!aligned_to(4, a->row_start, a->parents, a->draft_tokens, a->next, a->seq_len, a->held, a->page_table, a->tokens, a->count,
                   a->new_len, a->path, a->out_tokens))
     return fail(nullptr, DEC_EINVAL, "tree_accept_paged: a pointer is not aligned to its elements");
   if (a->tokens && a->tokens_stride < 0)
@@ -197,7 +197,7 @@ extern "C" dec_status tree_accept_paged(const tree_accept_args* a, void* stream)
                     {a->out_tokens, 4 * b * a->path_stride},
                     {a->tokens, 4 * b * static_cast<size_t>(a->tokens ? a->tokens_stride : 0)}},
                    {{a->row_start, 4 * (b + 1)}, {a->parents, 4 * r}, {a->draft_tokens, 4 * r}, {a->next, 4 * r},
-                    {a->seq_len, 4 * b}, {a->page_table, 4 * b * width}}))
+                    {a->seq_len, 4 * b}, {a->held, 4 * b}, {a->page_table, 4 * b * width}}))
     return fail(nullptr, DEC_EINVAL, "tree_accept_paged: an output overlaps another argument");
   DeviceInfo di;
   const dec_status st = device_info(&di, nullptr);
@@ -212,6 +212,7 @@ extern "C" dec_status tree_accept_paged(const tree_accept_args* a, void* stream)
   k.draft = a->draft_tokens;
   k.next = a->next;
   k.len = a->seq_len;
+  k.held = a->held;
   k.tokens = a->tokens;
   k.tokens_stride = a->tokens_stride;
   k.tokens_base = a->tokens_base;
