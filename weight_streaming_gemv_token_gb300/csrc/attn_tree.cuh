@@ -44,6 +44,7 @@ struct AtWalk {
   AtShares shares;
   AtSeam seam;                 // the segment that starts in this share and is cut behind it
   int seam_seg;
+  int segs;                    // of all requests
   int seg0, seg1;              // segments whose first tile lies in this share: seg0 .. seg1 - 1
 
   __device__ __forceinline__ static int clamp_row(const AtArgs& a, int r) { return min(max(0, r), a.a.rows); }
@@ -90,6 +91,9 @@ struct AtWalk {
         }
       }
       kt = at_tiles(a.cut, n, rows, t);
+      // (the CTA with a request's first unit reports tokens beyond the tables)
+      if (g == 0 && t == 0 && unit == 0 && static_cast<long long>(n) + rows > a.cut.capacity && (threadIdx.x & 31) == 0)
+        atomicOr(a.a.err, ERR_BAD_PAGE);
       p.prefix = false;
       p.whole = prefix == 0;
       p.s = s;
@@ -224,6 +228,7 @@ __device__ __forceinline__ AtWalk at_start(const AtArgs& a) {
   w.shares = AtShares{1, 0};
   w.seam = AtSeam{};
   w.seam_seg = -1;
+  w.segs = static_cast<int>(s.all & ((1 << 26) - 1));
   if (cta < W) {
     w.shares = at_shares(W, static_cast<int>(min(static_cast<long long>(ctas), W)));
     w.pos = at_first(w.shares, cta);
@@ -277,28 +282,29 @@ __device__ __forceinline__ AtWalk at_start(const AtArgs& a) {
   return w;
 }
 
-// One warp, behind its share's last piece: the records that the join goes by, and tokens
-// beyond the tables. Of requests s with s % gridDim.x == blockIdx.x.
-__device__ __forceinline__ void at_records(const AtArgs& a, const AtWalk& w) {
+// One warp, behind its share's last piece, without a prefix: the records that the join
+// goes by.
+__device__ __forceinline__ void at_seams(const AtArgs& a, const AtWalk& w) {
+  const int lane = threadIdx.x & 31;
+  if (!a.seam_segs) {
+    if (lane == 0) a.seam[blockIdx.x] = w.seam;
+    return;
+  }
+  // segments that start in this share, and in CTA 0 those that there are not
+  for (int k = w.seg0 + lane; k < w.seg1; k += 32) a.seam[k] = k == w.seam_seg ? w.seam : AtSeam{};
+  if (blockIdx.x == 0)
+    for (int k = w.segs + lane; k < a.seams; k += 32) a.seam[k] = AtSeam{};
+}
+
+// One warp, with a prefix, beside the work: the rows' records, of requests s with
+// s % gridDim.x == blockIdx.x.
+[[maybe_unused]] static __device__ __noinline__ void at_records(const AtArgs& a) {
   const int lane = threadIdx.x & 31;
   const AtSums s = at_sums(a);
-  const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles;
-  const bool by_row = a.prefix_tiles > 0;
-  if (blockIdx.x == 0 && lane == 0) *a.total = w.prefix + (s.all >> 26);
-  if (!by_row) {
-    if (!a.seam_segs) {
-      if (lane == 0) a.seam[blockIdx.x] = w.seam;
-    } else {
-      // segments that start in this share, and in CTA 0 those that there are not
-      for (int k = w.seg0 + lane; k < w.seg1; k += 32) a.seam[k] = k == w.seam_seg ? w.seam : AtSeam{};
-      if (blockIdx.x == 0)
-        for (int k = static_cast<int>(s.all & ((1 << 26) - 1)) + lane; k < a.seams; k += 32) a.seam[k] = AtSeam{};
-    }
-  }
+  const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * (a.prefix_tiles + kAtExtra);
+  if (blockIdx.x == 0 && lane == 0) *a.total = prefix + (s.all >> 26);
   at_each(a, s, [&](int i, int from, int rows, int len, long long size, long long x) {
     if (i % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) return;
-    if (rows > 0 && static_cast<long long>(len) + rows > a.cut.capacity) atomicOr(a.a.err, ERR_BAD_PAGE);
-    if (!by_row) return;
     if (rows == 0) {  // rows of an unused request
       const int e = max(from, AtWalk::clamp_row(a, a.row_start[i + 1]));
       for (int r = from; r < e; ++r) a.rec[r].tiles = 0;
@@ -306,7 +312,7 @@ __device__ __forceinline__ void at_records(const AtArgs& a, const AtWalk& w) {
     }
     const long long head = at_head_units(a.cut, len, rows);
     const int rt = at_row_tiles(a.cut, rows);
-    long long line = w.prefix + (x >> 26) + kAtExtra;
+    long long line = prefix + (x >> 26) + kAtExtra;
     int t = 0, tiles = at_tiles(a.cut, len, rows, 0);
     for (int k = 0; k < rows; ++k) {
       // a token's query heads may lie in two row tiles: the record is the first one's,
@@ -325,7 +331,7 @@ __device__ __forceinline__ void at_records(const AtArgs& a, const AtWalk& w) {
       a.rec[from + k] = r;
     }
   });
-  if (by_row && blockIdx.x == 0) {  // rows of no request
+  if (blockIdx.x == 0) {  // rows of no request
     const int first = AtWalk::clamp_row(a, a.row_start[0]);
     for (int r = lane; r < first; r += 32) a.rec[r].tiles = 0;
     for (int r = s.end + lane; r < a.a.rows; r += 32) a.rec[r].tiles = 0;

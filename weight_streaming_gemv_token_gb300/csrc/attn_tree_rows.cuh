@@ -29,7 +29,7 @@ template <typename QT, int DP, int QP>
 struct AtCore16 : ArCore<QT, DP, QP, 16> {
   using Base = ArCore<QT, DP, QP, 16>;
   static constexpr int KB = 16, TILE = Base::TILE, PITCH = Base::PITCH, KK = Base::KK, PP = Base::PP;
-  static constexpr int RING = 4 * TILE;
+
 
   // row, keys' words: seen[t][j] of row 8 t + 2 (lane % 4) + j
   __device__ __forceinline__ static int row_of(int i) { return 8 * (i >> 1) + 2 * (threadIdx.x & 3) + (i & 1); }
@@ -198,7 +198,7 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
 template <typename QT, int DP, int QP>
 struct AtCore32 {
   static constexpr int KB = 8, PITCH = DP * 4 + 16, TILE = KB * PITCH, NT = DP / 8;
-  static constexpr int RING = 4 * TILE;
+
   float o[NT][4];
   float m[2], l[2];
   const uint4* frag;  // queries in shared memory: [part][k step][lane], split once a piece
@@ -448,6 +448,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
     const AtPiece x = w.next(p);
     if (lane == 0) s_walk = w, s_piece = x;
   }
+  if (warp == 1 && p.prefix_tiles > 0) at_records(p);
   __syncthreads();
   while (s_piece.tiles > 0) {
     const AtPiece pc = s_piece;
@@ -588,7 +589,7 @@ __global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) 
     }
     __syncthreads();  // the results have left shared memory
   }
-  if (warp == 0) at_records(p, s_walk);
+  if (warp == 0 && p.prefix_tiles == 0) at_seams(p, s_walk);
 }
 
 template <typename QT, int DP, int QP, bool F32, int RG>

@@ -325,7 +325,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     }
     if (!ok && lane == 0) fail();
     if (who == 0) {
-      at_records(p, walk);
+      if (p.prefix_tiles == 0) at_seams(p, walk);
       // the last copies into each stage have landed before the CTA may end, after a failure too
       if (lane == 0) {
         for (int s = 0; s < STAGES; ++s)
@@ -459,6 +459,10 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(&q_full);
     };
+    if (warp == 1 + kTtSoft && p.prefix_tiles > 0) {
+      pdl_wait();
+      at_records(p);  // (while the first keys are on their way)
+    }
     int T = 1;
 #pragma unroll 1
     for (int piece = -1; T > 0; ++piece) {
