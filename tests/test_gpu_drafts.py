@@ -433,6 +433,27 @@ def test_attn_tree_paged(c, types):
     assert torch.equal(first[0], t["out"]) and torch.equal(first[1], t["lse"])
 
 
+def wide(batch, n_kv, page):
+    """Entries of tables wide enough that few rows too go to the tensor cores."""
+    return 49 * 153 * 128 // (batch * n_kv * page) + 1
+
+
+@pytest.mark.parametrize("c", [c for c in TREE_CASES if c[3] == 128 and c[4] == 0 and c[6] >= 8] + [
+    ([1], 2, 1, 128, 0, [0], 8, "chain"), ([2, 0, 5], 6, 2, 128, 0, [1, 7, -1], 8, "tree"), ([3, 4], 4, 2, 128, 0, [0, 3], 8, "none"),
+    ([4, 1, 3], 4, 2, 128, 0, [2500, 128, 127], 64, "tree"), ([5], 3, 1, 128, 0, [255], 16, "random")], ids=str)
+def test_attn_tree_paged_few_rows_of_wide_tables(c):
+    import torch
+
+    W = lib()
+    rows, n_q, n_kv, d, plen, lens, page, mask = c
+    a, t = tree_case(W, rows, n_q, n_kv, d, plen, lens, page, "bf16", "bf16", mask=mask, lead=2, tail=3, width=wide(len(rows), n_kv, page))
+    W.gemv_device_errors()
+    W.attn_tree_paged(a)
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    check_tree(t, rows, n_q, n_kv, d, plen, lens, page, "bf16")
+
+
 @pytest.mark.parametrize("types,d", [(t, d) for t in TYPES for d in (64, 128)], ids=str)
 def test_attn_tree_paged_drafts_that_are_not_finite(types, d):
     """Keys and values of drafted rows that are NaN or infinite reach the rows that see them and no others: a chain of 40
@@ -521,14 +542,15 @@ def test_attn_tree_paged_large_scores(q, kv):
 
 @pytest.mark.parametrize("types,d,plen", [(("bf16", "bf16"), 128, 0), (("bf16", "bf16"), 128, 300), (("bf16", "bf16"), 64, 0),
                                           (("f32", "f32"), 128, 0), (("f32", "bf16"), 96, 50)], ids=str)
-def test_attn_tree_paged_in_place(types, d, plen):
+@pytest.mark.parametrize("full", [False, True])
+def test_attn_tree_paged_in_place(types, d, plen, full):
     """The output over the queries, unused requests left as they are: the bits of a call with buffers of its own."""
     import torch
 
     W = lib()
     rows = [(3 * i) % 11 for i in range(20)]
     lens = [(37 * i) % 400 - 1 for i in range(20)]
-    a, t = tree_case(W, rows, 8, 4, d, plen, lens, 16, *types, tail=2)
+    a, t = tree_case(W, rows, 8, 4, d, plen, lens, 16, *types, tail=2, width=wide(20, 4, 16) if full else None)
     W.attn_tree_paged(a)
     torch.cuda.synchronize()
     live = torch.tensor(np.repeat(np.array(lens) >= 0, rows).tolist() + [False] * 2, device="cuda")
@@ -574,12 +596,13 @@ def test_attn_tree_paged_bad_pages(types, d):
 
 
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")], ids=str)
-def test_attn_tree_paged_row_starts_that_fall(types):
+@pytest.mark.parametrize("full", [False, True])
+def test_attn_tree_paged_row_starts_that_fall(types, full):
     """Starts outside the rows or falling are taken as the highest start so far: rows and workspace stay inside."""
     import torch
 
     W = lib()
-    a, t = tree_case(W, [4, 4, 4, 4], 4, 2, 128, 0, [20, 30, 40, 50], 16, *types, mask="chain")
+    a, t = tree_case(W, [4, 4, 4, 4], 4, 2, 128, 0, [20, 30, 40, 50], 16, *types, mask="chain", width=wide(4, 2, 16) if full else None)
     good = t["out"].clone()
     for starts in ([0, 16, 0, 16, 16], [-5, 4, 2, 8, 99], [16, 0, 16, 0, 16], [2**31 - 1, -2**31, 3, 3, 3]):
         a.set("row_start", ints(starts))
@@ -604,8 +627,8 @@ def test_attn_tree_paged_many_requests():
     rows[[0, 4095]] = 2
     lens = rng.integers(-1, 60, 4096)
     lens[[0, 4095]] = 30, 45
-    for types in (("bf16", "bf16"), ("f32", "f32")):
-        a, t = tree_case(W, rows.tolist(), 2, 1, 128, 0, lens.tolist(), 8, *types, poison=False)
+    for types, width in ((("bf16", "bf16"), None), (("bf16", "bf16"), wide(4096, 1, 8)), (("f32", "f32"), None)):
+        a, t = tree_case(W, rows.tolist(), 2, 1, 128, 0, lens.tolist(), 8, *types, poison=False, width=width)
         W.gemv_device_errors()
         W.attn_tree_paged(a)
         torch.cuda.synchronize()

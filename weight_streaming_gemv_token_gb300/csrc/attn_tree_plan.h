@@ -124,15 +124,23 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   p.cut.n_kv = a->n_kv;
   p.cut.chain = a->mask == nullptr;
   p.cut.capacity = a->table_stride << page_shift(a->page_size);
-  // bfloat16 throughout, a head of 64 or 128, pages of whole swizzled groups of rows
+  // rows that a request brings on average; key tiles a CTA, were the tables full
+  const long long most = static_cast<long long>(a->rows) * group / (a->batch < a->rows ? a->batch : a->rows);
+  const long long full = (static_cast<long long>(a->batch) * p.cut.capacity + a->prefix_len) / kAtKeys * a->n_kv / sms;
+  // bfloat16 throughout, a head of 64 or 128, pages of whole swizzled groups of rows: on the
+  // tensor cores, but for rows that one row tile of 16 holds (all of the step's, where a
+  // prefix is read once a row tile) and not too many keys of a head of 128. Warp-level
+  // and tensor-core form: 1 token x 500 9.6 and 12.0 us, 8 x 4,096 32 and 36, 32 x 4,096
+  // 95 and 94, 16 x 16,000 175 and 163; of heads of 64, where the latter's softmax takes
+  // longer than the bytes, 8 x 4,096 23.5 and 29, 48 x 7,000 129 and 184.
+  const bool few = most <= 16 && (a->prefix_len == 0 || static_cast<long long>(a->rows) * group <= 16);
   p.tc = a->qdtype == DEC_BF16 && a->kvdtype == DEC_BF16 && (a->head_dim == 128 || a->head_dim == 64) && a->page_size >= 8 &&
          a->table_stride > 0 && a->num_pages > 0 && static_cast<long long>(a->num_pages) * a->n_kv < 1ll << 31 &&
-         (a->prefix_len == 0 || a->prefix_stride < 1ll << 31);
+         (a->prefix_len == 0 || a->prefix_stride < 1ll << 31) && !(few && (a->head_dim == 64 || full <= 48));
   // otherwise as many rows a row tile as a request brings on average, 16 to 64. In tiles of
   // 16, of 32 or 64, float32 queries: 8 x 32 rows x 4,096 tokens of bfloat16 79 and 74 us,
   // 32 x 128 rows 932 and 622; of float32, where the products bound either, 117 and 120,
   // 1,610 and 1,530.
-  const long long most = static_cast<long long>(a->rows) * group / (a->batch < a->rows ? a->batch : a->rows);
   if (p.tc)
     p.cut.mshift = 7;
   else if (a->kvdtype == DEC_F32)
