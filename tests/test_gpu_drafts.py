@@ -540,6 +540,35 @@ def test_attn_tree_paged_large_scores(q, kv):
     check_tree(t, rows, 4, 2, 128, 300, lens, 64, q)
 
 
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+@pytest.mark.parametrize("R", [1, 64])
+def test_attn_tree_paged_long_sums_are_not_cut_off(R, kv):
+    """Float32 results over thousands of values of one sign. A matrix instruction cuts its sums off instead of rounding them:
+    a block's three lose up to 2 u each, whatever the number of blocks; that of all blocks is rounded, as are reciprocal and
+    product (one u each; the errors of probabilities enter numerator and denominator alike, those of rounded sums have no
+    sign). So the mean relative error of the results lies within 6 u + 2 u, and 8 u for what is left of the errors without a
+    sign. Sums that are cut off block by block lose some 1.5 u a block: 100 to 500 u here."""
+    import torch
+
+    W = lib()
+    batch, n_q, n_kv, d, ctx, page = 24, 16, 8, 128, 4096, 64
+    a, t = tree_case(W, [R] * batch, n_q, n_kv, d, 0, [ctx] * batch, page, "f32", kv, mask="chain", poison=False)
+    for b in range(len(t["vp"])):
+        t["vp"][b].uniform_(1, 2)
+    W.attn_tree_paged(a)
+    torch.cuda.synchronize()
+    errors = []
+    for b in (0, 11, 23):
+        pages = torch.tensor(t["table"][b], device="cuda").long()
+        k, v = (t[x][pages].transpose(0, 1).reshape(n_kv, -1, d)[:, : ctx + R].double() for x in ("kp", "vp"))
+        q = t["q"].double().view(batch, R, n_kv, n_q // n_kv, d)[b]
+        s = torch.einsum("rghd,gkd->ghrk", q, k) * d ** -0.5
+        s.masked_fill_(torch.arange(ctx + R, device="cuda") > ctx + torch.arange(R, device="cuda")[:, None], -float("inf"))
+        want = torch.einsum("ghrk,gkd->rghd", torch.softmax(s, -1), v)
+        errors.append((t["out"].double().view(batch, R, n_kv, n_q // n_kv, d)[b] / want - 1).mean().item())
+    assert max(map(abs, errors)) <= 16 * U, [e / U for e in errors]
+
+
 @pytest.mark.parametrize("types,d,plen", [(("bf16", "bf16"), 128, 0), (("bf16", "bf16"), 128, 300), (("bf16", "bf16"), 64, 0),
                                           (("f32", "f32"), 128, 0), (("f32", "bf16"), 96, 50)], ids=str)
 @pytest.mark.parametrize("full", [False, True])

@@ -23,6 +23,31 @@ __device__ __forceinline__ uint32_t at_finite2(uint32_t p) {  // such halves bec
 }
 __device__ __forceinline__ bool at_odd(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
 
+// D = A B, the first product of a sum. The matrix instructions cut their sums off where
+// an addition would round, always towards 0: over many keys that is a share of the result
+// (32 x 64 rows x 16,384 tokens: error 5.7e-5, against 7.8e-7). So for float32 results a
+// block's products are summed from 0 and added by themselves, 5 to 18% of the time; of
+// bfloat16 results it is a small part of their rounding.
+__device__ __forceinline__ void at_mma16z(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void at_mma8z(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+               : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+               : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(0.f));
+}
+
+// x += y, two elements an instruction.
+__device__ __forceinline__ void at_add4(float (&x)[4], const float (&y)[4]) {
+#pragma unroll
+  for (int i = 0; i < 4; i += 2)
+    asm("{\n.reg .b64 a, b;\nmov.b64 a, {%0, %1};\nmov.b64 b, {%2, %3};\nadd.rn.f32x2 a, a, b;\nmov.b64 {%0, %1}, a;\n}"
+        : "+f"(x[i]), "+f"(x[i + 1])
+        : "f"(y[i]), "f"(y[i + 1]));
+}
+
 // ---- bfloat16 caches -------------------------------------------------------------
 
 template <typename QT, int DP, int QP>
@@ -112,7 +137,7 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
       }
     }
     bool odd = false;
-    constexpr int KS = KK < 2 ? 1 : 2;  // k steps at a time
+    constexpr int KS = KK < 2 || sizeof(QT) == 4 ? 1 : 2;  // k steps at a time
 #pragma unroll
     for (int k = 0; k < KK; k += KS) {
       uint32_t va[KS][4];
@@ -128,12 +153,31 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
           }
         }
       }
+      if constexpr (sizeof(QT) == 4) {
+        float c[KS][2][4];
 #pragma unroll
-      for (int i = 0; i < PP; ++i)
+        for (int i = PP - 1; i >= 0; --i)
+#pragma unroll
+          for (int u = 0; u < KS; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              if (i == PP - 1)
+                at_mma16z(c[u][t], va[u], p[t][i][0], p[t][i][1]);
+              else
+                am_mma16(c[u][t], va[u], p[t][i][0], p[t][i][1]);
+            }
 #pragma unroll
         for (int u = 0; u < KS; ++u)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) am_mma16(this->o[k + u][t], va[u], p[t][i][0], p[t][i][1]);
+          for (int t = 0; t < 2; ++t) at_add4(this->o[k + u][t], c[u][t]);
+      } else {
+#pragma unroll
+        for (int i = 0; i < PP; ++i)
+#pragma unroll
+          for (int u = 0; u < KS; ++u)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) am_mma16(this->o[k + u][t], va[u], p[t][i][0], p[t][i][1]);
+      }
     }
     if (DRAFTS && __any_sync(0xffffffffu, odd)) {
       for (int key = 0; key < 16; ++key)
@@ -273,19 +317,35 @@ struct AtCore32 {
     am_split_tf32(s[3], &ph[3], &pl[3]);
     const unsigned char* vrow = vp + 2 * (lane & 3) * PITCH + (lane >> 2) * 4;
     bool odd = false;
+    constexpr int NS = NT < 4 ? NT : 4;  // columns at a time: products into one accumulator stand apart
 #pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      float v0 = *reinterpret_cast<const float*>(vrow + n * 32), v1 = *reinterpret_cast<const float*>(vrow + PITCH + n * 32);
-      if (DRAFTS) {
-        if (at_odd(v0)) v0 = 0.f, odd = true;
-        if (at_odd(v1)) v1 = 0.f, odd = true;
+    for (int n = 0; n < NT; n += NS) {
+      float c[NS][4];
+      uint32_t bh[NS][2], bl[NS][2];
+#pragma unroll
+      for (int u = 0; u < NS; ++u)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          float v = *reinterpret_cast<const float*>(vrow + e * PITCH + (n + u) * 32);
+          if (DRAFTS && at_odd(v)) v = 0.f, odd = true;
+          am_split_tf32(v, &bh[u][e], &bl[u][e]);
+        }
+      constexpr bool APART = sizeof(QT) == 4;
+#pragma unroll
+      for (int u = 0; u < NS; ++u) {
+        if constexpr (APART)
+          at_mma8z(c[u], pl, bh[u][0], bh[u][1]);
+        else
+          am_mma8(o[n + u], pl, bh[u][0], bh[u][1]);
       }
-      uint32_t bh0, bl0, bh1, bl1;
-      am_split_tf32(v0, &bh0, &bl0);
-      am_split_tf32(v1, &bh1, &bl1);
-      am_mma8(o[n], ph, bh0, bh1);
-      am_mma8(o[n], ph, bl0, bl1);
-      am_mma8(o[n], pl, bh0, bh1);
+#pragma unroll
+      for (int u = 0; u < NS; ++u) am_mma8(APART ? c[u] : o[n + u], ph, bl[u][0], bl[u][1]);
+#pragma unroll
+      for (int u = 0; u < NS; ++u) am_mma8(APART ? c[u] : o[n + u], ph, bh[u][0], bh[u][1]);
+      if constexpr (APART) {
+#pragma unroll
+        for (int u = 0; u < NS; ++u) at_add4(o[n + u], c[u]);
+      }
     }
     if (DRAFTS && __any_sync(0xffffffffu, odd)) {
       for (int key = 0; key < 8; ++key)
