@@ -1,7 +1,7 @@
 // Attention of a step's rows on warp-level matrix instructions, for every type, head
 // size and page size: row tiles of 16, 32 or 64 rows (attn_tree_plan.h), a CTA a share of
-// the line of key tiles. Its eight warps are RG groups of 16 rows times 8 / RG rings: the
-// warps of a ring stream blocks of keys through it together, each copying a part, and each
+// the line of key tiles. Its warps are RG groups of 16 rows times KG rings: the warps of a
+// ring stream blocks of keys through it together, each copying a part, and each
 // holds its 16 rows against every block (attn_rows.cuh: bfloat16 caches, blocks of 16 keys
 // as the M side; float32 caches as in attn_mma.cuh: blocks of 8 keys, tf32 value and
 // remainder, three products). So the keys are read once for up to 64 rows.
@@ -317,7 +317,8 @@ struct AtCore32 {
     am_split_tf32(s[3], &ph[3], &pl[3]);
     const unsigned char* vrow = vp + 2 * (lane & 3) * PITCH + (lane >> 2) * 4;
     bool odd = false;
-    constexpr int NS = NT < 4 ? NT : 4;  // columns at a time: products into one accumulator stand apart
+    constexpr bool APART = sizeof(QT) == 4;
+    constexpr int NS = APART || NT < 4 ? 2 : 4;  // columns at a time: products into one accumulator stand apart
 #pragma unroll
     for (int n = 0; n < NT; n += NS) {
       float c[NS][4];
@@ -330,7 +331,6 @@ struct AtCore32 {
           if (DRAFTS && at_odd(v)) v = 0.f, odd = true;
           am_split_tf32(v, &bh[u][e], &bl[u][e]);
         }
-      constexpr bool APART = sizeof(QT) == 4;
 #pragma unroll
       for (int u = 0; u < NS; ++u) {
         if constexpr (APART)
@@ -467,12 +467,15 @@ struct AtCopy {
 
 // ---- the kernel --------------------------------------------------------------------
 
-// RG groups of 16 rows, KG = 8 / RG rings of blocks; SLOTS blocks of a ring.
+// RG groups of 16 rows, KG = WARPS / RG rings of blocks; SLOTS blocks of a ring. The work on
+// a float32 block is one long chain (tensor pipe and issue slots 28 and 26% busy with 8 warps):
+// 12 warps, two blocks each, take 214 us for 32 rows x 4,096, 8 warps 245. For bfloat16 the
+// queries' parts leave no registers for more.
 template <typename QT, int DP, bool F32, int RG>
 struct AtGeom {
-  static constexpr int WARPS = 8, KG = WARPS / RG;
+  static constexpr int WARPS = F32 ? 12 : 8, KG = WARPS / RG;
   static constexpr int BLOCK = F32 ? 2 * 8 * (DP * 4 + 16) : 2 * 16 * (DP * 2 + 16);
-  static constexpr int SLOTS = RG == 1 ? 3 : RG == 2 ? 5 : 8;
+  static constexpr int SLOTS = F32 ? (RG == 1 ? 2 : 6) : RG == 1 ? 3 : RG == 2 ? 5 : 8;
   static constexpr int RING = SLOTS * BLOCK;
   static constexpr int JOIN = WARPS * 16 * DP * 4;
   static constexpr int QBYTES = F32 ? RG * 2 * (DP / 8) * 32 * 16 : 0;
@@ -480,7 +483,7 @@ struct AtGeom {
 };
 
 template <typename QT, int DP, int QP, bool F32, int RG>
-__global__ void __launch_bounds__(256, 1) attn_tree_rows_kernel(const AtArgs p) {
+__global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG>::WARPS, 1) attn_tree_rows_kernel(const AtArgs p) {
   using G = AtGeom<QT, DP, F32, RG>;
   using Core = std::conditional_t<F32, AtCore32<QT, DP, QP>, AtCore16<QT, DP, QP>>;
   constexpr int WARPS = G::WARPS, KG = G::KG, KB = Core::KB, NTHREADS = 32 * WARPS, SLOTS = G::SLOTS;
@@ -661,7 +664,7 @@ cudaError_t at_launch_one(const AtArgs& a, const DeviceInfo& di, cudaStream_t st
     if (e != cudaSuccess) return e;
     lifted[di.device] = true;
   }
-  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32, RG>, dim3(di.sms), dim3(256), smem, st, true, a);
+  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32, RG>, dim3(di.sms), dim3(32 * AtGeom<QT, DP, F32, RG>::WARPS), smem, st, true, a);
 }
 
 template <typename QT, int DP, int QP, bool F32>
