@@ -138,9 +138,9 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
          a->table_stride > 0 && a->num_pages > 0 && static_cast<long long>(a->num_pages) * a->n_kv < 1ll << 31 &&
          (a->prefix_len == 0 || a->prefix_stride < 1ll << 31) && !(few && (a->head_dim == 64 || full <= 48));
   // otherwise as many rows a row tile as a request brings on average, 16 to 64. In tiles of
-  // 16, of 32 or 64, float32 queries: 8 x 32 rows x 4,096 tokens of bfloat16 79 and 74 us,
-  // 32 x 128 rows 932 and 622; of float32, where the products bound either, 117 and 120,
-  // 1,610 and 1,530.
+  // 16, of 32 or 64, float32 queries: 8 x 32 rows x 4,096 tokens of bfloat16 79 and 73 us,
+  // 32 x 128 rows 932 and 743; of float32, where a block's chain bounds either, 117 and 120,
+  // 1,610 and 1,545.
   if (p.tc)
     p.cut.mshift = 7;
   else if (a->kvdtype == DEC_F32)

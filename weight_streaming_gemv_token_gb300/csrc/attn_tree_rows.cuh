@@ -6,6 +6,11 @@
 // as the M side; float32 caches as in attn_mma.cuh: blocks of 8 keys, tf32 value and
 // remainder, three products). So the keys are read once for up to 64 rows.
 //
+// Bound by a block's chain of instructions for many rows and for float32, by memory for few
+// rows of bfloat16. Measured (16 query heads over 8, heads of 128): 32 single tokens x 4,096
+// bfloat16 95 us (5.6 TB/s), float32 queries 127, float32 caches 214 (5.0 TB/s); 32 x 64
+// rows 743 and 1,545.
+//
 // Blocks that hold drafted rows' keys mask scores row by row. A value that is not
 // finite would reach rows that do not see it through its product with a weight of 0,
 // so in these blocks it enters the products as 0 and is added afterwards to the rows

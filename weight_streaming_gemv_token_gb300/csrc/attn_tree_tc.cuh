@@ -25,7 +25,9 @@
 // Tensor memory (512 columns): scores / probabilities at 0 and 128, O at 256, Q at
 // 384. The products of a tile of head size 128 take 24 x 64 cycles for any number of
 // rows, its 64 KB at the SM's share of the measured bandwidth 2,700 at 1.85 GHz: bound
-// by memory for up to 128 rows a head.
+// by memory for up to 128 rows a head. Measured (16 query heads over 8): 32 x 64 rows x
+// 16,384 tokens 353 us (6.1 TB/s), 48 single tokens x 7,000 210
+// (6.5 TB/s), 8 x 16 rows x 4,096 36.5.
 //
 // Every wait is bounded; on a timeout the CTA records ERR_TC_TIMEOUT, stops, waits
 // for its issued MMAs and copies and frees its tensor memory.
