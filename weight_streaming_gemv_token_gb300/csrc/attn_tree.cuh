@@ -296,25 +296,27 @@ __device__ __forceinline__ void at_seams(const AtArgs& a, const AtWalk& w) {
     for (int k = w.segs + lane; k < a.seams; k += 32) a.seam[k] = AtSeam{};
 }
 
-// One warp, with a prefix, beside the work: the rows' records, of requests s with
-// s % gridDim.x == blockIdx.x.
+// One warp, with a prefix, beside the work: the rows' records, of rows r with r % gridDim.x
+// == blockIdx.x (all of a request's by one lane took longer than its work for a prompt).
 [[maybe_unused]] static __device__ __noinline__ void at_records(const AtArgs& a) {
   const int lane = threadIdx.x & 31;
   const AtSums s = at_sums(a);
   const long long prefix_segs = static_cast<long long>(a.cut.n_kv) * a.prefix_row_tiles, prefix = prefix_segs * (a.prefix_tiles + kAtExtra);
   if (blockIdx.x == 0 && lane == 0) *a.total = prefix + (s.all >> 26);
   at_each(a, s, [&](int i, int from, int rows, int len, long long size, long long x) {
-    if (i % static_cast<int>(gridDim.x) != static_cast<int>(blockIdx.x)) return;
+    const int ctas = gridDim.x, place = from % ctas;  // k0: this CTA's first row of the request
+    const int k0 = static_cast<int>(blockIdx.x) - place + (static_cast<int>(blockIdx.x) < place ? ctas : 0);
     if (rows == 0) {  // rows of an unused request
       const int e = max(from, AtWalk::clamp_row(a, a.row_start[i + 1]));
-      for (int r = from; r < e; ++r) a.rec[r].tiles = 0;
+      for (int r = from + k0; r < e; r += ctas) a.rec[r].tiles = 0;
       return;
     }
+    if (k0 >= rows) return;
     const long long head = at_head_units(a.cut, len, rows);
     const int rt = at_row_tiles(a.cut, rows);
     long long line = prefix + (x >> 26) + kAtExtra;
     int t = 0, tiles = at_tiles(a.cut, len, rows, 0);
-    for (int k = 0; k < rows; ++k) {
+    for (int k = k0; k < rows; k += ctas) {
       // a token's query heads may lie in two row tiles: the record is the first one's,
       // the other's follows from it
       const int at = (k * a.cut.group) >> a.cut.mshift;
