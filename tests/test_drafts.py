@@ -34,11 +34,11 @@ def host(tmp_path_factory):
     src.write_text('#include "attn_tree_plan.h"\n#include "spans.h"\nusing namespace wsg;\nextern "C" {\n'
                    "int plan(const attn_tree_args* a, long long* o) {\n"
                    "  if (!attn_tree_sizes_ok(a)) return 0;\n  const AtPlan p = attn_tree_plan(a, 152);\n"
-                   "  const long long v[] = {1 << p.cut.mshift, p.prefix_row_tiles, p.prefix_tiles, p.pieces, (long long)p.o,\n"
+                   "  const long long v[] = {1 << p.cut.mshift, p.prefix_row_tiles, p.prefix_tiles, p.pieces, p.ctas, (long long)p.o,\n"
                    "    (long long)p.ml, (long long)p.rec, (long long)p.line, (long long)p.total,\n"
-                   "    (long long)(a->prefix_len ? a->rows * sizeof(AtRow) : 152 * sizeof(AtSeam))};\n"
-                   "  for (int i = 0; i < 10; ++i) o[i] = v[i];\n  return 1;\n}\n"
-                   "AtCut cut(int group, int mt, int chain, int cap) { return AtCut{group, 1, mt == 128 ? 7 : 4, chain, cap}; }\n"
+                   "    (long long)(a->prefix_len ? a->rows * sizeof(AtRow) : p.ctas * sizeof(AtSeam))};\n"
+                   "  for (int i = 0; i < 11; ++i) o[i] = v[i];\n  return 1;\n}\n"
+                   "AtCut cut(int group, int mt, int chain, int cap) { return AtCut{group, 1, __builtin_ctz(mt), chain, cap}; }\n"
                    "int keys(int group, int mt, int chain, int cap, int n, int rows, int t) {\n"
                    "  return at_keys(cut(group, mt, chain, cap), n, rows, t); }\n"
                    "int tiles(int group, int mt, int chain, int cap, int n, int rows, int t) {\n"
@@ -66,7 +66,7 @@ def host(tmp_path_factory):
     return L
 
 
-NAMES = "mt prefix_row_tiles prefix_tiles pieces o ml rec line total rec_bytes".split()
+NAMES = "mt prefix_row_tiles prefix_tiles pieces ctas o ml rec line total rec_bytes".split()
 
 
 def test_keys_of_row_tiles(host):
@@ -127,7 +127,8 @@ def test_pieces_have_numbers_of_their_own_inside_the_workspace(W, host):
             continue
         starts, seen = np.concatenate([[0], np.cumsum(np.array(segs) + E)]), {}
         line = int(starts[-1])
-        C = min(152, line)
+        assert p["ctas"] in (152, 304, 608)
+        C = min(p["ctas"], line)
         for c in range(C):
             lo, hi = host.first(line, C, c), host.first(line, C, c + 1)
             j = int(np.searchsorted(starts, lo, side="right")) - 1

@@ -435,7 +435,7 @@ def test_attn_tree_paged(c, types):
 
 def wide(batch, n_kv, page):
     """Entries of tables wide enough that few rows too go to the tensor cores."""
-    return 49 * 153 * 128 // (batch * n_kv * page) + 1
+    return max(49 * 153 * 128 // (batch * n_kv * page), 1024 // page) + 1
 
 
 @pytest.mark.parametrize("c", [c for c in TREE_CASES if c[3] == 128 and c[4] == 0 and c[6] >= 8] + [

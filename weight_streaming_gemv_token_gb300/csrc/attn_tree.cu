@@ -135,14 +135,14 @@ cudaError_t launch_join(const AtArgs& t, const AtPlan& p, const DeviceInfo& di, 
     const cudaError_t e = at_prepare(attn_tree_seam_kernel<QT>, &done[0][di.device]);
     if (e != cudaSuccess) return e;
     // as many CTAs of eight rows as the GPU holds at once
-    const int most = 4 * di.sms / p.seams, need = (1 << p.cut.mshift) / 8;
+    const int most = p.seams < 4 * di.sms ? 4 * di.sms / p.seams : 1, need = (1 << p.cut.mshift) / 8;
     return launch_k(attn_tree_seam_kernel<QT>, dim3(p.seams, need < most ? need : most), dim3(256), 0, s, true, t);
   }
   const cudaError_t e = at_prepare(attn_tree_join_kernel<QT>, &done[1][di.device]);
   if (e != cudaSuccess) return e;
   const long long warps = (static_cast<long long>(t.a.rows) * t.a.n_q + 3) / 4;
   return launch_k(attn_tree_join_kernel<QT>, dim3(static_cast<unsigned>(warps < 6 * di.sms ? warps : 6 * di.sms)), dim3(128), 0,
-                  s, true, t, di.sms);
+                  s, true, t, p.ctas);
 }
 
 }  // namespace
@@ -239,7 +239,8 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
   t.rec = reinterpret_cast<AtRow*>(w + p.rec);
   t.seam = reinterpret_cast<AtSeam*>(w + p.rec);
   t.seams = p.seams;
-  t.seam_segs = p.pieces - di.sms <= di.sms;
+  t.seam_segs = p.pieces - p.ctas <= p.ctas;
+  t.per_sm = p.per_sm;
   t.total = reinterpret_cast<long long*>(w + p.line);
   const bool qf = a->qdtype == DEC_F32;
   if (p.tc) {

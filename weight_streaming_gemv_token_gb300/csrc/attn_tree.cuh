@@ -20,6 +20,7 @@ struct AtArgs {
   AtRow* rec;        // with a prefix: of every row
   AtSeam* seam;      // without: [seams], by segment (seam_segs) or by CTA
   int seams, seam_segs;
+  int per_sm;        // CTAs an SM
   long long* total;  // [1]: units of the line
 };
 

@@ -90,6 +90,7 @@ inline bool attn_tree_sizes_ok(const attn_tree_args* a) {
 // Which kernel runs, and the workspace.
 struct AtPlan {
   bool tc;            // attn_tree_tc_kernel
+  int per_sm, ctas;   // CTAs an SM, in all: the shares of the line
   AtCut cut;
   int prefix_row_tiles, prefix_tiles;  // of a head; of a segment
   long long pieces;   // numbers that pieces can have
@@ -129,14 +130,15 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   const long long full = (static_cast<long long>(a->batch) * p.cut.capacity + a->prefix_len) / kAtKeys * a->n_kv / sms;
   // bfloat16 throughout, a head of 64 or 128, pages of whole swizzled groups of rows: on the
   // tensor cores, but for rows that one row tile of 16 holds (all of the step's, where a
-  // prefix is read once a row tile) and not too many keys of a head of 128. Warp-level
-  // and tensor-core form: 1 token x 500 9.6 and 12.0 us, 8 x 4,096 32 and 36, 32 x 4,096
-  // 95 and 94, 16 x 16,000 175 and 163; of heads of 64, where the latter's softmax takes
-  // longer than the bytes, 8 x 4,096 23.5 and 29, 48 x 7,000 129 and 184.
+  // prefix is read once a row tile) and, with heads of 128, not too many keys. Warp-level and
+  // tensor-core form: 1 token x 500 9.7 and 12.0 us, 256 x 500 102 and 152, 8 x 4,096 32 and
+  // 36, 32 x 4,096 93 and 94, 16 x 16,000 177 and 162; of heads of 64, where the latter's
+  // softmax takes longer than the bytes, 8 x 4,096 23.5 and 29, 48 x 7,000 120 and 184.
   const bool few = most <= 16 && (a->prefix_len == 0 || static_cast<long long>(a->rows) * group <= 16);
+  const bool brief = a->head_dim == 64 || full <= 48 || p.cut.capacity <= 1024;
   p.tc = a->qdtype == DEC_BF16 && a->kvdtype == DEC_BF16 && (a->head_dim == 128 || a->head_dim == 64) && a->page_size >= 8 &&
          a->table_stride > 0 && a->num_pages > 0 && static_cast<long long>(a->num_pages) * a->n_kv < 1ll << 31 &&
-         (a->prefix_len == 0 || a->prefix_stride < 1ll << 31) && !(few && (a->head_dim == 64 || full <= 48));
+         (a->prefix_len == 0 || a->prefix_stride < 1ll << 31) && !(few && brief);
   // otherwise as many rows a row tile as a request brings on average, 16 to 64. In tiles of
   // 16, of 32 or 64, float32 queries: 8 x 32 rows x 4,096 tokens of bfloat16 79 and 73 us,
   // 32 x 128 rows 932 and 743; of float32, where a block's chain bounds either, 117 and 120,
@@ -155,14 +157,22 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   // the requests' row tiles: rows * group / mt whole ones at most, one more each
   const long long own = static_cast<long long>(a->rows) * group / mt + (a->batch < a->rows ? a->batch : a->rows);
   const long long segments = (own + p.prefix_row_tiles) * a->n_kv;
-  p.pieces = sms + segments;
-  p.seams = segments < sms ? static_cast<int>(segments) : sms;
+  // where row tiles of 16 leave it the shared memory and registers, as many small CTAs an SM
+  // as there are segments for: 256 requests of one token x 16 tokens with one 64 us, with two
+  // 35, with four 25; 4 requests of 8 rows x 1,000 15, 16 and 17.
+  p.per_sm = p.tc || p.cut.mshift != 4 || a->kvdtype == DEC_F32 ? 1
+             : segments > sms                                  ? 4
+             : 2 * segments > sms || a->prefix_len > 0         ? 2
+                                                               : 1;
+  p.ctas = sms * p.per_sm;
+  p.pieces = p.ctas + segments;
+  p.seams = segments < p.ctas ? static_cast<int>(segments) : p.ctas;
   auto up = [](size_t x) { return (x + 255) / 256 * 256; };
   const size_t rows = static_cast<size_t>(p.pieces) * mt;
   p.o = 0;
   p.ml = up(rows * a->head_dim * 4);
   p.rec = p.ml + up(rows * 8);
-  p.line = p.rec + up(a->prefix_len > 0 ? static_cast<size_t>(a->rows) * sizeof(AtRow) : static_cast<size_t>(sms) * sizeof(AtSeam));
+  p.line = p.rec + up(a->prefix_len > 0 ? static_cast<size_t>(a->rows) * sizeof(AtRow) : static_cast<size_t>(p.ctas) * sizeof(AtSeam));
   p.total = p.line + 256;
   return p;
 }

@@ -8,7 +8,7 @@
 //
 // Bound by a block's chain of instructions for many rows and for float32, by memory for few
 // rows of bfloat16. Measured (16 query heads over 8, heads of 128): 32 single tokens x 4,096
-// bfloat16 95 us (5.6 TB/s), float32 queries 127, float32 caches 214 (5.0 TB/s); 32 x 64
+// bfloat16 93 us (5.8 TB/s), float32 queries 103, float32 caches 214 (5.0 TB/s); 32 x 64
 // rows 743 and 1,545.
 //
 // Blocks that hold drafted rows' keys mask scores row by row. A value that is not
@@ -475,10 +475,11 @@ struct AtCopy {
 // RG groups of 16 rows, KG = WARPS / RG rings of blocks; SLOTS blocks of a ring. The work on
 // a float32 block is one long chain (tensor pipe and issue slots 28 and 26% busy with 8 warps):
 // 12 warps, two blocks each, take 214 us for 32 rows x 4,096, 8 warps 245. For bfloat16 the
-// queries' parts leave no registers for more.
-template <typename QT, int DP, bool F32, int RG>
+// queries' parts leave no registers for more; row tiles of 16 run as PER CTAs of 8 / PER warps
+// an SM, so that segments of few keys do not wait for each other's chains (attn_tree_plan.h).
+template <typename QT, int DP, bool F32, int RG, int PER>
 struct AtGeom {
-  static constexpr int WARPS = F32 ? 12 : 8, KG = WARPS / RG;
+  static constexpr int WARPS = F32 ? 12 : 8 / PER, KG = WARPS / RG;
   static constexpr int BLOCK = F32 ? 2 * 8 * (DP * 4 + 16) : 2 * 16 * (DP * 2 + 16);
   static constexpr int SLOTS = F32 ? (RG == 1 ? 2 : 6) : RG == 1 ? 3 : RG == 2 ? 5 : 8;
   static constexpr int RING = SLOTS * BLOCK;
@@ -487,9 +488,9 @@ struct AtGeom {
   static constexpr int SMEM = QBYTES + (KG * RING > JOIN ? KG * RING : JOIN);
 };
 
-template <typename QT, int DP, int QP, bool F32, int RG>
-__global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG>::WARPS, 1) attn_tree_rows_kernel(const AtArgs p) {
-  using G = AtGeom<QT, DP, F32, RG>;
+template <typename QT, int DP, int QP, bool F32, int RG, int PER>
+__global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG, PER>::WARPS, PER) attn_tree_rows_kernel(const AtArgs p) {
+  using G = AtGeom<QT, DP, F32, RG, PER>;
   using Core = std::conditional_t<F32, AtCore32<QT, DP, QP>, AtCore16<QT, DP, QP>>;
   constexpr int WARPS = G::WARPS, KG = G::KG, KB = Core::KB, NTHREADS = 32 * WARPS, SLOTS = G::SLOTS;
   extern __shared__ __align__(128) unsigned char am_raw[];
@@ -660,20 +661,24 @@ __global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG>::WARPS, 1) attn_t
   if (warp == 0 && p.prefix_tiles == 0) at_seams(p, s_walk);
 }
 
-template <typename QT, int DP, int QP, bool F32, int RG>
+template <typename QT, int DP, int QP, bool F32, int RG, int PER = 1>
 cudaError_t at_launch_one(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  constexpr size_t smem = AtGeom<QT, DP, F32, RG>::SMEM;
+  constexpr size_t smem = AtGeom<QT, DP, F32, RG, PER>::SMEM;
   static bool lifted[64] = {};
   if (!lifted[di.device]) {
-    const cudaError_t e = allow_smem_shared(attn_tree_rows_kernel<QT, DP, QP, F32, RG>, smem);
+    const cudaError_t e = allow_smem_shared(attn_tree_rows_kernel<QT, DP, QP, F32, RG, PER>, smem);
     if (e != cudaSuccess) return e;
     lifted[di.device] = true;
   }
-  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32, RG>, dim3(di.sms), dim3(32 * AtGeom<QT, DP, F32, RG>::WARPS), smem, st, true, a);
+  return launch_k(attn_tree_rows_kernel<QT, DP, QP, F32, RG, PER>, dim3(di.sms * PER), dim3(32 * AtGeom<QT, DP, F32, RG, PER>::WARPS), smem, st, true, a);
 }
 
 template <typename QT, int DP, int QP, bool F32>
 cudaError_t at_launch_rows(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
+  if constexpr (!F32) {
+    if (a.per_sm == 2) return at_launch_one<QT, DP, QP, F32, 1, 2>(a, di, st);
+    if (a.per_sm == 4) return at_launch_one<QT, DP, QP, F32, 1, 4>(a, di, st);
+  }
   if (a.cut.mshift == 4) return at_launch_one<QT, DP, QP, F32, 1>(a, di, st);
   if constexpr (!F32)
     if (a.cut.mshift == 5) return at_launch_one<QT, DP, QP, F32, 2>(a, di, st);
