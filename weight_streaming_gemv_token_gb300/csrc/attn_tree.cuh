@@ -386,11 +386,15 @@ __device__ __forceinline__ void at_put(const AtArgs& p, int row, int head, int e
     p.lse[static_cast<long long>(row) * p.a.n_q + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718f;
 }
 
-// by the types of queries and cache
+// by the types of queries and cache; wide: heads above 64
 cudaError_t launch_tree_bf16_bf16(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_bf16_bf16_wide(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 cudaError_t launch_tree_f32_bf16(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_f32_bf16_wide(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 cudaError_t launch_tree_bf16_f32(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_bf16_f32_wide(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 cudaError_t launch_tree_f32_f32(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
+cudaError_t launch_tree_f32_f32_wide(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 dec_status launch_tree_tc(const AtArgs& a, const DeviceInfo& di, cudaStream_t st);
 
 }  // namespace wsg

@@ -4,7 +4,7 @@
 namespace wsg {
 
 cudaError_t launch_tree_f32_f32(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
-  return at_launch<float, 1, true>(a, di, st);
+  return a.a.d > 64 ? launch_tree_f32_f32_wide(a, di, st) : at_launch<float, 1, true>(a, di, st);
 }
 
 }  // namespace wsg

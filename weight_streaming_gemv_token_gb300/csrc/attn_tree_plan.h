@@ -157,13 +157,15 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   // the requests' row tiles: rows * group / mt whole ones at most, one more each
   const long long own = static_cast<long long>(a->rows) * group / mt + (a->batch < a->rows ? a->batch : a->rows);
   const long long segments = (own + p.prefix_row_tiles) * a->n_kv;
-  // where row tiles of 16 leave it the shared memory and registers, as many small CTAs an SM
-  // as there are segments for: 256 requests of one token x 16 tokens with one 64 us, with two
-  // 35, with four 25; 4 requests of 8 rows x 1,000 15, 16 and 17.
-  p.per_sm = p.tc || p.cut.mshift != 4 || a->kvdtype == DEC_F32 ? 1
-             : segments > sms                                  ? 4
-             : 2 * segments > sms || a->prefix_len > 0         ? 2
-                                                               : 1;
+  // as many small CTAs an SM as there are segments for (and as rings and row groups allow):
+  // 256 requests of one token x 16 tokens with one 64 us, with two 35, with four 25; 4
+  // requests of 8 rows x 1,000 15, 16 and 17; 64 of 32 float32 rows x 100 73 and 48.
+  if (p.tc || a->kvdtype == DEC_F32)
+    p.per_sm = 1;
+  else if (p.cut.mshift > 4)
+    p.per_sm = segments > sms ? 2 : 1;
+  else
+    p.per_sm = segments > sms ? 4 : 2 * segments > sms || a->prefix_len > 0 ? 2 : 1;
   p.ctas = sms * p.per_sm;
   p.pieces = p.ctas + segments;
   p.seams = segments < p.ctas ? static_cast<int>(segments) : p.ctas;

@@ -475,8 +475,8 @@ struct AtCopy {
 // RG groups of 16 rows, KG = WARPS / RG rings of blocks; SLOTS blocks of a ring. The work on
 // a float32 block is one long chain (tensor pipe and issue slots 28 and 26% busy with 8 warps):
 // 12 warps, two blocks each, take 214 us for 32 rows x 4,096, 8 warps 245. For bfloat16 the
-// queries' parts leave no registers for more; row tiles of 16 run as PER CTAs of 8 / PER warps
-// an SM, so that segments of few keys do not wait for each other's chains (attn_tree_plan.h).
+// queries' parts leave no registers for more; they run as PER CTAs of 8 / PER warps an SM, so
+// that segments of few keys do not wait for each other's chains (attn_tree_plan.h).
 template <typename QT, int DP, bool F32, int RG, int PER>
 struct AtGeom {
   static constexpr int WARPS = F32 ? 12 : 8 / PER, KG = WARPS / RG;
@@ -676,20 +676,21 @@ cudaError_t at_launch_one(const AtArgs& a, const DeviceInfo& di, cudaStream_t st
 template <typename QT, int DP, int QP, bool F32>
 cudaError_t at_launch_rows(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
   if constexpr (!F32) {
-    if (a.per_sm == 2) return at_launch_one<QT, DP, QP, F32, 1, 2>(a, di, st);
     if (a.per_sm == 4) return at_launch_one<QT, DP, QP, F32, 1, 4>(a, di, st);
-  }
-  if (a.cut.mshift == 4) return at_launch_one<QT, DP, QP, F32, 1>(a, di, st);
-  if constexpr (!F32)
+    if (a.per_sm == 2)
+      return a.cut.mshift == 4   ? at_launch_one<QT, DP, QP, F32, 1, 2>(a, di, st)
+             : a.cut.mshift == 5 ? at_launch_one<QT, DP, QP, F32, 2, 2>(a, di, st)
+                                 : at_launch_one<QT, DP, QP, F32, 4, 2>(a, di, st);
     if (a.cut.mshift == 5) return at_launch_one<QT, DP, QP, F32, 2>(a, di, st);
-  return at_launch_one<QT, DP, QP, F32, 4>(a, di, st);
+  }
+  return a.cut.mshift == 4 ? at_launch_one<QT, DP, QP, F32, 1>(a, di, st) : at_launch_one<QT, DP, QP, F32, 4>(a, di, st);
 }
 
+// (heads above 64 are a translation unit of their own)
 template <typename QT, int QP, bool F32>
 cudaError_t at_launch(const AtArgs& a, const DeviceInfo& di, cudaStream_t st) {
   if (a.a.d <= 16) return at_launch_rows<QT, 16, QP, F32>(a, di, st);
-  if (a.a.d <= 64) return at_launch_rows<QT, 64, QP, F32>(a, di, st);
-  return at_launch_rows<QT, 128, QP, F32>(a, di, st);
+  return at_launch_rows<QT, 64, QP, F32>(a, di, st);
 }
 
 }  // namespace wsg
