@@ -141,7 +141,7 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
          (a->prefix_len == 0 || a->prefix_stride < 1ll << 31) && !(few && brief);
   // otherwise as many rows a row tile as a request brings on average, 16 to 64. In tiles of
   // 16, of 32 or 64, float32 queries: 8 x 32 rows x 4,096 tokens of bfloat16 79 and 73 us,
-  // 32 x 128 rows 932 and 743; of float32, where a block's chain bounds either, 117 and 120,
+  // 32 x 128 rows 932 and 692; of float32, where a block's chain bounds either, 117 and 120,
   // 1,610 and 1,545.
   if (p.tc)
     p.cut.mshift = 7;
