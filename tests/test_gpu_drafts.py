@@ -569,6 +569,45 @@ def test_attn_tree_paged_long_sums_are_not_cut_off(R, kv):
     assert max(map(abs, errors)) <= 16 * U, [e / U for e in errors]
 
 
+@pytest.mark.parametrize("kv,d,R,batch,ctx", [("bf16", 128, 64, 24, 1 << 16), ("bf16", 64, 64, 24, 1 << 16), ("bf16", 96, 64, 24, 1 << 16),
+                                              ("bf16", 96, 1, 96, 1 << 18), ("f32", 128, 64, 24, 1 << 16), ("f32", 128, 1, 24, 1 << 17)], ids=str)
+def test_attn_tree_paged_bfloat16_results_of_long_sums_round_as_they_should(kv, d, R, batch, ctx):
+    """Bfloat16 results next to a border: values are 1 or 1 + 2^-7, chosen so that a result is 1 + 2^-8 (a border) and 2^-16
+    (256 u) more in even elements, less in odd ones; the choice leaves out at most the largest of 2^14 probabilities (2^-13 of
+    2^-7: 16 u). Matrix instructions cut up to 128 sums of a result off before these are added up rounded, by up to 2 u each
+    of a sum that grows evenly: 128 u. Weights enter by 2^-7: 2^-24 of each. What rounded sums of some thousand terms lose
+    has no sign: 64 u are more than what the root of their number gives. So 240 u are enough. Cut off all along, a result loses a quarter of u for every instruction: 960 u and more here. (One
+    request's pages serve all, over and over.)"""
+    import torch
+
+    W = lib()
+    n_q, n_kv, page, own = 16, 8, 64, 1 << 14
+    a, t = tree_case(W, [R] * batch, n_q, n_kv, d, 0, [0] * batch, page, "bf16", kv, mask="none", poison=False, lse=False)
+    g = torch.Generator(device="cuda").manual_seed(1)
+    k = torch.randn((own // page, n_kv, page, d), generator=g, device="cuda").to(tdt(kv))
+    q = torch.randn((n_kv, d), generator=g, device="cuda").bfloat16()
+    scale = float(np.float32(0.1 * d ** -0.5))
+    s = torch.einsum("gd,gkd->gk", q.double(), k.transpose(0, 1).reshape(n_kv, own, d).double()) * scale
+    p = torch.softmax(s, -1)
+    assert p.max() < 2.0 ** -13
+    order = torch.rand((n_kv, d, own), generator=g, device="cuda").argsort(-1)
+    weight = torch.gather(p[:, None].expand(-1, d, -1), -1, order).cumsum(-1)
+    target = torch.tensor([0.5 + 2.0 ** -9, 0.5 - 2.0 ** -9], dtype=torch.float64, device="cuda").repeat(d // 2)
+    high = torch.zeros_like(order, dtype=torch.bool).scatter_(-1, order, weight <= target[:, None])
+    v = (1 + high.transpose(1, 2).double() / 128).view(n_kv, own // page, page, d).transpose(0, 1).contiguous().to(tdt(kv))
+    t["q"].copy_(q.repeat_interleave(n_q // n_kv, 0).reshape(1, -1).expand(batch * R, -1))
+    table = torch.arange(own // page, dtype=torch.int32, device="cuda").repeat(batch, (ctx + R) // own + 1)
+    a.set("k_pages", k).set("v_pages", v).set("page_table", table).set("seq_len", ints([ctx] * batch))
+    a.num_pages, a.table_stride, a.scale = own // page, table.shape[1], scale
+    a.with_workspace(torch.empty(W.attn_tree_paged_workspace(a), dtype=torch.uint8, device="cuda"))
+    W.gemv_device_errors()
+    W.attn_tree_paged(a)
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    out = t["out"].view(batch * R * n_q, d).float()
+    assert (out[:, ::2] == 1 + 2.0 ** -7).all() and (out[:, 1::2] == 1.0).all(), [x.unique(return_counts=True) for x in (out[:, ::2], out[:, 1::2])]
+
+
 @pytest.mark.parametrize("types,d,plen", [(("bf16", "bf16"), 128, 0), (("bf16", "bf16"), 128, 300), (("bf16", "bf16"), 64, 0),
                                           (("f32", "f32"), 128, 0), (("f32", "bf16"), 96, 50)], ids=str)
 @pytest.mark.parametrize("full", [False, True])

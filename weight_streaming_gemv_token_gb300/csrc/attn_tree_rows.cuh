@@ -30,9 +30,11 @@ __device__ __forceinline__ bool at_odd(float x) { return (__float_as_uint(x) & 0
 
 // D = A B, the first product of a sum. The matrix instructions cut their sums off where
 // an addition would round, always towards 0: over many keys that is a share of the result
-// (32 x 64 rows x 16,384 tokens: error 5.7e-5, against 7.8e-7). So for float32 results a
-// block's products are summed from 0 and added by themselves, 5 to 18% of the time; of
-// bfloat16 results it is a small part of their rounding.
+// (32 x 64 rows x 16,384 tokens: error 5.7e-5, against 7.8e-7), and bfloat16 results next to a
+// border round to its other side. So a block's products are summed from 0 and added by themselves
+// (float32 results 5 to 18% of the time, bfloat16 ones over bfloat16 caches 2 to 10%). Bfloat16
+// results over float32 caches are summed in the instructions over 32 blocks, 96 instructions that
+// lose some 3e-6, and these sums added up in memory: 4% of the time, 15 if every block's were.
 __device__ __forceinline__ void at_mma16z(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
                : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
@@ -59,7 +61,7 @@ template <typename QT, int DP, int QP>
 struct AtCore16 : ArCore<QT, DP, QP, 16> {
   using Base = ArCore<QT, DP, QP, 16>;
   static constexpr int KB = 16, TILE = Base::TILE, PITCH = Base::PITCH, KK = Base::KK, PP = Base::PP;
-
+  static constexpr bool APART = true;  // a block's products are added by themselves
 
   // row, keys' words: seen[t][j] of row 8 t + 2 (lane % 4) + j
   __device__ __forceinline__ static int row_of(int i) { return 8 * (i >> 1) + 2 * (threadIdx.x & 3) + (i & 1); }
@@ -158,31 +160,22 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
           }
         }
       }
-      if constexpr (sizeof(QT) == 4) {
-        float c[KS][2][4];
+      float c[KS][2][4];
 #pragma unroll
-        for (int i = PP - 1; i >= 0; --i)
-#pragma unroll
-          for (int u = 0; u < KS; ++u)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-              if (i == PP - 1)
-                at_mma16z(c[u][t], va[u], p[t][i][0], p[t][i][1]);
-              else
-                am_mma16(c[u][t], va[u], p[t][i][0], p[t][i][1]);
-            }
+      for (int i = PP - 1; i >= 0; --i)
 #pragma unroll
         for (int u = 0; u < KS; ++u)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) at_add4(this->o[k + u][t], c[u][t]);
-      } else {
+          for (int t = 0; t < 2; ++t) {
+            if (i == PP - 1)
+              at_mma16z(c[u][t], va[u], p[t][i][0], p[t][i][1]);
+            else
+              am_mma16(c[u][t], va[u], p[t][i][0], p[t][i][1]);
+          }
 #pragma unroll
-        for (int i = 0; i < PP; ++i)
+      for (int u = 0; u < KS; ++u)
 #pragma unroll
-          for (int u = 0; u < KS; ++u)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) am_mma16(this->o[k + u][t], va[u], p[t][i][0], p[t][i][1]);
-      }
+        for (int t = 0; t < 2; ++t) at_add4(this->o[k + u][t], c[u][t]);
     }
     if (DRAFTS && __any_sync(0xffffffffu, odd)) {
       for (int key = 0; key < 16; ++key)
@@ -247,6 +240,7 @@ struct AtCore16 : ArCore<QT, DP, QP, 16> {
 template <typename QT, int DP, int QP>
 struct AtCore32 {
   static constexpr int KB = 8, PITCH = DP * 4 + 16, TILE = KB * PITCH, NT = DP / 8;
+  static constexpr bool APART = sizeof(QT) == 4;  // a block's products are added by themselves, or those of some blocks
 
   float o[NT][4];
   float m[2], l[2];
@@ -322,7 +316,6 @@ struct AtCore32 {
     am_split_tf32(s[3], &ph[3], &pl[3]);
     const unsigned char* vrow = vp + 2 * (lane & 3) * PITCH + (lane >> 2) * 4;
     bool odd = false;
-    constexpr bool APART = sizeof(QT) == 4;
     constexpr int NS = APART || NT < 4 ? 2 : 4;  // columns at a time: products into one accumulator stand apart
 #pragma unroll
     for (int n = 0; n < NT; n += NS) {
@@ -373,6 +366,25 @@ struct AtCore32 {
       consume<true>(kt, vp, ok, scale, seen);
     else
       consume<false>(kt, vp, ok, scale, seen);
+  }
+
+  // The sums over earlier blocks lie in `sum`, a row's part and its reference. JOIN: o becomes the
+  // whole; otherwise the total takes o in (first: becomes it).
+  template <bool JOIN>
+  __device__ __forceinline__ void total(volatile float* sum, bool first) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      volatile float* t = sum + h * (2 * NT + 1);
+      if (!first) {
+        const float ref = t[2 * NT], f = ref == m[h] ? 1.f : am_exp2(ref - m[h]);
+#pragma unroll
+        for (int i = 0; i < 2 * NT; ++i) o[i >> 1][2 * h + (i & 1)] = fmaf(t[i], f, o[i >> 1][2 * h + (i & 1)]);
+      }
+      if (JOIN) continue;
+      t[2 * NT] = m[h];
+#pragma unroll
+      for (int i = 0; i < 2 * NT; ++i) t[i] = o[i >> 1][2 * h + (i & 1)], o[i >> 1][2 * h + (i & 1)] = 0.f;
+    }
   }
 
   template <typename F>
@@ -592,6 +604,8 @@ __global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG, PER>::WARPS, PER)
 #pragma unroll
     for (int i = 0; i < 4; ++i) token[i] = min(row0 + Core::row_of(i), pc.m0 + pc.nrows - 1) / a.group;
     const int mine = (nblk - kg + KG - 1) / KG;  // blocks of this ring
+    constexpr int SUM = Core::APART ? 0 : 32;    // blocks whose products the matrix instructions sum; 0: one
+    volatile float total[SUM ? DP / 2 + 4 : 1];  // (in memory)
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
       am_wait<SLOTS - 2>();
@@ -607,10 +621,14 @@ __global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG, PER>::WARPS, PER)
         const int at = i % SLOTS * 2 * Core::TILE;
         core.block(ring32 + at, ring + at + Core::TILE, ok[0], a.scale_log2, drafts, seen);
       }
+      if constexpr (SUM > 0)
+        if (i % SUM == SUM - 1 && i + 1 < mine) core.template total<false>(total, i == SUM - 1);
 #pragma unroll
       for (int j = 0; j < SLOTS - 1; ++j) ok[j] = ok[j + 1];
     }
     am_wait<0>();
+    if constexpr (SUM > 0)
+      if (mine > SUM) core.template total<true>(total, false);
     core.sums([&](int r, float m, float l) { s_m[warp][r] = m, s_l[warp][r] = l; });
     __syncthreads();  // every warp is past its ring
     float* out = reinterpret_cast<float*>(am_raw + G::QBYTES) + warp * 16 * DP;

@@ -41,8 +41,15 @@ constexpr int kTtSoft = 16;  // warps of the softmax
 constexpr int kTtLoaders = 3;  // warps that issue copies: warp 0 and those behind the softmax's
 constexpr int kTtThreads = 32 * (1 + kTtSoft + kTtLoaders), kTtRows = 128;
 constexpr int kTtPieces = 8;  // pieces announced: the rings hold the tiles of fewer
-constexpr uint32_t kTtTmO = 256, kTtTmQ = 384;
+constexpr uint32_t kTtTmO = 256, kTtTmQ = 384, kTtTmTotal = 448;
 constexpr int kTtStage = 32 * 12;  // floats of a warp's way to memory: 32 rows of 32 bytes and 16 more
+// Tiles whose products are summed in the matrix instructions. These cut sums off where an addition
+// would round, always towards 0 (half a unit or less of 2^-23, 16 instructions a tile): over 16,384
+// keys 5.7e-5 of a result, and results next to a border of bfloat16 rounded to its other side. 8
+// tiles lose some 2e-6; their sums are added up rounded (32 x 64 rows x 16,384 tokens 354 us without
+// and 370 with it, 48 single tokens x 7,000 209 and 213; added up in front of the scores, not behind
+// them, so that the products before are waited for: 379 and 219).
+constexpr int kTtSum = 8;
 
 template <int D>
 struct TtGeom {
@@ -172,6 +179,51 @@ __device__ __noinline__ void tt_odd(const AtArgs& p, const AtPiece& x, uint32_t 
     tc_wait_st();
   }
 }
+
+// A thread's part of O over a piece's tiles but the last kTtSum or fewer, with reference `ref`: 16
+// columns in tensor memory at `at`, of D = 128 12 more in the warp's way to memory, 4 in registers.
+template <int D>
+struct TtTotal {
+  uint32_t at;
+  float* so;
+  float ref = -INFINITY, last[4] = {};
+
+  // JOIN: O, whose reference is m, becomes the whole sum; otherwise the total takes O in (first: becomes it).
+  template <bool JOIN>
+  __device__ __forceinline__ void add(uint32_t to, float m, bool first) {
+    const int lane = threadIdx.x & 31;
+    const float f = ref == m ? 1.f : at_exp2(ref - m);
+#pragma unroll
+    for (int c0 = 0; c0 < D / 4; c0 += 16) {
+      uint32_t o[16], x[16];
+      tc_ld16(o, to + c0);
+      if (c0 == 0) {
+        tc_ld16(x, at);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(k < 12 ? so[k * 32 + lane] : last[k - 12]);
+      }
+      tc_wait_ld();
+#pragma unroll
+      for (int k = 0; k < 16; ++k) x[k] = first ? o[k] : __float_as_uint(fmaf(__uint_as_float(x[k]), f, __uint_as_float(o[k])));
+      if (JOIN) {
+        tc_st16(to + c0, x);
+      } else if (c0 == 0) {
+        tc_st16(at, x);
+      } else {
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          if (k < 12)
+            so[k * 32 + lane] = __uint_as_float(x[k]);
+          else
+            last[k - 12] = __uint_as_float(x[k]);
+        }
+      }
+    }
+    tc_wait_st();
+    ref = m;
+  }
+};
 
 // pk, pv: the prefix as [n_kv][plen][D] in boxes of 128 x 64; kp, vp: the pools as
 // [pages * n_kv][page][D] in boxes of min(page, 128) x 64.
@@ -384,7 +436,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             const uint64_t db = tc_desc_sw128_mn(vb + kk * 2048, G::BOX, 1024);
 #pragma unroll
             for (int part = 0; part < 2; ++part)
-              tc_mma_f16_ts(tmem + kTtTmO, pb + part * 64 + kk * 8, db, idO, (t | kk | part) != 0);
+              tc_mma_f16_ts(tmem + kTtTmO, pb + part * 64 + kk * 8, db, idO, (t % kTtSum | kk | part) != 0);
           }
           tc_commit(&v_empty[s]);
           tc_commit(&o_done[j & 1]);
@@ -410,6 +462,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     // nowhere. It has the code of tiles and results fetched while the stream's previous kernel ends
     // (behind the first keys' copies, which fill the memory's queues, that takes 5 us).
     bool dry = true;
+    TtTotal<D> total{tl + kTtTmTotal + sl * 16, so};
     auto row_done = [&]() {
       tc_fence_before();
       __syncwarp();
@@ -559,6 +612,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           tt_unpair(sum, &s0, &s1);
           lsum += s0 + s1;
           tc_wait_st();
+          if (t > 0 && t % kTtSum == 0) {
+            // O into the total once P_{j-1} V_{j-1} has completed; this tile's product starts it anew
+            if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1))) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            total.template add<false>(to, m_ref, t == kTtSum);
+          }
         }
         if (special) {
           const int st = j % STAGES;
@@ -595,6 +657,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           break;
         }
         lsum = (x[0][v] + x[1][v]) + (x[2][v] + x[3][v]);
+        if (cur.tiles > kTtSum) total.template add<true>(to, m_ref, false);
         if (*vodd == piece + 1) tt_odd<D>(p, cur, to, sl, have, token);
         const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;  // a NaN sum stays one
         if (sl == 0 && have) {
