@@ -494,6 +494,36 @@ def test_attn_tree_paged_drafts_that_are_not_finite(types, d):
     assert W.gemv_device_errors() == 0
 
 
+@pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "bf16")], ids=str)
+@pytest.mark.parametrize("d", [64, 128])
+def test_attn_tree_paged_drafts_that_are_not_finite_in_every_request(types, d):
+    """Several hundred short requests without a prefix, each with a drafted value that is not finite in every head: a CTA has
+    one such piece after the other, each of one tile. Rows that see it are not finite, the others hold the bits they have
+    without it."""
+    import torch
+
+    W = lib()
+    n_q, n_kv, page, B, R, odd = 16, 8, 16, 300, 16, 3
+    lens = [(7 * i) % 90 for i in range(B)]
+    a, t = tree_case(W, [R] * B, n_q, n_kv, d, 0, lens, page, *types, seed=11, poison=False)
+    W.attn_tree_paged(a)
+    torch.cuda.synchronize()
+    clean = t["out"].clone()
+    hit = torch.tensor(np.concatenate([s[:, odd] for s in t["seen"]]), device="cuda")
+    assert B <= hit.sum() < B * R
+    i = np.array(lens) + odd
+    at = torch.tensor(t["table"][np.arange(B), i // page], device="cuda").long(), slice(None), torch.tensor(i % page, device="cuda")
+    t["vp"][at + (d - 1,)] = torch.tensor([float("nan"), float("inf"), -float("inf")], device="cuda").repeat(100)[:, None].to(t["vp"].dtype)
+    for _ in range(10):
+        t["out"].fill_(7.0)
+        W.attn_tree_paged(a)
+        torch.cuda.synchronize()
+        assert torch.equal(t["out"][~hit], clean[~hit])
+        assert not torch.isfinite(t["out"][hit].view(-1, n_q, d)[..., d - 1]).any()
+        assert torch.equal(t["out"][hit].view(-1, n_q, d)[..., : d - 1], clean[hit].view(-1, n_q, d)[..., : d - 1])
+    assert W.gemv_device_errors() == 0
+
+
 @pytest.mark.parametrize("types", [("bf16", "bf16"), ("f32", "f32")], ids=str)
 @pytest.mark.parametrize("d", [64, 128])
 def test_attn_tree_paged_strides_and_no_lse(types, d):

@@ -243,12 +243,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   __shared__ __align__(8) uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, o_free, drain, row_bar[4], told[kTtPieces];
   __shared__ uint32_t tmem_base;
-  __shared__ int s_fail, s_odd;
+  __shared__ int s_fail;
+  // whether a piece had drafted values that are not finite, by its parity: a warp may be at the piece behind while another
+  // has yet to read what this one had (not two behind: every warp puts each piece's queries)
+  __shared__ int s_odd[2];
   __shared__ float xch[2][4][kTtRows];
   const AmArgs& a = p.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   volatile int* vfail = &s_fail;
-  volatile int* vodd = &s_odd;
+  volatile int* vodd = s_odd;
 
   if (tid == 0) {
     for (int s = 0; s < STAGES; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1), mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
@@ -259,7 +262,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     for (int i = 0; i < 4; ++i) mbar_init(&row_bar[i], 4);
     for (int i = 0; i < kTtPieces; ++i) mbar_init(&told[i], 1);
     s_fail = 0;
-    s_odd = -1;
+    s_odd[0] = s_odd[1] = -1;
     s_dry = AtPiece{};
     s_dry.prefix = true;
     s_dry.nrows = kTtRows;
@@ -628,7 +631,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             ok = false;
             break;
           }
-          if (tt_mend<D>(Vs + st * G::TILE, tk, cur.n, k1, holes, page_shift_)) *vodd = piece + 1;
+          if (tt_mend<D>(Vs + st * G::TILE, tk, cur.n, k1, holes, page_shift_)) vodd[piece & 1] = piece + 1;
           fence_proxy_async_smem();
         }
         tc_fence_before();
@@ -658,7 +661,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         }
         lsum = (x[0][v] + x[1][v]) + (x[2][v] + x[3][v]);
         if (cur.tiles > kTtSum) total.template add<true>(to, m_ref, false);
-        if (*vodd == piece + 1) tt_odd<D>(p, cur, to, sl, have, token);
+        if (vodd[piece & 1] == piece + 1) tt_odd<D>(p, cur, to, sl, have, token);
         const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;  // a NaN sum stays one
         if (sl == 0 && have) {
           if (!cur.whole)
