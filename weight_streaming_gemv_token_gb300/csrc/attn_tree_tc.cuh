@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   __shared__ __align__(8) uint64_t k_full[STAGES], k_empty[STAGES], v_full[STAGES], v_empty[STAGES];
   __shared__ __align__(8) uint64_t s_full[2], p_full[2], o_done[2], q_full, o_free, drain, row_bar[4], told[kTtPieces];
   __shared__ uint32_t tmem_base;
-  __shared__ int s_fail;
+  __shared__ int s_fail, s_put[kTtLoaders][2];
   // whether a piece had drafted values that are not finite, by its parity: a warp may be at the piece behind while another
   // has yet to read what this one had (not two behind: every warp puts each piece's queries)
   __shared__ int s_odd[2];
@@ -254,7 +254,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
   volatile int* vodd = s_odd;
 
   if (tid == 0) {
-    for (int s = 0; s < STAGES; ++s) mbar_init(&k_full[s], 1), mbar_init(&k_empty[s], 1), mbar_init(&v_full[s], 1), mbar_init(&v_empty[s], 1);
+    for (int s = 0; s < STAGES; ++s) mbar_init(&k_full[s], kTtLoaders), mbar_init(&k_empty[s], 1), mbar_init(&v_full[s], kTtLoaders), mbar_init(&v_empty[s], 1);
     for (int b = 0; b < 2; ++b) mbar_init(&s_full[b], 1), mbar_init(&p_full[b], kTtSoft), mbar_init(&o_done[b], 1);
     mbar_init(&q_full, kTtSoft);
     mbar_init(&o_free, kTtSoft);
@@ -291,7 +291,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     pdl_trigger();
     AtWalk walk;
     if (who == 0) walk = at_start(p);
-    int j = 0;  // tiles so far
+    int j = 0, keys = 0, values = 0;  // tiles so far; those whose keys, values this loader has asked for
     bool ok = true;
     AtPiece pc{};
     // this loader's boxes are numbers who, who + loaders, .. of (page, 64 columns); this lane's one
@@ -334,28 +334,26 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         const bool there = e >= 0 && e < a.pool.num_pages;
         const int plane = e * a.n_kv + pc.g, y = shift > kAtKeyShift ? tk & ((1 << shift) - 1) : 0;
         const uint32_t part = 128u << page_shift_;  // bytes of a page's columns
-        uint32_t bytes = 0, holes = 0;
+        const bool mine = pc.prefix ? unit < G::BOXES : there;  // this lane copies a box
+        const uint32_t bytes = __popc(__ballot_sync(0xffffffffu, mine)) * (pc.prefix ? G::BOX : part);
+        uint32_t holes = 0;
         if (who == 0) {
           const bool wanted = !pc.prefix && lane < tile_pages && tk + (lane << page_shift_) < pc.k1;
-          const bool got = wanted && all >= 0 && all < a.pool.num_pages;
-          bytes = pc.prefix ? G::TILE : __popc(__ballot_sync(0xffffffffu, got)) * part * G::BOXES;
-          holes = __ballot_sync(0xffffffffu, wanted && !got);
+          holes = __ballot_sync(0xffffffffu, wanted && !(all >= 0 && all < a.pool.num_pages));
         }
         if (i + 1 < pc.tiles) {
           e = entry(tk + kAtKeys, unit_page);
           if (who == 0) all = entry(tk + kAtKeys, lane);
         }
+        // (every loader arrives for every tile: none falls so far behind that it mistakes a barrier's phase)
         auto load = [&](unsigned char* dst, const CUtensorMap* pre, const CUtensorMap* pages, uint64_t* bar) {
-          if (who == 0) {
-            if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
-            __syncwarp();
-          }
-          // (copies may complete before the bytes are announced: the phase ends with both)
-          if (pc.prefix) {
-            if (unit < G::BOXES) tma_load_3d_map(dst + unit * G::BOX, pre, unit * 64, tk, pc.g, bar);
-          } else if (there) {
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (!mine) return;
+          if (pc.prefix)
+            tma_load_3d_map(dst + unit * G::BOX, pre, unit * 64, tk, pc.g, bar);
+          else
             tma_load_3d_map(dst + unit_box * G::BOX + unit_page * part, pages, unit_box * 64, y, plane, bar);
-          }
         };
         if (j >= STAGES && !__all_sync(0xffffffffu, mbar_wait(&k_empty[st], ((j / STAGES) - 1) & 1))) {
           ok = false;
@@ -366,28 +364,34 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           if (holes) atomicOr(a.err, ERR_BAD_PAGE);
         }
         load(Ks + st * G::TILE, &pk, &kp, &k_full[st]);
+        keys = j + 1;
         if (j >= STAGES && !__all_sync(0xffffffffu, mbar_wait(&v_empty[st], ((j / STAGES) - 1) & 1))) {
           ok = false;
-          // the keys of this tile are on their way
-          if (who == 0 && lane == 0 && !mbar_wait(&k_full[st], (j / STAGES) & 1)) fail();
           break;
         }
         load(Vs + st * G::TILE, &pv, &vp, &v_full[st]);
+        values = j + 1;
         if (__any_sync(0xffffffffu, *vfail)) {
           ok = false;
-          ++j;
           break;
         }
       }
     }
     if (!ok && lane == 0) fail();
-    if (who == 0) {
-      if (p.prefix_tiles == 0) at_seams(p, walk);
-      // the last copies into each stage have landed before the CTA may end, after a failure too
-      if (lane == 0) {
+    if (who == 0 && p.prefix_tiles == 0) at_seams(p, walk);
+    // the last copies into each stage have landed before the CTA may end; after a failure a loader first
+    // arrives for the tiles (STAGES at most) that it did not come to and another did
+    if (lane == 0) s_put[who][0] = keys, s_put[who][1] = values;
+    __syncwarp();
+    asm volatile("bar.sync 1, %0;" ::"n"(32 * kTtLoaders) : "memory");
+    if (lane == 0) {
+      for (int w = 0; w < 2; ++w) {
+        int top = 0;
+        for (int i = 0; i < kTtLoaders; ++i) top = max(top, s_put[i][w]);
+        uint64_t* full = w ? v_full : k_full;
+        for (int i = s_put[who][w]; i < top; ++i) mbar_arrive(&full[i % STAGES]);
         for (int s = 0; s < STAGES; ++s)
-          if (s < j && (!mbar_wait(&k_full[s], ((j - 1 - s) / STAGES) & 1) || !mbar_wait(&v_full[s], ((j - 1 - s) / STAGES) & 1)))
-            fail();
+          if (who == 0 && s < top && !mbar_wait(&full[s], ((top - 1 - s) / STAGES) & 1)) fail();
       }
     }
   } else if (warp == 1) {
