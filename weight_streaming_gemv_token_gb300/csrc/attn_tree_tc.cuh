@@ -395,6 +395,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
     }
   } else if (warp == 1) {
+    pdl_wait();  // (the limits of its waits do not count the time of the stream's previous kernel)
     if (lane == 0) {
       constexpr uint32_t idS = tc_idesc(kTtRows, kAtKeys);
       constexpr uint32_t idO = tc_idesc(kTtRows, D) | (1u << 16);  // B (values) MN-major
