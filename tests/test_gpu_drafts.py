@@ -946,6 +946,32 @@ def test_logits_adjust_special_values():
     assert W.gemv_device_errors() == 0x4 and nxt[0] == 17 and torch.isfinite(out[0]).all()
 
 
+@pytest.mark.parametrize("x", ["f32", "bf16"])
+@pytest.mark.parametrize("v,pairs", [(1000, [(5, 9), (5, 600), (130, 999)]), (40000, [(5, 6), (100, 300), (511, 512), (3, 39999), (20000, 20001)]),
+                                     (300000, [(7, 299999), (4096, 8192)])], ids=str)
+def test_logits_adjust_zeros_of_both_signs_tie(v, pairs, x):
+    """A row whose greatest logits are -0.0 and, at a higher token, 0.0: of equal ones the lowest token is the greedy one,
+    whether one thread, warp or CTA has both or several do; tokens with a rule and without one."""
+    import torch
+
+    W = lib()
+    rows = 4 * len(pairs)
+    logits = -1 - rand((rows, v), x, 3).abs()
+    text = np.full((rows, 2), -1)
+    for r, (lo, hi) in enumerate(pairs * 4):
+        logits[r, lo], logits[r, hi] = -0.0, 0.0
+        text[r] = [(-1, -1), (lo, -1), (-1, hi), (lo, hi)][r // len(pairs)]
+    out, nxt = torch.empty_like(logits), torch.full((rows,), -9, dtype=torch.int32, device="cuda")
+    W.logits_adjust(W.logits_adjust_args(
+        rows=rows, vocab=v, requests=rows, xdtype=code(W, x), ydtype=code(W, x), logits=logits, logits_stride=v, out=out, out_stride=v,
+        next=nxt, tokens=ints(text), tokens_stride=2, tokens_len=ints([2] * rows), repetition=torch.full((rows,), 1.5, device="cuda")))
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    assert nxt.tolist() == [lo for lo, _ in pairs] * 4
+    at = torch.arange(rows, device="cuda"), torch.tensor([lo for lo, _ in pairs] * 4, device="cuda")
+    assert torch.signbit(out[at]).all()  # the logit itself stays -0.0
+
+
 def test_logits_adjust_long_texts_and_lists():
     """One token many times, its biases listed many times: counts are exact, the last bias counts, every pass the same bits."""
     import torch

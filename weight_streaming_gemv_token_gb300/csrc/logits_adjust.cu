@@ -64,9 +64,9 @@ struct LaArgs {
   uint32_t* err;
 };
 
-// Bits whose unsigned order is the order of finite floats and infinities; 0 is below all.
+// Bits whose unsigned order is the order of finite floats and infinities, both zeros alike; 0 is below all.
 __device__ __forceinline__ uint32_t order_bits(float x) {
-  const uint32_t u = __float_as_uint(x);
+  const uint32_t u = __float_as_uint(x == 0.f ? 0.f : x);
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
