@@ -782,10 +782,11 @@ dec_status attn_tree_paged(const attn_tree_args* a, void* stream);
 
 /* Logits by the rules of their requests. Row r belongs to request seq[r] (NULL: r;
  * outside [0, requests): the row is left as it was). Its text is the request's
- * tokens[0 .. tokens_len + tokens_base), of which the first prompt_len (NULL: 0) are
- * its prompt, and, with draft_tokens, the drafted tokens of those rows of the
- * request that mask says (NULL: up to r itself). With n(v) the times that token v
- * comes after the prompt, a logit x of v becomes
+ * tokens[0 .. tokens_len + tokens_base) and behind them, with draft_tokens, the
+ * drafted tokens of those rows of the request that mask says (NULL: up to r
+ * itself), in the rows' order. The first prompt_len (NULL: 0) tokens of it all are
+ * its prompt, rows that bring a prompt's tokens among them. With n(v) the times
+ * that token v comes after the prompt, a logit x of v becomes
  *   x / repetition (x > 0) or x * repetition, if v is in the text at all;
  *   x - frequency * n(v);  x - presence, if n(v) > 0;
  *   x + bias, if v is in the request's list of bias_len entries (of equal ones the

@@ -71,12 +71,13 @@ def step_slots(held, fresh, owned, table, ring, state, page, rows, parents=None,
 
 
 def adjust(x, text, prompt, drafted, rep, freq, pres, biases, allowed):
-    """One row of logits. text: its tokens, the first `prompt` of them the prompt; drafted: further tokens; biases: pairs
-    (token, value), the last of a token counts; allowed: bool [vocab] or None. Also the greedy token, or -1."""
+    """One row of logits. text, drafted: its tokens, one behind the other, the first `prompt` of them all the prompt; biases:
+    pairs (token, value), the last of a token counts; allowed: bool [vocab] or None. Also the greedy token, or -1."""
     x = np.array(x, dtype=np.float64)
     v = len(x)
-    said = [int(t) for t in list(text[prompt:]) + list(drafted) if 0 <= t < v]
-    for t in set(said) | {int(t) for t in text[:prompt] if 0 <= t < v}:
+    whole = [int(t) for t in list(text) + list(drafted)]
+    said = [t for t in whole[prompt:] if 0 <= t < v]
+    for t in {t for t in whole if 0 <= t < v}:
         x[t] = x[t] / rep if x[t] > 0 else x[t] * rep
         n = said.count(t)
         if n:

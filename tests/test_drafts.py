@@ -185,6 +185,16 @@ def test_definition_of_adjusted_logits():
     assert OD.adjust([math.nan, -math.inf], [], 0, [], 1.0, 0.0, 0.0, [], None)[1] == -1
 
 
+def test_definition_of_logits_of_a_prompts_rows():
+    """Tokens of the prompt that are still drafted rows do not count as said."""
+    one = OD.adjust([3.0, 3.0, 3.0, 3.0], [0], 3, [1, 2, 1, 3], 2.0, 0.25, 0.5, [], None)[0]
+    assert one.tolist() == [1.5, 0.75, 1.5, 0.75]  # 0, 2: prompt only; 1: prompt and once behind it; 3: once
+    for k in range(4):  # wherever the text ends
+        two = OD.adjust([3.0, 3.0, 3.0, 3.0], [0, 1, 2, 1, 3][:k], 3, [0, 1, 2, 1, 3][k:], 2.0, 0.25, 0.5, [], None)[0]
+        assert (one == two).all()
+    assert OD.adjust([3.0, 3.0], [], 9, [1], 2.0, 0.25, 0.5, [], None)[0].tolist() == [3.0, 1.5]
+
+
 def test_definition_of_acceptance():
     assert OD.accept([-1, 0, 0, 2, 2], [9, 5, 6, 7, 8], [6, 0, 8, 0, 3], 8) == [0, 2, 4]
     assert OD.accept([-1, 0, 0, 2, 2], [9, 5, 6, 7, 8], [6, 0, 8, 0, 3], 2) == [0, 2]

@@ -946,6 +946,62 @@ def test_logits_adjust_special_values():
     assert W.gemv_device_errors() == 0x4 and nxt[0] == 17 and torch.isfinite(out[0]).all()
 
 
+@pytest.mark.parametrize("c", [([1], 40, {}), ([3, 1, 0, 7], 512, {}), ([9, 40, 33], 4097, {"history": 400}), ([40, 64], 5000, {"mask": False, "base": 7}),
+                               ([400, 2, 290], 700, {"mask": False, "far": True}), ([270, 9], 1500, {"far": True}),
+                               ([33, 5], 300000, {"far": True, "mask": False}), ([50, 300, 20], 900, {"text": False, "mask": False})], ids=str)
+def test_logits_adjust_of_a_prompts_rows(c):
+    """A prompt that ends among the drafted rows, behind them, or where the text ends: its tokens count as the prompt's, in
+    the list of a row's drafted tokens, in the words (more than a list holds) and without a text."""
+    import torch
+
+    W = lib()
+    rows, vocab, o = c
+    o = dict(o)
+    text = o.pop("text", True)
+    rng = np.random.default_rng(sum(rows))
+    a, p = adjust_case(W, rows, vocab, "f32", "f32", **o)
+    if not text:
+        p["len"][:] = 0
+        a.set("tokens", None).set("tokens_len", None)
+    for k in range(3):
+        more = [0, max(rows) + 5, rng.integers(0, np.array(rows) + 2)][k]
+        p["prompt"] = p["len"] + more
+        a.set("prompt_len", ints(p["prompt"]))
+        p["out"].fill_(7.0)
+        W.gemv_device_errors()
+        W.logits_adjust(a)
+        torch.cuda.synchronize()
+        assert W.gemv_device_errors() == 0
+        check_adjust(p, "f32")
+
+
+@pytest.mark.parametrize("n,at", [(30, 0), (30, 29), (300, 17), (2000, 1000)])
+def test_logits_of_a_prompts_last_row_are_those_of_the_prompt_as_text(n, at):
+    """A prompt whose rows from `at` on are this step's: its last row's logits hold the bits of a call that has the whole
+    prompt as text, and so do those of a tree's rows behind it, drafted tokens counting as said."""
+    import torch
+
+    W = lib()
+    v, more = 1200, 3
+    rng = np.random.default_rng(n)
+    text = rng.integers(0, 60, n + more)
+    x = rand((1, v), "f32", 1, 3.0).expand(n + more - at, v).contiguous()
+    kw = dict(vocab=v, requests=1, xdtype=0, ydtype=0, logits_stride=v, out_stride=v, prompt_len=ints([n]),
+              repetition=torch.tensor([1.3], device="cuda"), frequency=torch.tensor([0.4], device="cuda"),
+              presence=torch.tensor([0.7], device="cuda"))
+    R = n + more - at
+    out, nxt = torch.empty_like(x), torch.empty(R, dtype=torch.int32, device="cuda")
+    W.logits_adjust(W.logits_adjust_args(rows=R, logits=x, out=out, next=nxt, seq=ints([0] * R), tokens=ints(text[None]), tokens_stride=n + more,
+                                         tokens_len=ints([at]), draft_tokens=ints(text[at:]), row_start=ints([0, R]), **kw))
+    for k in range(more + 1):
+        o, t = torch.empty_like(x[:1]), torch.empty(1, dtype=torch.int32, device="cuda")
+        W.logits_adjust(W.logits_adjust_args(rows=1, logits=x[:1], out=o, next=t, tokens=ints(text[None]), tokens_stride=n + more,
+                                             tokens_len=ints([n + k]), **kw))
+        torch.cuda.synchronize()
+        assert torch.equal(o[0], out[n - at - 1 + k]) and t[0] == nxt[n - at - 1 + k], k
+    assert W.gemv_device_errors() == 0
+
+
 @pytest.mark.parametrize("x", ["f32", "bf16"])
 @pytest.mark.parametrize("v,pairs", [(1000, [(5, 9), (5, 600), (130, 999)]), (40000, [(5, 6), (100, 300), (511, 512), (3, 39999), (20000, 20001)]),
                                      (300000, [(7, 299999), (4096, 8192)])], ids=str)

@@ -10,8 +10,8 @@
 // in turn (frequent tokens have neighbouring numbers: with a range each, the first CTA
 // had most of a text's). For its tokens a CTA keeps one word each in shared memory: the
 // times that the token came (bits 0-19), the number of its bias in the list (20-29) and
-// whether the prompt has it (31), built once a request from its text, by integer atomics
-// whose order does not matter, and a list of those that have one. A row then is
+// whether the prompt has it (31; 30: its drafted part), built once a request from its text, by
+// integer atomics whose order does not matter, and a list of those that have one. A row then is
 //   - a copy of all tokens without a rule but the mask, four a thread;
 //   - the listed tokens, one a thread, so that the long division runs in full warps;
 //   - the tokens drafted on the way to the row, which are listed apart for every row.
@@ -144,6 +144,7 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
   extern __shared__ __align__(16) uint32_t s_word[];  // [chunk], then [kLaRows][chunk / 128] bits of quads with drafted tokens
   __shared__ unsigned long long s_best[kLaRows];
   __shared__ LaRow s_row[kLaRows];
+  __shared__ int s_prompt[kLaRows];  // how many of the drafted tokens listed, the first ones, are the prompt's; not listed: those of rows before this
   __shared__ uint16_t s_draft[kLaRows][kLaDrafts], s_touched[kLaTouched];
   __shared__ uint32_t s_bits[kLaChunkMax / 32];  // tokens with a word
   __shared__ int s_count;                        // of them
@@ -162,13 +163,14 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
       if (v < 0 || v >= a.vocab || (v >> kLaSpan & vmask) != own) return -1;
       return (v >> kLaSpan >> a.vshift << kLaSpan) + (v & ((1 << kLaSpan) - 1));
     };
-    // number k of the drafted tokens on the way to row r, or -1
-    auto drafted = [&](int r, int begin, int k) -> int {
-      if (a.mask ? k >= 32 * a.mask_words || !(a.mask[static_cast<long long>(r) * a.mask_words + (k >> 5)] >> (k & 31) & 1u)
-                 : k > r - begin)
-        return -1;
-      return local(a.draft[begin + k]);
+    // whether row number k of the request is on the way to row r
+    auto on_way = [&](int r, int begin, int k) -> bool {
+      return a.mask ? k < 32 * a.mask_words && (a.mask[static_cast<long long>(r) * a.mask_words + (k >> 5)] >> (k & 31) & 1u)
+                    : k <= r - begin;
     };
+    auto drafted = [&](int r, int begin, int k) -> int { return on_way(r, begin, k) ? local(a.draft[begin + k]) : -1; };
+    // tokens of the request's text, as far as its arguments go
+    auto text_len = [&](int s) -> long long { return a.tokens ? max(static_cast<long long>(a.tokens_len[s]) + a.tokens_base, 0ll) : 0; };
     auto drafts = [&](int s, int* begin) -> int {  // how many rows the request has, and its first
       *begin = a.row_start[s];
       return *begin < 0 ? 0 : min(kLaDraftMax, min(a.row_start[s + 1], a.rows) - *begin);
@@ -180,10 +182,26 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
       const bool live = s >= 0 && s < a.requests;
       for (int k = lane; k < parts; k += 32) s_quad[warp * parts + k] = 0;
       __syncwarp();
-      int listed = 0;
+      int listed = 0, prompt = 0;
       if (live && a.draft) {
         int begin;
         const int rows = drafts(s, &begin);
+        // drafted tokens on the way that are the prompt's: all in front of row `cut`
+        const long long left = a.prompt_len ? a.prompt_len[s] - text_len(s) : 0;
+        int cut = 0;
+        if (left > 0) {
+          long long before = 0;
+          cut = 0x7fffffff;
+          for (int k0 = 0; k0 < rows && before < left; k0 += 32) {
+            const bool on = k0 + lane < rows && on_way(r, begin, k0 + lane);
+            const unsigned way = __ballot_sync(0xffffffffu, on);
+            if (before + __popc(way) >= left) {  // the one with number `left` is in this word
+              const unsigned last = __ballot_sync(0xffffffffu, on && before + __popc(way & ((2u << lane) - 1u)) == left);
+              cut = k0 + __ffs(last);
+            }
+            before += __popc(way);
+          }
+        }
         for (int k0 = 0; k0 < rows; k0 += 32) {
           const int t = k0 + lane < rows ? drafted(r, begin, k0 + lane) : -1;
           const unsigned hit = __ballot_sync(0xffffffffu, t >= 0);
@@ -193,7 +211,9 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
             atomicOr(s_quad + warp * parts + (t >> 7), 1u << (t >> 2 & 31));
           }
           listed += __popc(hit);
+          if (k0 < cut) prompt += __popc(cut - k0 < 32 ? hit & ((1u << (cut - k0)) - 1u) : hit);
         }
+        if (listed > kLaDrafts) prompt = cut;
         if (listed > kLaDrafts) {
           __syncwarp();
           for (int k = lane; k < parts; k += 32) s_quad[warp * parts + k] = 0;
@@ -204,6 +224,7 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
         x.s = live ? s : -1;
         x.allowed = -1;
         x.listed = listed;
+        s_prompt[warp] = prompt;
         x.rep = live && a.rep ? a.rep[s] : 1.f;
         x.freq = live && a.freq ? a.freq[s] : 0.f;
         x.pres = live && a.pres ? a.pres[s] : 0.f;
@@ -237,8 +258,7 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
         __syncthreads();
         if (a.tokens) {
           const int32_t* text = a.tokens + a.tokens_stride * s;
-          const long long len = static_cast<long long>(a.tokens_len[s]) + a.tokens_base;
-          const int held = static_cast<int>(min(max(len, 0ll), min(static_cast<long long>(kLaTextMax), a.tokens_stride)));
+          const int held = static_cast<int>(min(text_len(s), min(static_cast<long long>(kLaTextMax), a.tokens_stride)));
           const int prompt = a.prompt_len ? a.prompt_len[s] : 0;
 #pragma unroll 4
           for (int k = tid; k < held; k += kLaThreads) {
@@ -267,19 +287,22 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
         built = s;
       }
       // more drafted tokens than a list holds go into the words and leave them again
-      auto count = [&](uint32_t d) {
+      auto count = [&](bool in) {
         int begin;
         const int rows = drafts(s, &begin);
         __syncthreads();
         for (int k = tid; k < rows; k += kLaThreads) {
           const int t = drafted(r, begin, k);
-          if (t >= 0) touch(t, atomicAdd(s_word + t, d));
+          if (t < 0) continue;
+          const uint32_t bit = 1u << 30;
+          const uint32_t old = k >= s_prompt[i] ? atomicAdd(s_word + t, in ? 1u : 0xFFFFFFFFu) : in ? atomicOr(s_word + t, bit) : atomicAnd(s_word + t, ~bit);
+          if (in) touch(t, old);
         }
         __syncthreads();
       };
       const bool spill = row.listed > kLaDrafts;
       const int listed = spill ? 0 : row.listed;
-      if (spill) count(1u);
+      if (spill) count(true);
       const uint32_t* ok = row.allowed >= 0 ? a.allowed + a.allowed_stride * row.allowed : nullptr;
       const XT* x = static_cast<const XT*>(a.x) + a.x_stride * r;
       YT* y = a.y ? static_cast<YT*>(a.y) + a.y_stride * r : nullptr;
@@ -354,7 +377,7 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
         in.load(x + v, 1);
         float e = in.get(0);
         const uint32_t b = w >> 20 & 1023u;
-        if (times || w >> 31) e = e > 0.f ? __fdiv_rn(e, row.rep) : __fmul_rn(e, row.rep);
+        if (times || w >> 30) e = e > 0.f ? __fdiv_rn(e, row.rep) : __fmul_rn(e, row.rep);
         if (times) e = __fsub_rn(__fsub_rn(e, __fmul_rn(row.freq, static_cast<float>(times))), row.pres);
         if (b) e = __fadd_rn(e, a.bias[static_cast<long long>(a.bias_stride) * s + b - 1]);
         if (ok && !(ok[v >> 5] >> (v & 31) & 1u)) e = -INFINITY;
@@ -379,13 +402,14 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
       }
       for (int k = tid; k < listed; k += kLaThreads) {
         const int t = s_draft[i][k];
-        uint32_t times = s_word[t] & 0xFFFFFu;
+        uint32_t w = s_word[t], times = w & 0xFFFFFu;
         bool first = true;
         for (int d = 0; d < listed; ++d) {
-          times += s_draft[i][d] == t;
+          times += s_draft[i][d] == t && d >= s_prompt[i];
           first = first && (d >= k || s_draft[i][d] != t);
         }
-        if (first) rules(t, s_word[t], times);
+        if (k < s_prompt[i]) w |= 1u << 30;  // (the first of equal ones stands for all)
+        if (first) rules(t, w, times);
       }
       if (a.next) {
         unsigned long long key =
@@ -397,7 +421,7 @@ __global__ void __launch_bounds__(kLaThreads, 2) logits_adjust_kernel(const LaAr
         }
         if (lane == 0 && key) atomicMax(s_best + i, key);
       }
-      if (spill) count(0xFFFFFFFFu);
+      if (spill) count(false);
     }
     __syncthreads();
   }
