@@ -718,7 +718,8 @@ dec_status step_slots(const step_slots_args* a, void* stream);
  * page * page_size + row in the page. A padded row (positions[r] < 0) stores
  * nothing and leaves its q_out as it was; a slot of -1 stores nothing; one outside
  * the pool counts as a bad page, and its q_out is written. Two rows of one slot
- * leave a mixture of both there. */
+ * leave a mixture of both there. Outputs must not overlap inputs (q_out may be q
+ * itself; columns of one buffer do not overlap) or each other. */
 typedef struct {
   int32_t rows, n_q, n_kv, head_dim; /* n_q may be 0 */
   int32_t xdtype, ydtype, kvdtype;   /* q, k, v; q_out; pages */
@@ -850,7 +851,8 @@ dec_status logits_adjust(const logits_adjust_args* a, void* stream);
  * accepted row outside the pool or the table sets DEC_DEVERR_BAD_PAGE and that row is
  * not moved; a place outside tokens_stride is not written and sets
  * DEC_DEVERR_BAD_POSITION. layers may be 0 (nothing moves; no pools). path_stride up
- * to 256. Outputs must not overlap inputs (tokens apart) or each other. */
+ * to 256. Outputs, the pools among them, must not overlap inputs (tokens apart) or
+ * each other. */
 typedef struct {
   int32_t batch, rows, path_stride;
   int32_t layers, n_kv, head_dim, kvdtype;

@@ -339,6 +339,84 @@ def test_refusals_of_outputs_over_other_arguments(W, call):
                 assert e.value.status == 1 and call in str(e.value), (o, other)
 
 
+@pytest.fixture(scope="module")
+def series(tmp_path_factory):
+    """csrc/spans.h compiled as plain C++: whether two series of spans meet."""
+    cxx = shutil.which("g++") or shutil.which("c++")
+    if not cxx:
+        pytest.skip("no C++ compiler")
+    d = tmp_path_factory.mktemp("spans")
+    (d / "s.cpp").write_text('#include "spans.h"\nusing namespace wsg;\nextern "C" {\n'
+                             "int meet(size_t p, size_t a, long long n, long long s, size_t q, size_t b, long long m, long long t) {\n"
+                             "  return series_meet(Spans{{(void*)p, a}, n, s}, Spans{{(void*)q, b}, m, t}); }\n"
+                             "size_t pool(long long pages, long long page) { return span_pool((void*)16, pages, page).bytes; }\n}\n")
+    inc = os.path.join(ROOT, "weight_streaming_gemv_token_gb300", "csrc")
+    subprocess.run([cxx, "-std=c++17", "-O1", "-shared", "-fPIC", "-I", inc, str(d / "s.cpp"), "-o", str(d / "s.so")], check=True)
+    L, q, z = ctypes.CDLL(str(d / "s.so")), ctypes.c_longlong, ctypes.c_size_t
+    L.meet.argtypes, L.pool.argtypes, L.pool.restype = [z, z, q, q, z, z, q, q], [q, q], z
+    return L
+
+
+def test_series_of_spans(series):
+    """Against the bytes themselves: equal strides exactly, other strides by what each covers as a whole."""
+    rng = np.random.default_rng(0)
+    seen = set()
+    for _ in range(4000):
+        n, m = (int(x) for x in rng.integers(1, 6, 2))
+        s = int(rng.integers(1, 40))
+        t = s if rng.random() < 0.7 else int(rng.integers(1, 40))
+        a, b = int(rng.integers(1, s + 6)), int(rng.integers(1, t + 6))
+        p, q = (int(x) for x in rng.integers(1000, 1300, 2))
+        x, y = ({p0 + i * st + k for i in range(c) for k in range(w)} for p0, w, c, st in ((p, a, n, s), (q, b, m, t)))
+        got = bool(series.meet(p, a, n, s, q, b, m, t))
+        if s == t or n == 1 or m == 1:
+            assert got == bool(x & y), (p, a, n, s, q, b, m, t)
+        else:
+            assert got == (p <= max(y) and q <= max(x))
+        seen.add((got, s == t))
+    assert len(seen) == 4
+    assert not series.meet(0, 8, 2, 8, 0, 8, 2, 8) and not series.meet(100, 0, 2, 8, 100, 8, 1, 8)
+    assert series.meet(100, 8, 4, 0, 104, 8, 1, 0)
+    big = 1 << 62
+    assert series.pool(2**31 - 1, 16384 * 1024 * 128 * 4) == big and series.pool(3, 10) == 30 and series.pool(0, 10) == 0
+    assert series.meet(1 << 40, big, 1, 0, 3 << 50, 4, 1, 0) and not series.meet(1 << 40, big, 1, 0, (1 << 40) - 4, 4, 1, 0)
+
+
+def test_refusals_of_outputs_over_caches(W):
+    """An output over the prefix or a pool; a pool over another argument of the calls that write it."""
+    bf, pool = 2 * 16 * 16 * 2, 8 * 2 * 16 * 16 * 2  # a page, a pool
+    for o in ("out", "lse", "d_workspace"):
+        for name, size in (("prefix_k", 2 * 8 * 16 * 2), ("prefix_v", 2 * 8 * 16 * 2), ("k_pages", pool), ("v_pages", pool)):
+            for at in (0, (size - 1) // 256 * 256):
+                with pytest.raises(W.WsgError, match="attn_tree_paged: an output overlaps") as e:
+                    W.attn_tree_paged(W.attn_tree_args(**{**ATTN, o: ATTN[name] + at}))
+                assert e.value.status == 1
+    apart = places(*[n for n in APPEND if APPEND[n] == P])
+    good = {**APPEND, **apart}
+    inputs = ("q", "k", "v", "g_q", "g_k", "positions", "inv_freq", "slots")
+    for o, size in (("k_pages", pool), ("v_pages", pool), ("q_out", 64 * 4 * 4)):
+        for other in inputs + tuple(x for x in ("k_pages", "v_pages", "q_out") if x != o):
+            kw = {**good, other: good[o] + size - 16}  # its first bytes are the output's last
+            if o == "q_out" and other.endswith("pages"):
+                kw = {**good, "q_out": good[other] + pool - 16}
+            with pytest.raises(W.WsgError, match="kv_append_slots: an output overlaps") as e:
+                W.kv_append_slots(W.kv_slots_args(**kw))
+            assert e.value.status == 1, (o, other)
+    # one row of queries in place reaches into the keys beside it
+    with pytest.raises(W.WsgError, match="kv_append_slots: an output overlaps"):
+        W.kv_append_slots(W.kv_slots_args(**{**good, "q_out": good["q"], "k": good["q"] + 63 * 4, "q_stride": 96, "k_stride": 96, "q_out_stride": 96}))
+    layers = 2 * pool
+    for o in ("count", "new_len", "path", "out_tokens", "tokens", "row_start", "parents", "draft_tokens", "next", "seq_len", "held", "page_table"):
+        for name in ("k_pages", "v_pages"):
+            for at in (0, pool, layers - 4):
+                with pytest.raises(W.WsgError, match="tree_accept_paged: a pool overlaps") as e:
+                    W.tree_accept_paged(W.tree_accept_args(**{**ACCEPT, o: ACCEPT[name] + at}))
+                assert e.value.status == 1, (o, name, at)
+    for at in (0, pool, layers - bf):
+        with pytest.raises(W.WsgError, match="tree_accept_paged: a pool overlaps"):
+            W.tree_accept_paged(W.tree_accept_args(**{**ACCEPT, "v_pages": ACCEPT["k_pages"] + at}))
+
+
 def test_refusals_of_rows_that_move_in_place(W):
     for change in ({"out_stride": 72}, {"q_stride": 0}, {"q_stride": 128}):
         with pytest.raises(W.WsgError, match="attn_tree_paged: out over q needs") as e:

@@ -270,6 +270,50 @@ def test_kv_append_slots_is_the_append_by_tables(c):
         assert torch.equal(p, want)
 
 
+@pytest.mark.parametrize("x,kv,d", [("bf16", "bf16", 128), ("f32", "bf16", 40)])
+def test_kv_append_slots_in_place_in_a_fused_buffer(x, kv, d):
+    """Queries over themselves, keys and values the columns beside them: the bits of a call with buffers of its own."""
+    import torch
+
+    W = lib()
+    rows, n_q, n_kv, page = 37, 4, 2, 16
+    wide = (n_q + 2 * n_kv) * d
+    qkv = rand((rows, wide), x, 1)
+    freq, factor = W.rope_frequencies(d, 1e4)
+    kw = dict(rows=rows, n_q=n_q, n_kv=n_kv, head_dim=d, xdtype=code(W, x), ydtype=code(W, x), kvdtype=code(W, kv), q_stride=wide,
+              k_stride=wide, v_stride=wide, g_q=rand((d,), "f32", 2), g_k=rand((d,), "f32", 3), positions=ints(np.arange(rows) * 7),
+              inv_freq=torch.tensor(freq, dtype=torch.float64, device="cuda"), eps=1e-6, rope_factor=factor, rot_dim=d, interleaved=0,
+              slots=torch.arange(rows, device="cuda").flip(0) + 5, num_pages=4, page_size=page)
+    pools, own = torch.zeros((2, 4, n_kv, page, d), device="cuda").to(tdt(kv)), torch.zeros((2, 4, n_kv, page, d), device="cuda").to(tdt(kv))
+    q_out = torch.zeros((rows, n_q * d), dtype=tdt(x), device="cuda")
+    cols = [qkv, qkv[:, n_q * d:], qkv[:, (n_q + n_kv) * d:]]
+    W.kv_append_slots(W.kv_slots_args(q=cols[0], k=cols[1], v=cols[2], q_out=q_out, q_out_stride=n_q * d, k_pages=pools[0], v_pages=pools[1], **kw))
+    keep = qkv.clone()
+    W.kv_append_slots(W.kv_slots_args(q=cols[0], k=cols[1], v=cols[2], q_out=qkv, q_out_stride=wide, k_pages=own[0], v_pages=own[1], **kw))
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    assert torch.equal(qkv[:, : n_q * d], q_out) and torch.equal(pools, own) and torch.equal(qkv[:, n_q * d:], keep[:, n_q * d:])
+
+
+@pytest.mark.parametrize("kv", ["bf16", "f32"])
+def test_tree_accept_paged_of_keys_and_values_that_alternate(kv):
+    """One buffer with every layer's keys in front of its values: the pools' layers lie between each other."""
+    import torch
+
+    W = lib()
+    rows, lens, page = [9, 12], [5, 17], 4
+    a, t = accept_case(W, rows, lens, 3, 2, 16, page, kv, 8, seed=2)
+    both = torch.stack(t["pools"], 1).contiguous()  # [layer][keys, values][pages]..
+    t["pools"] = [both[:, 0], both[:, 1]]
+    a.set("k_pages", t["pools"][0]).set("v_pages", t["pools"][1])
+    a.layer_stride = both.stride(0)
+    W.gemv_device_errors()
+    W.tree_accept_paged(a)
+    torch.cuda.synchronize()
+    assert W.gemv_device_errors() == 0
+    assert check_accept(t, rows, lens, page, 8) > 1
+
+
 def test_kv_append_slots_outside_the_pool():
     import torch
 

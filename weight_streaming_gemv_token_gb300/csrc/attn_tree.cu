@@ -188,9 +188,15 @@ extern "C" dec_status attn_tree_paged(const attn_tree_args* a, void* stream) {
     return fail(nullptr, DEC_EINVAL, "attn_tree_paged: out over q needs q's stride");
   const size_t qe = elem_bytes(a->qdtype), rows = a->rows, batch = a->batch;
   const Span q = span_rows(a->out == a->q ? nullptr : a->q, a->rows, a->q_stride, width, qe);
+  const long long key = static_cast<long long>(elem_bytes(a->kvdtype)) * a->head_dim;
+  auto prefix = [&](const void* p) {
+    return span_rows(a->prefix_len > 0 ? p : nullptr, a->n_kv, a->prefix_stride * a->head_dim,
+                     static_cast<long long>(a->prefix_len) * a->head_dim, elem_bytes(a->kvdtype));
+  };
+  auto pool = [&](const void* p) { return span_pool(pages ? p : nullptr, a->num_pages, key * a->n_kv * a->page_size); };
   if (outputs_meet({span_rows(a->out, a->rows, a->out_stride, width, qe), {a->lse, 4 * rows * a->n_q},
                     {a->d_workspace, a->workspace_bytes}},
-                   {q, {a->row_start, 4 * (batch + 1)}, {a->mask, 4 * rows * a->mask_words}, {a->seq_len, 4 * batch},
+                   {q, prefix(a->prefix_k), prefix(a->prefix_v), pool(a->k_pages), pool(a->v_pages), {a->row_start, 4 * (batch + 1)}, {a->mask, 4 * rows * a->mask_words}, {a->seq_len, 4 * batch},
                     {pages ? a->page_table : nullptr, 4 * batch * a->table_stride}}))
     return fail(nullptr, DEC_EINVAL, "attn_tree_paged: an output overlaps another argument");
   DeviceInfo di;

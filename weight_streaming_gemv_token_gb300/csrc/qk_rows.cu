@@ -25,6 +25,7 @@
 #include "common.h"
 #include "paging.h"
 #include "ptx.cuh"
+#include "spans.h"
 
 namespace wsg {
 namespace {
@@ -573,9 +574,39 @@ extern "C" dec_status qk_norm_rope(const qk_rope_args* a, void* stream) {
 
 namespace {
 
-// The checks and fields of both appends but those of the way to the pages.
+// Whether an output of kv_append_slots meets another argument: columns of one buffer (queries in
+// place, keys and values beside them) do not.
+bool slots_overlap(const kv_slots_args* a) {
+  const long long row = static_cast<long long>(a->n_kv) * a->head_dim;
+  auto rows = [&](const void* p, int heads, int64_t stride, int dtype) {
+    const long long e = elem_bytes(dtype);
+    return Spans{{p, static_cast<size_t>(heads * e * a->head_dim)}, a->rows, stride * e};
+  };
+  auto one = [](const void* p, size_t bytes) { return Spans{{p, bytes}, 1, 0}; };
+  const Span pages = span_pool(a->k_pages, a->num_pages, row * a->page_size * static_cast<long long>(elem_bytes(a->kvdtype)));
+  const Spans outs[] = {one(a->k_pages, pages.bytes), one(a->v_pages, pages.bytes),
+                        rows(a->n_q > 0 ? a->q_out : nullptr, a->n_q, a->q_out_stride, a->ydtype)};
+  const Spans ins[] = {rows(a->n_q > 0 && a->q != a->q_out ? a->q : nullptr, a->n_q, a->q_stride, a->xdtype),
+                       rows(a->k, a->n_kv, a->k_stride, a->xdtype),
+                       rows(a->v, a->n_kv, a->v_stride, a->xdtype),
+                       one(a->g_q, a->n_q > 0 ? 4 * static_cast<size_t>(a->head_dim) : 0),
+                       one(a->g_k, 4 * static_cast<size_t>(a->head_dim)),
+                       one(a->positions, 4 * static_cast<size_t>(a->rows)),
+                       one(a->inv_freq, 8 * static_cast<size_t>(a->rot_dim / 2)),
+                       one(a->slots, 8 * static_cast<size_t>(a->rows))};
+  if (series_meet(outs[0], outs[1])) return true;
+  for (const Spans& i : ins)
+    for (const Spans& o : outs)
+      if (series_meet(o, i)) return true;
+  for (int i = 0; i < 2; ++i)
+    if (series_meet(outs[i], outs[2])) return true;
+  return false;
+}
+
+// The checks and fields of both appends but those of the way to the pages; `overlap`: whether an
+// output meets another argument.
 template <typename A>
-dec_status append_fields(const A* a, const char* who, QkRowsArgs* k, DeviceInfo* di) {
+dec_status append_fields(const A* a, const char* who, QkRowsArgs* k, DeviceInfo* di, bool (*overlap)(const A*) = nullptr) {
   dec_status s = check_rows(a, who);
   if (s != DEC_OK) return s;
   if (a->n_kv < 1) return fail(nullptr, DEC_EINVAL, "%s: n_kv must be >= 1", who);
@@ -592,6 +623,7 @@ dec_status append_fields(const A* a, const char* who, QkRowsArgs* k, DeviceInfo*
     return fail(nullptr, DEC_EINVAL, "%s: a pointer is not aligned to its elements", who);
   if (a->n_q > 0 && !in_place_ok(a->q, a->q_out, a->rows, a->xdtype, a->ydtype, a->q_stride, a->q_out_stride))
     return fail(nullptr, DEC_EINVAL, "%s: q_out over q needs q's type and stride", who);
+  if (overlap && overlap(a)) return fail(nullptr, DEC_EINVAL, "%s: an output overlaps another argument", who);
   if ((s = device_info(di, nullptr)) != DEC_OK) return s;
   *k = shared_fields(a);
   k->v = a->v;
@@ -634,7 +666,7 @@ extern "C" dec_status kv_append_slots(const kv_slots_args* a, void* stream) {
     return fail(nullptr, DEC_EINVAL, "kv_append_slots: a pointer is not aligned to its elements");
   QkRowsArgs k{};
   DeviceInfo di;
-  const dec_status s = append_fields(a, "kv_append_slots", &k, &di);
+  const dec_status s = append_fields(a, "kv_append_slots", &k, &di, slots_overlap);
   if (s != DEC_OK || a->rows == 0) return s;
   k.pool = PagePool{a->num_pages, a->n_kv, page_shift(a->page_size), 0};
   k.slots = a->slots;

@@ -200,6 +200,17 @@ extern "C" dec_status tree_accept_paged(const tree_accept_args* a, void* stream)
                    {{a->row_start, 4 * (b + 1)}, {a->parents, 4 * r}, {a->draft_tokens, 4 * r}, {a->next, 4 * r},
                     {a->seq_len, 4 * b}, {a->held, 4 * b}, {a->page_table, 4 * b * width}}))
     return fail(nullptr, DEC_EINVAL, "tree_accept_paged: an output overlaps another argument");
+  if (a->layers > 0) {  // the pools are written too; other arguments may lie between layers
+    const Span one = span_pool(a->k_pages, a->num_pages, static_cast<long long>(a->n_kv) * a->page_size * a->head_dim * elem);
+    const Spans k{one, a->layers, a->layer_stride * elem}, v{{a->v_pages, one.bytes}, a->layers, a->layer_stride * elem};
+    bool meet = series_meet(k, v);
+    for (const Span& s : {Span{a->count, 4 * b}, {a->new_len, 4 * b}, {a->path, 4 * b * a->path_stride}, {a->out_tokens, 4 * b * a->path_stride},
+                          {a->tokens, 4 * b * static_cast<size_t>(a->tokens ? a->tokens_stride : 0)}, {a->row_start, 4 * (b + 1)},
+                          {a->parents, 4 * r}, {a->draft_tokens, 4 * r}, {a->next, 4 * r}, {a->seq_len, 4 * b}, {a->held, 4 * b},
+                          {a->page_table, 4 * b * width}})
+      meet = meet || series_meet(k, Spans{s, 1, 0}) || series_meet(v, Spans{s, 1, 0});
+    if (meet) return fail(nullptr, DEC_EINVAL, "tree_accept_paged: a pool overlaps another argument");
+  }
   DeviceInfo di;
   const dec_status st = device_info(&di, nullptr);
   if (st != DEC_OK) return st;
