@@ -750,7 +750,8 @@ dec_status kv_append_slots(const kv_slots_args* a, void* stream);
  * used. row_start must not fall and lie in 0 .. rows (it is taken as if it did).
  * An index beyond table_stride * page_size counts as a bad page; its keys are left
  * out. Sizes, precision, order of results and the other rules are those of
- * attn_shared_prefix, with rows * n_q < 2^24 and batch <= 4096. Matrix instructions cut
+ * attn_shared_prefix, with rows * n_q < 2^24, batch <= 4096 and (rows * n_q / 16 +
+ * min(batch, rows) * n_kv) * (table_stride * page_size / 128 + 2) < 2^37. Matrix instructions cut
  * sums off instead of rounding them: at most 128 of one sum in a row, then it is added to a
  * total in float32, so what is lost does not grow with the length. The work is cut up on
  * the device by the requests' lengths, equal shares of key tiles for all SMs. */

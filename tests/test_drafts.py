@@ -152,6 +152,42 @@ def test_pieces_have_numbers_of_their_own_inside_the_workspace(W, host):
         assert p["ml"] % 256 == p["rec"] % 256 == p["line"] % 256 == 0
 
 
+def test_sizes_whose_work_cannot_be_counted(W, host):
+    """Sizes under which requests could have 2^37 units of work (a tile of 128 keys against a row tile of 16) are refused; under
+    all others their number fits, however rows and tokens fall on the requests."""
+    good = dict(batch=1, rows=1, n_q=1, n_kv=1, head_dim=64, qdtype=0, kvdtype=0, q=P, out=P, q_stride=64, out_stride=64, row_start=P,
+                k_pages=P, v_pages=P, page_table=P, seq_len=P, num_pages=1, page_size=1024, table_stride=1, scale=1.0,
+                d_workspace=P << 8, workspace_bytes=1 << 60)
+    out = (ctypes.c_longlong * len(NAMES))()
+
+    def ok(**kw):
+        return host.plan(ctypes.byref(W.attn_tree_args(**{**good, **kw})), out) == 1
+
+    full = dict(table_stride=1 << 20)  # 2^30 tokens, 2^23 tiles
+    assert ok(rows=1, **full) and ok(rows=(1 << 18) - 64, **full) and not ok(rows=(1 << 18), **full)
+    assert ok(batch=4096, rows=4096, n_q=3, n_kv=3, **full) and not ok(batch=4096, rows=4096, n_q=4, n_kv=4, **full)
+    assert ok(batch=4096, rows=(1 << 20) - 1, n_q=16, n_kv=16, table_stride=8) and not ok(batch=4096, rows=(1 << 20) - 1, n_q=16, table_stride=1 << 20)
+    kw = {**good, "batch": 4096, "rows": 4096, "n_q": 4, "n_kv": 4, "q_stride": 256, "out_stride": 256, **full}
+    with pytest.raises(W.WsgError, match="attn_tree_paged") as e:
+        W.attn_tree_paged(W.attn_tree_args(**kw))
+    assert e.value.status == 1
+    rng = np.random.default_rng(1)
+    most = 0
+    for _ in range(3000):
+        n_kv, group = 1 << int(rng.integers(0, 8)), int(rng.integers(1, 17))
+        rows, batch = int(2 ** rng.uniform(0, 24)), int(2 ** rng.uniform(0, 12))
+        width = int(2 ** rng.uniform(0, 20))
+        if rows * n_kv * group >= 1 << 24 or not ok(batch=batch, rows=rows, n_q=n_kv * group, n_kv=n_kv, table_stride=width):
+            continue
+        tiles = lambda r: -(-r * group // 16)
+        k = min(batch, rows)  # requests of one row and the rest in one, or shared out
+        for shares in ([1] * (k - 1) + [rows - k + 1], [rows // k + (i < rows % k) for i in range(k)]):
+            units = n_kv * sum(tiles(r) for r in shares) * (-(-width * 1024 // 128) + host.extra())
+            most = max(most, units)
+            assert units < 1 << 37
+    assert most > 1 << 36
+
+
 def test_spans(host):
     assert host.meet(100, 10, 109, 5) and host.meet(109, 5, 100, 10) and host.meet(100, 10, 100, 1)
     assert not host.meet(100, 10, 110, 5) and not host.meet(110, 5, 100, 10)

@@ -132,9 +132,9 @@ struct AtWalk {
 };
 
 // The requests' sums as one warp forms them, a run of requests a lane: units << 26 |
-// segments of all requests (at most n_kv times the rows and 2^24 / 16 of those; 2^37 units
-// are hours of work), of those before this lane's, and this lane's first request. Row
-// starts that fall are lifted to the highest before.
+// segments of all requests (at most n_kv times the rows and 2^24 / 16 of those; fewer than
+// 2^37 units, or the sizes are refused), of those before this lane's, and this lane's first
+// request. Row starts that fall are lifted to the highest before.
 struct AtSums {
   int lo, hi;          // this lane's requests
   int from, rows, len; // the first one's first row, rows, tokens

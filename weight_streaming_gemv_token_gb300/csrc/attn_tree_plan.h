@@ -21,6 +21,7 @@ namespace wsg {
 
 constexpr int kAtBatch = 4096, kAtKeyShift = 7, kAtKeys = 1 << kAtKeyShift;  // requests; keys a tile
 constexpr int kAtExtra = 2;
+constexpr long long kAtUnits = 1ll << 37;  // of all requests: what their sums hold (AtSums)
 
 // What the cutting goes by. rows * group < 2^24, capacity <= 2^30: 32-bit arithmetic.
 struct AtCut {
@@ -77,6 +78,14 @@ WSG_HD int at_owner(const AtShares& s, long long p) {
   return static_cast<int>(p < big ? at_div(p, s.each + 1) : s.more + at_div(p - big, s.each));
 }
 
+// Most units that requests can have at these sizes, rows in row tiles of 16 and tables full: a
+// request's row tiles are its rows * group / 16 and one more.
+inline long long at_most_units(const attn_tree_args* a) {
+  const long long tiles = ((static_cast<long long>(a->table_stride) << page_shift(a->page_size)) + kAtKeys - 1) / kAtKeys;
+  return (static_cast<long long>(a->rows) * a->n_q / 16 + static_cast<long long>(a->batch < a->rows ? a->batch : a->rows) * a->n_kv) *
+         ((tiles < 1 ? 1 : tiles) + kAtExtra);
+}
+
 inline bool attn_tree_sizes_ok(const attn_tree_args* a) {
   auto type = [](int t) { return t == DEC_F32 || t == DEC_BF16; };
   return a->batch >= 0 && a->batch <= kAtBatch && a->rows >= 0 && a->n_kv >= 1 && a->n_q >= a->n_kv && a->n_q <= 65535 &&
@@ -84,7 +93,8 @@ inline bool attn_tree_sizes_ok(const attn_tree_args* a) {
          a->head_dim >= 8 && a->head_dim <= 128 && a->head_dim % 8 == 0 && type(a->qdtype) && type(a->kvdtype) &&
          a->prefix_len >= 0 && page_shift(a->page_size) >= 0 && a->num_pages >= 0 && a->table_stride >= 0 &&
          a->mask_words >= 0 && a->mask_words <= 1 << 20 &&
-         (static_cast<long long>(a->table_stride) << page_shift(a->page_size)) + a->prefix_len <= (1ll << 30);
+         (static_cast<long long>(a->table_stride) << page_shift(a->page_size)) + a->prefix_len <= (1ll << 30) &&
+         at_most_units(a) < kAtUnits;
 }
 
 // Which kernel runs, and the workspace.
