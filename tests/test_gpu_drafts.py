@@ -759,6 +759,34 @@ def test_attn_tree_paged_row_starts_that_fall(types, full):
     assert good is not None
 
 
+@pytest.mark.parametrize("types,d,plen", [(("bf16", "bf16"), 128, 0), (("bf16", "bf16"), 128, 40), (("bf16", "bf16"), 96, 0), (("f32", "f32"), 64, 0),
+                                          (("f32", "bf16"), 128, 300)], ids=str)
+@pytest.mark.parametrize("batch,R", [(3, 40), (33, 6), (70, 9), (300, 3)])
+def test_attn_tree_paged_row_starts_that_fall_are_the_highest_so_far(batch, R, types, d, plen):
+    """Starts that fall or lie outside the rows: the bits of a call whose starts are the highest so far."""
+    import torch
+
+    W = lib()
+    rng = np.random.default_rng(batch + plen)
+    lens = rng.integers(-1, 200, batch).tolist()
+    a, t = tree_case(W, [R] * batch, 4, 2, d, plen, lens, 16, *types, mask="random", poison=False, seed=batch)
+    total = batch * R
+    rises = np.arange(batch + 1) * R
+    for k in range(4):
+        starts = rises.copy()
+        at = rng.permutation(batch + 1)[: max(1, (batch + 1) // (1, 2, 4, 12)[k])]
+        starts[at] = rng.integers(-R, total + R, len(at)) if k % 2 else rng.choice([-2**31, 2**31 - 1, 0, total, 5], len(at), p=[0.4, 0.1, 0.2, 0.1, 0.2])
+        got = []
+        for x in (starts, np.maximum.accumulate(np.clip(starts, 0, total))):
+            a.set("row_start", ints(x))
+            t["out"].fill_(7.0), t["lse"].fill_(7.0)
+            W.gemv_device_errors()
+            W.attn_tree_paged(a)
+            torch.cuda.synchronize()
+            got.append([t["out"].clone(), t["lse"].clone(), W.gemv_device_errors()])
+        assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1]) and got[0][2] == got[1][2], (k, starts)
+
+
 def test_attn_tree_paged_many_requests():
     """More requests than threads of a CTA, most of them without rows."""
     import torch
