@@ -64,7 +64,7 @@ typedef enum { DEC_F32 = 0, DEC_BF16 = 1, DEC_Q4G64 = 2 } dec_dtype;
 #define DEC_DEVERR_BAD_TOKEN 0x4u    /* a token ID outside [0, vocab) was read as 0 */
 #define DEC_DEVERR_BAD_POSITION 0x8u /* a position reached the KV capacity; the step did nothing */
 #define DEC_DEVERR_EXCHANGE_TIMEOUT 0x10u /* persistent engine: a wait for another CTA's words gave up */
-#define DEC_DEVERR_GEMM_TIMEOUT 0x20u     /* chunked prefill, attn_shared_prefix: a tensor-core pipeline wait gave up */
+#define DEC_DEVERR_GEMM_TIMEOUT 0x20u     /* chunked prefill, attn_shared_prefix, attn_tree_paged: a tensor-core pipeline wait gave up */
 #define DEC_DEVERR_BARRIER_TIMEOUT 0x40u  /* persistent 4-bit engine: a grid barrier gave up (dec_reset clears it) */
 #define DEC_DEVERR_BAD_PAGE 0x80u         /* a sequence, page or parent index of the paged calls was out of range */
 #define DEC_DEVERR_BAD_TREE 0x100u        /* a drafted row's parent is not an earlier row of its request, or a tree has more rows than its mask */

@@ -378,7 +378,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       }
     }
     if (!ok && lane == 0) fail();
-    if (who == 0 && p.prefix_tiles == 0) at_seams(p, walk);
+    if (who == 0 && p.prefix_tiles == 0) {
+      if (!ok) {  // the share's records all the same, for the join: nothing of its cut segment
+        while (walk.next(p).tiles > 0) {
+        }
+        walk.seam_seg = -1;
+        walk.seam = AtSeam{};
+      }
+      at_seams(p, walk);
+    }
     // the last copies into each stage have landed before the CTA may end; after a failure a loader first
     // arrives for the tiles (STAGES at most) that it did not come to and another did
     if (lane == 0) s_put[who][0] = keys, s_put[who][1] = values;
@@ -391,7 +399,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         uint64_t* full = w ? v_full : k_full;
         for (int i = s_put[who][w]; i < top; ++i) mbar_arrive(&full[i % STAGES]);
         for (int s = 0; s < STAGES; ++s)
-          if (who == 0 && s < top && !mbar_wait(&full[s], ((top - 1 - s) / STAGES) & 1)) fail();
+          if (who == 0 && s < top && !mbar_wait(&full[s], ((top - 1 - s) / STAGES) & 1, kLandLimitNs)) fail();
       }
     }
   } else if (warp == 1) {
@@ -454,7 +462,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       if (!ok) fail();
       if (issued) {  // every MMA of this thread is done before tensor memory is freed
         tc_commit(&drain);
-        if (!mbar_wait(&drain, 0)) fail();
+        if (!mbar_wait(&drain, 0, kLandLimitNs)) fail();
       }
     }
   } else {

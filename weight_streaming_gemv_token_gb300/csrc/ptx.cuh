@@ -11,6 +11,9 @@
 #ifndef WSG_WAIT_LIMIT_NS
 #define WSG_WAIT_LIMIT_NS 2000000000ull  // 2 s
 #endif
+#ifndef WSG_WAIT_TRIES
+#define WSG_WAIT_TRIES 64  // between two looks at the clock
+#endif
 
 namespace wsg {
 
@@ -85,14 +88,17 @@ __device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
   return ok != 0;
 }
 
+// The limit of a kernel's waits for its own copies and products in flight, with which it must not end.
+constexpr uint64_t kLandLimitNs = 2000000000ull;
+
 // Bounded wait for the given phase parity. Returns false on timeout.
-__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t phase) {
+__device__ __forceinline__ bool mbar_wait(uint64_t* bar, uint32_t phase, uint64_t limit_ns = WSG_WAIT_LIMIT_NS) {
   if (mbar_try_wait(bar, phase)) return true;
   const uint64_t t0 = globaltimer_ns();
   while (true) {
-    for (int i = 0; i < 64; ++i)
+    for (int i = 0; i < WSG_WAIT_TRIES; ++i)
       if (mbar_try_wait(bar, phase)) return true;
-    if (globaltimer_ns() - t0 > WSG_WAIT_LIMIT_NS) return false;
+    if (globaltimer_ns() - t0 > limit_ns) return false;
   }
 }
 
