@@ -691,11 +691,13 @@ dec_status beam_reorder_pages(const beam_reorder_args* a, void* stream);
  * requests that are not served and behind the last row. A row whose parent is not
  * an earlier row of its request (row 0's is not looked at), and rows below it,
  * have -1 and 0 too and set DEC_DEVERR_BAD_TREE; so does a request with more rows
- * than its mask has bits. Tables too narrow, rows past `rows`, an owned count
- * outside the table, pages out of range, a ring state outside the ring and more
- * returned pages than the ring has room for set DEC_DEVERR_BAD_PAGE; running out of
- * pages sets nothing. seq, positions, slots, mask and parents may be NULL (mask
- * without parents is a chain's). Up to 4096 requests, masks up to 8 words.
+ * than its mask has bits, or with parents and no mask more than 256 (such a prompt
+ * goes in a step of its own, without parents and mask). Tables too narrow, rows past
+ * `rows`, an owned count outside the table, pages out of range, a ring state outside
+ * the ring and more returned pages than the ring has room for set
+ * DEC_DEVERR_BAD_PAGE; running out of pages sets nothing. seq, positions, slots, mask
+ * and parents may be NULL (mask without parents is a chain's). Up to 4096 requests,
+ * masks up to 8 words.
  * Outputs must not overlap inputs or each other otherwise. */
 typedef struct {
   int32_t requests, rows;
@@ -751,10 +753,14 @@ dec_status kv_append_slots(const kv_slots_args* a, void* stream);
  * An index beyond table_stride * page_size counts as a bad page; its keys are left
  * out. Sizes, precision, order of results and the other rules are those of
  * attn_shared_prefix, with rows * n_q < 2^24, batch <= 4096 and (rows * n_q / 16 +
- * min(batch, rows) * n_kv) * (table_stride * page_size / 128 + 2) < 2^37. Matrix instructions cut
- * sums off instead of rounding them: at most 128 of one sum in a row, then it is added to a
- * total in float32, so what is lost does not grow with the length. The work is cut up on
- * the device by the requests' lengths, equal shares of key tiles for all SMs. */
+ * min(batch, rows) * n_kv) * (table_stride * page_size / 128 + 2) < 2^37. Matrix
+ * instructions cut sums off instead of rounding them: at most 128 of one sum in a
+ * row, then it is added to a total in float32, so what is lost does not grow with the
+ * length. The work is cut up on the device by the requests' lengths, equal shares of
+ * key tiles for all SMs; which kernel runs, and with it a result's last bits, goes by
+ * sizes that the host knows, the table's width among them, not the lengths: few rows
+ * of short requests take a quarter to a half longer with tables for some ten thousand
+ * tokens than with tables as wide as the requests. */
 typedef struct {
   int32_t batch, rows, n_q, n_kv, head_dim;
   int32_t qdtype, kvdtype;

@@ -356,6 +356,14 @@ __device__ __forceinline__ uint32_t at_seen(const AtArgs& a, int begin, int i, i
   return __funnelshift_r(lo, hi, j0 & 31);
 }
 
+__device__ __forceinline__ bool at_odd16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }  // a bfloat16 that is not finite
+// A pair of bfloat16 whose values that are not finite are 0.
+__device__ __forceinline__ uint32_t at_finite2(uint32_t p) {
+  if (at_odd16(p)) p &= 0xFFFF0000u;
+  if (at_odd16(p >> 16)) p &= 0xFFFFu;
+  return p;
+}
+
 // Elements e .. e + 3 of a row's result from its weighted sum x, reference m and sum l;
 // with e = 0 its log-sum.
 template <typename QT>

@@ -20,12 +20,6 @@
 
 namespace wsg {
 
-__device__ __forceinline__ bool at_odd16(uint32_t h) { return (h & 0x7F80u) == 0x7F80u; }  // a bfloat16 that is not finite
-__device__ __forceinline__ uint32_t at_finite2(uint32_t p) {  // such halves become 0
-  if (at_odd16(p)) p &= 0xFFFF0000u;
-  if (at_odd16(p >> 16)) p &= 0xFFFFu;
-  return p;
-}
 __device__ __forceinline__ bool at_odd(float x) { return (__float_as_uint(x) & 0x7F800000u) == 0x7F800000u; }
 
 // D = A B, the first product of a sum. The matrix instructions cut their sums off where

@@ -60,13 +60,6 @@ struct TtGeom {
   static constexpr size_t SMEM = 2 * STAGES * TILE + kTtSoft * kTtStage * 4 + 1024;
 };
 
-// A pair of bfloat16 whose values that are not finite are 0.
-__device__ __forceinline__ uint32_t tt_finite2(uint32_t x) {
-  if ((x & 0x7F80u) == 0x7F80u) x &= 0xFFFF0000u;
-  if ((x & 0x7F800000u) == 0x7F800000u) x &= 0xFFFFu;
-  return x;
-}
-
 // A tile's values in shared memory, a quarter of a row a thread (whole 128-byte lines, so
 // the swizzle does not matter): rows behind k1 or of a missing page become 0, and so do
 // values that are not finite of rows from n on; whether there were any. (Not inlined: its
@@ -85,7 +78,7 @@ __device__ __noinline__ bool tt_mend(unsigned char* tile, int tk, int n, int k1,
     for (int i = 0; i < N; ++i) {
       uint4* at16 = reinterpret_cast<uint4*>(line) + ((i + row) & (N - 1));
       const uint4 w = *at16;
-      const uint4 z = make_uint4(tt_finite2(w.x), tt_finite2(w.y), tt_finite2(w.z), tt_finite2(w.w));
+      const uint4 z = make_uint4(at_finite2(w.x), at_finite2(w.y), at_finite2(w.z), at_finite2(w.w));
       if ((z.x ^ w.x) | (z.y ^ w.y) | (z.z ^ w.z) | (z.w ^ w.w)) *at16 = z, odd = true;
     }
   }
