@@ -754,13 +754,13 @@ dec_status kv_append_slots(const kv_slots_args* a, void* stream);
  * out. Sizes, precision, order of results and the other rules are those of
  * attn_shared_prefix, with rows * n_q < 2^24, batch <= 4096 and (rows * n_q / 16 +
  * min(batch, rows) * n_kv) * (table_stride * page_size / 128 + 2) < 2^37. Matrix
- * instructions cut sums off instead of rounding them: at most 128 of one sum in a
- * row, then it is added to a total in float32, so what is lost does not grow with the
- * length. The work is cut up on the device by the requests' lengths, equal shares of
- * key tiles for all SMs; which kernel runs, and with it a result's last bits, goes by
- * sizes that the host knows, the table's width among them, not the lengths: few rows
- * of short requests take a quarter to a half longer with tables for some ten thousand
- * tokens than with tables as wide as the requests. */
+ * instructions cut sums off instead of rounding them: at most 256 of one sum in a
+ * row (2,048 keys), then it is added to a total in float32, so what is lost does not
+ * grow with the length. The work is cut up on the device by the requests' lengths,
+ * equal shares of key tiles for all SMs; which kernel runs, and with it a result's
+ * last bits, goes by sizes that the host knows, the table's width among them, not the
+ * lengths: few rows of short requests take a third to two thirds longer with tables for
+ * some ten thousand tokens than with tables as wide as the requests. */
 typedef struct {
   int32_t batch, rows, n_q, n_kv, head_dim;
   int32_t qdtype, kvdtype;

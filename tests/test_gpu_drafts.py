@@ -643,15 +643,16 @@ def test_attn_tree_paged_long_sums_are_not_cut_off(R, kv):
     assert max(map(abs, errors)) <= 16 * U, [e / U for e in errors]
 
 
-@pytest.mark.parametrize("kv,d,R,batch,ctx", [("bf16", 128, 64, 24, 1 << 16), ("bf16", 64, 64, 24, 1 << 16), ("bf16", 96, 64, 24, 1 << 16),
-                                              ("bf16", 96, 1, 96, 1 << 18), ("f32", 128, 64, 24, 1 << 16), ("f32", 128, 1, 24, 1 << 17)], ids=str)
+@pytest.mark.parametrize("kv,d,R,batch,ctx", [("bf16", 128, 64, 24, 1 << 17), ("bf16", 64, 64, 24, 1 << 17), ("bf16", 96, 64, 24, 1 << 18),
+                                              ("bf16", 96, 1, 96, 1 << 20), ("f32", 128, 64, 24, 1 << 17), ("f32", 128, 1, 24, 1 << 19)], ids=str)
 def test_attn_tree_paged_bfloat16_results_of_long_sums_round_as_they_should(kv, d, R, batch, ctx):
-    """Bfloat16 results next to a border: values are 1 or 1 + 2^-7, chosen so that a result is 1 + 2^-8 (a border) and 2^-16
-    (256 u) more in even elements, less in odd ones; the choice leaves out at most the largest of 2^14 probabilities (2^-13 of
-    2^-7: 16 u). Matrix instructions cut up to 128 sums of a result off before these are added up rounded, by up to 2 u each
-    of a sum that grows evenly: 128 u. Weights enter by 2^-7: 2^-24 of each. What rounded sums of some thousand terms lose
-    has no sign: 64 u are more than what the root of their number gives. So 240 u are enough. Cut off all along, a result loses a quarter of u for every instruction: 960 u and more here. (One
-    request's pages serve all, over and over.)"""
+    """Bfloat16 results next to a border: values are 1 or 1 + 2^-7, chosen so that a result is 1 + 2^-8 (a border) and 2^-14
+    (1024 u) more in even elements, less in odd ones; the choice leaves out at most the largest of 2^14 probabilities (2^-13
+    of 2^-7: 16 u). Matrix instructions cut up to 256 sums of a result off before these are added up rounded, by up to 2 u
+    each of a sum that grows evenly: 256 u. Weights enter by 2^-7: 2^-24 of each. What rounded sums of some thousand terms
+    lose has no sign: 64 u are more than what the root of their number gives. So 340 u are enough. Cut off all along, a
+    result loses a quarter of u for every instruction: 3,800 u and more here. (One request's pages serve all, over and
+    over.)"""
     import torch
 
     W = lib()
@@ -666,7 +667,7 @@ def test_attn_tree_paged_bfloat16_results_of_long_sums_round_as_they_should(kv, 
     assert p.max() < 2.0 ** -13
     order = torch.rand((n_kv, d, own), generator=g, device="cuda").argsort(-1)
     weight = torch.gather(p[:, None].expand(-1, d, -1), -1, order).cumsum(-1)
-    target = torch.tensor([0.5 + 2.0 ** -9, 0.5 - 2.0 ** -9], dtype=torch.float64, device="cuda").repeat(d // 2)
+    target = torch.tensor([0.5 + 2.0 ** -7, 0.5 - 2.0 ** -7], dtype=torch.float64, device="cuda").repeat(d // 2)
     high = torch.zeros_like(order, dtype=torch.bool).scatter_(-1, order, weight <= target[:, None])
     v = (1 + high.transpose(1, 2).double() / 128).view(n_kv, own // page, page, d).transpose(0, 1).contiguous().to(tdt(kv))
     t["q"].copy_(q.repeat_interleave(n_q // n_kv, 0).reshape(1, -1).expand(batch * R, -1))

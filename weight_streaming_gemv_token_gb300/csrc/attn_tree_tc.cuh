@@ -45,11 +45,11 @@ constexpr uint32_t kTtTmO = 256, kTtTmQ = 384, kTtTmTotal = 448;
 constexpr int kTtStage = 32 * 12;  // floats of a warp's way to memory: 32 rows of 32 bytes and 16 more
 // Tiles whose products are summed in the matrix instructions. These cut sums off where an addition
 // would round, always towards 0 (half a unit or less of 2^-23, 16 instructions a tile): over 16,384
-// keys 5.7e-5 of a result, and results next to a border of bfloat16 rounded to its other side. 8
-// tiles lose some 2e-6; their sums are added up rounded (32 x 64 rows x 16,384 tokens 354 us without
-// and 370 with it, 48 single tokens x 7,000 209 and 213; added up in front of the scores, not behind
-// them, so that the products before are waited for: 379 and 219).
-constexpr int kTtSum = 8;
+// keys 5.7e-5 of a result, and results next to a border of bfloat16 rounded to its other side. 16
+// tiles lose some 3.6e-6, less than probabilities in 16 bits do (4.4e-6); their sums are added up
+// rounded, behind the last one's product (32 x 64 rows x 16,384 tokens 349 us without and 373 with
+// it, 48 single tokens x 7,000 207 and 219; every 32 tiles 364 and 214, every 8 396 and 228).
+constexpr int kTtSum = 16;
 
 template <int D>
 struct TtGeom {
@@ -173,50 +173,54 @@ __device__ __noinline__ void tt_odd(const AtArgs& p, const AtPiece& x, uint32_t 
   }
 }
 
-// A thread's part of O over a piece's tiles but the last kTtSum or fewer, with reference `ref`: 16
-// columns in tensor memory at `at`, of D = 128 12 more in the warp's way to memory, 4 in registers.
-template <int D>
-struct TtTotal {
-  uint32_t at;
-  float* so;
-  float ref = -INFINITY, last[4] = {};
-
-  // JOIN: O, whose reference is m, becomes the whole sum; otherwise the total takes O in (first: becomes it).
-  template <bool JOIN>
-  __device__ __forceinline__ void add(uint32_t to, float m, bool first) {
-    const int lane = threadIdx.x & 31;
-    const float f = ref == m ? 1.f : at_exp2(ref - m);
+// A thread's part of O over a piece's tiles but the last kTtSum or fewer: 16 columns in tensor
+// memory at `at`, of D = 128 12 more in the warp's way to memory `so`; keep[0 .. 3]: the last 4, and
+// keep[4] the total's reference. JOIN: O at `to`, whose reference is m, becomes the whole sum;
+// otherwise the total takes O in (first: becomes it). One warp. (Not inlined, and not from within the
+// loop over tiles: pieces that never come here would take 5 to 9% longer.)
+template <int D, bool JOIN>
+__device__ __noinline__ void tt_total(uint32_t to, uint32_t at, float* so, float* keep, float m, bool first) {
+  const int lane = threadIdx.x & 31;
+  const float ref = first ? m : keep[4], f = ref == m ? 1.f : at_exp2(ref - m);
 #pragma unroll
-    for (int c0 = 0; c0 < D / 4; c0 += 16) {
-      uint32_t o[16], x[16];
-      tc_ld16(o, to + c0);
-      if (c0 == 0) {
-        tc_ld16(x, at);
-      } else {
+  for (int c0 = 0; c0 < D / 4; c0 += 16) {
+    uint32_t o[16], x[16];
+    tc_ld16(o, to + c0);
+    if (c0 == 0) {
+      tc_ld16(x, at);
+    } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(k < 12 ? so[k * 32 + lane] : last[k - 12]);
-      }
-      tc_wait_ld();
+      for (int k = 0; k < 16; ++k) x[k] = first ? 0u : __float_as_uint(k < 12 ? so[k * 32 + lane] : keep[k - 12]);
+    }
+    tc_wait_ld();
 #pragma unroll
-      for (int k = 0; k < 16; ++k) x[k] = first ? o[k] : __float_as_uint(fmaf(__uint_as_float(x[k]), f, __uint_as_float(o[k])));
-      if (JOIN) {
-        tc_st16(to + c0, x);
-      } else if (c0 == 0) {
-        tc_st16(at, x);
-      } else {
+    for (int k = 0; k < 16; ++k) x[k] = first ? o[k] : __float_as_uint(fmaf(__uint_as_float(x[k]), f, __uint_as_float(o[k])));
+    if (JOIN) {
+      tc_st16(to + c0, x);
+    } else if (c0 == 0) {
+      tc_st16(at, x);
+    } else {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          if (k < 12)
-            so[k * 32 + lane] = __uint_as_float(x[k]);
-          else
-            last[k - 12] = __uint_as_float(x[k]);
-        }
+      for (int k = 0; k < 16; ++k) {
+        if (k < 12)
+          so[k * 32 + lane] = __uint_as_float(x[k]);
+        else
+          keep[k - 12] = __uint_as_float(x[k]);
       }
     }
-    tc_wait_st();
-    ref = m;
   }
-};
+  tc_wait_st();
+  keep[4] = m;
+}
+
+// The total takes O in once the product before, which `bar` tells, has completed. Whether it has.
+template <int D>
+__device__ __noinline__ bool tt_fold(uint64_t* bar, uint32_t phase, uint32_t to, uint32_t at, float* so, float* keep, float m, bool first) {
+  if (!__all_sync(0xffffffffu, mbar_wait(bar, phase))) return false;
+  tc_fence_after();
+  tt_total<D, false>(to, at, so, keep, m, first);
+  return true;
+}
 
 // pk, pv: the prefix as [n_kv][plen][D] in boxes of 128 x 64; kp, vp: the pools as
 // [pages * n_kv][page][D] in boxes of min(page, 128) x 64.
@@ -471,7 +475,8 @@ __global__ void __launch_bounds__(kTtThreads, 1)
     // nowhere. It has the code of tiles and results fetched while the stream's previous kernel ends
     // (behind the first keys' copies, which fill the memory's queues, that takes 5 us).
     bool dry = true;
-    TtTotal<D> total{tl + kTtTmTotal + sl * 16, so};
+    float keep[5];  // of the total over earlier tiles
+    const uint32_t tt = tl + kTtTmTotal + sl * 16;
     auto row_done = [&]() {
       tc_fence_before();
       __syncwarp();
@@ -536,11 +541,11 @@ __global__ void __launch_bounds__(kTtThreads, 1)
       const int k0 = cur.k0, k1 = cur.k1;
       const int plain = cur.prefix ? k1 : min(cur.n, k1);  // keys before this one are seen by every row
       float m_ref = -INFINITY, lsum = 0.f;
-      for (int t = 0; t < T; ++t, ++j) {
+      int t = 0;
+      auto tile = [&]() -> bool {
         const int tk = k0 + t * kAtKeys;
         if (!dry && !__all_sync(0xffffffffu, mbar_wait(&s_full[j & 1], (j >> 1) & 1))) {
-          ok = false;
-          break;
+          return false;
         }
         tc_fence_after();
         const uint32_t holes = dry ? 0u : s_holes[j % kTtPieces];
@@ -571,8 +576,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           float(&x)[4][kTtRows] = xch[ex & 1];
           x[sl][v] = mh[0];
           if (!row_done()) {
-            ok = false;
-            break;
+            return false;
           }
           const float mx = fmaxf(fmaxf(x[0][v], x[1][v]), fmaxf(x[2][v], x[3][v])) * c;
           const bool move = mx > m_ref + kAmMargin;
@@ -583,8 +587,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
             if (t > 0) {
               // O holds the piece's tiles before this one once P_{j-1} V_{j-1} has completed
               if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1))) {
-                ok = false;
-                break;
+                return false;
               }
               tc_fence_after();
 #pragma unroll 1
@@ -621,21 +624,11 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           tt_unpair(sum, &s0, &s1);
           lsum += s0 + s1;
           tc_wait_st();
-          if (t > 0 && t % kTtSum == 0) {
-            // O into the total once P_{j-1} V_{j-1} has completed; this tile's product starts it anew
-            if (!__all_sync(0xffffffffu, mbar_wait(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1))) {
-              ok = false;
-              break;
-            }
-            tc_fence_after();
-            total.template add<false>(to, m_ref, t == kTtSum);
-          }
         }
         if (special) {
           const int st = j % STAGES;
           if (!__all_sync(0xffffffffu, mbar_wait(&v_full[st], (j / STAGES) & 1))) {
-            ok = false;
-            break;
+            return false;
           }
           if (tt_mend<D>(Vs + st * G::TILE, tk, cur.n, k1, holes, page_shift_)) vodd[piece & 1] = piece + 1;
           fence_proxy_async_smem();
@@ -643,6 +636,15 @@ __global__ void __launch_bounds__(kTtThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0 && !dry) mbar_arrive(&p_full[j & 1]);
+        return true;
+      };
+      while (true) {
+        for (const int end = min(T, t + kTtSum); ok && t < end; ++t, ++j) ok = tile();
+        if (!ok || t >= T) break;
+        // O into the total once the last product has completed; the next one starts it anew
+        if (works) {
+          if (!(ok = tt_fold<D>(&o_done[(j - 1) & 1], ((j - 1) >> 1) & 1, to, tt, so, keep, m_ref, t == kTtSum))) break;
+        }
       }
       if (!ok) break;
       if (dry) {
@@ -666,7 +668,7 @@ __global__ void __launch_bounds__(kTtThreads, 1)
           break;
         }
         lsum = (x[0][v] + x[1][v]) + (x[2][v] + x[3][v]);
-        if (cur.tiles > kTtSum) total.template add<true>(to, m_ref, false);
+        if (t > kTtSum) tt_total<D, true>(to, tt, so, keep, m_ref, false);
         if (vodd[piece & 1] == piece + 1) tt_odd<D>(p, cur, to, sl, have, token);
         const float inv = lsum == 0.f ? 0.f : 1.0f / lsum;  // a NaN sum stays one
         if (sl == 0 && have) {
