@@ -27,7 +27,7 @@ __device__ __forceinline__ bool at_odd(float x) { return (__float_as_uint(x) & 0
 // (32 x 64 rows x 16,384 tokens: error 5.7e-5, against 7.8e-7), and bfloat16 results next to a
 // border round to its other side. So a block's products are summed from 0 and added by themselves
 // (float32 results 5 to 18% of the time, bfloat16 ones over bfloat16 caches 2 to 10%). Bfloat16
-// results over float32 caches are summed in the instructions over 32 blocks, 96 instructions that
+// results over float32 caches are summed in the instructions over 64 blocks, 192 instructions that
 // lose some 3e-6, and these sums added up in memory: 4% of the time, 15 if every block's were.
 __device__ __forceinline__ void at_mma16z(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
@@ -598,7 +598,7 @@ __global__ void __launch_bounds__(32 * AtGeom<QT, DP, F32, RG, PER>::WARPS, PER)
 #pragma unroll
     for (int i = 0; i < 4; ++i) token[i] = min(row0 + Core::row_of(i), pc.m0 + pc.nrows - 1) / a.group;
     const int mine = (nblk - kg + KG - 1) / KG;  // blocks of this ring
-    constexpr int SUM = Core::APART ? 0 : 32;    // blocks whose products the matrix instructions sum; 0: one
+    constexpr int SUM = Core::APART ? 0 : 64;    // blocks whose products the matrix instructions sum; 0: one
     volatile float total[SUM ? DP / 2 + 4 : 1];  // (in memory)
 #pragma unroll 1
     for (int i = 0; i < mine; ++i) {
