@@ -759,8 +759,8 @@ dec_status kv_append_slots(const kv_slots_args* a, void* stream);
  * grow with the length. The work is cut up on the device by the requests' lengths,
  * equal shares of key tiles for all SMs; which kernel runs, and with it a result's
  * last bits, goes by sizes that the host knows, the table's width among them, not the
- * lengths: few rows of short requests take a third to two thirds longer with tables for
- * some ten thousand tokens than with tables as wide as the requests. */
+ * lengths: single tokens of many short requests take longer with wide tables (256 of
+ * 500 tokens 173 us with tables for more than 1,024, 104 with narrower ones). */
 typedef struct {
   int32_t batch, rows, n_q, n_kv, head_dim;
   int32_t qdtype, kvdtype;

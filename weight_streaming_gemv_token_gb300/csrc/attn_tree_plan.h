@@ -141,9 +141,10 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   // bfloat16 throughout, a head of 64 or 128, pages of whole swizzled groups of rows: on the
   // tensor cores, but for rows that one row tile of 16 holds (all of the step's, where a
   // prefix is read once a row tile) and, with heads of 128, not too many keys. Warp-level and
-  // tensor-core form: 1 token x 500 9.7 and 12.0 us, 256 x 500 102 and 152, 8 x 4,096 32 and
-  // 36, 32 x 4,096 93 and 94, 16 x 16,000 177 and 162; of heads of 64, where the latter's
-  // softmax takes longer than the bytes, 8 x 4,096 23.5 and 29, 48 x 7,000 120 and 184.
+  // tensor-core form: 1 token x 500 9.7 and 12.8 us, 256 x 500 104 and 173, 8 x 4,096 33 and
+  // 37, 32 x 4,096 98 and 99, 16 x 16,000 174 and 172; of heads of 64, where the latter's
+  // softmax takes longer than the bytes, 8 x 4,096 24 and 31, 48 x 7,000 120 and 194. (By the
+  // tables' width: the lengths are on the device.)
   const bool few = most <= 16 && (a->prefix_len == 0 || static_cast<long long>(a->rows) * group <= 16);
   const bool brief = a->head_dim == 64 || full <= 48 || p.cut.capacity <= 1024;
   p.tc = a->qdtype == DEC_BF16 && a->kvdtype == DEC_BF16 && (a->head_dim == 128 || a->head_dim == 64) && a->page_size >= 8 &&
@@ -168,8 +169,9 @@ inline AtPlan attn_tree_plan(const attn_tree_args* a, int sms) {
   const long long own = static_cast<long long>(a->rows) * group / mt + (a->batch < a->rows ? a->batch : a->rows);
   const long long segments = (own + p.prefix_row_tiles) * a->n_kv;
   // as many small CTAs an SM as there are segments for (and as rings and row groups allow):
-  // 256 requests of one token x 16 tokens with one 64 us, with two 35, with four 25; 4
-  // requests of 8 rows x 1,000 15, 16 and 17; 64 of 32 float32 rows x 100 73 and 48.
+  // 256 requests of one token x 16 tokens with one 64 us, with two 35, with four 25 (27 since a
+  // block's products are added by themselves); 4 requests of 8 rows x 1,000 15, 16 and 17; 64 of
+  // 32 float32 rows x 100 73 and 48.
   if (p.tc || a->kvdtype == DEC_F32)
     p.per_sm = 1;
   else if (p.cut.mshift > 4)

@@ -7,9 +7,9 @@
 // remainder, three products). So the keys are read once for up to 64 rows.
 //
 // Bound by a block's chain of instructions for many rows and for float32, by memory for few
-// rows of bfloat16. Measured (16 query heads over 8, heads of 128): 32 single tokens x 4,096
-// bfloat16 93 us (5.8 TB/s), float32 queries 103, float32 caches 214 (5.0 TB/s); 32 x 64
-// rows 692 and 1,545.
+// rows of bfloat16. Measured (16 query heads over 8, heads of 128, all requests as long as said): 32
+// single tokens x 4,096 bfloat16 98 us (5.5 TB/s), float32 queries 103, float32 caches 214 (5.0
+// TB/s; bfloat16 queries over them 180); 32 x 64 rows 693, 1,545 and 1,144.
 //
 // Blocks that hold drafted rows' keys mask scores row by row. A value that is not
 // finite would reach rows that do not see it through its product with a weight of 0,

@@ -6,17 +6,18 @@
 // per tensor-memory lane. The CTA runs through its pieces one after the other, tiles
 // of 128 keys in rings that do not stop between pieces:
 //   warp 0      finds the CTA's share and cuts it into pieces, which it announces to
-//               the others two or three tiles ahead; streams keys and values, a box of
-//               64 columns a page (128-byte swizzle), a lane a page, its table entry read
-//               one tile ahead;
+//               the others two or three tiles ahead; with warps 18 and 19 streams keys and
+//               values, a box of 64 columns a page (128-byte swizzle), a lane a box, its table
+//               entry read one tile ahead; each of the three arrives for every tile;
 //   warp 1      one thread issues S_j = Q K_j^T one tile ahead, then O += P_j V_j with
 //               P_j over the scores in tensor memory;
 //   warps 2-17  four threads a row, 32 of the tile's keys each: masked, scaled scores,
 //               reference maximum (moved only past a margin of 2^8, then O is rescaled in
 //               place), probabilities as bfloat16 value + remainder, running sums. They
 //               put the next piece's queries into tensor memory once the last scores of
-//               a piece are read, so its first scores run while O is read. (Two threads a row:
-//               longer chains and twice the code to fetch, 3,500 cycles a tile.)
+//               a piece are read, so its first scores run while O is read. Every 16 tiles O
+//               goes into a total (kTtSum). (Two threads a row: longer chains and twice the code to
+//               fetch, 3,500 cycles a tile.)
 // Tiles with drafted rows or the end of the keys: scores are masked row by row; value
 // rows behind the end or of a page that is not there become 0 in shared memory, and so
 // do values of drafted rows that are not finite, which are added afterwards to the rows
@@ -25,9 +26,9 @@
 // Tensor memory (512 columns): scores / probabilities at 0 and 128, O at 256, Q at
 // 384. The products of a tile of head size 128 take 24 x 64 cycles for any number of
 // rows, its 64 KB at the SM's share of the measured bandwidth 2,700 at 1.85 GHz: bound
-// by memory for up to 128 rows a head. Measured (16 query heads over 8): 32 x 64 rows x
-// 16,384 tokens 353 us (6.1 TB/s), 48 single tokens x 7,000 210
-// (6.5 TB/s), 8 x 16 rows x 4,096 36.5.
+// by memory for up to 128 rows a head. Measured (16 query heads over 8, all requests as long as
+// said): 32 x 64 rows x 16,384 tokens 373 us (5.8 TB/s), 48 single tokens x 7,000 219 (6.3 TB/s),
+// 8 x 16 rows x 4,096 37.4.
 //
 // Every wait is bounded; on a timeout the CTA records ERR_TC_TIMEOUT, stops, waits
 // for its issued MMAs and copies and frees its tensor memory.
